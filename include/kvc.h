@@ -319,6 +319,123 @@ KVC_API kvc_status kvc_decode_attn_noalloc(kvc_pool *pool, int32_t layer, const 
                                            const int32_t *seq_lens, int32_t B, float *out, float *lse,
                                            float scale, kvc_stream_t stream);
 
+/* ------------------------------------------------------------------ rotary write */
+
+/* Position rotation of queries and keys, with an optional RMS norm of each
+ * head before it.  For a head row x at position t:
+ *   y_i = x_i                                       (norm weight NULL)
+ *   y_i = x_i / sqrt(mean_j x_j^2 + norm_eps) * w_i
+ *   z_i = y_i cos(t f_i) - y_j sin(t f_i),  z_j = y_j cos(t f_i) + y_i sin(t f_i)
+ * for the pairs (i, j), i < rotary_dim / 2, with f = inv_freq; channels at or
+ * past rotary_dim pass through.  fp32 arithmetic on the bf16 inputs, angles
+ * to about 1e-6 radians at positions below 2^24, one rounding at the end. */
+typedef struct {
+    int32_t rotary_dim;      /* R: channels [0, R) rotate; a multiple of 16 (else KVC_ERR_UNSUPPORTED), 0 .. d_h */
+    int32_t interleaved;     /* 0: channel i pairs with i + R/2;  1: channel 2i with 2i + 1 */
+    const float *inv_freq;   /* device fp32 [R/2], radians per position (NULL only when R = 0) */
+    const void *q_norm;      /* device bf16 [d_h] norm weights of the query heads, or NULL: no norm */
+    const void *k_norm;      /* the key heads' */
+    float norm_eps;          /* finite, >= 0 */
+    int32_t reserved;
+} kvc_rope;
+
+/* kvc_append for a model with rotary positions: one launch rotates (and
+ * normalises) each sequence's query and key at position t = seq_lens[b],
+ * stores the rotated key and the value at that position, and writes the
+ * rotated query.  Values are stored as kvc_append stores them; keys are
+ * rounded once, from the fp32 result to the pool's element type (e4m3 and
+ * int4: after the division by the scale).
+ *   q, k_new, v_new: device bf16 rows of heads x d_h contiguous elements, one
+ *       row per sequence, q_stride / k_stride / v_stride elements apart
+ *       (multiples of 8, at least a row; views of a fused projection's output
+ *       are read in place); 16-byte aligned
+ *   num_q_heads: any count; 0 rotates keys only (q and q_out unused)
+ *   q_out: device bf16 [B][num_q_heads][d_h], 16-byte aligned; may be q itself
+ *       when q is contiguous, and must not overlap k_new, v_new or another
+ *       part of q (KVC_ERR_ARG)
+ * Pools of any block size.  A token with a bad table entry or position is
+ * not stored and recorded as in kvc_append; its q_out row is still written.
+ * B = 0 is a no-op.  Errors (synchronous): KVC_ERR_ARG, KVC_ERR_UNSUPPORTED,
+ * KVC_ERR_CUDA. */
+KVC_API kvc_status kvc_rope_append(kvc_pool *pool, int32_t layer, const int32_t *block_tables, int32_t max_blocks,
+                                   const int32_t *seq_lens, int32_t B, const void *q, int64_t q_stride,
+                                   int32_t num_q_heads, const void *k_new, int64_t k_stride, const void *v_new,
+                                   int64_t v_stride, const kvc_rope *rope, void *q_out, kvc_stream_t stream);
+
+/* The same for a ragged batch, as kvc_write_tokens: rows cu_tokens[b] ..
+ * cu_tokens[b+1]-1 are sequence b's tokens at positions start_pos[b],
+ * start_pos[b]+1, ...  n_rows is the number of rows that q, k, v and q_out
+ * hold (host); rows at or past cu_tokens[B] are neither read nor written.
+ * Sequences without tokens are allowed. */
+KVC_API kvc_status kvc_rope_write_tokens(kvc_pool *pool, int32_t layer, const int32_t *block_tables,
+                                         int32_t max_blocks, const int32_t *start_pos, const int32_t *cu_tokens,
+                                         int32_t B, int64_t n_rows, const void *q, int64_t q_stride,
+                                         int32_t num_q_heads, const void *k, int64_t k_stride, const void *v,
+                                         int64_t v_stride, const kvc_rope *rope, void *q_out, kvc_stream_t stream);
+
+/* ------------------------------------------------------------------ attention with modified scores */
+
+/* How the scores of a query at position p are modified and which positions t
+ * it reads.  With x_t = scale * <q, k_t>:
+ *   softcap > 0:  x_t <- softcap * tanh(x_t / softcap)
+ *   alibi:        x_t <- x_t - alibi[hq] * |p - t|
+ *   reads t in [lo, p] and t in [d, e), both below the sequence's length:
+ *     d  = max(doc_start[i], 0) of query i, or 0 without documents
+ *     lo = max(d, p - window + 1), or d when window = 0
+ *     e  = min(d + sink, p + 1) with a window (the sequence's or document's
+ *          first `sink` positions stay readable behind it), and at least
+ *          prefix (positions [0, prefix) are read by every query, earlier
+ *          queries included)
+ * A query that reads nothing (its document starts after it) gives out = 0 and
+ * lse = -inf.  Blocks that no query of a unit reads are not looked at: their
+ * table entries may be -1. */
+typedef struct {
+    float softcap;              /* 0: none; finite, >= 0 */
+    int32_t window;             /* 0: none */
+    int32_t sink;               /* used with a window */
+    int32_t prefix;             /* 0: none */
+    const float *alibi;         /* device fp32 [num_q_heads] slopes, or NULL */
+    const int32_t *doc_start;   /* prefill: device int32 [n_q], the first position of query i's document, or NULL;
+                                 * not together with prefix (KVC_ERR_UNSUPPORTED) nor in decode (KVC_ERR_ARG) */
+} kvc_score_mod;
+
+/* Bytes of a workspace that serves every kvc_decode_attn_mod call of up to
+ * `rows` sequences and every kvc_prefill_attn_mod call of up to `rows`
+ * queries, with num_q_heads query heads and up to max_blocks table entries.
+ * The caller allocates it on the pool's device (256-byte aligned), zeroes it
+ * once, and passes it to any number of calls in turn: every call leaves it
+ * ready for the next, of any shape it serves.  Calls that may overlap on the
+ * GPU (two streams, two captured graphs replayed side by side) need a
+ * workspace each; after KVC_ERR_TIMEOUT zero it again. */
+KVC_API kvc_status kvc_mod_workspace_bytes(const kvc_pool *pool, int32_t rows, int32_t num_q_heads,
+                                           int32_t max_blocks, uint64_t *bytes);
+
+/* kvc_decode_attn with modified scores (mod = NULL: none).  The query of
+ * sequence b sits at position seq_lens[b] - 1.
+ *   out: device bf16 [B][H_Q][d_h] (what a model's next projection takes),
+ *        16-byte aligned;  lse: device fp32 [B][H_Q] or NULL (natural log, of
+ *        the modified scores)
+ *   scale: finite and > 0
+ *   workspace: see kvc_mod_workspace_bytes; NULL plans one split per
+ *        (sequence, KV head): no extra memory, slow for few long sequences;
+ *        one too small for the call is KVC_ERR_ARG
+ * The library allocates nothing, so calls may be captured into a graph at any
+ * time.  Other arguments, requirements and errors as kvc_decode_attn. */
+KVC_API kvc_status kvc_decode_attn_mod(kvc_pool *pool, int32_t layer, const void *q, int32_t num_q_heads,
+                                       const int32_t *block_tables, int32_t max_blocks, const int32_t *seq_lens,
+                                       int32_t B, const kvc_score_mod *mod, void *out, float *lse, float scale,
+                                       void *workspace, uint64_t workspace_bytes, kvc_stream_t stream);
+
+/* kvc_prefill_attn with modified scores: query i sits at position q_start + i,
+ * and the row holds q_start + n_q positions.  out, lse, scale and workspace as
+ * kvc_decode_attn_mod; a value row that some query of a call reads must be
+ * finite for the call's other queries of the same chunk to be.  Other
+ * arguments, requirements and errors as kvc_prefill_attn. */
+KVC_API kvc_status kvc_prefill_attn_mod(kvc_pool *pool, int32_t layer, const void *q, int32_t n_q,
+                                        int32_t num_q_heads, const int32_t *block_table_row, int32_t max_blocks,
+                                        int32_t q_start, const kvc_score_mod *mod, void *out, float *lse, float scale,
+                                        void *workspace, uint64_t workspace_bytes, kvc_stream_t stream);
+
 /* ------------------------------------------------------------------ block allocator (host) */
 
 /* Host-side block allocator that produces the block tables the calls above

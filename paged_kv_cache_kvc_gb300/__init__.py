@@ -43,11 +43,23 @@ class kvc_pool_desc(ctypes.Structure):
                 ("elem_bits", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+class kvc_rope(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("inv_freq", ctypes.c_void_p),
+                ("q_norm", ctypes.c_void_p), ("k_norm", ctypes.c_void_p), ("norm_eps", ctypes.c_float),
+                ("reserved", ctypes.c_int32)]
+
+
+class kvc_score_mod(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("window", ctypes.c_int32), ("sink", ctypes.c_int32),
+                ("prefix", ctypes.c_int32), ("alibi", ctypes.c_void_p), ("doc_start", ctypes.c_void_p)]
+
+
 EXPORTS = ["kvc_pool_create", "kvc_pool_destroy", "kvc_pool_info", "kvc_pool_set_scales", "kvc_calibrate_fp8",
            "kvc_calibrate_scales",
            "kvc_append", "kvc_write_tokens", "kvc_decode_attn", "kvc_prefill_attn", "kvc_pool_reserve",
            "kvc_bytes", "kvc_pool_sync_status", "kvc_status_str", "kvc_launch_count", "kvc_decode_attn_noalloc", "kvc_decode_step",
-           "kvc_mixed_step",
+           "kvc_mixed_step", "kvc_rope_append", "kvc_rope_write_tokens", "kvc_mod_workspace_bytes",
+           "kvc_decode_attn_mod", "kvc_prefill_attn_mod",
            "kvc_alloc_create", "kvc_alloc_destroy", "kvc_alloc_new_seq", "kvc_alloc_fork", "kvc_alloc_reserve",
            "kvc_alloc_commit", "kvc_alloc_release", "kvc_alloc_publish", "kvc_alloc_match", "kvc_alloc_seq_info",
            "kvc_alloc_block_tables", "kvc_alloc_counts", "kvc_alloc_refcount", "kvc_alloc_lease", "kvc_alloc_check",
@@ -83,6 +95,16 @@ def load(path: str = LIB_PATH):
     L.kvc_mixed_step.restype = st
     L.kvc_mixed_step.argtypes = [vp, i32, vp, i32, vp, i32, vp, i32, vp, vp, vp, vp,
                                  vp, i32, vp, i32, i32, vp, vp, ctypes.c_float, vp]
+    rp, mp = ctypes.POINTER(kvc_rope), ctypes.POINTER(kvc_score_mod)
+    L.kvc_rope_append.restype = st
+    L.kvc_rope_append.argtypes = [vp, i32, vp, i32, vp, i32, vp, i64, i32, vp, i64, vp, i64, rp, vp, vp]
+    L.kvc_rope_write_tokens.restype = st
+    L.kvc_rope_write_tokens.argtypes = [vp, i32, vp, i32, vp, vp, i32, i64, vp, i64, i32, vp, i64, vp, i64, rp, vp, vp]
+    L.kvc_mod_workspace_bytes.restype, L.kvc_mod_workspace_bytes.argtypes = st, [vp, i32, i32, i32, ctypes.POINTER(u64)]
+    L.kvc_decode_attn_mod.restype = st
+    L.kvc_decode_attn_mod.argtypes = [vp, i32, vp, i32, vp, i32, vp, i32, mp, vp, vp, ctypes.c_float, vp, u64, vp]
+    L.kvc_prefill_attn_mod.restype = st
+    L.kvc_prefill_attn_mod.argtypes = [vp, i32, vp, i32, i32, vp, i32, i32, mp, vp, vp, ctypes.c_float, vp, u64, vp]
     L.kvc_pool_reserve.restype, L.kvc_pool_reserve.argtypes = st, [vp, i32, i32, i32]
     L.kvc_bytes.restype, L.kvc_bytes.argtypes = u64, [i64] * 6
     L.kvc_pool_sync_status.restype, L.kvc_pool_sync_status.argtypes = st, [vp, vp]
@@ -314,6 +336,159 @@ def kvc_mixed_step(pool, layer, q, block_tables, seq_lens_pre, k_new, v_new, out
                                  _dev(prefill_lse, torch.float32, "prefill_lse", optional=True), float(scale),
                                  _stream(stream)),
            "kvc_mixed_step")
+
+
+# ---------------------------------------------------------------------- rotary write
+class Rope:
+    """Position rotation (and optional per-head RMS norm) for kvc_rope_append / kvc_rope_write_tokens.
+
+    inv_freq: CUDA fp32 [rotary_dim / 2], radians per position (None: no rotation); q_norm, k_norm: CUDA
+    bf16 [d_h] norm weights or None.  Holds the tensors; one object serves any number of calls."""
+
+    def __init__(self, inv_freq=None, interleaved=False, q_norm=None, k_norm=None, eps=1e-6):
+        self.inv_freq, self.q_norm, self.k_norm = inv_freq, q_norm, k_norm
+        dim = 0 if inv_freq is None else 2 * inv_freq.numel()
+        self.desc = kvc_rope(dim, int(bool(interleaved)), _dev(inv_freq, torch.float32, "inv_freq", optional=True),
+                             _dev(q_norm, torch.bfloat16, "q_norm", optional=True),
+                             _dev(k_norm, torch.bfloat16, "k_norm", optional=True), float(eps), 0)
+
+    def _check(self, pool):
+        _same_device(pool, inv_freq=self.inv_freq, q_norm=self.q_norm, k_norm=self.k_norm)
+        for name in ("q_norm", "k_norm"):
+            w = getattr(self, name)
+            if w is not None and w.numel() != pool.head_dim:
+                raise ValueError(f"{name} must have head_dim = {pool.head_dim} elements, got {w.numel()}")
+
+
+def _same_device(pool, **tensors):
+    for name, t in tensors.items():
+        if t is not None and isinstance(t, torch.Tensor) and t.is_cuda and t.device.index != pool.device:
+            raise ValueError(f"{name} is on cuda:{t.device.index}, the pool on cuda:{pool.device}")
+
+
+def _want_shape(t, shape, name):
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _rows(t, name):
+    """(device pointer, elements between rows) of bf16 [rows][heads][d_h]; rows may be strided, a row not."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.bfloat16 or t.dim() != 3:
+        raise ValueError(f"{name} must be a CUDA bfloat16 tensor [rows][heads][head_dim]")
+    n, h, d = t.shape
+    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    return t.data_ptr(), (t.stride(0) if n > 1 else h * d)
+
+
+def _rope_args(pool, rows, block_tables, seqs, q, k, v, q_out, rope):
+    B = block_tables.shape[0]
+    _want_shape(seqs, (B,), "seq_lens / start_pos")
+    _want_shape(k, (rows, pool.num_kv_heads, pool.head_dim), "k")
+    _want_shape(v, (rows, pool.num_kv_heads, pool.head_dim), "v")
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    rope._check(pool)
+    _same_device(pool, block_tables=block_tables, seqs=seqs, q=q, k=k, v=v, q_out=q_out)
+    H_Q, qp, qs = 0, None, 0
+    if q is not None:
+        H_Q = q.shape[1]
+        _want_shape(q, (rows, H_Q, pool.head_dim), "q")
+        _want_shape(q_out, (rows, H_Q, pool.head_dim), "q_out")
+        qp, qs = _rows(q, "q")
+    (kp, ks), (vp, vs) = _rows(k, "k"), _rows(v, "v")
+    return (qp, qs, H_Q, kp, ks, vp, vs, ctypes.byref(rope.desc), _dev(q_out, torch.bfloat16, "q_out", optional=True))
+
+
+def kvc_rope_append(pool, layer, block_tables, seq_lens, q, k_new, v_new, q_out, rope, stream=None):
+    """Rotate (and normalise) one token per sequence at position seq_lens[b]: k_new, v_new into the pool, q to q_out.
+
+    q, k_new, v_new: bf16 [B][heads][head_dim], rows may be strided (views of a fused projection's output); q and
+    q_out may both be None; q_out may be q."""
+    B, mb = block_tables.shape
+    a = _rope_args(pool, B, block_tables, seq_lens, q, k_new, v_new, q_out, rope)
+    _check(load().kvc_rope_append(_h(pool), layer, _dev(block_tables, torch.int32, "block_tables"), mb,
+                                  _dev(seq_lens, torch.int32, "seq_lens"), B, *a, _stream(stream)), "kvc_rope_append")
+
+
+def kvc_rope_write_tokens(pool, layer, block_tables, start_pos, cu_tokens, q, k, v, q_out, rope, stream=None):
+    """kvc_rope_append for a ragged batch: rows cu_tokens[b] .. cu_tokens[b+1]-1 at positions start_pos[b], ...
+
+    Rows at or past cu_tokens[-1] are left as they are.  Nothing is copied to the host."""
+    B, mb = block_tables.shape
+    n = k.shape[0]
+    _want_shape(cu_tokens, (B + 1,), "cu_tokens")
+    _same_device(pool, cu_tokens=cu_tokens)
+    a = _rope_args(pool, n, block_tables, start_pos, q, k, v, q_out, rope)
+    _check(load().kvc_rope_write_tokens(_h(pool), layer, _dev(block_tables, torch.int32, "block_tables"), mb,
+                                        _dev(start_pos, torch.int32, "start_pos"),
+                                        _dev(cu_tokens, torch.int32, "cu_tokens"), B, n, *a, _stream(stream)),
+           "kvc_rope_write_tokens")
+
+
+# ---------------------------------------------------------------------- attention with modified scores
+class ScoreMod:
+    """Score modifiers and masks of kvc_decode_attn_mod / kvc_prefill_attn_mod (see kvc_score_mod in kvc.h).
+
+    alibi: CUDA fp32 [H_Q] slopes; doc_start: CUDA int32 [n_q] (prefill).  Holds the tensors."""
+
+    def __init__(self, softcap=0.0, window=0, sink=0, prefix=0, alibi=None, doc_start=None):
+        self.alibi, self.doc_start = alibi, doc_start
+        self.desc = kvc_score_mod(float(softcap), int(window), int(sink), int(prefix),
+                                  _dev(alibi, torch.float32, "alibi", optional=True),
+                                  _dev(doc_start, torch.int32, "doc_start", optional=True))
+
+
+def kvc_mod_workspace(pool, rows, num_q_heads, max_blocks) -> torch.Tensor:
+    """A zeroed workspace for kvc_decode_attn_mod / kvc_prefill_attn_mod calls of up to `rows` sequences or queries.
+
+    One workspace serves any number of calls in turn; calls that may overlap on the GPU need one each."""
+    n = ctypes.c_uint64()
+    _check(load().kvc_mod_workspace_bytes(_h(pool), rows, num_q_heads, max_blocks, ctypes.byref(n)),
+           "kvc_mod_workspace_bytes")
+    return torch.zeros(n.value, dtype=torch.uint8, device=f"cuda:{pool.device}")
+
+
+def _mod_args(pool, q, out, lse, mod, scale, workspace):
+    n, H_Q, D = q.shape
+    if D != pool.head_dim:
+        raise ValueError(f"q must have head_dim = {pool.head_dim}, got {D}")
+    _want_shape(out, q.shape, "out")
+    _want_shape(lse, (n, H_Q), "lse")
+    if mod is not None:
+        _want_shape(mod.alibi, (H_Q,), "alibi")
+        _want_shape(mod.doc_start, (n,), "doc_start")
+        _same_device(pool, alibi=mod.alibi, doc_start=mod.doc_start)
+    _same_device(pool, q=q, out=out, lse=lse, workspace=workspace)
+    return (None if mod is None else ctypes.byref(mod.desc), _dev(out, torch.bfloat16, "out"),
+            _dev(lse, torch.float32, "lse", optional=True), float(D ** -0.5 if scale is None else scale),
+            _dev(workspace, torch.uint8, "workspace", optional=True), 0 if workspace is None else workspace.numel())
+
+
+def kvc_decode_attn_mod(pool, layer, q, block_tables, seq_lens, out, lse=None, mod=None, scale=None, workspace=None,
+                        stream=None):
+    """kvc_decode_attn with modified scores; out is bf16.  workspace: kvc_mod_workspace, or None (no splits: slow
+    for few long sequences)."""
+    B, mb = block_tables.shape
+    if q.shape[0] != B:
+        raise ValueError(f"q has {q.shape[0]} rows for {B} sequences")
+    _want_shape(seq_lens, (B,), "seq_lens")
+    _same_device(pool, block_tables=block_tables, seq_lens=seq_lens)
+    a = _mod_args(pool, q, out, lse, mod, scale, workspace)
+    _check(load().kvc_decode_attn_mod(_h(pool), layer, _dev(q, torch.bfloat16, "q"), q.shape[1],
+                                      _dev(block_tables, torch.int32, "block_tables"), mb,
+                                      _dev(seq_lens, torch.int32, "seq_lens"), B, *a, _stream(stream)),
+           "kvc_decode_attn_mod")
+
+
+def kvc_prefill_attn_mod(pool, layer, q, block_table_row, q_start, out, lse=None, mod=None, scale=None,
+                         workspace=None, stream=None):
+    """kvc_prefill_attn with modified scores; out is bf16, workspace as for kvc_decode_attn_mod."""
+    _same_device(pool, block_table_row=block_table_row)
+    a = _mod_args(pool, q, out, lse, mod, scale, workspace)
+    _check(load().kvc_prefill_attn_mod(_h(pool), layer, _dev(q, torch.bfloat16, "q"), q.shape[0], q.shape[1],
+                                       _dev(block_table_row, torch.int32, "block_table_row"), block_table_row.shape[-1],
+                                       int(q_start), *a, _stream(stream)), "kvc_prefill_attn_mod")
 
 
 def kvc_pool_reserve(pool, max_batch, num_q_heads, max_blocks):

@@ -80,3 +80,17 @@ def test_product_path_fails_loudly_without_library(tmp_path):
     finally:
         k._lib = saved
         importlib.reload(k) if saved is None else None
+
+
+def test_rotary_and_modified_score_calls_refuse_without_a_pool(lib):
+    import paged_kv_cache_kvc_gb300 as k
+    rope, mod, n = k.kvc_rope(), k.kvc_score_mod(), ctypes.c_uint64()
+    assert ctypes.sizeof(rope) == 40 and ctypes.sizeof(mod) == 32   # the header's layout
+    assert lib.kvc_rope_append(None, 0, None, 1, None, 1, None, 0, 0, None, 0, None, 0, ctypes.byref(rope), None,
+                               None) == k.KVC_ERR_ARG
+    assert lib.kvc_rope_write_tokens(None, 0, None, 1, None, None, 1, 1, None, 0, 0, None, 0, None, 0, None, None,
+                                     None) == k.KVC_ERR_ARG
+    assert lib.kvc_decode_attn_mod(None, 0, None, 8, None, 1, None, 1, ctypes.byref(mod), None, None, 1.0, None, 0,
+                                   None) == k.KVC_ERR_ARG
+    assert lib.kvc_prefill_attn_mod(None, 0, None, 1, 8, None, 1, 0, None, None, None, 1.0, None, 0, None) == k.KVC_ERR_ARG
+    assert lib.kvc_mod_workspace_bytes(None, 1, 8, 1, ctypes.byref(n)) == k.KVC_ERR_ARG
