@@ -292,6 +292,7 @@ def prepare(case, seed):
             kvc.kvc_pool_set_scales(pool, 0, s["scales"][0].contiguous(), s["scales"][1].contiguous())
         s["handle"] = pool
         s["pool"] = pool.bytes_view().view(data.dtype).view(data.shape)
+        s["pool"].handle = pool   # the view does not own the pool's memory: keep the pool while it is in use
         if c["op"] == "rope":
             s["rope"] = kvc.Rope(s["inv_freq"], interleaved=c["interleaved"], q_norm=s["q_norm"], k_norm=s["k_norm"],
                                  eps=1e-6)
