@@ -3,7 +3,7 @@
 #include <cmath>
 #include <cstdlib>
 
-#include "kvc_mod.cuh"
+#include "kvc_mod_tc.cuh"
 
 namespace kvc {
 
@@ -152,6 +152,55 @@ static kvc_status run_split(kvc_pool *pool, ModParams &mp, const DecodeKernel &k
     return KVC_OK;
 }
 
+// The tensor-memory kernel's partials: two pieces of a unit's 256 rows per CTA.
+static size_t tc_partial_bytes(int64_t ctas, int D) { return static_cast<size_t>(ctas) * 2 * 256 * (D * sizeof(float) + sizeof(float2)); }
+
+// KVC_TC=0 selects the split kernel (as for the plain calls).
+static bool use_tc(const kvc_pool *pool)
+{
+    const char *e = std::getenv("KVC_TC");
+    return !(e && e[0] == '0') && pool->dtype == KVC_BF16 && pool->tmap16_ok;
+}
+
+// A chunk on the tensor-memory kernel, as many units at a time as one launch takes.
+static kvc_status run_tc(kvc_pool *pool, const ModParams &mp0, void *ws, size_t ws_bytes, cudaStream_t stream)
+{
+    ModTcParams tp{};
+    tp.m = mp0;
+    DecodeParams &p = tp.m.d;
+    p.ppu = 128 / p.g;
+    tp.total = p.len_base + p.n_pos;
+    const bool fixed = tp.m.capped && !tp.m.alibi && tp.m.cap_out <= kMtCapLimit;
+    const DecodeKernel k = select_mod_tc(pool->D, fixed);
+    if (!k.fn) return KVC_ERR_UNSUPPORTED;
+    if (k.ctas_per_sm <= 0) return KVC_ERR_CUDA;
+    const int per_launch = kMtUnits * 2 * p.ppu, n_q = p.n_pos, start = p.len_base;
+    for (int at = 0; at < n_q; at += per_launch) {
+        p.n_pos = std::min(per_launch, n_q - at);
+        p.len_base = start + at;
+        p.q = mp0.d.q + static_cast<size_t>(at) * p.H_Q * pool->D;
+        tp.m.out = mp0.out + static_cast<size_t>(at) * p.H_Q * pool->D;
+        p.lse = mp0.d.lse ? mp0.d.lse + static_cast<size_t>(at) * p.H_Q : nullptr;
+        tp.m.doc_start = mp0.doc_start ? mp0.doc_start + at : nullptr;
+        tp.units = (p.n_pos + 2 * p.ppu - 1) / (2 * p.ppu);
+        // no CTA without a tile: a line of tiles at least as long as what the units' ends need
+        const int64_t most = static_cast<int64_t>(p.H_KV) * tp.units * ((p.max_blocks + kMtBlocks - 1) / kMtBlocks);
+        const int64_t ctas = std::min<int64_t>(pool->num_sms, most);
+        tp.whole = !ws || 2ll * p.H_KV * tp.units > kCounters;
+        if (!tp.whole) {
+            if (ws_bytes < kCounterBytes + tc_partial_bytes(ctas, pool->D)) return KVC_ERR_ARG;
+            tp.counters = static_cast<uint32_t *>(ws);
+            tp.part_o = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + kCounterBytes);
+            tp.part_ml = reinterpret_cast<float2 *>(tp.part_o + static_cast<size_t>(ctas) * 2 * 256 * pool->D);
+        }
+        void *args[] = {&pool->tmap16, &tp};
+        const cudaError_t e = launch_dependent(k.fn, dim3(static_cast<unsigned>(ctas)), dim3(kMtThreads), k.smem, stream, args);
+        if (e != cudaSuccess) return cuda_status(e);
+        g_launches.fetch_add(1, std::memory_order_relaxed);
+    }
+    return KVC_OK;
+}
+
 static kvc_status mod_checks(kvc_pool *pool, int32_t layer, const void *q, int32_t H_Q, const int32_t *bt,
                              int32_t max_blocks, const kvc_score_mod *mod, void *out, float *lse, float scale, void *ws)
 {
@@ -235,7 +284,8 @@ extern "C" kvc_status kvc_mod_workspace_bytes(const kvc_pool *pool, int32_t rows
     const int64_t by_slots = ppu * (14ll * pool->num_sms / pool->H_KV + 1) + 2ll * rows;
     const int64_t by_cap = rows * ((max_blocks + 283ll) / 284 + 1);
     const int64_t n = std::min(rows * by_len, std::max(by_slots, by_cap));
-    *bytes = kCounterBytes + partial_bytes(n, num_q_heads, pool->D);
+    *bytes = kCounterBytes + std::max(partial_bytes(n, num_q_heads, pool->D),
+                                      pool->dtype == KVC_BF16 ? tc_partial_bytes(pool->num_sms, pool->D) : 0);
     return KVC_OK;
 }
 
@@ -277,6 +327,7 @@ extern "C" kvc_status kvc_prefill_attn_mod(kvc_pool *pool, int32_t layer, const 
     DecodeParams &p = mp.d;
     p.len_base = q_start;
     p.n_pos = n_q;
+    if (use_tc(pool)) return run_tc(pool, mp, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
     p.ppu = unit_positions(p.g, true);
     p.B = (n_q + p.ppu - 1) / p.ppu;
     return run_split(pool, mp, select(pool, p.ppu * p.g, true), most_blocks(mod, p.ppu, blocks), workspace, workspace_bytes,

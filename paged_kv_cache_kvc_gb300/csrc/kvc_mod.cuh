@@ -429,7 +429,14 @@ __global__ void __launch_bounds__(kThreads) mod_kernel(const __grid_constant__ C
         if (lane == 0 && !p.stall_loads) {
             const uint32_t bar = bar_base + 8u * static_cast<uint32_t>(jj % C::R);
             if (phys < 0 || static_cast<int64_t>(phys) >= p.N) {
-                atomicOr(p.err, KVC_EBIT_BAD_BLOCK);
+                const int t = br.at(blk0 + warp + kWarps * jj) * kBS;   // an error only if some column reads it
+                for (int qi = 0; qi < rows; ++qi) {
+                    const Range r = cols[qi].r;
+                    if ((t < r.hi && t + kBS > r.lo && r.hi > r.lo) || (t < r.e && t + kBS > r.d && r.e > r.d)) {
+                        atomicOr(p.err, KVC_EBIT_BAD_BLOCK);
+                        break;
+                    }
+                }
                 mbar_arrive(bar);   // complete the phase without data; the consumer skips it
             } else {
                 const int32_t y = static_cast<int32_t>(((row_layer + phys) * p.H_KV + h) * C::BOX_ROWS);

@@ -1,0 +1,779 @@
+// Attention with modified scores on the fifth-generation tensor cores (tcgen05), scores, weights
+// and outputs in tensor memory (TMEM).  The mathematics and the masks are kvc_mod.cuh's.
+//
+// A unit is KV head h and 256 query rows: 2 x 128 / g consecutive chunk positions x the g query
+// heads of h, as two tiles of 128 rows (row r of a tile = position r / g, head h g + r mod g).  A
+// staged tile of 128 keys and values serves both.  Each query tile is its own chain
+//     S[128 x 128] = Q K^T  ->  softmax warps: P over S in TMEM  ->  O += P V
+// and the two chains fill each other's gaps: one tile's weights are computed while the tensor cores
+// run the other's products.  384 threads:
+//   warps 0..3, 4..7  softmax of tile 0, 1; thread = query row (TMEM lane)
+//   warp 8, 9         TMA producers of the key and of the value tiles (rings of 2), one 16-row box per
+//                     block and 128-byte band (one warp's boxes issue ~40 ns apart, hence two warps);
+//                     warp 9 also zeroes value rows that no row of the unit reads, once landed
+//   warp 10, 11       MMA issuers of tile 0, 1
+//
+// Work split.  The unit's key tiles (only those that some row reads, kvc_mod.cuh) of every head and
+// unit form one line of W tiles; CTA c of G takes tiles [c W / G, (c + 1) W / G), whatever units they
+// belong to, so every SM gets the same work to within a tile: a late chunk of few long rows and a
+// long triangular one alike.  A unit that lies in one CTA is written at once; a unit cut by CTA
+// borders leaves fp32 partials (at most two per CTA), and the last of its CTAs to finish merges them
+// in CTA order (the result does not depend on who is last).
+//
+// Weights.  With capped scores (and no bias) x lies in [-cap, cap], so the softmax needs no maximum:
+// 2^(x - cap / 2) fits fp32 and bf16 for caps up to 55 (80 in log2 units), and a score needs no
+// second look.  Otherwise a row's reference maximum moves when a score passes it by more than 8
+// (log2 units), and the row's outputs are rescaled in TMEM.  The weights enter the value product
+// as bf16 (their sum is taken before the rounding): a relative error of 2^-9 in each, independent,
+// which an output rounded to bf16 hides.
+#pragma once
+#include "kvc_decode_tc.cuh"
+#include "kvc_mod.cuh"
+
+namespace kvc {
+
+constexpr int kMtKeys = 128;                       // keys per tile
+constexpr int kMtBlocks = kMtKeys / kBS;
+constexpr int kMtThreads = 384;
+constexpr int kMtUnits = 2048;                     // most units (per head) of one launch
+constexpr float kMtCapLimit = 80.f;                // cap in log2 units up to which no maximum is needed
+
+struct ModTcParams {
+    ModParams m;
+    int32_t units;        // units per head
+    int32_t whole;        // 1: no partials, units are dealt whole
+    int32_t total;        // positions the row holds (prefill)
+    uint32_t *counters;   // [H_KV][units], zero between launches
+    float *part_o;        // [2 G][256][D]
+    float2 *part_ml;      // [2 G][256]
+};
+
+template <int D>
+struct ModTcCfg {
+    static constexpr int BANDS = D / 64;
+    static constexpr int BAND = 128 * 128;             // one 128-byte column band of 128 rows
+    static constexpr int TILE = BANDS * BAND;          // keys, values or queries of one tile
+    static constexpr int Q = 0;                        // [2] query tiles
+    static constexpr int K = 2 * TILE;                 // [2] key tiles
+    static constexpr int V = 4 * TILE;                 // [2] value tiles
+    static constexpr int PREFIX = 6 * TILE;            // int32 [kMtUnits + 1]
+    static constexpr int RANGE = PREFIX + ((kMtUnits + 1) * 4 + 15) / 16 * 16;   // Range [256]
+    static constexpr int BARS = RANGE + 256 * 16;
+    static constexpr int NBARS = 20;
+    static constexpr int MISC = BARS + NBARS * 8;      // scan sums [12], abort, TMEM base, merge flags [2], block masks [4]
+    static constexpr int SMEM = 1024 + MISC + 128;
+};
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+        "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+// A vote of the 128 threads of a query tile (named barrier `id`).
+__device__ __forceinline__ bool tile_all(bool v, uint32_t id)
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, %2, 128, p;\n\t"
+                 "selp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r)
+                 : "r"(v ? 1u : 0u), "r"(id)
+                 : "memory");
+    return r != 0;
+}
+
+// What a unit reads and where its pieces are; the same in every thread of a warp.
+struct UnitView {
+    int pos0, n_pos;       // chunk positions [pos0, pos0 + n_pos)
+    int a0, a1, e0, e1;    // the union of its rows' runs: [a0, a1) and [e0, e1)
+    BlockRuns br;
+    int tiles;             // key tiles (at least 1: a unit that reads nothing still writes its zeros)
+};
+
+// Whole warp (the reductions), u: unit of a head.
+__device__ __forceinline__ UnitView unit_view(const ModTcParams &p, int u, int lane)
+{
+    const DecodeParams &d = p.m.d;
+    const int ppu = 2 * d.ppu;
+    UnitView v;
+    v.pos0 = u * ppu;
+    v.n_pos = min(ppu, d.n_pos - v.pos0);
+    int a0 = 0x7FFFFFFF, a1 = 0, e0 = 0x7FFFFFFF, e1 = 0;
+    // without documents lo, hi and e grow with the position: the first and the last row bound the runs
+    const int step = p.m.doc_start ? 1 : max(1, v.n_pos - 1);
+    for (int i = lane * step; i < v.n_pos; i += 32 * step) {
+        const int c = v.pos0 + i;
+        const Range r = query_range(p.m, d.len_base + c, p.total, p.m.doc_start ? __ldg(p.m.doc_start + c) : 0);
+        if (r.hi > r.lo) {
+            a0 = min(a0, r.lo);
+            a1 = max(a1, r.hi);
+        }
+        if (r.e > r.d) {
+            e0 = min(e0, r.d);
+            e1 = max(e1, r.e);
+        }
+    }
+    v.a1 = __reduce_max_sync(kFull, a1);
+    v.a0 = v.a1 > 0 ? __reduce_min_sync(kFull, a0) : 0;
+    v.e1 = __reduce_max_sync(kFull, e1);
+    v.e0 = v.e1 > 0 ? __reduce_min_sync(kFull, e0) : 0;
+    v.br = block_runs(v.e0, v.e1, v.a0, v.a1);
+    v.tiles = max(1, (v.br.n + kMtBlocks - 1) / kMtBlocks);
+    return v;
+}
+
+// A run of key tiles [k0, k1) of (head, unit).
+struct Segment {
+    int head, unit, k0, k1, tiles;
+    int64_t start;   // the unit's first tile on the line of all tiles
+    bool ok;
+};
+
+// Walks a CTA's share of the line of tiles; every role makes the same walk.
+struct Walk {
+    const int32_t *prefix;
+    int units, per_head;
+    int64_t at, end;      // whole: unit counters instead of tile counters
+    bool whole;
+    int stride;
+    __device__ __forceinline__ Segment next()
+    {
+        Segment s;
+        s.ok = at < end;
+        if (!s.ok) return s;
+        if (whole) {
+            s.head = static_cast<int>(at / units);
+            s.unit = static_cast<int>(at % units);
+            s.tiles = prefix[s.unit + 1] - prefix[s.unit];
+            s.k0 = 0;
+            s.k1 = s.tiles;
+            s.start = 0;
+            at += stride;
+            return s;
+        }
+        s.head = static_cast<int>(at / per_head);
+        const int r = static_cast<int>(at - static_cast<int64_t>(s.head) * per_head);
+        int lo = 0, hi = units;   // prefix[lo] <= r < prefix[hi]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (prefix[mid] <= r) lo = mid;
+            else hi = mid;
+        }
+        s.unit = lo;
+        s.tiles = prefix[lo + 1] - prefix[lo];
+        s.start = static_cast<int64_t>(s.head) * per_head + prefix[lo];
+        s.k0 = static_cast<int>(at - s.start);
+        s.k1 = static_cast<int>(min(static_cast<int64_t>(s.tiles), end - s.start));
+        at = s.start + s.k1;
+        return s;
+    }
+};
+
+// FIXED: capped scores against the fixed reference; else the running reference maximum.
+template <int D, bool FIXED>
+__global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_constant__ CUtensorMap tmap16,
+                                                                const ModTcParams tp)
+{
+    using C = ModTcCfg<D>;
+    const ModParams &mp = tp.m;
+    const DecodeParams &p = mp.d;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int g = p.g, ppt = p.ppu;   // positions per query tile
+    const uint32_t sbase = smem_u32(smem);
+    int32_t *prefix = reinterpret_cast<int32_t *>(smem + C::PREFIX);
+    Range *ranges = reinterpret_cast<Range *>(smem + C::RANGE);
+    int32_t *misc = reinterpret_cast<int32_t *>(smem + C::MISC);
+    volatile int32_t *abort_sh = misc + 12;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(misc + 13);
+    volatile int32_t *last_sh = misc + 14;
+    volatile uint32_t *mask_sh = reinterpret_cast<volatile uint32_t *>(misc + 16);   // loaded blocks of key tile kt, slot kt mod 4
+    auto bar = [&](int i) { return sbase + C::BARS + 8u * static_cast<uint32_t>(i); };
+    // barriers: per ring slot, then per query tile
+    auto kfull = [&](int s) { return bar(s); };
+    auto kfree = [&](int s) { return bar(2 + s); };
+    auto vfull = [&](int s) { return bar(4 + s); };
+    auto vfree = [&](int s) { return bar(6 + s); };
+    auto vready = [&](int s) { return bar(8 + s); };
+    auto qfull = [&](int x) { return bar(10 + x); };
+    auto sfull = [&](int x) { return bar(12 + x); };
+    auto pfull = [&](int x) { return bar(14 + x); };
+    auto pvdone = [&](int x) { return bar(16 + x); };
+
+    if (tid == 0) {
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(kfull(s), 1);
+            mbar_init(kfree(s), 2);
+            mbar_init(vfull(s), 1);
+            mbar_init(vfree(s), 2);
+            mbar_init(vready(s), 1);
+            mbar_init(qfull(s), 128);
+            mbar_init(sfull(s), 1);
+            mbar_init(pfull(s), 128);
+            mbar_init(pvdone(s), 1);
+        }
+        fence_barrier_init();
+        prefetch_tensormap(&tmap16);
+        *abort_sh = 0;
+    }
+    if (warp == 0) {
+        tmem_alloc(smem_u32(tmem_slot), 512);
+        tmem_relinquish();
+    }
+    allow_dependent_launch();
+    grid_dependency_wait();
+
+    // ---- tiles per unit and their running sum (12 warps, one unit each at a time)
+    for (int u = warp; u < tp.units; u += kMtThreads / 32) {
+        const UnitView v = unit_view(tp, u, lane);
+        if (lane == 0) prefix[u + 1] = v.tiles;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    {
+        const int per = (tp.units + kMtThreads - 1) / kMtThreads, b = tid * per, e = min(tp.units, b + per);
+        int sum = 0;
+        for (int u = b; u < e; ++u) sum += prefix[u + 1];
+        int inc = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int t = __shfl_up_sync(kFull, inc, o);
+            if (lane >= o) inc += t;
+        }
+        if (lane == 31) misc[warp] = inc;
+        __syncthreads();
+        int before = inc - sum;
+        for (int w = 0; w < warp; ++w) before += misc[w];
+        for (int u = b; u < e; ++u) {
+            before += prefix[u + 1];
+            prefix[u + 1] = before;
+        }
+        if (tid == 0) prefix[0] = 0;
+        __syncthreads();
+    }
+    Walk walk;
+    walk.prefix = prefix;
+    walk.units = tp.units;
+    walk.per_head = prefix[tp.units];
+    walk.whole = tp.whole != 0;
+    walk.stride = gridDim.x;
+    const int64_t W = static_cast<int64_t>(p.H_KV) * walk.per_head;
+    const int64_t G = min(static_cast<int64_t>(gridDim.x), W);
+    if (walk.whole) {
+        walk.at = blockIdx.x;
+        walk.end = static_cast<int64_t>(p.H_KV) * tp.units;
+    } else {
+        const bool idle = blockIdx.x >= G;
+        walk.at = idle ? 0 : blockIdx.x * W / G;
+        walk.end = idle ? 0 : (blockIdx.x + 1) * W / G;
+    }
+
+    const uint32_t tm_s[2] = {tmem, tmem + 128}, tm_o[2] = {tmem + 256, tmem + 384};
+    bool timed_out = false;
+    auto wait = [&](uint32_t b, uint32_t parity) {   // whole warp; false: the CTA gives up
+        const bool ok = mbar_wait_bounded(b, parity);
+        if (__all_sync(kFull, ok) && *abort_sh == 0) return true;
+        *abort_sh = 1;
+        timed_out = true;
+        return false;
+    };
+
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if (warp <= 9) {
+            // -------------------------------------------------------- TMA producers: keys (8), values (9)
+            const bool values = warp == 9;
+            const int64_t row_layer = static_cast<int64_t>(p.layer) * p.N;
+            const int bl = lane & (kMtBlocks - 1), band = lane >> 3;
+            const bool box = lane < kMtBlocks * C::BANDS;
+            uint32_t kt = 0;   // tiles so far
+            int prev_slot = -1, prev_unit = -1;
+            uint32_t prev_mask = 0, prev_parity = 0;
+            int prev_tile = 0;
+            UnitView v{}, pv{};
+            // values: once the previous tile has landed, zero the rows that nothing reads, then pass it on
+            auto finish = [&]() -> bool {
+                if (prev_slot < 0) return true;
+                if (!wait(vfull(prev_slot), prev_parity)) return false;
+                const int first = prev_tile * kMtBlocks;
+                const bool one_run = first + kMtBlocks <= pv.br.n && (first + kMtBlocks <= pv.br.n0 || first >= pv.br.n0);
+                const int t0 = pv.br.at(first) * kBS;
+                const bool clean = one_run && prev_mask == (1u << kMtBlocks) - 1u && !mp.doc_start &&
+                                   ((t0 >= pv.a0 && t0 + kMtKeys <= pv.a1) || (t0 >= pv.e0 && t0 + kMtKeys <= pv.e1));
+                if (!clean) {
+                    const uint32_t st = sbase + C::V + prev_slot * C::TILE;
+                    for (int k = lane; k < kMtKeys; k += 32) {
+                        const int vb = first + k / kBS;
+                        bool used = vb < pv.br.n && (prev_mask >> (k / kBS) & 1u);
+                        if (used) {
+                            const int t = pv.br.at(vb) * kBS + k % kBS;
+                            // rows at consecutive positions read consecutive runs, so without documents
+                            // the union has no holes; with them each row of the unit is asked
+                            used = (t >= pv.a0 && t < pv.a1) || (t >= pv.e0 && t < pv.e1);
+                            if (used && mp.doc_start) {
+                                used = false;
+                                for (int i = 0; i < pv.n_pos && !used; ++i) {
+                                    const int c = pv.pos0 + i;
+                                    const Range r = query_range(mp, p.len_base + c, tp.total, __ldg(mp.doc_start + c));
+                                    used = (t >= r.lo && t < r.hi) || (t >= r.d && t < r.e);
+                                }
+                            }
+                        }
+                        if (!used)
+#pragma unroll
+                            for (int c = 0; c < 8 * C::BANDS; ++c)
+                                sts128_zero(st + (c >> 3) * C::BAND + sw128(k, c & 7));
+                    }
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(vready(prev_slot));
+                prev_slot = -1;
+                return true;
+            };
+            bool go = true;
+            for (Segment s = walk.next(); go && s.ok; s = walk.next()) {
+                v = unit_view(tp, s.unit, lane);
+                auto entry = [&](int k) -> int32_t {   // table entry of this lane's block of tile k
+                    const int vb = k * kMtBlocks + bl;
+                    return k < s.k1 && vb < v.br.n ? __ldg(p.bt + v.br.at(vb)) : -1;
+                };
+                auto is_read = [&](int t) {   // some row of the unit reads a position of block [t, t + 16)
+                    for (int i = 0; i < v.n_pos; ++i) {
+                        const int c = v.pos0 + i;
+                        const Range r = query_range(mp, p.len_base + c, tp.total, mp.doc_start ? __ldg(mp.doc_start + c) : 0);
+                        if ((t < r.hi && t + kBS > r.lo && r.hi > r.lo) || (t < r.e && t + kBS > r.d && r.e > r.d)) return true;
+                    }
+                    return false;
+                };
+                int32_t e_next = entry(s.k0);
+                for (int k = s.k0; k < s.k1; ++k, ++kt) {
+                    const int slot = kt & 1;
+                    const int32_t e = e_next;
+                    e_next = entry(k + 1);
+                    if (kt >= 2) {
+                        const uint32_t fb = values ? vfree(slot) : kfree(slot), fp = ((kt >> 1) - 1) & 1;
+                        // while the slot is in use, pass the previous value tile on first
+                        if (values && !__any_sync(kFull, lane == 0 && mbar_test_wait(fb, fp)) && !finish()) {
+                            go = false;
+                            break;
+                        }
+                        if (!wait(fb, fp)) {
+                            go = false;
+                            break;
+                        }
+                    }
+                    const int vb = k * kMtBlocks + bl;
+                    const bool have = vb < v.br.n, ok = have && e >= 0 && static_cast<int64_t>(e) < p.N;
+                    if (!values && band == 0 && have && !ok && is_read(v.br.at(vb) * kBS)) atomicOr(p.err, KVC_EBIT_BAD_BLOCK);
+                    const uint32_t mask = __ballot_sync(kFull, ok && lane < kMtBlocks);
+                    if (!values && lane == 0) mask_sh[kt & 3] = mask;   // published by the arrive below
+                    const uint32_t full = values ? vfull(slot) : kfull(slot);
+                    if (p.stall_loads) {   // the test hook withholds every load
+                    } else if (mask == 0u) {
+                        if (lane == 0) mbar_arrive(full);
+                    } else if (lane == 0) {
+                        mbar_arrive_expect_tx(full, static_cast<uint32_t>(__popc(mask)) * C::BANDS * (kBS * 128u));
+                    }
+                    __syncwarp();
+                    if (box && ok && !p.stall_loads) {
+                        const int32_t y = static_cast<int32_t>(((row_layer + e) * p.H_KV + s.head) * (2 * kBS)) + (values ? kBS : 0);
+                        tma_load_2d(sbase + (values ? C::V : C::K) + slot * C::TILE + band * C::BAND + bl * (kBS * 128),
+                                    &tmap16, full, band * 64, y);
+                    }
+                    if (values) {
+                        if (!finish()) {
+                            go = false;
+                            break;
+                        }
+                        prev_slot = slot;
+                        prev_parity = (kt >> 1) & 1;
+                        prev_mask = mask;
+                        prev_tile = k;
+                        if (prev_unit != s.unit) {
+                            pv = v;
+                            prev_unit = s.unit;
+                        }
+                    }
+                }
+            }
+            if (values && go) go = finish();
+            // before the CTA ends: every copy issued has landed (immediate unless a wait expired)
+            if (!p.stall_loads)
+                for (uint32_t t = kt >= 2 ? kt - 2 : 0; t < kt; ++t)
+                    (void)mbar_wait_bounded(values ? vfull(t & 1) : kfull(t & 1), (t >> 1) & 1, 100000000ull);
+            __syncwarp();
+        } else {
+            // -------------------------------------------------------- MMA issuer of query tile x
+            const int x = warp - 10;
+            constexpr uint32_t idesc_qk = tc_idesc_f16(128, kMtKeys, true, false, false);
+            constexpr uint32_t idesc_pv = tc_idesc_f16(128, D, true, false, true);
+            const uint64_t desc_q = tc_smem_desc(sbase + C::Q + x * C::TILE, 16, 1024, kSwizzle128B);
+            uint32_t kt = 0, it = 0, seg = 0;   // key tiles, this query tile's steps and its segments so far
+            bool go = true;
+            for (Segment s = walk.next(); go && s.ok; s = walk.next()) {
+                // the second tile may hold no position: it only lets the key and value tiles go
+                const bool mine = s.unit * 2 * ppt + x * ppt < p.n_pos;
+                if (mine) {
+                    if (!wait(qfull(x), seg & 1)) break;
+                    ++seg;
+                    tc_fence_after();
+                }
+                for (int k = s.k0; k < s.k1; ++k, ++kt) {
+                    const int slot = kt & 1;
+                    const uint32_t par = (kt >> 1) & 1;
+                    if (!wait(kfull(slot), par)) {
+                        go = false;
+                        break;
+                    }
+                    if (!mine) {
+                        if (lane == 0) mbar_arrive(kfree(slot));
+                        if (!wait(vready(slot), par)) {
+                            go = false;
+                            break;
+                        }
+                        if (lane == 0) mbar_arrive(vfree(slot));
+                        __syncwarp();
+                        continue;
+                    }
+                    // S over the weights of the step before, whose product has been waited for below
+                    const uint64_t b0 = tc_smem_desc(sbase + C::K + slot * C::TILE, 16, 1024, kSwizzle128B);
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        tc_mma_f16_warp(tm_s[x], tc_desc_advance(desc_q, (kk >> 2) * C::BAND + (kk & 3) * 32),
+                                        tc_desc_advance(b0, (kk >> 2) * C::BAND + (kk & 3) * 32), idesc_qk, kk > 0 ? 1u : 0u);
+                    tc_commit_warp(sfull(x));
+                    tc_commit_warp(kfree(slot));
+                    if (!wait(vready(slot), par) || !wait(pfull(x), it & 1)) {
+                        go = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t v0 = tc_smem_desc(sbase + C::V + slot * C::TILE, C::BAND, 1024, kSwizzle128B);
+#pragma unroll
+                    for (int kk = 0; kk < kMtKeys / 16; ++kk)   // 16 keys: 8 columns of P, 2048 bytes of value rows
+                        tc_mma_f16_tmem_a_warp(tm_o[x], tm_s[x] + kk * 8, tc_desc_advance(v0, kk * 2048), idesc_pv,
+                                               (k > s.k0 || kk > 0) ? 1u : 0u);
+                    tc_commit_warp(vfree(slot));
+                    tc_commit_warp(pvdone(x));
+                    if (!wait(pvdone(x), it & 1)) {
+                        go = false;
+                        break;
+                    }
+                    ++it;
+                }
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        // ------------------------------------------------------------ softmax of query tile x
+        const int x = warp >> 2, row = tid & 127;
+        const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t ts = tm_s[x] + lane_off, to = tm_o[x] + lane_off;
+        const float ref = 0.5f * mp.cap_out;
+        uint32_t it = 0, kt = 0;   // this query tile's steps, key tiles so far
+        int piece = 0;             // segments so far
+        for (Segment s = walk.next(); s.ok; s = walk.next(), ++piece) {
+            const uint32_t kt0 = kt;
+            kt += s.k1 - s.k0;
+            const UnitView v = unit_view(tp, s.unit, lane);
+            const int c0 = v.pos0 + x * ppt, c = c0 + row / g;   // chunk position of this row
+            const bool mine = c0 < p.n_pos;
+            const bool real = row < ppt * g && c < p.n_pos;
+            const size_t orow = static_cast<size_t>(c) * p.H_Q + s.head * g + row % g;
+            if (!mine) continue;   // the same for the whole CTA
+            // ---- queries into shared memory (zero where there is none)
+#pragma unroll 4
+            for (int i = tid & 127; i < 128 * (D / 8); i += 128) {
+                const int r = i / (D / 8), ch = i % (D / 8), cp = c0 + r / g;
+                uint4 q = make_uint4(0u, 0u, 0u, 0u);
+                if (r < ppt * g && cp < p.n_pos)
+                    q = __ldg(reinterpret_cast<const uint4 *>(p.q + (static_cast<size_t>(cp) * p.H_Q + s.head * g + r % g) * D) + ch);
+                sts128(sbase + C::Q + x * C::TILE + (ch >> 3) * C::BAND + sw128(r, ch & 7), q);
+            }
+            fence_proxy_async_smem();
+            tc_fence_before();   // this thread's reads of the last segment's outputs
+            mbar_arrive(qfull(x));
+            Range r{0, 0, 0, 0};
+            float slope = 0.f;
+            const int pos = p.len_base + c;
+            if (real) {
+                r = query_range(mp, pos, tp.total, mp.doc_start ? __ldg(mp.doc_start + c) : 0);
+                if (mp.alibi) slope = __ldg(mp.alibi + s.head * g + row % g) * 1.4426950408889634f;
+            }
+            // every real row of the warp reads [flo, fhi) and [fd, fe)
+            const int flo = __reduce_max_sync(kFull, real ? r.lo : 0), fhi = __reduce_min_sync(kFull, real ? r.hi : 0x7FFFFFFF);
+            const int fd = __reduce_max_sync(kFull, real ? r.d : 0), fe = __reduce_min_sync(kFull, real ? r.e : 0x7FFFFFFF);
+            const bool any_real = __any_sync(kFull, real);
+            float m = FIXED ? ref : -INFINITY, l = 0.f;
+            bool go = true;
+            for (int k = s.k0; k < s.k1; ++k, ++it) {
+                if (!wait(sfull(x), it & 1)) {
+                    go = false;
+                    break;
+                }
+                tc_fence_after();
+                if (!any_real) {   // rows past the chunk: their weights stay in their own lanes and are never read
+                    mbar_arrive(pfull(x));
+                    continue;
+                }
+                const int first = k * kMtBlocks;
+                const bool one_run = first + kMtBlocks <= v.br.n && (first + kMtBlocks <= v.br.n0 || first >= v.br.n0);
+                const int t0 = v.br.at(first) * kBS;
+                const uint32_t loaded = mask_sh[(kt0 + (k - s.k0)) & 3];
+                const bool full = one_run && loaded == (1u << kMtBlocks) - 1u && ((t0 >= flo && t0 + kMtKeys <= fhi) || (t0 >= fd && t0 + kMtKeys <= fe));
+                // bit i of a 16-key block's mask: this row reads the block's key i
+                auto block_mask = [&](int b) -> uint32_t {
+                    const int vb = first + b;
+                    if (vb >= v.br.n || !(loaded >> b & 1u)) return 0u;
+                    const int t = v.br.at(vb) * kBS;
+                    auto below = [&](int end) -> uint32_t {   // keys of the block before position `end`
+                        return end <= t ? 0u : (end >= t + kBS ? 0xFFFFu : (1u << (end - t)) - 1u);
+                    };
+                    return (below(r.hi) & ~below(r.lo)) | (below(r.e) & ~below(r.d));
+                };
+                if constexpr (FIXED) {
+                    float ls[4] = {0.f, 0.f, 0.f, 0.f};
+                    uint32_t buf[2][32];
+                    tmem_ld32(ts, buf[0]);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        tmem_ld_wait(buf[q & 1]);
+                        if (q < 3) tmem_ld32(ts + 32 * (q + 1), buf[(q + 1) & 1]);
+                        uint32_t (&sv)[32] = buf[q & 1];
+                        const uint32_t seen = full ? 0xFFFFFFFFu : (block_mask(2 * q) | (block_mask(2 * q + 1) << 16));
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            float w[2];
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) {
+                                float rc;
+                                asm("rcp.approx.ftz.f32 %0, %1;"
+                                    : "=f"(rc)
+                                    : "f"(1.f + fast_exp2(__uint_as_float(sv[i + u]) * mp.cap_in)));
+                                w[u] = fast_exp2(fmaf(-2.f * mp.cap_out, rc, ref));   // 2^(x - cap / 2)
+                            }
+                            if (!full) {
+                                w[0] = (seen >> i) & 1u ? w[0] : 0.f;
+                                w[1] = (seen >> (i + 1)) & 1u ? w[1] : 0.f;
+                            }
+                            ls[(i / 2) & 3] += w[0] + w[1];
+                            pk[i / 2] = pack_bf16(w[0], w[1]);
+                        }
+                        tmem_st16(ts + 16 * q, pk);   // over scores already read
+                    }
+                    l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+                } else {
+                    float sv[128];
+                    {
+                        uint32_t raw[4][32];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) tmem_ld32(ts + 32 * q, raw[q]);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            tmem_ld_wait(raw[q]);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) sv[32 * q + i] = __uint_as_float(raw[q][i]);
+                        }
+                    }
+                    if (mp.capped) {
+#pragma unroll
+                        for (int i = 0; i < 128; ++i) sv[i] = modified(mp, sv[i]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 128; ++i) sv[i] *= p.scale_log2;
+                    }
+                    if (mp.alibi) {
+#pragma unroll
+                        for (int b = 0; b < kMtBlocks; ++b) {
+                            const int vb = min(first + b, max(v.br.n - 1, 0));
+                            const float away = static_cast<float>(pos - v.br.at(vb) * kBS);
+#pragma unroll
+                            for (int i = 0; i < kBS; ++i)
+                                sv[kBS * b + i] = fmaf(-slope, fabsf(away - static_cast<float>(i)), sv[kBS * b + i]);
+                        }
+                    }
+                    if (!full) {
+#pragma unroll
+                        for (int b = 0; b < kMtBlocks; ++b) {
+                            const uint32_t seen = block_mask(b);
+#pragma unroll
+                            for (int i = 0; i < kBS; ++i) sv[kBS * b + i] = (seen >> i) & 1u ? sv[kBS * b + i] : -INFINITY;
+                        }
+                    }
+                    float b0 = sv[0], b1 = sv[1], b2 = sv[2], b3 = sv[3];
+#pragma unroll
+                    for (int i = 4; i < 124; i += 8) {
+                        b0 = max3f(b0, sv[i], sv[i + 1]);
+                        b1 = max3f(b1, sv[i + 2], sv[i + 3]);
+                        b2 = max3f(b2, sv[i + 4], sv[i + 5]);
+                        b3 = max3f(b3, sv[i + 6], sv[i + 7]);
+                    }
+                    b0 = max3f(b0, sv[124], sv[125]);
+                    b1 = max3f(b1, sv[126], sv[127]);
+                    const float bm = max3f(b0, b1, fmaxf(b2, b3));
+                    const bool move = bm > m + kRescaleSlack;   // false while nothing has been read
+                    float alpha = 1.f;
+                    if (move) {
+                        alpha = fast_exp2(m - bm);
+                        m = bm;
+                        l *= alpha;
+                    }
+                    // the products before this tile's scores are complete (the issuer waited): O may be rescaled
+                    if (k > s.k0 && __any_sync(kFull, move && alpha != 1.f)) {
+#pragma unroll
+                        for (int part = 0; part < D / 16; ++part) {
+                            uint32_t o[16];
+                            asm volatile(
+                                "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+                                "%12, %13, %14, %15}, [%16];\n\ttcgen05.wait::ld.sync.aligned;"
+                                : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]),
+                                  "=r"(o[7]), "=r"(o[8]), "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]),
+                                  "=r"(o[14]), "=r"(o[15])
+                                : "r"(to + part * 16)
+                                : "memory");
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                            tmem_st16(to + part * 16, o);
+                        }
+                    }
+                    const float neg_m = m == -INFINITY ? 0.f : -m;
+                    float ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            const float w0 = fast_exp2(sv[32 * q + i] + neg_m), w1 = fast_exp2(sv[32 * q + i + 1] + neg_m);
+                            ls[(i / 2) & 3] += w0 + w1;
+                            pk[i / 2] = pack_bf16(w0, w1);
+                        }
+                        tmem_st16(ts + 16 * q, pk);
+                    }
+                    l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(pfull(x));
+            }
+            if (go) go = wait(pvdone(x), (it - 1) & 1);
+            // every thread of the query tile takes this vote once per segment, so the barriers below meet
+            if (!tile_all(go, 4 + x)) {
+                timed_out = true;
+                break;
+            }
+            tc_fence_after();
+
+            // ---- epilogue: the unit's rows, or a piece of them
+            const bool done = s.k0 == 0 && s.k1 == s.tiles;
+            const int64_t mypart = 2 * static_cast<int64_t>(blockIdx.x) + (piece > 0 ? 1 : 0);
+            const int prow = x * 128 + row;
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            if (any_real) {
+#pragma unroll
+                for (int part = 0; part < D / 32; ++part) {
+                    uint32_t o[32];
+                    tmem_ld32(to + part * 32, o);
+                    tmem_ld_wait(o);
+                    if (!real) continue;
+                    if (done) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(mp.out + orow * D + part * 32);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int u = 0; u < 4; ++u)
+                                w[u] = l == 0.f ? 0u : pack_bf16(__uint_as_float(o[8 * i + 2 * u]) * inv,
+                                                                 __uint_as_float(o[8 * i + 2 * u + 1]) * inv);
+                            dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    } else {
+                        float4 *dst = reinterpret_cast<float4 *>(tp.part_o) + (mypart * (D / 4) + part * 8) * 256 + prow;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)   // [channel / 4][row]: a warp's rows are contiguous
+                            dst[i * 256] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                                       __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+                    }
+                }
+            }
+            if (real && done && p.lse) p.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+            if (done) continue;
+            if (real) tp.part_ml[mypart * 256 + prow] = make_float2(m, l);
+            // ---- the unit's last CTA merges its pieces, tile by tile (each query tile counts on its own)
+            const int64_t a = s.start, b = s.start + s.tiles;
+            const int64_t cf = ((a + 1) * G - 1) / W, cl = (b * G - 1) / W;   // CTAs holding its first and last tile
+            const int n = static_cast<int>(cl - cf) + 1;
+            __threadfence();
+            asm volatile("bar.sync %0, 128;" ::"r"(4 + x) : "memory");
+            if (row == 0) {
+                uint32_t *ctr = tp.counters + 2 * (static_cast<size_t>(s.head) * tp.units + s.unit) + x;
+                const uint32_t before = atomicAdd(ctr, 1u);
+                last_sh[x] = before == static_cast<uint32_t>(n - 1);
+                if (before == static_cast<uint32_t>(n - 1)) *ctr = 0u;   // ready for the next launch
+            }
+            asm volatile("bar.sync %0, 128;" ::"r"(4 + x) : "memory");
+            const bool last = last_sh[x] != 0;
+            asm volatile("bar.sync %0, 128;" ::"r"(4 + x) : "memory");   // last_sh may be written again
+            if (!last) continue;
+            __threadfence();
+            const bool first_second = cf * W / G < a;   // the first CTA's piece is its second one
+            auto part_of = [&](int i) { return 2 * (cf + i) + (i == 0 && first_second ? 1 : 0); };
+            const int nrows = min(ppt, p.n_pos - c0) * g;
+            // items (row, 8 channels): lanes on consecutive rows
+            for (int i = row; i < ((nrows + 31) & ~31) * (D / 8); i += 128) {
+                const int rr = i % ((nrows + 31) & ~31), d8 = i / ((nrows + 31) & ~31);
+                if (rr >= nrows) continue;
+                const int pr = x * 128 + rr;
+                float M = -INFINITY;
+                for (int t = 0; t < n; ++t) {
+                    const float2 ml = __ldcg(tp.part_ml + part_of(t) * 256 + pr);
+                    if (ml.y != 0.f) M = fmaxf(M, ml.x);
+                }
+                float L = 0.f, acc[8] = {};
+#pragma unroll 4
+                for (int t = 0; t < n; ++t) {
+                    const int64_t pt = part_of(t);
+                    const float2 ml = __ldcg(tp.part_ml + pt * 256 + pr);
+                    const float4 *src = reinterpret_cast<const float4 *>(tp.part_o) + (pt * (D / 4) + 2 * d8) * 256 + pr;
+                    const float4 u0 = __ldcg(src), u1 = __ldcg(src + 256);
+                    if (ml.y == 0.f) continue;   // the piece reads nothing for this row
+                    const float e = fast_exp2(ml.x - M);
+                    L = fmaf(e, ml.y, L);
+                    acc[0] = fmaf(e, u0.x, acc[0]);
+                    acc[1] = fmaf(e, u0.y, acc[1]);
+                    acc[2] = fmaf(e, u0.z, acc[2]);
+                    acc[3] = fmaf(e, u0.w, acc[3]);
+                    acc[4] = fmaf(e, u1.x, acc[4]);
+                    acc[5] = fmaf(e, u1.y, acc[5]);
+                    acc[6] = fmaf(e, u1.z, acc[6]);
+                    acc[7] = fmaf(e, u1.w, acc[7]);
+                }
+                const size_t ob = static_cast<size_t>(c0 + rr / g) * p.H_Q + s.head * g + rr % g;
+                const float li = L == 0.f ? 0.f : 1.f / L;
+                *reinterpret_cast<uint4 *>(mp.out + ob * D + 8 * d8) =
+                    make_uint4(pack_bf16(acc[0] * li, acc[1] * li), pack_bf16(acc[2] * li, acc[3] * li),
+                               pack_bf16(acc[4] * li, acc[5] * li), pack_bf16(acc[6] * li, acc[7] * li));
+                if (d8 == 0 && p.lse) p.lse[ob] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+            }
+        }
+    }
+    if (timed_out && lane == 0) atomicOr(p.err, KVC_EBIT_TIMEOUT);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// The tensor-memory kernel for a head width (bf16 pools); fixed: capped scores against a fixed reference.
+DecodeKernel select_mod_tc(int D, bool fixed);
+
+}  // namespace kvc
