@@ -3,10 +3,11 @@
 //
 // A unit is KV head h and 256 query rows: 2 x 128 / g consecutive chunk positions x the g query
 // heads of h, as two tiles of 128 rows (row r of a tile = position r / g, head h g + r mod g).  A
-// staged tile of 128 keys and values serves both.  Each query tile is its own chain
-//     S[128 x 128] = Q K^T  ->  softmax warps: P over S in TMEM  ->  O += P V
-// and the two chains fill each other's gaps: one tile's weights are computed while the tensor cores
-// run the other's products.  384 threads:
+// staged tile of 128 keys and values serves both.  Each query tile is its own chain of 64-key steps
+//     S[128 x 64] = Q K^T  ->  softmax warps: P over S in TMEM  ->  O += P V
+// with two score buffers, so that a step's scores are there when the softmax warps are done with the
+// step before.  (One 128-key buffer per query tile measured 1.7x slower: the two chains fell into
+// step, both computing weights, then both waiting for the tensor cores.)  384 threads:
 //   warps 0..3, 4..7  softmax of tile 0, 1; thread = query row (TMEM lane)
 //   warp 8, 9         TMA producers of the key and of the value tiles (rings of 2), one 16-row box per
 //                     block and 128-byte band (one warp's boxes issue ~40 ns apart, hence two warps);
@@ -34,6 +35,8 @@ namespace kvc {
 
 constexpr int kMtKeys = 128;                       // keys per tile
 constexpr int kMtBlocks = kMtKeys / kBS;
+constexpr int kMtStep = 64;                        // keys per score buffer
+constexpr int kMtStepBlocks = kMtStep / kBS;
 constexpr int kMtThreads = 384;
 constexpr int kMtUnits = 2048;                     // most units (per head) of one launch
 constexpr float kMtCapLimit = 80.f;                // cap in log2 units up to which no maximum is needed
@@ -59,13 +62,24 @@ struct ModTcCfg {
     static constexpr int PREFIX = 6 * TILE;            // int32 [kMtUnits + 1]
     static constexpr int RANGE = PREFIX + ((kMtUnits + 1) * 4 + 15) / 16 * 16;   // Range [256]
     static constexpr int BARS = RANGE + 256 * 16;
-    static constexpr int NBARS = 20;
+    static constexpr int NBARS = 24;
     static constexpr int MISC = BARS + NBARS * 8;      // scan sums [12], abort, TMEM base, merge flags [2], block masks [4]
     static constexpr int SMEM = 1024 + MISC + 128;
 };
 
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16])
+// Scale 16 columns of this thread's TMEM lane (whole warp).
+__device__ __forceinline__ void tmem_scale16(uint32_t taddr, float f)
 {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+        "[%16];\n\ttcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
         "%15, %16};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
@@ -83,6 +97,53 @@ __device__ __forceinline__ bool tile_all(bool v, uint32_t id)
                  : "r"(v ? 1u : 0u), "r"(id)
                  : "memory");
     return r != 0;
+}
+
+// Two fp32 values per instruction.
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 f32x2_of(float lo, float hi)
+{
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float lo2(f32x2 v) { return __uint_as_float(static_cast<uint32_t>(v)); }
+__device__ __forceinline__ float hi2(f32x2 v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b)
+{
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b)
+{
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c)
+{
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b)   // NaN stays NaN
+{
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float fast_rcp(float x)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t ld_acquire(const uint32_t *a)
+{
+    uint32_t r;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(r) : "l"(a) : "memory");
+    return r;
 }
 
 // What a unit reads and where its pieces are; the same in every thread of a warp.
@@ -200,9 +261,9 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
     auto vfree = [&](int s) { return bar(6 + s); };
     auto vready = [&](int s) { return bar(8 + s); };
     auto qfull = [&](int x) { return bar(10 + x); };
-    auto sfull = [&](int x) { return bar(12 + x); };
-    auto pfull = [&](int x) { return bar(14 + x); };
-    auto pvdone = [&](int x) { return bar(16 + x); };
+    auto sfull = [&](int x, int b) { return bar(12 + 2 * x + b); };   // per query tile and score buffer
+    auto pfull = [&](int x, int b) { return bar(16 + 2 * x + b); };
+    auto pvdone = [&](int x, int b) { return bar(20 + 2 * x + b); };
 
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
@@ -212,9 +273,11 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
             mbar_init(vfree(s), 2);
             mbar_init(vready(s), 1);
             mbar_init(qfull(s), 128);
-            mbar_init(sfull(s), 1);
-            mbar_init(pfull(s), 128);
-            mbar_init(pvdone(s), 1);
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(sfull(s, b), 1);
+                mbar_init(pfull(s, b), 128);
+                mbar_init(pvdone(s, b), 1);
+            }
         }
         fence_barrier_init();
         prefetch_tensormap(&tmap16);
@@ -274,18 +337,22 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
         walk.end = idle ? 0 : (blockIdx.x + 1) * W / G;
     }
 
-    const uint32_t tm_s[2] = {tmem, tmem + 128}, tm_o[2] = {tmem + 256, tmem + 384};
+    // TMEM columns: query tile x has its score buffers at 128 x and 128 x + 64, its outputs at 256 + 128 x
     bool timed_out = false;
-    auto wait = [&](uint32_t b, uint32_t parity) {   // whole warp; false: the CTA gives up
-        const bool ok = mbar_wait_bounded(b, parity);
-        if (__all_sync(kFull, ok) && *abort_sh == 0) return true;
+    // Whole warp; false: the wait expired (2 s) here or elsewhere in the CTA, which gives up.
+    auto wait = [&](uint32_t b, uint32_t parity) {
+        if (__all_sync(kFull, mbar_try_wait(b, parity))) return true;
+        const uint64_t since = globaltimer_ns();
+        for (uint32_t i = 1;; ++i) {
+            if (__all_sync(kFull, mbar_try_wait(b, parity))) return true;
+            if ((i & 15u) == 0u && __any_sync(kFull, *abort_sh != 0 || globaltimer_ns() - since > 2000000000ull)) break;
+        }
         *abort_sh = 1;
         timed_out = true;
         return false;
     };
 
     if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (warp <= 9) {
             // -------------------------------------------------------- TMA producers: keys (8), values (9)
             const bool values = warp == 9;
@@ -412,70 +479,71 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
         } else {
             // -------------------------------------------------------- MMA issuer of query tile x
             const int x = warp - 10;
-            constexpr uint32_t idesc_qk = tc_idesc_f16(128, kMtKeys, true, false, false);
+            constexpr uint32_t idesc_qk = tc_idesc_f16(128, kMtStep, true, false, false);
             constexpr uint32_t idesc_pv = tc_idesc_f16(128, D, true, false, true);
             const uint64_t desc_q = tc_smem_desc(sbase + C::Q + x * C::TILE, 16, 1024, kSwizzle128B);
+            const uint32_t tm_s = tmem + 128 * x, tm_o = tmem + 256 + 128 * x;
             uint32_t kt = 0, it = 0, seg = 0;   // key tiles, this query tile's steps and its segments so far
+            // scores of step i of a segment whose first key tile is the CTA's kt0-th
+            auto scores = [&](uint32_t kt0, uint32_t i) -> bool {
+                const uint32_t tile = kt0 + (i >> 1), slot = tile & 1, half = i & 1;
+                if (half == 0 && !wait(kfull(slot), (tile >> 1) & 1)) return false;
+                tc_fence_after();
+                const uint64_t b0 = tc_smem_desc(sbase + C::K + slot * C::TILE + half * (kMtStep * 128), 16, 1024, kSwizzle128B);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)   // 16 channels (32 bytes) per MMA, 4 per 128-byte band
+                    tc_mma_f16_warp(tm_s + half * kMtStep, tc_desc_advance(desc_q, (kk >> 2) * C::BAND + (kk & 3) * 32),
+                                    tc_desc_advance(b0, (kk >> 2) * C::BAND + (kk & 3) * 32), idesc_qk, kk > 0 ? 1u : 0u);
+                tc_commit_warp(sfull(x, half));
+                if (half == 1) tc_commit_warp(kfree(slot));
+                return true;
+            };
             bool go = true;
             for (Segment s = walk.next(); go && s.ok; s = walk.next()) {
+                const int n = s.k1 - s.k0;
                 // the second tile may hold no position: it only lets the key and value tiles go
-                const bool mine = s.unit * 2 * ppt + x * ppt < p.n_pos;
-                if (mine) {
-                    if (!wait(qfull(x), seg & 1)) break;
-                    ++seg;
-                    tc_fence_after();
-                }
-                for (int k = s.k0; k < s.k1; ++k, ++kt) {
-                    const int slot = kt & 1;
-                    const uint32_t par = (kt >> 1) & 1;
-                    if (!wait(kfull(slot), par)) {
-                        go = false;
-                        break;
-                    }
-                    if (!mine) {
-                        if (lane == 0) mbar_arrive(kfree(slot));
-                        if (!wait(vready(slot), par)) {
-                            go = false;
-                            break;
-                        }
-                        if (lane == 0) mbar_arrive(vfree(slot));
+                if (s.unit * 2 * ppt + x * ppt >= p.n_pos) {
+                    for (int k = 0; go && k < n; ++k, ++kt) {
+                        const int slot = kt & 1;
+                        const uint32_t par = (kt >> 1) & 1;
+                        go = wait(kfull(slot), par);
+                        if (go && lane == 0) mbar_arrive(kfree(slot));
+                        go = go && wait(vready(slot), par);
+                        if (go && lane == 0) mbar_arrive(vfree(slot));
                         __syncwarp();
-                        continue;
                     }
-                    // S over the weights of the step before, whose product has been waited for below
-                    const uint64_t b0 = tc_smem_desc(sbase + C::K + slot * C::TILE, 16, 1024, kSwizzle128B);
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk)
-                        tc_mma_f16_warp(tm_s[x], tc_desc_advance(desc_q, (kk >> 2) * C::BAND + (kk & 3) * 32),
-                                        tc_desc_advance(b0, (kk >> 2) * C::BAND + (kk & 3) * 32), idesc_qk, kk > 0 ? 1u : 0u);
-                    tc_commit_warp(sfull(x));
-                    tc_commit_warp(kfree(slot));
-                    if (!wait(vready(slot), par) || !wait(pfull(x), it & 1)) {
+                    continue;
+                }
+                if (!wait(qfull(x), seg & 1)) break;
+                ++seg;
+                tc_fence_after();
+                go = scores(kt, 0) && scores(kt, 1);
+                for (uint32_t i = 0; go && i < 2u * n; ++i, ++it) {
+                    const uint32_t tile = kt + (i >> 1), slot = tile & 1, half = i & 1, par = (it >> 1) & 1;
+                    if ((half == 0 && !wait(vready(slot), (tile >> 1) & 1)) || !wait(pfull(x, half), par)) {
                         go = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint64_t v0 = tc_smem_desc(sbase + C::V + slot * C::TILE, C::BAND, 1024, kSwizzle128B);
+                    const uint64_t v0 = tc_smem_desc(sbase + C::V + slot * C::TILE + half * (kMtStep * 128), C::BAND, 1024,
+                                                     kSwizzle128B);
 #pragma unroll
-                    for (int kk = 0; kk < kMtKeys / 16; ++kk)   // 16 keys: 8 columns of P, 2048 bytes of value rows
-                        tc_mma_f16_tmem_a_warp(tm_o[x], tm_s[x] + kk * 8, tc_desc_advance(v0, kk * 2048), idesc_pv,
-                                               (k > s.k0 || kk > 0) ? 1u : 0u);
-                    tc_commit_warp(vfree(slot));
-                    tc_commit_warp(pvdone(x));
-                    if (!wait(pvdone(x), it & 1)) {
-                        go = false;
-                        break;
-                    }
-                    ++it;
+                    for (int kk = 0; kk < kMtStep / 16; ++kk)   // 16 keys: 8 columns of P, 2048 bytes of value rows
+                        tc_mma_f16_tmem_a_warp(tm_o, tm_s + half * kMtStep + kk * 8, tc_desc_advance(v0, kk * 2048),
+                                               idesc_pv, (i > 0 || kk > 0) ? 1u : 0u);
+                    if (half == 1) tc_commit_warp(vfree(slot));
+                    tc_commit_warp(pvdone(x, half));
+                    // the scores two steps on go over these weights, once the product has read them
+                    if (i + 2 < 2u * n) go = wait(pvdone(x, half), par) && scores(kt, i + 2);
                 }
+                kt += n;
             }
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         // ------------------------------------------------------------ softmax of query tile x
         const int x = warp >> 2, row = tid & 127;
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const uint32_t ts = tm_s[x] + lane_off, to = tm_o[x] + lane_off;
+        const uint32_t ts = tmem + 128 * x + lane_off, to = tmem + 256 + 128 * x + lane_off;
         const float ref = 0.5f * mp.cap_out;
         uint32_t it = 0, kt = 0;   // this query tile's steps, key tiles so far
         int piece = 0;             // segments so far
@@ -488,14 +556,20 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
             const bool real = row < ppt * g && c < p.n_pos;
             const size_t orow = static_cast<size_t>(c) * p.H_Q + s.head * g + row % g;
             if (!mine) continue;   // the same for the whole CTA
-            // ---- queries into shared memory (zero where there is none)
-#pragma unroll 4
-            for (int i = tid & 127; i < 128 * (D / 8); i += 128) {
-                const int r = i / (D / 8), ch = i % (D / 8), cp = c0 + r / g;
-                uint4 q = make_uint4(0u, 0u, 0u, 0u);
-                if (r < ppt * g && cp < p.n_pos)
-                    q = __ldg(reinterpret_cast<const uint4 *>(p.q + (static_cast<size_t>(cp) * p.H_Q + s.head * g + r % g) * D) + ch);
-                sts128(sbase + C::Q + x * C::TILE + (ch >> 3) * C::BAND + sw128(r, ch & 7), q);
+            // ---- queries into shared memory (zero where there is none), every load in flight at once
+            {
+                constexpr int N = D / 8;   // 16-byte chunks of a row, and chunks per thread
+                uint4 q[N];
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const int r = (row + 128 * i) / N, ch = row % N, cp = c0 + r / g;
+                    q[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (r < ppt * g && cp < p.n_pos)
+                        q[i] = __ldg(reinterpret_cast<const uint4 *>(p.q + (static_cast<size_t>(cp) * p.H_Q + s.head * g + r % g) * D) + ch);
+                }
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    sts128(sbase + C::Q + x * C::TILE + ((row % N) >> 3) * C::BAND + sw128((row + 128 * i) / N, row & 7), q[i]);
             }
             fence_proxy_async_smem();
             tc_fence_before();   // this thread's reads of the last segment's outputs
@@ -513,22 +587,31 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
             const bool any_real = __any_sync(kFull, real);
             float m = FIXED ? ref : -INFINITY, l = 0.f;
             bool go = true;
-            for (int k = s.k0; k < s.k1; ++k, ++it) {
-                if (!wait(sfull(x), it & 1)) {
+            // scores in registers are raw, or already modified and in log2 units (bias, or a cap with a maximum)
+            const bool ready = mp.capped || mp.alibi;
+            const float mul = ready ? 1.f : p.scale_log2;
+            for (int i = 0; i < 2 * (s.k1 - s.k0); ++i, ++it) {
+                const int half = it & 1;
+                if (!wait(sfull(x, half), (it >> 1) & 1)) {
                     go = false;
                     break;
                 }
                 tc_fence_after();
                 if (!any_real) {   // rows past the chunk: their weights stay in their own lanes and are never read
-                    mbar_arrive(pfull(x));
+                    mbar_arrive(pfull(x, half));
                     continue;
                 }
-                const int first = k * kMtBlocks;
-                const bool one_run = first + kMtBlocks <= v.br.n && (first + kMtBlocks <= v.br.n0 || first >= v.br.n0);
+                const uint32_t tsb = ts + half * kMtStep;
+                uint32_t r0[32], r1[32];
+                tmem_ld32(tsb, r0);
+                tmem_ld32(tsb + 32, r1);
+                const int first = s.k0 * kMtBlocks + i * kMtStepBlocks;   // the step's first virtual block
+                const bool one_run = first + kMtStepBlocks <= v.br.n && (first + kMtStepBlocks <= v.br.n0 || first >= v.br.n0);
                 const int t0 = v.br.at(first) * kBS;
-                const uint32_t loaded = mask_sh[(kt0 + (k - s.k0)) & 3];
-                const bool full = one_run && loaded == (1u << kMtBlocks) - 1u && ((t0 >= flo && t0 + kMtKeys <= fhi) || (t0 >= fd && t0 + kMtKeys <= fe));
-                // bit i of a 16-key block's mask: this row reads the block's key i
+                const uint32_t loaded = mask_sh[(kt0 + (i >> 1)) & 3] >> (half * kMtStepBlocks) & ((1u << kMtStepBlocks) - 1u);
+                const bool full = one_run && loaded == (1u << kMtStepBlocks) - 1u &&
+                                  ((t0 >= flo && t0 + kMtStep <= fhi) || (t0 >= fd && t0 + kMtStep <= fe));
+                // bit j of a 16-key block's mask: this row reads the block's key j
                 auto block_mask = [&](int b) -> uint32_t {
                     const int vb = first + b;
                     if (vb >= v.br.n || !(loaded >> b & 1u)) return 0u;
@@ -538,132 +621,127 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
                     };
                     return (below(r.hi) & ~below(r.lo)) | (below(r.e) & ~below(r.d));
                 };
+                uint32_t seen0 = 0xFFFFFFFFu, seen1 = 0xFFFFFFFFu;
+                if (!full) {
+                    seen0 = block_mask(0) | (block_mask(1) << 16);
+                    seen1 = block_mask(2) | (block_mask(3) << 16);
+                }
+                tmem_ld_wait(r0);
+                tmem_ld_wait(r1);
+                uint32_t pk[32];
+                f32x2 ls[4] = {f32x2_of(0.f, 0.f), f32x2_of(0.f, 0.f), f32x2_of(0.f, 0.f), f32x2_of(0.f, 0.f)};
                 if constexpr (FIXED) {
-                    float ls[4] = {0.f, 0.f, 0.f, 0.f};
-                    uint32_t buf[2][32];
-                    tmem_ld32(ts, buf[0]);
+                    if (!full) {   // a hidden key's score may be anything, and would reach its group's reciprocal
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        tmem_ld_wait(buf[q & 1]);
-                        if (q < 3) tmem_ld32(ts + 32 * (q + 1), buf[(q + 1) & 1]);
-                        uint32_t (&sv)[32] = buf[q & 1];
-                        const uint32_t seen = full ? 0xFFFFFFFFu : (block_mask(2 * q) | (block_mask(2 * q + 1) << 16));
-                        uint32_t pk[16];
-#pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
-                            float w[2];
-#pragma unroll
-                            for (int u = 0; u < 2; ++u) {
-                                float rc;
-                                asm("rcp.approx.ftz.f32 %0, %1;"
-                                    : "=f"(rc)
-                                    : "f"(1.f + fast_exp2(__uint_as_float(sv[i + u]) * mp.cap_in)));
-                                w[u] = fast_exp2(fmaf(-2.f * mp.cap_out, rc, ref));   // 2^(x - cap / 2)
-                            }
-                            if (!full) {
-                                w[0] = (seen >> i) & 1u ? w[0] : 0.f;
-                                w[1] = (seen >> (i + 1)) & 1u ? w[1] : 0.f;
-                            }
-                            ls[(i / 2) & 3] += w[0] + w[1];
-                            pk[i / 2] = pack_bf16(w[0], w[1]);
+                        for (int c = 0; c < 32; ++c) {
+                            r0[c] = seen0 >> c & 1u ? r0[c] : 0u;
+                            r1[c] = seen1 >> c & 1u ? r1[c] : 0u;
                         }
-                        tmem_st16(ts + 16 * q, pk);   // over scores already read
                     }
-                    l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+                    const f32x2 in = f32x2_of(mp.cap_in, mp.cap_in), one = f32x2_of(1.f, 1.f);
+                    const f32x2 out2 = f32x2_of(-2.f * mp.cap_out, -2.f * mp.cap_out), ref2 = f32x2_of(ref, ref);
+#pragma unroll
+                    for (int c = 0; c < 64; c += 4) {
+                        const uint32_t *sr = c < 32 ? r0 + c : r1 + (c - 32);
+                        // w = 2^(x - cap / 2), x = cap - 2 cap / (1 + 2^u): four scores share one reciprocal,
+                        // 1 / a_i = (product of the others) / (product of all).  u is held under 30, where
+                        // x already equals cap in fp32, so that the product stays finite.
+                        const f32x2 u01 = mul2(f32x2_of(__uint_as_float(sr[0]), __uint_as_float(sr[1])), in);
+                        const f32x2 u23 = mul2(f32x2_of(__uint_as_float(sr[2]), __uint_as_float(sr[3])), in);
+                        const f32x2 a = add2(f32x2_of(fast_exp2(min_nan(lo2(u01), 30.f)), fast_exp2(min_nan(hi2(u01), 30.f))), one);
+                        const f32x2 b = add2(f32x2_of(fast_exp2(min_nan(lo2(u23), 30.f)), fast_exp2(min_nan(hi2(u23), 30.f))), one);
+                        const f32x2 ab = mul2(a, b);   // (a0 a2, a1 a3)
+                        const float rc = fast_rcp(lo2(ab) * hi2(ab));
+                        const f32x2 ri = mul2(f32x2_of(rc, rc), f32x2_of(hi2(ab), lo2(ab)));   // (1 / a0 a2, 1 / a1 a3)
+                        const f32x2 x01 = fma2(mul2(ri, b), out2, ref2), x23 = fma2(mul2(ri, a), out2, ref2);
+                        float w0 = fast_exp2(lo2(x01)), w1 = fast_exp2(hi2(x01));
+                        float w2 = fast_exp2(lo2(x23)), w3 = fast_exp2(hi2(x23));
+                        if (!full) {
+                            const uint32_t seen = (c < 32 ? seen0 : seen1) >> (c & 31);
+                            w0 = seen & 1u ? w0 : 0.f;
+                            w1 = seen & 2u ? w1 : 0.f;
+                            w2 = seen & 4u ? w2 : 0.f;
+                            w3 = seen & 8u ? w3 : 0.f;
+                        }
+                        ls[(c >> 2) & 1] = add2(ls[(c >> 2) & 1], f32x2_of(w0, w1));
+                        ls[2 + ((c >> 2) & 1)] = add2(ls[2 + ((c >> 2) & 1)], f32x2_of(w2, w3));
+                        pk[c / 2] = pack_bf16(w0, w1);
+                        pk[c / 2 + 1] = pack_bf16(w2, w3);
+                    }
                 } else {
-                    float sv[128];
-                    {
-                        uint32_t raw[4][32];
+                    float sv[64];
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) tmem_ld32(ts + 32 * q, raw[q]);
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            tmem_ld_wait(raw[q]);
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) sv[32 * q + i] = __uint_as_float(raw[q][i]);
-                        }
+                    for (int c = 0; c < 32; ++c) {
+                        sv[c] = __uint_as_float(r0[c]);
+                        sv[32 + c] = __uint_as_float(r1[c]);
                     }
-                    if (mp.capped) {
+                    if (ready) {
 #pragma unroll
-                        for (int i = 0; i < 128; ++i) sv[i] = modified(mp, sv[i]);
-                    } else {
+                        for (int c = 0; c < 64; ++c) sv[c] = modified(mp, sv[c]);
+                        if (mp.alibi) {
 #pragma unroll
-                        for (int i = 0; i < 128; ++i) sv[i] *= p.scale_log2;
-                    }
-                    if (mp.alibi) {
+                            for (int b = 0; b < kMtStepBlocks; ++b) {
+                                const int vb = min(first + b, max(v.br.n - 1, 0));
+                                const float away = static_cast<float>(pos - v.br.at(vb) * kBS);
 #pragma unroll
-                        for (int b = 0; b < kMtBlocks; ++b) {
-                            const int vb = min(first + b, max(v.br.n - 1, 0));
-                            const float away = static_cast<float>(pos - v.br.at(vb) * kBS);
-#pragma unroll
-                            for (int i = 0; i < kBS; ++i)
-                                sv[kBS * b + i] = fmaf(-slope, fabsf(away - static_cast<float>(i)), sv[kBS * b + i]);
+                                for (int c = 0; c < kBS; ++c)
+                                    sv[kBS * b + c] = fmaf(-slope, fabsf(away - static_cast<float>(c)), sv[kBS * b + c]);
+                            }
                         }
                     }
                     if (!full) {
 #pragma unroll
-                        for (int b = 0; b < kMtBlocks; ++b) {
-                            const uint32_t seen = block_mask(b);
-#pragma unroll
-                            for (int i = 0; i < kBS; ++i) sv[kBS * b + i] = (seen >> i) & 1u ? sv[kBS * b + i] : -INFINITY;
+                        for (int c = 0; c < 32; ++c) {
+                            sv[c] = seen0 >> c & 1u ? sv[c] : -INFINITY;
+                            sv[32 + c] = seen1 >> c & 1u ? sv[32 + c] : -INFINITY;
                         }
                     }
-                    float b0 = sv[0], b1 = sv[1], b2 = sv[2], b3 = sv[3];
+                    float b0 = sv[0], b1 = sv[1], b2 = sv[2], b3 = sv[3];   // four chains of 3-input maxima
 #pragma unroll
-                    for (int i = 4; i < 124; i += 8) {
-                        b0 = max3f(b0, sv[i], sv[i + 1]);
-                        b1 = max3f(b1, sv[i + 2], sv[i + 3]);
-                        b2 = max3f(b2, sv[i + 4], sv[i + 5]);
-                        b3 = max3f(b3, sv[i + 6], sv[i + 7]);
+                    for (int c = 4; c < 60; c += 8) {
+                        b0 = max3f(b0, sv[c], sv[c + 1]);
+                        b1 = max3f(b1, sv[c + 2], sv[c + 3]);
+                        b2 = max3f(b2, sv[c + 4], sv[c + 5]);
+                        b3 = max3f(b3, sv[c + 6], sv[c + 7]);
                     }
-                    b0 = max3f(b0, sv[124], sv[125]);
-                    b1 = max3f(b1, sv[126], sv[127]);
-                    const float bm = max3f(b0, b1, fmaxf(b2, b3));
-                    const bool move = bm > m + kRescaleSlack;   // false while nothing has been read
+                    b0 = max3f(b0, sv[60], sv[61]);
+                    b1 = max3f(b1, sv[62], sv[63]);
+                    const float bm = max3f(b0, b1, fmaxf(b2, b3)) * mul;   // mul > 0
+                    const bool move = bm > m + kRescaleSlack;              // false while nothing has been read
                     float alpha = 1.f;
                     if (move) {
                         alpha = fast_exp2(m - bm);
                         m = bm;
                         l *= alpha;
                     }
-                    // the products before this tile's scores are complete (the issuer waited): O may be rescaled
-                    if (k > s.k0 && __any_sync(kFull, move && alpha != 1.f)) {
-#pragma unroll
-                        for (int part = 0; part < D / 16; ++part) {
-                            uint32_t o[16];
-                            asm volatile(
-                                "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-                                "%12, %13, %14, %15}, [%16];\n\ttcgen05.wait::ld.sync.aligned;"
-                                : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]),
-                                  "=r"(o[7]), "=r"(o[8]), "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]),
-                                  "=r"(o[14]), "=r"(o[15])
-                                : "r"(to + part * 16)
-                                : "memory");
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                            tmem_st16(to + part * 16, o);
+                    // the warp rescales its rows of O together, once the previous product is in them
+                    if (i > 0 && __any_sync(kFull, move && alpha != 1.f)) {
+                        if (!wait(pvdone(x, half ^ 1), ((it - 1) >> 1) & 1)) {
+                            go = false;
+                            break;
                         }
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int part = 0; part < D / 16; ++part) tmem_scale16(to + part * 16, alpha);
                     }
-                    const float neg_m = m == -INFINITY ? 0.f : -m;
-                    float ls[4] = {0.f, 0.f, 0.f, 0.f};
+                    const float neg = m == -INFINITY ? 0.f : -m;
+                    const f32x2 mul_2 = f32x2_of(mul, mul), neg2 = f32x2_of(neg, neg);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t pk[16];
-#pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
-                            const float w0 = fast_exp2(sv[32 * q + i] + neg_m), w1 = fast_exp2(sv[32 * q + i + 1] + neg_m);
-                            ls[(i / 2) & 3] += w0 + w1;
-                            pk[i / 2] = pack_bf16(w0, w1);
-                        }
-                        tmem_st16(ts + 16 * q, pk);
+                    for (int c = 0; c < 64; c += 2) {
+                        const f32x2 e = fma2(f32x2_of(sv[c], sv[c + 1]), mul_2, neg2);
+                        const float w0 = fast_exp2(lo2(e)), w1 = fast_exp2(hi2(e));
+                        ls[(c / 2) & 3] = add2(ls[(c / 2) & 3], f32x2_of(w0, w1));
+                        pk[c / 2] = pack_bf16(w0, w1);
                     }
-                    l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
                 }
+                const f32x2 lt = add2(add2(ls[0], ls[1]), add2(ls[2], ls[3]));
+                l += lo2(lt) + hi2(lt);
+                tmem_st32(tsb, pk);   // over the first half of the step's scores
                 tmem_st_wait();
                 tc_fence_before();
-                mbar_arrive(pfull(x));
+                mbar_arrive(pfull(x, half));
             }
-            if (go) go = wait(pvdone(x), (it - 1) & 1);
+            if (go) go = wait(pvdone(x, 1), ((it - 1) >> 1) & 1);   // a segment has an even number of steps
             // every thread of the query tile takes this vote once per segment, so the barriers below meet
             if (!tile_all(go, 4 + x)) {
                 timed_out = true;
@@ -671,97 +749,180 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
             }
             tc_fence_after();
 
-            // ---- epilogue: the unit's rows, or a piece of them
+            // ---- epilogue: the unit's rows, or a piece of them that the unit's last CTA merges (each query
+            // tile on its own)
             const bool done = s.k0 == 0 && s.k1 == s.tiles;
-            const int64_t mypart = 2 * static_cast<int64_t>(blockIdx.x) + (piece > 0 ? 1 : 0);
+            const int64_t a = s.start, b = s.start + s.tiles;
+            const int64_t cf = ((a + 1) * G - 1) / W, cl = (b * G - 1) / W;   // CTAs holding its first and last tile
+            const int n = done ? 1 : static_cast<int>(cl - cf) + 1;
+            const int nrows = min(ppt, p.n_pos - c0) * g;
+            const bool first_second = !done && cf * W / G < a;   // the first CTA's piece is its second one
+            auto part_of = [&](int i) { return 2 * (cf + i) + (i == 0 && first_second ? 1 : 0); };
             const int prow = x * 128 + row;
-            const float inv = l == 0.f ? 0.f : 1.f / l;
+            uint32_t *ctr = done ? nullptr : tp.counters + 2 * (static_cast<size_t>(s.head) * tp.units + s.unit) + x;
+            const int own = static_cast<int>(blockIdx.x - cf);
+            bool last = false, keep = false;   // keep: this piece is merged from TMEM and never written
+            if (!done) {
+                if (nrows > 32) {   // the other pieces may all be there already
+                    if (row == 0) last_sh[x] = ld_acquire(ctr) == static_cast<uint32_t>(n - 1);
+                    asm volatile("bar.sync %0, 128;" ::"r"(4 + x) : "memory");
+                    keep = last_sh[x] != 0;
+                }
+                if (!keep) {
+                    const int64_t mine_part = part_of(own);
+                    if (any_real) {
+#pragma unroll
+                        for (int part = 0; part < D / 32; ++part) {
+                            uint32_t o[32];
+                            tmem_ld32(to + part * 32, o);
+                            tmem_ld_wait(o);
+                            if (real) {
+                                // [channel / 4][row]: a warp's rows are contiguous
+                                float4 *dst = reinterpret_cast<float4 *>(tp.part_o) + (mine_part * (D / 4) + part * 8) * 256 + prow;
+#pragma unroll
+                                for (int c = 0; c < 8; ++c)
+                                    dst[c * 256] = make_float4(__uint_as_float(o[4 * c]), __uint_as_float(o[4 * c + 1]),
+                                                               __uint_as_float(o[4 * c + 2]), __uint_as_float(o[4 * c + 3]));
+                            }
+                        }
+                    }
+                    if (real) tp.part_ml[mine_part * 256 + prow] = make_float2(m, l);
+                    __threadfence();
+                    asm volatile("bar.sync %0, 128;" ::"r"(4 + x) : "memory");   // also: last_sh has been read
+                    if (row == 0) last_sh[x] = atomicAdd(ctr, 1u) == static_cast<uint32_t>(n - 1);
+                    asm volatile("bar.sync %0, 128;" ::"r"(4 + x) : "memory");
+                    last = last_sh[x] != 0;
+                }
+                asm volatile("bar.sync %0, 128;" ::"r"(4 + x) : "memory");   // last_sh may be written again
+                if (!keep && !last) continue;
+                __threadfence();
+                if (row == 0) *ctr = 0u;   // ready for the next launch
+            }
+            if (!done && !keep && nrows <= 32) {
+                // few rows, often many pieces: lane = row, the tile's warps share the channels
+                constexpr int CW = D / 4;   // channels per warp
+                if (lane < nrows) {
+                    const int pr = x * 128 + lane, w0 = (warp & 3) * CW;
+                    float M = -INFINITY;
+#pragma unroll 8
+                    for (int t = 0; t < n; ++t) {
+                        const float2 ml = __ldcg(tp.part_ml + part_of(t) * 256 + pr);
+                        M = fmaxf(M, ml.y != 0.f ? ml.x : -INFINITY);
+                    }
+                    float L = 0.f, acc[CW] = {};
+#pragma unroll 2
+                    for (int t = 0; t < n; ++t) {
+                        const int64_t pt = part_of(t);
+                        const float2 ml = __ldcg(tp.part_ml + pt * 256 + pr);
+                        const float4 *src = reinterpret_cast<const float4 *>(tp.part_o) + (pt * (D / 4) + w0 / 4) * 256 + pr;
+                        float4 u[CW / 4];
+#pragma unroll
+                        for (int c = 0; c < CW / 4; ++c) u[c] = __ldcg(src + c * 256);
+                        if (ml.y == 0.f) continue;   // the piece reads nothing for this row
+                        const float e = fast_exp2(ml.x - M);
+                        L = fmaf(e, ml.y, L);
+#pragma unroll
+                        for (int c = 0; c < CW / 4; ++c) {
+                            acc[4 * c] = fmaf(e, u[c].x, acc[4 * c]);
+                            acc[4 * c + 1] = fmaf(e, u[c].y, acc[4 * c + 1]);
+                            acc[4 * c + 2] = fmaf(e, u[c].z, acc[4 * c + 2]);
+                            acc[4 * c + 3] = fmaf(e, u[c].w, acc[4 * c + 3]);
+                        }
+                    }
+                    const size_t ob = static_cast<size_t>(c0 + lane / g) * p.H_Q + s.head * g + lane % g;
+                    const float li = L == 0.f ? 0.f : 1.f / L;
+                    uint4 *dst = reinterpret_cast<uint4 *>(mp.out + ob * D + w0);
+#pragma unroll
+                    for (int c = 0; c < CW / 8; ++c)
+                        dst[c] = make_uint4(pack_bf16(acc[8 * c] * li, acc[8 * c + 1] * li),
+                                            pack_bf16(acc[8 * c + 2] * li, acc[8 * c + 3] * li),
+                                            pack_bf16(acc[8 * c + 4] * li, acc[8 * c + 5] * li),
+                                            pack_bf16(acc[8 * c + 6] * li, acc[8 * c + 7] * li));
+                    if (w0 == 0 && p.lse) p.lse[ob] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+                }
+                continue;
+            }
+            // thread = row; the row's pieces in CTA order (this one from TMEM when kept), so that the sums do
+            // not depend on which CTA is last.  Weights in the tile's query memory (its products are done),
+            // every thread its own column.
             if (any_real) {
+                float M = m, L = l;
+                float *wsh = reinterpret_cast<float *>(smem + C::Q + x * C::TILE) + row;
+                if (!done) {
+                    M = -INFINITY;
+                    L = 0.f;
+                    if (real) {
+#pragma unroll 4
+                        for (int t = 0; t < n; ++t) {
+                            const float2 ml = keep && t == own ? make_float2(m, l) : __ldcg(tp.part_ml + part_of(t) * 256 + prow);
+                            M = fmaxf(M, ml.y != 0.f ? ml.x : -INFINITY);
+                        }
+#pragma unroll 4
+                        for (int t = 0; t < n; ++t) {
+                            const float2 ml = keep && t == own ? make_float2(m, l) : __ldcg(tp.part_ml + part_of(t) * 256 + prow);
+                            const float e = ml.y != 0.f ? fast_exp2(ml.x - M) : 0.f;   // 0: the piece reads nothing
+                            L = fmaf(e, ml.y, L);
+                            if (t < C::TILE / 512) wsh[t * 128] = e;
+                        }
+                    }
+                }
+                const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
                 for (int part = 0; part < D / 32; ++part) {
                     uint32_t o[32];
-                    tmem_ld32(to + part * 32, o);
-                    tmem_ld_wait(o);
+                    if (done || keep) {
+                        tmem_ld32(to + part * 32, o);
+                        tmem_ld_wait(o);
+                    }
                     if (!real) continue;
-                    if (done) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(mp.out + orow * D + part * 32);
+                    if (!done) {
+                        float acc[32] = {};
+                        for (int t = 0; t < n; ++t) {
+                            const bool here = keep && t == own;
+                            const int64_t pt = part_of(t);
+                            float e;
+                            if (t < C::TILE / 512) {
+                                e = wsh[t * 128];
+                            } else {
+                                const float2 ml = here ? make_float2(m, l) : __ldcg(tp.part_ml + pt * 256 + prow);
+                                e = ml.y != 0.f ? fast_exp2(ml.x - M) : 0.f;
+                            }
+                            if (here) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t w[4];
+                                for (int c = 0; c < 32; ++c) acc[c] = e == 0.f ? acc[c] : fmaf(e, __uint_as_float(o[c]), acc[c]);
+                            } else {
+                                const float4 *src = reinterpret_cast<const float4 *>(tp.part_o) + (pt * (D / 4) + part * 8) * 256 + prow;
+                                float4 u[8];
 #pragma unroll
-                            for (int u = 0; u < 4; ++u)
-                                w[u] = l == 0.f ? 0u : pack_bf16(__uint_as_float(o[8 * i + 2 * u]) * inv,
-                                                                 __uint_as_float(o[8 * i + 2 * u + 1]) * inv);
-                            dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                                for (int c = 0; c < 8; ++c) u[c] = __ldcg(src + c * 256);
+                                if (e != 0.f) {
+#pragma unroll
+                                    for (int c = 0; c < 8; ++c) {
+                                        acc[4 * c] = fmaf(e, u[c].x, acc[4 * c]);
+                                        acc[4 * c + 1] = fmaf(e, u[c].y, acc[4 * c + 1]);
+                                        acc[4 * c + 2] = fmaf(e, u[c].z, acc[4 * c + 2]);
+                                        acc[4 * c + 3] = fmaf(e, u[c].w, acc[4 * c + 3]);
+                                    }
+                                }
+                            }
                         }
-                    } else {
-                        float4 *dst = reinterpret_cast<float4 *>(tp.part_o) + (mypart * (D / 4) + part * 8) * 256 + prow;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)   // [channel / 4][row]: a warp's rows are contiguous
-                            dst[i * 256] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
-                                                       __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+                        for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(acc[c]);
+                    }
+                    uint4 *dst = reinterpret_cast<uint4 *>(mp.out + orow * D + part * 32);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            w[u] = L == 0.f ? 0u : pack_bf16(__uint_as_float(o[8 * c + 2 * u]) * inv,
+                                                             __uint_as_float(o[8 * c + 2 * u + 1]) * inv);
+                        dst[c] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
+                if (real && p.lse) p.lse[orow] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
             }
-            if (real && done && p.lse) p.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-            if (done) continue;
-            if (real) tp.part_ml[mypart * 256 + prow] = make_float2(m, l);
-            // ---- the unit's last CTA merges its pieces, tile by tile (each query tile counts on its own)
-            const int64_t a = s.start, b = s.start + s.tiles;
-            const int64_t cf = ((a + 1) * G - 1) / W, cl = (b * G - 1) / W;   // CTAs holding its first and last tile
-            const int n = static_cast<int>(cl - cf) + 1;
-            __threadfence();
-            asm volatile("bar.sync %0, 128;" ::"r"(4 + x) : "memory");
-            if (row == 0) {
-                uint32_t *ctr = tp.counters + 2 * (static_cast<size_t>(s.head) * tp.units + s.unit) + x;
-                const uint32_t before = atomicAdd(ctr, 1u);
-                last_sh[x] = before == static_cast<uint32_t>(n - 1);
-                if (before == static_cast<uint32_t>(n - 1)) *ctr = 0u;   // ready for the next launch
-            }
-            asm volatile("bar.sync %0, 128;" ::"r"(4 + x) : "memory");
-            const bool last = last_sh[x] != 0;
-            asm volatile("bar.sync %0, 128;" ::"r"(4 + x) : "memory");   // last_sh may be written again
-            if (!last) continue;
-            __threadfence();
-            const bool first_second = cf * W / G < a;   // the first CTA's piece is its second one
-            auto part_of = [&](int i) { return 2 * (cf + i) + (i == 0 && first_second ? 1 : 0); };
-            const int nrows = min(ppt, p.n_pos - c0) * g;
-            // items (row, 8 channels): lanes on consecutive rows
-            for (int i = row; i < ((nrows + 31) & ~31) * (D / 8); i += 128) {
-                const int rr = i % ((nrows + 31) & ~31), d8 = i / ((nrows + 31) & ~31);
-                if (rr >= nrows) continue;
-                const int pr = x * 128 + rr;
-                float M = -INFINITY;
-                for (int t = 0; t < n; ++t) {
-                    const float2 ml = __ldcg(tp.part_ml + part_of(t) * 256 + pr);
-                    if (ml.y != 0.f) M = fmaxf(M, ml.x);
-                }
-                float L = 0.f, acc[8] = {};
-#pragma unroll 4
-                for (int t = 0; t < n; ++t) {
-                    const int64_t pt = part_of(t);
-                    const float2 ml = __ldcg(tp.part_ml + pt * 256 + pr);
-                    const float4 *src = reinterpret_cast<const float4 *>(tp.part_o) + (pt * (D / 4) + 2 * d8) * 256 + pr;
-                    const float4 u0 = __ldcg(src), u1 = __ldcg(src + 256);
-                    if (ml.y == 0.f) continue;   // the piece reads nothing for this row
-                    const float e = fast_exp2(ml.x - M);
-                    L = fmaf(e, ml.y, L);
-                    acc[0] = fmaf(e, u0.x, acc[0]);
-                    acc[1] = fmaf(e, u0.y, acc[1]);
-                    acc[2] = fmaf(e, u0.z, acc[2]);
-                    acc[3] = fmaf(e, u0.w, acc[3]);
-                    acc[4] = fmaf(e, u1.x, acc[4]);
-                    acc[5] = fmaf(e, u1.y, acc[5]);
-                    acc[6] = fmaf(e, u1.z, acc[6]);
-                    acc[7] = fmaf(e, u1.w, acc[7]);
-                }
-                const size_t ob = static_cast<size_t>(c0 + rr / g) * p.H_Q + s.head * g + rr % g;
-                const float li = L == 0.f ? 0.f : 1.f / L;
-                *reinterpret_cast<uint4 *>(mp.out + ob * D + 8 * d8) =
-                    make_uint4(pack_bf16(acc[0] * li, acc[1] * li), pack_bf16(acc[2] * li, acc[3] * li),
-                               pack_bf16(acc[4] * li, acc[5] * li), pack_bf16(acc[6] * li, acc[7] * li));
-                if (d8 == 0 && p.lse) p.lse[ob] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
-            }
+            if (!done) asm volatile("bar.sync %0, 128;" ::"r"(4 + x) : "memory");   // the weights' memory takes queries next
         }
     }
     if (timed_out && lane == 0) atomicOr(p.err, KVC_EBIT_TIMEOUT);
