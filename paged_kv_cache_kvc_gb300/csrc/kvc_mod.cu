@@ -152,8 +152,13 @@ static kvc_status run_split(kvc_pool *pool, ModParams &mp, const DecodeKernel &k
     return KVC_OK;
 }
 
-// The tensor-memory kernel's partials: two pieces of a unit's 256 rows per CTA.
-static size_t tc_partial_bytes(int64_t ctas, int D) { return static_cast<size_t>(ctas) * 2 * 256 * (D * sizeof(float) + sizeof(float2)); }
+// The tensor-memory kernel's part of the workspace behind the counters: the units' running tile counts,
+// then two pieces of a unit's 256 rows per CTA.
+constexpr size_t kPrefixBytes = ((kMtUnits + 1) * sizeof(int32_t) + 255) & ~size_t(255);
+static size_t tc_bytes(int64_t ctas, int D)
+{
+    return kPrefixBytes + static_cast<size_t>(ctas) * 2 * 256 * (D * sizeof(float) + sizeof(float2));
+}
 
 // KVC_TC=0 selects the split kernel (as for the plain calls).
 static bool use_tc(const kvc_pool *pool)
@@ -162,19 +167,30 @@ static bool use_tc(const kvc_pool *pool)
     return !(e && e[0] == '0') && pool->dtype == KVC_BF16 && pool->tmap16_ok;
 }
 
-// A chunk on the tensor-memory kernel, as many units at a time as one launch takes.
+static int tc_min_group()
+{
+    const char *e = std::getenv("KVC_TC_GROUP");
+    return e ? std::atoi(e) : 17;
+}
+
+// A chunk (or a decode batch of large head groups) on the tensor-memory kernel, as many units at a time as one
+// launch takes.
 static kvc_status run_tc(kvc_pool *pool, const ModParams &mp0, void *ws, size_t ws_bytes, cudaStream_t stream)
 {
     ModTcParams tp{};
     tp.m = mp0;
     DecodeParams &p = tp.m.d;
-    p.ppu = 128 / p.g;
+    const bool decode = p.lens != nullptr;
+    p.ppu = decode ? 1 : 128 / p.g;
     tp.total = p.len_base + p.n_pos;
+    tp.whole = !ws;
+    tp.split = !tp.whole && (decode || p.n_pos <= p.ppu);
     const bool fixed = tp.m.capped && !tp.m.alibi && tp.m.cap_out <= kMtCapLimit;
     const DecodeKernel k = select_mod_tc(pool->D, fixed);
     if (!k.fn) return KVC_ERR_UNSUPPORTED;
     if (k.ctas_per_sm <= 0) return KVC_ERR_CUDA;
-    const int per_launch = kMtUnits * 2 * p.ppu, n_q = p.n_pos, start = p.len_base;
+    const int unit = tp.split ? p.ppu : 2 * p.ppu;   // positions per unit
+    const int per_launch = kMtUnits * unit, n_q = p.n_pos, start = p.len_base;
     for (int at = 0; at < n_q; at += per_launch) {
         p.n_pos = std::min(per_launch, n_q - at);
         p.len_base = start + at;
@@ -182,21 +198,33 @@ static kvc_status run_tc(kvc_pool *pool, const ModParams &mp0, void *ws, size_t 
         tp.m.out = mp0.out + static_cast<size_t>(at) * p.H_Q * pool->D;
         p.lse = mp0.d.lse ? mp0.d.lse + static_cast<size_t>(at) * p.H_Q : nullptr;
         tp.m.doc_start = mp0.doc_start ? mp0.doc_start + at : nullptr;
-        tp.units = (p.n_pos + 2 * p.ppu - 1) / (2 * p.ppu);
-        // no CTA without a tile: a line of tiles at least as long as what the units' ends need
+        if (decode) {
+            p.lens = mp0.d.lens + at;
+            p.bt = mp0.d.bt + static_cast<size_t>(at) * p.bt_stride;
+        }
+        tp.units = (p.n_pos + unit - 1) / unit;
+        // no more CTAs than the line of tiles can have tiles
         const int64_t most = static_cast<int64_t>(p.H_KV) * tp.units * ((p.max_blocks + kMtBlocks - 1) / kMtBlocks);
-        const int64_t ctas = std::min<int64_t>(pool->num_sms, most);
-        tp.whole = !ws || 2ll * p.H_KV * tp.units > kCounters;
+        const int ctas = static_cast<int>(std::min<int64_t>(pool->num_sms, most));
         if (!tp.whole) {
-            if (ws_bytes < kCounterBytes + tc_partial_bytes(ctas, pool->D)) return KVC_ERR_ARG;
-            tp.counters = static_cast<uint32_t *>(ws);
-            tp.part_o = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + kCounterBytes);
+            if (ws_bytes < kCounterBytes + tc_bytes(ctas, pool->D)) return KVC_ERR_ARG;
+            uint8_t *base = static_cast<uint8_t *>(ws) + kCounterBytes;
+            tp.prefix = reinterpret_cast<int32_t *>(base);
+            tp.part_o = reinterpret_cast<float *>(base + kPrefixBytes);
             tp.part_ml = reinterpret_cast<float2 *>(tp.part_o + static_cast<size_t>(ctas) * 2 * 256 * pool->D);
         }
         void *args[] = {&pool->tmap16, &tp};
-        const cudaError_t e = launch_dependent(k.fn, dim3(static_cast<unsigned>(ctas)), dim3(kMtThreads), k.smem, stream, args);
+        cudaError_t e = launch_dependent(k.fn, dim3(static_cast<unsigned>(ctas)), dim3(kMtThreads), k.smem, stream, args);
         if (e != cudaSuccess) return cuda_status(e);
         g_launches.fetch_add(1, std::memory_order_relaxed);
+        if (!tp.whole && (tp.split || most > 1)) {
+            const int rows = tp.split ? p.ppu * p.g : 256, per = 1024 / pool->D;
+            void *margs[] = {&tp, const_cast<int *>(&ctas)};
+            e = launch_dependent(select_mod_tc_merge(pool->D), dim3((rows + per - 1) / per, tp.units, p.H_KV), dim3(256), 0,
+                                 stream, margs);
+            if (e != cudaSuccess) return cuda_status(e);
+            g_launches.fetch_add(1, std::memory_order_relaxed);
+        }
     }
     return KVC_OK;
 }
@@ -285,7 +313,7 @@ extern "C" kvc_status kvc_mod_workspace_bytes(const kvc_pool *pool, int32_t rows
     const int64_t by_cap = rows * ((max_blocks + 283ll) / 284 + 1);
     const int64_t n = std::min(rows * by_len, std::max(by_slots, by_cap));
     *bytes = kCounterBytes + std::max(partial_bytes(n, num_q_heads, pool->D),
-                                      pool->dtype == KVC_BF16 ? tc_partial_bytes(pool->num_sms, pool->D) : 0);
+                                      pool->dtype == KVC_BF16 ? tc_bytes(pool->num_sms, pool->D) : 0);
     return KVC_OK;
 }
 
@@ -307,6 +335,9 @@ extern "C" kvc_status kvc_decode_attn_mod(kvc_pool *pool, int32_t layer, const v
     mp.d.B = B;
     mp.d.ppu = 1;
     mp.d.n_pos = B;
+    // Large head groups: one tensor-memory step serves the whole group
+    if (workspace && use_tc(pool) && mp.d.g >= tc_min_group())
+        return run_tc(pool, mp, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
     return run_split(pool, mp, select(pool, mp.d.g, false), most_blocks(mod, 1, max_blocks), workspace, workspace_bytes,
                      static_cast<cudaStream_t>(stream));
 }

@@ -27,4 +27,10 @@ DecodeKernel select_mod_tc(int D, bool fixed)
     return fixed ? instance<128, true>() : instance<128, false>();
 }
 
+const void *select_mod_tc_merge(int D)
+{
+    return D == 64 ? reinterpret_cast<const void *>(&mod_tc_merge_kernel<64>)
+                   : reinterpret_cast<const void *>(&mod_tc_merge_kernel<128>);
+}
+
 }  // namespace kvc

@@ -16,10 +16,14 @@
 //
 // Work split.  The unit's key tiles (only those that some row reads, kvc_mod.cuh) of every head and
 // unit form one line of W tiles; CTA c of G takes tiles [c W / G, (c + 1) W / G), whatever units they
-// belong to, so every SM gets the same work to within a tile: a late chunk of few long rows and a
-// long triangular one alike.  A unit that lies in one CTA is written at once; a unit cut by CTA
-// borders leaves fp32 partials (at most two per CTA), and the last of its CTAs to finish merges them
-// in CTA order (the result does not depend on who is last).
+// belong to, so every SM gets the same work to within a tile: a late chunk of few long rows, a long
+// triangular one and a ragged decode batch alike.  A unit that lies in one CTA is written at once; a
+// unit cut by CTA borders leaves fp32 partials (at most two per CTA) for mod_tc_merge_kernel, which
+// adds them in CTA order.  (Merged by the unit's last CTA instead, 600 queries of 1800 positions took
+// 43 us, 20 pieces of a 5-query chunk 9 us of its 36: one SM's loads against all SMs'.)
+//
+// Few rows (a chunk of at most 128 / g positions, a decode sequence): both chains take the same rows,
+// chain 0 the first 64 keys of every tile and chain 1 the rest, and the merge joins them too.
 //
 // Weights.  With capped scores (and no bias) x lies in [-cap, cap], so the softmax needs no maximum:
 // 2^(x - cap / 2) fits fp32 and bf16 for caps up to 55 (80 in log2 units), and a score needs no
@@ -42,12 +46,13 @@ constexpr int kMtUnits = 2048;                     // most units (per head) of o
 constexpr float kMtCapLimit = 80.f;                // cap in log2 units up to which no maximum is needed
 
 struct ModTcParams {
-    ModParams m;
+    ModParams m;          // m.d.ppu: positions per query tile (a decode sequence's one)
     int32_t units;        // units per head
     int32_t whole;        // 1: no partials, units are dealt whole
+    int32_t split;        // 1: a unit is one query tile's positions, and both chains take its rows (below)
     int32_t total;        // positions the row holds (prefill)
-    uint32_t *counters;   // [H_KV][units], zero between launches
-    float *part_o;        // [2 G][256][D]
+    int32_t *prefix;      // [units + 1] key tiles before each unit, for the merge
+    float *part_o;        // [2 G][D / 4][256] float4
     float2 *part_ml;      // [2 G][256]
 };
 
@@ -60,10 +65,9 @@ struct ModTcCfg {
     static constexpr int K = 2 * TILE;                 // [2] key tiles
     static constexpr int V = 4 * TILE;                 // [2] value tiles
     static constexpr int PREFIX = 6 * TILE;            // int32 [kMtUnits + 1]
-    static constexpr int RANGE = PREFIX + ((kMtUnits + 1) * 4 + 15) / 16 * 16;   // Range [256]
-    static constexpr int BARS = RANGE + 256 * 16;
+    static constexpr int BARS = PREFIX + ((kMtUnits + 1) * 4 + 15) / 16 * 16;
     static constexpr int NBARS = 24;
-    static constexpr int MISC = BARS + NBARS * 8;      // scan sums [12], abort, TMEM base, merge flags [2], block masks [4]
+    static constexpr int MISC = BARS + NBARS * 8;      // scan sums [12], abort, TMEM base, block masks [4]
     static constexpr int SMEM = 1024 + MISC + 128;
 };
 
@@ -139,14 +143,30 @@ __device__ __forceinline__ float fast_rcp(float x)
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-__device__ __forceinline__ uint32_t ld_acquire(const uint32_t *a)
+// Chunk position c (decode: sequence c): its position, the positions its row holds, what it reads.
+struct RowView {
+    int pos, total;
+    Range r;
+};
+
+__device__ __forceinline__ RowView row_view(const ModTcParams &p, int c)
 {
-    uint32_t r;
-    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(r) : "l"(a) : "memory");
-    return r;
+    const DecodeParams &d = p.m.d;
+    RowView v;
+    if (d.lens) {
+        v.total = __ldg(d.lens + c);
+        if (v.total < 0 || static_cast<int64_t>(v.total) > static_cast<int64_t>(d.max_blocks) * kBS) v.total = 0;
+        v.pos = v.total - 1;
+    } else {
+        v.total = p.total;
+        v.pos = d.len_base + c;
+    }
+    v.r = query_range(p.m, v.pos, v.total, p.m.doc_start ? __ldg(p.m.doc_start + c) : 0);
+    if (v.total == 0) v.r = Range{0, 0, 0, 0};
+    return v;
 }
 
-// What a unit reads and where its pieces are; the same in every thread of a warp.
+// What a unit reads; the same in every thread of a warp.
 struct UnitView {
     int pos0, n_pos;       // chunk positions [pos0, pos0 + n_pos)
     int a0, a1, e0, e1;    // the union of its rows' runs: [a0, a1) and [e0, e1)
@@ -158,7 +178,7 @@ struct UnitView {
 __device__ __forceinline__ UnitView unit_view(const ModTcParams &p, int u, int lane)
 {
     const DecodeParams &d = p.m.d;
-    const int ppu = 2 * d.ppu;
+    const int ppu = p.split ? d.ppu : 2 * d.ppu;
     UnitView v;
     v.pos0 = u * ppu;
     v.n_pos = min(ppu, d.n_pos - v.pos0);
@@ -166,8 +186,7 @@ __device__ __forceinline__ UnitView unit_view(const ModTcParams &p, int u, int l
     // without documents lo, hi and e grow with the position: the first and the last row bound the runs
     const int step = p.m.doc_start ? 1 : max(1, v.n_pos - 1);
     for (int i = lane * step; i < v.n_pos; i += 32 * step) {
-        const int c = v.pos0 + i;
-        const Range r = query_range(p.m, d.len_base + c, p.total, p.m.doc_start ? __ldg(p.m.doc_start + c) : 0);
+        const Range r = row_view(p, v.pos0 + i).r;
         if (r.hi > r.lo) {
             a0 = min(a0, r.lo);
             a1 = max(a1, r.hi);
@@ -247,11 +266,9 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
     const int g = p.g, ppt = p.ppu;   // positions per query tile
     const uint32_t sbase = smem_u32(smem);
     int32_t *prefix = reinterpret_cast<int32_t *>(smem + C::PREFIX);
-    Range *ranges = reinterpret_cast<Range *>(smem + C::RANGE);
     int32_t *misc = reinterpret_cast<int32_t *>(smem + C::MISC);
     volatile int32_t *abort_sh = misc + 12;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(misc + 13);
-    volatile int32_t *last_sh = misc + 14;
     volatile uint32_t *mask_sh = reinterpret_cast<volatile uint32_t *>(misc + 16);   // loaded blocks of key tile kt, slot kt mod 4
     auto bar = [&](int i) { return sbase + C::BARS + 8u * static_cast<uint32_t>(i); };
     // barriers: per ring slot, then per query tile
@@ -294,6 +311,10 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
     for (int u = warp; u < tp.units; u += kMtThreads / 32) {
         const UnitView v = unit_view(tp, u, lane);
         if (lane == 0) prefix[u + 1] = v.tiles;
+        if (p.lens && blockIdx.x == 0 && lane == 0) {
+            const int n = __ldg(p.lens + u);
+            if (n < 0 || static_cast<int64_t>(n) > static_cast<int64_t>(p.max_blocks) * kBS) atomicOr(p.err, KVC_EBIT_RANGE);
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -316,8 +337,12 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
         for (int u = b; u < e; ++u) {
             before += prefix[u + 1];
             prefix[u + 1] = before;
+            if (blockIdx.x == 0 && !tp.whole) tp.prefix[u + 1] = before;
         }
-        if (tid == 0) prefix[0] = 0;
+        if (tid == 0) {
+            prefix[0] = 0;
+            if (blockIdx.x == 0 && !tp.whole) tp.prefix[0] = 0;
+        }
         __syncthreads();
     }
     Walk walk;
@@ -386,8 +411,7 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
                             if (used && mp.doc_start) {
                                 used = false;
                                 for (int i = 0; i < pv.n_pos && !used; ++i) {
-                                    const int c = pv.pos0 + i;
-                                    const Range r = query_range(mp, p.len_base + c, tp.total, __ldg(mp.doc_start + c));
+                                    const Range r = row_view(tp, pv.pos0 + i).r;
                                     used = (t >= r.lo && t < r.hi) || (t >= r.d && t < r.e);
                                 }
                             }
@@ -407,14 +431,14 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
             bool go = true;
             for (Segment s = walk.next(); go && s.ok; s = walk.next()) {
                 v = unit_view(tp, s.unit, lane);
+                const int32_t *bt = p.bt + (p.lens ? static_cast<int64_t>(s.unit) * p.bt_stride : 0);
                 auto entry = [&](int k) -> int32_t {   // table entry of this lane's block of tile k
                     const int vb = k * kMtBlocks + bl;
-                    return k < s.k1 && vb < v.br.n ? __ldg(p.bt + v.br.at(vb)) : -1;
+                    return k < s.k1 && vb < v.br.n ? __ldg(bt + v.br.at(vb)) : -1;
                 };
                 auto is_read = [&](int t) {   // some row of the unit reads a position of block [t, t + 16)
                     for (int i = 0; i < v.n_pos; ++i) {
-                        const int c = v.pos0 + i;
-                        const Range r = query_range(mp, p.len_base + c, tp.total, mp.doc_start ? __ldg(mp.doc_start + c) : 0);
+                        const Range r = row_view(tp, v.pos0 + i).r;
                         if ((t < r.hi && t + kBS > r.lo && r.hi > r.lo) || (t < r.e && t + kBS > r.d && r.e > r.d)) return true;
                     }
                     return false;
@@ -484,25 +508,26 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
             const uint64_t desc_q = tc_smem_desc(sbase + C::Q + x * C::TILE, 16, 1024, kSwizzle128B);
             const uint32_t tm_s = tmem + 128 * x, tm_o = tmem + 256 + 128 * x;
             uint32_t kt = 0, it = 0, seg = 0;   // key tiles, this query tile's steps and its segments so far
-            // scores of step i of a segment whose first key tile is the CTA's kt0-th
-            auto scores = [&](uint32_t kt0, uint32_t i) -> bool {
-                const uint32_t tile = kt0 + (i >> 1), slot = tile & 1, half = i & 1;
-                if (half == 0 && !wait(kfull(slot), (tile >> 1) & 1)) return false;
+            // scores of step i of a segment whose first key tile is the CTA's kt0-th, into score buffer b: 64 keys
+            // of a tile (its halves in turn, or chain x's half of every tile)
+            auto scores = [&](uint32_t kt0, uint32_t i, uint32_t b) -> bool {
+                const uint32_t tile = kt0 + (tp.split ? i : i >> 1), slot = tile & 1, half = tp.split ? x : i & 1;
+                if ((tp.split || half == 0) && !wait(kfull(slot), (tile >> 1) & 1)) return false;
                 tc_fence_after();
                 const uint64_t b0 = tc_smem_desc(sbase + C::K + slot * C::TILE + half * (kMtStep * 128), 16, 1024, kSwizzle128B);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)   // 16 channels (32 bytes) per MMA, 4 per 128-byte band
-                    tc_mma_f16_warp(tm_s + half * kMtStep, tc_desc_advance(desc_q, (kk >> 2) * C::BAND + (kk & 3) * 32),
+                    tc_mma_f16_warp(tm_s + b * kMtStep, tc_desc_advance(desc_q, (kk >> 2) * C::BAND + (kk & 3) * 32),
                                     tc_desc_advance(b0, (kk >> 2) * C::BAND + (kk & 3) * 32), idesc_qk, kk > 0 ? 1u : 0u);
-                tc_commit_warp(sfull(x, half));
-                if (half == 1) tc_commit_warp(kfree(slot));
+                tc_commit_warp(sfull(x, b));
+                if (tp.split || half == 1) tc_commit_warp(kfree(slot));
                 return true;
             };
             bool go = true;
             for (Segment s = walk.next(); go && s.ok; s = walk.next()) {
                 const int n = s.k1 - s.k0;
                 // the second tile may hold no position: it only lets the key and value tiles go
-                if (s.unit * 2 * ppt + x * ppt >= p.n_pos) {
+                if (!tp.split && s.unit * 2 * ppt + x * ppt >= p.n_pos) {
                     for (int k = 0; go && k < n; ++k, ++kt) {
                         const int slot = kt & 1;
                         const uint32_t par = (kt >> 1) & 1;
@@ -517,10 +542,12 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
                 if (!wait(qfull(x), seg & 1)) break;
                 ++seg;
                 tc_fence_after();
-                go = scores(kt, 0) && scores(kt, 1);
-                for (uint32_t i = 0; go && i < 2u * n; ++i, ++it) {
-                    const uint32_t tile = kt + (i >> 1), slot = tile & 1, half = i & 1, par = (it >> 1) & 1;
-                    if ((half == 0 && !wait(vready(slot), (tile >> 1) & 1)) || !wait(pfull(x, half), par)) {
+                const uint32_t steps = tp.split ? n : 2 * n;
+                go = scores(kt, 0, it & 1) && (steps < 2 || scores(kt, 1, (it + 1) & 1));
+                for (uint32_t i = 0; go && i < steps; ++i, ++it) {
+                    const uint32_t tile = kt + (tp.split ? i : i >> 1), slot = tile & 1, half = tp.split ? x : i & 1;
+                    const uint32_t b = it & 1, par = (it >> 1) & 1;
+                    if (((tp.split || half == 0) && !wait(vready(slot), (tile >> 1) & 1)) || !wait(pfull(x, b), par)) {
                         go = false;
                         break;
                     }
@@ -529,12 +556,12 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
                                                      kSwizzle128B);
 #pragma unroll
                     for (int kk = 0; kk < kMtStep / 16; ++kk)   // 16 keys: 8 columns of P, 2048 bytes of value rows
-                        tc_mma_f16_tmem_a_warp(tm_o, tm_s + half * kMtStep + kk * 8, tc_desc_advance(v0, kk * 2048),
-                                               idesc_pv, (i > 0 || kk > 0) ? 1u : 0u);
-                    if (half == 1) tc_commit_warp(vfree(slot));
-                    tc_commit_warp(pvdone(x, half));
+                        tc_mma_f16_tmem_a_warp(tm_o, tm_s + b * kMtStep + kk * 8, tc_desc_advance(v0, kk * 2048), idesc_pv,
+                                               (i > 0 || kk > 0) ? 1u : 0u);
+                    if (tp.split || half == 1) tc_commit_warp(vfree(slot));
+                    tc_commit_warp(pvdone(x, b));
                     // the scores two steps on go over these weights, once the product has read them
-                    if (i + 2 < 2u * n) go = wait(pvdone(x, half), par) && scores(kt, i + 2);
+                    if (i + 2 < steps) go = wait(pvdone(x, b), par) && scores(kt, i + 2, b);
                 }
                 kt += n;
             }
@@ -551,34 +578,44 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
             const uint32_t kt0 = kt;
             kt += s.k1 - s.k0;
             const UnitView v = unit_view(tp, s.unit, lane);
-            const int c0 = v.pos0 + x * ppt, c = c0 + row / g;   // chunk position of this row
+            const int c0 = v.pos0 + (tp.split ? 0 : x * ppt), c = c0 + row / g;   // chunk position of this row
             const bool mine = c0 < p.n_pos;
             const bool real = row < ppt * g && c < p.n_pos;
             const size_t orow = static_cast<size_t>(c) * p.H_Q + s.head * g + row % g;
             if (!mine) continue;   // the same for the whole CTA
             // ---- queries into shared memory (zero where there is none), every load in flight at once
             {
-                constexpr int N = D / 8;   // 16-byte chunks of a row, and chunks per thread
+                constexpr int N = D / 8, STEP = 128 / N;   // 16-byte chunks of a row; rows between a thread's chunks
+                const int dc = STEP / g, dh = STEP % g, ch = row % N;
+                int r = row / N, cp = c0 + r / g, hh = r % g;
                 uint4 q[N];
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
-                    const int r = (row + 128 * i) / N, ch = row % N, cp = c0 + r / g;
                     q[i] = make_uint4(0u, 0u, 0u, 0u);
                     if (r < ppt * g && cp < p.n_pos)
-                        q[i] = __ldg(reinterpret_cast<const uint4 *>(p.q + (static_cast<size_t>(cp) * p.H_Q + s.head * g + r % g) * D) + ch);
+                        q[i] = __ldg(reinterpret_cast<const uint4 *>(p.q + (static_cast<size_t>(cp) * p.H_Q + s.head * g + hh) * D) + ch);
+                    r += STEP;
+                    cp += dc;
+                    hh += dh;
+                    if (hh >= g) {
+                        hh -= g;
+                        ++cp;
+                    }
                 }
 #pragma unroll
                 for (int i = 0; i < N; ++i)
-                    sts128(sbase + C::Q + x * C::TILE + ((row % N) >> 3) * C::BAND + sw128((row + 128 * i) / N, row & 7), q[i]);
+                    sts128(sbase + C::Q + x * C::TILE + (ch >> 3) * C::BAND + sw128(row / N + STEP * i, ch & 7), q[i]);
             }
             fence_proxy_async_smem();
             tc_fence_before();   // this thread's reads of the last segment's outputs
             mbar_arrive(qfull(x));
             Range r{0, 0, 0, 0};
             float slope = 0.f;
-            const int pos = p.len_base + c;
+            int pos = 0;
             if (real) {
-                r = query_range(mp, pos, tp.total, mp.doc_start ? __ldg(mp.doc_start + c) : 0);
+                const RowView rv = row_view(tp, c);
+                r = rv.r;
+                pos = rv.pos;
                 if (mp.alibi) slope = __ldg(mp.alibi + s.head * g + row % g) * 1.4426950408889634f;
             }
             // every real row of the warp reads [flo, fhi) and [fd, fe)
@@ -590,25 +627,26 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
             // scores in registers are raw, or already modified and in log2 units (bias, or a cap with a maximum)
             const bool ready = mp.capped || mp.alibi;
             const float mul = ready ? 1.f : p.scale_log2;
-            for (int i = 0; i < 2 * (s.k1 - s.k0); ++i, ++it) {
-                const int half = it & 1;
-                if (!wait(sfull(x, half), (it >> 1) & 1)) {
+            const int steps = tp.split ? s.k1 - s.k0 : 2 * (s.k1 - s.k0);
+            for (int i = 0; i < steps; ++i, ++it) {
+                const int b = it & 1, half = tp.split ? x : i & 1, tile = tp.split ? i : i >> 1;
+                if (!wait(sfull(x, b), (it >> 1) & 1)) {
                     go = false;
                     break;
                 }
                 tc_fence_after();
                 if (!any_real) {   // rows past the chunk: their weights stay in their own lanes and are never read
-                    mbar_arrive(pfull(x, half));
+                    mbar_arrive(pfull(x, b));
                     continue;
                 }
-                const uint32_t tsb = ts + half * kMtStep;
+                const uint32_t tsb = ts + b * kMtStep;
                 uint32_t r0[32], r1[32];
                 tmem_ld32(tsb, r0);
                 tmem_ld32(tsb + 32, r1);
-                const int first = s.k0 * kMtBlocks + i * kMtStepBlocks;   // the step's first virtual block
+                const int first = (s.k0 + tile) * kMtBlocks + half * kMtStepBlocks;   // the step's first virtual block
                 const bool one_run = first + kMtStepBlocks <= v.br.n && (first + kMtStepBlocks <= v.br.n0 || first >= v.br.n0);
                 const int t0 = v.br.at(first) * kBS;
-                const uint32_t loaded = mask_sh[(kt0 + (i >> 1)) & 3] >> (half * kMtStepBlocks) & ((1u << kMtStepBlocks) - 1u);
+                const uint32_t loaded = mask_sh[(kt0 + tile) & 3] >> (half * kMtStepBlocks) & ((1u << kMtStepBlocks) - 1u);
                 const bool full = one_run && loaded == (1u << kMtStepBlocks) - 1u &&
                                   ((t0 >= flo && t0 + kMtStep <= fhi) || (t0 >= fd && t0 + kMtStep <= fe));
                 // bit j of a 16-key block's mask: this row reads the block's key j
@@ -716,7 +754,7 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
                     }
                     // the warp rescales its rows of O together, once the previous product is in them
                     if (i > 0 && __any_sync(kFull, move && alpha != 1.f)) {
-                        if (!wait(pvdone(x, half ^ 1), ((it - 1) >> 1) & 1)) {
+                        if (!wait(pvdone(x, b ^ 1), ((it - 1) >> 1) & 1)) {
                             go = false;
                             break;
                         }
@@ -739,9 +777,9 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
                 tmem_st32(tsb, pk);   // over the first half of the step's scores
                 tmem_st_wait();
                 tc_fence_before();
-                mbar_arrive(pfull(x, half));
+                mbar_arrive(pfull(x, b));
             }
-            if (go) go = wait(pvdone(x, 1), ((it - 1) >> 1) & 1);   // a segment has an even number of steps
+            if (go) go = wait(pvdone(x, (it - 1) & 1), ((it - 1) >> 1) & 1);   // the segment's last product
             // every thread of the query tile takes this vote once per segment, so the barriers below meet
             if (!tile_all(go, 4 + x)) {
                 timed_out = true;
@@ -749,180 +787,40 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
             }
             tc_fence_after();
 
-            // ---- epilogue: the unit's rows, or a piece of them that the unit's last CTA merges (each query
-            // tile on its own)
-            const bool done = s.k0 == 0 && s.k1 == s.tiles;
-            const int64_t a = s.start, b = s.start + s.tiles;
-            const int64_t cf = ((a + 1) * G - 1) / W, cl = (b * G - 1) / W;   // CTAs holding its first and last tile
-            const int n = done ? 1 : static_cast<int>(cl - cf) + 1;
-            const int nrows = min(ppt, p.n_pos - c0) * g;
-            const bool first_second = !done && cf * W / G < a;   // the first CTA's piece is its second one
-            auto part_of = [&](int i) { return 2 * (cf + i) + (i == 0 && first_second ? 1 : 0); };
+            // ---- epilogue: the unit's rows, or a piece of them for the merge (rows [128 x, 128 x + 128) of a slot)
+            const bool done = s.k0 == 0 && s.k1 == s.tiles && !tp.split;
+            if (!any_real) continue;
+            const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (piece > 0 ? 1 : 0);
             const int prow = x * 128 + row;
-            uint32_t *ctr = done ? nullptr : tp.counters + 2 * (static_cast<size_t>(s.head) * tp.units + s.unit) + x;
-            const int own = static_cast<int>(blockIdx.x - cf);
-            bool last = false, keep = false;   // keep: this piece is merged from TMEM and never written
-            if (!done) {
-                if (nrows > 32) {   // the other pieces may all be there already
-                    if (row == 0) last_sh[x] = ld_acquire(ctr) == static_cast<uint32_t>(n - 1);
-                    asm volatile("bar.sync %0, 128;" ::"r"(4 + x) : "memory");
-                    keep = last_sh[x] != 0;
-                }
-                if (!keep) {
-                    const int64_t mine_part = part_of(own);
-                    if (any_real) {
+            const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-                        for (int part = 0; part < D / 32; ++part) {
-                            uint32_t o[32];
-                            tmem_ld32(to + part * 32, o);
-                            tmem_ld_wait(o);
-                            if (real) {
-                                // [channel / 4][row]: a warp's rows are contiguous
-                                float4 *dst = reinterpret_cast<float4 *>(tp.part_o) + (mine_part * (D / 4) + part * 8) * 256 + prow;
-#pragma unroll
-                                for (int c = 0; c < 8; ++c)
-                                    dst[c * 256] = make_float4(__uint_as_float(o[4 * c]), __uint_as_float(o[4 * c + 1]),
-                                                               __uint_as_float(o[4 * c + 2]), __uint_as_float(o[4 * c + 3]));
-                            }
-                        }
-                    }
-                    if (real) tp.part_ml[mine_part * 256 + prow] = make_float2(m, l);
-                    __threadfence();
-                    asm volatile("bar.sync %0, 128;" ::"r"(4 + x) : "memory");   // also: last_sh has been read
-                    if (row == 0) last_sh[x] = atomicAdd(ctr, 1u) == static_cast<uint32_t>(n - 1);
-                    asm volatile("bar.sync %0, 128;" ::"r"(4 + x) : "memory");
-                    last = last_sh[x] != 0;
-                }
-                asm volatile("bar.sync %0, 128;" ::"r"(4 + x) : "memory");   // last_sh may be written again
-                if (!keep && !last) continue;
-                __threadfence();
-                if (row == 0) *ctr = 0u;   // ready for the next launch
-            }
-            if (!done && !keep && nrows <= 32) {
-                // few rows, often many pieces: lane = row, the tile's warps share the channels
-                constexpr int CW = D / 4;   // channels per warp
-                if (lane < nrows) {
-                    const int pr = x * 128 + lane, w0 = (warp & 3) * CW;
-                    float M = -INFINITY;
-#pragma unroll 8
-                    for (int t = 0; t < n; ++t) {
-                        const float2 ml = __ldcg(tp.part_ml + part_of(t) * 256 + pr);
-                        M = fmaxf(M, ml.y != 0.f ? ml.x : -INFINITY);
-                    }
-                    float L = 0.f, acc[CW] = {};
-#pragma unroll 2
-                    for (int t = 0; t < n; ++t) {
-                        const int64_t pt = part_of(t);
-                        const float2 ml = __ldcg(tp.part_ml + pt * 256 + pr);
-                        const float4 *src = reinterpret_cast<const float4 *>(tp.part_o) + (pt * (D / 4) + w0 / 4) * 256 + pr;
-                        float4 u[CW / 4];
-#pragma unroll
-                        for (int c = 0; c < CW / 4; ++c) u[c] = __ldcg(src + c * 256);
-                        if (ml.y == 0.f) continue;   // the piece reads nothing for this row
-                        const float e = fast_exp2(ml.x - M);
-                        L = fmaf(e, ml.y, L);
-#pragma unroll
-                        for (int c = 0; c < CW / 4; ++c) {
-                            acc[4 * c] = fmaf(e, u[c].x, acc[4 * c]);
-                            acc[4 * c + 1] = fmaf(e, u[c].y, acc[4 * c + 1]);
-                            acc[4 * c + 2] = fmaf(e, u[c].z, acc[4 * c + 2]);
-                            acc[4 * c + 3] = fmaf(e, u[c].w, acc[4 * c + 3]);
-                        }
-                    }
-                    const size_t ob = static_cast<size_t>(c0 + lane / g) * p.H_Q + s.head * g + lane % g;
-                    const float li = L == 0.f ? 0.f : 1.f / L;
-                    uint4 *dst = reinterpret_cast<uint4 *>(mp.out + ob * D + w0);
-#pragma unroll
-                    for (int c = 0; c < CW / 8; ++c)
-                        dst[c] = make_uint4(pack_bf16(acc[8 * c] * li, acc[8 * c + 1] * li),
-                                            pack_bf16(acc[8 * c + 2] * li, acc[8 * c + 3] * li),
-                                            pack_bf16(acc[8 * c + 4] * li, acc[8 * c + 5] * li),
-                                            pack_bf16(acc[8 * c + 6] * li, acc[8 * c + 7] * li));
-                    if (w0 == 0 && p.lse) p.lse[ob] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
-                }
-                continue;
-            }
-            // thread = row; the row's pieces in CTA order (this one from TMEM when kept), so that the sums do
-            // not depend on which CTA is last.  Weights in the tile's query memory (its products are done),
-            // every thread its own column.
-            if (any_real) {
-                float M = m, L = l;
-                float *wsh = reinterpret_cast<float *>(smem + C::Q + x * C::TILE) + row;
-                if (!done) {
-                    M = -INFINITY;
-                    L = 0.f;
-                    if (real) {
-#pragma unroll 4
-                        for (int t = 0; t < n; ++t) {
-                            const float2 ml = keep && t == own ? make_float2(m, l) : __ldcg(tp.part_ml + part_of(t) * 256 + prow);
-                            M = fmaxf(M, ml.y != 0.f ? ml.x : -INFINITY);
-                        }
-#pragma unroll 4
-                        for (int t = 0; t < n; ++t) {
-                            const float2 ml = keep && t == own ? make_float2(m, l) : __ldcg(tp.part_ml + part_of(t) * 256 + prow);
-                            const float e = ml.y != 0.f ? fast_exp2(ml.x - M) : 0.f;   // 0: the piece reads nothing
-                            L = fmaf(e, ml.y, L);
-                            if (t < C::TILE / 512) wsh[t * 128] = e;
-                        }
-                    }
-                }
-                const float inv = L == 0.f ? 0.f : 1.f / L;
-#pragma unroll
-                for (int part = 0; part < D / 32; ++part) {
-                    uint32_t o[32];
-                    if (done || keep) {
-                        tmem_ld32(to + part * 32, o);
-                        tmem_ld_wait(o);
-                    }
-                    if (!real) continue;
-                    if (!done) {
-                        float acc[32] = {};
-                        for (int t = 0; t < n; ++t) {
-                            const bool here = keep && t == own;
-                            const int64_t pt = part_of(t);
-                            float e;
-                            if (t < C::TILE / 512) {
-                                e = wsh[t * 128];
-                            } else {
-                                const float2 ml = here ? make_float2(m, l) : __ldcg(tp.part_ml + pt * 256 + prow);
-                                e = ml.y != 0.f ? fast_exp2(ml.x - M) : 0.f;
-                            }
-                            if (here) {
-#pragma unroll
-                                for (int c = 0; c < 32; ++c) acc[c] = e == 0.f ? acc[c] : fmaf(e, __uint_as_float(o[c]), acc[c]);
-                            } else {
-                                const float4 *src = reinterpret_cast<const float4 *>(tp.part_o) + (pt * (D / 4) + part * 8) * 256 + prow;
-                                float4 u[8];
-#pragma unroll
-                                for (int c = 0; c < 8; ++c) u[c] = __ldcg(src + c * 256);
-                                if (e != 0.f) {
-#pragma unroll
-                                    for (int c = 0; c < 8; ++c) {
-                                        acc[4 * c] = fmaf(e, u[c].x, acc[4 * c]);
-                                        acc[4 * c + 1] = fmaf(e, u[c].y, acc[4 * c + 1]);
-                                        acc[4 * c + 2] = fmaf(e, u[c].z, acc[4 * c + 2]);
-                                        acc[4 * c + 3] = fmaf(e, u[c].w, acc[4 * c + 3]);
-                                    }
-                                }
-                            }
-                        }
-#pragma unroll
-                        for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(acc[c]);
-                    }
+            for (int part = 0; part < D / 32; ++part) {
+                uint32_t o[32];
+                tmem_ld32(to + part * 32, o);
+                tmem_ld_wait(o);
+                if (!real) continue;
+                if (done) {
                     uint4 *dst = reinterpret_cast<uint4 *>(mp.out + orow * D + part * 32);
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         uint32_t w[4];
 #pragma unroll
                         for (int u = 0; u < 4; ++u)
-                            w[u] = L == 0.f ? 0u : pack_bf16(__uint_as_float(o[8 * c + 2 * u]) * inv,
+                            w[u] = l == 0.f ? 0u : pack_bf16(__uint_as_float(o[8 * c + 2 * u]) * inv,
                                                              __uint_as_float(o[8 * c + 2 * u + 1]) * inv);
                         dst[c] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
+                } else {
+                    // [channel / 4][row]: a warp's rows are contiguous
+                    float4 *dst = reinterpret_cast<float4 *>(tp.part_o) + (slot * (D / 4) + part * 8) * 256 + prow;
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        dst[c * 256] = make_float4(__uint_as_float(o[4 * c]), __uint_as_float(o[4 * c + 1]),
+                                                   __uint_as_float(o[4 * c + 2]), __uint_as_float(o[4 * c + 3]));
                 }
-                if (real && p.lse) p.lse[orow] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
             }
-            if (!done) asm volatile("bar.sync %0, 128;" ::"r"(4 + x) : "memory");   // the weights' memory takes queries next
+            if (real && done && p.lse) p.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+            if (real && !done) tp.part_ml[slot * 256 + prow] = make_float2(m, l);
         }
     }
     if (timed_out && lane == 0) atomicOr(p.err, KVC_EBIT_TIMEOUT);
@@ -934,7 +832,66 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
     }
 }
 
+// Adds the pieces of units that CTA borders cut, in CTA order (in few-row calls: chain 0's and chain 1's of
+// every CTA):  M = max m_s, L = sum 2^(m_s - M) l_s, out = sum 2^(m_s - M) o_s / L, lse = (M + log2 L) ln 2.
+// grid (row groups, units, KV heads); 256 threads = 1024 / D rows x D / 4 float4 columns.  A programmatic
+// dependent of mod_tc_kernel (its CTAs are in place when that ends).  ctas: that kernel's grid.
+template <int D>
+__global__ void __launch_bounds__(256) mod_tc_merge_kernel(const ModTcParams tp, const int ctas)
+{
+    constexpr int RG = 1024 / D;   // rows per CTA
+    const ModParams &mp = tp.m;
+    const DecodeParams &p = mp.d;
+    const int unit = blockIdx.y, head = blockIdx.z, g = p.g;
+    const int rr = blockIdx.x * RG + threadIdx.x % RG, d4 = threadIdx.x / RG;   // row of the unit, float4 column
+    allow_dependent_launch();
+    grid_dependency_wait();
+    const int per_head = tp.prefix[tp.units];
+    const int64_t W = static_cast<int64_t>(p.H_KV) * per_head, G = min(static_cast<int64_t>(ctas), W);
+    const int64_t a = static_cast<int64_t>(head) * per_head + tp.prefix[unit];
+    const int64_t b = static_cast<int64_t>(head) * per_head + tp.prefix[unit + 1];
+    const int64_t cf = ((a + 1) * G - 1) / W, cl = (b * G - 1) / W;   // CTAs holding its first and last tile
+    if (cf == cl && !tp.split) return;
+    const int n = static_cast<int>(cl - cf + 1) * (tp.split ? 2 : 1);
+    const bool first_second = cf * W / G < a;   // the first CTA's piece is its second one
+    const int tile = rr >> 7, r = rr & 127;
+    const int c = unit * (tp.split ? p.ppu : 2 * p.ppu) + tile * p.ppu + r / g;
+    if (r >= p.ppu * g || c >= p.n_pos) return;
+    // piece t: slot and row in it
+    auto at = [&](int t) -> int64_t {
+        const int cta = tp.split ? t >> 1 : t, chain = tp.split ? t & 1 : tile;
+        return (2 * (cf + cta) + (cta == 0 && first_second ? 1 : 0)) * 256 + chain * 128 + r;
+    };
+    float M = -INFINITY;
+#pragma unroll 8
+    for (int t = 0; t < n; ++t) {
+        const float2 ml = tp.part_ml[at(t)];
+        M = fmaxf(M, ml.y != 0.f ? ml.x : -INFINITY);
+    }
+    float L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int t = 0; t < n; ++t) {
+        const int64_t i = at(t);
+        const float2 ml = tp.part_ml[i];
+        const float4 o = reinterpret_cast<const float4 *>(tp.part_o)[((i >> 8) * (D / 4) + d4) * 256 + (i & 255)];
+        const bool some = ml.y != 0.f;   // else the piece reads nothing for this row
+        const float e = some ? fast_exp2(ml.x - M) : 0.f;
+        L = fmaf(e, ml.y, L);
+        acc.x = some ? fmaf(e, o.x, acc.x) : acc.x;
+        acc.y = some ? fmaf(e, o.y, acc.y) : acc.y;
+        acc.z = some ? fmaf(e, o.z, acc.z) : acc.z;
+        acc.w = some ? fmaf(e, o.w, acc.w) : acc.w;
+    }
+    const size_t orow = static_cast<size_t>(c) * p.H_Q + head * g + r % g;
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    *reinterpret_cast<uint2 *>(mp.out + orow * D + 4 * d4) =
+        L == 0.f ? make_uint2(0u, 0u) : make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+    if (d4 == 0 && p.lse) p.lse[orow] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+}
+
 // The tensor-memory kernel for a head width (bf16 pools); fixed: capped scores against a fixed reference.
 DecodeKernel select_mod_tc(int D, bool fixed);
+const void *select_mod_tc_merge(int D);
 
 }  // namespace kvc
