@@ -204,7 +204,7 @@ static kvc_status run_tc(kvc_pool *pool, const ModParams &mp0, void *ws, size_t 
         }
         tp.units = (p.n_pos + unit - 1) / unit;
         // no more CTAs than the line of tiles can have tiles
-        const int64_t most = static_cast<int64_t>(p.H_KV) * tp.units * ((p.max_blocks + kMtBlocks - 1) / kMtBlocks);
+        const int64_t most = static_cast<int64_t>(p.H_KV) * tp.units * ((p.max_blocks + kMtBlocks - 1) / kMtBlocks + kMtStart);
         const int ctas = static_cast<int>(std::min<int64_t>(pool->num_sms, most));
         if (!tp.whole) {
             if (ws_bytes < kCounterBytes + tc_bytes(ctas, pool->D)) return KVC_ERR_ARG;
@@ -218,9 +218,9 @@ static kvc_status run_tc(kvc_pool *pool, const ModParams &mp0, void *ws, size_t 
         if (e != cudaSuccess) return cuda_status(e);
         g_launches.fetch_add(1, std::memory_order_relaxed);
         if (!tp.whole && (tp.split || most > 1)) {
-            const int rows = tp.split ? p.ppu * p.g : 256, per = 1024 / pool->D;
+            const int rows = tp.split ? std::min(p.ppu, p.n_pos) * p.g : 256, per = 1024 / pool->D / (tp.split ? 8 : 1);
             void *margs[] = {&tp, const_cast<int *>(&ctas)};
-            e = launch_dependent(select_mod_tc_merge(pool->D), dim3((rows + per - 1) / per, tp.units, p.H_KV), dim3(256), 0,
+            e = launch_dependent(select_mod_tc_merge(pool->D, tp.split != 0), dim3((rows + per - 1) / per, tp.units, p.H_KV), dim3(256), 0,
                                  stream, margs);
             if (e != cudaSuccess) return cuda_status(e);
             g_launches.fetch_add(1, std::memory_order_relaxed);

@@ -27,10 +27,13 @@ DecodeKernel select_mod_tc(int D, bool fixed)
     return fixed ? instance<128, true>() : instance<128, false>();
 }
 
-const void *select_mod_tc_merge(int D)
+const void *select_mod_tc_merge(int D, bool few)
 {
-    return D == 64 ? reinterpret_cast<const void *>(&mod_tc_merge_kernel<64>)
-                   : reinterpret_cast<const void *>(&mod_tc_merge_kernel<128>);
+    if (D == 64)
+        return few ? reinterpret_cast<const void *>(&mod_tc_merge_kernel<64, 8>)
+                   : reinterpret_cast<const void *>(&mod_tc_merge_kernel<64, 1>);
+    return few ? reinterpret_cast<const void *>(&mod_tc_merge_kernel<128, 8>)
+               : reinterpret_cast<const void *>(&mod_tc_merge_kernel<128, 1>);
 }
 
 }  // namespace kvc

@@ -18,6 +18,8 @@
 // unit form one line of W tiles; CTA c of G takes tiles [c W / G, (c + 1) W / G), whatever units they
 // belong to, so every SM gets the same work to within a tile: a late chunk of few long rows, a long
 // triangular one and a ragged decode batch alike.  A unit that lies in one CTA is written at once; a
+// unit's start costs about two tiles (its queries staged, its outputs written: 5 us against 2.5 us a
+// tile), so the line gives every unit kMtStart tiles more than it has.  A
 // unit cut by CTA borders leaves fp32 partials (at most two per CTA) for mod_tc_merge_kernel, which
 // adds them in CTA order.  (Merged by the unit's last CTA instead, 600 queries of 1800 positions took
 // 43 us, 20 pieces of a 5-query chunk 9 us of its 36: one SM's loads against all SMs'.)
@@ -43,6 +45,7 @@ constexpr int kMtStep = 64;                        // keys per score buffer
 constexpr int kMtStepBlocks = kMtStep / kBS;
 constexpr int kMtThreads = 384;
 constexpr int kMtUnits = 2048;                     // most units (per head) of one launch
+constexpr int kMtStart = 2;                        // a unit's start, in tiles
 constexpr float kMtCapLimit = 80.f;                // cap in log2 units up to which no maximum is needed
 
 struct ModTcParams {
@@ -51,7 +54,7 @@ struct ModTcParams {
     int32_t whole;        // 1: no partials, units are dealt whole
     int32_t split;        // 1: a unit is one query tile's positions, and both chains take its rows (below)
     int32_t total;        // positions the row holds (prefill)
-    int32_t *prefix;      // [units + 1] key tiles before each unit, for the merge
+    int32_t *prefix;      // [units + 1] place of each unit on a head's line, for the merge
     float *part_o;        // [2 G][D / 4][256] float4
     float2 *part_ml;      // [2 G][256]
 };
@@ -205,18 +208,28 @@ __device__ __forceinline__ UnitView unit_view(const ModTcParams &p, int u, int l
     return v;
 }
 
+// The same count of tiles without documents, one thread.
+__device__ __forceinline__ int unit_tiles(const ModTcParams &p, int u)
+{
+    const int ppu = p.split ? p.m.d.ppu : 2 * p.m.d.ppu, c = u * ppu;
+    const Range f = row_view(p, c).r, l = row_view(p, min(c + ppu, p.m.d.n_pos) - 1).r;
+    const bool fe = f.e > f.d, le = l.e > l.d;
+    const BlockRuns br = block_runs(le ? (fe ? min(f.d, l.d) : l.d) : 0, le ? l.e : 0, f.lo, l.hi);
+    return max(1, (br.n + kMtBlocks - 1) / kMtBlocks);
+}
+
 // A run of key tiles [k0, k1) of (head, unit).
 struct Segment {
     int head, unit, k0, k1, tiles;
-    int64_t start;   // the unit's first tile on the line of all tiles
     bool ok;
 };
 
-// Walks a CTA's share of the line of tiles; every role makes the same walk.
+// Walks a CTA's share of the line; every role makes the same walk.  A unit's first kMtStart places
+// hold no tile.
 struct Walk {
     const int32_t *prefix;
     int units, per_head;
-    int64_t at, end;      // whole: unit counters instead of tile counters
+    int64_t at, end;      // whole: unit counters instead of places
     bool whole;
     int stride;
     __device__ __forceinline__ Segment next()
@@ -227,10 +240,9 @@ struct Walk {
         if (whole) {
             s.head = static_cast<int>(at / units);
             s.unit = static_cast<int>(at % units);
-            s.tiles = prefix[s.unit + 1] - prefix[s.unit];
+            s.tiles = prefix[s.unit + 1] - prefix[s.unit] - kMtStart;
             s.k0 = 0;
             s.k1 = s.tiles;
-            s.start = 0;
             at += stride;
             return s;
         }
@@ -243,11 +255,12 @@ struct Walk {
             else hi = mid;
         }
         s.unit = lo;
-        s.tiles = prefix[lo + 1] - prefix[lo];
-        s.start = static_cast<int64_t>(s.head) * per_head + prefix[lo];
-        s.k0 = static_cast<int>(at - s.start);
-        s.k1 = static_cast<int>(min(static_cast<int64_t>(s.tiles), end - s.start));
-        at = s.start + s.k1;
+        s.tiles = prefix[lo + 1] - prefix[lo] - kMtStart;
+        const int64_t first = static_cast<int64_t>(s.head) * per_head + prefix[lo] + kMtStart;   // place of its tile 0
+        s.k0 = static_cast<int>(max(at - first, static_cast<int64_t>(0)));
+        s.k1 = static_cast<int>(min(static_cast<int64_t>(s.tiles), end - first));
+        s.ok = s.k1 > s.k0;   // else the share ends before the unit's first tile
+        at = first + s.k1;
         return s;
     }
 };
@@ -307,13 +320,19 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
     allow_dependent_launch();
     grid_dependency_wait();
 
-    // ---- tiles per unit and their running sum (12 warps, one unit each at a time)
-    for (int u = warp; u < tp.units; u += kMtThreads / 32) {
-        const UnitView v = unit_view(tp, u, lane);
-        if (lane == 0) prefix[u + 1] = v.tiles;
-        if (p.lens && blockIdx.x == 0 && lane == 0) {
-            const int n = __ldg(p.lens + u);
-            if (n < 0 || static_cast<int64_t>(n) > static_cast<int64_t>(p.max_blocks) * kBS) atomicOr(p.err, KVC_EBIT_RANGE);
+    // ---- what each unit takes of the line, and the running sum
+    if (mp.doc_start) {
+        for (int u = warp; u < tp.units; u += kMtThreads / 32) {
+            const UnitView v = unit_view(tp, u, lane);
+            if (lane == 0) prefix[u + 1] = v.tiles + kMtStart;
+        }
+    } else {
+        for (int u = tid; u < tp.units; u += kMtThreads) {
+            prefix[u + 1] = unit_tiles(tp, u) + kMtStart;
+            if (p.lens && blockIdx.x == 0) {
+                const int n = __ldg(p.lens + u);
+                if (n < 0 || static_cast<int64_t>(n) > static_cast<int64_t>(p.max_blocks) * kBS) atomicOr(p.err, KVC_EBIT_RANGE);
+            }
         }
     }
     tc_fence_before();
@@ -584,6 +603,7 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
             const size_t orow = static_cast<size_t>(c) * p.H_Q + s.head * g + row % g;
             if (!mine) continue;   // the same for the whole CTA
             // ---- queries into shared memory (zero where there is none), every load in flight at once
+            asm volatile("bar.sync %0, 128;" ::"r"(4 + x) : "memory");   // the last segment's rows have left it
             {
                 constexpr int N = D / 8, STEP = 128 / N;   // 16-byte chunks of a row; rows between a thread's chunks
                 const int dc = STEP / g, dh = STEP % g, ch = row % N;
@@ -793,6 +813,10 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
             const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (piece > 0 ? 1 : 0);
             const int prow = x * 128 + row;
             const float inv = l == 0.f ? 0.f : 1.f / l;
+            // finished rows go through the warp's quarter of the tile's query memory (its products are done;
+            // 16-byte chunk c of row r at c ^ (r mod 8)), so that whole rows leave: a lane's row written
+            // straight to global memory measured 2.8 us a unit against 1.3 us
+            const uint32_t stage = sbase + C::Q + x * C::TILE + (warp & 3) * (C::TILE / 4);
 #pragma unroll
             for (int part = 0; part < D / 32; ++part) {
                 uint32_t o[32];
@@ -800,7 +824,6 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
                 tmem_ld_wait(o);
                 if (!real) continue;
                 if (done) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(mp.out + orow * D + part * 32);
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         uint32_t w[4];
@@ -808,7 +831,7 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
                         for (int u = 0; u < 4; ++u)
                             w[u] = l == 0.f ? 0u : pack_bf16(__uint_as_float(o[8 * c + 2 * u]) * inv,
                                                              __uint_as_float(o[8 * c + 2 * u + 1]) * inv);
-                        dst[c] = make_uint4(w[0], w[1], w[2], w[3]);
+                        sts128(stage + lane * (D * 2) + (((part * 4 + c) ^ (lane & 7)) << 4), make_uint4(w[0], w[1], w[2], w[3]));
                     }
                 } else {
                     // [channel / 4][row]: a warp's rows are contiguous
@@ -817,6 +840,27 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
                     for (int c = 0; c < 8; ++c)
                         dst[c * 256] = make_float4(__uint_as_float(o[4 * c]), __uint_as_float(o[4 * c + 1]),
                                                    __uint_as_float(o[4 * c + 2]), __uint_as_float(o[4 * c + 3]));
+                }
+            }
+            if (done) {
+                __syncwarp();
+                constexpr int N = D / 8, STEP = 32 / N;   // chunks of a row, rows a warp writes at once
+                const int ch = lane % N;
+                int r = (warp & 3) * 32 + lane / N, cp = c0 + r / g, hh = r % g;
+                const int dc = STEP / g, dh = STEP % g;
+#pragma unroll 4
+                for (int i = 0; i < N; ++i) {
+                    const int ri = lane / N + STEP * i;
+                    if (r < ppt * g && cp < p.n_pos)
+                        *reinterpret_cast<uint4 *>(mp.out + (static_cast<size_t>(cp) * p.H_Q + s.head * g + hh) * D + 8 * ch) =
+                            lds128(stage + ri * (D * 2) + ((ch ^ (ri & 7)) << 4));
+                    r += STEP;
+                    cp += dc;
+                    hh += dh;
+                    if (hh >= g) {
+                        hh -= g;
+                        ++cp;
+                    }
                 }
             }
             if (real && done && p.lse) p.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
@@ -834,54 +878,86 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
 
 // Adds the pieces of units that CTA borders cut, in CTA order (in few-row calls: chain 0's and chain 1's of
 // every CTA):  M = max m_s, L = sum 2^(m_s - M) l_s, out = sum 2^(m_s - M) o_s / L, lse = (M + log2 L) ln 2.
-// grid (row groups, units, KV heads); 256 threads = 1024 / D rows x D / 4 float4 columns.  A programmatic
-// dependent of mod_tc_kernel (its CTAs are in place when that ends).  ctas: that kernel's grid.
-template <int D>
+// grid (row groups, units, KV heads); 256 threads = rows x D / 4 float4 columns x T groups of pieces
+// (T = 8 for few-row calls, whose rows have tens of pieces each; else 1).  A programmatic dependent of
+// mod_tc_kernel (its CTAs are in place when that ends).  ctas: that kernel's grid.
+template <int D, int T>
 __global__ void __launch_bounds__(256) mod_tc_merge_kernel(const ModTcParams tp, const int ctas)
 {
-    constexpr int RG = 1024 / D;   // rows per CTA
+    constexpr int RG = 1024 / D / T, COLS = D / 4;   // rows per CTA, float4 columns
+    __shared__ float4 part[T > 1 ? 256 : 1];
+    __shared__ float part_l[T > 1 ? 256 : 1];
     const ModParams &mp = tp.m;
     const DecodeParams &p = mp.d;
     const int unit = blockIdx.y, head = blockIdx.z, g = p.g;
-    const int rr = blockIdx.x * RG + threadIdx.x % RG, d4 = threadIdx.x / RG;   // row of the unit, float4 column
+    const int rr = blockIdx.x * RG + threadIdx.x % RG, d4 = threadIdx.x / RG % COLS, grp = threadIdx.x / (RG * COLS);
     allow_dependent_launch();
     grid_dependency_wait();
     const int per_head = tp.prefix[tp.units];
     const int64_t W = static_cast<int64_t>(p.H_KV) * per_head, G = min(static_cast<int64_t>(ctas), W);
     const int64_t a = static_cast<int64_t>(head) * per_head + tp.prefix[unit];
     const int64_t b = static_cast<int64_t>(head) * per_head + tp.prefix[unit + 1];
-    const int64_t cf = ((a + 1) * G - 1) / W, cl = (b * G - 1) / W;   // CTAs holding its first and last tile
+    const int64_t cf = ((a + kMtStart + 1) * G - 1) / W, cl = (b * G - 1) / W;   // CTAs of its first and last tile
     if (cf == cl && !tp.split) return;
     const int n = static_cast<int>(cl - cf + 1) * (tp.split ? 2 : 1);
     const bool first_second = cf * W / G < a;   // the first CTA's piece is its second one
     const int tile = rr >> 7, r = rr & 127;
     const int c = unit * (tp.split ? p.ppu : 2 * p.ppu) + tile * p.ppu + r / g;
-    if (r >= p.ppu * g || c >= p.n_pos) return;
+    const bool real = r < p.ppu * g && c < p.n_pos;
+    if (T == 1 && !real) return;
     // piece t: slot and row in it
     auto at = [&](int t) -> int64_t {
         const int cta = tp.split ? t >> 1 : t, chain = tp.split ? t & 1 : tile;
         return (2 * (cf + cta) + (cta == 0 && first_second ? 1 : 0)) * 256 + chain * 128 + r;
     };
-    float M = -INFINITY;
-#pragma unroll 8
-    for (int t = 0; t < n; ++t) {
-        const float2 ml = tp.part_ml[at(t)];
-        M = fmaxf(M, ml.y != 0.f ? ml.x : -INFINITY);
-    }
-    float L = 0.f;
+    // every group finds its own maximum; the groups meet below
+    float M = -INFINITY, L = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (real) {
 #pragma unroll 8
-    for (int t = 0; t < n; ++t) {
-        const int64_t i = at(t);
-        const float2 ml = tp.part_ml[i];
-        const float4 o = reinterpret_cast<const float4 *>(tp.part_o)[((i >> 8) * (D / 4) + d4) * 256 + (i & 255)];
-        const bool some = ml.y != 0.f;   // else the piece reads nothing for this row
-        const float e = some ? fast_exp2(ml.x - M) : 0.f;
-        L = fmaf(e, ml.y, L);
-        acc.x = some ? fmaf(e, o.x, acc.x) : acc.x;
-        acc.y = some ? fmaf(e, o.y, acc.y) : acc.y;
-        acc.z = some ? fmaf(e, o.z, acc.z) : acc.z;
-        acc.w = some ? fmaf(e, o.w, acc.w) : acc.w;
+        for (int t = grp; t < n; t += T) {
+            const float2 ml = tp.part_ml[at(t)];
+            M = fmaxf(M, ml.y != 0.f ? ml.x : -INFINITY);
+        }
+#pragma unroll 8
+        for (int t = grp; t < n; t += T) {
+            const int64_t i = at(t);
+            const float2 ml = tp.part_ml[i];
+            const float4 o = reinterpret_cast<const float4 *>(tp.part_o)[((i >> 8) * COLS + d4) * 256 + (i & 255)];
+            const bool some = ml.y != 0.f;   // else the piece reads nothing for this row
+            const float e = some ? fast_exp2(ml.x - M) : 0.f;
+            L = fmaf(e, ml.y, L);
+            acc.x = some ? fmaf(e, o.x, acc.x) : acc.x;
+            acc.y = some ? fmaf(e, o.y, acc.y) : acc.y;
+            acc.z = some ? fmaf(e, o.z, acc.z) : acc.z;
+            acc.w = some ? fmaf(e, o.w, acc.w) : acc.w;
+        }
+    }
+    if constexpr (T > 1) {
+        __shared__ float part_m[256];
+        part[threadIdx.x] = acc;
+        part_l[threadIdx.x] = L;
+        part_m[threadIdx.x] = M;
+        __syncthreads();
+        if (grp > 0 || !real) return;
+        float top = M;
+#pragma unroll
+        for (int k = 1; k < T; ++k) top = fmaxf(top, part_m[threadIdx.x + k * RG * COLS]);
+        acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        L = 0.f;
+#pragma unroll
+        for (int k = 0; k < T; ++k) {
+            const int i = threadIdx.x + k * RG * COLS;
+            const float lk = part_l[i];
+            const float e = lk != 0.f ? fast_exp2(part_m[i] - top) : 0.f;   // a group without pieces: nothing
+            const float4 o = part[i];
+            L = fmaf(e, lk, L);
+            acc.x = e != 0.f ? fmaf(e, o.x, acc.x) : acc.x;
+            acc.y = e != 0.f ? fmaf(e, o.y, acc.y) : acc.y;
+            acc.z = e != 0.f ? fmaf(e, o.z, acc.z) : acc.z;
+            acc.w = e != 0.f ? fmaf(e, o.w, acc.w) : acc.w;
+        }
+        M = top;
     }
     const size_t orow = static_cast<size_t>(c) * p.H_Q + head * g + r % g;
     const float inv = L == 0.f ? 0.f : 1.f / L;
@@ -892,6 +968,6 @@ __global__ void __launch_bounds__(256) mod_tc_merge_kernel(const ModTcParams tp,
 
 // The tensor-memory kernel for a head width (bf16 pools); fixed: capped scores against a fixed reference.
 DecodeKernel select_mod_tc(int D, bool fixed);
-const void *select_mod_tc_merge(int D);
+const void *select_mod_tc_merge(int D, bool few);
 
 }  // namespace kvc
