@@ -218,7 +218,7 @@ static kvc_status run_tc(kvc_pool *pool, const ModParams &mp0, void *ws, size_t 
         if (e != cudaSuccess) return cuda_status(e);
         g_launches.fetch_add(1, std::memory_order_relaxed);
         if (!tp.whole && (tp.split || most > 1)) {
-            const int rows = tp.split ? std::min(p.ppu, p.n_pos) * p.g : 256, per = 1024 / pool->D / (tp.split ? 8 : 1);
+            const int rows = tp.split ? std::min(p.ppu, p.n_pos) * p.g : 256, per = tp.split ? 128 / pool->D : 32;
             void *margs[] = {&tp, const_cast<int *>(&ctas)};
             e = launch_dependent(select_mod_tc_merge(pool->D, tp.split != 0), dim3((rows + per - 1) / per, tp.units, p.H_KV), dim3(256), 0,
                                  stream, margs);

@@ -878,64 +878,78 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
 
 // Adds the pieces of units that CTA borders cut, in CTA order (in few-row calls: chain 0's and chain 1's of
 // every CTA):  M = max m_s, L = sum 2^(m_s - M) l_s, out = sum 2^(m_s - M) o_s / L, lse = (M + log2 L) ln 2.
-// grid (row groups, units, KV heads); 256 threads = rows x D / 4 float4 columns x T groups of pieces
-// (T = 8 for few-row calls, whose rows have tens of pieces each; else 1).  A programmatic dependent of
-// mod_tc_kernel (its CTAs are in place when that ends).  ctas: that kernel's grid.
+// Whole chunks: grid (8, units, KV heads), 256 threads = 32 rows x 8 groups of D / 8 channels (a thread has its
+// loads of a piece in flight at once, and the grid is about one wave).  Few-row calls (T = 8), whose rows have
+// tens of pieces: 256 threads = 128 / D rows x D / 4 float4 columns x 8 groups of pieces.
+// A programmatic dependent of mod_tc_kernel (its CTAs are in place when that ends).  ctas: that kernel's grid.
 template <int D, int T>
 __global__ void __launch_bounds__(256) mod_tc_merge_kernel(const ModTcParams tp, const int ctas)
 {
-    constexpr int RG = 1024 / D / T, COLS = D / 4;   // rows per CTA, float4 columns
-    __shared__ float4 part[T > 1 ? 256 : 1];
-    __shared__ float part_l[T > 1 ? 256 : 1];
+    constexpr int V = T > 1 ? 1 : D / 32;                // float4 columns per thread
+    constexpr int COLS = D / 4 / V, RG = 256 / COLS / T;   // column groups, rows per CTA
     const ModParams &mp = tp.m;
     const DecodeParams &p = mp.d;
     const int unit = blockIdx.y, head = blockIdx.z, g = p.g;
-    const int rr = blockIdx.x * RG + threadIdx.x % RG, d4 = threadIdx.x / RG % COLS, grp = threadIdx.x / (RG * COLS);
-    allow_dependent_launch();
-    grid_dependency_wait();
-    const int per_head = tp.prefix[tp.units];
-    const int64_t W = static_cast<int64_t>(p.H_KV) * per_head, G = min(static_cast<int64_t>(ctas), W);
-    const int64_t a = static_cast<int64_t>(head) * per_head + tp.prefix[unit];
-    const int64_t b = static_cast<int64_t>(head) * per_head + tp.prefix[unit + 1];
-    const int64_t cf = ((a + kMtStart + 1) * G - 1) / W, cl = (b * G - 1) / W;   // CTAs of its first and last tile
-    if (cf == cl && !tp.split) return;
-    const int n = static_cast<int>(cl - cf + 1) * (tp.split ? 2 : 1);
-    const bool first_second = cf * W / G < a;   // the first CTA's piece is its second one
+    const int rr = blockIdx.x * RG + threadIdx.x % RG, dg = threadIdx.x / RG % COLS, grp = threadIdx.x / (RG * COLS);
     const int tile = rr >> 7, r = rr & 127;
     const int c = unit * (tp.split ? p.ppu : 2 * p.ppu) + tile * p.ppu + r / g;
     const bool real = r < p.ppu * g && c < p.n_pos;
+    allow_dependent_launch();
+    grid_dependency_wait();
+    const int per_head = __ldcg(tp.prefix + tp.units), u0 = __ldcg(tp.prefix + unit), u1 = __ldcg(tp.prefix + unit + 1);
+    const int64_t W = static_cast<int64_t>(p.H_KV) * per_head, G = min(static_cast<int64_t>(ctas), W);
+    const int64_t a = static_cast<int64_t>(head) * per_head + u0, b = static_cast<int64_t>(head) * per_head + u1;
+    // the CTA that has place w of the line: the last c with c W / G <= w
+    auto cta_of = [&](int64_t w) -> int {
+        const int64_t num = (w + 1) * G - 1;
+        if (W * G < 0x7FFFFFFF) return static_cast<int>(static_cast<uint32_t>(num) / static_cast<uint32_t>(W));
+        return static_cast<int>(num / W);
+    };
+    const int cf = cta_of(a + kMtStart), cl = cta_of(b - 1);   // CTAs of the unit's first and last tile
+    if (cf == cl && !tp.split) return;
+    const int n = (cl - cf + 1) * (tp.split ? 2 : 1);
+    const bool first_second = cta_of(a - 1) == cf && a > 0;   // the first CTA has places before the unit: its second piece
     if (T == 1 && !real) return;
-    // piece t: slot and row in it
-    auto at = [&](int t) -> int64_t {
+    // piece t: slot * 256 + row in it
+    auto at = [&](int t) -> int {
         const int cta = tp.split ? t >> 1 : t, chain = tp.split ? t & 1 : tile;
         return (2 * (cf + cta) + (cta == 0 && first_second ? 1 : 0)) * 256 + chain * 128 + r;
     };
-    // every group finds its own maximum; the groups meet below
     float M = -INFINITY, L = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (real) {
+    float4 acc[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (real) {   // every group of pieces finds its own maximum; the groups meet below
 #pragma unroll 8
         for (int t = grp; t < n; t += T) {
-            const float2 ml = tp.part_ml[at(t)];
+            const float2 ml = __ldcg(tp.part_ml + at(t));
             M = fmaxf(M, ml.y != 0.f ? ml.x : -INFINITY);
         }
-#pragma unroll 8
+        constexpr int U = T > 1 ? 8 : 2;
+#pragma unroll U
         for (int t = grp; t < n; t += T) {
-            const int64_t i = at(t);
-            const float2 ml = tp.part_ml[i];
-            const float4 o = reinterpret_cast<const float4 *>(tp.part_o)[((i >> 8) * COLS + d4) * 256 + (i & 255)];
+            const int i = at(t);
+            const float2 ml = __ldcg(tp.part_ml + i);
+            const float4 *src = reinterpret_cast<const float4 *>(tp.part_o) + (static_cast<size_t>(i >> 8) * (D / 4) + dg * V) * 256 + (i & 255);
+            float4 o[V];
+#pragma unroll
+            for (int k = 0; k < V; ++k) o[k] = __ldcg(src + k * 256);
             const bool some = ml.y != 0.f;   // else the piece reads nothing for this row
             const float e = some ? fast_exp2(ml.x - M) : 0.f;
             L = fmaf(e, ml.y, L);
-            acc.x = some ? fmaf(e, o.x, acc.x) : acc.x;
-            acc.y = some ? fmaf(e, o.y, acc.y) : acc.y;
-            acc.z = some ? fmaf(e, o.z, acc.z) : acc.z;
-            acc.w = some ? fmaf(e, o.w, acc.w) : acc.w;
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                acc[k].x = some ? fmaf(e, o[k].x, acc[k].x) : acc[k].x;
+                acc[k].y = some ? fmaf(e, o[k].y, acc[k].y) : acc[k].y;
+                acc[k].z = some ? fmaf(e, o[k].z, acc[k].z) : acc[k].z;
+                acc[k].w = some ? fmaf(e, o[k].w, acc[k].w) : acc[k].w;
+            }
         }
     }
     if constexpr (T > 1) {
-        __shared__ float part_m[256];
-        part[threadIdx.x] = acc;
+        __shared__ float4 part[256];
+        __shared__ float part_l[256], part_m[256];
+        part[threadIdx.x] = acc[0];
         part_l[threadIdx.x] = L;
         part_m[threadIdx.x] = M;
         __syncthreads();
@@ -943,7 +957,7 @@ __global__ void __launch_bounds__(256) mod_tc_merge_kernel(const ModTcParams tp,
         float top = M;
 #pragma unroll
         for (int k = 1; k < T; ++k) top = fmaxf(top, part_m[threadIdx.x + k * RG * COLS]);
-        acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        acc[0] = make_float4(0.f, 0.f, 0.f, 0.f);
         L = 0.f;
 #pragma unroll
         for (int k = 0; k < T; ++k) {
@@ -952,18 +966,21 @@ __global__ void __launch_bounds__(256) mod_tc_merge_kernel(const ModTcParams tp,
             const float e = lk != 0.f ? fast_exp2(part_m[i] - top) : 0.f;   // a group without pieces: nothing
             const float4 o = part[i];
             L = fmaf(e, lk, L);
-            acc.x = e != 0.f ? fmaf(e, o.x, acc.x) : acc.x;
-            acc.y = e != 0.f ? fmaf(e, o.y, acc.y) : acc.y;
-            acc.z = e != 0.f ? fmaf(e, o.z, acc.z) : acc.z;
-            acc.w = e != 0.f ? fmaf(e, o.w, acc.w) : acc.w;
+            acc[0].x = e != 0.f ? fmaf(e, o.x, acc[0].x) : acc[0].x;
+            acc[0].y = e != 0.f ? fmaf(e, o.y, acc[0].y) : acc[0].y;
+            acc[0].z = e != 0.f ? fmaf(e, o.z, acc[0].z) : acc[0].z;
+            acc[0].w = e != 0.f ? fmaf(e, o.w, acc[0].w) : acc[0].w;
         }
         M = top;
     }
     const size_t orow = static_cast<size_t>(c) * p.H_Q + head * g + r % g;
     const float inv = L == 0.f ? 0.f : 1.f / L;
-    *reinterpret_cast<uint2 *>(mp.out + orow * D + 4 * d4) =
-        L == 0.f ? make_uint2(0u, 0u) : make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-    if (d4 == 0 && p.lse) p.lse[orow] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+    uint2 *dst = reinterpret_cast<uint2 *>(mp.out + orow * D + 4 * V * dg);
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+        dst[k] = L == 0.f ? make_uint2(0u, 0u)
+                          : make_uint2(pack_bf16(acc[k].x * inv, acc[k].y * inv), pack_bf16(acc[k].z * inv, acc[k].w * inv));
+    if (dg == 0 && p.lse) p.lse[orow] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
 // The tensor-memory kernel for a head width (bf16 pools); fixed: capped scores against a fixed reference.
