@@ -1,7 +1,9 @@
 """Python binding of libkvc: a paged KV cache and its decode step on GB300.
 
 Argument marshalling only: every step runs in the CUDA library's kernels
-(``csrc/``), reached through its C ABI (``include/kvc.h``) with ctypes.
+(``csrc/``), reached through its C ABI (``include/kvc.h``) with ctypes; the
+rotary write and attention with modified scores go through a small native
+module instead (``csrc/kvc_call.cpp``), whose checks cost a microsecond.
 PyTorch supplies device memory and streams.  The names match the C entry
 points; tensors are passed where the C call takes device pointers, and the
 stream defaults to torch's current stream.
@@ -13,12 +15,15 @@ it with ``python -c "import __graft_entry__ as g; g.build()"`` (or
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 import torch
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "_build", "libkvc.so")
+CALL_PATH = os.path.join(HERE, "_build", "_kvc_call.so")
 
 KVC_BF16, KVC_FP8_E4M3, KVC_INT4 = 0, 1, 2
 (KVC_OK, KVC_ERR_ARG, KVC_ERR_OOM, KVC_ERR_BAD_BLOCK, KVC_ERR_RANGE, KVC_ERR_ALIAS, KVC_ERR_STALE,
@@ -168,11 +173,13 @@ class Pool:
         self.num_kv_heads, self.head_dim, self.dtype, self.elem_bytes = d.num_kv_heads, d.head_dim, d.dtype, d.elem_bytes
         self.elem_bits = d.elem_bits
         self.device = d.device
+        self.args = (handle, d.device, d.head_dim, d.num_kv_heads)   # what the native calls take
 
     def close(self):
         if self.handle:
             load().kvc_pool_destroy(ctypes.c_void_p(self.handle))
             self.handle = 0
+            self.args = None
 
     def __del__(self):
         try:
@@ -339,6 +346,22 @@ def kvc_mixed_step(pool, layer, q, block_tables, seq_lens_pre, k_new, v_new, out
 
 
 # ---------------------------------------------------------------------- rotary write
+_call = None
+
+
+def _native():
+    """The native marshalling module of the calls below (once).  Raises if it has not been built."""
+    global _call
+    if _call is None:
+        load()
+        if not os.path.exists(CALL_PATH):
+            raise RuntimeError(f"the kvc binding is not built ({CALL_PATH} missing); run __graft_entry__.build()")
+        loader = importlib.machinery.ExtensionFileLoader("_kvc_call", CALL_PATH)
+        _call = importlib.util.module_from_spec(importlib.util.spec_from_loader("_kvc_call", loader))
+        loader.exec_module(_call)
+    return _call
+
+
 class Rope:
     """Position rotation (and optional per-head RMS norm) for kvc_rope_append / kvc_rope_write_tokens.
 
@@ -348,82 +371,30 @@ class Rope:
     def __init__(self, inv_freq=None, interleaved=False, q_norm=None, k_norm=None, eps=1e-6):
         self.inv_freq, self.q_norm, self.k_norm = inv_freq, q_norm, k_norm
         dim = 0 if inv_freq is None else 2 * inv_freq.numel()
-        self.desc = kvc_rope(dim, int(bool(interleaved)), _dev(inv_freq, torch.float32, "inv_freq", optional=True),
-                             _dev(q_norm, torch.bfloat16, "q_norm", optional=True),
-                             _dev(k_norm, torch.bfloat16, "k_norm", optional=True), float(eps), 0)
-
-    def _check(self, pool):
-        _same_device(pool, inv_freq=self.inv_freq, q_norm=self.q_norm, k_norm=self.k_norm)
-        for name in ("q_norm", "k_norm"):
-            w = getattr(self, name)
-            if w is not None and w.numel() != pool.head_dim:
-                raise ValueError(f"{name} must have head_dim = {pool.head_dim} elements, got {w.numel()}")
-
-
-def _same_device(pool, **tensors):
-    for name, t in tensors.items():
-        if t is not None and isinstance(t, torch.Tensor) and t.is_cuda and t.device.index != pool.device:
-            raise ValueError(f"{name} is on cuda:{t.device.index}, the pool on cuda:{pool.device}")
-
-
-def _want_shape(t, shape, name):
-    if t is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-
-
-def _rows(t, name):
-    """(device pointer, elements between rows) of bf16 [rows][heads][d_h]; rows may be strided, a row not."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.bfloat16 or t.dim() != 3:
-        raise ValueError(f"{name} must be a CUDA bfloat16 tensor [rows][heads][head_dim]")
-    n, h, d = t.shape
-    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
-        raise ValueError(f"{name}: the heads of a row must be contiguous")
-    return t.data_ptr(), (t.stride(0) if n > 1 else h * d)
-
-
-def _rope_args(pool, rows, block_tables, seqs, q, k, v, q_out, rope):
-    B = block_tables.shape[0]
-    _want_shape(seqs, (B,), "seq_lens / start_pos")
-    _want_shape(k, (rows, pool.num_kv_heads, pool.head_dim), "k")
-    _want_shape(v, (rows, pool.num_kv_heads, pool.head_dim), "v")
-    if (q is None) != (q_out is None):
-        raise ValueError("q and q_out go together")
-    rope._check(pool)
-    _same_device(pool, block_tables=block_tables, seqs=seqs, q=q, k=k, v=v, q_out=q_out)
-    H_Q, qp, qs = 0, None, 0
-    if q is not None:
-        H_Q = q.shape[1]
-        _want_shape(q, (rows, H_Q, pool.head_dim), "q")
-        _want_shape(q_out, (rows, H_Q, pool.head_dim), "q_out")
-        qp, qs = _rows(q, "q")
-    (kp, ks), (vp, vs) = _rows(k, "k"), _rows(v, "v")
-    return (qp, qs, H_Q, kp, ks, vp, vs, ctypes.byref(rope.desc), _dev(q_out, torch.bfloat16, "q_out", optional=True))
+        self.args = (dim, int(bool(interleaved)), inv_freq, q_norm, k_norm, float(eps))
 
 
 def kvc_rope_append(pool, layer, block_tables, seq_lens, q, k_new, v_new, q_out, rope, stream=None):
     """Rotate (and normalise) one token per sequence at position seq_lens[b]: k_new, v_new into the pool, q to q_out.
 
     q, k_new, v_new: bf16 [B][heads][head_dim], rows may be strided (views of a fused projection's output); q and
-    q_out may both be None; q_out may be q."""
-    B, mb = block_tables.shape
-    a = _rope_args(pool, B, block_tables, seq_lens, q, k_new, v_new, q_out, rope)
-    _check(load().kvc_rope_append(_h(pool), layer, _dev(block_tables, torch.int32, "block_tables"), mb,
-                                  _dev(seq_lens, torch.int32, "seq_lens"), B, *a, _stream(stream)), "kvc_rope_append")
+    q_out may both be None; q_out may be q.  The stream defaults to torch's current stream of the pool's device."""
+    s = (_call or _native()).rope_write(pool.args, layer, block_tables, seq_lens, None, q, k_new, v_new, q_out, rope.args,
+                                        None if stream is None else _stream(stream))
+    if s:
+        raise KvcError(s, "kvc_rope_append")
 
 
 def kvc_rope_write_tokens(pool, layer, block_tables, start_pos, cu_tokens, q, k, v, q_out, rope, stream=None):
     """kvc_rope_append for a ragged batch: rows cu_tokens[b] .. cu_tokens[b+1]-1 at positions start_pos[b], ...
 
     Rows at or past cu_tokens[-1] are left as they are.  Nothing is copied to the host."""
-    B, mb = block_tables.shape
-    n = k.shape[0]
-    _want_shape(cu_tokens, (B + 1,), "cu_tokens")
-    _same_device(pool, cu_tokens=cu_tokens)
-    a = _rope_args(pool, n, block_tables, start_pos, q, k, v, q_out, rope)
-    _check(load().kvc_rope_write_tokens(_h(pool), layer, _dev(block_tables, torch.int32, "block_tables"), mb,
-                                        _dev(start_pos, torch.int32, "start_pos"),
-                                        _dev(cu_tokens, torch.int32, "cu_tokens"), B, n, *a, _stream(stream)),
-           "kvc_rope_write_tokens")
+    if cu_tokens is None:
+        raise ValueError("cu_tokens is required")
+    s = (_call or _native()).rope_write(pool.args, layer, block_tables, start_pos, cu_tokens, q, k, v, q_out, rope.args,
+                                        None if stream is None else _stream(stream))
+    if s:
+        raise KvcError(s, "kvc_rope_write_tokens")
 
 
 # ---------------------------------------------------------------------- attention with modified scores
@@ -434,9 +405,7 @@ class ScoreMod:
 
     def __init__(self, softcap=0.0, window=0, sink=0, prefix=0, alibi=None, doc_start=None):
         self.alibi, self.doc_start = alibi, doc_start
-        self.desc = kvc_score_mod(float(softcap), int(window), int(sink), int(prefix),
-                                  _dev(alibi, torch.float32, "alibi", optional=True),
-                                  _dev(doc_start, torch.int32, "doc_start", optional=True))
+        self.args = (float(softcap), int(window), int(sink), int(prefix), alibi, doc_start)
 
 
 def kvc_mod_workspace(pool, rows, num_q_heads, max_blocks) -> torch.Tensor:
@@ -449,46 +418,25 @@ def kvc_mod_workspace(pool, rows, num_q_heads, max_blocks) -> torch.Tensor:
     return torch.zeros(n.value, dtype=torch.uint8, device=f"cuda:{pool.device}")
 
 
-def _mod_args(pool, q, out, lse, mod, scale, workspace):
-    n, H_Q, D = q.shape
-    if D != pool.head_dim:
-        raise ValueError(f"q must have head_dim = {pool.head_dim}, got {D}")
-    _want_shape(out, q.shape, "out")
-    _want_shape(lse, (n, H_Q), "lse")
-    if mod is not None:
-        _want_shape(mod.alibi, (H_Q,), "alibi")
-        _want_shape(mod.doc_start, (n,), "doc_start")
-        _same_device(pool, alibi=mod.alibi, doc_start=mod.doc_start)
-    _same_device(pool, q=q, out=out, lse=lse, workspace=workspace)
-    return (None if mod is None else ctypes.byref(mod.desc), _dev(out, torch.bfloat16, "out"),
-            _dev(lse, torch.float32, "lse", optional=True), float(D ** -0.5 if scale is None else scale),
-            _dev(workspace, torch.uint8, "workspace", optional=True), 0 if workspace is None else workspace.numel())
-
-
 def kvc_decode_attn_mod(pool, layer, q, block_tables, seq_lens, out, lse=None, mod=None, scale=None, workspace=None,
                         stream=None):
     """kvc_decode_attn with modified scores; out is bf16.  workspace: kvc_mod_workspace, or None (no splits: slow
-    for few long sequences)."""
-    B, mb = block_tables.shape
-    if q.shape[0] != B:
-        raise ValueError(f"q has {q.shape[0]} rows for {B} sequences")
-    _want_shape(seq_lens, (B,), "seq_lens")
-    _same_device(pool, block_tables=block_tables, seq_lens=seq_lens)
-    a = _mod_args(pool, q, out, lse, mod, scale, workspace)
-    _check(load().kvc_decode_attn_mod(_h(pool), layer, _dev(q, torch.bfloat16, "q"), q.shape[1],
-                                      _dev(block_tables, torch.int32, "block_tables"), mb,
-                                      _dev(seq_lens, torch.int32, "seq_lens"), B, *a, _stream(stream)),
-           "kvc_decode_attn_mod")
+    for few long sequences).  The stream defaults to torch's current stream of the pool's device."""
+    s = (_call or _native()).decode_attn_mod(pool.args, layer, q, block_tables, seq_lens, out, lse,
+                                             None if mod is None else mod.args, scale, workspace,
+                                             None if stream is None else _stream(stream))
+    if s:
+        raise KvcError(s, "kvc_decode_attn_mod")
 
 
 def kvc_prefill_attn_mod(pool, layer, q, block_table_row, q_start, out, lse=None, mod=None, scale=None,
                          workspace=None, stream=None):
-    """kvc_prefill_attn with modified scores; out is bf16, workspace as for kvc_decode_attn_mod."""
-    _same_device(pool, block_table_row=block_table_row)
-    a = _mod_args(pool, q, out, lse, mod, scale, workspace)
-    _check(load().kvc_prefill_attn_mod(_h(pool), layer, _dev(q, torch.bfloat16, "q"), q.shape[0], q.shape[1],
-                                       _dev(block_table_row, torch.int32, "block_table_row"), block_table_row.shape[-1],
-                                       int(q_start), *a, _stream(stream)), "kvc_prefill_attn_mod")
+    """kvc_prefill_attn with modified scores; out is bf16, workspace and stream as for kvc_decode_attn_mod."""
+    s = (_call or _native()).prefill_attn_mod(pool.args, layer, q, block_table_row, q_start, out, lse,
+                                              None if mod is None else mod.args, scale, workspace,
+                                              None if stream is None else _stream(stream))
+    if s:
+        raise KvcError(s, "kvc_prefill_attn_mod")
 
 
 def kvc_pool_reserve(pool, max_batch, num_q_heads, max_blocks):

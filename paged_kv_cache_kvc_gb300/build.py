@@ -1,4 +1,5 @@
-"""Build libkvc.so in-tree for sm_103a (nvcc, translation units compiled in parallel)."""
+"""Build libkvc.so in-tree for sm_103a (nvcc, translation units compiled in parallel), and the Python binding's
+native marshalling module (g++ against torch's headers)."""
 from __future__ import annotations
 
 import os
@@ -9,6 +10,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(OUT_DIR, "libkvc.so")
+CALL_PATH = os.path.join(OUT_DIR, "_kvc_call.so")
 ROOT = os.path.dirname(HERE)
 
 SOURCES = ["kvc_core.cu", "kvc_attn.cu", "kvc_decode_bf16.cu", "kvc_decode_fp8.cu", "kvc_decode_int4.cu",
@@ -31,6 +33,23 @@ def _stale(target: str, deps: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def call_commands() -> tuple[list[str], list[str]]:
+    """Compile and link commands of the marshalling module."""
+    import sysconfig
+    import torch
+    home = os.path.dirname(torch.__file__)
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    obj = os.path.join(OUT_DIR, "kvc_call.o")
+    compile_ = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+                f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I" + os.path.join(home, "include"),
+                "-I" + os.path.join(home, "include", "torch", "csrc", "api", "include"),
+                "-I" + os.path.join(cuda, "include"), "-I" + sysconfig.get_paths()["include"],
+                "-c", os.path.join(CSRC, "kvc_call.cpp"), "-o", obj]
+    link = ["g++", "-shared", "-o", CALL_PATH, obj, "-L" + OUT_DIR, "-l:libkvc.so", "-Wl,-rpath,$ORIGIN",
+            "-L" + os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    return compile_, link
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
     os.makedirs(OUT_DIR, exist_ok=True)
     headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))]
@@ -46,6 +65,11 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
             if verbose:
                 print(" ".join(cmd), file=sys.stderr)
             procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+    call_src = os.path.join(CSRC, "kvc_call.cpp")
+    call_stale = force or _stale(CALL_PATH, [call_src, os.path.join(ROOT, "include", "kvc.h")])
+    if call_stale:
+        call_compile, call_link = call_commands()
+        procs.append(("kvc_call.cpp", subprocess.Popen(call_compile, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     failed = []
     for src, p in procs:
         out, _ = p.communicate()
@@ -59,6 +83,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
         tmp = LIB_PATH + f".tmp{os.getpid()}"
         subprocess.check_call([nvcc()] + ARCH + ["-shared", "-Xlinker", "-z,defs", "-o", tmp] + objs)
         os.replace(tmp, LIB_PATH)
+    if call_stale:
+        subprocess.check_call(call_link)
     return LIB_PATH
 
 

@@ -154,7 +154,7 @@ static kvc_status run_split(kvc_pool *pool, ModParams &mp, const DecodeKernel &k
 
 // The tensor-memory kernel's part of the workspace behind the counters: the units' running tile counts,
 // then two pieces of a unit's 256 rows per CTA.
-constexpr size_t kPrefixBytes = ((kMtUnits + 1) * sizeof(int32_t) + 255) & ~size_t(255);
+constexpr size_t kPrefixBytes = ((kMtUnits + 1) * sizeof(int32_t) + 255) & ~size_t(255);   // or one int4 per CTA
 static size_t tc_bytes(int64_t ctas, int D)
 {
     return kPrefixBytes + static_cast<size_t>(ctas) * 2 * 256 * (D * sizeof(float) + sizeof(float2));
@@ -205,11 +205,12 @@ static kvc_status run_tc(kvc_pool *pool, const ModParams &mp0, void *ws, size_t 
         tp.units = (p.n_pos + unit - 1) / unit;
         // no more CTAs than the line of tiles can have tiles
         const int64_t most = static_cast<int64_t>(p.H_KV) * tp.units * ((p.max_blocks + kMtBlocks - 1) / kMtBlocks + kMtStart);
-        const int ctas = static_cast<int>(std::min<int64_t>(pool->num_sms, most));
+        const int ctas = static_cast<int>(std::min<int64_t>(std::min(pool->num_sms, 512), most));
         if (!tp.whole) {
             if (ws_bytes < kCounterBytes + tc_bytes(ctas, pool->D)) return KVC_ERR_ARG;
             uint8_t *base = static_cast<uint8_t *>(ws) + kCounterBytes;
             tp.prefix = reinterpret_cast<int32_t *>(base);
+            tp.cuts = reinterpret_cast<int4 *>(base);
             tp.part_o = reinterpret_cast<float *>(base + kPrefixBytes);
             tp.part_ml = reinterpret_cast<float2 *>(tp.part_o + static_cast<size_t>(ctas) * 2 * 256 * pool->D);
         }
@@ -218,10 +219,10 @@ static kvc_status run_tc(kvc_pool *pool, const ModParams &mp0, void *ws, size_t 
         if (e != cudaSuccess) return cuda_status(e);
         g_launches.fetch_add(1, std::memory_order_relaxed);
         if (!tp.whole && (tp.split || most > 1)) {
-            const int rows = tp.split ? std::min(p.ppu, p.n_pos) * p.g : 256, per = tp.split ? 128 / pool->D : 32;
+            const int rows = std::min(p.ppu, p.n_pos) * p.g, per = 128 / pool->D;
+            const dim3 grid = tp.split ? dim3((rows + per - 1) / per, tp.units, p.H_KV) : dim3(8, ctas);
             void *margs[] = {&tp, const_cast<int *>(&ctas)};
-            e = launch_dependent(select_mod_tc_merge(pool->D, tp.split != 0), dim3((rows + per - 1) / per, tp.units, p.H_KV), dim3(256), 0,
-                                 stream, margs);
+            e = launch_dependent(select_mod_tc_merge(pool->D, tp.split != 0), grid, dim3(256), 0, stream, margs);
             if (e != cudaSuccess) return cuda_status(e);
             g_launches.fetch_add(1, std::memory_order_relaxed);
         }

@@ -54,8 +54,10 @@ struct ModTcParams {
     int32_t whole;        // 1: no partials, units are dealt whole
     int32_t split;        // 1: a unit is one query tile's positions, and both chains take its rows (below)
     int32_t total;        // positions the row holds (prefill)
-    int32_t *prefix;      // [units + 1] place of each unit on a head's line, for the merge
-    float *part_o;        // [2 G][D / 4][256] float4
+    int32_t *prefix;      // few-row calls: [units + 1] place of each unit on a head's line, for the merge
+    int4 *cuts;           // other calls: [G] {head, unit, pieces (0: none), slot} of the unit that CTA c starts
+                          // and a later CTA ends, for the merge
+    float *part_o;        // float4 [2 G][D / 4][256] (a warp's rows side by side), few-row calls [2 G][256][D / 4]
     float2 *part_ml;      // [2 G][256]
 };
 
@@ -265,6 +267,14 @@ struct Walk {
     }
 };
 
+// The CTA that has place w of a line of W shared by G: the last c with c W / G <= w.
+__device__ __forceinline__ int cta_of(int64_t w, int64_t W, int64_t G)
+{
+    const int64_t num = (w + 1) * G - 1;
+    if (W * G < 0x7FFFFFFF) return static_cast<int>(static_cast<uint32_t>(num) / static_cast<uint32_t>(W));
+    return static_cast<int>(num / W);
+}
+
 // FIXED: capped scores against the fixed reference; else the running reference maximum.
 template <int D, bool FIXED>
 __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_constant__ CUtensorMap tmap16,
@@ -356,11 +366,11 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
         for (int u = b; u < e; ++u) {
             before += prefix[u + 1];
             prefix[u + 1] = before;
-            if (blockIdx.x == 0 && !tp.whole) tp.prefix[u + 1] = before;
+            if (blockIdx.x == 0 && tp.split) tp.prefix[u + 1] = before;
         }
         if (tid == 0) {
             prefix[0] = 0;
-            if (blockIdx.x == 0 && !tp.whole) tp.prefix[0] = 0;
+            if (blockIdx.x == 0 && tp.split) tp.prefix[0] = 0;
         }
         __syncthreads();
     }
@@ -593,6 +603,7 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
         const float ref = 0.5f * mp.cap_out;
         uint32_t it = 0, kt = 0;   // this query tile's steps, key tiles so far
         int piece = 0;             // segments so far
+        int4 cut = make_int4(0, 0, 0, 0);
         for (Segment s = walk.next(); s.ok; s = walk.next(), ++piece) {
             const uint32_t kt0 = kt;
             kt += s.k1 - s.k0;
@@ -811,6 +822,10 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
             const bool done = s.k0 == 0 && s.k1 == s.tiles && !tp.split;
             if (!any_real) continue;
             const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (piece > 0 ? 1 : 0);
+            if (tid == 0 && !done && s.k0 == 0) {
+                const int64_t end = static_cast<int64_t>(s.head) * walk.per_head + prefix[s.unit + 1];
+                cut = make_int4(s.head, s.unit, cta_of(end - 1, W, G) - static_cast<int>(blockIdx.x) + 1, static_cast<int>(slot));
+            }
             const int prow = x * 128 + row;
             const float inv = l == 0.f ? 0.f : 1.f / l;
             // finished rows go through the warp's quarter of the tile's query memory (its products are done;
@@ -834,11 +849,12 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
                         sts128(stage + lane * (D * 2) + (((part * 4 + c) ^ (lane & 7)) << 4), make_uint4(w[0], w[1], w[2], w[3]));
                     }
                 } else {
-                    // [channel / 4][row]: a warp's rows are contiguous
-                    float4 *dst = reinterpret_cast<float4 *>(tp.part_o) + (slot * (D / 4) + part * 8) * 256 + prow;
+                    float4 *dst = reinterpret_cast<float4 *>(tp.part_o) +
+                                  (tp.split ? (slot * 256 + prow) * (D / 4) + part * 8 : (slot * (D / 4) + part * 8) * 256 + prow);
+                    const int step = tp.split ? 1 : 256;
 #pragma unroll
                     for (int c = 0; c < 8; ++c)
-                        dst[c * 256] = make_float4(__uint_as_float(o[4 * c]), __uint_as_float(o[4 * c + 1]),
+                        dst[c * step] = make_float4(__uint_as_float(o[4 * c]), __uint_as_float(o[4 * c + 1]),
                                                    __uint_as_float(o[4 * c + 2]), __uint_as_float(o[4 * c + 3]));
                 }
             }
@@ -866,6 +882,7 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
             if (real && done && p.lse) p.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
             if (real && !done) tp.part_ml[slot * 256 + prow] = make_float2(m, l);
         }
+        if (tid == 0 && !tp.whole && !tp.split) tp.cuts[blockIdx.x] = cut;
     }
     if (timed_out && lane == 0) atomicOr(p.err, KVC_EBIT_TIMEOUT);
     tc_fence_before();
@@ -878,10 +895,11 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
 
 // Adds the pieces of units that CTA borders cut, in CTA order (in few-row calls: chain 0's and chain 1's of
 // every CTA):  M = max m_s, L = sum 2^(m_s - M) l_s, out = sum 2^(m_s - M) o_s / L, lse = (M + log2 L) ln 2.
-// Whole chunks: grid (8, units, KV heads), 256 threads = 32 rows x 8 groups of D / 8 channels (a thread has its
-// loads of a piece in flight at once, and the grid is about one wave).  Few-row calls (T = 8), whose rows have
-// tens of pieces: 256 threads = 128 / D rows x D / 4 float4 columns x 8 groups of pieces.
-// A programmatic dependent of mod_tc_kernel (its CTAs are in place when that ends).  ctas: that kernel's grid.
+// Whole chunks (T = 1): grid (8, the attention kernel's CTAs), 256 threads = 32 rows x 8 groups of D / 8
+// channels; a thread has its loads of a piece in flight at once.  Few-row calls (T = 8), whose rows have tens
+// of pieces: grid (row groups, units, KV heads), 256 threads = 128 / D rows x D / 4 float4 columns x 8 groups of
+// pieces.  A programmatic dependent of mod_tc_kernel (its CTAs are in place when that ends).  ctas: that
+// kernel's grid.
 template <int D, int T>
 __global__ void __launch_bounds__(256) mod_tc_merge_kernel(const ModTcParams tp, const int ctas)
 {
@@ -889,31 +907,37 @@ __global__ void __launch_bounds__(256) mod_tc_merge_kernel(const ModTcParams tp,
     constexpr int COLS = D / 4 / V, RG = 256 / COLS / T;   // column groups, rows per CTA
     const ModParams &mp = tp.m;
     const DecodeParams &p = mp.d;
-    const int unit = blockIdx.y, head = blockIdx.z, g = p.g;
+    const int g = p.g;
     const int rr = blockIdx.x * RG + threadIdx.x % RG, dg = threadIdx.x / RG % COLS, grp = threadIdx.x / (RG * COLS);
     const int tile = rr >> 7, r = rr & 127;
-    const int c = unit * (tp.split ? p.ppu : 2 * p.ppu) + tile * p.ppu + r / g;
-    const bool real = r < p.ppu * g && c < p.n_pos;
+    const int hr = r % g, pr = tile * p.ppu + r / g;   // head of the group, position of the unit
     allow_dependent_launch();
     grid_dependency_wait();
-    const int per_head = __ldcg(tp.prefix + tp.units), u0 = __ldcg(tp.prefix + unit), u1 = __ldcg(tp.prefix + unit + 1);
-    const int64_t W = static_cast<int64_t>(p.H_KV) * per_head, G = min(static_cast<int64_t>(ctas), W);
-    const int64_t a = static_cast<int64_t>(head) * per_head + u0, b = static_cast<int64_t>(head) * per_head + u1;
-    // the CTA that has place w of the line: the last c with c W / G <= w
-    auto cta_of = [&](int64_t w) -> int {
-        const int64_t num = (w + 1) * G - 1;
-        if (W * G < 0x7FFFFFFF) return static_cast<int>(static_cast<uint32_t>(num) / static_cast<uint32_t>(W));
-        return static_cast<int>(num / W);
-    };
-    const int cf = cta_of(a + kMtStart), cl = cta_of(b - 1);   // CTAs of the unit's first and last tile
-    if (cf == cl && !tp.split) return;
-    const int n = (cl - cf + 1) * (tp.split ? 2 : 1);
-    const bool first_second = cta_of(a - 1) == cf && a > 0;   // the first CTA has places before the unit: its second piece
+    int unit, head, n, slot0;   // the unit's pieces: slot0 in its first CTA, then every later CTA's first slot
+    if constexpr (T == 1) {
+        const int4 cut = __ldcg(tp.cuts + blockIdx.y);
+        head = cut.x;
+        unit = cut.y;
+        n = cut.z;
+        slot0 = cut.w;
+        if (n == 0) return;
+    } else {
+        unit = blockIdx.y;
+        head = blockIdx.z;
+        const int per_head = __ldcg(tp.prefix + tp.units), u0 = __ldcg(tp.prefix + unit), u1 = __ldcg(tp.prefix + unit + 1);
+        const int64_t W = static_cast<int64_t>(p.H_KV) * per_head, G = min(static_cast<int64_t>(ctas), W);
+        const int64_t a = static_cast<int64_t>(head) * per_head + u0, b = static_cast<int64_t>(head) * per_head + u1;
+        const int cf = cta_of(a + kMtStart, W, G), cl = cta_of(b - 1, W, G);   // CTAs of the unit's first and last tile
+        n = (cl - cf + 1) * 2;
+        slot0 = 2 * cf + (a > 0 && cta_of(a - 1, W, G) == cf ? 1 : 0);   // places before the unit: its second piece
+    }
+    const int c = unit * (tp.split ? p.ppu : 2 * p.ppu) + pr;
+    const bool real = r < p.ppu * g && c < p.n_pos;
     if (T == 1 && !real) return;
-    // piece t: slot * 256 + row in it
+    // piece t: slot * 256 + row in it (few rows: chain t mod 2 of CTA t / 2)
     auto at = [&](int t) -> int {
-        const int cta = tp.split ? t >> 1 : t, chain = tp.split ? t & 1 : tile;
-        return (2 * (cf + cta) + (cta == 0 && first_second ? 1 : 0)) * 256 + chain * 128 + r;
+        const int cta = T > 1 ? t >> 1 : t, chain = T > 1 ? t & 1 : tile;
+        return (cta == 0 ? slot0 : (slot0 & ~1) + 2 * cta) * 256 + chain * 128 + r;
     };
     float M = -INFINITY, L = 0.f;
     float4 acc[V];
@@ -930,7 +954,9 @@ __global__ void __launch_bounds__(256) mod_tc_merge_kernel(const ModTcParams tp,
         for (int t = grp; t < n; t += T) {
             const int i = at(t);
             const float2 ml = __ldcg(tp.part_ml + i);
-            const float4 *src = reinterpret_cast<const float4 *>(tp.part_o) + (static_cast<size_t>(i >> 8) * (D / 4) + dg * V) * 256 + (i & 255);
+            const float4 *src = reinterpret_cast<const float4 *>(tp.part_o) +
+                                (T > 1 ? static_cast<size_t>(i) * (D / 4) + dg
+                                       : (static_cast<size_t>(i >> 8) * (D / 4) + dg * V) * 256 + (i & 255));
             float4 o[V];
 #pragma unroll
             for (int k = 0; k < V; ++k) o[k] = __ldcg(src + k * 256);
@@ -973,7 +999,7 @@ __global__ void __launch_bounds__(256) mod_tc_merge_kernel(const ModTcParams tp,
         }
         M = top;
     }
-    const size_t orow = static_cast<size_t>(c) * p.H_Q + head * g + r % g;
+    const size_t orow = static_cast<size_t>(c) * p.H_Q + head * g + hr;
     const float inv = L == 0.f ? 0.f : 1.f / L;
     uint2 *dst = reinterpret_cast<uint2 *>(mp.out + orow * D + 4 * V * dg);
 #pragma unroll

@@ -95,7 +95,7 @@ class Rows:
         assert np.array_equal(np.isneginf(l), np.isneginf(rl)), (row, l, rl)
         assert np.all(np.abs(o - ro) <= to), (row, float(np.max(np.abs(o - ro) - to)), float(np.max(np.abs(o - ro))))
         f = np.isfinite(rl)
-        assert np.all(np.abs(l - rl)[f] <= tl[f]), (row, np.max(np.abs(l - rl)[f]), tl[f])
+        assert np.all(np.abs(l[f] - rl[f]) <= tl[f]), (row, l[f], rl[f], tl[f])
 
     def check_decode(self, out, lse, m):
         torch.cuda.synchronize()
