@@ -365,7 +365,7 @@ KVC_API kvc_status kvc_rope_append(kvc_pool *pool, int32_t layer, const int32_t 
 /* The same for a ragged batch, as kvc_write_tokens: rows cu_tokens[b] ..
  * cu_tokens[b+1]-1 are sequence b's tokens at positions start_pos[b],
  * start_pos[b]+1, ...  n_rows is the number of rows that q, k, v and q_out
- * hold (host); rows at or past cu_tokens[B] are neither read nor written.
+ * hold (host); rows at or past cu_tokens[B] are left as they are.
  * Sequences without tokens are allowed. */
 KVC_API kvc_status kvc_rope_write_tokens(kvc_pool *pool, int32_t layer, const int32_t *block_tables,
                                          int32_t max_blocks, const int32_t *start_pos, const int32_t *cu_tokens,

@@ -17,6 +17,9 @@
 // in fp32), the products keep their fma remainders, and whole turns drop out
 // exactly at each step.  The angle is good to 1e-6 radians up to t = 2^24
 // (bf16 outputs round at 4e-3) without fp64, whose units are few on this part.
+#include <algorithm>
+#include <type_traits>
+
 #include "kvc_decode.cuh"
 
 namespace kvc {
@@ -71,17 +74,17 @@ __device__ __forceinline__ void unpack8(const uint4 &x, float (&f)[8])
     }
 }
 
-// Eight channels of a key or value row into the pool at element index e; vals in fp32.
-__device__ __forceinline__ void store_pool8(const RopeParams &p, int64_t e, const float (&y)[8], const float *sc)
+// Eight channels of a key or value row into the pool at d (the elements' bytes), in fp32.
+__device__ __forceinline__ void store_pool8(uint8_t *d, int bits, const float (&y)[8], const float *sc)
 {
-    if (p.bits == 16) {
-        *reinterpret_cast<uint4 *>(p.base + e * 2) =
+    if (bits == 16) {
+        *reinterpret_cast<uint4 *>(d) =
             make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
-    } else if (p.bits == 4) {
+    } else if (bits == 4) {
         uint32_t o = 0u;
 #pragma unroll
         for (int i = 0; i < 8; ++i) o |= int4_code(y[i], __ldg(sc + i)) << (4 * i);
-        *reinterpret_cast<uint32_t *>(p.base + e / 2) = o;
+        *reinterpret_cast<uint32_t *>(d) = o;
     } else {
         uint32_t o[2] = {0u, 0u};
 #pragma unroll
@@ -89,161 +92,250 @@ __device__ __forceinline__ void store_pool8(const RopeParams &p, int64_t e, cons
             const uint32_t c = __nv_cvt_float_to_fp8(__fdiv_rn(y[i], __ldg(sc + i)), __NV_SATFINITE, __NV_E4M3);
             o[i >> 2] |= c << (8 * (i & 3));
         }
-        *reinterpret_cast<uint2 *>(p.base + e) = make_uint2(o[0], o[1]);
+        *reinterpret_cast<uint2 *>(d) = make_uint2(o[0], o[1]);
     }
 }
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 256;              // the threads that move rows; one warp more looks ahead
+constexpr int kRopeCta = kRopeThreads + 32;
 
 // The sequence holding row r: the last b with cu[b] <= r, or -1 (r is past cu[B], or cu[0] > r).
-// Whole warp; 32 probes per step.
-__device__ __forceinline__ int find_sequence(const int32_t *cu, int B, int64_t r, int lane)
+__device__ __forceinline__ int find_sequence(const int32_t *cu, int B, int64_t r)
 {
-    if (r >= static_cast<int64_t>(__ldg(cu + B))) return -1;
-    int lo = 0, n = B;   // candidates lo .. lo + n - 1
-    while (true) {
-        const int step = (n + 31) / 32;
-        const int i = lo + lane * step;
-        const bool le = lane * step < n && static_cast<int64_t>(__ldg(cu + i)) <= r;
-        const int hits = __popc(__ballot_sync(kFull, le));   // cu is non-decreasing: a prefix of the probes
-        if (hits == 0) return -1;
-        lo += (hits - 1) * step;
-        n = min(step, n - (hits - 1) * step);
-        if (step == 1) return lo;
+    if (r >= static_cast<int64_t>(__ldg(cu + B)) || r < static_cast<int64_t>(__ldg(cu))) return -1;
+    int lo = 0, hi = B;   // cu[lo] <= r < cu[hi]
+    while (hi - lo > 1) {
+        const int mid = lo + (hi - lo) / 2;
+        if (static_cast<int64_t>(__ldg(cu + mid)) <= r) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// What the CTA knows of a batch of TPC tokens.
+template <int D, int TPC>
+struct alignas(16) RopeBatch {
+    // (own factor, mate's factor) of each channel of a query and a key row: the cosine and the signed sine
+    // with the norm's weights folded in,  z_i = r (x_i (w_i cos a) - x_j (w_j sin a))
+    float2 f[TPC][2][D];
+    int64_t block[TPC];   // layer * N + block, or -1: not stored
+    int32_t slot[TPC], pos[TPC];
+    bool live[TPC];
+};
+
+// One thread: sequence, position and place of row r, the batch's token w.
+template <int D, int TPC>
+__device__ __forceinline__ void resolve_token(const RopeParams &p, RopeBatch<D, TPC> &s, int w, int64_t r)
+{
+    int b = -1;
+    int64_t first = 0;
+    if (r < p.rows) {
+        if (p.cu) {
+            b = find_sequence(p.cu, p.B, r);
+            if (b >= 0) first = __ldg(p.cu + b);
+        } else {
+            b = static_cast<int>(r);
+            first = r;
+        }
+    }
+    s.live[w] = b >= 0;
+    int64_t blk = -1;
+    if (b >= 0) {
+        const int32_t st = __ldg(p.start + b);
+        const int64_t t = static_cast<int64_t>(st) + (r - first);
+        s.pos[w] = static_cast<int32_t>(min(t, static_cast<int64_t>(0x7FFFFFFF)));
+        if (st < 0 || t / p.bs >= p.max_blocks) {
+            atomicOr(p.err, KVC_EBIT_RANGE);
+        } else {
+            const int32_t phys = __ldg(p.bt + static_cast<int64_t>(b) * p.max_blocks + t / p.bs);
+            if (phys < 0 || static_cast<int64_t>(phys) >= p.N) atomicOr(p.err, KVC_EBIT_BAD_BLOCK);
+            else blk = static_cast<int64_t>(p.layer) * p.N + phys;
+            s.slot[w] = static_cast<int32_t>(t % p.bs);
+        }
+    }
+    s.block[w] = blk;
+}
+
+// Threads tid of n: the factors of the batch's tokens, a pair (i, j) at a time.
+template <int D, int TPC>
+__device__ __forceinline__ void build_factors(const RopeParams &p, RopeBatch<D, TPC> &s, int tid, int n)
+{
+    const int half = p.R >> 1;
+    const int per = D / 2;   // pairs of a row: half that turn, the rest pass through
+    for (int x = tid; x < TPC * per; x += n) {
+        const int tk = x / per, i = x - tk * per;
+        if (!s.live[tk]) continue;
+        const bool turn = i < half;
+        const int a = turn ? (p.interleaved ? 2 * i : i) : p.R + 2 * (i - half);
+        const int b = turn ? (p.interleaved ? 2 * i + 1 : i + half) : a + 1;
+        const float2 cs = turn ? rotation(s.pos[tk], __ldg(p.inv_freq + i)) : make_float2(1.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const uint16_t *w = k ? p.k_norm : p.q_norm;
+            const float wa = w ? __uint_as_float(static_cast<uint32_t>(__ldg(w + a)) << 16) : 1.f;
+            const float wb = w ? __uint_as_float(static_cast<uint32_t>(__ldg(w + b)) << 16) : 1.f;
+            s.f[tk][k][a] = make_float2(wa * cs.x, -wb * cs.y);
+            s.f[tk][k][b] = make_float2(wb * cs.x, wa * cs.y);
+        }
     }
 }
 
-// grid (tokens / TPC); 256 threads = TPC tokens x groups of D / 8 lanes, one lane per 16-byte
-// chunk of a head row, so a lane keeps its chunk (and its 8 angles) and walks the token's heads.
-template <int D, int TPC>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p)
+// Persistent CTAs; each walks batches of TPC tokens.  256 threads = TPC tokens x GPT groups of D / 8 lanes, one
+// lane per 16-byte chunk of a head row: a lane keeps its chunk and its eight channels' factors and walks the
+// token's heads, U rows at a time with the next ones' loads in flight.  A ninth warp finds the next batch's
+// sequences, positions and blocks (a chain of four dependent loads) and its factors meanwhile.
+// Bound by HBM and by issue slots alike: 16 384 tokens of 32 + 2 x 8 heads of 128, normalised, bf16 (403 MB) take
+// 72 us, 5.6 TB/s, 82 % of the copy rate; e4m3 pools 93 us (the exact divisions by the scales).  A CTA per four
+// tokens without the ninth warp took 97 us (each CTA began with the chain of loads), the same with one row in
+// flight 111 us; per-row address arithmetic and one loop over all kinds of head 95 us.
+template <int D, int GPT, int U>
+__global__ void __launch_bounds__(kRopeCta, 3) rope_kernel(const RopeParams p)
 {
     constexpr int CPR = D / 8;                            // chunks (lanes) per head row
-    constexpr int GPT = kRopeThreads / CPR / TPC;         // lane groups per token
-    __shared__ float2 cs[TPC][D / 2];
-    __shared__ int64_t dst_block[TPC];                    // (layer * N + block) of the token, or -1: not stored
-    __shared__ int32_t dst_slot[TPC], pos_sh[TPC];
-    __shared__ bool live[TPC];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int64_t row0 = static_cast<int64_t>(blockIdx.x) * TPC;
+    constexpr int TPC = kRopeThreads / CPR / GPT;         // tokens per batch
+    __shared__ RopeBatch<D, TPC> sh[2];
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int64_t batches = (p.rows + TPC - 1) / TPC;
+    const int c = tid % CPR, grp = tid / CPR;
+    const int tk = min(grp / GPT, TPC - 1), gi = grp % GPT;
+    const bool mover = tid < kRopeThreads;
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    if (warp < TPC) {   // warp w resolves token w
-        const int64_t r = row0 + warp;
-        int b = -1;
-        int64_t first = 0;
-        if (r < p.rows) {
-            if (p.cu) {
-                b = find_sequence(p.cu, p.B, r, lane);
-                if (b >= 0) first = __ldg(p.cu + b);
-            } else {
-                b = static_cast<int>(r);
-                first = r;
+    // Rows of one kind (0: q, 1: k, 2: v) of a token: this group takes heads gi, gi + GPT, ...
+    auto source = [&](int kind, int64_t r) {
+        return (kind == 0 ? p.q + r * p.q_stride : kind == 1 ? p.k + r * p.k_stride : p.v + r * p.v_stride) + gi * D + 8 * c;
+    };
+    auto load = [&](uint4 (&x)[U], const uint16_t *src, int left) {   // left: heads from this one on
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            x[u] = u * GPT < left ? *reinterpret_cast<const uint4 *>(src + u * GPT * D) : make_uint4(0u, 0u, 0u, 0u);
+    };
+    int64_t batch = blockIdx.x;
+    uint4 cur[U];
+    const int kind0 = p.H_Q > 0 ? 0 : 1;   // the first kind of a token
+    auto first_rows = [&](int64_t r) {
+        load(cur, source(kind0, r), r < p.rows ? (kind0 == 0 ? p.H_Q : p.H_KV) - gi : 0);
+    };
+    if (mover) first_rows(batch * TPC + tk);
+    static_assert(TPC <= 32, "one warp resolves a batch");
+    if (tid < TPC) resolve_token(p, sh[0], tid, batch * TPC + tid);
+    __syncthreads();
+    build_factors(p, sh[0], tid, kRopeCta);
+    const bool turns = 8 * c < p.R;
+    // partner chunk of the half-split pairing
+    const int hc = p.R >> 4;
+    const int pc = p.interleaved || !turns ? c : (c >= hc ? c - hc : c + hc);
+    const int src_lane = (lane & ~(CPR - 1)) | pc;
+    const int64_t head_bytes = static_cast<int64_t>(2) * p.bs * D * p.bits / 8;   // a block's keys and values of a head
+
+    for (int it = 0; batch < batches; batch += gridDim.x, ++it) {
+        __syncthreads();   // this batch's facts are there; the buffer of the batch before is free
+        const RopeBatch<D, TPC> &s = sh[it & 1];
+        const int64_t after = batch + gridDim.x;
+        if (!mover) {
+            if (after < batches) {
+                RopeBatch<D, TPC> &n = sh[(it + 1) & 1];
+                if (lane < TPC) resolve_token(p, n, lane, after * TPC + lane);
+                __syncwarp();
+                build_factors(p, n, lane, 32);
             }
+            continue;
         }
-        if (lane == 0) {
-            live[warp] = b >= 0;
-            int64_t blk = -1;
-            if (b >= 0) {
-                const int32_t s = __ldg(p.start + b);
-                const int64_t t = static_cast<int64_t>(s) + (r - first);
-                pos_sh[warp] = static_cast<int32_t>(min(t, static_cast<int64_t>(0x7FFFFFFF)));
-                if (s < 0 || t / p.bs >= p.max_blocks) {
-                    atomicOr(p.err, KVC_EBIT_RANGE);
-                } else {
-                    const int32_t phys = __ldg(p.bt + static_cast<int64_t>(b) * p.max_blocks + t / p.bs);
-                    if (phys < 0 || static_cast<int64_t>(phys) >= p.N) atomicOr(p.err, KVC_EBIT_BAD_BLOCK);
-                    else blk = static_cast<int64_t>(p.layer) * p.N + phys;
-                    dst_slot[warp] = static_cast<int32_t>(t % p.bs);
+        const int64_t r = batch * TPC + tk;
+        const bool on = s.live[tk];
+        const int64_t blk = on ? s.block[tk] : -1;
+        // this lane's bytes of head gi's key slot
+        uint8_t *pool = p.base + (blk >= 0 ? (blk * p.H_KV + gi) * head_bytes + (static_cast<int64_t>(s.slot[tk]) * D + 8 * c) * p.bits / 8 : 0);
+        auto rows = [&](auto kind_c) {
+            constexpr int KIND = decltype(kind_c)::value;
+            const int n = KIND == 0 ? p.H_Q : p.H_KV;
+            const bool act = KIND == 0 ? on : blk >= 0;
+            const bool norm = KIND == 0 ? p.q_norm != nullptr : (KIND == 1 && p.k_norm != nullptr);
+            const uint16_t *src = source(KIND, r);
+            uint16_t *q_dst = p.q_out + (r * p.H_Q + gi) * D + 8 * c;
+            uint8_t *dst = pool + (KIND == 2 ? static_cast<int64_t>(p.bs) * D * p.bits / 8 : 0);
+            const float *sc = p.scales ? p.scales + ((KIND == 2 ? p.H_KV : 0) + gi) * static_cast<int64_t>(D) + 8 * c : nullptr;
+            float2 f[8];
+            if constexpr (KIND < 2) {
+                const float4 *fs = reinterpret_cast<const float4 *>(&s.f[tk][KIND][8 * c]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float4 v = fs[j];
+                    f[2 * j] = make_float2(v.x, v.y);
+                    f[2 * j + 1] = make_float2(v.z, v.w);
                 }
             }
-            dst_block[warp] = blk;
-        }
-    }
-    __syncthreads();
-    const int half = p.R >> 1;
-    for (int i = tid; i < TPC * half; i += kRopeThreads) {
-        const int tk = i / half, j = i - tk * half;
-        if (live[tk]) cs[tk][j] = rotation(pos_sh[tk], __ldg(p.inv_freq + j));
-    }
-    __syncthreads();
-
-    const int c = tid % CPR, grp = tid / CPR;
-    const int tk = grp / GPT, gi = grp % GPT;
-    const int heads = p.H_Q + 2 * p.H_KV;
-    const bool on = live[tk];
-    const int64_t r = row0 + tk;
-    const int64_t blk = on ? dst_block[tk] : -1;
-    const int slot = on && blk >= 0 ? dst_slot[tk] : 0;
-    const bool turns = 8 * c < p.R;
-    // partner chunk of the half-split pairing and this lane's side of the pair
-    const int hc = half >> 3;
-    const bool second = !p.interleaved && turns && c >= hc;
-    const int pc = p.interleaved || !turns ? c : (second ? c - hc : c + hc);
-    const int src_lane = (lane & ~(CPR - 1)) | pc;
-    float co[8], si[8];   // the cosine and signed sine each channel takes
+            // every lane runs every iteration (the shuffles are warp-wide)
+            for (int h0 = 0; h0 < n; h0 += U * GPT) {
+                uint4 next[U];
+                src += U * GPT * D;
+                if (h0 + U * GPT < n) load(next, src, r < p.rows ? n - gi - h0 - U * GPT : 0);
+                else if constexpr (KIND < 2) load(next, source(KIND + 1, r), r < p.rows ? p.H_KV - gi : 0);
+                else {
+                    const int64_t r2 = r + static_cast<int64_t>(gridDim.x) * TPC;   // the next batch's first rows
+                    load(next, source(kind0, r2), r2 < p.rows ? (kind0 == 0 ? p.H_Q : p.H_KV) - gi : 0);
+                }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        co[j] = 1.f;
-        si[j] = 0.f;
-        if (on && turns) {
-            const int i = p.interleaved ? 4 * c + (j >> 1) : 8 * (second ? c - hc : c) + j;
-            const float2 v = cs[tk][i];
-            const bool minus = p.interleaved ? !(j & 1) : !second;
-            co[j] = v.x;
-            si[j] = minus ? -v.y : v.y;
-        }
-    }
-    // heads in order q, k, v; every lane runs every iteration (the shuffles are warp-wide)
-    for (int h = gi; h - gi < heads; h += GPT) {
-        const bool act = on && h < heads;
-        const int kind = h < p.H_Q ? 0 : (h < p.H_Q + p.H_KV ? 1 : 2);
-        const int hh = kind == 0 ? h : (kind == 1 ? h - p.H_Q : h - p.H_Q - p.H_KV);
-        uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-        if (act) {
-            const uint16_t *src = kind == 0 ? p.q + r * p.q_stride : (kind == 1 ? p.k + r * p.k_stride : p.v + r * p.v_stride);
-            raw = *reinterpret_cast<const uint4 *>(src + static_cast<int64_t>(hh) * D + 8 * c);
-        }
-        float y[8];
-        unpack8(raw, y);
-        const uint16_t *w = kind == 0 ? p.q_norm : (kind == 1 ? p.k_norm : nullptr);
-        float ss = 0.f;
-        if (p.q_norm || p.k_norm) {   // uniform: either norm runs the reduction for every lane
+                for (int u = 0; u < U; ++u) {
+                    const uint4 raw = cur[u];
+                    float y[8];
+                    if (KIND < 2 || p.bits != 16) unpack8(raw, y);
+                    if constexpr (KIND < 2) {
+                        uint4 mr;   // the mates: the partner chunk (half-split), or the pair's other channels
+                        if (p.interleaved) {
+                            mr = make_uint4(__byte_perm(raw.x, 0, 0x1032), __byte_perm(raw.y, 0, 0x1032),
+                                            __byte_perm(raw.z, 0, 0x1032), __byte_perm(raw.w, 0, 0x1032));
+                        } else {
+                            mr.x = __shfl_sync(kFull, raw.x, src_lane);
+                            mr.y = __shfl_sync(kFull, raw.y, src_lane);
+                            mr.z = __shfl_sync(kFull, raw.z, src_lane);
+                            mr.w = __shfl_sync(kFull, raw.w, src_lane);
+                        }
+                        if (!turns) mr = make_uint4(0u, 0u, 0u, 0u);   // whatever stands there, it adds nothing
+                        float inv = 1.f;
+                        if (norm) {
+                            float ss = 0.f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) ss = fmaf(y[j], y[j], ss);
+                            for (int j = 0; j < 8; ++j) ss = fmaf(y[j], y[j], ss);
 #pragma unroll
-            for (int o = CPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
-        }
-        if (act && w) {
-            const float inv = rsqrtf(ss * (1.f / D) + p.eps);
-            float wf[8];
-            unpack8(__ldg(reinterpret_cast<const uint4 *>(w) + c), wf);
+                            for (int o = CPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
+                            inv = rsqrtf(ss * (1.f / D) + p.eps);
+                        }
+                        float m[8];
+                        unpack8(mr, m);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = y[j] * inv * wf[j];
-        }
-        float z[8];
+                        for (int j = 0; j < 8; ++j) y[j] = fmaf(m[j], f[j].y, y[j] * f[j].x);
+                        if (norm)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float other = __shfl_sync(kFull, y[j], src_lane);   // the partner chunk's channel (half-split)
-            const float mate = p.interleaved ? y[j ^ 1] : other;
-            z[j] = kind == 2 || !turns ? y[j] : fmaf(y[j], co[j], mate * si[j]);
-        }
-        if (!act) continue;
-        if (kind == 0) {
-            *reinterpret_cast<uint4 *>(p.q_out + (r * p.H_Q + hh) * D + 8 * c) =
-                make_uint4(pack_bf16(z[0], z[1]), pack_bf16(z[2], z[3]), pack_bf16(z[4], z[5]), pack_bf16(z[6], z[7]));
-        } else if (blk >= 0) {
-            const int kv = kind - 1;
-            const int64_t e = (((blk * p.H_KV + hh) * 2 + kv) * p.bs + slot) * D + 8 * c;
-            if (kv == 1 && p.bits == 16) *reinterpret_cast<uint4 *>(p.base + e * 2) = raw;   // values: bits unchanged
-            else store_pool8(p, e, z, p.scales + (static_cast<int64_t>(kv) * p.H_KV + hh) * D + 8 * c);
-        }
+                            for (int j = 0; j < 8; ++j) y[j] *= inv;
+                    }
+                    if (act && gi + h0 + u * GPT < n) {
+                        if constexpr (KIND == 0)
+                            *reinterpret_cast<uint4 *>(q_dst + u * GPT * D) = make_uint4(
+                                pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+                        else if (KIND == 2 && p.bits == 16)
+                            *reinterpret_cast<uint4 *>(dst + u * GPT * head_bytes) = raw;   // values: bits unchanged
+                        else
+                            store_pool8(dst + u * GPT * head_bytes, p.bits, y, sc + u * GPT * D);
+                    }
+                }
+                q_dst += U * GPT * D;
+                dst += U * GPT * head_bytes;
+                if (sc) sc += U * GPT * D;
+#pragma unroll
+                for (int u = 0; u < U; ++u) cur[u] = next[u];
+            }
+        };
+        if (p.H_Q > 0) rows(std::integral_constant<int, 0>{});
+        rows(std::integral_constant<int, 1>{});
+        rows(std::integral_constant<int, 2>{});
     }
 }
 
-template <int D, int TPC>
-static cudaError_t launch_rope_tpc(const RopeParams &p, cudaStream_t stream)
+template <int D, int GPT, int U>
+static cudaError_t launch_rope(const RopeParams &p, int sms, cudaStream_t stream)
 {
+    constexpr int TPC = kRopeThreads / (D / 8) / GPT;
     // A programmatic dependent: its launch overlaps the tail of the kernel before it, which it
     // waits for before its first access.  It never lets its own dependents start early: the
     // chunk's kernel of kvc_mixed_step starts without waiting for the kernel before the step,
@@ -252,12 +344,16 @@ static cudaError_t launch_rope_tpc(const RopeParams &p, cudaStream_t stream)
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((p.rows + TPC - 1) / TPC));
-    cfg.blockDim = dim3(kRopeThreads);
+    static const int resident = [] {
+        int n = 0;
+        return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, rope_kernel<D, GPT, U>, kRopeCta, 0) == cudaSuccess && n > 0 ? n : 1;
+    }();
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>((p.rows + TPC - 1) / TPC, static_cast<int64_t>(sms) * resident)));
+    cfg.blockDim = dim3(kRopeCta);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, rope_kernel<D, TPC>, p);
+    return cudaLaunchKernelEx(&cfg, rope_kernel<D, GPT, U>, p);
 }
 
 static bool aligned(const void *ptr, size_t a) { return (reinterpret_cast<uintptr_t>(ptr) & (a - 1)) == 0; }
@@ -329,11 +425,19 @@ static kvc_status rope_write(kvc_pool *pool, int32_t layer, const int32_t *bt, i
     p.eps = rope->norm_eps;
     p.scales = pool->scales ? pool->scales + static_cast<size_t>(layer) * 2 * pool->H_KV * D : nullptr;
     p.err = pool->err;
-    // four tokens a CTA once that still gives every SM several CTAs, else one
-    const bool wide = rows >= 16ll * pool->num_sms;
+    // Lane groups per token and rows in flight per lane: a token per CTA while there are few (latency), more
+    // tokens per CTA as they grow (each batch costs a barrier and a look-up).  Measured, 32 + 2 x 8 heads of 128,
+    // normalised: 64 tokens 4.3 us (16 groups, 1 row) against 5.0 (8, 1) and 6.4 (4, 2); 600 tokens 8.1, 6.1 and
+    // 6.6; 4 000 tokens 32.5, 23.8 and 19.9; 16 384 tokens 121, 93 and 72.  Three rows in flight spill.
+    const int sms = pool->num_sms;
+    const int size = rows <= 2ll * sms ? 0 : (rows <= 8ll * sms ? 1 : 2);
     cudaError_t e;
-    if (D == 64) e = wide ? launch_rope_tpc<64, 4>(p, stream) : launch_rope_tpc<64, 1>(p, stream);
-    else e = wide ? launch_rope_tpc<128, 4>(p, stream) : launch_rope_tpc<128, 1>(p, stream);
+    if (D == 64)
+        e = size == 0 ? launch_rope<64, 32, 1>(p, sms, stream)
+                      : (size == 1 ? launch_rope<64, 8, 1>(p, sms, stream) : launch_rope<64, 2, 2>(p, sms, stream));
+    else
+        e = size == 0 ? launch_rope<128, 16, 1>(p, sms, stream)
+                      : (size == 1 ? launch_rope<128, 8, 1>(p, sms, stream) : launch_rope<128, 4, 2>(p, sms, stream));
     if (e != cudaSuccess) return cuda_status(e);
     g_launches.fetch_add(1, std::memory_order_relaxed);
     return KVC_OK;
