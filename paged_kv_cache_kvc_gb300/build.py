@@ -15,7 +15,7 @@ ROOT = os.path.dirname(HERE)
 
 SOURCES = ["kvc_core.cu", "kvc_attn.cu", "kvc_decode_bf16.cu", "kvc_decode_fp8.cu", "kvc_decode_int4.cu",
            "kvc_decode_tc.cu", "kvc_decode_tc8.cu", "kvc_prefill_tc.cu", "kvc_noalloc.cu", "kvc_alloc.cu", "kvc_rope.cu",
-           "kvc_mod.cu", "kvc_mod_bf16.cu", "kvc_mod_fp8.cu", "kvc_mod_int4.cu", "kvc_mod_tc.cu"]
+           "kvc_mod.cu", "kvc_mod_bf16.cu", "kvc_mod_fp8.cu", "kvc_mod_int4.cu", "kvc_mod_tc.cu", "kvc_mod_tcq.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hidden", "--expt-relaxed-constexpr",
               "-I" + os.path.join(ROOT, "include")]

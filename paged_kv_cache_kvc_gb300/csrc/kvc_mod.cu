@@ -164,7 +164,7 @@ static size_t tc_bytes(int64_t ctas, int D)
 static bool use_tc(const kvc_pool *pool)
 {
     const char *e = std::getenv("KVC_TC");
-    return !(e && e[0] == '0') && pool->dtype == KVC_BF16 && pool->tmap16_ok;
+    return !(e && e[0] == '0') && (pool->dtype != KVC_BF16 || pool->tmap16_ok);   // the other map is checked for every call
 }
 
 static int tc_min_group()
@@ -186,7 +186,8 @@ static kvc_status run_tc(kvc_pool *pool, const ModParams &mp0, void *ws, size_t 
     tp.whole = !ws;
     tp.split = !tp.whole && (decode || p.n_pos <= p.ppu);
     const bool fixed = tp.m.capped && !tp.m.alibi && tp.m.cap_out <= kMtCapLimit;
-    const DecodeKernel k = select_mod_tc(pool->D, fixed);
+    const DecodeKernel k = pool->dtype == KVC_BF16 ? select_mod_tc_bf16(pool->D, fixed)
+                                                   : select_mod_tc_quant(pool->dtype == KVC_INT4, fixed);
     if (!k.fn) return KVC_ERR_UNSUPPORTED;
     if (k.ctas_per_sm <= 0) return KVC_ERR_CUDA;
     const int unit = tp.split ? p.ppu : 2 * p.ppu;   // positions per unit
@@ -214,7 +215,7 @@ static kvc_status run_tc(kvc_pool *pool, const ModParams &mp0, void *ws, size_t 
             tp.part_o = reinterpret_cast<float *>(base + kPrefixBytes);
             tp.part_ml = reinterpret_cast<float2 *>(tp.part_o + static_cast<size_t>(ctas) * 2 * 256 * pool->D);
         }
-        void *args[] = {&pool->tmap16, &tp};
+        void *args[] = {k.tmap16 ? &pool->tmap16 : &pool->tmap, &tp};
         cudaError_t e = launch_dependent(k.fn, dim3(static_cast<unsigned>(ctas)), dim3(kMtThreads), k.smem, stream, args);
         if (e != cudaSuccess) return cuda_status(e);
         g_launches.fetch_add(1, std::memory_order_relaxed);
@@ -313,8 +314,7 @@ extern "C" kvc_status kvc_mod_workspace_bytes(const kvc_pool *pool, int32_t rows
     const int64_t by_slots = ppu * (14ll * pool->num_sms / pool->H_KV + 1) + 2ll * rows;
     const int64_t by_cap = rows * ((max_blocks + 283ll) / 284 + 1);
     const int64_t n = std::min(rows * by_len, std::max(by_slots, by_cap));
-    *bytes = kCounterBytes + std::max(partial_bytes(n, num_q_heads, pool->D),
-                                      pool->dtype == KVC_BF16 ? tc_bytes(pool->num_sms, pool->D) : 0);
+    *bytes = kCounterBytes + std::max(partial_bytes(n, num_q_heads, pool->D), tc_bytes(pool->num_sms, pool->D));
     return KVC_OK;
 }
 

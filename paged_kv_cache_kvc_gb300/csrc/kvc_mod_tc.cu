@@ -1,30 +1,12 @@
-// Instances of the tensor-memory (tcgen05) kernel of attention with modified scores.
+// bf16-pool instances of the tensor-memory (tcgen05) kernel of attention with modified scores, and its merge.
 #include "kvc_mod_tc.cuh"
 
 namespace kvc {
 
-template <int D, bool FIXED>
-static DecodeKernel instance()
+DecodeKernel select_mod_tc_bf16(int D, bool fixed)
 {
-    static DecodeKernel k = [] {
-        DecodeKernel r{nullptr, 0, 0};
-        const void *fn = reinterpret_cast<const void *>(&mod_tc_kernel<D, FIXED>);
-        r.fn = fn;
-        r.smem = ModTcCfg<D>::SMEM;
-        r.threads = kMtThreads;
-        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, r.smem) == cudaSuccess) {
-            int n = 0;
-            if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, kMtThreads, r.smem) == cudaSuccess) r.ctas_per_sm = n;
-        }
-        return r;
-    }();
-    return k;
-}
-
-DecodeKernel select_mod_tc(int D, bool fixed)
-{
-    if (D == 64) return fixed ? instance<64, true>() : instance<64, false>();
-    return fixed ? instance<128, true>() : instance<128, false>();
+    if (D == 64) return fixed ? mod_tc_instance<64, KV_BF16, true>() : mod_tc_instance<64, KV_BF16, false>();
+    return fixed ? mod_tc_instance<128, KV_BF16, true>() : mod_tc_instance<128, KV_BF16, false>();
 }
 
 const void *select_mod_tc_merge(int D, bool few)

@@ -3,29 +3,35 @@
 //
 // A unit is KV head h and 256 query rows: 2 x 128 / g consecutive chunk positions x the g query
 // heads of h, as two tiles of 128 rows (row r of a tile = position r / g, head h g + r mod g).  A
-// staged tile of 128 keys and values serves both.  Each query tile is its own chain of 64-key steps
+// staged tile of 64 keys and values serves both.  Each query tile is its own chain
 //     S[128 x 64] = Q K^T  ->  softmax warps: P over S in TMEM  ->  O += P V
 // with two score buffers, so that a step's scores are there when the softmax warps are done with the
 // step before.  (One 128-key buffer per query tile measured 1.7x slower: the two chains fell into
 // step, both computing weights, then both waiting for the tensor cores.)  384 threads:
 //   warps 0..3, 4..7  softmax of tile 0, 1; thread = query row (TMEM lane)
-//   warp 8, 9         TMA producers of the key and of the value tiles (rings of 2), one 16-row box per
-//                     block and 128-byte band (one warp's boxes issue ~40 ns apart, hence two warps);
-//                     warp 9 also zeroes value rows that no row of the unit reads, once landed
-//   warp 10, 11       MMA issuers of tile 0, 1
+//   warps 8, 9        bring the key and the value tiles into rings; warp 9 also zeroes value rows that
+//                     no row of the unit reads (a zero weight times NaN is NaN)
+//   warps 10, 11      MMA issuers of tile 0, 1
+// bf16 pools: warps 8 and 9 issue one 16-row TMA box per block and 128-byte band (one warp's boxes
+// issue ~40 ns apart, hence two warps).  e4m3 and int4 pools: warp 8 issues whole blocks of codes into
+// a third ring; warp 8 widens the landed keys to f16 and warp 9 the values to bf16, both exactly.  The
+// queries are then q times the key scales, rounded to f16 (as in the split kernel), and the value
+// scales multiply the outputs.  int4 codes widen in the order 0, 4, 1, 5, 2, 6, 3, 7 of every eight
+// channels (two nibbles 16 bits apart are one mask): the queries are staged in that order, and the
+// outputs' registers are read in it.
 //
 // Work split.  The unit's key tiles (only those that some row reads, kvc_mod.cuh) of every head and
 // unit form one line of W tiles; CTA c of G takes tiles [c W / G, (c + 1) W / G), whatever units they
 // belong to, so every SM gets the same work to within a tile: a late chunk of few long rows, a long
 // triangular one and a ragged decode batch alike.  A unit that lies in one CTA is written at once; a
-// unit's start costs about two tiles (its queries staged, its outputs written: 5 us against 2.5 us a
+// unit's start costs about four tiles (its queries staged, its outputs written: 5 us against 1.2 us a
 // tile), so the line gives every unit kMtStart tiles more than it has.  A
 // unit cut by CTA borders leaves fp32 partials (at most two per CTA) for mod_tc_merge_kernel, which
 // adds them in CTA order.  (Merged by the unit's last CTA instead, 600 queries of 1800 positions took
 // 43 us, 20 pieces of a 5-query chunk 9 us of its 36: one SM's loads against all SMs'.)
 //
 // Few rows (a chunk of at most 128 / g positions, a decode sequence): both chains take the same rows,
-// chain 0 the first 64 keys of every tile and chain 1 the rest, and the merge joins them too.
+// chain 0 every other tile and chain 1 the rest, and the merge joins them too.
 //
 // Weights.  With capped scores (and no bias) x lies in [-cap, cap], so the softmax needs no maximum:
 // 2^(x - cap / 2) fits fp32 and bf16 for caps up to 55 (80 in log2 units), and a score needs no
@@ -39,13 +45,11 @@
 
 namespace kvc {
 
-constexpr int kMtKeys = 128;                       // keys per tile
+constexpr int kMtKeys = 64;                        // keys per tile
 constexpr int kMtBlocks = kMtKeys / kBS;
-constexpr int kMtStep = 64;                        // keys per score buffer
-constexpr int kMtStepBlocks = kMtStep / kBS;
 constexpr int kMtThreads = 384;
 constexpr int kMtUnits = 2048;                     // most units (per head) of one launch
-constexpr int kMtStart = 2;                        // a unit's start, in tiles
+constexpr int kMtStart = 4;                        // a unit's start, in tiles
 constexpr float kMtCapLimit = 80.f;                // cap in log2 units up to which no maximum is needed
 
 struct ModTcParams {
@@ -61,20 +65,97 @@ struct ModTcParams {
     float2 *part_ml;      // [2 G][256]
 };
 
-template <int D>
+template <int D, int KIND>
 struct ModTcCfg {
+    static constexpr bool QUANT = KIND != KV_BF16;
     static constexpr int BANDS = D / 64;
-    static constexpr int BAND = 128 * 128;             // one 128-byte column band of 128 rows
-    static constexpr int TILE = BANDS * BAND;          // keys, values or queries of one tile
+    static constexpr int QBAND = 128 * 128;            // one 128-byte column band of 128 query rows
+    static constexpr int QTILE = BANDS * QBAND;
+    static constexpr int KBAND = kMtKeys * 128;        // one band of 64 key or value rows
+    static constexpr int STAGE = BANDS * KBAND;
+    static constexpr int R = QUANT ? 3 : 4;            // ring depths (with QUANT: codes, keys and values alike)
+    static constexpr int BLOCK = QUANT ? DecodeCfg<D, KIND>::STAGE : 0;   // a block's codes, keys then values
+    static constexpr int RAW = kMtBlocks * BLOCK;
     static constexpr int Q = 0;                        // [2] query tiles
-    static constexpr int K = 2 * TILE;                 // [2] key tiles
-    static constexpr int V = 4 * TILE;                 // [2] value tiles
-    static constexpr int PREFIX = 6 * TILE;            // int32 [kMtUnits + 1]
+    static constexpr int K = 2 * QTILE;                // [R] key tiles
+    static constexpr int V = K + R * STAGE;            // [R] value tiles
+    static constexpr int C = V + R * STAGE;            // [R] tiles of codes
+    static constexpr int PREFIX = C + R * RAW;         // int32 [kMtUnits + 1]
     static constexpr int BARS = PREFIX + ((kMtUnits + 1) * 4 + 15) / 16 * 16;
-    static constexpr int NBARS = 24;
-    static constexpr int MISC = BARS + NBARS * 8;      // scan sums [12], abort, TMEM base, block masks [4]
+    static constexpr int NBARS = 7 * R + 14;
+    static constexpr int MISC = BARS + NBARS * 8;      // scan sums [12], abort, TMEM base, block masks [16]
     static constexpr int SMEM = 1024 + MISC + 128;
+    static_assert(SMEM <= 232448, "shared memory of a CTA");
 };
+
+// Two f16 to two bf16 (through fp32; exact for e4m3 values).
+__device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t x)
+{
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&x));
+    return pack_bf16(f.x, f.y);
+}
+
+// Two nibbles, bits 0..3 and 16..19 of x (stored q + 8), to bf16x2 of q: 0x4300 | u is 128 + u, exact.
+__device__ __forceinline__ uint32_t nibbles_to_bf16x2(uint32_t x)
+{
+    const uint32_t biased = (x & 0x000F000Fu) | 0x43004300u;
+    uint32_t r;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(biased), "r"(0x43084308u));   // - (128 + 8)
+    return r;
+}
+
+// The eight nibbles of a word, widened to f16 (keys) or bf16 (values), in the order 0, 4, 1, 5, 2, 6, 3, 7.
+template <bool BF16>
+__device__ __forceinline__ uint4 widen_nibbles(uint32_t w)
+{
+    if constexpr (BF16)
+        return make_uint4(nibbles_to_bf16x2(w), nibbles_to_bf16x2(w >> 4), nibbles_to_bf16x2(w >> 8), nibbles_to_bf16x2(w >> 12));
+    else
+        return make_uint4(nibbles_to_f16x2(w), nibbles_hi_to_f16x2(w), nibbles_to_f16x2(w >> 8), nibbles_hi_to_f16x2(w >> 8));
+}
+
+// Column of a widened eight that holds channel e.
+template <int KIND>
+__host__ __device__ constexpr int widened_column(int e)
+{
+    return KIND != KV_INT4 ? e : (e < 4 ? 2 * e : 2 * (e - 4) + 1);
+}
+
+// One warp: the 64 key (VALUES = false) or value rows of a tile of codes, widened into a tile of 16-bit rows
+// (the 128-byte-swizzled bands that TMA writes for bf16 pools).  keep(row): false zeroes the row.
+template <int D, int KIND, bool VALUES, typename Keep>
+__device__ __forceinline__ void widen_tile(uint32_t codes, uint32_t wide, int lane, Keep keep)
+{
+    using C = ModTcCfg<D, KIND>;
+    constexpr int N = DecodeCfg<D, KIND>::CHUNKS;   // 16-byte chunks of codes per row
+    constexpr int OUT = 128 / DecodeCfg<D, KIND>::BITS / 8;   // chunks of 8 widened channels from one: e4m3 2, int4 4
+    static_assert(OUT == (KIND == KV_INT4 ? 4 : 2) && OUT * N * 8 == D, "a row of codes is a row of channels");
+#pragma unroll 4
+    for (int i = lane; i < kMtKeys * N; i += 32) {
+        const int row = i / N, ch = i % N;
+        const uint4 x = lds128(codes + (row / kBS) * C::BLOCK + row_chunk<D, KIND>((VALUES ? kBS : 0) + row % kBS, ch));
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        const bool ok = keep(row);
+#pragma unroll
+        for (int o = 0; o < OUT; ++o) {
+            uint4 y;
+            if constexpr (KIND == KV_INT4) {
+                y = widen_nibbles<VALUES>(w[o]);
+            } else {
+                uint32_t h[4];
+                e4m3x4_to_f16x2x2(w[2 * o], h[0], h[1]);
+                e4m3x4_to_f16x2x2(w[2 * o + 1], h[2], h[3]);
+                if constexpr (VALUES)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) h[u] = f16x2_to_bf16x2(h[u]);
+                y = make_uint4(h[0], h[1], h[2], h[3]);
+            }
+            if (!ok) y = make_uint4(0u, 0u, 0u, 0u);
+            const int c8 = OUT * ch + o;   // eight channels
+            sts128(wide + (c8 >> 3) * C::KBAND + sw128(row, c8 & 7), y);
+        }
+    }
+}
 
 // Scale 16 columns of this thread's TMEM lane (whole warp).
 __device__ __forceinline__ void tmem_scale16(uint32_t taddr, float f)
@@ -276,11 +357,13 @@ __device__ __forceinline__ int cta_of(int64_t w, int64_t W, int64_t G)
 }
 
 // FIXED: capped scores against the fixed reference; else the running reference maximum.
-template <int D, bool FIXED>
-__global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_constant__ CUtensorMap tmap16,
+// tmap: the pool's map of 16-row boxes (bf16), else the map of whole blocks.
+template <int D, int KIND, bool FIXED>
+__global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_constant__ CUtensorMap tmap,
                                                                 const ModTcParams tp)
 {
-    using C = ModTcCfg<D>;
+    using C = ModTcCfg<D, KIND>;
+    constexpr int R = C::R;
     const ModParams &mp = tp.m;
     const DecodeParams &p = mp.d;
     extern __shared__ uint8_t smem_raw[];
@@ -292,26 +375,32 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
     int32_t *misc = reinterpret_cast<int32_t *>(smem + C::MISC);
     volatile int32_t *abort_sh = misc + 12;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(misc + 13);
-    volatile uint32_t *mask_sh = reinterpret_cast<volatile uint32_t *>(misc + 16);   // loaded blocks of key tile kt, slot kt mod 4
+    volatile uint32_t *mask_sh = reinterpret_cast<volatile uint32_t *>(misc + 16);   // loaded blocks of tile kt, place kt mod 16
     auto bar = [&](int i) { return sbase + C::BARS + 8u * static_cast<uint32_t>(i); };
     // barriers: per ring slot, then per query tile
     auto kfull = [&](int s) { return bar(s); };
-    auto kfree = [&](int s) { return bar(2 + s); };
-    auto vfull = [&](int s) { return bar(4 + s); };
-    auto vfree = [&](int s) { return bar(6 + s); };
-    auto vready = [&](int s) { return bar(8 + s); };
-    auto qfull = [&](int x) { return bar(10 + x); };
-    auto sfull = [&](int x, int b) { return bar(12 + 2 * x + b); };   // per query tile and score buffer
-    auto pfull = [&](int x, int b) { return bar(16 + 2 * x + b); };
-    auto pvdone = [&](int x, int b) { return bar(20 + 2 * x + b); };
+    auto kfree = [&](int s) { return bar(R + s); };
+    auto vfull = [&](int s) { return bar(2 * R + s); };    // bf16: the copy; vready follows it
+    auto vfree = [&](int s) { return bar(3 * R + s); };
+    auto vready = [&](int s) { return bar(4 * R + s); };
+    auto cfull = [&](int s) { return bar(5 * R + s); };    // codes
+    auto cfree = [&](int s) { return bar(6 * R + s); };
+    auto qfull = [&](int x) { return bar(7 * R + x); };
+    auto sfull = [&](int x, int b) { return bar(7 * R + 2 + 2 * x + b); };   // per query tile and score buffer
+    auto pfull = [&](int x, int b) { return bar(7 * R + 6 + 2 * x + b); };
+    auto pvdone = [&](int x, int b) { return bar(7 * R + 10 + 2 * x + b); };
 
     if (tid == 0) {
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < R; ++s) {
             mbar_init(kfull(s), 1);
-            mbar_init(kfree(s), 2);
+            mbar_init(kfree(s), tp.split ? 1 : 2);   // the chains that take the tile
             mbar_init(vfull(s), 1);
-            mbar_init(vfree(s), 2);
+            mbar_init(vfree(s), tp.split ? 1 : 2);
             mbar_init(vready(s), 1);
+            mbar_init(cfull(s), 1);
+            mbar_init(cfree(s), 2);
+        }
+        for (int s = 0; s < 2; ++s) {
             mbar_init(qfull(s), 128);
             for (int b = 0; b < 2; ++b) {
                 mbar_init(sfull(s, b), 1);
@@ -320,7 +409,7 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
             }
         }
         fence_barrier_init();
-        prefetch_tensormap(&tmap16);
+        prefetch_tensormap(&tmap);
         *abort_sh = 0;
     }
     if (warp == 0) {
@@ -408,158 +497,227 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
 
     if (warp >= 8) {
         if (warp <= 9) {
-            // -------------------------------------------------------- TMA producers: keys (8), values (9)
+            // -------------------------------------------------------- keys (8) and values (9)
             const bool values = warp == 9;
             const int64_t row_layer = static_cast<int64_t>(p.layer) * p.N;
-            const int bl = lane & (kMtBlocks - 1), band = lane >> 3;
-            const bool box = lane < kMtBlocks * C::BANDS;
+            const int bl = lane & (kMtBlocks - 1), band = lane / kMtBlocks;   // this lane's block of a tile (and band)
             uint32_t kt = 0;   // tiles so far
-            int prev_slot = -1, prev_unit = -1;
-            uint32_t prev_mask = 0, prev_parity = 0;
-            int prev_tile = 0;
-            UnitView v{}, pv{};
-            // values: once the previous tile has landed, zero the rows that nothing reads, then pass it on
-            auto finish = [&]() -> bool {
-                if (prev_slot < 0) return true;
-                if (!wait(vfull(prev_slot), prev_parity)) return false;
-                const int first = prev_tile * kMtBlocks;
-                const bool one_run = first + kMtBlocks <= pv.br.n && (first + kMtBlocks <= pv.br.n0 || first >= pv.br.n0);
-                const int t0 = pv.br.at(first) * kBS;
-                const bool clean = one_run && prev_mask == (1u << kMtBlocks) - 1u && !mp.doc_start &&
-                                   ((t0 >= pv.a0 && t0 + kMtKeys <= pv.a1) || (t0 >= pv.e0 && t0 + kMtKeys <= pv.e1));
-                if (!clean) {
-                    const uint32_t st = sbase + C::V + prev_slot * C::TILE;
-                    for (int k = lane; k < kMtKeys; k += 32) {
-                        const int vb = first + k / kBS;
-                        bool used = vb < pv.br.n && (prev_mask >> (k / kBS) & 1u);
-                        if (used) {
-                            const int t = pv.br.at(vb) * kBS + k % kBS;
-                            // rows at consecutive positions read consecutive runs, so without documents
-                            // the union has no holes; with them each row of the unit is asked
-                            used = (t >= pv.a0 && t < pv.a1) || (t >= pv.e0 && t < pv.e1);
-                            if (used && mp.doc_start) {
-                                used = false;
-                                for (int i = 0; i < pv.n_pos && !used; ++i) {
-                                    const Range r = row_view(tp, pv.pos0 + i).r;
-                                    used = (t >= r.lo && t < r.hi) || (t >= r.d && t < r.e);
-                                }
-                            }
-                        }
-                        if (!used)
-#pragma unroll
-                            for (int c = 0; c < 8 * C::BANDS; ++c)
-                                sts128_zero(st + (c >> 3) * C::BAND + sw128(k, c & 7));
-                    }
-                    fence_proxy_async_smem();
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(vready(prev_slot));
-                prev_slot = -1;
-                return true;
-            };
             bool go = true;
-            for (Segment s = walk.next(); go && s.ok; s = walk.next()) {
-                v = unit_view(tp, s.unit, lane);
-                const int32_t *bt = p.bt + (p.lens ? static_cast<int64_t>(s.unit) * p.bt_stride : 0);
-                auto entry = [&](int k) -> int32_t {   // table entry of this lane's block of tile k
-                    const int vb = k * kMtBlocks + bl;
-                    return k < s.k1 && vb < v.br.n ? __ldg(bt + v.br.at(vb)) : -1;
-                };
-                auto is_read = [&](int t) {   // some row of the unit reads a position of block [t, t + 16)
-                    for (int i = 0; i < v.n_pos; ++i) {
-                        const Range r = row_view(tp, v.pos0 + i).r;
-                        if ((t < r.hi && t + kBS > r.lo && r.hi > r.lo) || (t < r.e && t + kBS > r.d && r.e > r.d)) return true;
-                    }
-                    return false;
-                };
-                int32_t e_next = entry(s.k0);
-                for (int k = s.k0; k < s.k1; ++k, ++kt) {
-                    const int slot = kt & 1;
-                    const int32_t e = e_next;
-                    e_next = entry(k + 1);
-                    if (kt >= 2) {
-                        const uint32_t fb = values ? vfree(slot) : kfree(slot), fp = ((kt >> 1) - 1) & 1;
-                        // while the slot is in use, pass the previous value tile on first
-                        if (values && !__any_sync(kFull, lane == 0 && mbar_test_wait(fb, fp)) && !finish()) {
-                            go = false;
-                            break;
-                        }
-                        if (!wait(fb, fp)) {
-                            go = false;
-                            break;
-                        }
-                    }
-                    const int vb = k * kMtBlocks + bl;
-                    const bool have = vb < v.br.n, ok = have && e >= 0 && static_cast<int64_t>(e) < p.N;
-                    if (!values && band == 0 && have && !ok && is_read(v.br.at(vb) * kBS)) atomicOr(p.err, KVC_EBIT_BAD_BLOCK);
-                    const uint32_t mask = __ballot_sync(kFull, ok && lane < kMtBlocks);
-                    if (!values && lane == 0) mask_sh[kt & 3] = mask;   // published by the arrive below
-                    const uint32_t full = values ? vfull(slot) : kfull(slot);
-                    if (p.stall_loads) {   // the test hook withholds every load
-                    } else if (mask == 0u) {
-                        if (lane == 0) mbar_arrive(full);
-                    } else if (lane == 0) {
-                        mbar_arrive_expect_tx(full, static_cast<uint32_t>(__popc(mask)) * C::BANDS * (kBS * 128u));
+            // which of a tile's value rows some row of the unit reads
+            auto is_clean = [&](const UnitView &v, int k, uint32_t mask) {
+                const int first = k * kMtBlocks;
+                const bool one_run = first + kMtBlocks <= v.br.n && (first + kMtBlocks <= v.br.n0 || first >= v.br.n0);
+                const int t0 = v.br.at(first) * kBS;
+                return one_run && mask == (1u << kMtBlocks) - 1u && !mp.doc_start &&
+                       ((t0 >= v.a0 && t0 + kMtKeys <= v.a1) || (t0 >= v.e0 && t0 + kMtKeys <= v.e1));
+            };
+            auto is_used = [&](const UnitView &v, int k, uint32_t mask, int row) {
+                const int vb = k * kMtBlocks + row / kBS;
+                if (vb >= v.br.n || !(mask >> (row / kBS) & 1u)) return false;
+                const int t = v.br.at(vb) * kBS + row % kBS;
+                // rows at consecutive positions read consecutive runs, so without documents the union
+                // has no holes; with them each row of the unit is asked
+                if (!((t >= v.a0 && t < v.a1) || (t >= v.e0 && t < v.e1))) return false;
+                if (!mp.doc_start) return true;
+                for (int i = 0; i < v.n_pos; ++i) {
+                    const Range r = row_view(tp, v.pos0 + i).r;
+                    if ((t >= r.lo && t < r.hi) || (t >= r.d && t < r.e)) return true;
+                }
+                return false;
+            };
+            auto is_read = [&](const UnitView &v, int t) {   // some row of the unit reads a position of block [t, t + 16)
+                for (int i = 0; i < v.n_pos; ++i) {
+                    const Range r = row_view(tp, v.pos0 + i).r;
+                    if ((t < r.hi && t + kBS > r.lo && r.hi > r.lo) || (t < r.e && t + kBS > r.d && r.e > r.d)) return true;
+                }
+                return false;
+            };
+            auto table = [&](const Segment &s) { return p.bt + (p.lens ? static_cast<int64_t>(s.unit) * p.bt_stride : 0); };
+            // table entry of this lane's block of the segment's tile k (-1: none)
+            auto entry = [&](const Segment &s, const UnitView &v, int k) -> int32_t {
+                const int vb = k * kMtBlocks + bl;
+                return k < s.k1 && vb < v.br.n ? __ldg(table(s) + v.br.at(vb)) : -1;
+            };
+            auto valid = [&](int32_t e) { return e >= 0 && static_cast<int64_t>(e) < p.N; };
+            if constexpr (!C::QUANT) {
+                const bool box = lane < kMtBlocks * C::BANDS;
+                int prev_slot = -1, prev_unit = -1, prev_tile = 0;
+                uint32_t prev_mask = 0, prev_parity = 0;
+                UnitView v{}, pv{};
+                // values: once the previous tile has landed, zero the rows that nothing reads, then pass it on
+                auto finish = [&]() -> bool {
+                    if (prev_slot < 0) return true;
+                    if (!wait(vfull(prev_slot), prev_parity)) return false;
+                    if (!is_clean(pv, prev_tile, prev_mask)) {
+                        const uint32_t st = sbase + C::V + prev_slot * C::STAGE;
+                        for (int k = lane; k < kMtKeys; k += 32)
+                            if (!is_used(pv, prev_tile, prev_mask, k))
+#pragma unroll
+                                for (int c = 0; c < 8 * C::BANDS; ++c)
+                                    sts128_zero(st + (c >> 3) * C::KBAND + sw128(k, c & 7));
+                        fence_proxy_async_smem();
                     }
                     __syncwarp();
-                    if (box && ok && !p.stall_loads) {
-                        const int32_t y = static_cast<int32_t>(((row_layer + e) * p.H_KV + s.head) * (2 * kBS)) + (values ? kBS : 0);
-                        tma_load_2d(sbase + (values ? C::V : C::K) + slot * C::TILE + band * C::BAND + bl * (kBS * 128),
-                                    &tmap16, full, band * 64, y);
-                    }
-                    if (values) {
-                        if (!finish()) {
-                            go = false;
-                            break;
+                    if (lane == 0) mbar_arrive(vready(prev_slot));
+                    prev_slot = -1;
+                    return true;
+                };
+                for (Segment s = walk.next(); go && s.ok; s = walk.next()) {
+                    v = unit_view(tp, s.unit, lane);
+                    int32_t e_next = entry(s, v, s.k0);
+                    for (int k = s.k0; k < s.k1; ++k, ++kt) {
+                        const int slot = kt % R;
+                        const int32_t e = e_next;
+                        e_next = entry(s, v, k + 1);
+                        if (kt >= R) {
+                            const uint32_t fb = values ? vfree(slot) : kfree(slot), fp = (kt / R - 1) & 1;
+                            // while the slot is in use, pass the previous value tile on first
+                            if (values && !__any_sync(kFull, lane == 0 && mbar_test_wait(fb, fp))) go = finish();
+                            go = go && wait(fb, fp);
+                            if (!go) break;
                         }
-                        prev_slot = slot;
-                        prev_parity = (kt >> 1) & 1;
-                        prev_mask = mask;
-                        prev_tile = k;
-                        if (prev_unit != s.unit) {
-                            pv = v;
-                            prev_unit = s.unit;
+                        const int vb = k * kMtBlocks + bl;
+                        const bool have = vb < v.br.n, ok = have && valid(e);
+                        if (!values && band == 0 && have && !ok && is_read(v, v.br.at(vb) * kBS)) atomicOr(p.err, KVC_EBIT_BAD_BLOCK);
+                        const uint32_t mask = __ballot_sync(kFull, ok && lane < kMtBlocks);
+                        if (!values && lane == 0) mask_sh[kt & 15] = mask;   // published by the arrive below
+                        const uint32_t full = values ? vfull(slot) : kfull(slot);
+                        if (p.stall_loads) {   // the test hook withholds every load
+                        } else if (mask == 0u) {
+                            if (lane == 0) mbar_arrive(full);
+                        } else if (lane == 0) {
+                            mbar_arrive_expect_tx(full, static_cast<uint32_t>(__popc(mask)) * C::BANDS * (kBS * 128u));
+                        }
+                        __syncwarp();
+                        if (box && ok && !p.stall_loads) {
+                            const int32_t y = static_cast<int32_t>(((row_layer + e) * p.H_KV + s.head) * (2 * kBS)) + (values ? kBS : 0);
+                            tma_load_2d(sbase + (values ? C::V : C::K) + slot * C::STAGE + band * C::KBAND + bl * (kBS * 128), &tmap,
+                                        full, band * 64, y);
+                        }
+                        if (values) {
+                            go = finish();
+                            if (!go) break;
+                            prev_slot = slot;
+                            prev_parity = (kt / R) & 1;
+                            prev_mask = mask;
+                            prev_tile = k;
+                            if (prev_unit != s.unit) {
+                                pv = v;
+                                prev_unit = s.unit;
+                            }
                         }
                     }
                 }
+                if (values && go) go = finish();
+                // before the CTA ends: every copy issued has landed (immediate unless a wait expired)
+                if (!p.stall_loads)
+                    for (uint32_t t = kt >= R ? kt - R : 0; t < kt; ++t)
+                        (void)mbar_wait_bounded(values ? vfull(t % R) : kfull(t % R), (t / R) & 1, 100000000ull);
+            } else {
+                // Warp 8 issues the codes of up to R tiles ahead of the one that both warps widen; `ahead` makes
+                // its own walk.
+                Walk far = walk;
+                Segment fs = far.next();
+                UnitView fv{};
+                int fk = fs.ok ? fs.k0 : 0;
+                if (!values && fs.ok) fv = unit_view(tp, fs.unit, lane);
+                uint32_t issued = 0;
+                auto issue = [&]() -> bool {   // the next tile's codes, if there is one
+                    if (!fs.ok) return true;
+                    const int slot = issued % R;
+                    if (issued >= R && !wait(cfree(slot), (issued / R - 1) & 1)) return false;
+                    const int vb = fk * kMtBlocks + bl;
+                    const int32_t e = entry(fs, fv, fk);
+                    const bool have = vb < fv.br.n, ok = have && valid(e);
+                    if (lane < kMtBlocks && have && !ok && is_read(fv, fv.br.at(vb) * kBS)) atomicOr(p.err, KVC_EBIT_BAD_BLOCK);
+                    const uint32_t mask = __ballot_sync(kFull, ok && lane < kMtBlocks);
+                    if (lane == 0) mask_sh[issued & 15] = mask;   // published by the arrive below
+                    if (p.stall_loads) {   // the test hook withholds every load
+                    } else if (lane == 0) {
+                        if (mask == 0u) mbar_arrive(cfull(slot));
+                        else mbar_arrive_expect_tx(cfull(slot), static_cast<uint32_t>(__popc(mask)) * C::BLOCK);
+                    }
+                    __syncwarp();
+                    if (lane < kMtBlocks && ok && !p.stall_loads)
+                        tma_load_2d(sbase + C::C + slot * C::RAW + bl * C::BLOCK, &tmap, cfull(slot), 0,
+                                    static_cast<int32_t>(((row_layer + e) * p.H_KV + fs.head) * DecodeCfg<D, KIND>::BOX_ROWS));
+                    ++issued;
+                    if (++fk == fs.k1) {
+                        const int unit = fs.unit;
+                        fs = far.next();
+                        if (fs.ok) {
+                            fk = fs.k0;
+                            if (fs.unit != unit) fv = unit_view(tp, fs.unit, lane);
+                        }
+                    }
+                    return true;
+                };
+                if (!values)
+                    for (int i = 0; go && i < R - 1; ++i) go = issue();
+                for (Segment s = walk.next(); go && s.ok; s = walk.next()) {
+                    UnitView v{};
+                    if (values) v = unit_view(tp, s.unit, lane);
+                    for (int k = s.k0; k < s.k1; ++k, ++kt) {
+                        const int slot = kt % R;
+                        const uint32_t par = (kt / R) & 1;
+                        if (!values) go = issue();   // into the slot whose tile both warps widened last
+                        go = go && wait(cfull(slot), par);
+                        if (kt >= R) go = go && wait(values ? vfree(slot) : kfree(slot), (kt / R - 1) & 1);
+                        if (!go) break;
+                        const uint32_t codes = sbase + C::C + slot * C::RAW;
+                        if (!values) {
+                            widen_tile<D, KIND, false>(codes, sbase + C::K + slot * C::STAGE, lane, [](int) { return true; });
+                        } else {
+                            const uint32_t mask = mask_sh[kt & 15];
+                            if (is_clean(v, k, mask))
+                                widen_tile<D, KIND, true>(codes, sbase + C::V + slot * C::STAGE, lane, [](int) { return true; });
+                            else
+                                widen_tile<D, KIND, true>(codes, sbase + C::V + slot * C::STAGE, lane,
+                                                          [&](int row) { return is_used(v, k, mask, row); });
+                        }
+                        fence_proxy_async_smem();   // written here, read by the MMA; the codes' slot is rewritten by TMA
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(values ? vready(slot) : kfull(slot));
+                            mbar_arrive(cfree(slot));
+                        }
+                    }
+                }
+                if (!values && !p.stall_loads)
+                    for (uint32_t t = issued >= R ? issued - R : 0; t < issued; ++t)
+                        (void)mbar_wait_bounded(cfull(t % R), (t / R) & 1, 100000000ull);
             }
-            if (values && go) go = finish();
-            // before the CTA ends: every copy issued has landed (immediate unless a wait expired)
-            if (!p.stall_loads)
-                for (uint32_t t = kt >= 2 ? kt - 2 : 0; t < kt; ++t)
-                    (void)mbar_wait_bounded(values ? vfull(t & 1) : kfull(t & 1), (t >> 1) & 1, 100000000ull);
             __syncwarp();
         } else {
             // -------------------------------------------------------- MMA issuer of query tile x
             const int x = warp - 10;
-            constexpr uint32_t idesc_qk = tc_idesc_f16(128, kMtStep, true, false, false);
+            constexpr uint32_t idesc_qk = tc_idesc_f16(128, kMtKeys, !C::QUANT, false, false);
             constexpr uint32_t idesc_pv = tc_idesc_f16(128, D, true, false, true);
-            const uint64_t desc_q = tc_smem_desc(sbase + C::Q + x * C::TILE, 16, 1024, kSwizzle128B);
+            const uint64_t desc_q = tc_smem_desc(sbase + C::Q + x * C::QTILE, 16, 1024, kSwizzle128B);
             const uint32_t tm_s = tmem + 128 * x, tm_o = tmem + 256 + 128 * x;
-            uint32_t kt = 0, it = 0, seg = 0;   // key tiles, this query tile's steps and its segments so far
-            // scores of step i of a segment whose first key tile is the CTA's kt0-th, into score buffer b: 64 keys
-            // of a tile (its halves in turn, or chain x's half of every tile)
-            auto scores = [&](uint32_t kt0, uint32_t i, uint32_t b) -> bool {
-                const uint32_t tile = kt0 + (tp.split ? i : i >> 1), slot = tile & 1, half = tp.split ? x : i & 1;
-                if ((tp.split || half == 0) && !wait(kfull(slot), (tile >> 1) & 1)) return false;
+            uint32_t kt = 0, it = 0, seg = 0;   // key tiles, this chain's steps and its segments so far
+            // scores against the CTA's key tile `tile`, into score buffer b
+            auto scores = [&](uint32_t tile, uint32_t b) -> bool {
+                const uint32_t slot = tile % R;
+                if (!wait(kfull(slot), (tile / R) & 1)) return false;
                 tc_fence_after();
-                const uint64_t b0 = tc_smem_desc(sbase + C::K + slot * C::TILE + half * (kMtStep * 128), 16, 1024, kSwizzle128B);
+                const uint64_t b0 = tc_smem_desc(sbase + C::K + slot * C::STAGE, 16, 1024, kSwizzle128B);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)   // 16 channels (32 bytes) per MMA, 4 per 128-byte band
-                    tc_mma_f16_warp(tm_s + b * kMtStep, tc_desc_advance(desc_q, (kk >> 2) * C::BAND + (kk & 3) * 32),
-                                    tc_desc_advance(b0, (kk >> 2) * C::BAND + (kk & 3) * 32), idesc_qk, kk > 0 ? 1u : 0u);
+                    tc_mma_f16_warp(tm_s + b * kMtKeys, tc_desc_advance(desc_q, (kk >> 2) * C::QBAND + (kk & 3) * 32),
+                                    tc_desc_advance(b0, (kk >> 2) * C::KBAND + (kk & 3) * 32), idesc_qk, kk > 0 ? 1u : 0u);
                 tc_commit_warp(sfull(x, b));
-                if (tp.split || half == 1) tc_commit_warp(kfree(slot));
+                tc_commit_warp(kfree(slot));
                 return true;
             };
             bool go = true;
             for (Segment s = walk.next(); go && s.ok; s = walk.next()) {
-                const int n = s.k1 - s.k0;
+                const uint32_t n = s.k1 - s.k0;
                 // the second tile may hold no position: it only lets the key and value tiles go
                 if (!tp.split && s.unit * 2 * ppt + x * ppt >= p.n_pos) {
-                    for (int k = 0; go && k < n; ++k, ++kt) {
-                        const int slot = kt & 1;
-                        const uint32_t par = (kt >> 1) & 1;
+                    for (uint32_t k = 0; go && k < n; ++k, ++kt) {
+                        const int slot = kt % R;
+                        const uint32_t par = (kt / R) & 1;
                         go = wait(kfull(slot), par);
                         if (go && lane == 0) mbar_arrive(kfree(slot));
                         go = go && wait(vready(slot), par);
@@ -571,26 +729,26 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
                 if (!wait(qfull(x), seg & 1)) break;
                 ++seg;
                 tc_fence_after();
-                const uint32_t steps = tp.split ? n : 2 * n;
-                go = scores(kt, 0, it & 1) && (steps < 2 || scores(kt, 1, (it + 1) & 1));
+                // few rows: chain x takes the segment's tiles x, x + 2, ...
+                const uint32_t steps = tp.split ? (n + 1 - x) / 2 : n, stride = tp.split ? 2 : 1, t0 = kt + (tp.split ? x : 0);
+                if (steps > 0) go = scores(t0, it & 1);
+                if (go && steps > 1) go = scores(t0 + stride, (it + 1) & 1);
                 for (uint32_t i = 0; go && i < steps; ++i, ++it) {
-                    const uint32_t tile = kt + (tp.split ? i : i >> 1), slot = tile & 1, half = tp.split ? x : i & 1;
-                    const uint32_t b = it & 1, par = (it >> 1) & 1;
-                    if (((tp.split || half == 0) && !wait(vready(slot), (tile >> 1) & 1)) || !wait(pfull(x, b), par)) {
+                    const uint32_t tile = t0 + i * stride, slot = tile % R, b = it & 1, par = (it >> 1) & 1;
+                    if (!wait(vready(slot), (tile / R) & 1) || !wait(pfull(x, b), par)) {
                         go = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint64_t v0 = tc_smem_desc(sbase + C::V + slot * C::TILE + half * (kMtStep * 128), C::BAND, 1024,
-                                                     kSwizzle128B);
+                    const uint64_t v0 = tc_smem_desc(sbase + C::V + slot * C::STAGE, C::KBAND, 1024, kSwizzle128B);
 #pragma unroll
-                    for (int kk = 0; kk < kMtStep / 16; ++kk)   // 16 keys: 8 columns of P, 2048 bytes of value rows
-                        tc_mma_f16_tmem_a_warp(tm_o, tm_s + b * kMtStep + kk * 8, tc_desc_advance(v0, kk * 2048), idesc_pv,
+                    for (int kk = 0; kk < kMtKeys / 16; ++kk)   // 16 keys: 8 columns of P, 2048 bytes of value rows
+                        tc_mma_f16_tmem_a_warp(tm_o, tm_s + b * kMtKeys + kk * 8, tc_desc_advance(v0, kk * 2048), idesc_pv,
                                                (i > 0 || kk > 0) ? 1u : 0u);
-                    if (tp.split || half == 1) tc_commit_warp(vfree(slot));
+                    tc_commit_warp(vfree(slot));
                     tc_commit_warp(pvdone(x, b));
                     // the scores two steps on go over these weights, once the product has read them
-                    if (i + 2 < steps) go = wait(pvdone(x, b), par) && scores(kt, i + 2, b);
+                    if (i + 2 < steps) go = wait(pvdone(x, b), par) && scores(tile + 2 * stride, b);
                 }
                 kt += n;
             }
@@ -633,9 +791,23 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
                         ++cp;
                     }
                 }
+                if constexpr (C::QUANT) {   // times the key scales, rounded to f16, in the widened keys' order
+                    float sk[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) sk[j] = __ldg(p.s_k + static_cast<size_t>(s.head) * D + 8 * ch + j);
+#pragma unroll
+                    for (int i = 0; i < N; ++i) {
+                        const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+                        float f[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            f[widened_column<KIND>(j)] = ((j & 1) ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1])) * sk[j];
+                        q[i] = make_uint4(pack_f16(f[0], f[1]), pack_f16(f[2], f[3]), pack_f16(f[4], f[5]), pack_f16(f[6], f[7]));
+                    }
+                }
 #pragma unroll
                 for (int i = 0; i < N; ++i)
-                    sts128(sbase + C::Q + x * C::TILE + (ch >> 3) * C::BAND + sw128(row / N + STEP * i, ch & 7), q[i]);
+                    sts128(sbase + C::Q + x * C::QTILE + (ch >> 3) * C::QBAND + sw128(row / N + STEP * i, ch & 7), q[i]);
             }
             fence_proxy_async_smem();
             tc_fence_before();   // this thread's reads of the last segment's outputs
@@ -658,9 +830,9 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
             // scores in registers are raw, or already modified and in log2 units (bias, or a cap with a maximum)
             const bool ready = mp.capped || mp.alibi;
             const float mul = ready ? 1.f : p.scale_log2;
-            const int steps = tp.split ? s.k1 - s.k0 : 2 * (s.k1 - s.k0);
+            const int steps = tp.split ? (s.k1 - s.k0 + 1 - x) / 2 : s.k1 - s.k0;
             for (int i = 0; i < steps; ++i, ++it) {
-                const int b = it & 1, half = tp.split ? x : i & 1, tile = tp.split ? i : i >> 1;
+                const int b = it & 1, tile = tp.split ? 2 * i + x : i;
                 if (!wait(sfull(x, b), (it >> 1) & 1)) {
                     go = false;
                     break;
@@ -670,16 +842,16 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
                     mbar_arrive(pfull(x, b));
                     continue;
                 }
-                const uint32_t tsb = ts + b * kMtStep;
+                const uint32_t tsb = ts + b * kMtKeys;
                 uint32_t r0[32], r1[32];
                 tmem_ld32(tsb, r0);
                 tmem_ld32(tsb + 32, r1);
-                const int first = (s.k0 + tile) * kMtBlocks + half * kMtStepBlocks;   // the step's first virtual block
-                const bool one_run = first + kMtStepBlocks <= v.br.n && (first + kMtStepBlocks <= v.br.n0 || first >= v.br.n0);
+                const int first = (s.k0 + tile) * kMtBlocks;   // the tile's first virtual block
+                const bool one_run = first + kMtBlocks <= v.br.n && (first + kMtBlocks <= v.br.n0 || first >= v.br.n0);
                 const int t0 = v.br.at(first) * kBS;
-                const uint32_t loaded = mask_sh[(kt0 + tile) & 3] >> (half * kMtStepBlocks) & ((1u << kMtStepBlocks) - 1u);
-                const bool full = one_run && loaded == (1u << kMtStepBlocks) - 1u &&
-                                  ((t0 >= flo && t0 + kMtStep <= fhi) || (t0 >= fd && t0 + kMtStep <= fe));
+                const uint32_t loaded = mask_sh[(kt0 + tile) & 15];
+                const bool full = one_run && loaded == (1u << kMtBlocks) - 1u &&
+                                  ((t0 >= flo && t0 + kMtKeys <= fhi) || (t0 >= fd && t0 + kMtKeys <= fe));
                 // bit j of a 16-key block's mask: this row reads the block's key j
                 auto block_mask = [&](int b) -> uint32_t {
                     const int vb = first + b;
@@ -749,7 +921,7 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
                         for (int c = 0; c < 64; ++c) sv[c] = modified(mp, sv[c]);
                         if (mp.alibi) {
 #pragma unroll
-                            for (int b = 0; b < kMtStepBlocks; ++b) {
+                            for (int b = 0; b < kMtBlocks; ++b) {
                                 const int vb = min(first + b, max(v.br.n - 1, 0));
                                 const float away = static_cast<float>(pos - v.br.at(vb) * kBS);
 #pragma unroll
@@ -810,7 +982,7 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
                 tc_fence_before();
                 mbar_arrive(pfull(x, b));
             }
-            if (go) go = wait(pvdone(x, (it - 1) & 1), ((it - 1) >> 1) & 1);   // the segment's last product
+            if (go && steps > 0) go = wait(pvdone(x, (it - 1) & 1), ((it - 1) >> 1) & 1);   // the segment's last product
             // every thread of the query tile takes this vote once per segment, so the barriers below meet
             if (!tile_all(go, 4 + x)) {
                 timed_out = true;
@@ -831,13 +1003,26 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
             // finished rows go through the warp's quarter of the tile's query memory (its products are done;
             // 16-byte chunk c of row r at c ^ (r mod 8)), so that whole rows leave: a lane's row written
             // straight to global memory measured 2.8 us a unit against 1.3 us
-            const uint32_t stage = sbase + C::Q + x * C::TILE + (warp & 3) * (C::TILE / 4);
+            const uint32_t stage = sbase + C::Q + x * C::QTILE + (warp & 3) * (C::QTILE / 4);
 #pragma unroll
             for (int part = 0; part < D / 32; ++part) {
                 uint32_t o[32];
                 tmem_ld32(to + part * 32, o);
                 tmem_ld_wait(o);
                 if (!real) continue;
+                if constexpr (C::QUANT) {   // the channels' order, and the value scales
+                    uint32_t w[32];
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) w[c] = o[(c & ~7) + widened_column<KIND>(c & 7)];
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        const float4 sv = __ldg(reinterpret_cast<const float4 *>(p.s_v + static_cast<size_t>(s.head) * D + part * 32) + c);
+                        o[4 * c] = __float_as_uint(__uint_as_float(w[4 * c]) * sv.x);
+                        o[4 * c + 1] = __float_as_uint(__uint_as_float(w[4 * c + 1]) * sv.y);
+                        o[4 * c + 2] = __float_as_uint(__uint_as_float(w[4 * c + 2]) * sv.z);
+                        o[4 * c + 3] = __float_as_uint(__uint_as_float(w[4 * c + 3]) * sv.w);
+                    }
+                }
                 if (done) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
@@ -1009,8 +1194,28 @@ __global__ void __launch_bounds__(256) mod_tc_merge_kernel(const ModTcParams tp,
     if (dg == 0 && p.lse) p.lse[orow] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
-// The tensor-memory kernel for a head width (bf16 pools); fixed: capped scores against a fixed reference.
-DecodeKernel select_mod_tc(int D, bool fixed);
+template <int D, int KIND, bool FIXED>
+DecodeKernel mod_tc_instance()
+{
+    static DecodeKernel k = [] {
+        DecodeKernel r{nullptr, 0, 0};
+        const void *fn = reinterpret_cast<const void *>(&mod_tc_kernel<D, KIND, FIXED>);
+        r.fn = fn;
+        r.smem = ModTcCfg<D, KIND>::SMEM;
+        r.threads = kMtThreads;
+        r.tmap16 = KIND == KV_BF16;
+        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, r.smem) == cudaSuccess) {
+            int n = 0;
+            if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, kMtThreads, r.smem) == cudaSuccess) r.ctas_per_sm = n;
+        }
+        return r;
+    }();
+    return k;
+}
+
+// The tensor-memory kernel for a head width and pool kind; fixed: capped scores against a fixed reference.
+DecodeKernel select_mod_tc_bf16(int D, bool fixed);
+DecodeKernel select_mod_tc_quant(bool int4, bool fixed);
 const void *select_mod_tc_merge(int D, bool few);
 
 }  // namespace kvc

@@ -52,8 +52,15 @@ def visible(mod: Mod, i: int, p: int, total: int) -> np.ndarray:
     return see
 
 
-def attend(q, K, V, p, see, mod: Mod, scale, heads_per_kv, kind="bf16", split_weights=True):
-    """One query row: q [H_Q, D], K / V [T, H_KV, D] fp64, position p.  Returns out, lse and their error bounds."""
+# half step of a softmax weight as the operand of the value product: a bf16 high / low pair keeps 16 bits
+WEIGHTS = {"pair": 2.0 ** -16, "bf16": HALF["bf16"], "f16": HALF["f16"]}
+
+
+def attend(q, K, V, p, see, mod: Mod, scale, heads_per_kv, kind="bf16", weights="pair"):
+    """One query row: q [H_Q, D], K / V [T, H_KV, D] fp64, position p.  Returns out, lse and their error bounds.
+
+    weights: the type in which the kernel feeds the softmax weights to the value product.  Rounding every weight
+    by at most half a step h moves the mixture by at most h * sum w |v|, which is what the bound adds."""
     H_Q, D = q.shape
     out, lse = np.zeros((H_Q, D)), np.full(H_Q, -np.inf)
     tol_o, tol_l = np.zeros((H_Q, D)), np.zeros(H_Q)
@@ -85,10 +92,9 @@ def attend(q, K, V, p, see, mod: Mod, scale, heads_per_kv, kind="bf16", split_we
         ds += 4 * 2.0 ** -23 * float(np.max(np.abs(x)) + (np.max(np.abs(p - t)) * abs(float(mod.alibi[h]))
                                                          if mod.alibi is not None else 0.0))
         ds = ds * grow
-        # weights: their rounding as an operand (a bf16 high / low pair keeps 2^-16, one bf16 2^-8, f16
-        # 2^-11), the exponential's few steps, and the sum of t.size fp32 terms in any order
-        wr = 2.0 ** -16 if (kind == "bf16" and split_weights) else (HALF["bf16"] if kind == "bf16" else HALF["f16"])
-        rel = 2 * math.expm1(ds) + wr + 16 * 2.0 ** -23 + min(t.size, 4096) * 2.0 ** -23
+        # weights: their rounding as an operand, the exponential's few steps, and the sum of t.size fp32
+        # terms in any order
+        rel = 2 * math.expm1(ds) + WEIGHTS[weights] + 16 * 2.0 ** -23 + min(t.size, 4096) * 2.0 ** -23
         tol_o[h] = HALF["bf16"] * (np.abs(out[h]) + rel * ((w / L) @ np.abs(v))) + rel * ((w / L) @ np.abs(v)) + 2.0 ** -130
         tol_l[h] = math.expm1(ds) + (16 + min(t.size, 4096)) * 2.0 ** -23 + 4 * 2.0 ** -24 * abs(lse[h])
     return out, lse, tol_o, tol_l

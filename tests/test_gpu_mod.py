@@ -89,20 +89,28 @@ class Rows:
                                       mod=self.dev_mod(m), scale=self.scale, workspace=ws)
         return out, lse
 
-    def hold(self, out, lse, row, q, K, V, p, see, m, split_weights):
-        ro, rl, to, tl = attend(f64(q), K, V, p, see, m, self.scale, self.H_Q // self.H_KV, self.dtype, split_weights)
+    def hold(self, out, lse, row, q, K, V, p, see, m, weights):
+        ro, rl, to, tl = attend(f64(q), K, V, p, see, m, self.scale, self.H_Q // self.H_KV, self.dtype, weights)
         o, l = f64(out), f64(lse)
         assert np.array_equal(np.isneginf(l), np.isneginf(rl)), (row, l, rl)
         assert np.all(np.abs(o - ro) <= to), (row, float(np.max(np.abs(o - ro) - to)), float(np.max(np.abs(o - ro))))
         f = np.isfinite(rl)
         assert np.all(np.abs(l[f] - rl[f]) <= tl[f]), (row, l[f], rl[f], tl[f])
 
-    def check_decode(self, out, lse, m):
+    def decode_weights(self, workspace):
+        """The weights' operand type: groups of more than 16 heads run on the tensor-memory kernel (bf16 weights)
+        when there is a workspace, else the split kernel takes a pair (bf16 pools, up to 16 heads), one bf16 or f16."""
+        large = self.H_Q // self.H_KV > 16
+        if large and workspace:
+            return "bf16"
+        return "f16" if self.dtype != "bf16" else ("bf16" if large else "pair")
+
+    def check_decode(self, out, lse, m, workspace=True):
         torch.cuda.synchronize()
         assert self.kvc.kvc_pool_sync_status(self.pool) == self.kvc.KVC_OK
         for b, n in enumerate(self.lens):
             K, V = self.kv(b, n)
-            self.hold(out[b], lse[b], b, self.q[b], K, V, n - 1, visible(m, b, n - 1, n), m, self.H_Q // self.H_KV <= 16)
+            self.hold(out[b], lse[b], b, self.q[b], K, V, n - 1, visible(m, b, n - 1, n), m, self.decode_weights(workspace))
 
     def check_prefill(self, out, lse, m, q, q_start, row=0, some=None):
         torch.cuda.synchronize()
@@ -111,7 +119,7 @@ class Rows:
         K, V = self.kv(row, q_start + n_q)
         for i in range(n_q) if some is None else some:
             p = q_start + i
-            self.hold(out[i], lse[i], i, q[i], K, V, p, visible(m, i, p, q_start + n_q), m, False)
+            self.hold(out[i], lse[i], i, q[i], K, V, p, visible(m, i, p, q_start + n_q), m, "bf16")
 
     def queries(self, n):
         return bf16(self.r.standard_normal((n, self.H_Q, self.D)) * 2).cuda()
@@ -161,7 +169,7 @@ def test_decode_long_and_few(kvc, heads, mod):
             o2, l2 = c.decode(m, ws)
             assert torch.equal(out, o2) and torch.equal(lse, l2)
         assert not torch.any(ws[:65536])
-        c.check_decode(*c.decode(m, None), m)
+        c.check_decode(*c.decode(m, None), m, workspace=False)
     finally:
         c.close()
 
@@ -394,7 +402,7 @@ def test_write_then_attend(kvc):
         assert np.all(np.abs(K - kr) <= 2.0 ** -8 * (np.abs(kr) + kt) + kt) and np.array_equal(V, f64(v))
         for i in range(total):
             n = n0 if i < n0 else i + 1
-            ro, rl, to, tl = attend(got_q[i], K[:n], V[:n], i, visible(m, i, i, n), m, D ** -0.5, H_Q // H_KV, "bf16", i >= n0)
+            ro, rl, to, tl = attend(got_q[i], K[:n], V[:n], i, visible(m, i, i, n), m, D ** -0.5, H_Q // H_KV, "bf16", "pair" if i >= n0 else "bf16")
             assert np.all(np.abs(f64(out[i]) - ro) <= to) and np.all(np.abs(f64(lse[i]) - rl) <= tl), i
     finally:
         pool.close()
