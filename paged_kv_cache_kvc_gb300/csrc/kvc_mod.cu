@@ -185,9 +185,9 @@ static kvc_status run_tc(kvc_pool *pool, const ModParams &mp0, void *ws, size_t 
     tp.total = p.len_base + p.n_pos;
     tp.whole = !ws;
     tp.split = !tp.whole && (decode || p.n_pos <= p.ppu);
-    const bool fixed = tp.m.capped && !tp.m.alibi && tp.m.cap_out <= kMtCapLimit;
+    const bool fixed = pool->dtype == KVC_BF16 && tp.m.capped && !tp.m.alibi && tp.m.cap_out <= kMtCapLimit;
     const DecodeKernel k = pool->dtype == KVC_BF16 ? select_mod_tc_bf16(pool->D, fixed)
-                                                   : select_mod_tc_quant(pool->dtype == KVC_INT4, fixed);
+                                                   : select_mod_tc_quant(pool->dtype == KVC_INT4);
     if (!k.fn) return KVC_ERR_UNSUPPORTED;
     if (k.ctas_per_sm <= 0) return KVC_ERR_CUDA;
     const int unit = tp.split ? p.ppu : 2 * p.ppu;   // positions per unit
@@ -216,7 +216,7 @@ static kvc_status run_tc(kvc_pool *pool, const ModParams &mp0, void *ws, size_t 
             tp.part_ml = reinterpret_cast<float2 *>(tp.part_o + static_cast<size_t>(ctas) * 2 * 256 * pool->D);
         }
         void *args[] = {k.tmap16 ? &pool->tmap16 : &pool->tmap, &tp};
-        cudaError_t e = launch_dependent(k.fn, dim3(static_cast<unsigned>(ctas)), dim3(kMtThreads), k.smem, stream, args);
+        cudaError_t e = launch_dependent(k.fn, dim3(static_cast<unsigned>(ctas)), dim3(k.threads), k.smem, stream, args);
         if (e != cudaSuccess) return cuda_status(e);
         g_launches.fetch_add(1, std::memory_order_relaxed);
         if (!tp.whole && (tp.split || most > 1)) {

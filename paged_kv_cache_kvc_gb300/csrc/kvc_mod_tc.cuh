@@ -13,8 +13,10 @@
 //                     no row of the unit reads (a zero weight times NaN is NaN)
 //   warps 10, 11      MMA issuers of tile 0, 1
 // bf16 pools: warps 8 and 9 issue one 16-row TMA box per block and 128-byte band (one warp's boxes
-// issue ~40 ns apart, hence two warps).  e4m3 and int4 pools: warp 8 issues whole blocks of codes into
-// a third ring; warp 8 widens the landed keys to f16 and warp 9 the values to bf16, both exactly.  The
+// issue ~40 ns apart, hence two warps).  e4m3 and int4 pools: 512 threads, warp 8 issues whole blocks of
+// codes into a third ring, warps 12 and 13 widen the landed keys and 14 and 15 the values to f16,
+// exactly (one warp for each of the two took 800 and 2 000 cycles a tile, against 1 000 for the rest of
+// the work on it), and the softmax warps take registers over from the others.  The
 // queries are then q times the key scales, rounded to f16 (as in the split kernel), and the value
 // scales multiply the outputs.  int4 codes widen in the order 0, 4, 1, 5, 2, 6, 3, 7 of every eight
 // channels (two nibbles 16 bits apart are one mask): the queries are staged in that order, and the
@@ -33,12 +35,13 @@
 // Few rows (a chunk of at most 128 / g positions, a decode sequence): both chains take the same rows,
 // chain 0 every other tile and chain 1 the rest, and the merge joins them too.
 //
-// Weights.  With capped scores (and no bias) x lies in [-cap, cap], so the softmax needs no maximum:
-// 2^(x - cap / 2) fits fp32 and bf16 for caps up to 55 (80 in log2 units), and a score needs no
-// second look.  Otherwise a row's reference maximum moves when a score passes it by more than 8
-// (log2 units), and the row's outputs are rescaled in TMEM.  The weights enter the value product
-// as bf16 (their sum is taken before the rounding): a relative error of 2^-9 in each, independent,
-// which an output rounded to bf16 hides.
+// Weights.  On bf16 pools with capped scores (and no bias) x lies in [-cap, cap], so the softmax needs
+// no maximum: 2^(x - cap / 2) fits fp32 and bf16 for caps up to 55 (80 in log2 units), and a score
+// needs no second look.  Otherwise a row's reference maximum moves when a score passes it by more
+// than 8 (log2 units), and the row's outputs are rescaled in TMEM.  The weights enter the value
+// product as bf16 (f16 with e4m3 and int4 pools, where they stay under 2^8); their sum is taken before
+// the rounding: a relative error of at most 2^-8 in each, independent, which an output rounded to
+// bf16 hides.
 #pragma once
 #include "kvc_decode_tc.cuh"
 #include "kvc_mod.cuh"
@@ -47,7 +50,6 @@ namespace kvc {
 
 constexpr int kMtKeys = 64;                        // keys per tile
 constexpr int kMtBlocks = kMtKeys / kBS;
-constexpr int kMtThreads = 384;
 constexpr int kMtUnits = 2048;                     // most units (per head) of one launch
 constexpr int kMtStart = 4;                        // a unit's start, in tiles
 constexpr float kMtCapLimit = 80.f;                // cap in log2 units up to which no maximum is needed
@@ -68,6 +70,7 @@ struct ModTcParams {
 template <int D, int KIND>
 struct ModTcCfg {
     static constexpr bool QUANT = KIND != KV_BF16;
+    static constexpr int THREADS = QUANT ? 512 : 384;
     static constexpr int BANDS = D / 64;
     static constexpr int QBAND = 128 * 128;            // one 128-byte column band of 128 query rows
     static constexpr int QTILE = BANDS * QBAND;
@@ -83,35 +86,15 @@ struct ModTcCfg {
     static constexpr int PREFIX = C + R * RAW;         // int32 [kMtUnits + 1]
     static constexpr int BARS = PREFIX + ((kMtUnits + 1) * 4 + 15) / 16 * 16;
     static constexpr int NBARS = 7 * R + 14;
-    static constexpr int MISC = BARS + NBARS * 8;      // scan sums [12], abort, TMEM base, block masks [16]
-    static constexpr int SMEM = 1024 + MISC + 128;
+    static constexpr int MISC = BARS + NBARS * 8;      // scan sums [16], abort, TMEM base, block masks [16]
+    static constexpr int SMEM = 1024 + MISC + 160;
     static_assert(SMEM <= 232448, "shared memory of a CTA");
 };
 
-// Two f16 to two bf16 (through fp32; exact for e4m3 values).
-__device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t x)
-{
-    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&x));
-    return pack_bf16(f.x, f.y);
-}
-
-// Two nibbles, bits 0..3 and 16..19 of x (stored q + 8), to bf16x2 of q: 0x4300 | u is 128 + u, exact.
-__device__ __forceinline__ uint32_t nibbles_to_bf16x2(uint32_t x)
-{
-    const uint32_t biased = (x & 0x000F000Fu) | 0x43004300u;
-    uint32_t r;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(biased), "r"(0x43084308u));   // - (128 + 8)
-    return r;
-}
-
-// The eight nibbles of a word, widened to f16 (keys) or bf16 (values), in the order 0, 4, 1, 5, 2, 6, 3, 7.
-template <bool BF16>
+// The eight nibbles of a word (stored q + 8), widened to f16 in the order 0, 4, 1, 5, 2, 6, 3, 7.
 __device__ __forceinline__ uint4 widen_nibbles(uint32_t w)
 {
-    if constexpr (BF16)
-        return make_uint4(nibbles_to_bf16x2(w), nibbles_to_bf16x2(w >> 4), nibbles_to_bf16x2(w >> 8), nibbles_to_bf16x2(w >> 12));
-    else
-        return make_uint4(nibbles_to_f16x2(w), nibbles_hi_to_f16x2(w), nibbles_to_f16x2(w >> 8), nibbles_hi_to_f16x2(w >> 8));
+    return make_uint4(nibbles_to_f16x2(w), nibbles_hi_to_f16x2(w), nibbles_to_f16x2(w >> 8), nibbles_hi_to_f16x2(w >> 8));
 }
 
 // Column of a widened eight that holds channel e.
@@ -121,38 +104,54 @@ __host__ __device__ constexpr int widened_column(int e)
     return KIND != KV_INT4 ? e : (e < 4 ? 2 * e : 2 * (e - 4) + 1);
 }
 
-// One warp: the 64 key (VALUES = false) or value rows of a tile of codes, widened into a tile of 16-bit rows
-// (the 128-byte-swizzled bands that TMA writes for bf16 pools).  keep(row): false zeroes the row.
+// One warp: half of the 64 key (VALUES = false) or value rows of a tile of codes, widened into a tile of 16-bit rows
+// (the 128-byte-swizzled bands that TMA writes for bf16 pools).  keep(row): false zeroes the row.  A lane takes the
+// same 16-byte chunk of every 4th (e4m3) or 8th (int4) row, so that its addresses are a few bases with the swizzle
+// folded in by exclusive or, plus constants.
 template <int D, int KIND, bool VALUES, typename Keep>
-__device__ __forceinline__ void widen_tile(uint32_t codes, uint32_t wide, int lane, Keep keep)
+__device__ __forceinline__ void widen_half(uint32_t codes, uint32_t wide, int half, int lane, Keep keep)
 {
     using C = ModTcCfg<D, KIND>;
-    constexpr int N = DecodeCfg<D, KIND>::CHUNKS;   // 16-byte chunks of codes per row
-    constexpr int OUT = 128 / DecodeCfg<D, KIND>::BITS / 8;   // chunks of 8 widened channels from one: e4m3 2, int4 4
-    static_assert(OUT == (KIND == KV_INT4 ? 4 : 2) && OUT * N * 8 == D, "a row of codes is a row of channels");
-#pragma unroll 4
-    for (int i = lane; i < kMtKeys * N; i += 32) {
-        const int row = i / N, ch = i % N;
-        const uint4 x = lds128(codes + (row / kBS) * C::BLOCK + row_chunk<D, KIND>((VALUES ? kBS : 0) + row % kBS, ch));
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-        const bool ok = keep(row);
+    constexpr bool INT4 = KIND == KV_INT4;
+    static_assert(D == 128, "rows of 8 (e4m3) or 4 (int4) chunks of codes");
+    constexpr int N = INT4 ? 4 : 8, ROWS = 32 / N, ITEMS = kMtKeys / 2 / ROWS;   // chunks of a row, rows at a time
+    constexpr int OUT = INT4 ? 4 : 2;                                        // chunks of 8 widened channels from one
+    const int lr = lane / N, ch = lane % N;
+    // codes: row ROWS b + lr; int4 rows lie two to a 128-byte line (see swz, swz64)
+    const uint32_t src = codes + (INT4 ? (lr >> 1) * 128 + (((((lr & 1) << 2) + ch) ^ (lr >> 1)) << 4) : lr * 128 + ((ch ^ lr) << 4)) +
+                         (VALUES ? C::BLOCK / 2 : 0) + half * 2 * C::BLOCK;
+    const int c8 = OUT * ch;   // the first eight channels of the chunk
+    const uint32_t dst = wide + half * (kMtKeys / 2 * 128) + (c8 >> 3) * C::KBAND + lr * 128 + (((c8 & 7) ^ lr) << 4);
+    constexpr int PB = kBS / ROWS;   // rows at a time per block of 16
+    constexpr int LOADS = ITEMS < 8 ? ITEMS : 8;   // chunks in flight: one load at a time costs its latency
 #pragma unroll
-        for (int o = 0; o < OUT; ++o) {
-            uint4 y;
-            if constexpr (KIND == KV_INT4) {
-                y = widen_nibbles<VALUES>(w[o]);
-            } else {
-                uint32_t h[4];
-                e4m3x4_to_f16x2x2(w[2 * o], h[0], h[1]);
-                e4m3x4_to_f16x2x2(w[2 * o + 1], h[2], h[3]);
-                if constexpr (VALUES)
+    for (int b0 = 0; b0 < ITEMS; b0 += LOADS) {
+        uint4 x[LOADS];
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) h[u] = f16x2_to_bf16x2(h[u]);
-                y = make_uint4(h[0], h[1], h[2], h[3]);
+        for (int i = 0; i < LOADS; ++i) {
+            const int b = b0 + i;
+            x[i] = lds128((src ^ ((b & 1) ? 64u : 0u)) + (b / PB) * C::BLOCK + (b % PB) * 512);
+        }
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+            const int b = b0 + i;
+            const uint32_t to = (dst ^ (!INT4 && (b & 1) ? 64u : 0u)) + b * ROWS * 128;
+            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            const bool ok = keep(half * (kMtKeys / 2) + b * ROWS + lr);
+#pragma unroll
+            for (int o = 0; o < OUT; ++o) {
+                uint4 y;
+                if constexpr (INT4) {
+                    y = widen_nibbles(w[o]);
+                } else {
+                    uint32_t h[4];
+                    e4m3x4_to_f16x2x2(w[2 * o], h[0], h[1]);
+                    e4m3x4_to_f16x2x2(w[2 * o + 1], h[2], h[3]);
+                    y = make_uint4(h[0], h[1], h[2], h[3]);
+                }
+                if (!ok) y = make_uint4(0u, 0u, 0u, 0u);
+                sts128(to ^ (o << 4), y);
             }
-            if (!ok) y = make_uint4(0u, 0u, 0u, 0u);
-            const int c8 = OUT * ch + o;   // eight channels
-            sts128(wide + (c8 >> 3) * C::KBAND + sw128(row, c8 & 7), y);
         }
     }
 }
@@ -229,6 +228,21 @@ __device__ __forceinline__ float fast_rcp(float x)
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+// Four capped scores in log2 units, plus (top - cap): x = top - 2 cap / (1 + 2^u), u = s * in, out = -2 cap.
+// They share one reciprocal: 1 / a_i = (product of the others) / (product of all).  u is held under 30, where
+// x already equals cap in fp32, so that the product stays finite.
+__device__ __forceinline__ void capped4(f32x2 s01, f32x2 s23, f32x2 in, f32x2 out, f32x2 top, f32x2 &x01, f32x2 &x23)
+{
+    const f32x2 one = f32x2_of(1.f, 1.f), u01 = mul2(s01, in), u23 = mul2(s23, in);
+    const f32x2 a = add2(f32x2_of(fast_exp2(min_nan(lo2(u01), 30.f)), fast_exp2(min_nan(hi2(u01), 30.f))), one);
+    const f32x2 b = add2(f32x2_of(fast_exp2(min_nan(lo2(u23), 30.f)), fast_exp2(min_nan(hi2(u23), 30.f))), one);
+    const f32x2 ab = mul2(a, b);   // (a0 a2, a1 a3)
+    const float rc = fast_rcp(lo2(ab) * hi2(ab));
+    const f32x2 ri = mul2(f32x2_of(rc, rc), f32x2_of(hi2(ab), lo2(ab)));   // (1 / a0 a2, 1 / a1 a3)
+    x01 = fma2(mul2(ri, b), out, top);
+    x23 = fma2(mul2(ri, a), out, top);
+}
+
 // Chunk position c (decode: sequence c): its position, the positions its row holds, what it reads.
 struct RowView {
     int pos, total;
@@ -359,7 +373,7 @@ __device__ __forceinline__ int cta_of(int64_t w, int64_t W, int64_t G)
 // FIXED: capped scores against the fixed reference; else the running reference maximum.
 // tmap: the pool's map of 16-row boxes (bf16), else the map of whole blocks.
 template <int D, int KIND, bool FIXED>
-__global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_constant__ CUtensorMap tmap,
+__global__ void __launch_bounds__(ModTcCfg<D, KIND>::THREADS, 1) mod_tc_kernel(const __grid_constant__ CUtensorMap tmap,
                                                                 const ModTcParams tp)
 {
     using C = ModTcCfg<D, KIND>;
@@ -373,8 +387,8 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
     const uint32_t sbase = smem_u32(smem);
     int32_t *prefix = reinterpret_cast<int32_t *>(smem + C::PREFIX);
     int32_t *misc = reinterpret_cast<int32_t *>(smem + C::MISC);
-    volatile int32_t *abort_sh = misc + 12;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(misc + 13);
+    volatile int32_t *abort_sh = misc + 32;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(misc + 33);
     volatile uint32_t *mask_sh = reinterpret_cast<volatile uint32_t *>(misc + 16);   // loaded blocks of tile kt, place kt mod 16
     auto bar = [&](int i) { return sbase + C::BARS + 8u * static_cast<uint32_t>(i); };
     // barriers: per ring slot, then per query tile
@@ -392,13 +406,13 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
 
     if (tid == 0) {
         for (int s = 0; s < R; ++s) {
-            mbar_init(kfull(s), 1);
+            mbar_init(kfull(s), C::QUANT ? 2 : 1);   // the copy, or the warps that widen
             mbar_init(kfree(s), tp.split ? 1 : 2);   // the chains that take the tile
             mbar_init(vfull(s), 1);
             mbar_init(vfree(s), tp.split ? 1 : 2);
-            mbar_init(vready(s), 1);
+            mbar_init(vready(s), C::QUANT ? 2 : 1);
             mbar_init(cfull(s), 1);
-            mbar_init(cfree(s), 2);
+            mbar_init(cfree(s), 4);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(qfull(s), 128);
@@ -421,12 +435,12 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
 
     // ---- what each unit takes of the line, and the running sum
     if (mp.doc_start) {
-        for (int u = warp; u < tp.units; u += kMtThreads / 32) {
+        for (int u = warp; u < tp.units; u += C::THREADS / 32) {
             const UnitView v = unit_view(tp, u, lane);
             if (lane == 0) prefix[u + 1] = v.tiles + kMtStart;
         }
     } else {
-        for (int u = tid; u < tp.units; u += kMtThreads) {
+        for (int u = tid; u < tp.units; u += C::THREADS) {
             prefix[u + 1] = unit_tiles(tp, u) + kMtStart;
             if (p.lens && blockIdx.x == 0) {
                 const int n = __ldg(p.lens + u);
@@ -439,7 +453,7 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     {
-        const int per = (tp.units + kMtThreads - 1) / kMtThreads, b = tid * per, e = min(tp.units, b + per);
+        const int per = (tp.units + C::THREADS - 1) / C::THREADS, b = tid * per, e = min(tp.units, b + per);
         int sum = 0;
         for (int u = b; u < e; ++u) sum += prefix[u + 1];
         int inc = sum;
@@ -496,9 +510,10 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
     };
 
     if (warp >= 8) {
-        if (warp <= 9) {
-            // -------------------------------------------------------- keys (8) and values (9)
-            const bool values = warp == 9;
+        if constexpr (C::QUANT) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp <= 9 || warp >= 12) {
+            // -------------------------------------------------------- keys (8; 12, 13) and values (9; 14, 15)
+            const bool values = C::QUANT ? warp >= 14 : warp == 9;
             const int64_t row_layer = static_cast<int64_t>(p.layer) * p.N;
             const int bl = lane & (kMtBlocks - 1), band = lane / kMtBlocks;   // this lane's block of a tile (and band)
             uint32_t kt = 0;   // tiles so far
@@ -614,85 +629,75 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
                     for (uint32_t t = kt >= R ? kt - R : 0; t < kt; ++t)
                         (void)mbar_wait_bounded(values ? vfull(t % R) : kfull(t % R), (t / R) & 1, 100000000ull);
             } else {
-                // Warp 8 issues the codes of up to R tiles ahead of the one that both warps widen; `ahead` makes
-                // its own walk.
-                Walk far = walk;
-                Segment fs = far.next();
-                UnitView fv{};
-                int fk = fs.ok ? fs.k0 : 0;
-                if (!values && fs.ok) fv = unit_view(tp, fs.unit, lane);
-                uint32_t issued = 0;
-                auto issue = [&]() -> bool {   // the next tile's codes, if there is one
-                    if (!fs.ok) return true;
-                    const int slot = issued % R;
-                    if (issued >= R && !wait(cfree(slot), (issued / R - 1) & 1)) return false;
-                    const int vb = fk * kMtBlocks + bl;
-                    const int32_t e = entry(fs, fv, fk);
-                    const bool have = vb < fv.br.n, ok = have && valid(e);
-                    if (lane < kMtBlocks && have && !ok && is_read(fv, fv.br.at(vb) * kBS)) atomicOr(p.err, KVC_EBIT_BAD_BLOCK);
-                    const uint32_t mask = __ballot_sync(kFull, ok && lane < kMtBlocks);
-                    if (lane == 0) mask_sh[issued & 15] = mask;   // published by the arrive below
-                    if (p.stall_loads) {   // the test hook withholds every load
-                    } else if (lane == 0) {
-                        if (mask == 0u) mbar_arrive(cfull(slot));
-                        else mbar_arrive_expect_tx(cfull(slot), static_cast<uint32_t>(__popc(mask)) * C::BLOCK);
-                    }
-                    __syncwarp();
-                    if (lane < kMtBlocks && ok && !p.stall_loads)
-                        tma_load_2d(sbase + C::C + slot * C::RAW + bl * C::BLOCK, &tmap, cfull(slot), 0,
-                                    static_cast<int32_t>(((row_layer + e) * p.H_KV + fs.head) * DecodeCfg<D, KIND>::BOX_ROWS));
-                    ++issued;
-                    if (++fk == fs.k1) {
-                        const int unit = fs.unit;
-                        fs = far.next();
-                        if (fs.ok) {
-                            fk = fs.k0;
-                            if (fs.unit != unit) fv = unit_view(tp, fs.unit, lane);
+                if (warp == 8) {   // the codes
+                    for (Segment s = walk.next(); go && s.ok; s = walk.next()) {
+                        const UnitView v = unit_view(tp, s.unit, lane);
+                        int32_t e_next = entry(s, v, s.k0);
+                        for (int k = s.k0; k < s.k1; ++k, ++kt) {
+                            const int slot = kt % R;
+                            const int32_t e = e_next;
+                            e_next = entry(s, v, k + 1);
+                            if (kt >= R && !wait(cfree(slot), (kt / R - 1) & 1)) {
+                                go = false;
+                                break;
+                            }
+                            const int vb = k * kMtBlocks + bl;
+                            const bool have = vb < v.br.n, ok = have && valid(e);
+                            if (band == 0 && have && !ok && is_read(v, v.br.at(vb) * kBS)) atomicOr(p.err, KVC_EBIT_BAD_BLOCK);
+                            const uint32_t mask = __ballot_sync(kFull, ok && lane < kMtBlocks);
+                            if (lane == 0) mask_sh[kt & 15] = mask;   // published by the arrive below
+                            if (p.stall_loads) {   // the test hook withholds every load
+                            } else if (lane == 0) {
+                                if (mask == 0u) mbar_arrive(cfull(slot));
+                                else mbar_arrive_expect_tx(cfull(slot), static_cast<uint32_t>(__popc(mask)) * C::BLOCK);
+                            }
+                            __syncwarp();
+                            if (lane < kMtBlocks && ok && !p.stall_loads)
+                                tma_load_2d(sbase + C::C + slot * C::RAW + bl * C::BLOCK, &tmap, cfull(slot), 0,
+                                            static_cast<int32_t>(((row_layer + e) * p.H_KV + s.head) * DecodeCfg<D, KIND>::BOX_ROWS));
                         }
                     }
-                    return true;
-                };
-                if (!values)
-                    for (int i = 0; go && i < R - 1; ++i) go = issue();
-                for (Segment s = walk.next(); go && s.ok; s = walk.next()) {
-                    UnitView v{};
-                    if (values) v = unit_view(tp, s.unit, lane);
-                    for (int k = s.k0; k < s.k1; ++k, ++kt) {
-                        const int slot = kt % R;
-                        const uint32_t par = (kt / R) & 1;
-                        if (!values) go = issue();   // into the slot whose tile both warps widened last
-                        go = go && wait(cfull(slot), par);
-                        if (kt >= R) go = go && wait(values ? vfree(slot) : kfree(slot), (kt / R - 1) & 1);
-                        if (!go) break;
-                        const uint32_t codes = sbase + C::C + slot * C::RAW;
-                        if (!values) {
-                            widen_tile<D, KIND, false>(codes, sbase + C::K + slot * C::STAGE, lane, [](int) { return true; });
-                        } else {
-                            const uint32_t mask = mask_sh[kt & 15];
-                            if (is_clean(v, k, mask))
-                                widen_tile<D, KIND, true>(codes, sbase + C::V + slot * C::STAGE, lane, [](int) { return true; });
-                            else
-                                widen_tile<D, KIND, true>(codes, sbase + C::V + slot * C::STAGE, lane,
-                                                          [&](int row) { return is_used(v, k, mask, row); });
-                        }
-                        fence_proxy_async_smem();   // written here, read by the MMA; the codes' slot is rewritten by TMA
-                        __syncwarp();
-                        if (lane == 0) {
-                            mbar_arrive(values ? vready(slot) : kfull(slot));
-                            mbar_arrive(cfree(slot));
+                    // before the CTA ends: every copy issued has landed (immediate unless a wait expired)
+                    if (!p.stall_loads)
+                        for (uint32_t t = kt >= R ? kt - R : 0; t < kt; ++t)
+                            (void)mbar_wait_bounded(cfull(t % R), (t / R) & 1, 100000000ull);
+                } else if (warp >= 12) {
+                    const int half = warp & 1;
+                    for (Segment s = walk.next(); go && s.ok; s = walk.next()) {
+                        UnitView v{};
+                        if (values) v = unit_view(tp, s.unit, lane);
+                        for (int k = s.k0; k < s.k1; ++k, ++kt) {
+                            const int slot = kt % R;
+                            go = wait(cfull(slot), (kt / R) & 1);
+                            if (kt >= R) go = go && wait(values ? vfree(slot) : kfree(slot), (kt / R - 1) & 1);
+                            if (!go) break;
+                            const uint32_t codes = sbase + C::C + slot * C::RAW;
+                            if (!values) {
+                                widen_half<D, KIND, false>(codes, sbase + C::K + slot * C::STAGE, half, lane, [](int) { return true; });
+                            } else {
+                                const uint32_t mask = mask_sh[kt & 15];
+                                if (is_clean(v, k, mask))
+                                    widen_half<D, KIND, true>(codes, sbase + C::V + slot * C::STAGE, half, lane, [](int) { return true; });
+                                else
+                                    widen_half<D, KIND, true>(codes, sbase + C::V + slot * C::STAGE, half, lane,
+                                                              [&](int row) { return is_used(v, k, mask, row); });
+                            }
+                            fence_proxy_async_smem();   // written here, read by the MMA; the codes' slot is rewritten by TMA
+                            __syncwarp();
+                            if (lane == 0) {
+                                mbar_arrive(values ? vready(slot) : kfull(slot));
+                                mbar_arrive(cfree(slot));
+                            }
                         }
                     }
                 }
-                if (!values && !p.stall_loads)
-                    for (uint32_t t = issued >= R ? issued - R : 0; t < issued; ++t)
-                        (void)mbar_wait_bounded(cfull(t % R), (t / R) & 1, 100000000ull);
             }
             __syncwarp();
         } else {
             // -------------------------------------------------------- MMA issuer of query tile x
             const int x = warp - 10;
             constexpr uint32_t idesc_qk = tc_idesc_f16(128, kMtKeys, !C::QUANT, false, false);
-            constexpr uint32_t idesc_pv = tc_idesc_f16(128, D, true, false, true);
+            constexpr uint32_t idesc_pv = tc_idesc_f16(128, D, !C::QUANT, false, true);
             const uint64_t desc_q = tc_smem_desc(sbase + C::Q + x * C::QTILE, 16, 1024, kSwizzle128B);
             const uint32_t tm_s = tmem + 128 * x, tm_o = tmem + 256 + 128 * x;
             uint32_t kt = 0, it = 0, seg = 0;   // key tiles, this chain's steps and its segments so far
@@ -755,6 +760,7 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
         }
     } else {
         // ------------------------------------------------------------ softmax of query tile x
+        if constexpr (C::QUANT) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         const int x = warp >> 2, row = tid & 127;
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + 128 * x + lane_off, to = tmem + 256 + 128 * x + lane_off;
@@ -879,22 +885,14 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
                             r1[c] = seen1 >> c & 1u ? r1[c] : 0u;
                         }
                     }
-                    const f32x2 in = f32x2_of(mp.cap_in, mp.cap_in), one = f32x2_of(1.f, 1.f);
+                    const f32x2 in = f32x2_of(mp.cap_in, mp.cap_in);
                     const f32x2 out2 = f32x2_of(-2.f * mp.cap_out, -2.f * mp.cap_out), ref2 = f32x2_of(ref, ref);
 #pragma unroll
                     for (int c = 0; c < 64; c += 4) {
                         const uint32_t *sr = c < 32 ? r0 + c : r1 + (c - 32);
-                        // w = 2^(x - cap / 2), x = cap - 2 cap / (1 + 2^u): four scores share one reciprocal,
-                        // 1 / a_i = (product of the others) / (product of all).  u is held under 30, where
-                        // x already equals cap in fp32, so that the product stays finite.
-                        const f32x2 u01 = mul2(f32x2_of(__uint_as_float(sr[0]), __uint_as_float(sr[1])), in);
-                        const f32x2 u23 = mul2(f32x2_of(__uint_as_float(sr[2]), __uint_as_float(sr[3])), in);
-                        const f32x2 a = add2(f32x2_of(fast_exp2(min_nan(lo2(u01), 30.f)), fast_exp2(min_nan(hi2(u01), 30.f))), one);
-                        const f32x2 b = add2(f32x2_of(fast_exp2(min_nan(lo2(u23), 30.f)), fast_exp2(min_nan(hi2(u23), 30.f))), one);
-                        const f32x2 ab = mul2(a, b);   // (a0 a2, a1 a3)
-                        const float rc = fast_rcp(lo2(ab) * hi2(ab));
-                        const f32x2 ri = mul2(f32x2_of(rc, rc), f32x2_of(hi2(ab), lo2(ab)));   // (1 / a0 a2, 1 / a1 a3)
-                        const f32x2 x01 = fma2(mul2(ri, b), out2, ref2), x23 = fma2(mul2(ri, a), out2, ref2);
+                        f32x2 x01, x23;   // x - cap / 2
+                        capped4(f32x2_of(__uint_as_float(sr[0]), __uint_as_float(sr[1])),
+                                f32x2_of(__uint_as_float(sr[2]), __uint_as_float(sr[3])), in, out2, ref2, x01, x23);
                         float w0 = fast_exp2(lo2(x01)), w1 = fast_exp2(hi2(x01));
                         float w2 = fast_exp2(lo2(x23)), w3 = fast_exp2(hi2(x23));
                         if (!full) {
@@ -916,18 +914,37 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
                         sv[c] = __uint_as_float(r0[c]);
                         sv[32 + c] = __uint_as_float(r1[c]);
                     }
-                    if (ready) {
+                    if (mp.capped) {
+                        if (!full) {   // a hidden key's score may be anything, and would reach its group's reciprocal
 #pragma unroll
-                        for (int c = 0; c < 64; ++c) sv[c] = modified(mp, sv[c]);
-                        if (mp.alibi) {
-#pragma unroll
-                            for (int b = 0; b < kMtBlocks; ++b) {
-                                const int vb = min(first + b, max(v.br.n - 1, 0));
-                                const float away = static_cast<float>(pos - v.br.at(vb) * kBS);
-#pragma unroll
-                                for (int c = 0; c < kBS; ++c)
-                                    sv[kBS * b + c] = fmaf(-slope, fabsf(away - static_cast<float>(c)), sv[kBS * b + c]);
+                            for (int c = 0; c < 32; ++c) {
+                                sv[c] = seen0 >> c & 1u ? sv[c] : 0.f;
+                                sv[32 + c] = seen1 >> c & 1u ? sv[32 + c] : 0.f;
                             }
+                        }
+                        const f32x2 in = f32x2_of(mp.cap_in, mp.cap_in);
+                        const f32x2 out2 = f32x2_of(-2.f * mp.cap_out, -2.f * mp.cap_out), cap2 = f32x2_of(mp.cap_out, mp.cap_out);
+#pragma unroll
+                        for (int c = 0; c < 64; c += 4) {
+                            f32x2 x01, x23;
+                            capped4(f32x2_of(sv[c], sv[c + 1]), f32x2_of(sv[c + 2], sv[c + 3]), in, out2, cap2, x01, x23);
+                            sv[c] = lo2(x01);
+                            sv[c + 1] = hi2(x01);
+                            sv[c + 2] = lo2(x23);
+                            sv[c + 3] = hi2(x23);
+                        }
+                    } else if (ready) {
+#pragma unroll
+                        for (int c = 0; c < 64; ++c) sv[c] *= p.scale_log2;
+                    }
+                    if (mp.alibi) {
+#pragma unroll
+                        for (int b2 = 0; b2 < kMtBlocks; ++b2) {
+                            const int vb = min(first + b2, max(v.br.n - 1, 0));
+                            const float away = static_cast<float>(pos - v.br.at(vb) * kBS);
+#pragma unroll
+                            for (int c = 0; c < kBS; ++c)
+                                sv[kBS * b2 + c] = fmaf(-slope, fabsf(away - static_cast<float>(c)), sv[kBS * b2 + c]);
                         }
                     }
                     if (!full) {
@@ -972,7 +989,7 @@ __global__ void __launch_bounds__(kMtThreads, 1) mod_tc_kernel(const __grid_cons
                         const f32x2 e = fma2(f32x2_of(sv[c], sv[c + 1]), mul_2, neg2);
                         const float w0 = fast_exp2(lo2(e)), w1 = fast_exp2(hi2(e));
                         ls[(c / 2) & 3] = add2(ls[(c / 2) & 3], f32x2_of(w0, w1));
-                        pk[c / 2] = pack_bf16(w0, w1);
+                        pk[c / 2] = C::QUANT ? pack_f16(w0, w1) : pack_bf16(w0, w1);
                     }
                 }
                 const f32x2 lt = add2(add2(ls[0], ls[1]), add2(ls[2], ls[3]));
@@ -1202,11 +1219,11 @@ DecodeKernel mod_tc_instance()
         const void *fn = reinterpret_cast<const void *>(&mod_tc_kernel<D, KIND, FIXED>);
         r.fn = fn;
         r.smem = ModTcCfg<D, KIND>::SMEM;
-        r.threads = kMtThreads;
+        r.threads = ModTcCfg<D, KIND>::THREADS;
         r.tmap16 = KIND == KV_BF16;
         if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, r.smem) == cudaSuccess) {
             int n = 0;
-            if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, kMtThreads, r.smem) == cudaSuccess) r.ctas_per_sm = n;
+            if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, r.threads, r.smem) == cudaSuccess) r.ctas_per_sm = n;
         }
         return r;
     }();
@@ -1215,7 +1232,7 @@ DecodeKernel mod_tc_instance()
 
 // The tensor-memory kernel for a head width and pool kind; fixed: capped scores against a fixed reference.
 DecodeKernel select_mod_tc_bf16(int D, bool fixed);
-DecodeKernel select_mod_tc_quant(bool int4, bool fixed);
+DecodeKernel select_mod_tc_quant(bool int4);
 const void *select_mod_tc_merge(int D, bool few);
 
 }  // namespace kvc

@@ -97,20 +97,17 @@ class Rows:
         f = np.isfinite(rl)
         assert np.all(np.abs(l[f] - rl[f]) <= tl[f]), (row, l[f], rl[f], tl[f])
 
-    def decode_weights(self, workspace):
-        """The weights' operand type: groups of more than 16 heads run on the tensor-memory kernel (bf16 weights)
-        when there is a workspace, else the split kernel takes a pair (bf16 pools, up to 16 heads), one bf16 or f16."""
-        large = self.H_Q // self.H_KV > 16
-        if large and workspace:
-            return "bf16"
-        return "f16" if self.dtype != "bf16" else ("bf16" if large else "pair")
+    def decode_weights(self):
+        """The weights' operand type: f16 on e4m3 and int4 pools; on bf16 pools a pair for groups of up to 16 heads,
+        one bf16 for larger ones."""
+        return "f16" if self.dtype != "bf16" else ("bf16" if self.H_Q // self.H_KV > 16 else "pair")
 
-    def check_decode(self, out, lse, m, workspace=True):
+    def check_decode(self, out, lse, m):
         torch.cuda.synchronize()
         assert self.kvc.kvc_pool_sync_status(self.pool) == self.kvc.KVC_OK
         for b, n in enumerate(self.lens):
             K, V = self.kv(b, n)
-            self.hold(out[b], lse[b], b, self.q[b], K, V, n - 1, visible(m, b, n - 1, n), m, self.decode_weights(workspace))
+            self.hold(out[b], lse[b], b, self.q[b], K, V, n - 1, visible(m, b, n - 1, n), m, self.decode_weights())
 
     def check_prefill(self, out, lse, m, q, q_start, row=0, some=None):
         torch.cuda.synchronize()
@@ -119,7 +116,8 @@ class Rows:
         K, V = self.kv(row, q_start + n_q)
         for i in range(n_q) if some is None else some:
             p = q_start + i
-            self.hold(out[i], lse[i], i, q[i], K, V, p, visible(m, i, p, q_start + n_q), m, "bf16")
+            self.hold(out[i], lse[i], i, q[i], K, V, p, visible(m, i, p, q_start + n_q), m,
+                      "bf16" if self.dtype == "bf16" else "f16")
 
     def queries(self, n):
         return bf16(self.r.standard_normal((n, self.H_Q, self.D)) * 2).cuda()
@@ -169,7 +167,7 @@ def test_decode_long_and_few(kvc, heads, mod):
             o2, l2 = c.decode(m, ws)
             assert torch.equal(out, o2) and torch.equal(lse, l2)
         assert not torch.any(ws[:65536])
-        c.check_decode(*c.decode(m, None), m, workspace=False)
+        c.check_decode(*c.decode(m, None), m)
     finally:
         c.close()
 
