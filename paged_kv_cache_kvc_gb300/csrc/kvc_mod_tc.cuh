@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(ModTcCfg<D, KIND>::THREADS, 1) mod_tc_kernel(c
     };
 
     if (warp >= 8) {
-        if constexpr (C::QUANT) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if constexpr (C::QUANT) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (warp <= 9 || warp >= 12) {
             // -------------------------------------------------------- keys (8; 12, 13) and values (9; 14, 15)
             const bool values = C::QUANT ? warp >= 14 : warp == 9;
@@ -760,7 +760,7 @@ __global__ void __launch_bounds__(ModTcCfg<D, KIND>::THREADS, 1) mod_tc_kernel(c
         }
     } else {
         // ------------------------------------------------------------ softmax of query tile x
-        if constexpr (C::QUANT) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+        if constexpr (C::QUANT) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
         const int x = warp >> 2, row = tid & 127;
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + 128 * x + lane_off, to = tmem + 256 + 128 * x + lane_off;
@@ -772,10 +772,15 @@ __global__ void __launch_bounds__(ModTcCfg<D, KIND>::THREADS, 1) mod_tc_kernel(c
             const uint32_t kt0 = kt;
             kt += s.k1 - s.k0;
             const UnitView v = unit_view(tp, s.unit, lane);
-            const int c0 = v.pos0 + (tp.split ? 0 : x * ppt), c = c0 + row / g;   // chunk position of this row
+            const int c0 = v.pos0 + (tp.split ? 0 : x * ppt);
             const bool mine = c0 < p.n_pos;
-            const bool real = row < ppt * g && c < p.n_pos;
-            const size_t orow = static_cast<size_t>(c) * p.H_Q + s.head * g + row % g;
+            // up to 64 rows in a few-row call: chain 1's sit in the tile's upper half, so that the warps that have
+            // work to do are on different schedulers
+            const int ro = tp.split && x == 1 && min(ppt, p.n_pos - c0) * g <= 64 ? 64 : 0;
+            const int rq = row - ro;            // row of the query tile
+            const int c = c0 + max(rq, 0) / g;   // its chunk position
+            const bool real = rq >= 0 && rq < ppt * g && c < p.n_pos;
+            const size_t orow = static_cast<size_t>(c) * p.H_Q + s.head * g + max(rq, 0) % g;
             if (!mine) continue;   // the same for the whole CTA
             // ---- queries into shared memory (zero where there is none), every load in flight at once
             asm volatile("bar.sync %0, 128;" ::"r"(4 + x) : "memory");   // the last segment's rows have left it
@@ -813,7 +818,7 @@ __global__ void __launch_bounds__(ModTcCfg<D, KIND>::THREADS, 1) mod_tc_kernel(c
                 }
 #pragma unroll
                 for (int i = 0; i < N; ++i)
-                    sts128(sbase + C::Q + x * C::QTILE + (ch >> 3) * C::QBAND + sw128(row / N + STEP * i, ch & 7), q[i]);
+                    sts128(sbase + C::Q + x * C::QTILE + (ch >> 3) * C::QBAND + sw128((row / N + STEP * i + ro) & 127, ch & 7), q[i]);
             }
             fence_proxy_async_smem();
             tc_fence_before();   // this thread's reads of the last segment's outputs
@@ -825,7 +830,7 @@ __global__ void __launch_bounds__(ModTcCfg<D, KIND>::THREADS, 1) mod_tc_kernel(c
                 const RowView rv = row_view(tp, c);
                 r = rv.r;
                 pos = rv.pos;
-                if (mp.alibi) slope = __ldg(mp.alibi + s.head * g + row % g) * 1.4426950408889634f;
+                if (mp.alibi) slope = __ldg(mp.alibi + s.head * g + rq % g) * 1.4426950408889634f;
             }
             // every real row of the warp reads [flo, fhi) and [fd, fe)
             const int flo = __reduce_max_sync(kFull, real ? r.lo : 0), fhi = __reduce_min_sync(kFull, real ? r.hi : 0x7FFFFFFF);
@@ -1015,7 +1020,7 @@ __global__ void __launch_bounds__(ModTcCfg<D, KIND>::THREADS, 1) mod_tc_kernel(c
                 const int64_t end = static_cast<int64_t>(s.head) * walk.per_head + prefix[s.unit + 1];
                 cut = make_int4(s.head, s.unit, cta_of(end - 1, W, G) - static_cast<int>(blockIdx.x) + 1, static_cast<int>(slot));
             }
-            const int prow = x * 128 + row;
+            const int prow = x * 128 + rq;
             const float inv = l == 0.f ? 0.f : 1.f / l;
             // finished rows go through the warp's quarter of the tile's query memory (its products are done;
             // 16-byte chunk c of row r at c ^ (r mod 8)), so that whole rows leave: a lane's row written
