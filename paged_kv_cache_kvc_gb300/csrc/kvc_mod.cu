@@ -175,7 +175,7 @@ static int tc_min_group()
 
 // A chunk (or a decode batch of large head groups) on the tensor-memory kernel, as many units at a time as one
 // launch takes.
-static kvc_status run_tc(kvc_pool *pool, const ModParams &mp0, void *ws, size_t ws_bytes, cudaStream_t stream)
+static kvc_status run_tc(kvc_pool *pool, const ModParams &mp0, int visit, void *ws, size_t ws_bytes, cudaStream_t stream)
 {
     ModTcParams tp{};
     tp.m = mp0;
@@ -183,14 +183,21 @@ static kvc_status run_tc(kvc_pool *pool, const ModParams &mp0, void *ws, size_t 
     const bool decode = p.lens != nullptr;
     p.ppu = decode ? 1 : 128 / p.g;
     tp.total = p.len_base + p.n_pos;
-    tp.whole = !ws;
+    // Whole units or cut ones: in tiles (about 1.1 us each), a unit costs its tiles and kMtStart, and cutting costs
+    // the partials' way through memory and the merge's launch, together about 8.  Measured, capped: 64 queries at 0,
+    // 8 heads (whole) 8.4 us against 12.4 cut; 600 at 1 200 (cut) 38 against 43 whole.
+    const int64_t tiles = (visit + kMtBlocks - 1) / kMtBlocks + kMtStart;   // of the longest unit
+    const int64_t few_units = static_cast<int64_t>(p.H_KV) * (decode ? p.n_pos : (p.n_pos + 2 * p.ppu - 1) / (2 * p.ppu));
+    const int64_t sms = pool->num_sms;
+    tp.whole = !ws || (few_units + sms - 1) / sms * tiles <= few_units * tiles / sms + 8;
     tp.split = !tp.whole && (decode || p.n_pos <= p.ppu);
+    tp.single = decode && tp.whole;
     const bool fixed = pool->dtype == KVC_BF16 && tp.m.capped && !tp.m.alibi && tp.m.cap_out <= kMtCapLimit;
     const DecodeKernel k = pool->dtype == KVC_BF16 ? select_mod_tc_bf16(pool->D, fixed)
                                                    : select_mod_tc_quant(pool->dtype == KVC_INT4);
     if (!k.fn) return KVC_ERR_UNSUPPORTED;
     if (k.ctas_per_sm <= 0) return KVC_ERR_CUDA;
-    const int unit = tp.split ? p.ppu : 2 * p.ppu;   // positions per unit
+    const int unit = tp.split || tp.single ? p.ppu : 2 * p.ppu;   // positions per unit
     const int per_launch = kMtUnits * unit, n_q = p.n_pos, start = p.len_base;
     for (int at = 0; at < n_q; at += per_launch) {
         p.n_pos = std::min(per_launch, n_q - at);
@@ -204,8 +211,8 @@ static kvc_status run_tc(kvc_pool *pool, const ModParams &mp0, void *ws, size_t 
             p.bt = mp0.d.bt + static_cast<size_t>(at) * p.bt_stride;
         }
         tp.units = (p.n_pos + unit - 1) / unit;
-        // no more CTAs than the line of tiles can have tiles
-        const int64_t most = static_cast<int64_t>(p.H_KV) * tp.units * ((p.max_blocks + kMtBlocks - 1) / kMtBlocks + kMtStart);
+        // no more CTAs than units dealt whole, or places on the line
+        const int64_t most = static_cast<int64_t>(p.H_KV) * tp.units * (tp.whole ? 1 : (p.max_blocks + kMtBlocks - 1) / kMtBlocks + kMtStart);
         const int ctas = static_cast<int>(std::min<int64_t>(std::min(pool->num_sms, 512), most));
         if (!tp.whole) {
             if (ws_bytes < kCounterBytes + tc_bytes(ctas, pool->D)) return KVC_ERR_ARG;
@@ -219,7 +226,7 @@ static kvc_status run_tc(kvc_pool *pool, const ModParams &mp0, void *ws, size_t 
         cudaError_t e = launch_dependent(k.fn, dim3(static_cast<unsigned>(ctas)), dim3(k.threads), k.smem, stream, args);
         if (e != cudaSuccess) return cuda_status(e);
         g_launches.fetch_add(1, std::memory_order_relaxed);
-        if (!tp.whole && (tp.split || most > 1)) {
+        if (!tp.whole) {
             const int rows = std::min(p.ppu, p.n_pos) * p.g, per = 128 / pool->D;
             const dim3 grid = tp.split ? dim3((rows + per - 1) / per, tp.units, p.H_KV) : dim3(8, ctas);
             void *margs[] = {&tp, const_cast<int *>(&ctas)};
@@ -338,7 +345,7 @@ extern "C" kvc_status kvc_decode_attn_mod(kvc_pool *pool, int32_t layer, const v
     mp.d.n_pos = B;
     // Large head groups: one tensor-memory step serves the whole group
     if (workspace && use_tc(pool) && mp.d.g >= tc_min_group())
-        return run_tc(pool, mp, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+        return run_tc(pool, mp, most_blocks(mod, 1, max_blocks), workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
     return run_split(pool, mp, select(pool, mp.d.g, false), most_blocks(mod, 1, max_blocks), workspace, workspace_bytes,
                      static_cast<cudaStream_t>(stream));
 }
@@ -359,7 +366,8 @@ extern "C" kvc_status kvc_prefill_attn_mod(kvc_pool *pool, int32_t layer, const 
     DecodeParams &p = mp.d;
     p.len_base = q_start;
     p.n_pos = n_q;
-    if (use_tc(pool)) return run_tc(pool, mp, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+    if (use_tc(pool))
+        return run_tc(pool, mp, most_blocks(mod, 256 / p.g, blocks), workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
     p.ppu = unit_positions(p.g, true);
     p.B = (n_q + p.ppu - 1) / p.ppu;
     return run_split(pool, mp, select(pool, p.ppu * p.g, true), most_blocks(mod, p.ppu, blocks), workspace, workspace_bytes,

@@ -32,6 +32,9 @@
 // adds them in CTA order.  (Merged by the unit's last CTA instead, 600 queries of 1800 positions took
 // 43 us, 20 pieces of a 5-query chunk 9 us of its 36: one SM's loads against all SMs'.)
 //
+// Short units (little more than the start and the merge they would cost) are dealt whole instead, one
+// after the other, and nothing is merged.
+//
 // Few rows (a chunk of at most 128 / g positions, a decode sequence): both chains take the same rows,
 // chain 0 every other tile and chain 1 the rest, and the merge joins them too.
 //
@@ -59,6 +62,7 @@ struct ModTcParams {
     int32_t units;        // units per head
     int32_t whole;        // 1: no partials, units are dealt whole
     int32_t split;        // 1: a unit is one query tile's positions, and both chains take its rows (below)
+    int32_t single;       // 1: a unit is one query tile's positions, and chain 0 takes them
     int32_t total;        // positions the row holds (prefill)
     int32_t *prefix;      // few-row calls: [units + 1] place of each unit on a head's line, for the merge
     int4 *cuts;           // other calls: [G] {head, unit, pieces (0: none), slot} of the unit that CTA c starts
@@ -266,6 +270,11 @@ __device__ __forceinline__ RowView row_view(const ModTcParams &p, int c)
     return v;
 }
 
+__device__ __forceinline__ int unit_positions_of(const ModTcParams &p)
+{
+    return p.split || p.single ? p.m.d.ppu : 2 * p.m.d.ppu;
+}
+
 // What a unit reads; the same in every thread of a warp.
 struct UnitView {
     int pos0, n_pos;       // chunk positions [pos0, pos0 + n_pos)
@@ -278,7 +287,7 @@ struct UnitView {
 __device__ __forceinline__ UnitView unit_view(const ModTcParams &p, int u, int lane)
 {
     const DecodeParams &d = p.m.d;
-    const int ppu = p.split ? d.ppu : 2 * d.ppu;
+    const int ppu = unit_positions_of(p);
     UnitView v;
     v.pos0 = u * ppu;
     v.n_pos = min(ppu, d.n_pos - v.pos0);
@@ -308,7 +317,7 @@ __device__ __forceinline__ UnitView unit_view(const ModTcParams &p, int u, int l
 // The same count of tiles without documents, one thread.
 __device__ __forceinline__ int unit_tiles(const ModTcParams &p, int u)
 {
-    const int ppu = p.split ? p.m.d.ppu : 2 * p.m.d.ppu, c = u * ppu;
+    const int ppu = unit_positions_of(p), c = u * ppu;
     const Range f = row_view(p, c).r, l = row_view(p, min(c + ppu, p.m.d.n_pos) - 1).r;
     const bool fe = f.e > f.d, le = l.e > l.d;
     const BlockRuns br = block_runs(le ? (fe ? min(f.d, l.d) : l.d) : 0, le ? l.e : 0, f.lo, l.hi);
@@ -337,9 +346,8 @@ struct Walk {
         if (whole) {
             s.head = static_cast<int>(at / units);
             s.unit = static_cast<int>(at % units);
-            s.tiles = prefix[s.unit + 1] - prefix[s.unit] - kMtStart;
             s.k0 = 0;
-            s.k1 = s.tiles;
+            s.tiles = s.k1 = 0;   // the caller's: see unit_of
             at += stride;
             return s;
         }
@@ -361,6 +369,14 @@ struct Walk {
         return s;
     }
 };
+
+// The view of a segment's unit; a whole unit's segment gets its tiles from it.
+__device__ __forceinline__ UnitView unit_of(const ModTcParams &p, Segment &s, int lane)
+{
+    const UnitView v = unit_view(p, s.unit, lane);
+    if (p.whole) s.tiles = s.k1 = v.tiles;
+    return v;
+}
 
 // The CTA that has place w of a line of W shared by G: the last c with c W / G <= w.
 __device__ __forceinline__ int cta_of(int64_t w, int64_t W, int64_t G)
@@ -434,7 +450,8 @@ __global__ void __launch_bounds__(ModTcCfg<D, KIND>::THREADS, 1) mod_tc_kernel(c
     grid_dependency_wait();
 
     // ---- what each unit takes of the line, and the running sum
-    if (mp.doc_start) {
+    if (tp.whole) {   // no line
+    } else if (mp.doc_start) {
         for (int u = warp; u < tp.units; u += C::THREADS / 32) {
             const UnitView v = unit_view(tp, u, lane);
             if (lane == 0) prefix[u + 1] = v.tiles + kMtStart;
@@ -442,17 +459,18 @@ __global__ void __launch_bounds__(ModTcCfg<D, KIND>::THREADS, 1) mod_tc_kernel(c
     } else {
         for (int u = tid; u < tp.units; u += C::THREADS) {
             prefix[u + 1] = unit_tiles(tp, u) + kMtStart;
-            if (p.lens && blockIdx.x == 0) {
-                const int n = __ldg(p.lens + u);
-                if (n < 0 || static_cast<int64_t>(n) > static_cast<int64_t>(p.max_blocks) * kBS) atomicOr(p.err, KVC_EBIT_RANGE);
-            }
         }
     }
+    if (p.lens && blockIdx.x == 0)
+        for (int u = tid; u < tp.units; u += C::THREADS) {
+            const int n = __ldg(p.lens + u);
+            if (n < 0 || static_cast<int64_t>(n) > static_cast<int64_t>(p.max_blocks) * kBS) atomicOr(p.err, KVC_EBIT_RANGE);
+        }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    {
+    if (!tp.whole) {
         const int per = (tp.units + C::THREADS - 1) / C::THREADS, b = tid * per, e = min(tp.units, b + per);
         int sum = 0;
         for (int u = b; u < e; ++u) sum += prefix[u + 1];
@@ -480,7 +498,7 @@ __global__ void __launch_bounds__(ModTcCfg<D, KIND>::THREADS, 1) mod_tc_kernel(c
     Walk walk;
     walk.prefix = prefix;
     walk.units = tp.units;
-    walk.per_head = prefix[tp.units];
+    walk.per_head = tp.whole ? 1 : prefix[tp.units];
     walk.whole = tp.whole != 0;
     walk.stride = gridDim.x;
     const int64_t W = static_cast<int64_t>(p.H_KV) * walk.per_head;
@@ -526,19 +544,32 @@ __global__ void __launch_bounds__(ModTcCfg<D, KIND>::THREADS, 1) mod_tc_kernel(c
                 return one_run && mask == (1u << kMtBlocks) - 1u && !mp.doc_start &&
                        ((t0 >= v.a0 && t0 + kMtKeys <= v.a1) || (t0 >= v.e0 && t0 + kMtKeys <= v.e1));
             };
-            auto is_used = [&](const UnitView &v, int k, uint32_t mask, int row) {
-                const int vb = k * kMtBlocks + row / kBS;
-                if (vb >= v.br.n || !(mask >> (row / kBS) & 1u)) return false;
-                const int t = v.br.at(vb) * kBS + row % kBS;
-                // rows at consecutive positions read consecutive runs, so without documents the union
-                // has no holes; with them each row of the unit is asked
-                if (!((t >= v.a0 && t < v.a1) || (t >= v.e0 && t < v.e1))) return false;
-                if (!mp.doc_start) return true;
-                for (int i = 0; i < v.n_pos; ++i) {
-                    const Range r = row_view(tp, v.pos0 + i).r;
-                    if ((t >= r.lo && t < r.hi) || (t >= r.d && t < r.e)) return true;
+            // which of tile k's value rows some row of the unit reads: bit row (whole warp)
+            auto used_rows = [&](const UnitView &v, int k, uint32_t mask) -> uint64_t {
+                const int first = k * kMtBlocks;
+                uint32_t m[2] = {0u, 0u};
+                auto add = [&](int lo, int hi) {   // positions [lo, hi)
+#pragma unroll
+                    for (int b = 0; b < kMtBlocks; ++b) {
+                        if (first + b >= v.br.n || !(mask >> b & 1u)) continue;
+                        const int t = v.br.at(first + b) * kBS;
+                        auto below = [&](int end) -> uint32_t { return end <= t ? 0u : (end >= t + kBS ? 0xFFFFu : (1u << (end - t)) - 1u); };
+                        m[b >> 1] |= (below(hi) & ~below(lo)) << (16 * (b & 1));
+                    }
+                };
+                if (!mp.doc_start) {   // rows at consecutive positions read consecutive runs: their union has no holes
+                    add(v.a0, v.a1);
+                    add(v.e0, v.e1);
+                } else {
+                    for (int i = lane; i < v.n_pos; i += 32) {
+                        const Range r = row_view(tp, v.pos0 + i).r;
+                        add(r.lo, r.hi);
+                        add(r.d, r.e);
+                    }
+                    m[0] = __reduce_or_sync(kFull, m[0]);
+                    m[1] = __reduce_or_sync(kFull, m[1]);
                 }
-                return false;
+                return m[0] | static_cast<uint64_t>(m[1]) << 32;
             };
             auto is_read = [&](const UnitView &v, int t) {   // some row of the unit reads a position of block [t, t + 16)
                 for (int i = 0; i < v.n_pos; ++i) {
@@ -565,8 +596,9 @@ __global__ void __launch_bounds__(ModTcCfg<D, KIND>::THREADS, 1) mod_tc_kernel(c
                     if (!wait(vfull(prev_slot), prev_parity)) return false;
                     if (!is_clean(pv, prev_tile, prev_mask)) {
                         const uint32_t st = sbase + C::V + prev_slot * C::STAGE;
+                        const uint64_t used = used_rows(pv, prev_tile, prev_mask);
                         for (int k = lane; k < kMtKeys; k += 32)
-                            if (!is_used(pv, prev_tile, prev_mask, k))
+                            if (!(used >> k & 1u))
 #pragma unroll
                                 for (int c = 0; c < 8 * C::BANDS; ++c)
                                     sts128_zero(st + (c >> 3) * C::KBAND + sw128(k, c & 7));
@@ -578,7 +610,7 @@ __global__ void __launch_bounds__(ModTcCfg<D, KIND>::THREADS, 1) mod_tc_kernel(c
                     return true;
                 };
                 for (Segment s = walk.next(); go && s.ok; s = walk.next()) {
-                    v = unit_view(tp, s.unit, lane);
+                    v = unit_of(tp, s, lane);
                     int32_t e_next = entry(s, v, s.k0);
                     for (int k = s.k0; k < s.k1; ++k, ++kt) {
                         const int slot = kt % R;
@@ -631,7 +663,7 @@ __global__ void __launch_bounds__(ModTcCfg<D, KIND>::THREADS, 1) mod_tc_kernel(c
             } else {
                 if (warp == 8) {   // the codes
                     for (Segment s = walk.next(); go && s.ok; s = walk.next()) {
-                        const UnitView v = unit_view(tp, s.unit, lane);
+                        const UnitView v = unit_of(tp, s, lane);
                         int32_t e_next = entry(s, v, s.k0);
                         for (int k = s.k0; k < s.k1; ++k, ++kt) {
                             const int slot = kt % R;
@@ -664,8 +696,7 @@ __global__ void __launch_bounds__(ModTcCfg<D, KIND>::THREADS, 1) mod_tc_kernel(c
                 } else if (warp >= 12) {
                     const int half = warp & 1;
                     for (Segment s = walk.next(); go && s.ok; s = walk.next()) {
-                        UnitView v{};
-                        if (values) v = unit_view(tp, s.unit, lane);
+                        const UnitView v = unit_of(tp, s, lane);
                         for (int k = s.k0; k < s.k1; ++k, ++kt) {
                             const int slot = kt % R;
                             go = wait(cfull(slot), (kt / R) & 1);
@@ -678,9 +709,11 @@ __global__ void __launch_bounds__(ModTcCfg<D, KIND>::THREADS, 1) mod_tc_kernel(c
                                 const uint32_t mask = mask_sh[kt & 15];
                                 if (is_clean(v, k, mask))
                                     widen_half<D, KIND, true>(codes, sbase + C::V + slot * C::STAGE, half, lane, [](int) { return true; });
-                                else
+                                else {
+                                    const uint64_t used = used_rows(v, k, mask);
                                     widen_half<D, KIND, true>(codes, sbase + C::V + slot * C::STAGE, half, lane,
-                                                              [&](int row) { return is_used(v, k, mask, row); });
+                                                              [=](int row) { return (used >> row & 1u) != 0; });
+                                }
                             }
                             fence_proxy_async_smem();   // written here, read by the MMA; the codes' slot is rewritten by TMA
                             __syncwarp();
@@ -717,9 +750,10 @@ __global__ void __launch_bounds__(ModTcCfg<D, KIND>::THREADS, 1) mod_tc_kernel(c
             };
             bool go = true;
             for (Segment s = walk.next(); go && s.ok; s = walk.next()) {
+                if (tp.whole) (void)unit_of(tp, s, lane);
                 const uint32_t n = s.k1 - s.k0;
                 // the second tile may hold no position: it only lets the key and value tiles go
-                if (!tp.split && s.unit * 2 * ppt + x * ppt >= p.n_pos) {
+                if (!tp.split && (tp.single ? x == 1 : s.unit * 2 * ppt + x * ppt >= p.n_pos)) {
                     for (uint32_t k = 0; go && k < n; ++k, ++kt) {
                         const int slot = kt % R;
                         const uint32_t par = (kt / R) & 1;
@@ -770,10 +804,10 @@ __global__ void __launch_bounds__(ModTcCfg<D, KIND>::THREADS, 1) mod_tc_kernel(c
         int4 cut = make_int4(0, 0, 0, 0);
         for (Segment s = walk.next(); s.ok; s = walk.next(), ++piece) {
             const uint32_t kt0 = kt;
+            const UnitView v = unit_of(tp, s, lane);
             kt += s.k1 - s.k0;
-            const UnitView v = unit_view(tp, s.unit, lane);
-            const int c0 = v.pos0 + (tp.split ? 0 : x * ppt);
-            const bool mine = c0 < p.n_pos;
+            const int c0 = v.pos0 + (tp.split || tp.single ? 0 : x * ppt);
+            const bool mine = c0 < p.n_pos && !(tp.single && x == 1);
             // up to 64 rows in a few-row call: chain 1's sit in the tile's upper half, so that the warps that have
             // work to do are on different schedulers
             const int ro = tp.split && x == 1 && min(ppt, p.n_pos - c0) * g <= 64 ? 64 : 0;
@@ -1138,7 +1172,7 @@ __global__ void __launch_bounds__(256) mod_tc_merge_kernel(const ModTcParams tp,
         n = (cl - cf + 1) * 2;
         slot0 = 2 * cf + (a > 0 && cta_of(a - 1, W, G) == cf ? 1 : 0);   // places before the unit: its second piece
     }
-    const int c = unit * (tp.split ? p.ppu : 2 * p.ppu) + pr;
+    const int c = unit * unit_positions_of(tp) + pr;
     const bool real = r < p.ppu * g && c < p.n_pos;
     if (T == 1 && !real) return;
     // piece t: slot * 256 + row in it (few rows: chain t mod 2 of CTA t / 2)
