@@ -428,9 +428,15 @@ KVC_API kvc_status kvc_decode_attn_mod(kvc_pool *pool, int32_t layer, const void
 
 /* kvc_prefill_attn with modified scores: query i sits at position q_start + i,
  * and the row holds q_start + n_q positions.  out, lse, scale and workspace as
- * kvc_decode_attn_mod; a value row that some query of a call reads must be
- * finite for the call's other queries of the same chunk to be.  Other
- * arguments, requirements and errors as kvc_prefill_attn. */
+ * kvc_decode_attn_mod.  Positions that no query of the call reads may hold
+ * anything.  A key or value of a position that some query reads and another
+ * does not (the causal diagonal, a window's edge, another document of the
+ * chunk) never weighs in the other's result while it is finite; a NaN or
+ * infinite value there may turn the other's output into NaN too, as it does in
+ * a product with zero weights (NaN keys do not).  The kernels run on the
+ * tensor cores' tensor memory; the environment variable KVC_TC=0 selects the
+ * warp-level kernel.  Other arguments, requirements and errors as
+ * kvc_prefill_attn. */
 KVC_API kvc_status kvc_prefill_attn_mod(kvc_pool *pool, int32_t layer, const void *q, int32_t n_q,
                                         int32_t num_q_heads, const int32_t *block_table_row, int32_t max_blocks,
                                         int32_t q_start, const kvc_score_mod *mod, void *out, float *lse, float scale,

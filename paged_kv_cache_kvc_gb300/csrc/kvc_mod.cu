@@ -167,11 +167,11 @@ static bool use_tc(const kvc_pool *pool)
     return !(e && e[0] == '0') && (pool->dtype != KVC_BF16 || pool->tmap16_ok);   // the other map is checked for every call
 }
 
-static int tc_min_group()
-{
-    const char *e = std::getenv("KVC_TC_GROUP");
-    return e ? std::atoi(e) : 17;
-}
+// Decode groups of query heads from which the tensor-memory kernel serves a step.  Measured, capped, 32 heads: 8 x
+// 32 768 positions bf16 39 us against the split kernel's 44, e4m3 43 / 44, int4 51 / 53; 1 x 32 768: 32 / 37, 36 / 38,
+// 34 / 43; 64 x 1 000: 29 / 40, 38 / 39, 40 / 47.  Smaller groups: 8 heads, 8 x 8 192 x 4 KV heads 36 / 31; 16 heads
+// (bf16, whose weights the split kernel feeds as 16 bits), 8 x 8 192 x 2: 24 / 21.
+constexpr int kTcGroup = 17;
 
 // A chunk (or a decode batch of large head groups) on the tensor-memory kernel, as many units at a time as one
 // launch takes.
@@ -344,7 +344,7 @@ extern "C" kvc_status kvc_decode_attn_mod(kvc_pool *pool, int32_t layer, const v
     mp.d.ppu = 1;
     mp.d.n_pos = B;
     // Large head groups: one tensor-memory step serves the whole group
-    if (workspace && use_tc(pool) && mp.d.g >= tc_min_group())
+    if (workspace && use_tc(pool) && mp.d.g >= kTcGroup)
         return run_tc(pool, mp, most_blocks(mod, 1, max_blocks), workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
     return run_split(pool, mp, select(pool, mp.d.g, false), most_blocks(mod, 1, max_blocks), workspace, workspace_bytes,
                      static_cast<cudaStream_t>(stream));

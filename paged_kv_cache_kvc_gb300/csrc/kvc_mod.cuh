@@ -22,6 +22,8 @@
 // at (a serving engine frees them).  Blocks that some column may not read in
 // full mask per column; the other blocks mask nothing.
 #pragma once
+#include <mutex>
+
 #include "kvc_decode.cuh"
 
 namespace kvc {
@@ -676,21 +678,34 @@ __global__ void __launch_bounds__(kThreads) mod_kernel(const __grid_constant__ C
     if (threadIdx.x == 0) p.counters[static_cast<size_t>(b) * p.H_KV + h] = 0u;   // ready for the next call
 }
 
+// A kernel with its dynamic shared memory, configured once on every device that it runs on.  Tag: one per kernel.
+template <typename Tag>
+DecodeKernel configured(const void *fn, int smem, int threads, bool tmap16)
+{
+    constexpr int kDevices = 64;
+    static std::once_flag once[kDevices];
+    static DecodeKernel kernels[kDevices];
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return DecodeKernel{nullptr, 0, 0};
+    std::call_once(once[dev], [&] {
+        DecodeKernel &k = kernels[dev];
+        k = DecodeKernel{fn, smem, 0};
+        k.threads = threads;
+        k.tmap16 = tmap16;
+        int n = 0;
+        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess &&
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, threads, smem) == cudaSuccess)
+            k.ctas_per_sm = n;
+    });
+    return kernels[dev];
+}
+
 template <int D, int NT, int KIND, bool PSPLIT, bool TILE>
 DecodeKernel mod_instance()
 {
-    static DecodeKernel k = [] {
-        DecodeKernel r{nullptr, 0, 0};
-        const void *fn = reinterpret_cast<const void *>(&mod_kernel<D, NT, KIND, PSPLIT, TILE>);
-        r.fn = fn;
-        r.smem = mod_smem_bytes<D, NT, KIND>();
-        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, r.smem) == cudaSuccess) {
-            int n = 0;
-            if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, kThreads, r.smem) == cudaSuccess) r.ctas_per_sm = n;
-        }
-        return r;
-    }();
-    return k;
+    struct Tag {};
+    return configured<Tag>(reinterpret_cast<const void *>(&mod_kernel<D, NT, KIND, PSPLIT, TILE>),
+                           mod_smem_bytes<D, NT, KIND>(), kThreads, false);
 }
 
 // The split kernel's instance for a pool kind, head width and columns per unit (fn = nullptr: none).

@@ -1253,20 +1253,9 @@ __global__ void __launch_bounds__(256) mod_tc_merge_kernel(const ModTcParams tp,
 template <int D, int KIND, bool FIXED>
 DecodeKernel mod_tc_instance()
 {
-    static DecodeKernel k = [] {
-        DecodeKernel r{nullptr, 0, 0};
-        const void *fn = reinterpret_cast<const void *>(&mod_tc_kernel<D, KIND, FIXED>);
-        r.fn = fn;
-        r.smem = ModTcCfg<D, KIND>::SMEM;
-        r.threads = ModTcCfg<D, KIND>::THREADS;
-        r.tmap16 = KIND == KV_BF16;
-        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, r.smem) == cudaSuccess) {
-            int n = 0;
-            if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, r.threads, r.smem) == cudaSuccess) r.ctas_per_sm = n;
-        }
-        return r;
-    }();
-    return k;
+    struct Tag {};
+    return configured<Tag>(reinterpret_cast<const void *>(&mod_tc_kernel<D, KIND, FIXED>), ModTcCfg<D, KIND>::SMEM,
+                           ModTcCfg<D, KIND>::THREADS, KIND == KV_BF16);
 }
 
 // The tensor-memory kernel for a head width and pool kind; fixed: capped scores against a fixed reference.

@@ -298,6 +298,93 @@ def test_prefill_hidden_positions_may_hold_nan(kvc, dtype):
         c.close()
 
 
+@pytest.mark.parametrize("heads", [HEADS[1], HEADS[6], HEADS[8], HEADS[11]], ids=lambda h: "-".join(f"{k}{v}" for k, v in h.items()))
+@pytest.mark.parametrize("mod", ["cap", "window33_sink20_cap", "prefix", "documents_with_empty_rows"])
+def test_warp_level_kernels(kvc, monkeypatch, heads, mod):
+    """KVC_TC=0: chunks and large decode groups on the split kernel, with and without a workspace."""
+    monkeypatch.setenv("KVC_TC", "0")
+    c = Rows(kvc, [1500, 40], **heads)
+    try:
+        for q_start, n_q in ((1400, 70), (0, 1), (13, 150)):
+            m = PREFILL_MODS[mod](c.H_Q, q_start, n_q)
+            q = c.queries(n_q)
+            some = sorted({0, n_q // 2, n_q - 1})
+            c.check_prefill(*c.prefill(m, q, q_start), m, q, q_start, some=some)
+            c.check_prefill(*c.prefill(m, q, q_start, workspace=None), m, q, q_start, some=some)
+        m = Mod(softcap=9.0, window=300, sink=4)
+        c.check_decode(*c.decode(m), m)
+    finally:
+        c.close()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8", "int4"])
+def test_more_units_than_one_launch_takes(kvc, dtype):
+    """A chunk of 17 000 queries of 32 heads on one KV head (2 125 units of 8 positions), and 2 100 sequences."""
+    n = 17000
+    c = Rows(kvc, [n], H_Q=32, H_KV=1, dtype=dtype)
+    try:
+        doc = (np.arange(n) // 700) * 700
+        q = c.queries(n)
+        for m in (Mod(window=40, sink=3, softcap=9.0), Mod(doc_start=doc, window=50)):
+            out, lse = c.prefill(m, q, 0)
+            c.check_prefill(out, lse, m, q, 0, some=[0, 39, 40, 8000, 16383, 16384, 16391, n - 1])
+    finally:
+        c.close()
+    d = Rows(kvc, [1 + (7 * i) % 90 for i in range(2100)], H_Q=32, H_KV=1, dtype=dtype)
+    try:
+        m = Mod(softcap=9.0, window=60)
+        out, lse = d.decode(m)
+        torch.cuda.synchronize()
+        for b in (0, 1, 89, 2047, 2048, 2049, 2099):
+            K, V = d.kv(b, d.lens[b])
+            d.hold(out[b], lse[b], b, d.q[b], K, V, d.lens[b] - 1, visible(m, b, d.lens[b] - 1, d.lens[b]), m, d.decode_weights())
+    finally:
+        d.close()
+
+
+@pytest.mark.parametrize("heads", [HEADS[1], HEADS[6], HEADS[8], HEADS[11]], ids=lambda h: "-".join(f"{k}{v}" for k, v in h.items()))
+def test_whole_and_cut_units(kvc, heads):
+    """Chunks on both sides of the choice between whole units and cut ones, with and without a workspace."""
+    c = Rows(kvc, [5000], **heads)
+    try:
+        for q_start, n_q in ((0, 64), (400, 100), (1900, 100), (4000, 1000), (4990, 10)):
+            m = Mod(softcap=7.0)
+            q = c.queries(n_q)
+            some = sorted({0, n_q // 2, n_q - 1})
+            c.check_prefill(*c.prefill(m, q, q_start), m, q, q_start, some=some)
+            c.check_prefill(*c.prefill(m, q, q_start, workspace=None), m, q, q_start, some=some)
+    finally:
+        c.close()
+
+
+def test_nan_and_infinite_scores(kvc):
+    """A NaN key of a read position makes its row NaN and no other; hidden ones do nothing; huge scores under a cap
+    weigh like the cap."""
+    c = Rows(kvc, [300, 300], H_Q=8, H_KV=2)
+    try:
+        view = c.pool.bytes_view().view(torch.bfloat16).view(2, c.N, 2, 2, 16, 128)
+        view[1, int(c.table[0, 6]), :, 0, 4] = float("nan")   # key 100 of row 0
+        m = Mod(softcap=8.0, window=150)
+        out, lse = c.decode(m)   # reads 150..299
+        assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+        out, lse = c.decode(Mod(softcap=8.0))
+        assert torch.isnan(out[0]).all() and torch.isfinite(out[1]).all()
+        q = c.queries(200)
+        for cap in (8.0, 0.0):
+            out, lse = c.prefill(Mod(softcap=cap), q, 0)
+            assert torch.isfinite(out[:100]).all() and torch.isnan(out[100:]).all()
+        # a huge finite key: with |q| < 20 the 128 products of up to 2e36 sum to under 2.6e38, inside fp32 (a larger one
+        # overflows to infinities of both signs, whose sum is NaN whatever the cap)
+        assert q.abs().max() < 20 and c.q.abs().max() < 20
+        view[1, int(c.table[1, 6]), :, 0, 4] = 1e35
+        out, lse = c.decode(Mod(softcap=8.0))
+        assert torch.isfinite(out[1]).all() and torch.isfinite(lse[1]).all()
+        out, lse = c.prefill(Mod(softcap=8.0), q, 0, row=1)
+        assert torch.isfinite(out).all()
+    finally:
+        c.close()
+
+
 def test_decode_equals_a_chunk_of_one(kvc):
     """The decode form and the chunk form of one token agree within both forms' bounds."""
     c = Rows(kvc, [777])
@@ -353,6 +440,48 @@ def test_two_graphs_side_by_side(kvc):
     finally:
         c.close()
         d.close()
+
+
+def test_first_calls_inside_a_capture():
+    """The first calls of a process, captured into a graph at once, then replayed (a child process)."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch
+import paged_kv_cache_kvc_gb300 as kvc
+p = kvc.kvc_pool_create(64, 16, 1, 2, 128)
+p.bytes_view().view(torch.bfloat16).normal_()
+bt = torch.arange(60, device="cuda").int().view(2, 30)
+lens = torch.tensor([300, 470], device="cuda").int()
+q = torch.randn(2, 8, 128, device="cuda").bfloat16()
+kv = torch.randn(2, 2, 128, device="cuda").bfloat16()
+ws = kvc.kvc_mod_workspace(p, 64, 8, 30)
+rope = kvc.Rope(torch.ones(64, device="cuda") * 0.01)
+mod = kvc.ScoreMod(softcap=20.0)
+qr, out, out2 = torch.empty_like(q), torch.empty_like(q), torch.empty_like(q)
+row = bt[0].contiguous()
+after = lens + 1
+torch.cuda.synchronize()
+def step():
+    kvc.kvc_rope_append(p, 0, bt, lens, q, kv, kv, qr, rope)
+    kvc.kvc_decode_attn_mod(p, 0, qr, bt, after, out, mod=mod, workspace=ws)
+    kvc.kvc_prefill_attn_mod(p, 0, qr, row, 299, out2, mod=mod, workspace=ws)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    step()
+g.replay()
+torch.cuda.synchronize()
+a, b = out.clone(), out2.clone()
+step()
+torch.cuda.synchronize()
+assert kvc.kvc_pool_sync_status(p) == kvc.KVC_OK
+assert torch.equal(a, out) and torch.equal(b, out2) and torch.isfinite(a).all() and torch.isfinite(b).all()
+print("captured")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
 
 
 def test_write_then_attend(kvc):
