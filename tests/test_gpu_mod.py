@@ -385,6 +385,28 @@ def test_nan_and_infinite_scores(kvc):
         c.close()
 
 
+@pytest.mark.parametrize("softcap", [0.0, 5.0, 50.0])
+@pytest.mark.parametrize("heads", HEADS[:8], ids=head_ids[:8])
+def test_one_key_read_gives_its_value(kvc, heads, softcap):
+    """A row that reads one key has that key's value as its output, bit for bit: the weight w (one bf16, or a pair)
+    is divided by the same w in fp32, and the few fp32 roundings of (w v) / w stay far inside bf16's half step."""
+    n_q, q_start = 150, 700
+    c = Rows(kvc, [q_start + n_q, 77], **heads)
+    try:
+        m = Mod(softcap=softcap, window=1)
+        q = c.queries(n_q)
+        out, lse = c.prefill(m, q, q_start)
+        c.check_prefill(out, lse, m, q, q_start)
+        V = np.repeat(c.kv(0, q_start + n_q)[1][q_start:], c.H_Q // c.H_KV, axis=1)
+        assert np.array_equal(f64(out), V)
+        out, lse = c.decode(m)
+        c.check_decode(out, lse, m)
+        for b, n in enumerate(c.lens):
+            assert np.array_equal(f64(out[b]), np.repeat(c.kv(b, n)[1][n - 1], c.H_Q // c.H_KV, axis=0))
+    finally:
+        c.close()
+
+
 def test_decode_equals_a_chunk_of_one(kvc):
     """The decode form and the chunk form of one token agree within both forms' bounds."""
     c = Rows(kvc, [777])
