@@ -23,7 +23,6 @@ __global__ void __launch_bounds__(128) mod_merge_kernel(const ModParams mp)
     const int S = p.max_splits;
     const float2 *ml = p.part_ml + bq * S;
     const float4 *po = reinterpret_cast<const float4 *>(p.part_o + bq * S * D) + d4;
-    allow_dependent_launch();
     grid_dependency_wait();
     if (ml[0].y < 0.f) return;   // uniform
     float m = -INFINITY;

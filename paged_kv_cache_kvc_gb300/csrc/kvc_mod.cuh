@@ -324,7 +324,9 @@ __global__ void __launch_bounds__(kThreads) mod_kernel(const __grid_constant__ C
     const int gq = lane >> 2, tg = lane & 3;
     const int hq0 = h * p.g;
     const int rows = TILE ? p.ppu * p.g : p.g;
-    allow_dependent_launch();
+    // Only this call's own merge may start early (it waits for this grid): the chunk's kernel of kvc_mixed_step
+    // starts without waiting for the kernel before the step, whose outputs it may overwrite.
+    if (p.part_ml && !p.counters) allow_dependent_launch();
     grid_dependency_wait();
 
     auto col_pos = [&](int qi) { return TILE ? b * p.ppu + qi / p.g : b; };   // row of q: chunk position or sequence

@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(ModTcCfg<D, KIND>::THREADS, 1) mod_tc_kernel(c
         tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
     }
-    allow_dependent_launch();
+    if (!tp.whole) allow_dependent_launch();   // for this call's own merge, which waits for this grid (kvc_mod.cuh)
     grid_dependency_wait();
 
     // ---- what each unit takes of the line, and the running sum
@@ -1189,7 +1189,6 @@ __global__ void __launch_bounds__(256) mod_tc_merge_kernel(const ModTcParams tp,
     const int rr = blockIdx.x * RG + threadIdx.x % RG, dg = threadIdx.x / RG % COLS, grp = threadIdx.x / (RG * COLS);
     const int tile = rr >> 7, r = rr & 127;
     const int hr = r % g, pr = tile * p.ppu + r / g;   // head of the group, position of the unit
-    allow_dependent_launch();
     grid_dependency_wait();
     int unit, head, n, slot0;   // the unit's pieces: slot0 in its first CTA, then every later CTA's first slot
     if constexpr (T == 1) {

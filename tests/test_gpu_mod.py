@@ -557,6 +557,42 @@ def test_write_then_attend(kvc):
         pool.close()
 
 
+@pytest.mark.parametrize("heads", [HEADS[1], HEADS[6]], ids=[head_ids[1], head_ids[6]])
+@pytest.mark.parametrize("first", ["decode", "decode_unsplit", "prefill", "prefill_short"])
+def test_a_step_after_the_call_sees_its_outputs(kvc, first, heads):
+    """kvc_mixed_step's chunk starts without waiting for the kernel before the step: these calls' kernels let nothing
+    but their own merge start early, so a chunk whose queries are the outputs of such a call reads them finished."""
+    n = 64 if first == "prefill_short" else 200
+    rows = n if first.startswith("decode") else 2
+    c = Rows(kvc, [9000] + [33] * (rows - 1), **heads)
+    try:
+        q, m = c.queries(n), Mod(softcap=5.0)
+        ws = kvc.kvc_mod_workspace(c.pool, n, c.H_Q, c.table.shape[1])
+        one, lens = c.bt[1:2].contiguous(), torch.tensor([33], dtype=torch.int32, device="cuda")
+        k_new, v_new = (bf16(c.r.standard_normal((1, c.H_KV, c.D))).cuda() for _ in range(2))
+
+        def run(wait):
+            out, lse = c.outputs(n)
+            if first == "prefill":
+                c.kvc.kvc_prefill_attn_mod(c.pool, c.layer, q, c.bt[0].contiguous(), 8800, out, lse, mod=c.dev_mod(m), workspace=ws)
+            elif first == "prefill_short":
+                c.kvc.kvc_prefill_attn_mod(c.pool, c.layer, q, c.bt[0].contiguous(), 0, out, lse, mod=c.dev_mod(m), workspace=ws)
+            else:
+                c.decode(m, ws if first == "decode" else None, out, lse)
+            if wait:
+                torch.cuda.synchronize()
+            o1, chunk = torch.empty((1, c.H_Q, c.D), device="cuda"), torch.empty((n, c.H_Q, c.D), device="cuda")
+            kvc.kvc_mixed_step(c.pool, c.layer, q[:1].contiguous(), one, lens, k_new, v_new, o1, None, out, c.bt[0].contiguous(), 300, chunk)
+            return chunk
+
+        want = run(True)
+        assert bool(torch.isfinite(want).all())
+        for _ in range(4):
+            assert torch.equal(run(False), want)
+    finally:
+        c.close()
+
+
 def test_expired_waits_are_reported(kvc, monkeypatch):
     """With every load withheld (a test hook) the calls report KVC_ERR_TIMEOUT and return; the pool then works."""
     c = Rows(kvc, [300, 20])
