@@ -191,9 +191,9 @@ static kvc_status run_tc(kvc_pool *pool, const ModParams &mp0, int visit, void *
     tp.whole = !ws || (few_units + sms - 1) / sms * tiles <= few_units * tiles / sms + 8;
     tp.split = !tp.whole && (decode || p.n_pos <= p.ppu);
     tp.single = decode && tp.whole;
-    const bool fixed = pool->dtype == KVC_BF16 && tp.m.capped && !tp.m.alibi && tp.m.cap_out <= kMtCapLimit;
+    const bool fixed = tp.m.capped && !tp.m.alibi && (pool->dtype != KVC_BF16 || tp.m.cap_out <= kMtCapLimit);
     const DecodeKernel k = pool->dtype == KVC_BF16 ? select_mod_tc_bf16(pool->D, fixed)
-                                                   : select_mod_tc_quant(pool->dtype == KVC_INT4);
+                                                   : select_mod_tc_quant(pool->dtype == KVC_INT4, fixed);
     if (!k.fn) return KVC_ERR_UNSUPPORTED;
     if (k.ctas_per_sm <= 0) return KVC_ERR_CUDA;
     const int unit = tp.split || tp.single ? p.ppu : 2 * p.ppu;   // positions per unit

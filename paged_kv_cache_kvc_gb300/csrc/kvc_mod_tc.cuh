@@ -40,9 +40,9 @@
 //
 // Weights.  On bf16 pools with capped scores (and no bias) x lies in [-cap, cap], so the softmax needs
 // no maximum: 2^(x - cap / 2) fits fp32 and bf16 for caps up to 55 (80 in log2 units), and a score
-// needs no second look.  Otherwise a row's reference maximum moves when a score passes it by more
-// than 8 (log2 units), and the row's outputs are rescaled in TMEM.  The weights enter the value
-// product as bf16 (f16 with e4m3 and int4 pools, where they stay under 2^8); their sum is taken before
+// needs no second look.  Otherwise a row's reference moves when a score passes it by more
+// than SLACK, and the row's outputs are rescaled in TMEM.  The weights enter the value
+// product as bf16 (f16 with e4m3 and int4 pools, where they stay under 2^15); their sum is taken before
 // the rounding: a relative error of at most 2^-8 in each, independent, which an output rounded to
 // bf16 hides.  A row that reads a few keys has no such average: against the fixed reference its outputs are
 // divided by the sum of the rounded weights of the tiles it does not read whole (one key read gives its
@@ -84,6 +84,11 @@ struct ModTcCfg {
     static constexpr int QTILE = BANDS * QBAND;
     static constexpr int KBAND = kMtKeys * 128;        // one band of 64 key or value rows
     static constexpr int STAGE = BANDS * KBAND;
+    // A row's reference moves when a score passes it by more (log2 units).  f16 weights stay under 2^16; bf16's and
+    // the sums have fp32's range.  (8 instead, with scores of deviation 4.6: one of a tile's 128 rows moves in every
+    // fifth tile and holds it up: 2048 positions over 18 432, int4 capped 1 022 us against 813, bf16 with a bias 709
+    // against 578.)
+    static constexpr float SLACK = QUANT ? 15.f : 40.f;
     static constexpr int R = QUANT ? 3 : 4;            // ring depths (with QUANT: codes, keys and values alike)
     static constexpr int BLOCK = QUANT ? DecodeCfg<D, KIND>::STAGE : 0;   // a block's codes, keys then values
     static constexpr int RAW = kMtBlocks * BLOCK;
@@ -399,7 +404,7 @@ __device__ __forceinline__ int cta_of(int64_t w, int64_t W, int64_t G)
     return static_cast<int>(num / W);
 }
 
-// FIXED: capped scores against the fixed reference; else the running reference maximum.
+// FIXED: capped scores without a bias (bf16 pools: against the fixed reference).
 // tmap: the pool's map of 16-row boxes (bf16), else the map of whole blocks.
 template <int D, int KIND, bool FIXED>
 __global__ void __launch_bounds__(ModTcCfg<D, KIND>::THREADS, 1) mod_tc_kernel(const __grid_constant__ CUtensorMap tmap,
@@ -883,7 +888,7 @@ __global__ void __launch_bounds__(ModTcCfg<D, KIND>::THREADS, 1) mod_tc_kernel(c
             const int flo = __reduce_max_sync(kFull, real ? r.lo : 0), fhi = __reduce_min_sync(kFull, real ? r.hi : 0x7FFFFFFF);
             const int fd = __reduce_max_sync(kFull, real ? r.d : 0), fe = __reduce_min_sync(kFull, real ? r.e : 0x7FFFFFFF);
             const bool any_real = __any_sync(kFull, real);
-            float m = FIXED ? ref : -INFINITY, l = 0.f;
+            float m = FIXED && !C::QUANT ? ref : -INFINITY, l = 0.f;
             float dl = 0.f;   // FIXED: what rounding the weights added to their sum, in the tiles not read whole
             bool go = true;
             // scores in registers are raw, or already modified and in log2 units (bias, or a cap with a maximum)
@@ -931,56 +936,103 @@ __global__ void __launch_bounds__(ModTcCfg<D, KIND>::THREADS, 1) mod_tc_kernel(c
                 f32x2 ls[4] = {f32x2_of(0.f, 0.f), f32x2_of(0.f, 0.f), f32x2_of(0.f, 0.f), f32x2_of(0.f, 0.f)};
                 if constexpr (FIXED) {
                     const f32x2 in = f32x2_of(mp.cap_in, mp.cap_in);
-                    const f32x2 out2 = f32x2_of(-2.f * mp.cap_out, -2.f * mp.cap_out), ref2 = f32x2_of(ref, ref);
-                    auto weigh4 = [&](const uint32_t *s, float (&w)[4]) {
-                        f32x2 x01, x23;   // x - cap / 2
-                        capped4(f32x2_of(__uint_as_float(s[0]), __uint_as_float(s[1])),
-                                f32x2_of(__uint_as_float(s[2]), __uint_as_float(s[3])), in, out2, ref2, x01, x23);
-                        w[0] = fast_exp2(lo2(x01));
-                        w[1] = fast_exp2(hi2(x01));
-                        w[2] = fast_exp2(lo2(x23));
-                        w[3] = fast_exp2(hi2(x23));
-                    };
-                    // Code of their own for the tiles read whole: with the others' selects between them, a score
-                    // and the weight before it were not interleaved (2048 positions over 18 432: 592 against 571 us).
-                    if (full) {
-                        uint32_t pk[32];
+                    const f32x2 out2 = f32x2_of(-2.f * mp.cap_out, -2.f * mp.cap_out);
+                    // Quantised pools: weights against the reference so far, which moves when a score turns out to
+                    // pass it by more than the slack; the weights are then taken again (in a row's first tile, and
+                    // seldom after).  (The tile's maximum first, then the weights: 833 us against 710 at 2048
+                    // positions over 18 432, e4m3.)
+                    for (;;) {
+                        const float mref = m == -INFINITY ? 0.f : m, top = mp.cap_out - mref;
+                        const f32x2 top2 = f32x2_of(top, top);
+                        float best0 = -INFINITY, best1 = -INFINITY;
+                        auto weigh4 = [&](const uint32_t *s, float (&x)[4], float (&w)[4]) {
+                            f32x2 x01, x23;   // x - the reference
+                            capped4(f32x2_of(__uint_as_float(s[0]), __uint_as_float(s[1])),
+                                    f32x2_of(__uint_as_float(s[2]), __uint_as_float(s[3])), in, out2, top2, x01, x23);
+                            x[0] = lo2(x01);
+                            x[1] = hi2(x01);
+                            x[2] = lo2(x23);
+                            x[3] = hi2(x23);
 #pragma unroll
-                        for (int c = 0; c < 64; c += 4) {
-                            float w[4];
-                            weigh4(c < 32 ? r0 + c : r1 + (c - 32), w);
-                            ls[(c >> 2) & 1] = add2(ls[(c >> 2) & 1], f32x2_of(w[0], w[1]));
-                            ls[2 + ((c >> 2) & 1)] = add2(ls[2 + ((c >> 2) & 1)], f32x2_of(w[2], w[3]));
-                            pk[c / 2] = pack_bf16(w[0], w[1]);
-                            pk[c / 2 + 1] = pack_bf16(w[2], w[3]);
-                        }
-                        tmem_st32(tsb, pk);   // over the first half of the step's scores
-                    } else {
-                        // Thirty-two scores at a time, which keeps the code small: a few tiles come this way, and
-                        // with straight code for all 64 a 600-position chunk over 1 800 took 45.7 us against 43.7.
-#pragma unroll 1
-                        for (int half = 0; half < 2; ++half) {
-                            const uint32_t seen = half ? seen1 : seen0;
-                            uint32_t pk[16];
-                            // a hidden key's score may be anything, and would reach its group's reciprocal
+                            for (int k = 0; k < 4; ++k) w[k] = fast_exp2(x[k]);
+                        };
+                        auto pack = [](float a, float b) { return C::QUANT ? pack_f16(a, b) : pack_bf16(a, b); };
 #pragma unroll
-                            for (int c = 0; c < 32; ++c) r0[c] = seen >> c & 1u ? (half ? r1[c] : r0[c]) : 0u;
+                        for (int k = 0; k < 4; ++k) ls[k] = f32x2_of(0.f, 0.f);
+                        // Code of their own for the tiles read whole: with the others' selects between them, a score
+                        // and the weight before it were not interleaved (2048 positions over 18 432: 592 against 571 us).
+                        if (full) {
+                            uint32_t pk[32];
 #pragma unroll
-                            for (int c = 0; c < 32; c += 4) {
-                                float w[4];
-                                weigh4(r0 + c, w);
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) w[k] = seen >> (c + k) & 1u ? w[k] : 0.f;
-                                ls[0] = add2(ls[0], f32x2_of(w[0], w[1]));
-                                ls[1] = add2(ls[1], f32x2_of(w[2], w[3]));
-                                pk[c / 2] = pack_bf16(w[0], w[1]);
-                                pk[c / 2 + 1] = pack_bf16(w[2], w[3]);
-                                dl += ((bf16_lo(pk[c / 2]) - w[0]) + (bf16_hi(pk[c / 2]) - w[1])) +
-                                      ((bf16_lo(pk[c / 2 + 1]) - w[2]) + (bf16_hi(pk[c / 2 + 1]) - w[3]));
+                            for (int c = 0; c < 64; c += 4) {
+                                float x[4], w[4];
+                                weigh4(c < 32 ? r0 + c : r1 + (c - 32), x, w);
+                                if constexpr (C::QUANT) {
+                                    best0 = max3f(best0, x[0], x[1]);
+                                    best1 = max3f(best1, x[2], x[3]);
+                                }
+                                ls[(c >> 2) & 1] = add2(ls[(c >> 2) & 1], f32x2_of(w[0], w[1]));
+                                ls[2 + ((c >> 2) & 1)] = add2(ls[2 + ((c >> 2) & 1)], f32x2_of(w[2], w[3]));
+                                pk[c / 2] = pack(w[0], w[1]);
+                                pk[c / 2 + 1] = pack(w[2], w[3]);
                             }
-                            tmem_st16(tsb + 16 * half, pk);
+                            tmem_st32(tsb, pk);   // over the first half of the step's scores
+                        } else {
+                            // Thirty-two scores at a time, which keeps the code small: a few tiles come this way, and
+                            // with straight code for all 64 a 600-position chunk over 1 800 took 45.7 us against 43.7.
+#pragma unroll 1
+                            for (int half = 0; half < 2; ++half) {
+                                const uint32_t seen = half ? seen1 : seen0;
+                                uint32_t pk[16];
+                                // a hidden key's score may be anything, and would reach its group's reciprocal
+#pragma unroll
+                                for (int c = 0; c < 32; ++c) r0[c] = seen >> c & 1u ? r0[c] : 0u;
+#pragma unroll
+                                for (int c = 0; c < 32; c += 4) {
+                                    float x[4], w[4];
+                                    weigh4(r0 + c, x, w);
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k) {
+                                        w[k] = seen >> (c + k) & 1u ? w[k] : 0.f;
+                                        if constexpr (C::QUANT) best0 = fmaxf(best0, seen >> (c + k) & 1u ? x[k] : -INFINITY);
+                                    }
+                                    ls[0] = add2(ls[0], f32x2_of(w[0], w[1]));
+                                    ls[1] = add2(ls[1], f32x2_of(w[2], w[3]));
+                                    pk[c / 2] = pack(w[0], w[1]);
+                                    pk[c / 2 + 1] = pack(w[2], w[3]);
+                                    if constexpr (!C::QUANT)
+                                        dl += ((bf16_lo(pk[c / 2]) - w[0]) + (bf16_hi(pk[c / 2]) - w[1])) +
+                                              ((bf16_lo(pk[c / 2 + 1]) - w[2]) + (bf16_hi(pk[c / 2 + 1]) - w[3]));
+                                }
+                                tmem_st16(tsb + 16 * half, pk);
+#pragma unroll
+                                for (int c = 0; c < 32; ++c) {   // the other half; after two turns they are back
+                                    const uint32_t t = r0[c];
+                                    r0[c] = r1[c];
+                                    r1[c] = t;
+                                }
+                            }
+                        }
+                        if constexpr (!C::QUANT) break;
+                        const float bm = fmaxf(best0, best1) + mref;
+                        const bool move = bm > m + C::SLACK;   // false while nothing has been read
+                        if (!__any_sync(kFull, move)) break;
+                        float alpha = 1.f;
+                        if (move) {
+                            alpha = fast_exp2(m - bm);
+                            m = bm;
+                            l *= alpha;
+                        }
+                        // the warp rescales its rows of O together, once the previous product is in them
+                        if (i > 0) {
+                            go = wait(pvdone(x, b ^ 1), ((it - 1) >> 1) & 1);
+                            if (!go) break;
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int part = 0; part < D / 16; ++part) tmem_scale16(to + part * 16, alpha);
                         }
                     }
+                    if (!go) break;
                 } else {
                     uint32_t pk[32];
                     float sv[64];
@@ -1040,7 +1092,7 @@ __global__ void __launch_bounds__(ModTcCfg<D, KIND>::THREADS, 1) mod_tc_kernel(c
                     b0 = max3f(b0, sv[60], sv[61]);
                     b1 = max3f(b1, sv[62], sv[63]);
                     const float bm = max3f(b0, b1, fmaxf(b2, b3)) * mul;   // mul > 0
-                    const bool move = bm > m + kRescaleSlack;              // false while nothing has been read
+                    const bool move = bm > m + C::SLACK;              // false while nothing has been read
                     float alpha = 1.f;
                     if (move) {
                         alpha = fast_exp2(m - bm);
@@ -1092,7 +1144,7 @@ __global__ void __launch_bounds__(ModTcCfg<D, KIND>::THREADS, 1) mod_tc_kernel(c
             }
             const int prow = x * 128 + rq;
             const float inv = l == 0.f ? 0.f : 1.f / (l + dl);
-            const float even = FIXED && l != 0.f ? l * inv : 1.f;   // a piece's outputs go with its l
+            const float even = FIXED && !C::QUANT && l != 0.f ? l * inv : 1.f;   // a piece's outputs go with its l
             // finished rows go through the warp's quarter of the tile's query memory (its products are done;
             // 16-byte chunk c of row r at c ^ (r mod 8)), so that whole rows leave: a lane's row written
             // straight to global memory measured 2.8 us a unit against 1.3 us
@@ -1294,9 +1346,9 @@ DecodeKernel mod_tc_instance()
                            ModTcCfg<D, KIND>::THREADS, KIND == KV_BF16);
 }
 
-// The tensor-memory kernel for a head width and pool kind; fixed: capped scores against a fixed reference.
+// The tensor-memory kernel for a head width and pool kind; fixed: see FIXED.
 DecodeKernel select_mod_tc_bf16(int D, bool fixed);
-DecodeKernel select_mod_tc_quant(bool int4);
+DecodeKernel select_mod_tc_quant(bool int4, bool fixed);
 const void *select_mod_tc_merge(int D, bool few);
 
 }  // namespace kvc

@@ -3,9 +3,10 @@
 
 namespace kvc {
 
-DecodeKernel select_mod_tc_quant(bool int4)
+DecodeKernel select_mod_tc_quant(bool int4, bool fixed)
 {
-    return int4 ? mod_tc_instance<128, KV_INT4, false>() : mod_tc_instance<128, KV_E4M3, false>();
+    if (int4) return fixed ? mod_tc_instance<128, KV_INT4, true>() : mod_tc_instance<128, KV_INT4, false>();
+    return fixed ? mod_tc_instance<128, KV_E4M3, true>() : mod_tc_instance<128, KV_E4M3, false>();
 }
 
 }  // namespace kvc
