@@ -3,11 +3,14 @@
 
 namespace kvc {
 
-DecodeKernel select_mod_tc_bf16(int D, bool fixed)
+template <int D>
+static DecodeKernel bf16_instance(TcMode mode)
 {
-    if (D == 64) return fixed ? mod_tc_instance<64, KV_BF16, true>() : mod_tc_instance<64, KV_BF16, false>();
-    return fixed ? mod_tc_instance<128, KV_BF16, true>() : mod_tc_instance<128, KV_BF16, false>();
+    return mode == kMtCapped        ? mod_tc_instance<D, KV_BF16, kMtCapped>()
+           : mode == kMtCappedBrief ? mod_tc_instance<D, KV_BF16, kMtCappedBrief>() : mod_tc_instance<D, KV_BF16, kMtGeneral>();
 }
+
+DecodeKernel select_mod_tc_bf16(int D, TcMode mode) { return D == 64 ? bf16_instance<64>(mode) : bf16_instance<128>(mode); }
 
 const void *select_mod_tc_merge(int D, bool few)
 {

@@ -26,8 +26,8 @@
 // unit form one line of W tiles; CTA c of G takes tiles [c W / G, (c + 1) W / G), whatever units they
 // belong to, so every SM gets the same work to within a tile: a late chunk of few long rows, a long
 // triangular one and a ragged decode batch alike.  A unit that lies in one CTA is written at once; a
-// unit's start costs about four tiles (its queries staged, its outputs written: 5 us against 1.2 us a
-// tile), so the line gives every unit kMtStart tiles more than it has.  A
+// unit's start and end cost about eight tiles (its queries staged, the first scores, its outputs written:
+// 9 us against 1.1 us a tile), so the line gives every unit kMtStart tiles more than it has.  A
 // unit cut by CTA borders leaves fp32 partials (at most two per CTA) for mod_tc_merge_kernel, which
 // adds them in CTA order.  (Merged by the unit's last CTA instead, 600 queries of 1800 positions took
 // 43 us, 20 pieces of a 5-query chunk 9 us of its 36: one SM's loads against all SMs'.)
@@ -58,7 +58,9 @@ namespace kvc {
 constexpr int kMtKeys = 64;                        // keys per tile
 constexpr int kMtBlocks = kMtKeys / kBS;
 constexpr int kMtUnits = 2048;                     // most units (per head) of one launch
-constexpr int kMtStart = 4;                        // a unit's start, in tiles
+constexpr int kMtStart = 8;                        // a unit's start and end, in tiles (4: 600 queries over 1 800 44 us, 8: 40)
+constexpr int kMtCut = 16;                         // what cutting units costs a CTA, in tiles (run_tc)
+constexpr int kMtBrief = 16;                       // a CTA's share of the line up to which kMtCappedBrief serves
 constexpr float kMtCapLimit = 80.f;                // cap in log2 units up to which no maximum is needed
 
 struct ModTcParams {
@@ -74,6 +76,11 @@ struct ModTcParams {
     float *part_o;        // float4 [2 G][D / 4][256] (a warp's rows side by side), few-row calls [2 G][256][D / 4]
     float2 *part_ml;      // [2 G][256]
 };
+
+// How the weights are taken.  Capped: capped scores without a bias.  Brief: the same with one code for all tiles, half
+// as much to fetch when a call starts and a tenth slower per tile; us brief / not, 32 heads over 8: 64 queries at 0
+// 10.4 / 11.6, 256 at 0 13.9 / 15.1 (from a cold cache 21 / 25), 1500 at 0 54 / 51, 2048 over 18 432 619 / 573.
+enum TcMode { kMtGeneral, kMtCapped, kMtCappedBrief };
 
 template <int D, int KIND>
 struct ModTcCfg {
@@ -404,14 +411,15 @@ __device__ __forceinline__ int cta_of(int64_t w, int64_t W, int64_t G)
     return static_cast<int>(num / W);
 }
 
-// FIXED: capped scores without a bias (bf16 pools: against the fixed reference).
 // tmap: the pool's map of 16-row boxes (bf16), else the map of whole blocks.
-template <int D, int KIND, bool FIXED>
+template <int D, int KIND, TcMode MODE>
 __global__ void __launch_bounds__(ModTcCfg<D, KIND>::THREADS, 1) mod_tc_kernel(const __grid_constant__ CUtensorMap tmap,
                                                                 const ModTcParams tp)
 {
     using C = ModTcCfg<D, KIND>;
     constexpr int R = C::R;
+    constexpr bool CAPPED = MODE != kMtGeneral, FIXED = CAPPED && !C::QUANT;   // FIXED: against the fixed reference
+    static_assert(!C::QUANT || MODE != kMtCappedBrief, "bf16 pools");
     const ModParams &mp = tp.m;
     const DecodeParams &p = mp.d;
     extern __shared__ uint8_t smem_raw[];
@@ -888,7 +896,7 @@ __global__ void __launch_bounds__(ModTcCfg<D, KIND>::THREADS, 1) mod_tc_kernel(c
             const int flo = __reduce_max_sync(kFull, real ? r.lo : 0), fhi = __reduce_min_sync(kFull, real ? r.hi : 0x7FFFFFFF);
             const int fd = __reduce_max_sync(kFull, real ? r.d : 0), fe = __reduce_min_sync(kFull, real ? r.e : 0x7FFFFFFF);
             const bool any_real = __any_sync(kFull, real);
-            float m = FIXED && !C::QUANT ? ref : -INFINITY, l = 0.f;
+            float m = FIXED ? ref : -INFINITY, l = 0.f;
             float dl = 0.f;   // FIXED: what rounding the weights added to their sum, in the tiles not read whole
             bool go = true;
             // scores in registers are raw, or already modified and in log2 units (bias, or a cap with a maximum)
@@ -934,7 +942,7 @@ __global__ void __launch_bounds__(ModTcCfg<D, KIND>::THREADS, 1) mod_tc_kernel(c
                 tmem_ld_wait(r0);
                 tmem_ld_wait(r1);
                 f32x2 ls[4] = {f32x2_of(0.f, 0.f), f32x2_of(0.f, 0.f), f32x2_of(0.f, 0.f), f32x2_of(0.f, 0.f)};
-                if constexpr (FIXED) {
+                if constexpr (CAPPED) {
                     const f32x2 in = f32x2_of(mp.cap_in, mp.cap_in);
                     const f32x2 out2 = f32x2_of(-2.f * mp.cap_out, -2.f * mp.cap_out);
                     // Quantised pools: weights against the reference so far, which moves when a score turns out to
@@ -959,6 +967,39 @@ __global__ void __launch_bounds__(ModTcCfg<D, KIND>::THREADS, 1) mod_tc_kernel(c
                         auto pack = [](float a, float b) { return C::QUANT ? pack_f16(a, b) : pack_bf16(a, b); };
 #pragma unroll
                         for (int k = 0; k < 4; ++k) ls[k] = f32x2_of(0.f, 0.f);
+                        if constexpr (MODE == kMtCappedBrief) {
+                            uint32_t pk[32];
+                            if (!full) {   // a hidden key's score may be anything, and would reach its group's reciprocal
+#pragma unroll
+                                for (int c = 0; c < 32; ++c) {
+                                    r0[c] = seen0 >> c & 1u ? r0[c] : 0u;
+                                    r1[c] = seen1 >> c & 1u ? r1[c] : 0u;
+                                }
+                            }
+#pragma unroll
+                            for (int c = 0; c < 64; c += 4) {
+                                float x[4], w[4];
+                                weigh4(c < 32 ? r0 + c : r1 + (c - 32), x, w);
+                                if (!full) {
+                                    const uint32_t seen = (c < 32 ? seen0 : seen1) >> (c & 31);
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k) w[k] = seen >> k & 1u ? w[k] : 0.f;
+                                }
+                                ls[(c >> 2) & 1] = add2(ls[(c >> 2) & 1], f32x2_of(w[0], w[1]));
+                                ls[2 + ((c >> 2) & 1)] = add2(ls[2 + ((c >> 2) & 1)], f32x2_of(w[2], w[3]));
+                                pk[c / 2] = pack(w[0], w[1]);
+                                pk[c / 2 + 1] = pack(w[2], w[3]);
+                            }
+                            if (!full) {
+                                f32x2 rounded = f32x2_of(0.f, 0.f);
+#pragma unroll
+                                for (int c = 0; c < 32; ++c) rounded = add2(rounded, f32x2_of(bf16_lo(pk[c]), bf16_hi(pk[c])));
+                                const f32x2 sum = add2(add2(ls[0], ls[1]), add2(ls[2], ls[3]));
+                                dl += (lo2(rounded) + hi2(rounded)) - (lo2(sum) + hi2(sum));
+                            }
+                            tmem_st32(tsb, pk);   // over the first half of the step's scores
+                            break;
+                        }
                         // Code of their own for the tiles read whole: with the others' selects between them, a score
                         // and the weight before it were not interleaved (2048 positions over 18 432: 592 against 571 us).
                         if (full) {
@@ -1144,7 +1185,7 @@ __global__ void __launch_bounds__(ModTcCfg<D, KIND>::THREADS, 1) mod_tc_kernel(c
             }
             const int prow = x * 128 + rq;
             const float inv = l == 0.f ? 0.f : 1.f / (l + dl);
-            const float even = FIXED && !C::QUANT && l != 0.f ? l * inv : 1.f;   // a piece's outputs go with its l
+            const float even = FIXED && l != 0.f ? l * inv : 1.f;   // a piece's outputs go with its l
             // finished rows go through the warp's quarter of the tile's query memory (its products are done;
             // 16-byte chunk c of row r at c ^ (r mod 8)), so that whole rows leave: a lane's row written
             // straight to global memory measured 2.8 us a unit against 1.3 us
@@ -1338,17 +1379,17 @@ __global__ void __launch_bounds__(256) mod_tc_merge_kernel(const ModTcParams tp,
     if (dg == 0 && p.lse) p.lse[orow] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
-template <int D, int KIND, bool FIXED>
+template <int D, int KIND, TcMode MODE>
 DecodeKernel mod_tc_instance()
 {
     struct Tag {};
-    return configured<Tag>(reinterpret_cast<const void *>(&mod_tc_kernel<D, KIND, FIXED>), ModTcCfg<D, KIND>::SMEM,
+    return configured<Tag>(reinterpret_cast<const void *>(&mod_tc_kernel<D, KIND, MODE>), ModTcCfg<D, KIND>::SMEM,
                            ModTcCfg<D, KIND>::THREADS, KIND == KV_BF16);
 }
 
-// The tensor-memory kernel for a head width and pool kind; fixed: see FIXED.
-DecodeKernel select_mod_tc_bf16(int D, bool fixed);
-DecodeKernel select_mod_tc_quant(bool int4, bool fixed);
+// The tensor-memory kernel for a head width, pool kind and mode.
+DecodeKernel select_mod_tc_bf16(int D, TcMode mode);
+DecodeKernel select_mod_tc_quant(bool int4, TcMode mode);
 const void *select_mod_tc_merge(int D, bool few);
 
 }  // namespace kvc

@@ -3,10 +3,12 @@
 
 namespace kvc {
 
-DecodeKernel select_mod_tc_quant(bool int4, bool fixed)
+template <int KIND>
+static DecodeKernel quant_instance(TcMode mode)
 {
-    if (int4) return fixed ? mod_tc_instance<128, KV_INT4, true>() : mod_tc_instance<128, KV_INT4, false>();
-    return fixed ? mod_tc_instance<128, KV_E4M3, true>() : mod_tc_instance<128, KV_E4M3, false>();
+    return mode == kMtCapped ? mod_tc_instance<128, KIND, kMtCapped>() : mod_tc_instance<128, KIND, kMtGeneral>();
 }
+
+DecodeKernel select_mod_tc_quant(bool int4, TcMode mode) { return int4 ? quant_instance<KV_INT4>(mode) : quant_instance<KV_E4M3>(mode); }
 
 }  // namespace kvc
