@@ -390,7 +390,8 @@ KVC_API kvc_status kvc_rope_write_tokens(kvc_pool *pool, int32_t layer, const in
  * lse = -inf.  Blocks that no query of a unit reads are not looked at: their
  * table entries may be -1. */
 typedef struct {
-    float softcap;              /* 0: none; finite, >= 0 */
+    float softcap;              /* 0: none; finite, >= 0, at most 4096 (else KVC_ERR_UNSUPPORTED): capped scores
+                                 * carry an absolute error of about 2^-23 of it */
     int32_t window;             /* 0: none */
     int32_t sink;               /* used with a window */
     int32_t prefix;             /* 0: none */

@@ -257,6 +257,8 @@ static kvc_status mod_checks(kvc_pool *pool, int32_t layer, const void *q, int32
         if (!std::isfinite(mod->softcap) || mod->softcap < 0.f || mod->window < 0 || mod->sink < 0 || mod->prefix < 0)
             return KVC_ERR_ARG;
         if (mod->softcap > 0.f && !std::isfinite(2.f * scale * 1.4426950408889634f / mod->softcap)) return KVC_ERR_ARG;
+        // the cap's error is absolute, 2^-23 of it: past this it would show in the weights, however small the scores
+        if (mod->softcap > 4096.f) return KVC_ERR_UNSUPPORTED;
         if (!aligned(mod->alibi, 4) || !aligned(mod->doc_start, 4)) return KVC_ERR_ARG;
         if (mod->doc_start && mod->prefix > 0) return KVC_ERR_UNSUPPORTED;
     }

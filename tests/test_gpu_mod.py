@@ -385,6 +385,30 @@ def test_nan_and_infinite_scores(kvc):
         c.close()
 
 
+@pytest.mark.parametrize("softcap", [0.0, 50.0, 100.0, 4096.0])
+@pytest.mark.parametrize("dtype", ["bf16", "fp8", "int4"])
+def test_scores_that_climb(kvc, dtype, softcap):
+    """Scores that grow along the row past every slack of the running references, up to about 150."""
+    n, D = 1500, 128
+    c = Rows(kvc, [n, 40], dtype=dtype)
+    try:
+        u = np.where(c.r.random(D) < 0.5, -1.0, 1.0)
+        ramp = np.linspace(0.0, 1.2, n)[:, None, None] * u + 0.05 * c.r.standard_normal((n, c.H_KV, D))
+        k, v = bf16(ramp).cuda(), bf16(c.r.standard_normal((n, c.H_KV, D))).cuda()
+        kvc.kvc_write_tokens(c.pool, c.layer, c.bt[:1].contiguous(), torch.zeros(1, dtype=torch.int32, device="cuda"),
+                             torch.tensor([0, n], dtype=torch.int32, device="cuda"), k, v, max_tokens=n)
+        torch.cuda.synchronize()
+        raw = c.pool.bytes_view().cpu().numpy().reshape(c.pool.num_layers, -1)[c.layer]
+        c.stored = pool_values(raw, dtype, c.N, c.H_KV, 16, D)
+        m = Mod(softcap=softcap)
+        q = bf16(11.0 * u + 0.5 * c.r.standard_normal((70, c.H_Q, D))).cuda()
+        c.check_prefill(*c.prefill(m, q, n - 70), m, q, n - 70)
+        c.q = q[:2].contiguous()
+        c.check_decode(*c.decode(m), m)
+    finally:
+        c.close()
+
+
 @pytest.mark.parametrize("softcap", [0.0, 5.0, 50.0])
 @pytest.mark.parametrize("heads", HEADS[:8], ids=head_ids[:8])
 def test_one_key_read_gives_its_value(kvc, heads, softcap):
@@ -635,6 +659,7 @@ def test_refusals(kvc):
         for status, k in ((kvc.KVC_ERR_ARG, dict(layer=2)), (kvc.KVC_ERR_ARG, dict(mod=kvc.ScoreMod(softcap=-1.0))),
                           (kvc.KVC_ERR_ARG, dict(mod=kvc.ScoreMod(softcap=float("nan")))),
                           (kvc.KVC_ERR_ARG, dict(mod=kvc.ScoreMod(softcap=1e-42))),
+                          (kvc.KVC_ERR_UNSUPPORTED, dict(mod=kvc.ScoreMod(softcap=4097.0))),
                           (kvc.KVC_ERR_ARG, dict(mod=kvc.ScoreMod(window=-1))), (kvc.KVC_ERR_ARG, dict(mod=kvc.ScoreMod(sink=-1))),
                           (kvc.KVC_ERR_ARG, dict(mod=kvc.ScoreMod(doc_start=doc))), (kvc.KVC_ERR_ARG, dict(scale=0.0)),
                           (kvc.KVC_ERR_ARG, dict(scale=-1.0)), (kvc.KVC_ERR_ARG, dict(scale=float("inf")))):
