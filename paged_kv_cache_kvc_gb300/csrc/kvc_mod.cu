@@ -197,7 +197,7 @@ static kvc_status run_tc(kvc_pool *pool, const ModParams &mp0, int visit, void *
     tp.split = !tp.whole && (decode || p.n_pos <= p.ppu);
     tp.single = decode && tp.whole;
     const bool fixed = tp.m.capped && !tp.m.alibi && (pool->dtype != KVC_BF16 || tp.m.cap_out <= kMtCapLimit);
-    const TcMode mode = !fixed ? kMtGeneral : pool->dtype == KVC_BF16 && line <= kMtBrief ? kMtCappedBrief : kMtCapped;
+    const TcMode mode = !tp.m.capped && !tp.m.alibi ? kMtPlain : !fixed ? kMtGeneral : pool->dtype == KVC_BF16 && line <= kMtBrief ? kMtCappedBrief : kMtCapped;
     const DecodeKernel k = pool->dtype == KVC_BF16 ? select_mod_tc_bf16(pool->D, mode)
                                                    : select_mod_tc_quant(pool->dtype == KVC_INT4, mode);
     if (!k.fn) return KVC_ERR_UNSUPPORTED;

@@ -6,7 +6,8 @@ namespace kvc {
 template <int D>
 static DecodeKernel bf16_instance(TcMode mode)
 {
-    return mode == kMtCapped        ? mod_tc_instance<D, KV_BF16, kMtCapped>()
+    return mode == kMtPlain         ? mod_tc_instance<D, KV_BF16, kMtPlain>()
+           : mode == kMtCapped      ? mod_tc_instance<D, KV_BF16, kMtCapped>()
            : mode == kMtCappedBrief ? mod_tc_instance<D, KV_BF16, kMtCappedBrief>() : mod_tc_instance<D, KV_BF16, kMtGeneral>();
 }
 

@@ -77,10 +77,10 @@ struct ModTcParams {
     float2 *part_ml;      // [2 G][256]
 };
 
-// How the weights are taken.  Capped: capped scores without a bias.  Brief: the same with one code for all tiles, half
+// How the weights are taken.  Plain: neither cap nor bias.  Capped: capped scores without a bias.  Brief: the same with one code for all tiles, half
 // as much to fetch when a call starts and a tenth slower per tile; us brief / not, 32 heads over 8: 64 queries at 0
 // 10.4 / 11.6, 256 at 0 13.9 / 15.1 (from a cold cache 21 / 25), 1500 at 0 54 / 51, 2048 over 18 432 619 / 573.
-enum TcMode { kMtGeneral, kMtCapped, kMtCappedBrief };
+enum TcMode { kMtGeneral, kMtPlain, kMtCapped, kMtCappedBrief };
 
 template <int D, int KIND>
 struct ModTcCfg {
@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(ModTcCfg<D, KIND>::THREADS, 1) mod_tc_kernel(c
 {
     using C = ModTcCfg<D, KIND>;
     constexpr int R = C::R;
-    constexpr bool CAPPED = MODE != kMtGeneral, FIXED = CAPPED && !C::QUANT;   // FIXED: against the fixed reference
+    constexpr bool CAPPED = MODE == kMtCapped || MODE == kMtCappedBrief, FIXED = CAPPED && !C::QUANT;   // FIXED: against the fixed reference
     static_assert(!C::QUANT || MODE != kMtCappedBrief, "bf16 pools");
     const ModParams &mp = tp.m;
     const DecodeParams &p = mp.d;
@@ -899,9 +899,8 @@ __global__ void __launch_bounds__(ModTcCfg<D, KIND>::THREADS, 1) mod_tc_kernel(c
             float m = FIXED ? ref : -INFINITY, l = 0.f;
             float dl = 0.f;   // FIXED: what rounding the weights added to their sum, in the tiles not read whole
             bool go = true;
-            // scores in registers are raw, or already modified and in log2 units (bias, or a cap with a maximum)
-            const bool ready = mp.capped || mp.alibi;
-            const float mul = ready ? 1.f : p.scale_log2;
+            // every real row of the warp is at this position or past it
+            const int from = __reduce_min_sync(kFull, real ? pos : 0x7FFFFFFF);
             const int steps = tp.split ? (s.k1 - s.k0 + 1 - x) / 2 : s.k1 - s.k0;
             for (int i = 0; i < steps; ++i, ++it) {
                 const int b = it & 1, tile = tp.split ? 2 * i + x : i;
@@ -1074,6 +1073,56 @@ __global__ void __launch_bounds__(ModTcCfg<D, KIND>::THREADS, 1) mod_tc_kernel(c
                         }
                     }
                     if (!go) break;
+                } else if constexpr (MODE == kMtPlain) {
+                    // Against the reference so far, and again where a score passes it by more than the slack (in a
+                    // row's first tile, and seldom after): the maximum first took 520 us against 501.
+                    for (;;) {
+                        const float neg = m == -INFINITY ? 0.f : -m;
+                        const f32x2 sc2 = f32x2_of(p.scale_log2, p.scale_log2), neg2 = f32x2_of(neg, neg);
+                        float b0 = -INFINITY, b1 = -INFINITY;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) ls[k] = f32x2_of(0.f, 0.f);
+                        uint32_t pk[32];
+                        if (!full) {
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) {
+                                r0[c] = seen0 >> c & 1u ? r0[c] : 0xFF800000u;
+                                r1[c] = seen1 >> c & 1u ? r1[c] : 0xFF800000u;
+                            }
+                        }
+#pragma unroll
+                        for (int c = 0; c < 64; c += 4) {
+                            const uint32_t *sr = c < 32 ? r0 + c : r1 + (c - 32);
+                            const float s0 = __uint_as_float(sr[0]), s1 = __uint_as_float(sr[1]), s2 = __uint_as_float(sr[2]), s3 = __uint_as_float(sr[3]);
+                            b0 = max3f(b0, s0, s1);
+                            b1 = max3f(b1, s2, s3);
+                            const f32x2 e01 = fma2(f32x2_of(s0, s1), sc2, neg2), e23 = fma2(f32x2_of(s2, s3), sc2, neg2);
+                            const float w0 = fast_exp2(lo2(e01)), w1 = fast_exp2(hi2(e01)), w2 = fast_exp2(lo2(e23)), w3 = fast_exp2(hi2(e23));
+                            ls[(c >> 2) & 1] = add2(ls[(c >> 2) & 1], f32x2_of(w0, w1));
+                            ls[2 + ((c >> 2) & 1)] = add2(ls[2 + ((c >> 2) & 1)], f32x2_of(w2, w3));
+                            pk[c / 2] = C::QUANT ? pack_f16(w0, w1) : pack_bf16(w0, w1);
+                            pk[c / 2 + 1] = C::QUANT ? pack_f16(w2, w3) : pack_bf16(w2, w3);
+                        }
+                        tmem_st32(tsb, pk);   // over the first half of the step's scores
+                        const float bm = fmaxf(b0, b1) * p.scale_log2;
+                        const bool move = bm > m + C::SLACK;   // false while nothing has been read
+                        if (!__any_sync(kFull, move)) break;
+                        float alpha = 1.f;
+                        if (move) {
+                            alpha = fast_exp2(m - bm);
+                            m = bm;
+                            l *= alpha;
+                        }
+                        // the warp rescales its rows of O together, once the previous product is in them
+                        if (i > 0) {
+                            go = wait(pvdone(x, b ^ 1), ((it - 1) >> 1) & 1);
+                            if (!go) break;
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int part = 0; part < D / 16; ++part) tmem_scale16(to + part * 16, alpha);
+                        }
+                    }
+                    if (!go) break;
                 } else {
                     uint32_t pk[32];
                     float sv[64];
@@ -1101,18 +1150,33 @@ __global__ void __launch_bounds__(ModTcCfg<D, KIND>::THREADS, 1) mod_tc_kernel(c
                             sv[c + 2] = lo2(x23);
                             sv[c + 3] = hi2(x23);
                         }
-                    } else if (ready) {
-#pragma unroll
-                        for (int c = 0; c < 64; ++c) sv[c] *= p.scale_log2;
                     }
-                    if (mp.alibi) {
+                    const float mul = mp.capped ? 1.f : p.scale_log2;   // into log2 units
+                    if (mp.alibi && one_run && from >= t0 + kMtKeys - 1) {
+                        // keys before the row's position: the bias is slope (t - p), a line.  Eight chains of pairs, four
+                        // additions each; with every key's distance on its own 2048 over 18 432 took 577 us against 543 (e4m3
+                        // 775 against 696).
+                        f32x2 line[8];
+                        const float at = slope * static_cast<float>(t0 - pos);
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+                            line[c] = f32x2_of(fmaf(slope, static_cast<float>(2 * c), at), fmaf(slope, static_cast<float>(2 * c + 1), at));
+                        const f32x2 on = f32x2_of(16.f * slope, 16.f * slope), mul2_ = f32x2_of(mul, mul);
+#pragma unroll
+                        for (int c = 0; c < 64; c += 2) {
+                            const f32x2 y = fma2(f32x2_of(sv[c], sv[c + 1]), mul2_, line[(c / 2) & 7]);
+                            line[(c / 2) & 7] = add2(line[(c / 2) & 7], on);
+                            sv[c] = lo2(y);
+                            sv[c + 1] = hi2(y);
+                        }
+                    } else if (C::QUANT || mp.alibi) {   // quantised pools: always with a bias here
 #pragma unroll
                         for (int b2 = 0; b2 < kMtBlocks; ++b2) {
                             const int vb = min(first + b2, max(v.br.n - 1, 0));
                             const float away = static_cast<float>(pos - v.br.at(vb) * kBS);
 #pragma unroll
                             for (int c = 0; c < kBS; ++c)
-                                sv[kBS * b2 + c] = fmaf(-slope, fabsf(away - static_cast<float>(c)), sv[kBS * b2 + c]);
+                                sv[kBS * b2 + c] = fmaf(sv[kBS * b2 + c], mul, -slope * fabsf(away - static_cast<float>(c)));
                         }
                     }
                     if (!full) {
@@ -1132,7 +1196,7 @@ __global__ void __launch_bounds__(ModTcCfg<D, KIND>::THREADS, 1) mod_tc_kernel(c
                     }
                     b0 = max3f(b0, sv[60], sv[61]);
                     b1 = max3f(b1, sv[62], sv[63]);
-                    const float bm = max3f(b0, b1, fmaxf(b2, b3)) * mul;   // mul > 0
+                    const float bm = max3f(b0, b1, fmaxf(b2, b3));
                     const bool move = bm > m + C::SLACK;              // false while nothing has been read
                     float alpha = 1.f;
                     if (move) {
@@ -1151,10 +1215,10 @@ __global__ void __launch_bounds__(ModTcCfg<D, KIND>::THREADS, 1) mod_tc_kernel(c
                         for (int part = 0; part < D / 16; ++part) tmem_scale16(to + part * 16, alpha);
                     }
                     const float neg = m == -INFINITY ? 0.f : -m;
-                    const f32x2 mul_2 = f32x2_of(mul, mul), neg2 = f32x2_of(neg, neg);
+                    const f32x2 neg2 = f32x2_of(neg, neg);
 #pragma unroll
                     for (int c = 0; c < 64; c += 2) {
-                        const f32x2 e = fma2(f32x2_of(sv[c], sv[c + 1]), mul_2, neg2);
+                        const f32x2 e = add2(f32x2_of(sv[c], sv[c + 1]), neg2);
                         const float w0 = fast_exp2(lo2(e)), w1 = fast_exp2(hi2(e));
                         ls[(c / 2) & 3] = add2(ls[(c / 2) & 3], f32x2_of(w0, w1));
                         pk[c / 2] = C::QUANT ? pack_f16(w0, w1) : pack_bf16(w0, w1);

@@ -6,7 +6,8 @@ namespace kvc {
 template <int KIND>
 static DecodeKernel quant_instance(TcMode mode)
 {
-    return mode == kMtCapped ? mod_tc_instance<128, KIND, kMtCapped>() : mod_tc_instance<128, KIND, kMtGeneral>();
+    return mode == kMtPlain    ? mod_tc_instance<128, KIND, kMtPlain>()
+           : mode == kMtCapped ? mod_tc_instance<128, KIND, kMtCapped>() : mod_tc_instance<128, KIND, kMtGeneral>();
 }
 
 DecodeKernel select_mod_tc_quant(bool int4, TcMode mode) { return int4 ? quant_instance<KV_INT4>(mode) : quant_instance<KV_E4M3>(mode); }
