@@ -281,6 +281,44 @@ def test_prefill_long(kvc, heads, mod):
         c.close()
 
 
+LONG_MODS = {"plain": lambda H, q0, n: Mod(), "cap": lambda H, q0, n: Mod(softcap=5.0), "alibi": lambda H, q0, n: Mod(alibi=slopes(H)),
+             "cap_alibi": lambda H, q0, n: Mod(softcap=20.0, alibi=slopes(H)), "cap_past_the_fixed_reference": lambda H, q0, n: Mod(softcap=90.0),
+             "cap_window_sink": lambda H, q0, n: Mod(softcap=20.0, window=1500, sink=70),
+             "cap_documents": lambda H, q0, n: Mod(softcap=20.0, doc_start=(np.arange(q0, q0 + n) // 1501) * 1501)}
+
+
+@pytest.mark.parametrize("heads", [dict(H_Q=32, H_KV=8), dict(H_Q=32, H_KV=8, D=64), dict(H_Q=32, H_KV=8, dtype="fp8"),
+                                   dict(H_Q=32, H_KV=8, dtype="int4")], ids=lambda h: "-".join(f"{k}{v}" for k, v in h.items()))
+@pytest.mark.parametrize("mod", LONG_MODS)
+def test_prefill_many_tiles(kvc, heads, mod):
+    """Chunks with tens of tiles for every SM: units cut across SMs and the code for long calls."""
+    c = Rows(kvc, [3300], **heads)
+    try:
+        for q_start, n_q in ((2100, 1200), (0, 2500)):
+            m = LONG_MODS[mod](c.H_Q, q_start, n_q)
+            q = c.queries(n_q)
+            out, lse = c.prefill(m, q, q_start)
+            c.check_prefill(out, lse, m, q, q_start, some=[0, 1, 63, 64, n_q // 2, n_q - 100, n_q - 1])
+            o2, l2 = c.prefill(m, q, q_start)
+            assert torch.equal(out, o2) and torch.equal(lse, l2)
+    finally:
+        c.close()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_one_key_read_in_a_long_call(kvc, D):
+    """As test_one_key_read_gives_its_value, with documents of one position, on the code for long calls."""
+    n_q, q_start = 2048, 1000
+    c = Rows(kvc, [q_start + n_q], H_Q=32, H_KV=8, D=D)
+    try:
+        m = Mod(softcap=50.0, doc_start=np.arange(q_start, q_start + n_q))
+        out, lse = c.prefill(m, c.queries(n_q), q_start)
+        torch.cuda.synchronize()
+        assert np.array_equal(f64(out), np.repeat(c.kv(0, q_start + n_q)[1][q_start:], 4, axis=1))
+    finally:
+        c.close()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp8"])
 def test_prefill_hidden_positions_may_hold_nan(kvc, dtype):
     """Positions that no query reads (behind the window, past the row's end, freed blocks) may hold anything."""
