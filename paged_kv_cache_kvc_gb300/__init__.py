@@ -401,7 +401,7 @@ def kvc_rope_write_tokens(pool, layer, block_tables, start_pos, cu_tokens, q, k,
 class ScoreMod:
     """Score modifiers and masks of kvc_decode_attn_mod / kvc_prefill_attn_mod (see kvc_score_mod in kvc.h).
 
-    alibi: CUDA fp32 [H_Q] slopes; doc_start: CUDA int32 [n_q] (prefill).  Holds the tensors."""
+    softcap: at most 4096; alibi: CUDA fp32 [H_Q] slopes; doc_start: CUDA int32 [n_q] (prefill).  Holds the tensors."""
 
     def __init__(self, softcap=0.0, window=0, sink=0, prefix=0, alibi=None, doc_start=None):
         self.alibi, self.doc_start = alibi, doc_start
