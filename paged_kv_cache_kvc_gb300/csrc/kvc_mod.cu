@@ -168,7 +168,7 @@ static bool use_tc(const kvc_pool *pool)
 
 // Decode groups of query heads from which the tensor-memory kernel serves a step.  Measured, capped, 32 heads, us against
 // the split kernel's: 8 x 32 768 positions bf16 46 / 44, e4m3 40 / 44, int4 51 / 52; 1 x 32 768: 34 / 37, 38 / 38, 35 / 43;
-// 64 x 1 000: 23 / 36, 30 / 37, 33 / 41.  Smaller groups: 8 heads, 8 x 8 192 x 4 KV heads 42 / 32; 16 heads (bf16, whose
+// 64 x 1 000: 20 / 36, 25 / 37, 25 / 41.  Smaller groups: 8 heads, 8 x 8 192 x 4 KV heads 42 / 32; 16 heads (bf16, whose
 // weights the split kernel feeds as 16 bits), 8 x 8 192 x 2: 27 / 19.
 constexpr int kTcGroup = 17;
 
@@ -182,27 +182,30 @@ static kvc_status run_tc(kvc_pool *pool, const ModParams &mp0, int visit, void *
     const bool decode = p.lens != nullptr;
     p.ppu = decode ? 1 : 128 / p.g;
     tp.total = p.len_base + p.n_pos;
-    // Whole units or cut ones, by the busiest CTA's time in tiles of 1.1 us.  A unit costs its tiles and kMtStart;
-    // cutting costs the partials' way through memory and the merge, together about kMtCut.  The lengths of documents
-    // and of decode sequences are not known here: documents are taken as a quarter of the row, sequences as full.
-    // Measured, 32 heads over 8, us whole / cut: 64 queries at 0 11.5 / 15.5, 300 at 300 22 / 24, 1500 at 0 61 / 51,
-    // 100 at 2 000 48 / 29, 2 000 in documents of 333 (e4m3) 57 / 65, in one document 82 / 72.
+    // Whole units of two query tiles ("dealt"), whole units of one that both chains share ("joined"), or cut units, by
+    // the busiest CTA's time in tiles of 1.1 us.  A unit costs its tiles (joined: half of them, and kMtJoin) and
+    // kMtStart; cutting costs the partials' way through memory and the merge, together about kMtCut.  The lengths of
+    // documents and of decode sequences are not known here: documents are taken as a quarter of the row, sequences as
+    // full.  Measured, 32 heads over 8, us dealt / joined / cut: 64 queries at 0 11 / - / 15, 300 at 300 22 / 17 / 24,
+    // 600 at 1 200 42 / 36 / 40, 1500 at 0 61 / - / 51, 100 at 2 000 48 / - / 29, 2 000 in documents of 333 (e4m3)
+    // 57 / - / 65, in one document 82 / - / 72; decode, 64 x 1 000, 32 heads over 1: 23 (one chain idle) / 20 / 34.
     int64_t longest = (visit + kMtBlocks - 1) / kMtBlocks, average = longest;
     if (mp0.doc_start) longest = average = longest / 4 + 1;
     else if (!decode && visit == p.max_blocks) average = std::max<int64_t>(1, longest - p.n_pos / 2 / kMtKeys);   // causal
-    const int64_t few_units = static_cast<int64_t>(p.H_KV) * (decode ? p.n_pos : (p.n_pos + 2 * p.ppu - 1) / (2 * p.ppu));
-    const int64_t sms = pool->num_sms;
-    const int64_t line = few_units * (average + kMtStart) / sms;   // a CTA's share of the line
-    tp.whole = !ws || (few_units + sms - 1) / sms * (longest + kMtStart) <= line + kMtCut;
-    tp.split = !tp.whole && (decode || p.n_pos <= p.ppu);
-    tp.single = decode && tp.whole;
+    const int64_t sms = pool->num_sms, tall = (p.n_pos + 2 * p.ppu - 1) / (2 * p.ppu), low = (p.n_pos + p.ppu - 1) / p.ppu;
+    auto rounds = [&](int64_t units) { return (p.H_KV * units + sms - 1) / sms; };
+    const int64_t line = p.H_KV * (decode ? low : tall) * (average + kMtStart) / sms;   // a CTA's share of the line
+    const int64_t joined = rounds(low) * (longest / 2 + kMtStart + kMtJoin);
+    const int64_t dealt = decode ? joined : rounds(tall) * (longest + kMtStart);
+    tp.whole = !ws || std::min(dealt, joined) <= line + kMtCut;
+    tp.split = tp.whole ? joined <= dealt : decode || p.n_pos <= p.ppu;
     const bool fixed = tp.m.capped && !tp.m.alibi && (pool->dtype != KVC_BF16 || tp.m.cap_out <= kMtCapLimit);
     const TcMode mode = !tp.m.capped && !tp.m.alibi ? kMtPlain : !fixed ? kMtGeneral : pool->dtype == KVC_BF16 && line <= kMtBrief ? kMtCappedBrief : kMtCapped;
     const DecodeKernel k = pool->dtype == KVC_BF16 ? select_mod_tc_bf16(pool->D, mode)
                                                    : select_mod_tc_quant(pool->dtype == KVC_INT4, mode);
     if (!k.fn) return KVC_ERR_UNSUPPORTED;
     if (k.ctas_per_sm <= 0) return KVC_ERR_CUDA;
-    const int unit = tp.split || tp.single ? p.ppu : 2 * p.ppu;   // positions per unit
+    const int unit = tp.split ? p.ppu : 2 * p.ppu;   // positions per unit
     const int per_launch = kMtUnits * unit, n_q = p.n_pos, start = p.len_base;
     for (int at = 0; at < n_q; at += per_launch) {
         p.n_pos = std::min(per_launch, n_q - at);

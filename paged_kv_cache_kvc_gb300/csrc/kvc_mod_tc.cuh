@@ -36,7 +36,9 @@
 // after the other, and nothing is merged.
 //
 // Few rows (a chunk of at most 128 / g positions, a decode sequence): both chains take the same rows,
-// chain 0 every other tile and chain 1 the rest, and the merge joins them too.
+// chain 0 every other tile and chain 1 the rest, and the merge joins them too.  Where such units fill the
+// SMs without being cut (a chunk of 600 positions of 32 heads over 8 is 152 of them), the chains' sums meet
+// in shared memory and nothing is merged.
 //
 // Weights.  On bf16 pools with capped scores (and no bias) x lies in [-cap, cap], so the softmax needs
 // no maximum: 2^(x - cap / 2) fits fp32 and bf16 for caps up to 55 (80 in log2 units), and a score
@@ -59,6 +61,7 @@ constexpr int kMtKeys = 64;                        // keys per tile
 constexpr int kMtBlocks = kMtKeys / kBS;
 constexpr int kMtUnits = 2048;                     // most units (per head) of one launch
 constexpr int kMtStart = 8;                        // a unit's start and end, in tiles (4: 600 queries over 1 800 44 us, 8: 40)
+constexpr int kMtJoin = 2;                         // the meeting of two chains, in tiles
 constexpr int kMtCut = 16;                         // what cutting units costs a CTA, in tiles (run_tc)
 constexpr int kMtBrief = 16;                       // a CTA's share of the line up to which kMtCappedBrief serves
 constexpr float kMtCapLimit = 80.f;                // cap in log2 units up to which no maximum is needed
@@ -67,8 +70,8 @@ struct ModTcParams {
     ModParams m;          // m.d.ppu: positions per query tile (a decode sequence's one)
     int32_t units;        // units per head
     int32_t whole;        // 1: no partials, units are dealt whole
-    int32_t split;        // 1: a unit is one query tile's positions, and both chains take its rows (below)
-    int32_t single;       // 1: a unit is one query tile's positions, and chain 0 takes them
+    int32_t split;        // 1: a unit is one query tile's positions, and both chains take its rows (below);
+                          // with whole set, they meet in the CTA
     int32_t total;        // positions the row holds (prefill)
     int32_t *prefix;      // few-row calls: [units + 1] place of each unit on a head's line, for the merge
     int4 *cuts;           // other calls: [G] {head, unit, pieces (0: none), slot} of the unit that CTA c starts
@@ -106,8 +109,11 @@ struct ModTcCfg {
     static constexpr int PREFIX = C + R * RAW;         // int32 [kMtUnits + 1]
     static constexpr int BARS = PREFIX + ((kMtUnits + 1) * 4 + 15) / 16 * 16;
     static constexpr int NBARS = 7 * R + 14;
+    static constexpr int MEET_PART = 128 * 128;        // where chains meet: 128 rows x 32 fp32 columns, twice
     static constexpr int MISC = BARS + NBARS * 8;      // scan sums [16], abort, TMEM base, block masks [16]
-    static constexpr int SMEM = 1024 + MISC + 160;
+    static constexpr int END = MISC + 160;
+    static constexpr int MEET = QTILE >= 2 * MEET_PART ? Q + QTILE : END;   // chain 1's query tile if it is large enough
+    static constexpr int SMEM = 1024 + (MEET == END ? END + 2 * MEET_PART : END);
     static_assert(SMEM <= 232448, "shared memory of a CTA");
 };
 
@@ -196,14 +202,14 @@ __device__ __forceinline__ void tmem_scale16(uint32_t taddr, float f)
         : "memory");
 }
 
-// A vote of the 128 threads of a query tile (named barrier `id`).
-__device__ __forceinline__ bool tile_all(bool v, uint32_t id)
+// A vote of the 128 threads of a query tile, or of both tiles' 256 (named barrier `id`).
+__device__ __forceinline__ bool tile_all(bool v, uint32_t id, uint32_t threads)
 {
     uint32_t r;
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, %2, 128, p;\n\t"
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, %2, %3, p;\n\t"
                  "selp.u32 %0, 1, 0, q;\n\t}"
                  : "=r"(r)
-                 : "r"(v ? 1u : 0u), "r"(id)
+                 : "r"(v ? 1u : 0u), "r"(id), "r"(threads)
                  : "memory");
     return r != 0;
 }
@@ -297,7 +303,7 @@ __device__ __forceinline__ RowView row_view(const ModTcParams &p, int c)
 
 __device__ __forceinline__ int unit_positions_of(const ModTcParams &p)
 {
-    return p.split || p.single ? p.m.d.ppu : 2 * p.m.d.ppu;
+    return p.split ? p.m.d.ppu : 2 * p.m.d.ppu;
 }
 
 // What a unit reads; the same in every thread of a warp.
@@ -779,7 +785,7 @@ __global__ void __launch_bounds__(ModTcCfg<D, KIND>::THREADS, 1) mod_tc_kernel(c
                 if (tp.whole) (void)unit_of(tp, s, lane);
                 const uint32_t n = s.k1 - s.k0;
                 // the second tile may hold no position: it only lets the key and value tiles go
-                if (!tp.split && (tp.single ? x == 1 : s.unit * 2 * ppt + x * ppt >= p.n_pos)) {
+                if (!tp.split && s.unit * 2 * ppt + x * ppt >= p.n_pos) {
                     for (uint32_t k = 0; go && k < n; ++k, ++kt) {
                         const int slot = kt % R;
                         const uint32_t par = (kt / R) & 1;
@@ -825,6 +831,8 @@ __global__ void __launch_bounds__(ModTcCfg<D, KIND>::THREADS, 1) mod_tc_kernel(c
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + 128 * x + lane_off, to = tmem + 256 + 128 * x + lane_off;
         const float ref = 0.5f * mp.cap_out;
+        const bool join = tp.split && tp.whole;   // the two chains' sums meet here, not in the merge
+        auto bar_both = [] { asm volatile("bar.sync 6, 256;" ::: "memory"); };   // both chains' threads
         uint32_t it = 0, kt = 0;   // this query tile's steps, key tiles so far
         int piece = 0;             // segments so far
         int4 cut = make_int4(0, 0, 0, 0);
@@ -832,11 +840,11 @@ __global__ void __launch_bounds__(ModTcCfg<D, KIND>::THREADS, 1) mod_tc_kernel(c
             const uint32_t kt0 = kt;
             const UnitView v = unit_of(tp, s, lane);
             kt += s.k1 - s.k0;
-            const int c0 = v.pos0 + (tp.split || tp.single ? 0 : x * ppt);
-            const bool mine = c0 < p.n_pos && !(tp.single && x == 1);
+            const int c0 = v.pos0 + (tp.split ? 0 : x * ppt);
+            const bool mine = c0 < p.n_pos;
             // up to 64 rows in a few-row call: chain 1's sit in the tile's upper half, so that the warps that have
             // work to do are on different schedulers
-            const int ro = tp.split && x == 1 && min(ppt, p.n_pos - c0) * g <= 64 ? 64 : 0;
+            const int ro = tp.split && !join && x == 1 && min(ppt, p.n_pos - c0) * g <= 64 ? 64 : 0;
             const int rq = row - ro;            // row of the query tile
             const int c = c0 + max(rq, 0) / g;   // its chunk position
             const bool real = rq >= 0 && rq < ppt * g && c < p.n_pos;
@@ -1233,7 +1241,7 @@ __global__ void __launch_bounds__(ModTcCfg<D, KIND>::THREADS, 1) mod_tc_kernel(c
             }
             if (go && steps > 0) go = wait(pvdone(x, (it - 1) & 1), ((it - 1) >> 1) & 1);   // the segment's last product
             // every thread of the query tile takes this vote once per segment, so the barriers below meet
-            if (!tile_all(go, 4 + x)) {
+            if (!tile_all(go, join ? 6 : 4 + x, join ? 256 : 128)) {
                 timed_out = true;
                 break;
             }
@@ -1241,25 +1249,39 @@ __global__ void __launch_bounds__(ModTcCfg<D, KIND>::THREADS, 1) mod_tc_kernel(c
 
             // ---- epilogue: the unit's rows, or a piece of them for the merge (rows [128 x, 128 x + 128) of a slot)
             const bool done = s.k0 == 0 && s.k1 == s.tiles && !tp.split;
-            if (!any_real) continue;
+            if (!any_real && !join) continue;
             const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (piece > 0 ? 1 : 0);
-            if (tid == 0 && !done && s.k0 == 0) {
+            if (tid == 0 && !done && !tp.whole && s.k0 == 0) {
                 const int64_t end = static_cast<int64_t>(s.head) * walk.per_head + prefix[s.unit + 1];
                 cut = make_int4(s.head, s.unit, cta_of(end - 1, W, G) - static_cast<int>(blockIdx.x) + 1, static_cast<int>(slot));
             }
             const int prow = x * 128 + rq;
-            const float inv = l == 0.f ? 0.f : 1.f / (l + dl);
+            float inv = l == 0.f ? 0.f : 1.f / (l + dl), other = 0.f;
+            if (join) {   // chain 1 hands over m, l and the sum that its outputs go with; chain 0 weighs both
+                float4 *meet = reinterpret_cast<float4 *>(smem + C::PREFIX);
+                if (x == 1) meet[row] = make_float4(m, l, l + dl, 0.f);
+                bar_both();
+                if (x == 0) {
+                    const float4 o = meet[row];
+                    const float M = fmaxf(l != 0.f ? m : -INFINITY, o.y != 0.f ? o.x : -INFINITY);
+                    const float e0 = l != 0.f ? fast_exp2(m - M) : 0.f, e1 = o.y != 0.f ? fast_exp2(o.x - M) : 0.f;
+                    const float sum = e0 * (l + dl) + e1 * o.z;
+                    l = e0 * l + e1 * o.y;
+                    m = M;
+                    const float r = l == 0.f ? 0.f : 1.f / sum;
+                    inv = e0 * r;
+                    other = e1 * r;
+                }
+            }
+            const bool leaves = done || (join && x == 0);   // this thread's row leaves finished
             const float even = FIXED && l != 0.f ? l * inv : 1.f;   // a piece's outputs go with its l
             // finished rows go through the warp's quarter of the tile's query memory (its products are done;
             // 16-byte chunk c of row r at c ^ (r mod 8)), so that whole rows leave: a lane's row written
             // straight to global memory measured 2.8 us a unit against 1.3 us
             const uint32_t stage = sbase + C::Q + x * C::QTILE + (warp & 3) * (C::QTILE / 4);
-#pragma unroll
-            for (int part = 0; part < D / 32; ++part) {
-                uint32_t o[32];
+            auto load_part = [&](int part, uint32_t (&o)[32]) {   // 32 channels of this row's sums
                 tmem_ld32(to + part * 32, o);
                 tmem_ld_wait(o);
-                if (!real) continue;
                 if constexpr (C::QUANT) {   // the channels' order, and the value scales
                     uint32_t w[32];
 #pragma unroll
@@ -1273,27 +1295,64 @@ __global__ void __launch_bounds__(ModTcCfg<D, KIND>::THREADS, 1) mod_tc_kernel(c
                         o[4 * c + 3] = __float_as_uint(__uint_as_float(w[4 * c + 3]) * sv.w);
                     }
                 }
-                if (done) {
+            };
+            auto stage_part = [&](int part, const uint32_t (&o)[32], float by) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t w[4];
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t w[4];
 #pragma unroll
-                        for (int u = 0; u < 4; ++u)
-                            w[u] = l == 0.f ? 0u : pack_bf16(__uint_as_float(o[8 * c + 2 * u]) * inv,
-                                                             __uint_as_float(o[8 * c + 2 * u + 1]) * inv);
-                        sts128(stage + lane * (D * 2) + (((part * 4 + c) ^ (lane & 7)) << 4), make_uint4(w[0], w[1], w[2], w[3]));
+                    for (int u = 0; u < 4; ++u)
+                        w[u] = l == 0.f ? 0u : pack_bf16(__uint_as_float(o[8 * c + 2 * u]) * by,
+                                                         __uint_as_float(o[8 * c + 2 * u + 1]) * by);
+                    sts128(stage + lane * (D * 2) + (((part * 4 + c) ^ (lane & 7)) << 4), make_uint4(w[0], w[1], w[2], w[3]));
+                }
+            };
+            if (join) {   // 32 channels at a time through two buffers: one barrier each
+#pragma unroll 1
+                for (int part = 0; part < D / 32; ++part) {
+                    uint32_t o[32];
+                    load_part(part, o);
+                    const uint32_t at = sbase + C::MEET + (part & 1) * C::MEET_PART + row * 16;
+                    if (x == 1) {
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+                            sts128(at + c * 2048, make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]));
                     }
-                } else {
-                    float4 *dst = reinterpret_cast<float4 *>(tp.part_o) +
-                                  (tp.split ? (slot * 256 + prow) * (D / 4) + part * 8 : (slot * (D / 4) + part * 8) * 256 + prow);
-                    const int step = tp.split ? 1 : 256;
+                    bar_both();
+                    if (x == 1) continue;
 #pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        dst[c * step] = make_float4(__uint_as_float(o[4 * c]) * even, __uint_as_float(o[4 * c + 1]) * even,
-                                                   __uint_as_float(o[4 * c + 2]) * even, __uint_as_float(o[4 * c + 3]) * even);
+                    for (int c = 0; c < 8; ++c) {
+                        const uint4 e = lds128(at + c * 2048);
+                        const uint32_t ew[4] = {e.x, e.y, e.z, e.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {   // a chain that read nothing left nothing to add
+                            const float a = inv != 0.f ? __uint_as_float(o[4 * c + k]) * inv : 0.f;
+                            o[4 * c + k] = __float_as_uint(other != 0.f ? fmaf(__uint_as_float(ew[k]), other, a) : a);
+                        }
+                    }
+                    stage_part(part, o, 1.f);
+                }
+                bar_both();   // chain 1's columns have been read: its next queries may go there
+            } else {
+#pragma unroll
+                for (int part = 0; part < D / 32; ++part) {
+                    uint32_t o[32];
+                    load_part(part, o);
+                    if (!real) continue;
+                    if (done) {
+                        stage_part(part, o, inv);
+                    } else {
+                        float4 *dst = reinterpret_cast<float4 *>(tp.part_o) +
+                                      (tp.split ? (slot * 256 + prow) * (D / 4) + part * 8 : (slot * (D / 4) + part * 8) * 256 + prow);
+                        const int step = tp.split ? 1 : 256;
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+                            dst[c * step] = make_float4(__uint_as_float(o[4 * c]) * even, __uint_as_float(o[4 * c + 1]) * even,
+                                                       __uint_as_float(o[4 * c + 2]) * even, __uint_as_float(o[4 * c + 3]) * even);
+                    }
                 }
             }
-            if (done) {
+            if (leaves) {
                 __syncwarp();
                 constexpr int N = D / 8, STEP = 32 / N;   // chunks of a row, rows a warp writes at once
                 const int ch = lane % N;
@@ -1314,8 +1373,8 @@ __global__ void __launch_bounds__(ModTcCfg<D, KIND>::THREADS, 1) mod_tc_kernel(c
                     }
                 }
             }
-            if (real && done && p.lse) p.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-            if (real && !done) tp.part_ml[slot * 256 + prow] = make_float2(m, l);
+            if (real && leaves && p.lse) p.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+            if (real && !done && !join) tp.part_ml[slot * 256 + prow] = make_float2(m, l);
         }
         if (tid == 0 && !tp.whole && !tp.split) tp.cuts[blockIdx.x] = cut;
     }
