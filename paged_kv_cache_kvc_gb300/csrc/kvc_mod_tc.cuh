@@ -80,9 +80,9 @@ struct ModTcParams {
     float2 *part_ml;      // [2 G][256]
 };
 
-// How the weights are taken.  Plain: neither cap nor bias.  Capped: capped scores without a bias.  Brief: the same with one code for all tiles, half
-// as much to fetch when a call starts and a tenth slower per tile; us brief / not, 32 heads over 8: 64 queries at 0
-// 10.4 / 11.6, 256 at 0 13.9 / 15.1 (from a cold cache 21 / 25), 1500 at 0 54 / 51, 2048 over 18 432 619 / 573.
+// How the weights are taken.  Plain: neither cap nor bias.  Capped: capped scores without a bias.  Brief: the same with
+// one code for all tiles, half as much to fetch when a call starts and a tenth slower per tile; us brief / not, 32 heads
+// over 8: 64 queries at 0 10.4 / 11.6 (from a cold cache 21 / 23), 1500 at 0 54 / 51, 2048 over 18 432 619 / 573.
 enum TcMode { kMtGeneral, kMtPlain, kMtCapped, kMtCappedBrief };
 
 template <int D, int KIND>
