@@ -28,17 +28,17 @@
 // triangular one and a ragged decode batch alike.  A unit that lies in one CTA is written at once; a
 // unit's start and end cost about eight tiles (its queries staged, the first scores, its outputs written:
 // 9 us against 1.1 us a tile), so the line gives every unit kMtStart tiles more than it has.  A
-// unit cut by CTA borders leaves fp32 partials (at most two per CTA) for mod_tc_merge_kernel, which
-// adds them in CTA order.  (Merged by the unit's last CTA instead, 600 queries of 1800 positions took
+// unit cut by CTA borders leaves fp32 partials for mod_tc_merge_kernel, which adds them in CTA order; a
+// CTA leaves pieces of two units at most (kvc_mod_line.cuh).  (Merged by the unit's last CTA instead, 600 queries of 1800 positions took
 // 43 us, 20 pieces of a 5-query chunk 9 us of its 36: one SM's loads against all SMs'.)
 //
 // Short units (little more than the start and the merge they would cost) are dealt whole instead, one
 // after the other, and nothing is merged.
 //
 // Few rows (a chunk of at most 128 / g positions, a decode sequence): both chains take the same rows,
-// chain 0 every other tile and chain 1 the rest, and the merge joins them too.  Where such units fill the
-// SMs without being cut (a chunk of 600 positions of 32 heads over 8 is 152 of them), the chains' sums meet
-// in shared memory and nothing is merged.
+// chain 0 every other tile and chain 1 the rest.  In a unit that lies in one CTA (a chunk of 600 positions of
+// 32 heads over 8 is 152 of them, dealt whole; the short sequences of a ragged batch that is cut) the chains'
+// sums meet in shared memory; the pieces of a cut one hold both chains' sums, and the merge joins them too.
 //
 // Weights.  On bf16 pools with capped scores (and no bias) x lies in [-cap, cap], so the softmax needs
 // no maximum: 2^(x - cap / 2) fits fp32 and bf16 for caps up to 55 (80 in log2 units), and a score
@@ -54,13 +54,12 @@
 
 #include "kvc_decode_tc.cuh"
 #include "kvc_mod.cuh"
+#include "kvc_mod_line.cuh"
 
 namespace kvc {
 
 constexpr int kMtKeys = 64;                        // keys per tile
 constexpr int kMtBlocks = kMtKeys / kBS;
-constexpr int kMtUnits = 2048;                     // most units (per head) of one launch
-constexpr int kMtStart = 8;                        // a unit's start and end, in tiles (4: 600 queries over 1 800 44 us, 8: 40)
 constexpr int kMtJoin = 2;                         // the meeting of two chains, in tiles
 constexpr int kMtCut = 16;                         // what cutting units costs a CTA, in tiles (run_tc)
 constexpr int kMtBrief = 16;                       // a CTA's share of the line up to which kMtCappedBrief serves
@@ -70,8 +69,7 @@ struct ModTcParams {
     ModParams m;          // m.d.ppu: positions per query tile (a decode sequence's one)
     int32_t units;        // units per head
     int32_t whole;        // 1: no partials, units are dealt whole
-    int32_t split;        // 1: a unit is one query tile's positions, and both chains take its rows (below);
-                          // with whole set, they meet in the CTA
+    int32_t split;        // 1: a unit is one query tile's positions, and both chains take its rows (below)
     int32_t total;        // positions the row holds (prefill)
     int32_t *prefix;      // few-row calls: [units + 1] place of each unit on a head's line, for the merge
     int4 *cuts;           // other calls: [G] {head, unit, pieces (0: none), slot} of the unit that CTA c starts
@@ -111,7 +109,8 @@ struct ModTcCfg {
     static constexpr int NBARS = 7 * R + 14;
     static constexpr int MEET_PART = 128 * 128;        // where chains meet: 128 rows x 32 fp32 columns, twice
     static constexpr int MISC = BARS + NBARS * 8;      // scan sums [16], abort, TMEM base, block masks [16]
-    static constexpr int END = MISC + 160;
+    static constexpr int MEET_SUMS = (MISC + 160 + 15) / 16 * 16;   // (m, l, divisor) of chain 1's 128 rows
+    static constexpr int END = MEET_SUMS + 128 * 16;
     static constexpr int MEET = QTILE >= 2 * MEET_PART ? Q + QTILE : END;   // chain 1's query tile if it is large enough
     static constexpr int SMEM = 1024 + (MEET == END ? END + 2 * MEET_PART : END);
     static_assert(SMEM <= 232448, "shared memory of a CTA");
@@ -355,66 +354,12 @@ __device__ __forceinline__ int unit_tiles(const ModTcParams &p, int u)
     return max(1, (br.n + kMtBlocks - 1) / kMtBlocks);
 }
 
-// A run of key tiles [k0, k1) of (head, unit).
-struct Segment {
-    int head, unit, k0, k1, tiles;
-    bool ok;
-};
-
-// Walks a CTA's share of the line; every role makes the same walk.  A unit's first kMtStart places
-// hold no tile.
-struct Walk {
-    const int32_t *prefix;
-    int units, per_head;
-    int64_t at, end;      // whole: unit counters instead of places
-    bool whole;
-    int stride;
-    __device__ __forceinline__ Segment next()
-    {
-        Segment s;
-        s.ok = at < end;
-        if (!s.ok) return s;
-        if (whole) {
-            s.head = static_cast<int>(at / units);
-            s.unit = static_cast<int>(at % units);
-            s.k0 = 0;
-            s.tiles = s.k1 = 0;   // the caller's: see unit_of
-            at += stride;
-            return s;
-        }
-        s.head = static_cast<int>(at / per_head);
-        const int r = static_cast<int>(at - static_cast<int64_t>(s.head) * per_head);
-        int lo = 0, hi = units;   // prefix[lo] <= r < prefix[hi]
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (prefix[mid] <= r) lo = mid;
-            else hi = mid;
-        }
-        s.unit = lo;
-        s.tiles = prefix[lo + 1] - prefix[lo] - kMtStart;
-        const int64_t first = static_cast<int64_t>(s.head) * per_head + prefix[lo] + kMtStart;   // place of its tile 0
-        s.k0 = static_cast<int>(max(at - first, static_cast<int64_t>(0)));
-        s.k1 = static_cast<int>(min(static_cast<int64_t>(s.tiles), end - first));
-        s.ok = s.k1 > s.k0;   // else the share ends before the unit's first tile
-        at = first + s.k1;
-        return s;
-    }
-};
-
 // The view of a segment's unit; a whole unit's segment gets its tiles from it.
 __device__ __forceinline__ UnitView unit_of(const ModTcParams &p, Segment &s, int lane)
 {
     const UnitView v = unit_view(p, s.unit, lane);
     if (p.whole) s.tiles = s.k1 = v.tiles;
     return v;
-}
-
-// The CTA that has place w of a line of W shared by G: the last c with c W / G <= w.
-__device__ __forceinline__ int cta_of(int64_t w, int64_t W, int64_t G)
-{
-    const int64_t num = (w + 1) * G - 1;
-    if (W * G < 0x7FFFFFFF) return static_cast<int>(static_cast<uint32_t>(num) / static_cast<uint32_t>(W));
-    return static_cast<int>(num / W);
 }
 
 // tmap: the pool's map of 16-row boxes (bf16), else the map of whole blocks.
@@ -527,22 +472,7 @@ __global__ void __launch_bounds__(ModTcCfg<D, KIND>::THREADS, 1) mod_tc_kernel(c
         }
         __syncthreads();
     }
-    Walk walk;
-    walk.prefix = prefix;
-    walk.units = tp.units;
-    walk.per_head = tp.whole ? 1 : prefix[tp.units];
-    walk.whole = tp.whole != 0;
-    walk.stride = gridDim.x;
-    const int64_t W = static_cast<int64_t>(p.H_KV) * walk.per_head;
-    const int64_t G = min(static_cast<int64_t>(gridDim.x), W);
-    if (walk.whole) {
-        walk.at = blockIdx.x;
-        walk.end = static_cast<int64_t>(p.H_KV) * tp.units;
-    } else {
-        const bool idle = blockIdx.x >= G;
-        walk.at = idle ? 0 : blockIdx.x * W / G;
-        walk.end = idle ? 0 : (blockIdx.x + 1) * W / G;
-    }
+    Walk walk(prefix, tp.units, p.H_KV, blockIdx.x, gridDim.x, tp.whole != 0);
 
     // TMEM columns: query tile x has its score buffers at 128 x and 128 x + 64, its outputs at 256 + 128 x
     bool timed_out = false;
@@ -831,7 +761,6 @@ __global__ void __launch_bounds__(ModTcCfg<D, KIND>::THREADS, 1) mod_tc_kernel(c
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + 128 * x + lane_off, to = tmem + 256 + 128 * x + lane_off;
         const float ref = 0.5f * mp.cap_out;
-        const bool join = tp.split && tp.whole;   // the two chains' sums meet here, not in the merge
         auto bar_both = [] { asm volatile("bar.sync 6, 256;" ::: "memory"); };   // both chains' threads
         uint32_t it = 0, kt = 0;   // this query tile's steps, key tiles so far
         int piece = 0;             // segments so far
@@ -842,6 +771,7 @@ __global__ void __launch_bounds__(ModTcCfg<D, KIND>::THREADS, 1) mod_tc_kernel(c
             kt += s.k1 - s.k0;
             const int c0 = v.pos0 + (tp.split ? 0 : x * ppt);
             const bool mine = c0 < p.n_pos;
+            const bool join = tp.split && s.all();   // the two chains' sums meet here, not in the merge
             // up to 64 rows in a few-row call: chain 1's sit in the tile's upper half, so that the warps that have
             // work to do are on different schedulers
             const int ro = tp.split && !join && x == 1 && min(ppt, p.n_pos - c0) * g <= 64 ? 64 : 0;
@@ -1240,25 +1170,26 @@ __global__ void __launch_bounds__(ModTcCfg<D, KIND>::THREADS, 1) mod_tc_kernel(c
                 mbar_arrive(pfull(x, b));
             }
             if (go && steps > 0) go = wait(pvdone(x, (it - 1) & 1), ((it - 1) >> 1) & 1);   // the segment's last product
-            // every thread of the query tile takes this vote once per segment, so the barriers below meet
-            if (!tile_all(go, join ? 6 : 4 + x, join ? 256 : 128)) {
+            // every thread of the query tile takes this vote once per segment, so the barriers below meet; of both
+            // tiles where the chains share rows: the next segment may be one in which they meet
+            if (!tile_all(go, tp.split ? 6 : 4 + x, tp.split ? 256 : 128)) {
                 timed_out = true;
                 break;
             }
             tc_fence_after();
 
             // ---- epilogue: the unit's rows, or a piece of them for the merge (rows [128 x, 128 x + 128) of a slot)
-            const bool done = s.k0 == 0 && s.k1 == s.tiles && !tp.split;
+            const bool done = s.all() && !tp.split;
             if (!any_real && !join) continue;
-            const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (piece > 0 ? 1 : 0);
+            const int64_t slot = piece_slot(blockIdx.x, piece);
             if (tid == 0 && !done && !tp.whole && s.k0 == 0) {
                 const int64_t end = static_cast<int64_t>(s.head) * walk.per_head + prefix[s.unit + 1];
-                cut = make_int4(s.head, s.unit, cta_of(end - 1, W, G) - static_cast<int>(blockIdx.x) + 1, static_cast<int>(slot));
+                cut = make_int4(s.head, s.unit, cta_of(end - 1, walk.W, walk.G) - static_cast<int>(blockIdx.x) + 1, static_cast<int>(slot));
             }
             const int prow = x * 128 + rq;
             float inv = l == 0.f ? 0.f : 1.f / (l + dl), other = 0.f;
             if (join) {   // chain 1 hands over m, l and the sum that its outputs go with; chain 0 weighs both
-                float4 *meet = reinterpret_cast<float4 *>(smem + C::PREFIX);
+                float4 *meet = reinterpret_cast<float4 *>(smem + C::MEET_SUMS);
                 if (x == 1) meet[row] = make_float4(m, l, l + dl, 0.f);
                 bar_both();
                 if (x == 0) {
@@ -1419,10 +1350,11 @@ __global__ void __launch_bounds__(256) mod_tc_merge_kernel(const ModTcParams tp,
         head = blockIdx.z;
         const int per_head = __ldcg(tp.prefix + tp.units), u0 = __ldcg(tp.prefix + unit), u1 = __ldcg(tp.prefix + unit + 1);
         const int64_t W = static_cast<int64_t>(p.H_KV) * per_head, G = min(static_cast<int64_t>(ctas), W);
-        const int64_t a = static_cast<int64_t>(head) * per_head + u0, b = static_cast<int64_t>(head) * per_head + u1;
-        const int cf = cta_of(a + kMtStart, W, G), cl = cta_of(b - 1, W, G);   // CTAs of the unit's first and last tile
-        n = (cl - cf + 1) * 2;
-        slot0 = 2 * cf + (a > 0 && cta_of(a - 1, W, G) == cf ? 1 : 0);   // places before the unit: its second piece
+        const int64_t at = static_cast<int64_t>(head) * per_head;
+        const Pieces ps = pieces_of(at + u0, at + u1, W, G);
+        if (ps.ctas == 1) return;   // finished by its CTA (the same for the whole block)
+        n = ps.ctas * 2;
+        slot0 = ps.slot0;
     }
     const int c = unit * unit_positions_of(tp) + pr;
     const bool real = r < p.ppu * g && c < p.n_pos;
