@@ -395,7 +395,7 @@ static DecodeKernel prefill_tc_for(const kvc_pool *pool)
 
 // grid (1, KV head, tile of 128 / g positions).  dependent: launched as a
 // programmatic dependent of the kernel before it on the stream, whose CTAs it may
-// run beside (it reads nothing that kernel writes and never waits on it).
+// run beside (it reads nothing that kernel writes, and waits for it only to end after it).
 static kvc_status launch_prefill_tc(const kvc_pool *pool, DecodeParams &p, const DecodeKernel &k, bool dependent,
                                     cudaStream_t stream)
 {
@@ -576,7 +576,7 @@ extern "C" kvc_status kvc_mixed_step(kvc_pool *pool, int32_t layer, const void *
     if (static_cast<int64_t>(q_start) + n_q > static_cast<int64_t>(prefill_max_blocks) * kBS) return KVC_ERR_RANGE;
     if (const DecodeKernel tc = prefill_tc_for(pool); tc.fn) {
         // the decode step, then the chunk on the tensor-memory prefill kernel as a programmatic
-        // dependent: its CTAs take SMs as the decode CTAs drain, and it never waits on them
+        // dependent: its CTAs take SMs as the decode CTAs drain, and their work never waits on them
         st = kvc_decode_step(pool, layer, q, num_q_heads, block_tables, max_blocks, seq_lens, B, k_new, v_new, out, lse,
                              scale, stream);
         if (st != KVC_OK) return st;

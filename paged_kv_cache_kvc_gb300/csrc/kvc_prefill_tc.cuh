@@ -461,12 +461,17 @@ __device__ __forceinline__ void prefill_tc_cta(const CUtensorMap &tmap16, const 
 
 // grid (1, KV head, tile of 128 / g positions), 384 threads.  Launched as a
 // programmatic dependent in the mixed step: it reads only the chunk's row,
-// which the step before it does not write, so it never waits on that step.
+// which the step before it does not write, so its work never waits on that
+// step.  Its last CTA does, when its work is done: a programmatic dependent of
+// this grid (a rotary write, the next step) waits for this grid alone, so this
+// grid has to end after the step that it ran beside.  (The step's CTAs are all
+// in place before this grid's begin, so the wait ends.)
 template <int D>
 __global__ void __launch_bounds__(kPtThreads, 1) prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap16,
                                                                     const DecodeParams p)
 {
     prefill_tc_cta<D>(tmap16, p, blockIdx.z, blockIdx.y);
+    if (threadIdx.x == 0 && blockIdx.y == gridDim.y - 1 && blockIdx.z == gridDim.z - 1) grid_dependency_wait();
 }
 
 // The tensor-memory prefill kernel for a pool (fn = nullptr: d_h 64 / 128 bf16 pools only).
