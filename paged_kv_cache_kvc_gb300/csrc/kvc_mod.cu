@@ -206,7 +206,8 @@ static kvc_status run_tc(kvc_pool *pool, const ModParams &mp0, int visit, void *
     if (!k.fn) return KVC_ERR_UNSUPPORTED;
     if (k.ctas_per_sm <= 0) return KVC_ERR_CUDA;
     const int unit = tp.split ? p.ppu : 2 * p.ppu;   // positions per unit
-    const int per_launch = kMtUnits * unit, n_q = p.n_pos, start = p.len_base;
+    const int units = tp.whole ? kMtUnits : units_per_launch((static_cast<int64_t>(p.max_blocks) + kMtBlocks - 1) / kMtBlocks);
+    const int per_launch = units * unit, n_q = p.n_pos, start = p.len_base;
     for (int at = 0; at < n_q; at += per_launch) {
         p.n_pos = std::min(per_launch, n_q - at);
         p.len_base = start + at;

@@ -16,6 +16,14 @@ namespace kvc {
 constexpr int kMtUnits = 2048;                     // most units (per head) of one launch
 constexpr int kMtStart = 8;                        // a unit's start and end, in tiles (4: 600 queries over 1 800 44 us, 8: 40)
 
+// Units (per head) of one launch: at most kMtUnits, and so few that a head's places stay inside 32 bits however long its
+// units are (2 048 units of 16 million positions would pass them).
+inline int units_per_launch(int64_t longest_unit)
+{
+    const int64_t n = 0x7FFFFFFF / (longest_unit + kMtStart);
+    return static_cast<int>(n < 1 ? 1 : (n < kMtUnits ? n : kMtUnits));
+}
+
 // A run of key tiles [k0, k1) of (head, unit).
 struct Segment {
     int head, unit, k0, k1, tiles;

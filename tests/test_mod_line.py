@@ -124,3 +124,20 @@ def test_long_lines_pass_32_bits(walk):
     """Places times CTAs past 2^31, and a line of more than 2^31 places."""
     for case in [(8, 152, [500000] * 40 + [3] * 100), (64, 152, [1 << 24] * 8 + [1])]:
         hold(*case, walk([case])[0])
+
+
+def test_a_launch_keeps_its_places_inside_32_bits(tmp_path):
+    """A call's tables hold up to 2^26 blocks (2^24 tiles a unit), a launch up to 2 048 units a head."""
+    nvcc = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "bin", "nvcc")
+    nvcc = nvcc if os.path.exists(nvcc) else shutil.which("nvcc")
+    if not nvcc:
+        pytest.skip("nvcc not available")
+    tiles = sorted({1, 2, 313, 2 ** 19, 2 ** 20, *(2 ** e + d for e in range(2, 25) for d in (-1, 0, 1) if 2 ** e + d <= 2 ** 24)})
+    body = "".join(f'printf("%d %d\\n", kvc::units_per_launch({t}), kvc::kMtStart);\n' for t in tiles)
+    (tmp_path / "units.cu").write_text(f'#include <cstdio>\n#include "{HEADER}"\nint main() {{\n{body}return 0;\n}}\n')
+    subprocess.check_call([nvcc, "-std=c++17", "-o", str(tmp_path / "units"), str(tmp_path / "units.cu")], cwd=tmp_path)
+    out = subprocess.check_output([str(tmp_path / "units")], text=True).splitlines()
+    for t, line in zip(tiles, out, strict=True):
+        units, start = map(int, line.split())
+        assert 1 <= units <= 2048 and units * (t + start) < 2 ** 31
+        assert units == 2048 or (units + 1) * (t + start) >= 2 ** 31   # no more launches than that takes
