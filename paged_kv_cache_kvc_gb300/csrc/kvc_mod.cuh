@@ -22,8 +22,7 @@
 // at (a serving engine frees them).  Blocks that some column may not read in
 // full mask per column; the other blocks mask nothing.
 #pragma once
-#include <mutex>
-
+#include "kvc_configured.cuh"
 #include "kvc_decode.cuh"
 
 namespace kvc {
@@ -678,28 +677,6 @@ __global__ void __launch_bounds__(kThreads) mod_kernel(const __grid_constant__ C
             make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
     }
     if (threadIdx.x == 0) p.counters[static_cast<size_t>(b) * p.H_KV + h] = 0u;   // ready for the next call
-}
-
-// A kernel with its dynamic shared memory, configured once on every device that it runs on.  Tag: one per kernel.
-template <typename Tag>
-DecodeKernel configured(const void *fn, int smem, int threads, bool tmap16)
-{
-    constexpr int kDevices = 64;
-    static std::once_flag once[kDevices];
-    static DecodeKernel kernels[kDevices];
-    int dev = -1;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return DecodeKernel{nullptr, 0, 0};
-    std::call_once(once[dev], [&] {
-        DecodeKernel &k = kernels[dev];
-        k = DecodeKernel{fn, smem, 0};
-        k.threads = threads;
-        k.tmap16 = tmap16;
-        int n = 0;
-        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess &&
-            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, threads, smem) == cudaSuccess)
-            k.ctas_per_sm = n;
-    });
-    return kernels[dev];
 }
 
 template <int D, int NT, int KIND, bool PSPLIT, bool TILE>

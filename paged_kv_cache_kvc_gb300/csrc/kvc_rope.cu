@@ -20,7 +20,7 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "kvc_decode.cuh"
+#include "kvc_configured.cuh"
 
 namespace kvc {
 
@@ -333,9 +333,12 @@ __global__ void __launch_bounds__(kRopeCta, 3) rope_kernel(const RopeParams p)
 }
 
 template <int D, int GPT, int U>
-static cudaError_t launch_rope(const RopeParams &p, int sms, cudaStream_t stream)
+static kvc_status launch_rope(const RopeParams &p, int sms, cudaStream_t stream)
 {
     constexpr int TPC = kRopeThreads / (D / 8) / GPT;
+    struct Tag {};
+    const DecodeKernel k = configured<Tag>(reinterpret_cast<const void *>(&rope_kernel<D, GPT, U>), 0, kRopeCta, false);
+    if (k.ctas_per_sm <= 0) return KVC_ERR_CUDA;
     // A programmatic dependent: its launch overlaps the tail of the kernel before it, which it
     // waits for before its first access.  It never lets its own dependents start early: the
     // chunk's kernel of kvc_mixed_step starts without waiting for the kernel before the step,
@@ -344,16 +347,15 @@ static cudaError_t launch_rope(const RopeParams &p, int sms, cudaStream_t stream
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    static const int resident = [] {
-        int n = 0;
-        return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, rope_kernel<D, GPT, U>, kRopeCta, 0) == cudaSuccess && n > 0 ? n : 1;
-    }();
-    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>((p.rows + TPC - 1) / TPC, static_cast<int64_t>(sms) * resident)));
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>((p.rows + TPC - 1) / TPC, static_cast<int64_t>(sms) * k.ctas_per_sm)));
     cfg.blockDim = dim3(kRopeCta);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, rope_kernel<D, GPT, U>, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, rope_kernel<D, GPT, U>, p);
+    if (e != cudaSuccess) return cuda_status(e);
+    g_launches.fetch_add(1, std::memory_order_relaxed);
+    return KVC_OK;
 }
 
 static bool aligned(const void *ptr, size_t a) { return (reinterpret_cast<uintptr_t>(ptr) & (a - 1)) == 0; }
@@ -431,16 +433,11 @@ static kvc_status rope_write(kvc_pool *pool, int32_t layer, const int32_t *bt, i
     // 6.6; 4 000 tokens 32.5, 23.8 and 19.9; 16 384 tokens 121, 93 and 72.  Three rows in flight spill.
     const int sms = pool->num_sms;
     const int size = rows <= 2ll * sms ? 0 : (rows <= 8ll * sms ? 1 : 2);
-    cudaError_t e;
     if (D == 64)
-        e = size == 0 ? launch_rope<64, 32, 1>(p, sms, stream)
-                      : (size == 1 ? launch_rope<64, 8, 1>(p, sms, stream) : launch_rope<64, 2, 2>(p, sms, stream));
-    else
-        e = size == 0 ? launch_rope<128, 16, 1>(p, sms, stream)
-                      : (size == 1 ? launch_rope<128, 8, 1>(p, sms, stream) : launch_rope<128, 4, 2>(p, sms, stream));
-    if (e != cudaSuccess) return cuda_status(e);
-    g_launches.fetch_add(1, std::memory_order_relaxed);
-    return KVC_OK;
+        return size == 0 ? launch_rope<64, 32, 1>(p, sms, stream)
+                         : (size == 1 ? launch_rope<64, 8, 1>(p, sms, stream) : launch_rope<64, 2, 2>(p, sms, stream));
+    return size == 0 ? launch_rope<128, 16, 1>(p, sms, stream)
+                     : (size == 1 ? launch_rope<128, 8, 1>(p, sms, stream) : launch_rope<128, 4, 2>(p, sms, stream));
 }
 
 }  // namespace kvc
