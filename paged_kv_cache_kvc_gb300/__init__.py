@@ -350,12 +350,15 @@ _call = None
 
 
 def _native():
-    """The native marshalling module of the calls below (once).  Raises if it has not been built."""
+    """The native marshalling module of the calls below (once).  Raises if it has not been built against this torch."""
     global _call
     if _call is None:
         load()
         if not os.path.exists(CALL_PATH):
             raise RuntimeError(f"the kvc binding is not built ({CALL_PATH} missing); run __graft_entry__.build()")
+        from . import build
+        if not build.call_current():   # it reads torch's C++ objects directly
+            raise RuntimeError(f"{CALL_PATH} was built against another torch or Python; run __graft_entry__.build()")
         loader = importlib.machinery.ExtensionFileLoader("_kvc_call", CALL_PATH)
         _call = importlib.util.module_from_spec(importlib.util.spec_from_loader("_kvc_call", loader))
         loader.exec_module(_call)

@@ -11,6 +11,7 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(OUT_DIR, "libkvc.so")
 CALL_PATH = os.path.join(OUT_DIR, "_kvc_call.so")
+CALL_STAMP = CALL_PATH + ".abi"   # what _kvc_call.so was built against, see call_abi
 ROOT = os.path.dirname(HERE)
 
 SOURCES = ["kvc_core.cu", "kvc_attn.cu", "kvc_decode_bf16.cu", "kvc_decode_fp8.cu", "kvc_decode_int4.cu",
@@ -33,19 +34,52 @@ def _stale(target: str, deps: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def call_commands() -> tuple[list[str], list[str]]:
-    """Compile and link commands of the marshalling module."""
+def call_abi() -> str:
+    """What the marshalling module depends on beside its sources: torch's C++ classes and the interpreter's objects."""
+    import sysconfig
+    import torch
+    return f"torch {torch.__version__} {os.path.dirname(torch.__file__)} python {sysconfig.get_config_var('SOABI')}"
+
+
+def call_current() -> bool:
+    """Whether the marshalling module was built against the torch and Python that run now."""
+    try:
+        with open(CALL_STAMP) as f:
+            return f.read() == call_abi()
+    except OSError:
+        return False
+
+
+def call_stale() -> bool:
+    """Whether the marshalling module is missing, older than its sources, or built against another torch or Python."""
+    sources = [os.path.join(CSRC, "kvc_call.cpp"), os.path.join(ROOT, "include", "kvc.h")]
+    return _stale(CALL_PATH, sources) or not call_current()
+
+
+def _replace(path: str, make) -> None:
+    """make(temporary path), then the file takes its place at once: a process that has the old one mapped keeps it."""
+    tmp = f"{path}.tmp{os.getpid()}"
+    try:
+        make(tmp)
+        os.replace(tmp, path)
+    finally:
+        if os.path.exists(tmp):
+            os.remove(tmp)
+
+
+def call_commands(out: str = CALL_PATH) -> tuple[list[str], list[str]]:
+    """Compile and link commands of the marshalling module, through out + ".o"."""
     import sysconfig
     import torch
     home = os.path.dirname(torch.__file__)
     cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
-    obj = os.path.join(OUT_DIR, "kvc_call.o")
+    obj = out + ".o"
     compile_ = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
                 f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I" + os.path.join(home, "include"),
                 "-I" + os.path.join(home, "include", "torch", "csrc", "api", "include"),
                 "-I" + os.path.join(cuda, "include"), "-I" + sysconfig.get_paths()["include"],
                 "-c", os.path.join(CSRC, "kvc_call.cpp"), "-o", obj]
-    link = ["g++", "-shared", "-o", CALL_PATH, obj, "-L" + OUT_DIR, "-l:libkvc.so", "-Wl,-rpath,$ORIGIN",
+    link = ["g++", "-shared", "-o", out, obj, "-L" + OUT_DIR, "-l:libkvc.so", "-Wl,-rpath,$ORIGIN",
             "-L" + os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
     return compile_, link
 
@@ -65,11 +99,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
             if verbose:
                 print(" ".join(cmd), file=sys.stderr)
             procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
-    call_src = os.path.join(CSRC, "kvc_call.cpp")
-    call_stale = force or _stale(CALL_PATH, [call_src, os.path.join(ROOT, "include", "kvc.h")])
-    if call_stale:
-        call_compile, call_link = call_commands()
-        procs.append(("kvc_call.cpp", subprocess.Popen(call_compile, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+    call = force or call_stale()
+    call_tmp = f"{CALL_PATH}.tmp{os.getpid()}"
+    if call:
+        procs.append(("kvc_call.cpp", subprocess.Popen(call_commands(call_tmp)[0], stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     failed = []
     for src, p in procs:
         out, _ = p.communicate()
@@ -78,13 +111,17 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
         elif verbose and out:
             print(out.decode(errors="replace"), file=sys.stderr)
     if failed:
+        if os.path.exists(call_tmp + ".o"):
+            os.remove(call_tmp + ".o")
         raise RuntimeError("nvcc failed:\n" + "\n".join(f"--- {s}\n{o}" for s, o in failed))
     if force or procs or _stale(LIB_PATH, objs):
-        tmp = LIB_PATH + f".tmp{os.getpid()}"
-        subprocess.check_call([nvcc()] + ARCH + ["-shared", "-Xlinker", "-z,defs", "-o", tmp] + objs)
-        os.replace(tmp, LIB_PATH)
-    if call_stale:
-        subprocess.check_call(call_link)
+        _replace(LIB_PATH, lambda tmp: subprocess.check_call(
+            [nvcc()] + ARCH + ["-shared", "-Xlinker", "-z,defs", "-o", tmp] + objs))
+    if call:
+        _replace(CALL_PATH, lambda tmp: subprocess.check_call(call_commands(tmp)[1]))   # the object made above
+        os.remove(call_tmp + ".o")
+        with open(CALL_STAMP, "w") as f:   # last: without it the module counts as stale
+            f.write(call_abi())
     return LIB_PATH
 
 
