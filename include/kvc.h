@@ -414,7 +414,8 @@ KVC_API kvc_status kvc_mod_workspace_bytes(const kvc_pool *pool, int32_t rows, i
 /* kvc_decode_attn with modified scores (mod = NULL: none).  The query of
  * sequence b sits at position seq_lens[b] - 1.
  *   out: device bf16 [B][H_Q][d_h] (what a model's next projection takes),
- *        16-byte aligned;  lse: device fp32 [B][H_Q] or NULL (natural log, of
+ *        16-byte aligned; may be q itself, and must not overlap it otherwise
+ *        (KVC_ERR_ARG);  lse: device fp32 [B][H_Q] or NULL (natural log, of
  *        the modified scores)
  *   scale: finite and > 0
  *   workspace: see kvc_mod_workspace_bytes; NULL plans one split per

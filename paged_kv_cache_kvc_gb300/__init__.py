@@ -423,8 +423,8 @@ def kvc_mod_workspace(pool, rows, num_q_heads, max_blocks) -> torch.Tensor:
 
 def kvc_decode_attn_mod(pool, layer, q, block_tables, seq_lens, out, lse=None, mod=None, scale=None, workspace=None,
                         stream=None):
-    """kvc_decode_attn with modified scores; out is bf16.  workspace: kvc_mod_workspace, or None (no splits: slow
-    for few long sequences).  The stream defaults to torch's current stream of the pool's device."""
+    """kvc_decode_attn with modified scores; out is bf16 and may be q.  workspace: kvc_mod_workspace, or None (no
+    splits: slow for few long sequences).  The stream defaults to torch's current stream of the pool's device."""
     s = (_call or _native()).decode_attn_mod(pool.args, layer, q, block_tables, seq_lens, out, lse,
                                              None if mod is None else mod.args, scale, workspace,
                                              None if stream is None else _stream(stream))
@@ -434,7 +434,7 @@ def kvc_decode_attn_mod(pool, layer, q, block_tables, seq_lens, out, lse=None, m
 
 def kvc_prefill_attn_mod(pool, layer, q, block_table_row, q_start, out, lse=None, mod=None, scale=None,
                          workspace=None, stream=None):
-    """kvc_prefill_attn with modified scores; out is bf16, workspace and stream as for kvc_decode_attn_mod."""
+    """kvc_prefill_attn with modified scores; out, workspace and stream as for kvc_decode_attn_mod."""
     s = (_call or _native()).prefill_attn_mod(pool.args, layer, q, block_table_row, q_start, out, lse,
                                               None if mod is None else mod.args, scale, workspace,
                                               None if stream is None else _stream(stream))

@@ -247,7 +247,7 @@ static kvc_status run_tc(kvc_pool *pool, const ModParams &mp0, int visit, void *
     return KVC_OK;
 }
 
-static kvc_status mod_checks(kvc_pool *pool, int32_t layer, const void *q, int32_t H_Q, const int32_t *bt,
+static kvc_status mod_checks(kvc_pool *pool, int32_t layer, const void *q, int32_t rows, int32_t H_Q, const int32_t *bt,
                              int32_t max_blocks, const kvc_score_mod *mod, void *out, float *lse, float scale, void *ws)
 {
     if (!pool || !q || !bt || !out) return KVC_ERR_ARG;
@@ -257,6 +257,11 @@ static kvc_status mod_checks(kvc_pool *pool, int32_t layer, const void *q, int32
     // scores are compared before they are scaled: a scale that is not positive would turn their order
     if (!std::isfinite(scale) || scale <= 0.f) return KVC_ERR_ARG;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(bt, 4) || !aligned(ws, 256)) return KVC_ERR_ARG;
+    // out may be q: a row is written by the unit that has read it, or by the merge after every unit.  Shifted, a unit
+    // would write rows that another has yet to read.
+    const uintptr_t q0 = reinterpret_cast<uintptr_t>(q), o0 = reinterpret_cast<uintptr_t>(out);
+    const uintptr_t bytes = static_cast<uintptr_t>(rows) * H_Q * pool->D * 2;
+    if (q0 != o0 && q0 < o0 + bytes && o0 < q0 + bytes) return KVC_ERR_ARG;
     if (mod) {
         if (!std::isfinite(mod->softcap) || mod->softcap < 0.f || mod->window < 0 || mod->sink < 0 || mod->prefix < 0)
             return KVC_ERR_ARG;
@@ -345,7 +350,7 @@ extern "C" kvc_status kvc_decode_attn_mod(kvc_pool *pool, int32_t layer, const v
     if (B == 0) return pool ? KVC_OK : KVC_ERR_ARG;
     if (!seq_lens || !aligned(seq_lens, 4)) return KVC_ERR_ARG;
     if (mod && mod->doc_start) return KVC_ERR_ARG;
-    kvc_status st = mod_checks(pool, layer, q, num_q_heads, block_tables, max_blocks, mod, out, lse, scale, workspace);
+    kvc_status st = mod_checks(pool, layer, q, B, num_q_heads, block_tables, max_blocks, mod, out, lse, scale, workspace);
     if (st != KVC_OK) return st;
     ModParams mp{};
     fill(mp, pool, layer, q, num_q_heads, block_tables, max_blocks, mod, out, lse, scale);
@@ -368,7 +373,7 @@ extern "C" kvc_status kvc_prefill_attn_mod(kvc_pool *pool, int32_t layer, const 
 {
     if (n_q < 0 || n_q > 65535 || q_start < 0) return KVC_ERR_ARG;
     if (n_q == 0) return pool ? KVC_OK : KVC_ERR_ARG;
-    kvc_status st = mod_checks(pool, layer, q, num_q_heads, block_table_row, max_blocks, mod, out, lse, scale, workspace);
+    kvc_status st = mod_checks(pool, layer, q, n_q, num_q_heads, block_table_row, max_blocks, mod, out, lse, scale, workspace);
     if (st != KVC_OK) return st;
     if (static_cast<int64_t>(q_start) + n_q > static_cast<int64_t>(max_blocks) * kBS) return KVC_ERR_RANGE;
     ModParams mp{};
