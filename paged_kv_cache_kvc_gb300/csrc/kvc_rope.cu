@@ -174,8 +174,9 @@ __device__ __forceinline__ void build_factors(const RopeParams &p, RopeBatch<D, 
             const uint16_t *w = k ? p.k_norm : p.q_norm;
             const float wa = w ? __uint_as_float(static_cast<uint32_t>(__ldg(w + a)) << 16) : 1.f;
             const float wb = w ? __uint_as_float(static_cast<uint32_t>(__ldg(w + b)) << 16) : 1.f;
-            s.f[tk][k][a] = make_float2(wa * cs.x, -wb * cs.y);
-            s.f[tk][k][b] = make_float2(wb * cs.x, wa * cs.y);
+            // a channel that passes through has no mate: not even a weight that is not finite reaches it
+            s.f[tk][k][a] = make_float2(wa * cs.x, turn ? -wb * cs.y : 0.f);
+            s.f[tk][k][b] = make_float2(wb * cs.x, turn ? wa * cs.y : 0.f);
         }
     }
 }
