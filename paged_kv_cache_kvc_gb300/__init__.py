@@ -369,12 +369,18 @@ class Rope:
     """Position rotation (and optional per-head RMS norm) for kvc_rope_append / kvc_rope_write_tokens.
 
     inv_freq: CUDA fp32 [rotary_dim / 2], radians per position (None: no rotation); q_norm, k_norm: CUDA
-    bf16 [d_h] norm weights or None.  Holds the tensors; one object serves any number of calls."""
+    bf16 [d_h] norm weights or None.  Holds the tensors; one object serves any number of calls.  What it holds is
+    fixed (a tensor's values may change); another weight is another Rope."""
+
+    __slots__ = ("args", "__weakref__")
 
     def __init__(self, inv_freq=None, interleaved=False, q_norm=None, k_norm=None, eps=1e-6):
-        self.inv_freq, self.q_norm, self.k_norm = inv_freq, q_norm, k_norm
         dim = 0 if inv_freq is None else 2 * inv_freq.numel()
         self.args = (dim, int(bool(interleaved)), inv_freq, q_norm, k_norm, float(eps))
+
+    inv_freq = property(lambda self: self.args[2])
+    q_norm = property(lambda self: self.args[3])
+    k_norm = property(lambda self: self.args[4])
 
 
 def kvc_rope_append(pool, layer, block_tables, seq_lens, q, k_new, v_new, q_out, rope, stream=None):
@@ -404,11 +410,16 @@ def kvc_rope_write_tokens(pool, layer, block_tables, start_pos, cu_tokens, q, k,
 class ScoreMod:
     """Score modifiers and masks of kvc_decode_attn_mod / kvc_prefill_attn_mod (see kvc_score_mod in kvc.h).
 
-    softcap: at most 4096; alibi: CUDA fp32 [H_Q] slopes; doc_start: CUDA int32 [n_q] (prefill).  Holds the tensors."""
+    softcap: at most 4096; alibi: CUDA fp32 [H_Q] slopes; doc_start: CUDA int32 [n_q] (prefill).  Holds the tensors.
+    What it holds is fixed (a tensor's values may change); another chunk's doc_start is another ScoreMod."""
+
+    __slots__ = ("args", "__weakref__")
 
     def __init__(self, softcap=0.0, window=0, sink=0, prefix=0, alibi=None, doc_start=None):
-        self.alibi, self.doc_start = alibi, doc_start
         self.args = (float(softcap), int(window), int(sink), int(prefix), alibi, doc_start)
+
+    alibi = property(lambda self: self.args[4])
+    doc_start = property(lambda self: self.args[5])
 
 
 def kvc_mod_workspace(pool, rows, num_q_heads, max_blocks) -> torch.Tensor:
