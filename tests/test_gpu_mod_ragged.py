@@ -216,3 +216,21 @@ def test_many_short_sequences(kvc, many, dtype):
             c.check(out, lse, m)
     finally:
         c.close()
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("lens", [[8192, 50] * 16, [40] * 30], ids=["cut", "whole"])
+def test_expired_waits_are_reported(kvc, monkeypatch, lens, dtype):
+    """With every load withheld (a test hook) a cut call and a whole one report KVC_ERR_TIMEOUT and return, both chains
+    of every CTA together; with a fresh workspace the pool then works."""
+    c = Batch(kvc, lens, dtype=dtype)
+    try:
+        m = Mod(softcap=10.0)
+        monkeypatch.setenv("KVC_TEST_STALL", "1")
+        c.decode(m)
+        assert kvc.kvc_pool_sync_status(c.pool) == kvc.KVC_ERR_TIMEOUT
+        monkeypatch.delenv("KVC_TEST_STALL")
+        c.ws.zero_()
+        c.check(*c.decode(m), m)
+    finally:
+        c.close()
