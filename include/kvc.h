@@ -421,6 +421,11 @@ KVC_API kvc_status kvc_mod_workspace_bytes(const kvc_pool *pool, int32_t rows, i
  *   workspace: see kvc_mod_workspace_bytes; NULL plans one split per
  *        (sequence, KV head): no extra memory, slow for few long sequences;
  *        one too small for the call is KVC_ERR_ARG
+ * Softmax weights enter the value product as a bf16 high / low pair (16 bits)
+ * on bf16 pools with up to 16 query heads per KV head; as one bf16 with more
+ * (kvc_decode_attn keeps the pair for groups of 32 heads of 128 channels) and
+ * in kvc_prefill_attn_mod; as f16 on e4m3 and int4 pools.  Scores, sums and
+ * outputs are fp32 until the outputs' one rounding.
  * The library allocates nothing, so calls may be captured into a graph at any
  * time.  Other arguments, requirements and errors as kvc_decode_attn. */
 KVC_API kvc_status kvc_decode_attn_mod(kvc_pool *pool, int32_t layer, const void *q, int32_t num_q_heads,

@@ -280,7 +280,7 @@ __device__ __forceinline__ void block_update(uint32_t st, const uint32_t (&qf)[N
     // exceeds it by more than kRescaleSlack (log2 units): below that the weights
     // 2^(s - m_run) stay under 2^kRescaleSlack, l and O keep the same reference, and
     // the output accumulators need no rescale -- the warp skips it unless one of its
-    // columns moved (conditional rescaling, as in FlashAttention-4).  The merge and
+    // columns moved (conditional rescaling, a published technique).  The merge and
     // lse use each partial's own reference, so the result is the same softmax.
     uint32_t pb[NT][2], pl[NT][2];
     float alpha[NT][2];

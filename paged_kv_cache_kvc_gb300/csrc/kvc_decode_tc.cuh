@@ -33,7 +33,7 @@
 //               x = scale * s (log2 units), p = 2^(x - m_ref) with a per-head
 //               reference max m_ref that moves only when some score exceeds it
 //               by more than 8 (then O^T and the partial sums are rescaled by
-//               2^(m_old - m_new); conditional rescaling as in FlashAttention-4).
+//               2^(m_old - m_new); conditional rescaling, a published technique).
 //               Whether any head must move is one CTA-wide vote (bar.red.or);
 //               only then are per-head maxima reduced across the 128 threads.
 //               P^T row t (high and low bf16 parts) goes to shared memory.

@@ -167,9 +167,10 @@ static bool use_tc(const kvc_pool *pool)
 }
 
 // Decode groups of query heads from which the tensor-memory kernel serves a step.  Measured, capped, 32 heads, us against
-// the split kernel's: 8 x 32 768 positions bf16 46 / 44, e4m3 40 / 44, int4 51 / 52; 1 x 32 768: 34 / 37, 38 / 38, 35 / 43;
-// 64 x 1 000: 20 / 36, 25 / 37, 25 / 41.  Smaller groups: 8 heads, 8 x 8 192 x 4 KV heads 42 / 32; 16 heads (bf16, whose
-// weights the split kernel feeds as 16 bits), 8 x 8 192 x 2: 27 / 19.
+// the split kernel's, bf16, e4m3, int4: 8 x 32 768 positions 45 / 44, 43 / 45, 50 / 53 (as good as level); 1 x 32 768:
+// 34 / 37, 37 / 37, 38 / 42; 64 x 1 000: 20 / 37, 23 / 36, 25 / 40; ragged, bf16: 64 of 117 .. 30 000 63 / 120, 5 x 32 768
+// beside 59 x 16 46 / 120, but 1 x 32 768 beside 79 x 500 371 / 119 (dealt whole, run_tc).  Smaller groups: 8 heads,
+// 8 x 8 192 x 4 KV heads 42 / 32; 16 heads (bf16, whose weights the split kernel feeds as 16 bits), 8 x 8 192 x 2: 27 / 19.
 constexpr int kTcGroup = 17;
 
 // A chunk (or a decode batch of large head groups) on the tensor-memory kernel, as many units at a time as one
@@ -186,9 +187,11 @@ static kvc_status run_tc(kvc_pool *pool, const ModParams &mp0, int visit, void *
     // the busiest CTA's time in tiles of 1.1 us.  A unit costs its tiles (joined: half of them, and kMtJoin) and
     // kMtStart; cutting costs the partials' way through memory and the merge, together about kMtCut.  The lengths of
     // documents and of decode sequences are not known here: documents are taken as a quarter of the row, sequences as
-    // full.  Measured, 32 heads over 8, us dealt / joined / cut: 64 queries at 0 11 / - / 15, 300 at 300 22 / 17 / 24,
-    // 600 at 1 200 42 / 36 / 40, 1500 at 0 61 / - / 51, 100 at 2 000 48 / - / 29, 2 000 in documents of 333 (e4m3)
-    // 57 / - / 65, in one document 82 / - / 72; decode, 64 x 1 000, 32 heads over 1: 23 (one chain idle) / 20 / 34.
+    // full, which is where the rule goes wrong.  Measured, capped, 32 heads over 8, us dealt / joined / cut: 64 queries at 0
+    // 10 / 10 / 14, 300 at 300 20 / 16 / 24, 600 at 1 200 42 / 35 / 40, 1500 at 0 61 / 66 / 53, 100 at 2 000 48 / 37 / 27,
+    // 2 000 in documents of 333 (e4m3, bias) 59 / 74 / 72, in one document 165 / 189 / 143 (dealt); decode, 32 heads over 1,
+    // joined / cut: 64 x 1 000 20 / 31, 8 x 32 768 376 / 45, 64 of 117 .. 30 000 344 / 62, 1 x 32 768 beside 79 x 500
+    // 372 / 35 (joined).
     int64_t longest = (visit + kMtBlocks - 1) / kMtBlocks, average = longest;
     if (mp0.doc_start) longest = average = longest / 4 + 1;
     else if (!decode && visit == p.max_blocks) average = std::max<int64_t>(1, longest - p.n_pos / 2 / kMtKeys);   // causal

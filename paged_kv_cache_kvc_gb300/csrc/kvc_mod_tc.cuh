@@ -79,8 +79,9 @@ struct ModTcParams {
 };
 
 // How the weights are taken.  Plain: neither cap nor bias.  Capped: capped scores without a bias.  Brief: the same with
-// one code for all tiles, half as much to fetch when a call starts and a tenth slower per tile; us brief / not, 32 heads
-// over 8: 64 queries at 0 10.4 / 11.6 (from a cold cache 21 / 23), 1500 at 0 54 / 51, 2048 over 18 432 619 / 573.
+// one code for all tiles, half as much to fetch when a call starts and up to 5 % slower per tile; us brief / not, 32 heads
+// over 8: 64 queries at 0 10.1 / 10.3, 256 at 0 10.5 / 11.9, 5 over 20 005 33.4 / 34.6, 1500 at 0 53.8 / 53.1, 2048 over
+// 18 432 613 / 583.
 enum TcMode { kMtGeneral, kMtPlain, kMtCapped, kMtCappedBrief };
 
 template <int D, int KIND>
@@ -93,9 +94,9 @@ struct ModTcCfg {
     static constexpr int KBAND = kMtKeys * 128;        // one band of 64 key or value rows
     static constexpr int STAGE = BANDS * KBAND;
     // A row's reference moves when a score passes it by more (log2 units).  f16 weights stay under 2^16; bf16's and
-    // the sums have fp32's range.  (8 instead, with scores of deviation 4.6: one of a tile's 128 rows moves in every
-    // fifth tile and holds it up: 2048 positions over 18 432, int4 capped 1 022 us against 813, bf16 with a bias 709
-    // against 578.)
+    // the sums have fp32's range.  (8 instead, 2048 positions over 18 432, scores of deviation 2: with a bias of slope
+    // 2^-8 bf16 617 us against 533, e4m3 713 against 657; capped int4 794 against 787.  Where the bias itself climbs past
+    // the slack every few tiles, slopes 2^(-8 i / H), 687 against 681 and 782 against 781.)
     static constexpr float SLACK = QUANT ? 15.f : 40.f;
     static constexpr int R = QUANT ? 3 : 4;            // ring depths (with QUANT: codes, keys and values alike)
     static constexpr int BLOCK = QUANT ? DecodeCfg<D, KIND>::STAGE : 0;   // a block's codes, keys then values
@@ -1092,8 +1093,8 @@ __global__ void __launch_bounds__(ModTcCfg<D, KIND>::THREADS, 1) mod_tc_kernel(c
                     const float mul = mp.capped ? 1.f : p.scale_log2;   // into log2 units
                     if (mp.alibi && one_run && from >= t0 + kMtKeys - 1) {
                         // keys before the row's position: the bias is slope (t - p), a line.  Eight chains of pairs, four
-                        // additions each; with every key's distance on its own 2048 over 18 432 took 577 us against 543 (e4m3
-                        // 775 against 696).
+                        // additions each; with every key's distance on its own 2048 over 18 432, slopes 2^(-8 i / H), took
+                        // 708 us against 681 (e4m3 826 against 781).
                         f32x2 line[8];
                         const float at = slope * static_cast<float>(t0 - pos);
 #pragma unroll

@@ -186,9 +186,9 @@ __device__ __forceinline__ void build_factors(const RopeParams &p, RopeBatch<D, 
 // token's heads, U rows at a time with the next ones' loads in flight.  A ninth warp finds the next batch's
 // sequences, positions and blocks (a chain of four dependent loads) and its factors meanwhile.
 // Bound by HBM and by issue slots alike: 16 384 tokens of 32 + 2 x 8 heads of 128, normalised, bf16 (403 MB) take
-// 72 us, 5.6 TB/s, 82 % of the copy rate; e4m3 pools 93 us (the exact divisions by the scales).  A CTA per four
-// tokens without the ninth warp took 97 us (each CTA began with the chain of loads), the same with one row in
-// flight 111 us; per-row address arithmetic and one loop over all kinds of head 95 us.
+// 74 us, 5.4 TB/s, 80 % of the copy rate; e4m3 pools 95 us and int4 98 (the exact divisions by the scales).  A CTA
+// per four tokens without the ninth warp took 97 us (each CTA began with the chain of loads), the same with one row
+// in flight 111 us; per-row address arithmetic and one loop over all kinds of head 95 us.
 template <int D, int GPT, int U>
 __global__ void __launch_bounds__(kRopeCta, 3) rope_kernel(const RopeParams p)
 {
