@@ -15,7 +15,7 @@ namespace kvc {
 
 constexpr int kMtUnits = 2048;                     // most units (per head) of one launch
 constexpr int kMtStart = 8;                        // a unit's start and end, in tiles: 9 us at 1.1 us a tile (4 instead: within
-                                                   // 2 % either way for chunks of 5 to 2 048 queries)
+                                                   // 3 % either way for chunks of 5 to 2 048 queries)
 
 // Units (per head) of one launch: at most kMtUnits, and so few that a head's places stay inside 32 bits however long its
 // units are (2 048 units of 16 million positions would pass them).

@@ -78,9 +78,16 @@ class Batch:
         return out, lse
 
     def check(self, out, lse, m):
-        """Every row within the bounds of mod_reference.attend (the same terms, on the device)."""
+        """Every row within the bounds of mod_reference.attend (the same terms, on the device), and two more.
+
+        bf16 pools, capped scores: in tiles that a row does not read whole its outputs are divided by the sum of the
+        rounded weights.  With weights w (1 + e), |e| <= h, and p = w / sum w, the mixture is sum p (1 + e) v over
+        1 + E, E = sum p e: off by sum p (e - E) v to first order in h, and |e - E| <= 2 h.
+        e4m3 and int4 pools: a weight under 2^-14 of the largest is a subnormal f16, off by half of its step, 2^-25 of
+        the largest; the largest is at most sum w = L of those scaled to 1, so the mixture is off by 2^-25 sum |v| / L
+        more, which shows where the values of the heavy keys are zero."""
         assert self.kvc.kvc_pool_sync_status(self.pool) == self.kvc.KVC_OK
-        w_half = WEIGHTS["bf16" if self.dtype == "bf16" else "f16"]
+        w_half = WEIGHTS["bf16"] * (2 if m.softcap else 1) if self.dtype == "bf16" else WEIGHTS["f16"]
         g = self.H_Q // self.H_KV
         slope = torch.zeros(self.H_Q, device="cuda", dtype=torch.float64)
         if m.alibi is not None:
@@ -122,7 +129,10 @@ class Batch:
             ds = ds + 4 * 2.0 ** -23 * (x.abs().amax(-1) + away.max() * slope.abs())
             terms = min(int(t.numel()), 4096)
             rel = (2 * torch.expm1(ds) + w_half + (16 + terms) * 2.0 ** -23)[:, None]
-            to = HALF["bf16"] * (ro.abs() + rel * mix) + rel * mix + 2.0 ** -130
+            off = rel * mix
+            if self.dtype != "bf16":
+                off = off + 2.0 ** -25 * V.abs().sum(1).repeat_interleave(g, 0) / L
+            to = HALF["bf16"] * (ro.abs() + off) + off + 2.0 ** -130
             tl = torch.expm1(ds) + (16 + terms) * 2.0 ** -23 + 4 * 2.0 ** -24 * rl.abs()
             if not (bool(((o - ro).abs() <= to).all()) and bool(((l - rl).abs() <= tl).all())):
                 bad.append(b)
