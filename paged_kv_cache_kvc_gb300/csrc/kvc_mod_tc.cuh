@@ -29,8 +29,9 @@
 // unit's start and end cost about eight tiles (its queries staged, the first scores, its outputs written:
 // 9 us against 1.1 us a tile), so the line gives every unit kMtStart tiles more than it has.  A
 // unit cut by CTA borders leaves fp32 partials for mod_tc_merge_kernel, which adds them in CTA order; a
-// CTA leaves pieces of two units at most (kvc_mod_line.cuh).  (Merged by the unit's last CTA instead, 600 queries of 1800 positions took
-// 43 us, 20 pieces of a 5-query chunk 9 us of its 36: one SM's loads against all SMs'.)
+// CTA leaves pieces of two units at most (kvc_mod_line.cuh).  (Merged by the unit's last CTA instead, 600
+// queries of 1800 positions took 43 us, 20 pieces of a 5-query chunk 9 us of its 36: one SM's loads against
+// all SMs'.)
 //
 // Short units (little more than the start and the merge they would cost) are dealt whole instead, one
 // after the other, and nothing is merged.
