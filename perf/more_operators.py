@@ -379,7 +379,8 @@ def _inputs(c, seed):
             x = _normal(g, b - a, H_KV, 2, D) * 17.0
             x[:, :, 0] += 57.0
             x[:, :, 1] -= 57.0
-            codes[a:b] = x.round_().clamp_(-127, 127).to(torch.int8)
+            x = x.round_().clamp_(-127, 127).sort(2, descending=True).values
+            codes[a:b] = x.to(torch.int8)
         s["codes"] = codes
         s["exps"] = torch.exp2(torch.randint(-6, -3, (N, H_KV), generator=g, device=DEV).float())
         return s
@@ -543,7 +544,7 @@ def _values(c, s, x, kind):
 def _power(x):
     """The smallest e with x <= 127 * 2^e, kept in [-100, 100]."""
     m, e = torch.frexp(x)
-    return (e - 7 + (m * 128 > 127).int()).clamp(-100, 100)
+    return torch.where(x == 0, -100, (e - 7 + (m * 128 > 127).int()).clamp(-100, 100))
 
 
 def _plain_bounds(s):
@@ -778,7 +779,7 @@ def _exact_select(c, s):
                 whole = torch.round(q / 2.0 ** e)
                 score = torch.full((nb,), -math.inf, device=DEV, dtype=torch.float64)
                 for x in whole:
-                    score = torch.maximum(score, torch.maximum(rec[:, h, 0] * x, rec[:, h, 1] * x).sum(-1))
+                    score = torch.maximum(score, torch.maximum(rec[:, h, 0] * x, rec[:, h, 1] * x).sum(-1))   # hi >= lo
                 score = (score * unit[:, h]).cpu().numpy()
                 last = (rows[b][0] - n + i - at) // bs
                 forced = [j for j in range(last + 1) if j < c["sink"] or j > last - c["recent"]]
