@@ -116,7 +116,7 @@ typedef struct {
  * kvc_mixed_step, kvc_decode_attn_noalloc) needs block_size 16; a pool of
  * another block size serves kvc_append, kvc_write_tokens and kvc_copy_blocks
  * (e.g. the 4-position blocks of Table 21.1) and its attention calls return
- * KVC_ERR_UNSUPPORTED.  Errors: KVC_ERR_ARG, KVC_ERR_OOM, KVC_ERR_CUDA; *out is
+ * KVC_ERR_UNSUPPORTED (kvc_sparse_attn serves multiples of 16).  Errors: KVC_ERR_ARG, KVC_ERR_OOM, KVC_ERR_CUDA; *out is
  * NULL on error. */
 KVC_API kvc_status kvc_pool_create(int64_t num_blocks, int32_t block_size, int32_t num_layers,
                            int32_t num_kv_heads, int32_t head_dim, kvc_dtype dtype, kvc_pool **out);
@@ -448,6 +448,156 @@ KVC_API kvc_status kvc_prefill_attn_mod(kvc_pool *pool, int32_t layer, const voi
                                         int32_t num_q_heads, const int32_t *block_table_row, int32_t max_blocks,
                                         int32_t q_start, const kvc_score_mod *mod, void *out, float *lse, float scale,
                                         void *workspace, uint64_t workspace_bytes, kvc_stream_t stream);
+
+/* ------------------------------------------------------------------ planned steps */
+
+/* Block tables and slot maps built on the GPU from the lengths that sequences
+ * have and shall have, so that a serving step needs no host allocation and can
+ * be captured whole: the device's counterpart of kvc_alloc_reserve,
+ * kvc_alloc_release and kvc_alloc_block_tables for blocks that one sequence
+ * maps alone (no reference counts; the caller keeps shared prefixes out of
+ * what a step releases).
+ *
+ * With have_b = ceil(seq_lens[b] / bs) and want_b = ceil(new_lens[b] / bs):
+ *   - A sequence that shrinks (finished: new_lens[b] = 0; drafts rejected)
+ *     returns its row's entries want_b .. have_b - 1 to the free list, which is
+ *     a stack: they are pushed in order of (b, entry).
+ *   - Then sequences grow in order of b, first come, first served: sequence b
+ *     is granted while the blocks and the rows (new tokens) that sequences
+ *     0 .. b ask for fit the free blocks and n_rows.  From the first one that does
+ *     not fit, no sequence of the call grows (not even inside its last block).  A
+ *     granted one pops its blocks off the stack into entries have_b .. want_b - 1.
+ *   - lens_out[b] is the length that b has now: new_lens[b], or seq_lens[b]
+ *     where growth was not granted (not an error: the caller sees it there).
+ *   - Row r of the step, cu_tokens[b] <= r < cu_tokens[b+1], is sequence b's
+ *     token at position seq_lens[b] + r - cu_tokens[b]: positions[r], its
+ *     sequence seq_ids[r] = b and its slot slots[r] = block * bs + position mod
+ *     bs.  Rows at or past cu_tokens[B] get -1 in all three.
+ * Entries of a row at or past its new length mean nothing and are not cleared.
+ *   block_tables: device int32 [B][max_blocks], changed in place
+ *   seq_lens, new_lens: device int32 [B];  lens_out: device int32 [B], may be
+ *       seq_lens or new_lens itself
+ *   free_list: device int32 [free_capacity]; entries 0 .. *free_count - 1 are
+ *       free; free_capacity >= num_blocks (else KVC_ERR_ARG)
+ *   free_count, count_out: device int32, the number of free blocks before and
+ *       after; may be the same
+ *   cu_tokens: device int32 [B+1];  slots, positions, seq_ids: device int32
+ *       [n_rows], any of positions and seq_ids may be NULL
+ * B is at most 32768 (else KVC_ERR_UNSUPPORTED).  A sequence whose lengths are
+ * negative or past its row keeps its length and gets no rows (KVC_ERR_RANGE via
+ * kvc_pool_sync_status); so are a count outside [0, free_capacity] (taken as
+ * the nearest bound) and more returned blocks than the list holds (dropped).
+ * A token whose table entry is outside the pool gets slot -1 and is recorded
+ * (KVC_ERR_BAD_BLOCK).  B = 0 fills the rows with -1.  The pool gives block
+ * size, block count, device and error word; its keys and values are not
+ * touched.  Errors (synchronous): KVC_ERR_ARG, KVC_ERR_UNSUPPORTED, KVC_ERR_CUDA. */
+KVC_API kvc_status kvc_plan_step(kvc_pool *pool, int32_t *block_tables, int32_t max_blocks, const int32_t *seq_lens,
+                                 const int32_t *new_lens, int32_t B, int32_t *free_list, int64_t free_capacity,
+                                 const int32_t *free_count, int32_t *lens_out, int32_t *count_out, int32_t *cu_tokens,
+                                 int32_t *slots, int32_t *positions, int32_t *seq_ids, int64_t n_rows,
+                                 kvc_stream_t stream);
+
+/* kvc_rope_write_tokens for rows whose place and position are given: row r is
+ * stored at slot slots[r] (block slots[r] / bs, place slots[r] mod bs) and
+ * rotated by positions with several axes, e.g. (time, height, width) of an
+ * image's or a video's tokens: frequency i turns by the angle
+ * positions[axis_of[i]][r] * inv_freq[i].
+ *   slots: device int32 [n_rows]; a row with slot -1 is padding: nothing is
+ *       stored and its q_out row is left as it is.  Two rows must not have the
+ *       same slot.  Any other slot outside the pool is not stored and recorded
+ *       (KVC_ERR_BAD_BLOCK); its q_out row is still written.
+ *   positions: device int32, num_axes rows of n_rows elements, axis_stride
+ *       elements apart; any value (angles to about 1e-6 radians while the
+ *       magnitude is below 2^24)
+ *   axis_of: device uint8 [rotary_dim / 2], or NULL: all axis 0.  A value that
+ *       is not below num_axes counts as axis 0 and is recorded (KVC_ERR_RANGE).
+ *   num_axes: 1 .. 8 (else KVC_ERR_ARG)
+ * Other arguments, storage and errors as kvc_rope_write_tokens. */
+KVC_API kvc_status kvc_rope_write_slots(kvc_pool *pool, int32_t layer, const int32_t *slots, const int32_t *positions,
+                                        int64_t axis_stride, int32_t num_axes, const uint8_t *axis_of, int64_t n_rows,
+                                        const void *q, int64_t q_stride, int32_t num_q_heads, const void *k,
+                                        int64_t k_stride, const void *v, int64_t v_stride, const kvc_rope *rope,
+                                        void *q_out, kvc_stream_t stream);
+
+/* ------------------------------------------------------------------ sparse attention */
+
+/* Attention that reads, for each query, only the blocks that can matter.  Every
+ * block keeps 8-bit bounds of its keys, a query's score against them bounds its
+ * products with the block's keys from above, and the query attends to the blocks
+ * of the largest bounds.
+ *
+ * Bounds of a block and KV head whose keys k_t (the values that the stored
+ * elements stand for: code * scale in fp32) fill places t = 0 .. n-1:
+ *   hi_i = max_t k_ti,  lo_i = min_t k_ti  (a NaN counts as +inf in hi, -inf in lo)
+ *   e    = the smallest integer in [-100, 100] with |hi_i|, |lo_i| <= 127 * 2^e (100 if none)
+ *   codes: int8 ceil(hi_i / 2^e) and floor(lo_i / 2^e), clamped to [-127, 127]; the unit 2^e as fp32
+ * A bounds buffer holds, layer after layer (kvc_bounds_bytes / num_layers bytes
+ * each), int8 [num_blocks][H_KV][2][d_h] (hi, lo) and then fp32
+ * [num_blocks][H_KV] units.  The caller allocates it (256-byte aligned, on the
+ * pool's device) and keeps it beside the pool. */
+KVC_API kvc_status kvc_bounds_bytes(const kvc_pool *pool, uint64_t *bytes);
+
+/* Recompute the bounds of every block that the given rows were written to, from
+ * the pool (after the write, on the same stream): places 0 .. slot mod bs of the
+ * last row in each block.
+ *   slots: device int32 [n_rows], the write's slot map: the rows of one block
+ *       adjacent and in ascending order, as kvc_plan_step gives them; -1 rows
+ *       are skipped, another slot outside the pool is recorded
+ *       (KVC_ERR_BAD_BLOCK)
+ * Pools of any block size.  Errors (synchronous): KVC_ERR_ARG (also a buffer
+ * smaller than kvc_bounds_bytes), KVC_ERR_CUDA. */
+KVC_API kvc_status kvc_update_bounds(kvc_pool *pool, int32_t layer, const int32_t *slots, int64_t n_rows, void *bounds,
+                                     uint64_t bounds_bytes, kvc_stream_t stream);
+
+/* For each query row r of sequence s = seq_ids[r] at position p = positions[r],
+ * and each KV head h, the list of blocks to read among the sequence's blocks
+ * 0 .. m = p / bs:
+ *   Q_g  = the g-th query head of h's group, rounded to integers: rint(q / 2^f),
+ *          f = the smallest integer in [-100, 100] with |q| <= 127 * 2^f over the
+ *          whole group (rounding half to even, clamped to [-127, 127]; NaN counts as 0)
+ *   score_j = 2^e_j * max_g sum_i Q_gi * (hi_ji where Q_gi > 0, else lo_ji)
+ * All of it is exact in fp32.  Listed are the first `sink` blocks, the last
+ * `recent` ones (m among them), and of the others those of the largest scores,
+ * the lower block first among equals, until top_k are listed or none is left.
+ *   selected: device int32 [n_rows][H_KV][top_k]: block indices (into the
+ *       table row) in ascending order, then -1
+ *   q: device bf16 [n_rows][H_Q][d_h], 16-byte aligned
+ *   seq_ids: device int32 [n_rows], or NULL: row r is sequence r (n_rows <= B)
+ *   positions: device int32 [n_rows].  A row whose position or sequence is -1
+ *       is padding: its list is left as it is.
+ *   top_k: at least sink + recent and at most 65536; recent at least 1
+ * A block whose table entry is outside the pool is not listed (recorded as
+ * KVC_ERR_BAD_BLOCK); a row whose sequence is not below B, whose position is past the table, or
+ * where either is below -1, lists nothing (KVC_ERR_RANGE).  H_Q / H_KV as
+ * kvc_decode_attn; pools of any block size; max_blocks up to 262144 (else
+ * KVC_ERR_UNSUPPORTED).  Nothing is allocated.  Errors (synchronous):
+ * KVC_ERR_ARG, KVC_ERR_UNSUPPORTED, KVC_ERR_CUDA. */
+KVC_API kvc_status kvc_select_blocks(kvc_pool *pool, int32_t layer, const void *bounds, uint64_t bounds_bytes,
+                                     const void *q, int32_t num_q_heads, const int32_t *block_tables,
+                                     int32_t max_blocks, int32_t B, const int32_t *seq_ids, const int32_t *positions,
+                                     int64_t n_rows, int32_t top_k, int32_t sink, int32_t recent, int32_t *selected,
+                                     kvc_stream_t stream);
+
+/* Attention of each query row over its listed blocks: kvc_decode_attn with the
+ * positions t <= positions[r] of the blocks selected[r][h][0 .. top_k) in place of all.  Entries
+ * of -1 are skipped wherever they stand; the order does not matter; a block listed
+ * twice counts twice.  An entry past the query's own block or below -1 is skipped and
+ * recorded (KVC_ERR_RANGE), a block whose table entry is outside the pool too
+ * (KVC_ERR_BAD_BLOCK).  A row that reads nothing gives out = 0 and lse = -inf.
+ *   out: device bf16 [n_rows][H_Q][d_h], 16-byte aligned, may be q itself and
+ *       must not overlap it otherwise (KVC_ERR_ARG);  lse: device fp32
+ *       [n_rows][H_Q] or NULL
+ *   Rows, sequences and positions as kvc_select_blocks: rows of padding leave
+ *   out and lse as they are, rows in error read nothing.
+ *   scale: finite and > 0
+ * block_size 16, 32, 48 .. 128 (a multiple of 16, else KVC_ERR_UNSUPPORTED);
+ * weights and precision as kvc_decode_attn_mod.  Nothing is allocated and no
+ * workspace is needed: the CTAs of a row merge in shared memory.  Other
+ * requirements and errors as kvc_decode_attn. */
+KVC_API kvc_status kvc_sparse_attn(kvc_pool *pool, int32_t layer, const void *q, int32_t num_q_heads,
+                                   const int32_t *block_tables, int32_t max_blocks, int32_t B, const int32_t *seq_ids,
+                                   const int32_t *positions, int64_t n_rows, const int32_t *selected, int32_t top_k,
+                                   void *out, float *lse, float scale, kvc_stream_t stream);
 
 /* ------------------------------------------------------------------ block allocator (host) */
 

@@ -2,8 +2,9 @@
 
 Argument marshalling only: every step runs in the CUDA library's kernels
 (``csrc/``), reached through its C ABI (``include/kvc.h``) with ctypes; the
-rotary write and attention with modified scores go through a small native
-module instead (``csrc/kvc_call.cpp``), whose checks cost a microsecond.
+rotary writes, attention with modified scores, planned steps and sparse
+attention go through a small native module instead (``csrc/kvc_call.cpp``),
+whose checks cost a microsecond.
 PyTorch supplies device memory and streams.  The names match the C entry
 points; tensors are passed where the C call takes device pointers, and the
 stream defaults to torch's current stream.
@@ -64,7 +65,8 @@ EXPORTS = ["kvc_pool_create", "kvc_pool_destroy", "kvc_pool_info", "kvc_pool_set
            "kvc_append", "kvc_write_tokens", "kvc_decode_attn", "kvc_prefill_attn", "kvc_pool_reserve",
            "kvc_bytes", "kvc_pool_sync_status", "kvc_status_str", "kvc_launch_count", "kvc_decode_attn_noalloc", "kvc_decode_step",
            "kvc_mixed_step", "kvc_rope_append", "kvc_rope_write_tokens", "kvc_mod_workspace_bytes",
-           "kvc_decode_attn_mod", "kvc_prefill_attn_mod",
+           "kvc_decode_attn_mod", "kvc_prefill_attn_mod", "kvc_plan_step", "kvc_rope_write_slots", "kvc_bounds_bytes",
+           "kvc_update_bounds", "kvc_select_blocks", "kvc_sparse_attn",
            "kvc_alloc_create", "kvc_alloc_destroy", "kvc_alloc_new_seq", "kvc_alloc_fork", "kvc_alloc_reserve",
            "kvc_alloc_commit", "kvc_alloc_release", "kvc_alloc_publish", "kvc_alloc_match", "kvc_alloc_seq_info",
            "kvc_alloc_block_tables", "kvc_alloc_counts", "kvc_alloc_refcount", "kvc_alloc_lease", "kvc_alloc_check",
@@ -110,6 +112,16 @@ def load(path: str = LIB_PATH):
     L.kvc_decode_attn_mod.argtypes = [vp, i32, vp, i32, vp, i32, vp, i32, mp, vp, vp, ctypes.c_float, vp, u64, vp]
     L.kvc_prefill_attn_mod.restype = st
     L.kvc_prefill_attn_mod.argtypes = [vp, i32, vp, i32, i32, vp, i32, i32, mp, vp, vp, ctypes.c_float, vp, u64, vp]
+    L.kvc_plan_step.restype = st
+    L.kvc_plan_step.argtypes = [vp, vp, i32, vp, vp, i32, vp, i64, vp, vp, vp, vp, vp, vp, vp, i64, vp]
+    L.kvc_rope_write_slots.restype = st
+    L.kvc_rope_write_slots.argtypes = [vp, i32, vp, vp, i64, i32, vp, i64, vp, i64, i32, vp, i64, vp, i64, rp, vp, vp]
+    L.kvc_bounds_bytes.restype, L.kvc_bounds_bytes.argtypes = st, [vp, ctypes.POINTER(u64)]
+    L.kvc_update_bounds.restype, L.kvc_update_bounds.argtypes = st, [vp, i32, vp, i64, vp, u64, vp]
+    L.kvc_select_blocks.restype = st
+    L.kvc_select_blocks.argtypes = [vp, i32, vp, u64, vp, i32, vp, i32, i32, vp, vp, i64, i32, i32, i32, vp, vp]
+    L.kvc_sparse_attn.restype = st
+    L.kvc_sparse_attn.argtypes = [vp, i32, vp, i32, vp, i32, i32, vp, vp, i64, vp, i32, vp, vp, ctypes.c_float, vp]
     L.kvc_pool_reserve.restype, L.kvc_pool_reserve.argtypes = st, [vp, i32, i32, i32]
     L.kvc_bytes.restype, L.kvc_bytes.argtypes = u64, [i64] * 6
     L.kvc_pool_sync_status.restype, L.kvc_pool_sync_status.argtypes = st, [vp, vp]
@@ -366,18 +378,22 @@ def _native():
 
 
 class Rope:
-    """Position rotation (and optional per-head RMS norm) for kvc_rope_append / kvc_rope_write_tokens.
+    """Position rotation (and optional per-head RMS norm) for kvc_rope_append / kvc_rope_write_tokens /
+    kvc_rope_write_slots.
 
     inv_freq: CUDA fp32 [rotary_dim / 2], radians per position (None: no rotation); q_norm, k_norm: CUDA
-    bf16 [d_h] norm weights or None.  Holds the tensors; one object serves any number of calls.  What it holds is
-    fixed (a tensor's values may change); another weight is another Rope."""
+    bf16 [d_h] norm weights or None; axis_of: CUDA uint8 [rotary_dim / 2], the axis of each frequency (None: axis 0;
+    kvc_rope_write_slots alone reads it, the other calls refuse it).  Holds the tensors; one object serves any number
+    of calls.  What it holds is fixed (a tensor's values may change); another weight is another Rope."""
 
-    __slots__ = ("args", "__weakref__")
+    __slots__ = ("args", "axes", "__weakref__")
 
-    def __init__(self, inv_freq=None, interleaved=False, q_norm=None, k_norm=None, eps=1e-6):
+    def __init__(self, inv_freq=None, interleaved=False, q_norm=None, k_norm=None, eps=1e-6, axis_of=None):
         dim = 0 if inv_freq is None else 2 * inv_freq.numel()
         self.args = (dim, int(bool(interleaved)), inv_freq, q_norm, k_norm, float(eps))
+        self.axes = (axis_of,)
 
+    axis_of = property(lambda self: self.axes[0])
     inv_freq = property(lambda self: self.args[2])
     q_norm = property(lambda self: self.args[3])
     k_norm = property(lambda self: self.args[4])
@@ -388,6 +404,8 @@ def kvc_rope_append(pool, layer, block_tables, seq_lens, q, k_new, v_new, q_out,
 
     q, k_new, v_new: bf16 [B][heads][head_dim], rows may be strided (views of a fused projection's output); q and
     q_out may both be None; q_out may be q.  The stream defaults to torch's current stream of the pool's device."""
+    if rope.axes[0] is not None:
+        raise ValueError("a Rope with axes needs positions with axes: kvc_rope_write_slots")
     s = (_call or _native()).rope_write(pool.args, layer, block_tables, seq_lens, None, q, k_new, v_new, q_out, rope.args,
                                         None if stream is None else _stream(stream))
     if s:
@@ -400,6 +418,8 @@ def kvc_rope_write_tokens(pool, layer, block_tables, start_pos, cu_tokens, q, k,
     Rows at or past cu_tokens[-1] are left as they are.  Nothing is copied to the host."""
     if cu_tokens is None:
         raise ValueError("cu_tokens is required")
+    if rope.axes[0] is not None:
+        raise ValueError("a Rope with axes needs positions with axes: kvc_rope_write_slots")
     s = (_call or _native()).rope_write(pool.args, layer, block_tables, start_pos, cu_tokens, q, k, v, q_out, rope.args,
                                         None if stream is None else _stream(stream))
     if s:
@@ -451,6 +471,82 @@ def kvc_prefill_attn_mod(pool, layer, q, block_table_row, q_start, out, lse=None
                                               None if stream is None else _stream(stream))
     if s:
         raise KvcError(s, "kvc_prefill_attn_mod")
+
+
+# ---------------------------------------------------------------------- planned steps
+def kvc_plan_step(pool, block_tables, seq_lens, new_lens, free_list, free_count, lens_out, count_out, cu_tokens, slots,
+                  positions=None, seq_ids=None, stream=None):
+    """Block tables and slot maps of a step, built on the GPU: sequence b goes from seq_lens[b] to new_lens[b] tokens.
+
+    All CUDA int32.  block_tables [B][max_blocks] is changed in place; free_list is a stack of at least num_blocks
+    entries whose first free_count[0] are free; lens_out may be seq_lens or new_lens, count_out may be free_count.
+    slots, positions, seq_ids [n_rows]: a row for every new token, then -1.  A sequence whose blocks or rows are no
+    longer there keeps its length (see lens_out), and so does every later one that would grow."""
+    s = (_call or _native()).plan_step(pool.args, block_tables, seq_lens, new_lens, free_list, free_count, lens_out,
+                                       count_out, cu_tokens, slots, positions, seq_ids,
+                                       None if stream is None else _stream(stream))
+    if s:
+        raise KvcError(s, "kvc_plan_step")
+
+
+def kvc_rope_write_slots(pool, layer, slots, positions, q, k, v, q_out, rope, stream=None):
+    """kvc_rope_write_tokens for rows whose places are given: row r into slot slots[r] (-1: padding, left as it is).
+
+    positions: CUDA int32 [n_rows], or [axes][n_rows] with rope.axis_of naming each frequency's axis."""
+    s = (_call or _native()).rope_write_slots(pool.args, layer, slots, positions, q, k, v, q_out, rope.args,
+                                              rope.axes[0], None if stream is None else _stream(stream))
+    if s:
+        raise KvcError(s, "kvc_rope_write_slots")
+
+
+# ---------------------------------------------------------------------- sparse attention
+def kvc_block_bounds(pool) -> torch.Tensor:
+    """A zeroed buffer for the bounds of every block's keys, all layers (see kvc_bounds_bytes in kvc.h)."""
+    n = ctypes.c_uint64()
+    _check(load().kvc_bounds_bytes(_h(pool), ctypes.byref(n)), "kvc_bounds_bytes")
+    return torch.zeros(n.value, dtype=torch.uint8, device=f"cuda:{pool.device}")
+
+
+def kvc_block_bounds_views(pool, layer, bounds):
+    """A layer's bounds as tensors: codes int8 [num_blocks][H_KV][2][head_dim] (upper, lower) and the units they
+    count in, fp32 [num_blocks][H_KV].  Views of the buffer, no copy."""
+    if not 0 <= layer < pool.num_layers:
+        raise ValueError("layer is out of range")
+    n = bounds.numel() // pool.num_layers
+    heads = pool.num_blocks * pool.num_kv_heads
+    part, at = bounds[layer * n:(layer + 1) * n], heads * 2 * pool.head_dim
+    codes = part[:at].view(torch.int8).view(pool.num_blocks, pool.num_kv_heads, 2, pool.head_dim)
+    return codes, part[at:at + 4 * heads].view(torch.float32).view(pool.num_blocks, pool.num_kv_heads)
+
+
+def kvc_update_bounds(pool, layer, bounds, slots, stream=None):
+    """Recompute the bounds of every block that the rows of a slot map were written to (after the write)."""
+    s = (_call or _native()).update_bounds(pool.args, layer, bounds, slots, None if stream is None else _stream(stream))
+    if s:
+        raise KvcError(s, "kvc_update_bounds")
+
+
+def kvc_select_blocks(pool, layer, bounds, q, block_tables, positions, selected, seq_ids=None, sink=1, recent=1,
+                      stream=None):
+    """For each query row and KV head the blocks to read: the first `sink`, the last `recent`, and those whose bounds
+    allow the largest scores, selected.shape[2] in all.
+
+    q: bf16 [n_rows][H_Q][head_dim]; positions: int32 [n_rows]; seq_ids: int32 [n_rows] (None: row r is sequence r);
+    selected: int32 [n_rows][H_KV][top_k], ascending block indices, then -1.  Padding rows (-1) are left as they are."""
+    s = (_call or _native()).select_blocks(pool.args, layer, bounds, q, block_tables, positions, selected, seq_ids, sink,
+                                           recent, None if stream is None else _stream(stream))
+    if s:
+        raise KvcError(s, "kvc_select_blocks")
+
+
+def kvc_sparse_attn(pool, layer, q, block_tables, positions, selected, out, lse=None, seq_ids=None, scale=None,
+                    stream=None):
+    """Attention of each query row over the positions up to its own in its listed blocks; out is bf16 and may be q.
+    Needs no workspace.  Rows, sequences and positions as for kvc_select_blocks."""
+    s = (_call or _native()).sparse_attn(pool.args, layer, q, block_tables, positions, selected, out, lse, seq_ids, scale,
+                                         None if stream is None else _stream(stream))
+    if s:
+        raise KvcError(s, "kvc_sparse_attn")
 
 
 def kvc_pool_reserve(pool, max_batch, num_q_heads, max_blocks):

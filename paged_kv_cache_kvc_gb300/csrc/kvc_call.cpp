@@ -1,7 +1,7 @@
-// CPython module `_kvc_call`: argument checks and marshalling of the rotary write and of attention with
-// modified scores, for the Python binding.  A decode step's smallest calls take a few microseconds on the
-// GPU; checking nine tensors and filling a C call through ctypes took 16 on the host.  Here a call reads the
-// tensors' headers directly and takes about 5, most of it the launch.
+// CPython module `_kvc_call`: argument checks and marshalling of the rotary writes, of attention with modified
+// scores, of planned steps and of sparse attention, for the Python binding.  A decode step's smallest calls take a
+// few microseconds on the GPU; checking nine tensors and filling a C call through ctypes took 16 on the host.  Here a
+// call reads the tensors' headers directly and takes about 5, most of it the launch.
 //
 // Every function takes its arguments by position, raises ValueError for a tensor that is not what the call
 // takes, and returns the library's status.
@@ -261,6 +261,145 @@ long prefill_attn_mod(PyObject *const *a, Py_ssize_t n)
                                 ptr(m.ws), m.ws ? m.ws->numel() : 0, s);
 }
 
+const int32_t *i32(const at::Tensor *t) { return static_cast<const int32_t *>(ptr(t)); }
+int32_t *i32_out(const at::Tensor *t) { return static_cast<int32_t *>(ptr(t)); }
+
+// A size that the C call takes as int32.
+int32_t narrow(int64_t v, const char *name)
+{
+    if (v != static_cast<int32_t>(v)) fail(name, "is too large");
+    return static_cast<int32_t>(v);
+}
+
+// (pool, block_tables, seq_lens, new_lens, free_list, free_count, lens_out, count_out, cu_tokens, slots,
+//  positions or None, seq_ids or None, stream)
+long plan_step(PyObject *const *a, Py_ssize_t n)
+{
+    count(n, 13);
+    const PoolArgs p = pool_args(a[0]);
+    const at::Tensor *bt = shaped(a[1], at::kInt, p.device, {-1, -1}, "block_tables");
+    const int64_t B = bt->size(0);
+    const at::Tensor *lens = shaped(a[2], at::kInt, p.device, {B}, "seq_lens");
+    const at::Tensor *want = shaped(a[3], at::kInt, p.device, {B}, "new_lens");
+    const at::Tensor *stack = shaped(a[4], at::kInt, p.device, {-1}, "free_list");
+    const at::Tensor *have = shaped(a[5], at::kInt, p.device, {1}, "free_count");
+    const at::Tensor *lens_out = shaped(a[6], at::kInt, p.device, {B}, "lens_out");
+    const at::Tensor *left = shaped(a[7], at::kInt, p.device, {1}, "count_out");
+    const at::Tensor *cu = shaped(a[8], at::kInt, p.device, {B + 1}, "cu_tokens");
+    const at::Tensor *slots = shaped(a[9], at::kInt, p.device, {-1}, "slots");
+    const int64_t rows = slots->size(0);
+    const at::Tensor *pos = shaped(a[10], at::kInt, p.device, {rows}, "positions", true);
+    const at::Tensor *seq = shaped(a[11], at::kInt, p.device, {rows}, "seq_ids", true);
+    const int32_t b32 = narrow(B, "block_tables"), mb = narrow(bt->size(1), "block_tables");
+    void *s = stream_of(a[12], p);
+    const Unlocked unlocked;
+    return kvc_plan_step(p.pool, i32_out(bt), mb, i32(lens), i32(want), b32, i32_out(stack), stack->size(0), i32(have),
+                         i32_out(lens_out), i32_out(left), i32_out(cu), i32_out(slots), i32_out(pos), i32_out(seq), rows, s);
+}
+
+// (pool, layer, slots, positions, q or None, k, v, q_out or None, rope, axis_of or None, stream)
+long rope_write_slots(PyObject *const *a, Py_ssize_t n)
+{
+    count(n, 11);
+    const PoolArgs p = pool_args(a[0]);
+    const int32_t layer = int32(a[1], "layer");
+    const at::Tensor *slots = shaped(a[2], at::kInt, p.device, {-1}, "slots");
+    const int64_t rows = slots->size(0);
+    const at::Tensor *pos = tensor(a[3], at::kInt, p.device, "positions");   // [rows] or [axes][rows], rows contiguous
+    const bool one = pos->dim() == 1;
+    if ((!one && pos->dim() != 2) || pos->size(one ? 0 : 1) != rows) fail("positions", "has the wrong shape");
+    if (rows > 1 && pos->stride(one ? 0 : 1) != 1) fail("positions", "must have each axis contiguous");
+    const int64_t axes = one ? 1 : pos->size(0);
+    const int64_t axis_stride = one || axes < 2 ? rows : pos->stride(0);
+    const Rows k = head_rows(a[5], p.device, rows, p.heads, p.d, "k");
+    const Rows v = head_rows(a[6], p.device, rows, p.heads, p.d, "v");
+    if ((a[4] == Py_None) != (a[7] == Py_None)) fail("q and q_out", "go together");
+    Rows q;
+    void *q_out = nullptr;
+    if (a[4] != Py_None) {
+        q = head_rows(a[4], p.device, rows, -1, p.d, "q");
+        q_out = ptr(shaped(a[7], at::kBFloat16, p.device, {rows, q.heads, p.d}, "q_out"));
+    }
+    const kvc_rope rope = rope_of(a[8], p);
+    const at::Tensor *axis_of = shaped(a[9], at::kByte, p.device, {rope.rotary_dim / 2}, "axis_of", true);
+    const int32_t n_axes = narrow(axes, "positions"), hq = narrow(q.heads, "q");
+    void *s = stream_of(a[10], p);
+    const Unlocked unlocked;
+    return kvc_rope_write_slots(p.pool, layer, i32(slots), i32(pos), axis_stride, n_axes,
+                                static_cast<const uint8_t *>(ptr(axis_of)), rows, q.data, q.stride, hq, k.data, k.stride,
+                                v.data, v.stride, &rope, q_out, s);
+}
+
+// (pool, layer, bounds, slots, stream)
+long update_bounds(PyObject *const *a, Py_ssize_t n)
+{
+    count(n, 5);
+    const PoolArgs p = pool_args(a[0]);
+    const int32_t layer = int32(a[1], "layer");
+    const at::Tensor *bounds = shaped(a[2], at::kByte, p.device, {-1}, "bounds");
+    const at::Tensor *slots = shaped(a[3], at::kInt, p.device, {-1}, "slots");
+    void *s = stream_of(a[4], p);
+    const Unlocked unlocked;
+    return kvc_update_bounds(p.pool, layer, i32(slots), slots->size(0), ptr(bounds), bounds->numel(), s);
+}
+
+// The rows of a sparse call: queries, their sequences and positions.
+struct SparseArgs {
+    const at::Tensor *q, *bt, *pos, *seq, *lists;
+    int32_t heads, mb, B, top_k;
+    int64_t rows;
+};
+
+SparseArgs sparse_args(const PoolArgs &p, PyObject *q, PyObject *bt, PyObject *pos, PyObject *lists, PyObject *seq)
+{
+    SparseArgs r{};
+    r.q = shaped(q, at::kBFloat16, p.device, {-1, -1, p.d}, "q");
+    r.rows = r.q->size(0);
+    r.bt = shaped(bt, at::kInt, p.device, {-1, -1}, "block_tables");
+    r.pos = shaped(pos, at::kInt, p.device, {r.rows}, "positions");
+    r.seq = shaped(seq, at::kInt, p.device, {r.rows}, "seq_ids", true);
+    r.lists = shaped(lists, at::kInt, p.device, {r.rows, p.heads, -1}, "selected");
+    r.heads = narrow(r.q->size(1), "q");
+    r.B = narrow(r.bt->size(0), "block_tables");
+    r.mb = narrow(r.bt->size(1), "block_tables");
+    r.top_k = narrow(r.lists->size(2), "selected");
+    if (!r.seq && r.rows > r.B) fail("seq_ids", "is required: there are more rows than sequences");
+    return r;
+}
+
+// (pool, layer, bounds, q, block_tables, positions, selected, seq_ids or None, sink, recent, stream)
+long select_blocks(PyObject *const *a, Py_ssize_t n)
+{
+    count(n, 11);
+    const PoolArgs p = pool_args(a[0]);
+    const int32_t layer = int32(a[1], "layer");
+    const at::Tensor *bounds = shaped(a[2], at::kByte, p.device, {-1}, "bounds");
+    const SparseArgs r = sparse_args(p, a[3], a[4], a[5], a[6], a[7]);
+    const int32_t sink = int32(a[8], "sink"), recent = int32(a[9], "recent");
+    void *s = stream_of(a[10], p);
+    const Unlocked unlocked;
+    return kvc_select_blocks(p.pool, layer, ptr(bounds), bounds->numel(), ptr(r.q), r.heads, i32(r.bt), r.mb, r.B,
+                             i32(r.seq), i32(r.pos), r.rows, r.top_k, sink, recent, i32_out(r.lists), s);
+}
+
+// (pool, layer, q, block_tables, positions, selected, out, lse or None, seq_ids or None, scale or None, stream)
+long sparse_attn(PyObject *const *a, Py_ssize_t n)
+{
+    count(n, 11);
+    const PoolArgs p = pool_args(a[0]);
+    const int32_t layer = int32(a[1], "layer");
+    const SparseArgs r = sparse_args(p, a[2], a[3], a[4], a[5], a[8]);
+    const at::Tensor *out = shaped(a[6], at::kBFloat16, p.device, {r.rows, r.heads, p.d}, "out");
+    const at::Tensor *lse = shaped(a[7], at::kFloat, p.device, {r.rows, r.heads}, "lse", true);
+    const float scale = a[9] == Py_None ? static_cast<float>(1.0 / std::sqrt(static_cast<double>(p.d)))
+                                        : static_cast<float>(PyFloat_AsDouble(a[9]));
+    if (PyErr_Occurred()) throw Bad{};
+    void *s = stream_of(a[10], p);
+    const Unlocked unlocked;
+    return kvc_sparse_attn(p.pool, layer, ptr(r.q), r.heads, i32(r.bt), r.mb, r.B, i32(r.seq), i32(r.pos), r.rows,
+                           i32(r.lists), r.top_k, ptr(out), static_cast<float *>(ptr(lse)), scale, s);
+}
+
 template <long (*F)(PyObject *const *, Py_ssize_t)>
 PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n)
 {
@@ -281,7 +420,9 @@ PyMethodDef method(const char *name)
 }
 
 PyMethodDef methods[] = {method<rope_write>("rope_write"), method<decode_attn_mod>("decode_attn_mod"),
-                         method<prefill_attn_mod>("prefill_attn_mod"), {nullptr, nullptr, 0, nullptr}};
+                         method<prefill_attn_mod>("prefill_attn_mod"), method<plan_step>("plan_step"),
+                         method<rope_write_slots>("rope_write_slots"), method<update_bounds>("update_bounds"),
+                         method<select_blocks>("select_blocks"), method<sparse_attn>("sparse_attn"), {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kvc_call", "Argument marshalling of the kvc binding.", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

@@ -330,6 +330,15 @@ extern "C" kvc_status kvc_pool_create(int64_t num_blocks, int32_t block_size, in
                                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
             pool->tmap16_ok = (r16 == CUDA_SUCCESS);
         }
+        // the same for every element type (int4: 8 lines of two rows), for attention over lists of blocks
+        pool->tmap_sub_ok = false;
+        if (block_size % 16 == 0) {
+            cuuint32_t box_sub[2] = {box[0], lines ? 8u : 16u};
+            pool->tmap_sub_ok = enc(&pool->tmap_sub, bits == 16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8,
+                                    2, pool->base, gdim, gstride, box_sub, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+        }
     }
     noalloc_prepare(pool->device);   // the allocation-free decode's scratch: reserved now, not mid-step
     (void)cudaGetLastError();

@@ -25,6 +25,8 @@ struct kvc_pool {
     bool tmap_ok;
     CUtensorMap tmap16;   // same rows, box {128 B, 16 rows}: the keys or the values of 16 positions
     bool tmap16_ok;
+    CUtensorMap tmap_sub; // pools whose blocks are whole groups of 16 positions: box {128 B, the rows of 16 positions}
+    bool tmap_sub_ok;
     void *ws;             // workspace: arrival counters [ws_counters], then split / record partials
     size_t ws_bytes;      // partial bytes after the counter region
     size_t ws_counters;   // arrival counters at the front (zero between launches)

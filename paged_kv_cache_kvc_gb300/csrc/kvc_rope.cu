@@ -42,6 +42,12 @@ struct RopeParams {
     float eps;
     const float *scales;       // this layer's [2][H_KV][D], or nullptr (bf16)
     uint32_t *err;
+    // rows by slot (kvc_rope_write_slots): bt, start and cu are unused
+    const int32_t *slots;      // [rows]
+    const int32_t *positions;  // [num_axes][axis_stride]
+    int64_t axis_stride;
+    int32_t num_axes;
+    const uint8_t *axis_of;    // [R / 2] or nullptr
 };
 
 // cos and sin of t * f (radians), t a position
@@ -123,6 +129,21 @@ struct alignas(16) RopeBatch {
     bool live[TPC];
 };
 
+// One thread: the given place of row r, the batch's token w.
+template <int D, int TPC>
+__device__ __forceinline__ void resolve_slot(const RopeParams &p, RopeBatch<D, TPC> &s, int w, int64_t r)
+{
+    const int32_t slot = r < p.rows ? __ldg(p.slots + r) : -1;
+    s.live[w] = slot != -1;
+    int64_t blk = -1;
+    if (slot != -1) {
+        if (slot < 0 || slot / p.bs >= p.N) atomicOr(p.err, KVC_EBIT_BAD_BLOCK);
+        else blk = static_cast<int64_t>(p.layer) * p.N + slot / p.bs;
+        s.slot[w] = slot % p.bs;
+    }
+    s.block[w] = blk;
+}
+
 // One thread: sequence, position and place of row r, the batch's token w.
 template <int D, int TPC>
 __device__ __forceinline__ void resolve_token(const RopeParams &p, RopeBatch<D, TPC> &s, int w, int64_t r)
@@ -156,9 +177,10 @@ __device__ __forceinline__ void resolve_token(const RopeParams &p, RopeBatch<D, 
     s.block[w] = blk;
 }
 
-// Threads tid of n: the factors of the batch's tokens, a pair (i, j) at a time.
-template <int D, int TPC>
-__device__ __forceinline__ void build_factors(const RopeParams &p, RopeBatch<D, TPC> &s, int tid, int n)
+// Threads tid of n: the factors of the batch's tokens, a pair (i, j) at a time.  SLOTS: r0 is the batch's first row,
+// whose positions the pairs take from their axes.
+template <int D, int TPC, bool SLOTS>
+__device__ __forceinline__ void build_factors(const RopeParams &p, RopeBatch<D, TPC> &s, int tid, int n, int64_t r0)
 {
     const int half = p.R >> 1;
     const int per = D / 2;   // pairs of a row: half that turn, the rest pass through
@@ -168,7 +190,18 @@ __device__ __forceinline__ void build_factors(const RopeParams &p, RopeBatch<D, 
         const bool turn = i < half;
         const int a = turn ? (p.interleaved ? 2 * i : i) : p.R + 2 * (i - half);
         const int b = turn ? (p.interleaved ? 2 * i + 1 : i + half) : a + 1;
-        const float2 cs = turn ? rotation(s.pos[tk], __ldg(p.inv_freq + i)) : make_float2(1.f, 0.f);
+        int32_t t = 0;
+        if constexpr (SLOTS) {
+            int axis = turn && p.axis_of ? __ldg(p.axis_of + i) : 0;
+            if (axis >= p.num_axes) {
+                atomicOr(p.err, KVC_EBIT_RANGE);
+                axis = 0;
+            }
+            if (turn) t = __ldg(p.positions + axis * p.axis_stride + r0 + tk);
+        } else {
+            t = s.pos[tk];
+        }
+        const float2 cs = turn ? rotation(t, __ldg(p.inv_freq + i)) : make_float2(1.f, 0.f);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const uint16_t *w = k ? p.k_norm : p.q_norm;
@@ -189,7 +222,8 @@ __device__ __forceinline__ void build_factors(const RopeParams &p, RopeBatch<D, 
 // 74 us, 5.4 TB/s, 80 % of the copy rate; e4m3 pools 95 us and int4 98 (the exact divisions by the scales).  A CTA
 // per four tokens without the ninth warp took 97 us (each CTA began with the chain of loads), the same with one row
 // in flight 111 us; per-row address arithmetic and one loop over all kinds of head 95 us.
-template <int D, int GPT, int U>
+// SLOTS: rows whose places and positions are given; else sequences' runs of tokens.
+template <int D, int GPT, int U, bool SLOTS>
 __global__ void __launch_bounds__(kRopeCta, 3) rope_kernel(const RopeParams p)
 {
     constexpr int CPR = D / 8;                            // chunks (lanes) per head row
@@ -219,9 +253,13 @@ __global__ void __launch_bounds__(kRopeCta, 3) rope_kernel(const RopeParams p)
     };
     if (mover) first_rows(batch * TPC + tk);
     static_assert(TPC <= 32, "one warp resolves a batch");
-    if (tid < TPC) resolve_token(p, sh[0], tid, batch * TPC + tid);
+    auto resolve = [&](RopeBatch<D, TPC> &n, int w, int64_t r) {
+        if constexpr (SLOTS) resolve_slot(p, n, w, r);
+        else resolve_token(p, n, w, r);
+    };
+    if (tid < TPC) resolve(sh[0], tid, batch * TPC + tid);
     __syncthreads();
-    build_factors(p, sh[0], tid, kRopeCta);
+    build_factors<D, TPC, SLOTS>(p, sh[0], tid, kRopeCta, batch * TPC);
     const bool turns = 8 * c < p.R;
     // partner chunk of the half-split pairing
     const int hc = p.R >> 4;
@@ -236,9 +274,9 @@ __global__ void __launch_bounds__(kRopeCta, 3) rope_kernel(const RopeParams p)
         if (!mover) {
             if (after < batches) {
                 RopeBatch<D, TPC> &n = sh[(it + 1) & 1];
-                if (lane < TPC) resolve_token(p, n, lane, after * TPC + lane);
+                if (lane < TPC) resolve(n, lane, after * TPC + lane);
                 __syncwarp();
-                build_factors(p, n, lane, 32);
+                build_factors<D, TPC, SLOTS>(p, n, lane, 32, after * TPC);
             }
             continue;
         }
@@ -333,12 +371,12 @@ __global__ void __launch_bounds__(kRopeCta, 3) rope_kernel(const RopeParams p)
     }
 }
 
-template <int D, int GPT, int U>
-static kvc_status launch_rope(const RopeParams &p, int sms, cudaStream_t stream)
+template <int D, int GPT, int U, bool SLOTS>
+static kvc_status launch_rope_as(const RopeParams &p, int sms, cudaStream_t stream)
 {
     constexpr int TPC = kRopeThreads / (D / 8) / GPT;
     struct Tag {};
-    const DecodeKernel k = configured<Tag>(reinterpret_cast<const void *>(&rope_kernel<D, GPT, U>), 0, kRopeCta, false);
+    const DecodeKernel k = configured<Tag>(reinterpret_cast<const void *>(&rope_kernel<D, GPT, U, SLOTS>), 0, kRopeCta, false);
     if (k.ctas_per_sm <= 0) return KVC_ERR_CUDA;
     // A programmatic dependent: its launch overlaps the tail of the kernel before it, which it
     // waits for before its first access.  It never lets its own dependents start early: the
@@ -353,10 +391,16 @@ static kvc_status launch_rope(const RopeParams &p, int sms, cudaStream_t stream)
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, rope_kernel<D, GPT, U>, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, rope_kernel<D, GPT, U, SLOTS>, p);
     if (e != cudaSuccess) return cuda_status(e);
     g_launches.fetch_add(1, std::memory_order_relaxed);
     return KVC_OK;
+}
+
+template <int D, int GPT, int U>
+static kvc_status launch_rope(const RopeParams &p, int sms, cudaStream_t stream)
+{
+    return p.slots ? launch_rope_as<D, GPT, U, true>(p, sms, stream) : launch_rope_as<D, GPT, U, false>(p, sms, stream);
 }
 
 static bool aligned(const void *ptr, size_t a) { return (reinterpret_cast<uintptr_t>(ptr) & (a - 1)) == 0; }
@@ -370,12 +414,24 @@ static bool overlap(const void *a, int64_t sa, int64_t wa, const void *b, int64_
     return a0 < b1 && b0 < a1;
 }
 
-static kvc_status rope_write(kvc_pool *pool, int32_t layer, const int32_t *bt, int32_t max_blocks,
-                             const int32_t *start, const int32_t *cu, int32_t B, int64_t rows, const void *q,
+// Where the rows go: runs of sequences' tokens through a block table, or slots with positions of their own.
+struct RopePlaces {
+    const int32_t *bt = nullptr;
+    int32_t max_blocks = 0;
+    const int32_t *start = nullptr, *cu = nullptr;
+    int32_t B = 0;
+    bool by_slot = false;
+    const int32_t *slots = nullptr, *positions = nullptr;
+    int64_t axis_stride = 0;
+    int32_t num_axes = 0;
+    const uint8_t *axis_of = nullptr;
+};
+
+static kvc_status rope_write(kvc_pool *pool, int32_t layer, const RopePlaces &at, int64_t rows, const void *q,
                              int64_t q_stride, int32_t H_Q, const void *k, int64_t k_stride, const void *v,
                              int64_t v_stride, const kvc_rope *rope, void *q_out, cudaStream_t stream)
 {
-    if (!pool || !rope || B < 0 || rows < 0 || rows > 0x7FFFFFFF || H_Q < 0 || H_Q > 65536) return KVC_ERR_ARG;
+    if (!pool || !rope || at.B < 0 || rows < 0 || rows > 0x7FFFFFFF || H_Q < 0 || H_Q > 65536) return KVC_ERR_ARG;
     const int D = pool->D;
     if (rope->rotary_dim < 0 || rope->rotary_dim > D || (rope->rotary_dim > 0 && !rope->inv_freq) ||
         !aligned(rope->inv_freq, 4) || !aligned(rope->q_norm, 16) || !aligned(rope->k_norm, 16) ||
@@ -383,10 +439,15 @@ static kvc_status rope_write(kvc_pool *pool, int32_t layer, const int32_t *bt, i
         return KVC_ERR_ARG;
     if (rope->rotary_dim % 16 != 0) return KVC_ERR_UNSUPPORTED;
     if ((rope->q_norm || rope->k_norm) && !(std::isfinite(rope->norm_eps) && rope->norm_eps >= 0.f)) return KVC_ERR_ARG;
-    if (B == 0 || rows == 0) return KVC_OK;
-    if (layer < 0 || layer >= pool->L || max_blocks <= 0) return KVC_ERR_ARG;
-    if (!bt || !start || !k || !v || !aligned(k, 16) || !aligned(v, 16) || !aligned(bt, 4) || !aligned(start, 4))
+    if (at.by_slot && (at.num_axes < 1 || at.num_axes > 8 || at.axis_stride < 0)) return KVC_ERR_ARG;
+    if ((!at.by_slot && at.B == 0) || rows == 0) return KVC_OK;
+    if (layer < 0 || layer >= pool->L) return KVC_ERR_ARG;
+    if (at.by_slot) {
+        if (!at.slots || !at.positions || !aligned(at.slots, 4) || !aligned(at.positions, 4)) return KVC_ERR_ARG;
+    } else if (at.max_blocks <= 0 || !at.bt || !at.start || !aligned(at.bt, 4) || !aligned(at.start, 4)) {
         return KVC_ERR_ARG;
+    }
+    if (!k || !v || !aligned(k, 16) || !aligned(v, 16)) return KVC_ERR_ARG;
     const int64_t qw = static_cast<int64_t>(H_Q) * D, kw = static_cast<int64_t>(pool->H_KV) * D;
     if (k_stride < kw || v_stride < kw || k_stride % 8 != 0 || v_stride % 8 != 0) return KVC_ERR_ARG;
     if (H_Q > 0) {
@@ -407,11 +468,16 @@ static kvc_status rope_write(kvc_pool *pool, int32_t layer, const int32_t *bt, i
     p.H_Q = H_Q;
     p.layer = layer;
     p.bits = pool->bits;
-    p.bt = bt;
-    p.max_blocks = max_blocks;
-    p.B = B;
-    p.start = start;
-    p.cu = cu;
+    p.bt = at.bt;
+    p.max_blocks = at.max_blocks;
+    p.B = at.B;
+    p.start = at.start;
+    p.cu = at.cu;
+    p.slots = at.slots;
+    p.positions = at.positions;
+    p.axis_stride = at.axis_stride;
+    p.num_axes = at.num_axes;
+    p.axis_of = at.axis_of;
     p.rows = rows;
     p.q = static_cast<const uint16_t *>(q);
     p.k = static_cast<const uint16_t *>(k);
@@ -450,8 +516,13 @@ extern "C" kvc_status kvc_rope_append(kvc_pool *pool, int32_t layer, const int32
                                       int32_t num_q_heads, const void *k_new, int64_t k_stride, const void *v_new,
                                       int64_t v_stride, const kvc_rope *rope, void *q_out, kvc_stream_t stream)
 {
-    return rope_write(pool, layer, block_tables, max_blocks, seq_lens, nullptr, B, B, q, q_stride, num_q_heads, k_new,
-                      k_stride, v_new, v_stride, rope, q_out, static_cast<cudaStream_t>(stream));
+    RopePlaces at;
+    at.bt = block_tables;
+    at.max_blocks = max_blocks;
+    at.start = seq_lens;
+    at.B = B;
+    return rope_write(pool, layer, at, B, q, q_stride, num_q_heads, k_new, k_stride, v_new, v_stride, rope, q_out,
+                      static_cast<cudaStream_t>(stream));
 }
 
 extern "C" kvc_status kvc_rope_write_tokens(kvc_pool *pool, int32_t layer, const int32_t *block_tables,
@@ -461,6 +532,29 @@ extern "C" kvc_status kvc_rope_write_tokens(kvc_pool *pool, int32_t layer, const
                                             int64_t v_stride, const kvc_rope *rope, void *q_out, kvc_stream_t stream)
 {
     if (B > 0 && (!cu_tokens || !aligned(cu_tokens, 4))) return KVC_ERR_ARG;
-    return rope_write(pool, layer, block_tables, max_blocks, start_pos, cu_tokens, B, n_rows, q, q_stride, num_q_heads,
-                      k, k_stride, v, v_stride, rope, q_out, static_cast<cudaStream_t>(stream));
+    RopePlaces at;
+    at.bt = block_tables;
+    at.max_blocks = max_blocks;
+    at.start = start_pos;
+    at.cu = cu_tokens;
+    at.B = B;
+    return rope_write(pool, layer, at, n_rows, q, q_stride, num_q_heads, k, k_stride, v, v_stride, rope, q_out,
+                      static_cast<cudaStream_t>(stream));
+}
+
+extern "C" kvc_status kvc_rope_write_slots(kvc_pool *pool, int32_t layer, const int32_t *slots,
+                                           const int32_t *positions, int64_t axis_stride, int32_t num_axes,
+                                           const uint8_t *axis_of, int64_t n_rows, const void *q, int64_t q_stride,
+                                           int32_t num_q_heads, const void *k, int64_t k_stride, const void *v,
+                                           int64_t v_stride, const kvc_rope *rope, void *q_out, kvc_stream_t stream)
+{
+    RopePlaces at;
+    at.by_slot = true;
+    at.slots = slots;
+    at.positions = positions;
+    at.axis_stride = axis_stride;
+    at.num_axes = num_axes;
+    at.axis_of = axis_of;
+    return rope_write(pool, layer, at, n_rows, q, q_stride, num_q_heads, k, k_stride, v, v_stride, rope, q_out,
+                      static_cast<cudaStream_t>(stream));
 }

@@ -1,0 +1,631 @@
+// Block bounds and the choice of blocks for sparse attention.
+//
+// Bounds of a block and KV head, over its filled places t:  hi_i = max_t k_ti, lo_i = min_t k_ti, kept as int8
+// codes ceil(hi / 2^e), floor(lo / 2^e) with the smallest e in [-100, 100] that fits both into 127.  A power of two
+// as the unit makes every step exact but the outward rounding, and with queries rounded to integers Q the score
+//   s_j = 2^e_j max_g sum_i Q_gi (Q_gi > 0 ? hi_ji : lo_ji)
+// is an integer below 127 * 127 * 128 < 2^21 times a power of two: exact in fp32 whatever the order of the sum.  So
+// the blocks chosen depend on the inputs alone, not on the grid, and equal scores go to the lower block.
+#include <algorithm>
+
+#include "kvc_cluster.cuh"
+#include "kvc_configured.cuh"
+
+namespace kvc {
+
+// ------------------------------------------------------------------ bounds layout
+static uint64_t bounds_layer_bytes(const kvc_pool *pool)
+{
+    const uint64_t n = static_cast<uint64_t>(pool->N) * pool->H_KV * (2 * pool->D + 4);
+    return (n + 255) / 256 * 256;
+}
+
+// The smallest e in [-100, 100] with x <= 127 * 2^e (100 if none), x >= 0 as float bits.
+__device__ __forceinline__ int unit_exponent(float x)
+{
+    const uint32_t u = __float_as_uint(x) & 0x7FFFFFFFu;
+    // x = (1 + f / 2^23) 2^(E - 127); it fits into 127 * 2^e = 1.984375 * 2^(e + 6) from e = E - 133 on, or one later
+    const int e = static_cast<int>(u >> 23) - 133 + ((u & 0x7FFFFFu) > 0x7E0000u ? 1 : 0);
+    return min(max(e, -100), 100);
+}
+
+__device__ __forceinline__ float exp2_int(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+
+__device__ __forceinline__ uint32_t max2_bf16(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t min2_bf16(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t max2_f16(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t min2_f16(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+struct BoundsParams {
+    const uint8_t *base;
+    int64_t N;
+    int32_t bs, H_KV, layer;
+    const int32_t *slots;
+    int64_t rows;
+    int32_t rows_per_cta;
+    int8_t *codes;             // this layer's [N][H_KV][2][D]
+    float *units;              // [N][H_KV]
+    const float *s_k;          // this layer's key scales [H_KV][D] or nullptr
+    uint32_t *err;
+};
+
+constexpr int kBoundsThreads = 256;
+
+// grid (row chunk, KV head).  A CTA finds the chunk's last rows of blocks, then its warps take a block each: LPR lanes
+// per key row, 16 bytes a lane, 32 / LPR rows at a time; channels' extremes in packed halves, then across the rows'
+// lanes.  Bound by HBM: the keys are read once.
+template <int D, int KIND>
+__global__ void __launch_bounds__(kBoundsThreads) bounds_kernel(const BoundsParams p)
+{
+    constexpr int BITS = KIND == KV_BF16 ? 16 : (KIND == KV_E4M3 ? 8 : 4);
+    constexpr int ROW = D * BITS / 8;             // bytes of a key row
+    constexpr int LPR = ROW / 16;                 // lanes per row
+    constexpr int RPS = 32 / LPR;                 // rows per step
+    constexpr int E = D / LPR;                    // channels per lane
+    constexpr int P = E / 2;                      // packed pairs
+    __shared__ int32_t ends[kBoundsThreads];      // slots of the last rows of this chunk's blocks
+    __shared__ int32_t n_ends;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, h = blockIdx.y;
+    if (tid == 0) n_ends = 0;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    __syncthreads();
+    const int64_t r = static_cast<int64_t>(blockIdx.x) * p.rows_per_cta + tid;
+    if (tid < p.rows_per_cta && r < p.rows) {
+        const int32_t slot = __ldg(p.slots + r);
+        if (slot < -1 || (slot >= 0 && slot / p.bs >= p.N)) {
+            if (h == 0) atomicOr(p.err, KVC_EBIT_BAD_BLOCK);
+        } else if (slot >= 0 && ((slot + 1) % p.bs == 0 || r + 1 == p.rows || __ldg(p.slots + r + 1) != slot + 1)) {
+            ends[atomicAdd(&n_ends, 1)] = slot;
+        }
+    }
+    __syncthreads();
+    const int c = lane % LPR, sub = lane / LPR;
+    for (int i = warp; i < n_ends; i += kBoundsThreads / 32) {
+        const int32_t slot = ends[i], blk = slot / p.bs;
+        const int n = slot - blk * p.bs + 1;
+        const uint8_t *keys = p.base + ((static_cast<int64_t>(p.layer) * p.N + blk) * p.H_KV + h) * (2ll * p.bs * ROW);
+        uint32_t hi[P], lo[P];
+#pragma unroll
+        for (int x = 0; x < P; ++x) {   // -inf, +inf: no key yet
+            hi[x] = KIND == KV_BF16 ? 0xFF80FF80u : 0xFC00FC00u;
+            lo[x] = KIND == KV_BF16 ? 0x7F807F80u : 0x7C007C00u;
+        }
+        constexpr int U = RPS >= 8 ? 2 : (RPS >= 4 ? 4 : 8);
+        for (int t0 = sub; t0 < n; t0 += U * RPS) {
+            uint4 v[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {   // past the last row: the last one of this lane's again
+                const int t = min(t0 + u * RPS, n - 1);
+                v[u] = *reinterpret_cast<const uint4 *>(keys + static_cast<int64_t>(t) * ROW + 16 * c);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if constexpr (KIND == KV_BF16) {
+                        hi[k] = max2_bf16(hi[k], w[k]);
+                        lo[k] = min2_bf16(lo[k], w[k]);
+                    } else if constexpr (KIND == KV_E4M3) {
+                        uint32_t a, b;
+                        e4m3x4_to_f16x2x2(w[k], a, b);
+                        hi[2 * k] = max2_f16(hi[2 * k], a);
+                        lo[2 * k] = min2_f16(lo[2 * k], a);
+                        hi[2 * k + 1] = max2_f16(hi[2 * k + 1], b);
+                        lo[2 * k + 1] = min2_f16(lo[2 * k + 1], b);
+                    } else {   // pair m of word k: channels 8k + m and 8k + m + 4
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) {
+                            const uint32_t a = nibbles_to_f16x2(w[k] >> (4 * m));
+                            hi[4 * k + m] = max2_f16(hi[4 * k + m], a);
+                            lo[4 * k + m] = min2_f16(lo[4 * k + m], a);
+                        }
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int o = LPR; o < 32; o <<= 1)
+#pragma unroll
+            for (int x = 0; x < P; ++x) {
+                const uint32_t a = __shfl_xor_sync(kFull, hi[x], o), b = __shfl_xor_sync(kFull, lo[x], o);
+                hi[x] = KIND == KV_BF16 ? max2_bf16(hi[x], a) : max2_f16(hi[x], a);
+                lo[x] = KIND == KV_BF16 ? min2_bf16(lo[x], b) : min2_f16(lo[x], b);
+            }
+        // this lane finishes its channels' upper bounds (sub 0) or lower ones (sub 1); the rest only help with e
+        float y[E], top = 0.f;
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+#pragma unroll
+            for (int x = 0; x < P; ++x) {
+                const uint32_t w = which ? lo[x] : hi[x];
+                float2 f;
+                if constexpr (KIND == KV_BF16) {
+                    f = make_float2(bf16_lo(w), bf16_hi(w));
+                } else {
+                    f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+                }
+                const int c0 = KIND == KV_INT4 ? 8 * (x >> 2) + (x & 3) : 2 * x, c1 = KIND == KV_INT4 ? c0 + 4 : c0 + 1;
+                if constexpr (KIND != KV_BF16) {
+                    const float *sc = p.s_k + static_cast<int64_t>(h) * D + E * c;
+                    f.x *= __ldg(sc + c0);
+                    f.y *= __ldg(sc + c1);
+                }
+                const float none = which ? -INFINITY : INFINITY;   // what a NaN counts as
+                f.x = isnan(f.x) ? none : f.x;
+                f.y = isnan(f.y) ? none : f.y;
+                top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+                if (which == (sub & 1)) {
+                    y[c0] = f.x;
+                    y[c1] = f.y;
+                }
+            }
+        }
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+        const int e = unit_exponent(top);
+        const float inv = exp2_int(-e);
+        if (sub < 2) {
+            uint32_t out[E / 4];
+#pragma unroll
+            for (int x = 0; x < E / 4; ++x) {
+                out[x] = 0u;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float z = y[4 * x + k] * inv;
+                    const float w = fminf(fmaxf(sub ? floorf(z) : ceilf(z), -127.f), 127.f);
+                    out[x] |= (static_cast<uint32_t>(static_cast<int>(w)) & 255u) << (8 * k);
+                }
+            }
+            const int64_t rec = static_cast<int64_t>(blk) * p.H_KV + h;
+            int8_t *dst = p.codes + rec * (2 * D) + sub * D + E * c;
+            if constexpr (E == 8) {
+                *reinterpret_cast<uint2 *>(dst) = make_uint2(out[0], out[1]);
+            } else {
+#pragma unroll
+                for (int x = 0; x < E / 16; ++x)
+                    reinterpret_cast<uint4 *>(dst)[x] = make_uint4(out[4 * x], out[4 * x + 1], out[4 * x + 2], out[4 * x + 3]);
+            }
+            if (lane == 0) p.units[rec] = exp2_int(e);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ selection
+struct SelectParams {
+    const int8_t *codes;
+    const float *units;
+    const uint16_t *q;         // bf16 [rows][H_Q][D]
+    int32_t H_Q, H_KV, g, bs;
+    int64_t N;
+    const int32_t *bt;
+    int32_t max_blocks, B;
+    const int32_t *seqs, *positions;
+    int32_t top_k, sink, recent;
+    int32_t *lists;            // [rows][H_KV][top_k]
+    uint32_t *err;
+};
+
+constexpr int kSelThreads = 256;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelMostBlocks = 262144;
+constexpr int kSelKeys = 32768;     // keys that a CTA holds
+
+// Scores as unsigned numbers of the same order; 0 and ~0 are no finite score's.
+__device__ __forceinline__ uint32_t score_key(float x)
+{
+    const uint32_t u = __float_as_uint(x);
+    return (u >> 31) ? ~u : (u | 0x80000000u);
+}
+
+// grid (C x rows, KV head), clusters of C CTAs along x.  CTA c of a cluster scores the c-th part of the row's blocks
+// into keys in shared memory; the k-th largest key is found digit by digit over the cluster's histograms, and each
+// CTA writes its part of the list in order.
+template <int D>
+__global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams p)
+{
+    constexpr int LPR = D / 16;          // lanes per record: 16 channels each
+    constexpr int RPS = 32 / LPR;        // records per step
+    constexpr int U = 4;                 // steps at a time
+    extern __shared__ uint32_t keys[];
+    __shared__ __align__(16) uint32_t qw[32][2][D / 4];   // the group's queries: positive parts, negative parts, int8
+    __shared__ uint32_t hist[2][256], sum[256];
+    __shared__ uint32_t top_bits, pick_bin, pick_above, n_valid, n_gt, n_eq;
+    __shared__ uint32_t warp_gt[kSelWarps], warp_eq[kSelWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int cs = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
+    const int64_t row = blockIdx.x / static_cast<unsigned>(cs);
+    const int h = blockIdx.y;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int seq = p.seqs ? __ldg(p.seqs + row) : static_cast<int>(row);
+    const int pos = __ldg(p.positions + row);
+    if (seq == -1 || pos == -1) return;   // padding: the whole cluster leaves
+    int32_t *list = p.lists + (row * p.H_KV + h) * p.top_k;
+    if (seq < 0 || seq >= p.B || pos < 0 || pos / p.bs >= p.max_blocks) {
+        if (rank == 0 && h == 0 && tid == 0) atomicOr(p.err, KVC_EBIT_RANGE);
+        for (int i = rank * kSelThreads + tid; i < p.top_k; i += cs * kSelThreads) list[i] = -1;
+        return;
+    }
+    const int nb = pos / p.bs + 1;
+    const int per = (nb + cs - 1) / cs;
+    const int j0 = min(nb, rank * per), n = min(nb, j0 + per) - j0;   // this CTA's blocks
+    const int32_t *bt = p.bt + static_cast<int64_t>(seq) * p.max_blocks;
+    const bool all = nb <= p.top_k;   // every block is listed: no score needed
+
+    // ---- the group's queries as integers
+    if (tid == 0) {
+        top_bits = 0u;
+        n_valid = n_gt = n_eq = 0u;
+    }
+    __syncthreads();
+    if (!all) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (row * p.H_Q + static_cast<int64_t>(h) * p.g) * D);
+        const int chunks = p.g * D / 8;
+        uint4 x[2];
+        float m = 0.f;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int i = tid + u * kSelThreads;
+            x[u] = i < chunks ? src[i] : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) m = fmaxf(m, fmaxf(fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k]))));   // NaNs drop out
+        }
+        const uint32_t bits = __reduce_max_sync(kFull, __float_as_uint(m));   // not negative: ordered as integers
+        if (lane == 0) atomicMax(&top_bits, bits);
+        __syncthreads();
+        const float inv = exp2_int(-unit_exponent(__uint_as_float(top_bits)));
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int i = tid + u * kSelThreads;
+            if (i >= chunks) continue;
+            const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+            uint32_t pw[2] = {0u, 0u}, nw[2] = {0u, 0u};
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float f = (k & 1) ? bf16_hi(w[k >> 1]) : bf16_lo(w[k >> 1]);
+                const int z = isnan(f) ? 0 : static_cast<int>(fminf(fmaxf(rintf(f * inv), -127.f), 127.f));
+                pw[k >> 2] |= (static_cast<uint32_t>(max(z, 0)) & 255u) << (8 * (k & 3));
+                nw[k >> 2] |= (static_cast<uint32_t>(min(z, 0)) & 255u) << (8 * (k & 3));
+            }
+            const int head = 8 * i / D, word = (8 * i % D) / 4;
+            qw[head][0][word] = pw[0];
+            qw[head][0][word + 1] = pw[1];
+            qw[head][1][word] = nw[0];
+            qw[head][1][word + 1] = nw[1];
+        }
+        __syncthreads();
+    }
+
+    // ---- scores of this CTA's blocks, 32 blocks a warp at a time
+    const int c = lane % LPR, sub = lane / LPR;
+    for (int t0 = warp * 32; t0 < n; t0 += kSelThreads) {
+        const int j = j0 + t0 + lane;
+        const bool in = t0 + lane < n;
+        int phys = in ? __ldg(bt + j) : -1;
+        if (in && (phys < 0 || static_cast<int64_t>(phys) >= p.N)) {
+            if (h == 0) atomicOr(p.err, KVC_EBIT_BAD_BLOCK);
+            phys = -1;
+        }
+        const bool forced = j < p.sink || j >= nb - p.recent || all;
+        if (all) {
+            if (in) keys[t0 + lane] = phys < 0 ? 0u : 0xFFFFFFFFu;
+            continue;
+        }
+        const float unit = phys < 0 ? 0.f : __ldg(p.units + static_cast<int64_t>(phys) * p.H_KV + h);
+#pragma unroll
+        for (int it = 0; it < 32; it += U * RPS) {
+            if (t0 + it >= n) break;
+            uint4 hi[U], lo[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int blk = __shfl_sync(kFull, phys, it + u * RPS + sub);
+                const int8_t *rec = p.codes + (static_cast<int64_t>(max(blk, 0)) * p.H_KV + h) * (2 * D) + 16 * c;
+                hi[u] = __ldg(reinterpret_cast<const uint4 *>(rec));
+                lo[u] = __ldg(reinterpret_cast<const uint4 *>(rec + D));
+            }
+            int best = INT32_MIN;
+            for (int g = 0; g < p.g; ++g) {
+                const uint4 a = *reinterpret_cast<const uint4 *>(&qw[g][0][4 * c]);
+                const uint4 b = *reinterpret_cast<const uint4 *>(&qw[g][1][4 * c]);
+                int acc[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    int x = __dp4a(static_cast<int>(hi[u].x), static_cast<int>(a.x), 0);
+                    x = __dp4a(static_cast<int>(hi[u].y), static_cast<int>(a.y), x);
+                    x = __dp4a(static_cast<int>(hi[u].z), static_cast<int>(a.z), x);
+                    x = __dp4a(static_cast<int>(hi[u].w), static_cast<int>(a.w), x);
+                    x = __dp4a(static_cast<int>(lo[u].x), static_cast<int>(b.x), x);
+                    x = __dp4a(static_cast<int>(lo[u].y), static_cast<int>(b.y), x);
+                    x = __dp4a(static_cast<int>(lo[u].z), static_cast<int>(b.z), x);
+                    acc[u] = __dp4a(static_cast<int>(lo[u].w), static_cast<int>(b.w), x);
+                }
+                // sum over the record's lanes, each lane keeping fewer of the U records: record 2 x + y ends in the
+                // lanes whose highest two bits (of the record's LPR lanes) are x, y
+                constexpr int o1 = LPR / 2, o2 = LPR / 4;
+                const bool b1 = (c & o1) != 0, b2 = (c & o2) != 0;
+                const int s0 = b1 ? acc[0] : acc[2], s1 = b1 ? acc[1] : acc[3];
+                int k0 = b1 ? acc[2] : acc[0], k1 = b1 ? acc[3] : acc[1];
+                k0 += __shfl_xor_sync(kFull, s0, o1);
+                k1 += __shfl_xor_sync(kFull, s1, o1);
+                int v = (b2 ? k1 : k0) + __shfl_xor_sync(kFull, b2 ? k0 : k1, o2);
+                if constexpr (LPR == 8) v += __shfl_xor_sync(kFull, v, 1);
+                best = max(best, v);
+            }
+            const int u = (c & (LPR / 2) ? 2 : 0) + (c & (LPR / 4) ? 1 : 0);
+            const int at = it + u * RPS + sub;   // of the warp's 32 blocks
+            const float un = __shfl_sync(kFull, unit, at);
+            const int ph = __shfl_sync(kFull, phys, at);
+            const bool fo = __shfl_sync(kFull, static_cast<int>(forced), at) != 0;
+            if ((LPR == 4 || (c & 1) == 0) && t0 + at < n)
+                keys[t0 + at] = ph < 0 ? 0u : (fo ? 0xFFFFFFFFu : score_key(static_cast<float>(best) * un));
+        }
+    }
+    __syncthreads();
+
+    // ---- the k-th largest key
+    {
+        uint32_t valid = 0u;
+        for (int i = tid; i < n; i += kSelThreads) valid += keys[i] != 0u;
+        valid = __reduce_add_sync(kFull, valid);
+        if (lane == 0) atomicAdd(&n_valid, valid);
+    }
+    for (int i = tid; i < 512; i += kSelThreads) (&hist[0][0])[i] = 0u;
+    if (cs > 1) cluster_sync();
+    else __syncthreads();
+    uint32_t valid_in_all = 0u;
+    for (int r = 0; r < cs; ++r) valid_in_all += cluster_ld(cluster_addr(smem_u32(&n_valid), r));
+    uint32_t threshold = 0u, want = 0u;   // keys above the threshold are listed, and `want` keys equal to it
+    if (valid_in_all > static_cast<uint32_t>(p.top_k)) {
+        want = static_cast<uint32_t>(p.top_k);
+        uint32_t mask = 0u;
+#pragma unroll 1
+        for (int pass = 0; pass < 4; ++pass) {
+            const int shift = 24 - 8 * pass;
+            uint32_t *hs = hist[pass & 1];
+            for (int i = tid; i < n; i += kSelThreads) {
+                const uint32_t k = keys[i];
+                if (k != 0u && (k & mask) == threshold) atomicAdd(&hs[(k >> shift) & 255u], 1u);
+            }
+            if (cs > 1) cluster_sync();
+            else __syncthreads();
+            uint32_t s = 0u;
+            for (int r = 0; r < cs; ++r) s += cluster_ld(cluster_addr(smem_u32(&hs[tid]), r));
+            sum[tid] = s;
+            __syncthreads();
+            if (warp == 0) {   // lane l: bins 255 - 8 l downwards
+                uint32_t mine = 0u;
+#pragma unroll
+                for (int x = 0; x < 8; ++x) mine += sum[255 - 8 * lane - x];
+                uint32_t inc = mine;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const uint32_t y = __shfl_up_sync(kFull, inc, o);
+                    if (lane >= o) inc += y;
+                }
+                uint32_t above = inc - mine;
+                if (above < want && inc >= want)
+                    for (int x = 0; x < 8; ++x) {
+                        const uint32_t s1 = sum[255 - 8 * lane - x];
+                        if (above + s1 >= want) {
+                            pick_bin = static_cast<uint32_t>(255 - 8 * lane - x);
+                            pick_above = above;
+                            break;
+                        }
+                        above += s1;
+                    }
+            }
+            __syncthreads();
+            threshold |= pick_bin << shift;
+            mask |= 255u << shift;
+            want -= pick_above;
+            hist[(pass + 1) & 1][tid] = 0u;   // last read, by any CTA, before this pass's barrier
+            __syncthreads();
+        }
+    }
+
+    // ---- the list, in order of the blocks
+    {
+        uint32_t gt = 0u, eq = 0u;
+        for (int i = tid; i < n; i += kSelThreads) {
+            const uint32_t k = keys[i];
+            gt += k > threshold;
+            eq += k != 0u && k == threshold;
+        }
+        gt = __reduce_add_sync(kFull, gt);
+        eq = __reduce_add_sync(kFull, eq);
+        if (lane == 0) {
+            atomicAdd(&n_gt, gt);
+            atomicAdd(&n_eq, eq);
+        }
+    }
+    if (cs > 1) cluster_sync();
+    else __syncthreads();
+    uint32_t gt_before = 0u, eq_before = 0u, listed = 0u, eq_all = 0u;
+    for (int r = 0; r < cs; ++r) {
+        const uint32_t a = cluster_ld(cluster_addr(smem_u32(&n_gt), r)), b = cluster_ld(cluster_addr(smem_u32(&n_eq), r));
+        if (r < rank) {
+            gt_before += a;
+            eq_before += b;
+        }
+        listed += a;
+        eq_all += b;
+    }
+    listed += min(eq_all, want);
+    for (int base = 0; base < n; base += kSelThreads) {
+        const int i = base + tid;
+        const uint32_t k = i < n ? keys[i] : 0u;
+        const bool gt = k > threshold, eq = k != 0u && k == threshold;
+        const uint32_t mg = __ballot_sync(kFull, gt), me = __ballot_sync(kFull, eq);
+        if (lane == 0) {
+            warp_gt[warp] = __popc(mg);
+            warp_eq[warp] = __popc(me);
+        }
+        __syncthreads();
+        uint32_t g0 = gt_before, e0 = eq_before;
+        for (int w = 0; w < kSelWarps; ++w) {
+            if (w < warp) {
+                g0 += warp_gt[w];
+                e0 += warp_eq[w];
+            }
+            gt_before += warp_gt[w];
+            eq_before += warp_eq[w];
+        }
+        const uint32_t below = (1u << lane) - 1u;
+        g0 += __popc(mg & below);
+        e0 += __popc(me & below);
+        if (gt || (eq && e0 < want)) list[g0 + min(e0, want)] = j0 + i;
+        __syncthreads();
+    }
+    for (int i = static_cast<int>(listed) + rank * kSelThreads + tid; i < p.top_k; i += cs * kSelThreads) list[i] = -1;
+    if (cs > 1) cluster_sync();   // a CTA's shared memory stays until the others have read it
+}
+
+static bool aligned(const void *ptr, size_t a) { return (reinterpret_cast<uintptr_t>(ptr) & (a - 1)) == 0; }
+
+// A launch that may start while the kernel before it drains, in clusters of `cluster` CTAs along x.
+template <typename P>
+static kvc_status launch(void (*fn)(P), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t stream, const P &p)
+{
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, p);
+    if (e != cudaSuccess) return cuda_status(e);
+    g_launches.fetch_add(1, std::memory_order_relaxed);
+    return KVC_OK;
+}
+
+template <int D>
+static kvc_status launch_select(const SelectParams &p, int64_t rows, int sms, cudaStream_t stream)
+{
+    struct Tag {};
+    const DecodeKernel k = configured<Tag>(reinterpret_cast<const void *>(&select_kernel<D>), 4 * kSelKeys, kSelThreads, false);
+    if (k.ctas_per_sm <= 0) return KVC_ERR_CUDA;
+    const int64_t units = rows * p.H_KV;
+    int c = 1;
+    while (c < 8 && ((units * c < 2ll * sms && p.max_blocks > 256 * c) || p.max_blocks > kSelKeys / 2 * c)) c *= 2;
+    if (rows * c > 0x7FFFFFFF) return KVC_ERR_UNSUPPORTED;
+    const int per = (p.max_blocks + c - 1) / c;
+    return launch(&select_kernel<D>, dim3(static_cast<unsigned>(rows * c), p.H_KV), kSelThreads, 4 * static_cast<size_t>(per), c,
+                  stream, p);
+}
+
+template <int D, int KIND>
+static kvc_status launch_bounds(const kvc_pool *pool, BoundsParams &p, cudaStream_t stream)
+{
+    // Few rows are a decoding batch's, nearly each the last one of its block: small chunks, so that every SM gets some.
+    p.rows_per_cta = p.rows * p.H_KV >= 64ll * 1024 ? kBoundsThreads : 16;
+    const int64_t chunks = (p.rows + p.rows_per_cta - 1) / p.rows_per_cta;
+    return launch(&bounds_kernel<D, KIND>, dim3(static_cast<unsigned>(chunks), pool->H_KV), kBoundsThreads, 0, 1, stream, p);
+}
+
+}  // namespace kvc
+
+using namespace kvc;
+
+extern "C" kvc_status kvc_bounds_bytes(const kvc_pool *pool, uint64_t *bytes)
+{
+    if (!pool || !bytes) return KVC_ERR_ARG;
+    *bytes = bounds_layer_bytes(pool) * pool->L;
+    return KVC_OK;
+}
+
+extern "C" kvc_status kvc_update_bounds(kvc_pool *pool, int32_t layer, const int32_t *slots, int64_t n_rows,
+                                        void *bounds, uint64_t bounds_bytes, kvc_stream_t stream)
+{
+    if (!pool || n_rows < 0 || n_rows > 0x7FFFFFFF || layer < 0 || layer >= pool->L) return KVC_ERR_ARG;
+    if (!bounds || !aligned(bounds, 256) || bounds_bytes < bounds_layer_bytes(pool) * pool->L) return KVC_ERR_ARG;
+    if (n_rows == 0) return KVC_OK;
+    if (!slots || !aligned(slots, 4)) return KVC_ERR_ARG;
+    const kvc_status st = check_device(pool);
+    if (st != KVC_OK) return st;
+    BoundsParams p{};
+    p.base = pool->base;
+    p.N = pool->N;
+    p.bs = pool->bs;
+    p.H_KV = pool->H_KV;
+    p.layer = layer;
+    p.slots = slots;
+    p.rows = n_rows;
+    p.codes = static_cast<int8_t *>(bounds) + bounds_layer_bytes(pool) * layer;
+    p.units = reinterpret_cast<float *>(p.codes + static_cast<size_t>(pool->N) * pool->H_KV * 2 * pool->D);
+    p.s_k = pool->scales ? pool->scales + static_cast<size_t>(layer) * 2 * pool->H_KV * pool->D : nullptr;
+    p.err = pool->err;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (pool->dtype == KVC_FP8_E4M3) return launch_bounds<128, KV_E4M3>(pool, p, s);
+    if (pool->dtype == KVC_INT4) return launch_bounds<128, KV_INT4>(pool, p, s);
+    return pool->D == 64 ? launch_bounds<64, KV_BF16>(pool, p, s) : launch_bounds<128, KV_BF16>(pool, p, s);
+}
+
+extern "C" kvc_status kvc_select_blocks(kvc_pool *pool, int32_t layer, const void *bounds, uint64_t bounds_bytes,
+                                        const void *q, int32_t num_q_heads, const int32_t *block_tables,
+                                        int32_t max_blocks, int32_t B, const int32_t *seq_ids,
+                                        const int32_t *positions, int64_t n_rows, int32_t top_k, int32_t sink,
+                                        int32_t recent, int32_t *selected, kvc_stream_t stream)
+{
+    if (!pool || B < 0 || n_rows < 0 || n_rows > 0x7FFFFFFF || num_q_heads <= 0 || num_q_heads % pool->H_KV != 0)
+        return KVC_ERR_ARG;
+    if (sink < 0 || recent < 1 || top_k > 65536 || static_cast<int64_t>(sink) + recent > top_k) return KVC_ERR_ARG;
+    if (num_q_heads / pool->H_KV > 32) return KVC_ERR_UNSUPPORTED;
+    if (!bounds || !aligned(bounds, 256) || bounds_bytes < bounds_layer_bytes(pool) * pool->L) return KVC_ERR_ARG;
+    if (n_rows == 0) return KVC_OK;
+    if (layer < 0 || layer >= pool->L || max_blocks <= 0 || (!seq_ids && n_rows > B)) return KVC_ERR_ARG;
+    if (max_blocks > kSelMostBlocks) return KVC_ERR_UNSUPPORTED;
+    if (!q || !block_tables || !positions || !selected || !aligned(q, 16) || !aligned(block_tables, 4) ||
+        !aligned(positions, 4) || !aligned(seq_ids, 4) || !aligned(selected, 4))
+        return KVC_ERR_ARG;
+    const kvc_status st = check_device(pool);
+    if (st != KVC_OK) return st;
+    SelectParams p{};
+    p.codes = static_cast<const int8_t *>(bounds) + bounds_layer_bytes(pool) * layer;
+    p.units = reinterpret_cast<const float *>(p.codes + static_cast<size_t>(pool->N) * pool->H_KV * 2 * pool->D);
+    p.q = static_cast<const uint16_t *>(q);
+    p.H_Q = num_q_heads;
+    p.H_KV = pool->H_KV;
+    p.g = num_q_heads / pool->H_KV;
+    p.bs = pool->bs;
+    p.N = pool->N;
+    p.bt = block_tables;
+    p.max_blocks = max_blocks;
+    p.B = B;
+    p.seqs = seq_ids;
+    p.positions = positions;
+    p.top_k = top_k;
+    p.sink = sink;
+    p.recent = recent;
+    p.lists = selected;
+    p.err = pool->err;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return pool->D == 64 ? launch_select<64>(p, n_rows, pool->num_sms, s) : launch_select<128>(p, n_rows, pool->num_sms, s);
+}

@@ -1,0 +1,19 @@
+// Sparse attention: e4m3 and int4 instances (d_h 128).  Weights enter the value product as f16.
+#include "kvc_sparse.cuh"
+
+namespace kvc {
+
+template <int KIND>
+static SparseKernel pick(int g)
+{
+    switch (n_tiles(g)) {
+    case 1: return sparse_instance<128, 1, KIND, false>();
+    case 2: return sparse_instance<128, 2, KIND, false>();
+    }
+    return sparse_instance<128, 4, KIND, false>();
+}
+
+SparseKernel select_sparse_fp8(int g) { return pick<KV_E4M3>(g); }
+SparseKernel select_sparse_int4(int g) { return pick<KV_INT4>(g); }
+
+}  // namespace kvc
