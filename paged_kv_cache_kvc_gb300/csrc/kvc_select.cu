@@ -8,8 +8,7 @@
 // the blocks chosen depend on the inputs alone, not on the grid, and equal scores go to the lower block.
 #include <algorithm>
 
-#include "kvc_cluster.cuh"
-#include "kvc_configured.cuh"
+#include "kvc_select.cuh"
 
 namespace kvc {
 
@@ -19,17 +18,6 @@ static uint64_t bounds_layer_bytes(const kvc_pool *pool)
     const uint64_t n = static_cast<uint64_t>(pool->N) * pool->H_KV * (2 * pool->D + 4);
     return (n + 255) / 256 * 256;
 }
-
-// The smallest e in [-100, 100] with x <= 127 * 2^e (100 if none), x >= 0 as float bits.
-__device__ __forceinline__ int unit_exponent(float x)
-{
-    const uint32_t u = __float_as_uint(x) & 0x7FFFFFFFu;
-    // x = (1 + f / 2^23) 2^(E - 127); it fits into 127 * 2^e = 1.984375 * 2^(e + 6) from e = E - 133 on, or one later
-    const int e = static_cast<int>(u >> 23) - 133 + ((u & 0x7FFFFFu) > 0x7E0000u ? 1 : 0);
-    return min(max(e, -100), 100);
-}
-
-__device__ __forceinline__ float exp2_int(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
 __device__ __forceinline__ uint32_t max2_bf16(uint32_t a, uint32_t b)
 {
@@ -212,32 +200,6 @@ __global__ void __launch_bounds__(kBoundsThreads) bounds_kernel(const BoundsPara
 }
 
 // ------------------------------------------------------------------ selection
-struct SelectParams {
-    const int8_t *codes;
-    const float *units;
-    const uint16_t *q;         // bf16 [rows][H_Q][D]
-    int32_t H_Q, H_KV, g, bs;
-    int64_t N;
-    const int32_t *bt;
-    int32_t max_blocks, B;
-    const int32_t *seqs, *positions;
-    int32_t top_k, sink, recent;
-    int32_t *lists;            // [rows][H_KV][top_k]
-    uint32_t *err;
-};
-
-constexpr int kSelThreads = 256;
-constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelMostBlocks = 262144;
-constexpr int kSelKeys = 32768;     // keys that a CTA holds
-
-// Scores as unsigned numbers of the same order; 0 and ~0 are no finite score's.
-__device__ __forceinline__ uint32_t score_key(float x)
-{
-    const uint32_t u = __float_as_uint(x);
-    return (u >> 31) ? ~u : (u | 0x80000000u);
-}
-
 // grid (C x rows, KV head), clusters of C CTAs along x.  CTA c of a cluster scores the c-th part of the row's blocks
 // into keys in shared memory; the k-th largest key is found digit by digit over the cluster's histograms, and each
 // CTA writes its part of the list in order.
@@ -503,28 +465,8 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
 
 static bool aligned(const void *ptr, size_t a) { return (reinterpret_cast<uintptr_t>(ptr) & (a - 1)) == 0; }
 
-// A launch that may start while the kernel before it drains, in clusters of `cluster` CTAs along x.
-template <typename P>
-static kvc_status launch(void (*fn)(P), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t stream, const P &p)
-{
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = cluster;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = cluster > 1 ? 2 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, p);
-    if (e != cudaSuccess) return cuda_status(e);
-    g_launches.fetch_add(1, std::memory_order_relaxed);
-    return KVC_OK;
-}
+// Rows per sequence, on average, from which on rows are scored together.
+constexpr int kTileRuns = 8;
 
 template <int D>
 static kvc_status launch_select(const SelectParams &p, int64_t rows, int sms, cudaStream_t stream)
@@ -627,5 +569,9 @@ extern "C" kvc_status kvc_select_blocks(kvc_pool *pool, int32_t layer, const voi
     p.lists = selected;
     p.err = pool->err;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (seq_ids && n_rows >= kTileRuns * static_cast<int64_t>(B)) {
+        const kvc_status tiled = select_tiles(p, pool->D, n_rows, pool->num_sms, s);
+        if (tiled != KVC_ERR_UNSUPPORTED) return tiled;
+    }
     return pool->D == 64 ? launch_select<64>(p, n_rows, pool->num_sms, s) : launch_select<128>(p, n_rows, pool->num_sms, s);
 }
