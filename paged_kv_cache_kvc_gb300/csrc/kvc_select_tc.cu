@@ -20,10 +20,12 @@
 
 namespace kvc {
 
-constexpr int kStThreads = 256;
+constexpr int kStThreads = 512;
+constexpr int kStWarps = kStThreads / 32;
 constexpr int kStTile = 128;       // blocks per MMA
 constexpr int kStCols = 128;       // query columns at most
 constexpr int kStRows = 32;        // rows at most
+constexpr int kStPick = 8;         // warps that finish rows
 
 template <int D>
 struct StCfg {
@@ -54,88 +56,19 @@ __device__ __forceinline__ uint2 s8x4_to_f16(uint32_t x)
     return r;
 }
 
-__device__ __forceinline__ float key_score(uint32_t k) { return __uint_as_float((k >> 31) ? (k & 0x7FFFFFFFu) : ~k); }
-
-// One warp: writes the list of a row from its keys k[0 .. n4) in shared memory (n4 a multiple of 128, unused ones 0).
-__device__ __forceinline__ void pick_row(const uint32_t *k, int n4, int32_t *list, int top_k, int lane)
-{
-    const uint4 *k4 = reinterpret_cast<const uint4 *>(k);
-    uint32_t valid = 0u, forced = 0u, lo = 0xFFFFFFFFu, hi = 0u;
-    for (int i = lane; i < n4 / 4; i += 32) {
-        const uint4 v = k4[i];
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const bool top = w[u] == 0xFFFFFFFFu;
-            valid += w[u] != 0u;
-            forced += top;
-            lo = min(lo, w[u] == 0u ? 0xFFFFFFFFu : w[u]);
-            hi = max(hi, top ? 0u : w[u]);
-        }
-    }
-    valid = __reduce_add_sync(kFull, valid);
-    forced = __reduce_add_sync(kFull, forced);
-    lo = __reduce_min_sync(kFull, lo);
-    hi = __reduce_max_sync(kFull, hi);
-    const uint32_t want_all = static_cast<uint32_t>(top_k);
-    uint32_t above = 0u, equal = 0u;   // listed: keys > above, and the first `equal` ones of those equal to it
-    if (valid > want_all) {
-        if (forced >= want_all) {      // only when the forced ones alone fill the list
-            above = 0xFFFFFFFEu;
-        } else {
-            // keys >= lo are more than wanted, keys > hi fewer; halve by score while that moves fast, then by key
-            above = hi;
-            uint32_t n_hi = forced;    // keys > hi
-            for (int it = 0; lo < hi; ++it) {
-                uint32_t mid = lo + ((hi - lo + 1u) >> 1);
-                if (it < 24) {
-                    const uint32_t m = score_key(0.5f * key_score(lo) + 0.5f * key_score(hi));
-                    mid = min(max(m, lo + 1u), hi);
-                }
-                uint32_t c = 0u;
-                for (int i = lane; i < n4 / 4; i += 32) {
-                    const uint4 v = k4[i];
-                    c += (v.x >= mid) + (v.y >= mid) + (v.z >= mid) + (v.w >= mid);
-                }
-                c = __reduce_add_sync(kFull, c);
-                if (c == want_all) {
-                    lo = hi = mid - 1u;
-                    n_hi = c;
-                } else if (c > want_all) {
-                    lo = mid;
-                } else {
-                    hi = mid - 1u;
-                    n_hi = c;
-                }
-            }
-            above = lo;
-            equal = want_all - n_hi;
-        }
-    }
-    const uint32_t below = (1u << lane) - 1u;
-    uint32_t g0 = 0u, e0 = 0u;
-    for (int i = 0; i < n4; i += 32) {
-        const uint32_t w = k[i + lane];
-        const bool gt = w > above, eq = w != 0u && w == above;
-        const uint32_t mg = __ballot_sync(kFull, gt), me = __ballot_sync(kFull, eq);
-        if ((mg | me) == 0u) continue;
-        const uint32_t ge = g0 + __popc(mg & below), ee = e0 + __popc(me & below);
-        if (gt || (eq && ee < equal)) list[ge + min(ee, equal)] = i + lane;
-        g0 += __popc(mg);
-        e0 += __popc(me);
-    }
-    for (int i = static_cast<int>(g0 + min(e0, equal)) + lane; i < top_k; i += 32) list[i] = -1;
-}
-
 // grid (C x row tiles, KV head), clusters of C CTAs along x; one CTA per SM.
-template <int D>
+// G: query heads per KV head where that divides 32 and is at most 8, else 0 (any).
+template <int D, int G>
 __global__ void __launch_bounds__(kStThreads, 1) select_tile_kernel(const SelectTileParams tp)
 {
     using C = StCfg<D>;
     const SelectParams &p = tp.s;
     extern __shared__ uint8_t st_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(st_raw) + 1023) & ~uintptr_t(1023));
-    uint32_t *keys = reinterpret_cast<uint32_t *>(smem + C::KEYS);   // [row][tile of this CTA][128]
+    Candidates *cand = reinterpret_cast<Candidates *>(smem + C::KEYS);                     // [kStPick]
+    int32_t *phys_s = reinterpret_cast<int32_t *>(smem + C::KEYS + kStPick * sizeof(Candidates));   // [tile of this CTA][128]
+    float *unit_s = reinterpret_cast<float *>(phys_s + tp.tiles * kStTile);                // [tile of this CTA][128]
+    uint32_t *keys = reinterpret_cast<uint32_t *>(unit_s + tp.tiles * kStTile);            // [row][tile of this CTA][128]
     __shared__ int32_t row_seq[kStRows], row_nb[kStRows];            // sequence (-1: no work), blocks of the row
     __shared__ uint64_t bar;
     __shared__ uint32_t tmem_base;
@@ -177,25 +110,54 @@ __global__ void __launch_bounds__(kStThreads, 1) select_tile_kernel(const Select
     const uint32_t tmem = tmem_base;
     const uint32_t a_base = smem_u32(smem), b_base = a_base + C::A;
 
+    // the first run's table entries, ahead of their use
+    int early = -1;
+    {
+        const int s = lane < tp.RT ? row_seq[lane] : -1;
+        const uint32_t live = __ballot_sync(kFull, s >= 0);
+        const int j = (rank + (tid / kStTile) * cs) * kStTile + tid % kStTile;
+        if (live) {
+            const int64_t at = static_cast<int64_t>(__shfl_sync(kFull, s, __ffs(live) - 1)) * p.max_blocks;
+            if (j < p.max_blocks) early = __ldg(p.bt + at + j);
+        }
+    }
+
     // ---- the rows' queries as whole numbers, positive parts then negative ones: a warp per row
-    for (int r = warp; r < tp.RT; r += kStThreads / 32) {
+    constexpr int KEEP = 2;   // chunks of a lane that stay in registers between the two passes
+    const int chunks = p.g * (D / 8);
+    auto source = [&](int r) {
+        return reinterpret_cast<const uint4 *>(p.q + ((r0 + r) * p.H_Q + static_cast<int64_t>(h) * p.g) * D);
+    };
+    auto fetch = [&](int r, uint4 (&x)[KEEP]) {
+#pragma unroll
+        for (int u = 0; u < KEEP; ++u) {
+            x[u] = make_uint4(0u, 0u, 0u, 0u);
+            if (r < tp.RT && row_seq[r] >= 0 && lane + 32 * u < chunks) x[u] = __ldg(source(r) + lane + 32 * u);
+        }
+    };
+    uint4 next[KEEP];
+    fetch(warp, next);
+    for (int r = warp; r < tp.RT; r += kStWarps) {
+        uint4 kept[KEEP];
+#pragma unroll
+        for (int u = 0; u < KEEP; ++u) kept[u] = next[u];
+        fetch(r + kStWarps, next);
         if (row_seq[r] == -2) {
             int32_t *list = p.lists + ((r0 + r) * p.H_KV + h) * p.top_k;
             for (int i = rank * 32 + lane; i < p.top_k; i += 32 * cs) list[i] = -1;
         }
         if (row_seq[r] < 0) continue;
-        const uint4 *src = reinterpret_cast<const uint4 *>(p.q + ((r0 + r) * p.H_Q + static_cast<int64_t>(h) * p.g) * D);
-        const int chunks = p.g * (D / 8);
         float m = 0.f;
-        for (int i = lane; i < chunks; i += 32) {
-            const uint4 x = __ldg(src + i);
+        auto largest = [&](const uint4 &x) {
             const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k) m = fmaxf(m, fmaxf(fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k]))));   // NaNs drop out
-        }
+        };
+#pragma unroll
+        for (int u = 0; u < KEEP; ++u) largest(kept[u]);
+        for (int i = lane + 32 * KEEP; i < chunks; i += 32) largest(__ldg(source(r) + i));
         const float inv = exp2_int(-unit_exponent(__uint_as_float(__reduce_max_sync(kFull, __float_as_uint(m)))));
-        for (int i = lane; i < chunks; i += 32) {
-            const uint4 x = __ldg(src + i);
+        auto place = [&](int i, const uint4 &x) {
             const uint32_t w[4] = {x.x, x.y, x.z, x.w};
             uint32_t pos[4], neg[4];
 #pragma unroll
@@ -210,7 +172,11 @@ __global__ void __launch_bounds__(kStThreads, 1) select_tile_kernel(const Select
             const uint32_t at = b_base + (ch >> 3) * C::BAND + sw128(n, ch & 7);
             sts128(at, make_uint4(pos[0], pos[1], pos[2], pos[3]));
             sts128(at + (D / 64) * C::BAND, make_uint4(neg[0], neg[1], neg[2], neg[3]));
-        }
+        };
+#pragma unroll
+        for (int u = 0; u < KEEP; ++u)
+            if (lane + 32 * u < chunks) place(lane + 32 * u, kept[u]);
+        for (int i = lane + 32 * KEEP; i < chunks; i += 32) place(i, __ldg(source(r) + i));
     }
     __syncthreads();
 
@@ -218,29 +184,43 @@ __global__ void __launch_bounds__(kStThreads, 1) select_tile_kernel(const Select
     const uint64_t desc_a = tc_smem_desc(a_base, 16, 1024, kSwizzle128B), desc_b = tc_smem_desc(b_base, 16, 1024, kSwizzle128B);
     const int chunk = tid % C::CPR, rec0 = tid / C::CPR;
     uint32_t phase = 0u;
+    bool begun = false;
 
+    const int lane_seq = lane < tp.RT ? row_seq[lane] : -3, lane_nb = lane < tp.RT ? row_nb[lane] : 0;   // RT <= 32
     for (int first = 0; first < tp.RT;) {   // runs of rows of one sequence
-        const int seq = row_seq[first];
-        int end = first + 1;
-        while (end < tp.RT && row_seq[end] == seq) ++end;
+        const int seq = __shfl_sync(kFull, lane_seq, first);
+        const uint32_t others = __ballot_sync(kFull, lane_seq != seq) & (0xFFFFFFFFu << first);
+        const int end = others ? __ffs(others) - 1 : 32;
         if (seq < 0) {
             first = end;
             continue;
         }
-        int most = 0;
-        for (int r = first; r < end; ++r) most = max(most, row_nb[r]);
+        const bool mine_row = lane >= first && lane < end;
+        const int most = __reduce_max_sync(kFull, mine_row ? lane_nb : 0), least = __reduce_min_sync(kFull, mine_row ? lane_nb : 0x7FFFFFFF);
         const int32_t *bt = p.bt + static_cast<int64_t>(seq) * p.max_blocks;
         const int n_tiles = (most + kStTile - 1) / kStTile;
         const int mine = n_tiles > rank ? (n_tiles - rank + cs - 1) / cs : 0;
 
-        // this thread's 16 bytes of U records of a tile, and the table entry and unit of the epilogue's block
+        // the blocks and units of this CTA's tiles
+        for (int i = tid; i < mine * kStTile; i += kStThreads) {
+            const int j = (rank + (i / kStTile) * cs) * kStTile + i % kStTile;
+            int phys = j >= most ? -1 : (begun || i != tid ? __ldg(bt + j) : early);
+            if (j < most && (phys < 0 || static_cast<int64_t>(phys) >= p.N)) {
+                if (h == 0) atomicOr(p.err, KVC_EBIT_BAD_BLOCK);
+                phys = -1;
+            }
+            phys_s[i] = phys;
+            unit_s[i] = phys < 0 ? 0.f : __ldg(p.units + static_cast<int64_t>(phys) * p.H_KV + h);
+        }
+        begun = true;
+        __syncthreads();
+
+        // this thread's 16 bytes of U records of a tile
         uint4 raw[C::U];
         auto load = [&](int t) {
 #pragma unroll
             for (int u = 0; u < C::U; ++u) {
-                const int j = (rank + t * cs) * kStTile + u * C::STEP + rec0;
-                int phys = j < most ? __ldg(bt + j) : -1;
-                if (phys >= p.N) phys = -1;
+                const int phys = phys_s[t * kStTile + u * C::STEP + rec0];
                 raw[u] = make_uint4(0u, 0u, 0u, 0u);
                 if (phys >= 0)
                     raw[u] = __ldg(reinterpret_cast<const uint4 *>(p.codes + (static_cast<int64_t>(phys) * p.H_KV + h) * (2 * D)) + chunk);
@@ -279,13 +259,6 @@ __global__ void __launch_bounds__(kStThreads, 1) select_tile_kernel(const Select
         }
         for (int t = 0; t < mine; ++t) {
             if (t + 1 < mine) load(t + 1);
-            const int j = (rank + t * cs) * kStTile + 32 * (warp & 3) + lane;   // the epilogue's block
-            int phys = j < most ? __ldg(bt + j) : -1;
-            if (j < most && (phys < 0 || static_cast<int64_t>(phys) >= p.N)) {
-                if (h == 0) atomicOr(p.err, KVC_EBIT_BAD_BLOCK);
-                phys = -1;
-            }
-            const float unit = phys < 0 ? 0.f : __ldg(p.units + static_cast<int64_t>(phys) * p.H_KV + h);
             if (!mbar_wait_bounded(smem_u32(&bar), phase) && lane == 0) atomicOr(p.err, KVC_EBIT_TIMEOUT);
             phase ^= 1u;
             tc_fence_after();
@@ -293,29 +266,55 @@ __global__ void __launch_bounds__(kStThreads, 1) select_tile_kernel(const Select
                 widen();
                 multiply(t + 1);
             }
-            // warps 0 .. 3 take the first half of the run's rows, 4 .. 7 the second
-            const int half = (end - first + 1) >> 1;
-            const int ra = first + (warp >> 2) * half, rb = min(end, ra + half);
+            // a lane holds a block; warps w, w + 4, ... of its quarter take a part of the run's rows each
+            const int place = t * kStTile + 32 * (warp & 3) + lane, j = (rank + t * cs) * kStTile + 32 * (warp & 3) + lane;
+            const int phys = phys_s[place];
+            const float unit = unit_s[place];
+            // tiles between the forced blocks of every row look at no row's length
+            const bool plain = (rank + t * cs) * kStTile >= p.sink && (rank + t * cs + 1) * kStTile <= least - p.recent;
+            auto keep = [&](int r, float best) {
+                uint32_t key = score_key(best * unit);
+                if (!plain) {
+                    const int nb = row_nb[r];
+                    if (j < p.sink || j >= nb - p.recent) key = 0xFFFFFFFFu;
+                    if (j >= nb) key = 0u;
+                }
+                keys[r * stride + place] = phys < 0 ? 0u : key;
+            };
             const uint32_t d = tmem + (t & 1) * kStCols + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
-            float best = -INFINITY;
-            int r = ra, left = p.g;
-            for (int c0 = (ra * p.g) & ~31; c0 < rb * p.g; c0 += 32) {
-                uint32_t v[32];
-                tmem_ld32(d + c0, v);
-                tmem_ld_wait(v);
+            if constexpr (G > 0) {   // 32 columns are whole rows
+                constexpr int RPC = 32 / G;
+                for (int r = (first / RPC + (warp >> 2)) * RPC; r < end; r += (kStWarps / 4) * RPC) {
+                    uint32_t v[32];
+                    tmem_ld32(d + r * G, v);
+                    tmem_ld_wait(v);
 #pragma unroll
-                for (int x = 0; x < 32; ++x) {
-                    if (c0 + x < ra * p.g || r >= rb) continue;   // warp-uniform
-                    best = fmaxf(best, __uint_as_float(v[x]));
-                    if (--left == 0) {
-                        const int nb = row_nb[r];
-                        uint32_t key = score_key(best * unit);
-                        if (j < p.sink || j >= nb - p.recent) key = 0xFFFFFFFFu;
-                        if (phys < 0 || j >= nb) key = 0u;
-                        keys[r * stride + t * kStTile + 32 * (warp & 3) + lane] = key;
-                        best = -INFINITY;
-                        left = p.g;
-                        ++r;
+                    for (int x = 0; x < RPC; ++x) {
+                        float best = __uint_as_float(v[x * G]);
+#pragma unroll
+                        for (int y = 1; y < G; ++y) best = fmaxf(best, __uint_as_float(v[x * G + y]));
+                        if (r + x >= first && r + x < end) keep(r + x, best);
+                    }
+                }
+            } else {
+                const int part = (end - first + kStWarps / 4 - 1) / (kStWarps / 4);
+                const int ra = min(end, first + (warp >> 2) * part), rb = min(end, ra + part);
+                float best = -INFINITY;
+                int r = ra, left = p.g;
+                for (int c0 = (ra * p.g) & ~31; c0 < rb * p.g; c0 += 32) {
+                    uint32_t v[32];
+                    tmem_ld32(d + c0, v);
+                    tmem_ld_wait(v);
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) {
+                        if (c0 + x < ra * p.g || r >= rb) continue;   // warp-uniform
+                        best = fmaxf(best, __uint_as_float(v[x]));
+                        if (--left == 0) {
+                            keep(r, best);
+                            best = -INFINITY;
+                            left = p.g;
+                            ++r;
+                        }
                     }
                 }
             }
@@ -326,18 +325,25 @@ __global__ void __launch_bounds__(kStThreads, 1) select_tile_kernel(const Select
 
         // ---- a warp per row: gather its keys into A's place, choose, write
         const int n4 = n_tiles * kStTile;
-        const int lanes_of = min(kStThreads / 32, C::A / 4 / n4);   // rows at a time
+        const int lanes_of = min(kStPick, C::A / 4 / n4);   // rows at a time
         if (warp < lanes_of) {
             uint32_t *mine_k = reinterpret_cast<uint32_t *>(smem) + warp * n4;
             for (int r = first + rank + cs * warp; r < end; r += cs * lanes_of) {
-                for (int i = lane; i < n4 / 4; i += 32) {
-                    const int t = i / (kStTile / 4);
-                    const uint32_t a = smem_u32(keys + r * stride + (t / cs) * kStTile + 4 * (i % (kStTile / 4)));
-                    const float4 v = cluster_ld4(cluster_addr(a, t % cs));
-                    reinterpret_cast<float4 *>(mine_k)[i] = v;
+                constexpr int UG = 8;
+                for (int i0 = lane; i0 < n4 / 4; i0 += 32 * UG) {
+                    float4 v[UG];
+#pragma unroll
+                    for (int u = 0; u < UG; ++u) {
+                        const int i = min(i0 + 32 * u, n4 / 4 - 1), t = i / (kStTile / 4);
+                        const uint32_t a = smem_u32(keys + r * stride + (t / cs) * kStTile + 4 * (i % (kStTile / 4)));
+                        v[u] = cluster_ld4(cluster_addr(a, t % cs));
+                    }
+#pragma unroll
+                    for (int u = 0; u < UG; ++u)
+                        if (i0 + 32 * u < n4 / 4) reinterpret_cast<float4 *>(mine_k)[i0 + 32 * u] = v[u];
                 }
                 __syncwarp();
-                pick_row(mine_k, n4, p.lists + ((r0 + r) * p.H_KV + h) * p.top_k, p.top_k, lane);
+                pick_row(mine_k, n4, cand[warp], p.lists + ((r0 + r) * p.H_KV + h) * p.top_k, p.top_k, lane);
                 __syncwarp();
             }
         }
@@ -353,31 +359,47 @@ __global__ void __launch_bounds__(kStThreads, 1) select_tile_kernel(const Select
     }
 }
 
+// Largest shared memory that the kernel is launched with, beside its static variables.
+constexpr int kStRoom = 226 * 1024;
+
+template <int D, int G>
+static kvc_status launch_tile_kernel(const SelectTileParams &tp, dim3 grid, size_t smem, int c, cudaStream_t stream)
+{
+    struct Tag {};
+    const DecodeKernel k = configured<Tag>(reinterpret_cast<const void *>(&select_tile_kernel<D, G>), kStRoom, kStThreads, false);
+    if (k.ctas_per_sm <= 0) return KVC_ERR_CUDA;
+    return launch(&select_tile_kernel<D, G>, grid, kStThreads, smem, c, stream, tp);
+}
+
 template <int D>
 static kvc_status launch_tiles(SelectTileParams &tp, int sms, cudaStream_t stream)
 {
     using C = StCfg<D>;
     const SelectParams &p = tp.s;
-    constexpr int kRoom = 227 * 1024 - 1024 - 1024;   // dynamic shared memory beside the static
-    constexpr int kKeyTiles = (kRoom - 1024 - C::KEYS) / (4 * kStTile);   // row tiles of keys
-    const int blocks = (p.max_blocks + kStTile - 1) / kStTile;     // tiles of the widest row
+    constexpr int kFixed = 1024 + C::KEYS + kStPick * static_cast<int>(sizeof(Candidates));
+    constexpr int kTiles = (kStRoom - kFixed) / (4 * kStTile);      // runs of 128 words that there is room for
+    const int blocks = (p.max_blocks + kStTile - 1) / kStTile;      // tiles of the widest row
     tp.RT = std::min(kStRows, kStCols / p.g);
     int c = 1;
-    auto per_cta = [&] { return (blocks + c - 1) / c; };
-    while (c < 8 && per_cta() * tp.RT > kKeyTiles) c *= 2;
-    while (tp.RT > 4 && per_cta() * tp.RT > kKeyTiles) tp.RT /= 2;
-    if (per_cta() * tp.RT > kKeyTiles || blocks * kStTile > C::A / 4) return KVC_ERR_UNSUPPORTED;
+    auto room = [&] { return (blocks + c - 1) / c * (tp.RT + 2) <= kTiles; };   // keys, blocks and units
+    while (c < 8 && !room()) c *= 2;
+    while (tp.RT > 4 && !room()) tp.RT /= 2;
+    if (!room() || blocks * kStTile > C::A / 4 || blocks * kStTile > kPickMost) return KVC_ERR_UNSUPPORTED;
     const int64_t row_tiles = (tp.rows + tp.RT - 1) / tp.RT;
     while (c < 8 && c < blocks && row_tiles * p.H_KV * c < sms) c *= 2;
-    tp.tiles = per_cta();
+    tp.tiles = (blocks + c - 1) / c;
     if (row_tiles * c > 0x7FFFFFFF) return KVC_ERR_UNSUPPORTED;
-    struct Tag {};
-    const DecodeKernel k = configured<Tag>(reinterpret_cast<const void *>(&select_tile_kernel<D>), kRoom, kStThreads, false);
-    if (k.ctas_per_sm <= 0) return KVC_ERR_CUDA;
     // At least 80 KB: no more than two CTAs to an SM, whose tensor memory holds two allocations.  (A CTA that waited for
     // tensor memory while its cluster waits for it could wait for a CTA of another cluster that does the same.)
-    const size_t smem = std::max<size_t>(80 * 1024, 1024 + C::KEYS + static_cast<size_t>(4) * kStTile * tp.tiles * tp.RT);
-    return launch(&select_tile_kernel<D>, dim3(static_cast<unsigned>(row_tiles * c), p.H_KV), kStThreads, smem, c, stream, tp);
+    const size_t smem = std::max<size_t>(80 * 1024, kFixed + static_cast<size_t>(4) * kStTile * tp.tiles * (tp.RT + 2));
+    const dim3 grid(static_cast<unsigned>(row_tiles * c), p.H_KV);
+    switch (p.g) {
+    case 1: return launch_tile_kernel<D, 1>(tp, grid, smem, c, stream);
+    case 2: return launch_tile_kernel<D, 2>(tp, grid, smem, c, stream);
+    case 4: return launch_tile_kernel<D, 4>(tp, grid, smem, c, stream);
+    case 8: return launch_tile_kernel<D, 8>(tp, grid, smem, c, stream);
+    }
+    return launch_tile_kernel<D, 0>(tp, grid, smem, c, stream);
 }
 
 kvc_status select_tiles(const SelectParams &p, int D, int64_t rows, int sms, cudaStream_t stream)
