@@ -59,21 +59,24 @@ struct BoundsParams {
 
 constexpr int kBoundsThreads = 256;
 
-// grid (row chunk, KV head).  A CTA finds the chunk's last rows of blocks, then its warps take a block each: LPR lanes
-// per key row, 16 bytes a lane, 32 / LPR rows at a time; channels' extremes in packed halves, then across the rows'
-// lanes.  Bound by HBM: the keys are read once.
+// grid (row chunk).  A CTA finds the chunk's last rows of blocks, then its warps take a (block, head) each, the next
+// one's keys on their way meanwhile: LPR lanes per key row, 16 bytes a lane, 32 / LPR rows at a time; the channels'
+// extremes in packed halves.  Across the row's lanes each halving step passes on half the channels, so that every lane
+// ends with 2 or 4 channels of its own to round and store.
 template <int D, int KIND>
-__global__ void __launch_bounds__(kBoundsThreads) bounds_kernel(const BoundsParams p)
+__global__ void __launch_bounds__(kBoundsThreads, KIND == KV_BF16 && D == 128 ? 3 : 4) bounds_kernel(const BoundsParams p)
 {
     constexpr int BITS = KIND == KV_BF16 ? 16 : (KIND == KV_E4M3 ? 8 : 4);
     constexpr int ROW = D * BITS / 8;             // bytes of a key row
     constexpr int LPR = ROW / 16;                 // lanes per row
     constexpr int RPS = 32 / LPR;                 // rows per step
-    constexpr int E = D / LPR;                    // channels per lane
+    constexpr int E = D / LPR;                    // channels of a lane's 16 bytes
     constexpr int P = E / 2;                      // packed pairs
-    __shared__ int32_t ends[kBoundsThreads];      // slots of the last rows of this chunk's blocks
+    constexpr int KEEP = P / RPS;                 // pairs that a lane finishes
+    constexpr int U = 16 / RPS;                   // steps at a time: 16 rows
+    __shared__ int2 ends[kBoundsThreads];         // (block, place) of the last rows of this chunk's blocks
     __shared__ int32_t n_ends;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, h = blockIdx.y;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) n_ends = 0;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     __syncthreads();
@@ -81,34 +84,55 @@ __global__ void __launch_bounds__(kBoundsThreads) bounds_kernel(const BoundsPara
     if (tid < p.rows_per_cta && r < p.rows) {
         const int32_t slot = __ldg(p.slots + r);
         if (slot < -1 || (slot >= 0 && slot / p.bs >= p.N)) {
-            if (h == 0) atomicOr(p.err, KVC_EBIT_BAD_BLOCK);
+            atomicOr(p.err, KVC_EBIT_BAD_BLOCK);
         } else if (slot >= 0 && ((slot + 1) % p.bs == 0 || r + 1 == p.rows || __ldg(p.slots + r + 1) != slot + 1)) {
-            ends[atomicAdd(&n_ends, 1)] = slot;
+            ends[atomicAdd(&n_ends, 1)] = make_int2(slot / p.bs, slot % p.bs);
         }
     }
     __syncthreads();
     const int c = lane % LPR, sub = lane / LPR;
-    for (int i = warp; i < n_ends; i += kBoundsThreads / 32) {
-        const int32_t slot = ends[i], blk = slot / p.bs;
-        const int n = slot - blk * p.bs + 1;
-        const uint8_t *keys = p.base + ((static_cast<int64_t>(p.layer) * p.N + blk) * p.H_KV + h) * (2ll * p.bs * ROW);
+    constexpr int kBoundsWarps = kBoundsThreads / 32;
+    const int count = n_ends;
+    const uint8_t *layer = p.base + static_cast<int64_t>(p.layer) * p.N * p.H_KV * (2ll * p.bs * ROW) + 16 * c;
+
+    // rows t0 + sub, t0 + sub + RPS, ... of the keys of (end, head); past the last row: the last one again
+    auto fetch = [&](int i, int h, int t0, uint4 (&v)[U]) {
+        const int2 e = ends[i];
+        const uint8_t *keys = layer + (static_cast<int64_t>(e.x) * p.H_KV + h) * (2 * p.bs * ROW);
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[u] = *reinterpret_cast<const uint4 *>(keys + min(t0 + sub + u * RPS, e.y) * ROW);
+    };
+    auto advance = [&](int &i, int &h) {
+        h += kBoundsWarps;
+        while (h >= p.H_KV) {
+            h -= p.H_KV;
+            ++i;
+        }
+    };
+    int i = 0, h = warp - kBoundsWarps;
+    advance(i, h);
+    uint4 v[U];
+    if (i < count) fetch(i, h, 0, v);
+    while (i < count) {
+        const int32_t blk = ends[i].x;
+        const int n = ends[i].y + 1;
+        int i2 = i, h2 = h;
+        advance(i2, h2);
         uint32_t hi[P], lo[P];
 #pragma unroll
         for (int x = 0; x < P; ++x) {   // -inf, +inf: no key yet
             hi[x] = KIND == KV_BF16 ? 0xFF80FF80u : 0xFC00FC00u;
             lo[x] = KIND == KV_BF16 ? 0x7F807F80u : 0x7C007C00u;
         }
-        constexpr int U = RPS >= 8 ? 2 : (RPS >= 4 ? 4 : 8);
-        for (int t0 = sub; t0 < n; t0 += U * RPS) {
-            uint4 v[U];
+        for (int t0 = 0; t0 < n; t0 += 16) {
+            uint4 cur[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {   // past the last row: the last one of this lane's again
-                const int t = min(t0 + u * RPS, n - 1);
-                v[u] = *reinterpret_cast<const uint4 *>(keys + static_cast<int64_t>(t) * ROW + 16 * c);
-            }
+            for (int u = 0; u < U; ++u) cur[u] = v[u];
+            if (t0 + 16 < n) fetch(i, h, t0 + 16, v);
+            else if (i2 < count) fetch(i2, h2, 0, v);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+                const uint32_t w[4] = {cur[u].x, cur[u].y, cur[u].z, cur[u].w};
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     if constexpr (KIND == KV_BF16) {
@@ -132,70 +156,73 @@ __global__ void __launch_bounds__(kBoundsThreads) bounds_kernel(const BoundsPara
                 }
             }
         }
+        // across the lanes of a channel: keep half the pairs, pass on the other half
+        int x0 = 0;
 #pragma unroll
-        for (int o = LPR; o < 32; o <<= 1)
+        for (int o = 16, m = P; o >= LPR; o >>= 1) {
+            m >>= 1;
+            const bool up = (lane & o) != 0;
+            x0 += up ? m : 0;
 #pragma unroll
-            for (int x = 0; x < P; ++x) {
-                const uint32_t a = __shfl_xor_sync(kFull, hi[x], o), b = __shfl_xor_sync(kFull, lo[x], o);
-                hi[x] = KIND == KV_BF16 ? max2_bf16(hi[x], a) : max2_f16(hi[x], a);
-                lo[x] = KIND == KV_BF16 ? min2_bf16(lo[x], b) : min2_f16(lo[x], b);
+            for (int x = 0; x < P / 2; ++x) {
+                if (x >= m) break;
+                const uint32_t a = __shfl_xor_sync(kFull, up ? hi[x] : hi[x + m], o);
+                const uint32_t b = __shfl_xor_sync(kFull, up ? lo[x] : lo[x + m], o);
+                const uint32_t ka = up ? hi[x + m] : hi[x], kb = up ? lo[x + m] : lo[x];
+                hi[x] = KIND == KV_BF16 ? max2_bf16(ka, a) : max2_f16(ka, a);
+                lo[x] = KIND == KV_BF16 ? min2_bf16(kb, b) : min2_f16(kb, b);
             }
-        // this lane finishes its channels' upper bounds (sub 0) or lower ones (sub 1); the rest only help with e
-        float y[E], top = 0.f;
+        }
+        // pair x of the lane: channels first + 2 x and the next one; int4: first + x and first + x + 4
+        const int first = E * c + (KIND == KV_INT4 ? 8 * (x0 >> 2) + (x0 & 3) : 2 * x0);
+        float y[2][KEEP][2];
+        uint32_t top = 0u;   // magnitudes as bits: a NaN's are above infinity's
 #pragma unroll
-        for (int which = 0; which < 2; ++which) {
+        for (int which = 0; which < 2; ++which)
 #pragma unroll
-            for (int x = 0; x < P; ++x) {
+            for (int x = 0; x < KEEP; ++x) {
                 const uint32_t w = which ? lo[x] : hi[x];
                 float2 f;
-                if constexpr (KIND == KV_BF16) {
-                    f = make_float2(bf16_lo(w), bf16_hi(w));
-                } else {
-                    f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
-                }
-                const int c0 = KIND == KV_INT4 ? 8 * (x >> 2) + (x & 3) : 2 * x, c1 = KIND == KV_INT4 ? c0 + 4 : c0 + 1;
+                if constexpr (KIND == KV_BF16) f = make_float2(bf16_lo(w), bf16_hi(w));
+                else f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
                 if constexpr (KIND != KV_BF16) {
-                    const float *sc = p.s_k + static_cast<int64_t>(h) * D + E * c;
-                    f.x *= __ldg(sc + c0);
-                    f.y *= __ldg(sc + c1);
+                    const float *sc = p.s_k + static_cast<int64_t>(h) * D + first + (KIND == KV_INT4 ? x : 2 * x);
+                    f.x *= __ldg(sc);
+                    f.y *= __ldg(sc + (KIND == KV_INT4 ? 4 : 1));
                 }
-                const float none = which ? -INFINITY : INFINITY;   // what a NaN counts as
-                f.x = isnan(f.x) ? none : f.x;
-                f.y = isnan(f.y) ? none : f.y;
-                top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
-                if (which == (sub & 1)) {
-                    y[c0] = f.x;
-                    y[c1] = f.y;
-                }
+                y[which][x][0] = f.x;
+                y[which][x][1] = f.y;
+                top = max(top, max(__float_as_uint(f.x) & 0x7FFFFFFFu, __float_as_uint(f.y) & 0x7FFFFFFFu));
             }
-        }
-#pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-        const int e = unit_exponent(top);
+        const int e = unit_exponent(__uint_as_float(__reduce_max_sync(kFull, top)));
         const float inv = exp2_int(-e);
-        if (sub < 2) {
-            uint32_t out[E / 4];
+        const int64_t rec = static_cast<int64_t>(blk) * p.H_KV + h;
 #pragma unroll
-            for (int x = 0; x < E / 4; ++x) {
-                out[x] = 0u;
+        for (int which = 0; which < 2; ++which) {
+            uint32_t code[KEEP][2];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float z = y[4 * x + k] * inv;
-                    const float w = fminf(fmaxf(sub ? floorf(z) : ceilf(z), -127.f), 127.f);
-                    out[x] |= (static_cast<uint32_t>(static_cast<int>(w)) & 255u) << (8 * k);
+            for (int x = 0; x < KEEP; ++x)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float z = y[which][x][k] * inv;   // a NaN becomes the first bound that it is compared with
+                    code[x][k] = static_cast<uint32_t>(which ? __float2int_rd(fminf(fmaxf(z, -127.f), 127.f))
+                                                             : __float2int_ru(fmaxf(fminf(z, 127.f), -127.f))) & 255u;
                 }
-            }
-            const int64_t rec = static_cast<int64_t>(blk) * p.H_KV + h;
-            int8_t *dst = p.codes + rec * (2 * D) + sub * D + E * c;
-            if constexpr (E == 8) {
-                *reinterpret_cast<uint2 *>(dst) = make_uint2(out[0], out[1]);
+            int8_t *dst = p.codes + rec * (2 * D) + which * D + first;
+            if constexpr (KIND == KV_INT4) {
+                static_assert(KIND != KV_INT4 || KEEP == 2, "two neighbours, twice");
+                *reinterpret_cast<uint16_t *>(dst) = static_cast<uint16_t>(code[0][0] | (code[KEEP - 1][0] << 8));
+                *reinterpret_cast<uint16_t *>(dst + 4) = static_cast<uint16_t>(code[0][1] | (code[KEEP - 1][1] << 8));
+            } else if constexpr (KEEP == 2) {
+                *reinterpret_cast<uint32_t *>(dst) = code[0][0] | (code[0][1] << 8) | (code[1][0] << 16) | (code[1][1] << 24);
             } else {
-#pragma unroll
-                for (int x = 0; x < E / 16; ++x)
-                    reinterpret_cast<uint4 *>(dst)[x] = make_uint4(out[4 * x], out[4 * x + 1], out[4 * x + 2], out[4 * x + 3]);
+                static_assert(KIND == KV_INT4 || KEEP <= 2, "whole words");
+                *reinterpret_cast<uint16_t *>(dst) = static_cast<uint16_t>(code[0][0] | (code[0][1] << 8));
             }
-            if (lane == 0) p.units[rec] = exp2_int(e);
         }
+        if (lane == 0) p.units[rec] = exp2_int(e);
+        i = i2;
+        h = h2;
     }
 }
 
@@ -486,10 +513,11 @@ static kvc_status launch_select(const SelectParams &p, int64_t rows, int sms, cu
 template <int D, int KIND>
 static kvc_status launch_bounds(const kvc_pool *pool, BoundsParams &p, cudaStream_t stream)
 {
-    // Few rows are a decoding batch's, nearly each the last one of its block: small chunks, so that every SM gets some.
-    p.rows_per_cta = p.rows * p.H_KV >= 64ll * 1024 ? kBoundsThreads : 16;
+    // Few rows are a decoding batch's, nearly each the last one of its block: as many CTAs as rows, until there are four
+    // for every SM.
+    p.rows_per_cta = static_cast<int32_t>(std::min<int64_t>(std::max<int64_t>((p.rows + 4 * pool->num_sms - 1) / (4 * pool->num_sms), 1), kBoundsThreads));
     const int64_t chunks = (p.rows + p.rows_per_cta - 1) / p.rows_per_cta;
-    return launch(&bounds_kernel<D, KIND>, dim3(static_cast<unsigned>(chunks), pool->H_KV), kBoundsThreads, 0, 1, stream, p);
+    return launch(&bounds_kernel<D, KIND>, dim3(static_cast<unsigned>(chunks)), kBoundsThreads, 0, 1, stream, p);
 }
 
 }  // namespace kvc
