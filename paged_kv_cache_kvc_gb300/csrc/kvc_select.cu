@@ -238,7 +238,9 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
     constexpr int U = 4;                 // steps at a time
     extern __shared__ uint32_t keys[];
     __shared__ __align__(16) uint32_t qw[32][2][D / 4];   // the group's queries: positive parts, negative parts, int8
-    __shared__ uint32_t hist[2][256], sum[256];
+    __shared__ __align__(16) uint32_t hist[2][256], sum[256];
+    __shared__ Candidates cand;
+    __shared__ uint32_t n_cand, limit;
     __shared__ uint32_t top_bits, pick_bin, pick_above, n_valid, n_gt, n_eq;
     __shared__ uint32_t warp_gt[kSelWarps], warp_eq[kSelWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -264,7 +266,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
     // ---- the group's queries as integers
     if (tid == 0) {
         top_bits = 0u;
-        n_valid = n_gt = n_eq = 0u;
+        n_valid = n_gt = n_eq = n_cand = limit = 0u;
     }
     __syncthreads();
     if (!all) {
@@ -371,6 +373,104 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
         }
     }
     __syncthreads();
+
+    // ---- short lists: the largest keys of 256 groups over the cluster; at least top_k keys reach what top_k of those
+    // reach, and not many more.  The first CTA ranks those few by counting.
+    if (p.top_k <= 128 && nb <= kPickMost) {
+        uint32_t m = 0u;
+        for (int i = tid; i < n; i += kSelThreads) m = max(m, keys[i]);
+        for (int o = 1; o < cs; o <<= 1) m = max(m, __shfl_xor_sync(kFull, m, o));   // cs a power of two: 256 / cs groups
+        if (tid % cs == 0) hist[0][tid / cs] = m;
+        if (cs > 1) cluster_sync();
+        else __syncthreads();
+        const int groups = kSelThreads / cs;
+        m = cs > 1 ? cluster_ld(cluster_addr(smem_u32(&hist[0][tid % groups]), tid / groups)) : hist[0][tid];
+        sum[tid] = m;
+        __syncthreads();
+        {
+            const uint4 *all4 = reinterpret_cast<const uint4 *>(sum);
+            int reached = 0;
+#pragma unroll 8
+            for (int i = 0; i < kSelThreads / 4; ++i) {
+                const uint4 v = all4[i];
+                reached += (v.x >= m) + (v.y >= m) + (v.z >= m) + (v.w >= m);
+            }
+            if (reached >= p.top_k) atomicMax(&limit, m);
+        }
+        __syncthreads();
+        const uint32_t lim = max(limit, 1u);
+        int mine = 0;
+        for (int i = tid; i < n; i += kSelThreads) mine += keys[i] >= lim;
+        int at = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(kFull, at, o);
+            if (lane >= o) at += y;
+        }
+        int base = 0;
+        if (lane == 31) base = static_cast<int>(atomicAdd(&n_cand, static_cast<uint32_t>(at)));
+        at += __shfl_sync(kFull, base, 31) - mine;
+        if (mine > 0)
+            for (int i = tid; i < n; i += kSelThreads) {
+                const uint32_t k = keys[i];
+                if (k >= lim) {
+                    if (at < kCand) {
+                        cand.key[at] = k;
+                        cand.block[at] = j0 + i;
+                    }
+                    ++at;
+                }
+            }
+        if (cs > 1) cluster_sync();
+        else __syncthreads();
+        uint32_t total = 0u;
+        for (int r = 0; r < cs; ++r) total += cluster_ld(cluster_addr(smem_u32(&n_cand), r));
+        if (total <= kSelThreads) {
+            if (rank == 0) {
+                const int c = static_cast<int>(total);
+                int from = static_cast<int>(n_cand);
+                for (int r = 1; r < cs; ++r) {
+                    const int more = static_cast<int>(cluster_ld(cluster_addr(smem_u32(&n_cand), r)));
+                    if (tid < more) {
+                        cand.key[from + tid] = cluster_ld(cluster_addr(smem_u32(&cand.key[tid]), r));
+                        cand.block[from + tid] = static_cast<int32_t>(cluster_ld(cluster_addr(smem_u32(&cand.block[tid]), r)));
+                    }
+                    from += more;
+                }
+                if (tid < 4) cand.key[c + tid] = 0u;   // whole fours (kCand is more than kSelThreads + 4)
+                __syncthreads();
+                const uint32_t k = tid < c ? cand.key[tid] : 0xFFFFFFFFu;
+                const int blk = tid < c ? cand.block[tid] : -1;
+                const uint4 *k4 = reinterpret_cast<const uint4 *>(cand.key);
+                int larger = 0;
+#pragma unroll 8
+                for (int i = 0; i < (c + 3) / 4; ++i) {
+                    const uint4 v = k4[i];
+                    larger += (v.x > k) + (v.y > k) + (v.z > k) + (v.w > k);
+                }
+                bool pick = tid < c && larger < p.top_k;
+                if (__syncthreads_count(pick) > p.top_k) {   // equal keys at the border: the lower blocks
+                    if (pick)
+                        for (int i = 0; i < c; ++i) larger += cand.key[i] == k && cand.block[i] < blk;
+                    pick = pick && larger < p.top_k;
+                }
+                sum[tid] = pick ? static_cast<uint32_t>(blk) : 0x7FFFFFFFu;
+                const int picks = __syncthreads_count(pick);
+                const int4 *b4 = reinterpret_cast<const int4 *>(sum);
+                int place = 0;
+#pragma unroll 8
+                for (int i = 0; i < (c + 3) / 4; ++i) {
+                    const int4 v = b4[i];
+                    place += (v.x < blk) + (v.y < blk) + (v.z < blk) + (v.w < blk);
+                }
+                if (pick) list[place] = blk;
+                for (int i = picks + tid; i < p.top_k; i += kSelThreads) list[i] = -1;
+            }
+            if (cs > 1) cluster_sync();   // a CTA's shared memory stays until the first has read it
+            return;
+        }
+        __syncthreads();   // many equal keys: all of them are counted below
+    }
 
     // ---- the k-th largest key
     {

@@ -108,7 +108,7 @@ __device__ __forceinline__ Cut find_cut(uint32_t want, uint32_t forced, uint32_t
 
 // Keys that a row's list is chosen from, in any order: those at or above a limit that at least top_k keys reach.
 constexpr int kCand = 384;
-struct Candidates {
+struct alignas(16) Candidates {
     uint32_t key[kCand];
     int32_t block[kCand];
 };
@@ -178,6 +178,68 @@ __device__ __forceinline__ void list_candidates(Candidates &s, int n, int blocks
     at -= mine;
     for (int i = 0; i < per && lane * per + i < words; ++i)
         for (uint32_t w = bits[lane * per + i]; w; w &= w - 1u) list[at++] = (lane * per + i) * 32 + __ffs(w) - 1;
+    for (int i = total + lane; i < top_k; i += 32) list[i] = -1;
+}
+
+// One warp: the same for n <= 128 candidates by counting, for each, the larger ones and then the listed ones in lower
+// blocks: more additions than a search, but no chain of them.
+__device__ __forceinline__ void list_few(Candidates &s, int n, int blocks, int32_t *list, int top_k, int lane)
+{
+    constexpr int S = 4;
+    uint32_t k[S];
+    int32_t blk[S], larger[S] = {0, 0, 0, 0};
+    const int n4 = (n + 3) / 4;
+    if (lane < 4 * n4 - n) {   // whole fours: keys of 0, blocks past all
+        s.key[n + lane] = 0u;
+        s.block[n + lane] = 0x7FFFFFFF;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int u = 0; u < S; ++u) {
+        const bool in = 32 * u + lane < n;
+        k[u] = in ? s.key[32 * u + lane] : 0xFFFFFFFFu;
+        blk[u] = in ? s.block[32 * u + lane] : -1;
+    }
+    const uint4 *k4 = reinterpret_cast<const uint4 *>(s.key);
+#pragma unroll 4
+    for (int j = 0; j < n4; ++j) {
+        const uint4 v = k4[j];
+#pragma unroll
+        for (int u = 0; u < S; ++u) larger[u] += (v.x > k[u]) + (v.y > k[u]) + (v.z > k[u]) + (v.w > k[u]);
+    }
+    bool pick[S];
+    int picks = 0;
+#pragma unroll
+    for (int u = 0; u < S; ++u) {
+        pick[u] = blk[u] >= 0 && larger[u] < top_k;
+        picks += pick[u];
+    }
+    if (__reduce_add_sync(kFull, picks) > top_k) {   // equal keys at the border: the lower blocks
+        list_candidates<S>(s, n, blocks, list, top_k, lane);
+        return;
+    }
+    __syncwarp();
+    int total = 0;
+#pragma unroll
+    for (int u = 0; u < S; ++u) {   // the listed blocks, in the keys' place
+        const uint32_t m = __ballot_sync(kFull, pick[u]);
+        if (pick[u]) s.key[total + __popc(m & ((1u << lane) - 1u))] = static_cast<uint32_t>(blk[u]);
+        total += __popc(m);
+    }
+    const int t4 = (total + 3) / 4;
+    if (lane < 4 * t4 - total) s.key[total + lane] = 0x7FFFFFFFu;
+    __syncwarp();
+    int at[S] = {0, 0, 0, 0};
+#pragma unroll 4
+    for (int j = 0; j < t4; ++j) {
+        const uint4 v = k4[j];
+#pragma unroll
+        for (int u = 0; u < S; ++u)
+            at[u] += (static_cast<int>(v.x) < blk[u]) + (static_cast<int>(v.y) < blk[u]) + (static_cast<int>(v.z) < blk[u]) + (static_cast<int>(v.w) < blk[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < S; ++u)
+        if (pick[u]) list[at[u]] = blk[u];
     for (int i = total + lane; i < top_k; i += 32) list[i] = -1;
 }
 
@@ -263,7 +325,7 @@ __device__ __forceinline__ void pick_row(const uint32_t *k, int n, Candidates &s
                     }
             }
             __syncwarp();
-            if (c <= 128) list_candidates<4>(s, c, n, list, top_k, lane);
+            if (c <= 128) list_few(s, c, n, list, top_k, lane);
             else list_candidates<kCand / 32>(s, c, n, list, top_k, lane);
             return;
         }
