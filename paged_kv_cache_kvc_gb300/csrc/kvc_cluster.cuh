@@ -24,6 +24,11 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
+// The two halves of a barrier that orders no memory: after the second, every CTA of the cluster has begun, so that its
+// shared memory may be written to.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait;" ::: "memory"); }
+
 // The address of CTA `rank`'s copy of a shared variable.
 __device__ __forceinline__ uint32_t cluster_addr(uint32_t local, uint32_t rank)
 {
@@ -49,6 +54,26 @@ __device__ __forceinline__ float4 cluster_ld4(uint32_t addr)
                  : "r"(addr)
                  : "memory");
     return v;
+}
+
+__device__ __forceinline__ float2 cluster_ld2(uint32_t addr)
+{
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+
+// Stores to, and adds to, another CTA's shared memory; the second returns the value before.
+__device__ __forceinline__ void cluster_st(uint32_t addr, uint32_t v)
+{
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ uint32_t cluster_add(uint32_t addr, uint32_t v)
+{
+    uint32_t old;
+    asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(old) : "r"(addr), "r"(v) : "memory");
+    return old;
 }
 
 }  // namespace kvc

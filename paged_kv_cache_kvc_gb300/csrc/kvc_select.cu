@@ -250,6 +250,14 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int seq = p.seqs ? __ldg(p.seqs + row) : static_cast<int>(row);
     const int pos = __ldg(p.positions + row);
+    uint4 x[2];   // the group's queries: 16 bytes of each thread, twice
+    const int chunks = p.g * D / 8;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int i = tid + u * kSelThreads;
+        x[u] = i < chunks ? __ldg(reinterpret_cast<const uint4 *>(p.q + (row * p.H_Q + static_cast<int64_t>(h) * p.g) * D) + i)
+                          : make_uint4(0u, 0u, 0u, 0u);
+    }
     if (seq == -1 || pos == -1) return;   // padding: the whole cluster leaves
     int32_t *list = p.lists + (row * p.H_KV + h) * p.top_k;
     if (seq < 0 || seq >= p.B || pos < 0 || pos / p.bs >= p.max_blocks) {
@@ -257,6 +265,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
         for (int i = rank * kSelThreads + tid; i < p.top_k; i += cs * kSelThreads) list[i] = -1;
         return;
     }
+    if (cs > 1) cluster_arrive();
     const int nb = pos / p.bs + 1;
     const int per = (nb + cs - 1) / cs;
     const int j0 = min(nb, rank * per), n = min(nb, j0 + per) - j0;   // this CTA's blocks
@@ -270,14 +279,9 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
     }
     __syncthreads();
     if (!all) {
-        const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (row * p.H_Q + static_cast<int64_t>(h) * p.g) * D);
-        const int chunks = p.g * D / 8;
-        uint4 x[2];
         float m = 0.f;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const int i = tid + u * kSelThreads;
-            x[u] = i < chunks ? src[i] : make_uint4(0u, 0u, 0u, 0u);
             const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
 #pragma unroll
             for (int k = 0; k < 4; ++k) m = fmaxf(m, fmaxf(fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k]))));   // NaNs drop out
@@ -373,6 +377,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
         }
     }
     __syncthreads();
+    if (cs > 1) cluster_wait();
 
     // ---- short lists: the largest keys of 256 groups over the cluster; at least top_k keys reach what top_k of those
     // reach, and not many more.  The first CTA ranks those few by counting.
@@ -380,22 +385,17 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
         uint32_t m = 0u;
         for (int i = tid; i < n; i += kSelThreads) m = max(m, keys[i]);
         for (int o = 1; o < cs; o <<= 1) m = max(m, __shfl_xor_sync(kFull, m, o));   // cs a power of two: 256 / cs groups
-        if (tid % cs == 0) hist[0][tid / cs] = m;
+        const int groups = kSelThreads / cs;
+        // lane tid mod cs of a group's threads tells CTA tid mod cs
+        cluster_st(cluster_addr(smem_u32(&sum[rank * groups + tid / cs]), tid % cs), m);
         if (cs > 1) cluster_sync();
         else __syncthreads();
-        const int groups = kSelThreads / cs;
-        m = cs > 1 ? cluster_ld(cluster_addr(smem_u32(&hist[0][tid % groups]), tid / groups)) : hist[0][tid];
-        sum[tid] = m;
-        __syncthreads();
-        {
-            const uint4 *all4 = reinterpret_cast<const uint4 *>(sum);
-            int reached = 0;
-#pragma unroll 8
-            for (int i = 0; i < kSelThreads / 4; ++i) {
-                const uint4 v = all4[i];
-                reached += (v.x >= m) + (v.y >= m) + (v.z >= m) + (v.w >= m);
-            }
-            if (reached >= p.top_k) atomicMax(&limit, m);
+        if (warp == 0) {
+            uint32_t v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v[u] = sum[32 * u + lane];
+            const uint32_t lim = reach_limit(v, static_cast<uint32_t>(p.top_k));
+            if (lane == 0) limit = lim;
         }
         __syncthreads();
         const uint32_t lim = max(limit, 1u);
@@ -407,36 +407,27 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
             const int y = __shfl_up_sync(kFull, at, o);
             if (lane >= o) at += y;
         }
-        int base = 0;
-        if (lane == 31) base = static_cast<int>(atomicAdd(&n_cand, static_cast<uint32_t>(at)));
-        at += __shfl_sync(kFull, base, 31) - mine;
+        // every CTA counts all candidates; the first one's count gives them their places, in its shared memory
+        const uint32_t warp_has = __shfl_sync(kFull, at, 31);
+        uint32_t base = 0u;
+        if (lane < cs && warp_has > 0u) base = cluster_add(cluster_addr(smem_u32(&n_cand), lane), warp_has);
+        at += static_cast<int>(__shfl_sync(kFull, base, 0)) - mine;
         if (mine > 0)
             for (int i = tid; i < n; i += kSelThreads) {
                 const uint32_t k = keys[i];
                 if (k >= lim) {
                     if (at < kCand) {
-                        cand.key[at] = k;
-                        cand.block[at] = j0 + i;
+                        cluster_st(cluster_addr(smem_u32(&cand.key[at]), 0), k);
+                        cluster_st(cluster_addr(smem_u32(&cand.block[at]), 0), static_cast<uint32_t>(j0 + i));
                     }
                     ++at;
                 }
             }
         if (cs > 1) cluster_sync();
         else __syncthreads();
-        uint32_t total = 0u;
-        for (int r = 0; r < cs; ++r) total += cluster_ld(cluster_addr(smem_u32(&n_cand), r));
-        if (total <= kSelThreads) {
+        if (n_cand <= kSelThreads) {
             if (rank == 0) {
-                const int c = static_cast<int>(total);
-                int from = static_cast<int>(n_cand);
-                for (int r = 1; r < cs; ++r) {
-                    const int more = static_cast<int>(cluster_ld(cluster_addr(smem_u32(&n_cand), r)));
-                    if (tid < more) {
-                        cand.key[from + tid] = cluster_ld(cluster_addr(smem_u32(&cand.key[tid]), r));
-                        cand.block[from + tid] = static_cast<int32_t>(cluster_ld(cluster_addr(smem_u32(&cand.block[tid]), r)));
-                    }
-                    from += more;
-                }
+                const int c = static_cast<int>(n_cand);
                 if (tid < 4) cand.key[c + tid] = 0u;   // whole fours (kCand is more than kSelThreads + 4)
                 __syncthreads();
                 const uint32_t k = tid < c ? cand.key[tid] : 0xFFFFFFFFu;
@@ -466,7 +457,6 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
                 if (pick) list[place] = blk;
                 for (int i = picks + tid; i < p.top_k; i += kSelThreads) list[i] = -1;
             }
-            if (cs > 1) cluster_sync();   // a CTA's shared memory stays until the first has read it
             return;
         }
         __syncthreads();   // many equal keys: all of them are counted below

@@ -80,7 +80,7 @@ extern "C" kvc_status kvc_sparse_attn(kvc_pool *pool, int32_t layer, const void 
     // CTAs per (row, KV head): as many as the grid has room for, each with a few tiles for every warp
     const int64_t units = n_rows * pool->H_KV, tiles = static_cast<int64_t>(top_k) * sp.sub;
     int c = 1;
-    while (c < 8 && units * c * 2 <= static_cast<int64_t>(pool->num_sms) * k.k.ctas_per_sm && tiles >= 2 * kWarps * c) c *= 2;
+    while (c < kSparseMost && units * c * 2 <= static_cast<int64_t>(pool->num_sms) * k.k.ctas_per_sm && tiles >= 2 * kWarps * c) c *= 2;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
