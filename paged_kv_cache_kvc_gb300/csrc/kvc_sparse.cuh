@@ -7,9 +7,11 @@
 // into the value product).
 //
 // Decomposition: a cluster of C CTAs (1, 2, 4 or 8) per (row, KV head), 4 warps each; warp w of CTA c takes tiles
-// c + C (w + 4 i), each warp through a ring of TMA stages of its own.  The warps of a CTA merge in shared memory and
-// the CTAs through distributed shared memory: no partial goes to global memory, so a call needs no workspace and
-// one launch, and two calls share nothing.
+// c + C (w + 4 i), T of them at a time (32 positions, for up to 16 query heads), through a ring of TMA stages of its
+// own.  A step's instructions wait on one another (products, maximum, exponentials, products), so what counts is how
+// much a step does: two tiles to a step share the maximum over lanes, the rescaling and the loop.  The warps of a CTA
+// merge in shared memory and the CTAs through distributed shared memory: no partial goes to global memory, so a call
+// needs no workspace and one launch, and two calls share nothing.
 #pragma once
 #include "kvc_cluster.cuh"
 #include "kvc_mod.cuh"
@@ -28,18 +30,236 @@ struct SparseParams {
 constexpr int kSparseMost = 8;   // CTAs of a cluster
 
 template <int D, int NT, int KIND>
-__host__ __device__ constexpr int sparse_smem_bytes()
+struct SparseCfg {
+    using C = DecodeCfg<D, KIND>;
+    static constexpr int T = NT == 4 ? 1 : 2;          // tiles per step (more columns leave no registers for two)
+    // tiles in flight per warp, so that shared memory holds what registers hold: bf16 two (64 KB a CTA, three CTAs or 12
+    // warps to an SM), e4m3 three (48 KB, four CTAs), int4 six
+    static constexpr int R = KIND == KV_BF16 ? (D == 64 ? 3 : 2) : (KIND == KV_E4M3 ? 3 : 6);
+    static constexpr int RING = kWarps * R * C::STAGE;
+    static constexpr int QW = NT * 8;
+    static constexpr int MERGE = (kWarps * QW * 2 + kWarps * QW * D) * 4;   // the warps' partials, in the ring's place
+    static constexpr int BARS = RING > MERGE ? RING : MERGE;                // offset of the barriers
+    static constexpr int SMEM = 1024 /* alignment */ + BARS + kWarps * R * 8;
+};
+
+// One step of a warp's running softmax: T tiles of 16 positions at st[t], of which the first valid[t] are read (all of
+// them when full).  Operand layouts as in kvc_decode.cuh.  Value rows that are not read hold finite numbers.
+template <int D, int NT, int KIND, bool PSPLIT, int T>
+__device__ __forceinline__ void tiles_update(float scale_log2, const uint32_t (&st)[T], const uint32_t (&qf)[NT][D / 16][2],
+                                             float (&m_run)[NT][2], float (&l_run)[NT][2], float (&oacc)[D / 16][NT][4],
+                                             bool full, const int (&valid)[T], int lane)
 {
-    return mod_smem_bytes<D, NT, KIND>();
+    using C = DecodeCfg<D, KIND>;
+    constexpr bool INT4 = KIND == KV_INT4, QUANT = KIND != KV_BF16;
+    constexpr int NACC = NT == 1 ? 2 : 1;   // with one column tile, even and odd k-steps accumulate apart
+    const int gq = lane >> 2, tg = lane & 3;
+    float sc[T][NT][4], sc2[T][NT][4];
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+#pragma unroll
+        for (int jn = 0; jn < NT; ++jn)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) sc[t][jn][c] = sc2[t][jn][c] = 0.f;
+    auto acc = [&](int t, int jn, int kk) -> float(&)[4] { return (NACC == 2 && (kk & 1)) ? sc2[t][jn] : sc[t][jn]; };
+    // ---- S^T = K Q^T
+    if constexpr (!QUANT) {
+#pragma unroll
+        for (int kk = 0; kk < C::KSTEPS; ++kk)
+#pragma unroll
+            for (int t = 0; t < T; ++t) {
+                uint32_t a[4];
+                ldsm_x4(a, st[t] + swz((lane & 7) + ((lane >> 3) & 1) * 8, 2 * kk + (lane >> 4)));
+#pragma unroll
+                for (int jn = 0; jn < NT; ++jn) mma_bf16(acc(t, jn, kk), a, qf[jn][kk]);
+            }
+    } else if constexpr (INT4) {
+        uint4 kw[T][2];
+#pragma unroll
+        for (int t = 0; t < T; ++t)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) kw[t][r] = lds128(st[t] + swz64(gq + 8 * r, tg));
+#pragma unroll
+        for (int kk = 0; kk < C::KSTEPS; ++kk)
+#pragma unroll
+            for (int t = 0; t < T; ++t) {
+                const uint32_t k0[4] = {kw[t][0].x, kw[t][0].y, kw[t][0].z, kw[t][0].w};
+                const uint32_t k1[4] = {kw[t][1].x, kw[t][1].y, kw[t][1].z, kw[t][1].w};
+                const int sh = 8 * (kk & 1);
+                const uint32_t w0 = k0[kk >> 1] >> sh, w1 = k1[kk >> 1] >> sh;
+                const uint32_t a[4] = {nibbles_to_f16x2(w0), nibbles_to_f16x2(w1), nibbles_hi_to_f16x2(w0), nibbles_hi_to_f16x2(w1)};
+#pragma unroll
+                for (int jn = 0; jn < NT; ++jn) mma_f16(acc(t, jn, kk), a, qf[jn][kk]);
+            }
+    } else {
+        uint32_t kw[T][2][D / 16];
+#pragma unroll
+        for (int t = 0; t < T; ++t)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int u = 0; u < D / 64; ++u) {
+                    const uint4 v = lds128(st[t] + swz(gq + 8 * r, (D / 64) * tg + u));
+                    kw[t][r][4 * u + 0] = v.x;
+                    kw[t][r][4 * u + 1] = v.y;
+                    kw[t][r][4 * u + 2] = v.z;
+                    kw[t][r][4 * u + 3] = v.w;
+                }
+#pragma unroll
+        for (int kk = 0; kk < C::KSTEPS; ++kk)
+#pragma unroll
+            for (int t = 0; t < T; ++t) {
+                uint32_t a[4];
+                e4m3x4_to_f16x2x2(kw[t][0][kk], a[0], a[2]);
+                e4m3x4_to_f16x2x2(kw[t][1][kk], a[1], a[3]);
+#pragma unroll
+                for (int jn = 0; jn < NT; ++jn) mma_f16(acc(t, jn, kk), a, qf[jn][kk]);
+            }
+    }
+
+    // ---- scale, mask, and the online softmax (log2 units; reference maxima move only past the slack)
+    uint32_t pb[T][NT][2], pl[T][NT][2];
+    float alpha[NT][2];
+    bool moved = false;
+#pragma unroll
+    for (int jn = 0; jn < NT; ++jn) {
+#pragma unroll
+        for (int t = 0; t < T; ++t)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                float x = sc[t][jn][c];
+                if constexpr (NACC == 2) x += sc2[t][jn][c];
+                x *= scale_log2;
+                sc[t][jn][c] = full || gq + 8 * (c >> 1) < valid[t] ? x : -INFINITY;
+            }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            float bm = fmaxf(sc[0][jn][c], sc[0][jn][c + 2]);
+#pragma unroll
+            for (int t = 1; t < T; ++t) bm = fmaxf(bm, fmaxf(sc[t][jn][c], sc[t][jn][c + 2]));
+            bm = fmaxf(bm, __shfl_xor_sync(kFull, bm, 4));
+            bm = fmaxf(bm, __shfl_xor_sync(kFull, bm, 8));
+            bm = fmaxf(bm, __shfl_xor_sync(kFull, bm, 16));
+            const bool up = bm > m_run[jn][c] + kRescaleSlack;   // false while nothing has been read
+            alpha[jn][c] = up ? fast_exp2(m_run[jn][c] - bm) : 1.f;
+            m_run[jn][c] = up ? bm : m_run[jn][c];
+            moved |= up;
+            const float mref = m_run[jn][c] == -INFINITY ? 0.f : m_run[jn][c];
+            float sum = 0.f;
+#pragma unroll
+            for (int t = 0; t < T; ++t) {
+                const float p0 = fast_exp2(sc[t][jn][c] - mref), p1 = fast_exp2(sc[t][jn][c + 2] - mref);
+                sum += p0 + p1;
+                sc[t][jn][c] = p0;
+                sc[t][jn][c + 2] = p1;
+            }
+            l_run[jn][c] = fmaf(l_run[jn][c], alpha[jn][c], sum);
+        }
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+            if constexpr (!QUANT) {
+                const uint32_t h0 = pack_bf16(sc[t][jn][0], sc[t][jn][1]), h1 = pack_bf16(sc[t][jn][2], sc[t][jn][3]);
+                pb[t][jn][0] = movmatrix_trans(h0);
+                pb[t][jn][1] = movmatrix_trans(h1);
+                if constexpr (PSPLIT) {
+                    pl[t][jn][0] = movmatrix_trans(pack_bf16(sc[t][jn][0] - bf16_lo(h0), sc[t][jn][1] - bf16_hi(h0)));
+                    pl[t][jn][1] = movmatrix_trans(pack_bf16(sc[t][jn][2] - bf16_lo(h1), sc[t][jn][3] - bf16_hi(h1)));
+                }
+            } else {
+                pb[t][jn][0] = movmatrix_trans(pack_f16(sc[t][jn][0], sc[t][jn][1]));
+                pb[t][jn][1] = movmatrix_trans(pack_f16(sc[t][jn][2], sc[t][jn][3]));
+            }
+        }
+    }
+    if (__any_sync(kFull, moved)) {
+#pragma unroll
+        for (int jn = 0; jn < NT; ++jn)
+#pragma unroll
+            for (int mt = 0; mt < C::MT; ++mt)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    oacc[mt][jn][c] *= alpha[jn][c];
+                    oacc[mt][jn][c + 2] *= alpha[jn][c];
+                }
+    }
+
+    // ---- O^T += V^T P^T
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+        const uint32_t sv = st[t];
+        if constexpr (!QUANT) {
+#pragma unroll
+            for (int mt = 0; mt < C::MT; ++mt) {
+                uint32_t a[4];
+                ldsm_x4_trans(a, sv + swz(kBS + (lane & 7) + ((lane >> 4) & 1) * 8, 2 * mt + ((lane >> 3) & 1)));
+#pragma unroll
+                for (int jn = 0; jn < NT; ++jn) {
+                    mma_bf16(oacc[mt][jn], a, pb[t][jn]);
+                    if constexpr (PSPLIT) mma_bf16(oacc[mt][jn], a, pl[t][jn]);
+                }
+            }
+        } else if constexpr (INT4) {
+            const uint32_t par = static_cast<uint32_t>(tg & 1);
+            uint32_t vw[4][2];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = kBS + 2 * tg + ((r & 1) ^ static_cast<int>(par)) + (r >> 1) * 8;
+                const uint32_t a = sv + swz64(row, gq >> 1) + 8 * (gq & 1);
+                asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(vw[r][0]), "=r"(vw[r][1]) : "r"(a));
+            }
+            const uint32_t sel0 = par ? 0x0044u : 0x4400u;
+#pragma unroll
+            for (int w = 0; w < 2; ++w)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t sel = sel0 + 0x1111u * static_cast<uint32_t>(k);
+                    const uint32_t x01 = __byte_perm(vw[0][w], vw[1][w], sel);
+                    const uint32_t x89 = __byte_perm(vw[2][w], vw[3][w], sel);
+                    const uint32_t a[4] = {nibbles_to_f16x2(x01), nibbles_hi_to_f16x2(x01), nibbles_to_f16x2(x89), nibbles_hi_to_f16x2(x89)};
+#pragma unroll
+                    for (int jn = 0; jn < NT; ++jn) mma_f16(oacc[4 * w + k][jn], a, pb[t][jn]);
+                }
+        } else {
+            uint32_t vw[4][D / 32];
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int u = 0; u < D / 128; ++u) {
+                    const uint4 v = lds128(sv + swz(kBS + 2 * tg + (r & 1) + (r >> 1) * 8, (D / 128) * gq + u));
+                    vw[r][4 * u + 0] = v.x;
+                    vw[r][4 * u + 1] = v.y;
+                    vw[r][4 * u + 2] = v.z;
+                    vw[r][4 * u + 3] = v.w;
+                }
+#pragma unroll
+            for (int w = 0; w < D / 32; ++w) {
+                const uint32_t x01 = __byte_perm(vw[0][w], vw[1][w], 0x5140);
+                const uint32_t y01 = __byte_perm(vw[0][w], vw[1][w], 0x7362);
+                const uint32_t x89 = __byte_perm(vw[2][w], vw[3][w], 0x5140);
+                const uint32_t y89 = __byte_perm(vw[2][w], vw[3][w], 0x7362);
+                uint32_t a0[4], a1[4];
+                e4m3x4_to_f16x2x2(x01, a0[0], a0[1]);
+                e4m3x4_to_f16x2x2(x89, a0[2], a0[3]);
+                e4m3x4_to_f16x2x2(y01, a1[0], a1[1]);
+                e4m3x4_to_f16x2x2(y89, a1[2], a1[3]);
+#pragma unroll
+                for (int jn = 0; jn < NT; ++jn) {
+                    mma_f16(oacc[2 * w][jn], a0, pb[t][jn]);
+                    mma_f16(oacc[2 * w + 1][jn], a1, pb[t][jn]);
+                }
+            }
+        }
+    }
 }
 
 // grid (C x rows, KV head), clusters of C CTAs along x
 template <int D, int NT, int KIND, bool PSPLIT>
 __global__ void __launch_bounds__(kThreads) sparse_kernel(const __grid_constant__ CUtensorMap tmap, const SparseParams sp)
 {
+    using S = SparseCfg<D, NT, KIND>;
     using C = DecodeCfg<D, KIND>;
     constexpr bool INT4 = KIND == KV_INT4, QUANT = KIND != KV_BF16;
-    constexpr int QW = NT * 8;
+    constexpr int QW = S::QW, T = S::T, R = S::R;
     const ModParams &mp = sp.m;
     const DecodeParams &p = mp.d;
     extern __shared__ uint8_t smem_raw[];
@@ -51,11 +271,9 @@ __global__ void __launch_bounds__(kThreads) sparse_kernel(const __grid_constant_
     const int gq = lane >> 2, tg = lane & 3;
     const size_t orow = static_cast<size_t>(row) * p.H_Q + static_cast<size_t>(h) * p.g;   // of the group's first head
 
-    constexpr int kBars = decode_smem_bytes<D, NT, KIND>() - 1024 - kWarps * C::R * 8;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kBars);
-    Column *cols = reinterpret_cast<Column *>(smem + kBars + kWarps * C::R * 8);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::BARS) + warp * R;   // this warp's
     if (lane == 0) {
-        for (int s = 0; s < C::R; ++s) mbar_init(smem_u32(&bars[warp * C::R + s]), 1);
+        for (int i = 0; i < R; ++i) mbar_init(smem_u32(&bars[i]), 1);
         fence_barrier_init();
     }
     if (threadIdx.x == 0) prefetch_tensormap(&tmap);
@@ -110,20 +328,14 @@ __global__ void __launch_bounds__(kThreads) sparse_kernel(const __grid_constant_
         if (rank == 0 && threadIdx.x == 0) atomicOr(p.err, KVC_EBIT_RANGE);
         len = 0;
     }
-    for (int qi = threadIdx.x; qi < 32; qi += kThreads) {
-        Column k;
-        k.r = Range{0, qi < p.g ? len : 0, 0, 0};
-        k.slope = 0.f;
-        k.pos = pos;
-        cols[qi] = k;
-    }
-    __syncthreads();
+    __syncwarp();   // the barriers are this warp's own
 
     const int tiles = len > 0 ? listed : 0;
     const int nmine = tiles > first ? (tiles - first + step - 1) / step : 0;
     const int32_t *bt_row = p.bt + static_cast<int64_t>(seq) * p.bt_stride;
-    const uint32_t st_base = smem_u32(smem + warp * C::R * C::STAGE);
-    const uint32_t bar_base = smem_u32(&bars[warp * C::R]);
+    const int nsteps = (nmine + T - 1) / T;
+    const uint32_t st_base = smem_u32(smem + warp * R * C::STAGE);
+    const uint32_t bar_base = smem_u32(bars);
     const int own = pos / (sp.sub * kBS);
 
     // This warp's tiles, 32 at a time in registers: (first position, block), block -1: nothing to read.
@@ -144,25 +356,26 @@ __global__ void __launch_bounds__(kThreads) sparse_kernel(const __grid_constant_
         return make_int2(tok0, phys);
     };
     int2 t_cur = load_tile(lane, e_cur), t_next = load_tile(32 + lane, e_next);
-    auto entry = [&](int jj, int jbase) -> int2 {
+    auto entry = [&](int jj, int jbase) -> int2 {   // tile jj, which may differ from lane to lane
         const int2 v = (jj - jbase < 32) ? t_cur : t_next;
         return make_int2(__shfl_sync(kFull, v.x, (jj - jbase) & 31), __shfl_sync(kFull, v.y, (jj - jbase) & 31));
     };
     const int64_t layer_row = static_cast<int64_t>(p.layer) * p.N;
-    auto issue = [&](int jj, int jbase) {   // warp-collective; lane 0 issues
-        const int2 e = entry(jj, jbase);
-        if (lane == 0 && !p.stall_loads) {
-            const uint32_t bar = bar_base + 8u * static_cast<uint32_t>(jj % C::R);
+    // Tile j is stage j % R of the ring.  Lane t issues tile from + t, t < n.
+    auto issue = [&](int from, int n, int jbase) {   // warp-collective
+        const int j = from + lane;
+        const int2 e = entry(j, jbase);
+        if (lane < n && j < nmine && !p.stall_loads) {
+            const uint32_t bar = bar_base + 8u * static_cast<uint32_t>(j % R);
             if (e.y < 0) {
                 mbar_arrive(bar);   // complete the phase without data; the consumer skips it
             } else {
-                const uint32_t dst = st_base + static_cast<uint32_t>((jj % C::R) * C::STAGE);
-                const int64_t blk = (layer_row + e.y) * p.H_KV + h;
-                mbar_arrive_expect_tx(bar, C::STAGE);
+                const uint32_t dst = st_base + static_cast<uint32_t>((j % R) * C::STAGE);
                 // keys, then the values behind them in the same stage, one box per 128-byte band each
                 constexpr int rows_per_tile = C::BOX_ROWS / 2;   // map rows (int4: 128-byte lines) of 16 positions
-                const int part = (e.x / kBS) % sp.sub;
-                const int32_t y = static_cast<int32_t>(blk * (2 * rows_per_tile) * sp.sub) + part * rows_per_tile;
+                const int part_i = (e.x / kBS) % sp.sub;
+                const int32_t y = static_cast<int32_t>(((layer_row + e.y) * p.H_KV + h) * (2 * rows_per_tile) * sp.sub) + part_i * rows_per_tile;
+                mbar_arrive_expect_tx(bar, C::STAGE);
 #pragma unroll
                 for (int band = 0; band < C::BANDS; ++band) {
                     tma_load_2d(dst + band * C::BOX_BYTES, &tmap, bar, band * C::BOX_X, y);
@@ -172,7 +385,7 @@ __global__ void __launch_bounds__(kThreads) sparse_kernel(const __grid_constant_
             }
         }
     };
-    for (int jj = 0; jj < min(C::R, nmine); ++jj) issue(jj, 0);
+    issue(0, R, 0);
 
     float m_run[NT][2], l_run[NT][2];
     float oacc[C::MT][NT][4];
@@ -184,44 +397,59 @@ __global__ void __launch_bounds__(kThreads) sparse_kernel(const __grid_constant_
         for (int mt = 0; mt < C::MT; ++mt) oacc[mt][j][0] = oacc[mt][j][1] = oacc[mt][j][2] = oacc[mt][j][3] = 0.f;
     }
 
-    int j = 0;
+    int i = 0;
     bool timed_out = false;
-    for (; j < nmine; ++j) {
-        const int jbase = j & ~31;
+    for (; i < nsteps; ++i) {
+        const int j = i * T, jbase = j & ~31;
         if (j > 0 && (j & 31) == 0) {
             t_cur = t_next;
             t_next = load_tile(j + 32 + lane, load_entry(j + 32 + lane));
         }
-        const int s = j % C::R;
-        const bool ok = mbar_wait_bounded(bar_base + 8u * s, static_cast<uint32_t>((j / C::R) & 1));
+        uint32_t st[T];
+        bool ok = true;
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+            st[t] = st_base + static_cast<uint32_t>(((j + t) % R) * C::STAGE);
+            if (j + t < nmine) ok &= mbar_wait_bounded(bar_base + 8u * ((j + t) % R), static_cast<uint32_t>(((j + t) / R) & 1));
+        }
         if (!__all_sync(kFull, ok)) {
             timed_out = true;
             break;
         }
-        const int2 e = entry(j, jbase);
-        if (e.y >= 0) {
-            const uint32_t st = st_base + static_cast<uint32_t>(s * C::STAGE);
-            const int valid = min(kBS, len - e.x);
-            // value rows past the query may hold anything (NaN included): zero them
-            if (!INT4 && valid < kBS) {
-                const int nz = (kBS - valid) * C::BANDS * 8;
-                for (int i = lane; i < nz; i += 32)
-                    sts128_zero(st + swz(kBS + valid + i / (C::BANDS * 8), i % (C::BANDS * 8)));
+        int valid[T];
+        bool full = true, some = false;
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+            const int2 e = entry(j + t, jbase);
+            valid[t] = e.y < 0 ? 0 : min(kBS, len - e.x);
+            full &= valid[t] == kBS;
+            some |= valid[t] > 0;
+        }
+        if (some) {
+            // value rows past the query, or of no tile, may hold anything (NaN included): zero them
+            // (every int4 nibble is a finite value, and its weight there is 0)
+            if (!INT4 && !full) {
+#pragma unroll
+                for (int t = 0; t < T; ++t) {
+                    const int nz = (kBS - valid[t]) * C::BANDS * 8;
+                    for (int z = lane; z < nz; z += 32)
+                        sts128_zero(st[t] + swz(kBS + valid[t] + z / (C::BANDS * 8), z % (C::BANDS * 8)));
+                }
             }
             __syncwarp();
-            mod_block_update<D, NT, KIND, PSPLIT>(mp, st, qf, m_run, l_run, oacc, valid == kBS, e.x, cols, lane);
+            tiles_update<D, NT, KIND, PSPLIT, T>(p.scale_log2, st, qf, m_run, l_run, oacc, full, valid, lane);
         }
         __syncwarp();
-        if (j + C::R < nmine) {
-            if (lane == 0) fence_proxy_async_smem();
-            issue(j + C::R, jbase);
+        if (j + R < nmine) {
+            if (lane < T) fence_proxy_async_smem();   // the lanes that issue
+            issue(j + R, T, jbase);
         }
     }
     if (timed_out) {   // record, then let copies already in flight land before the CTA exits
         if (lane == 0) {
             atomicOr(p.err, KVC_EBIT_TIMEOUT);
-            for (int jj = j; jj < min(nmine, j + C::R); ++jj)
-                (void)mbar_wait_bounded(bar_base + 8u * (jj % C::R), static_cast<uint32_t>((jj / C::R) & 1), 100000000ull);
+            for (int x = i * T; x < min(nmine, i * T + R); ++x)
+                (void)mbar_wait_bounded(bar_base + 8u * (x % R), static_cast<uint32_t>((x / R) & 1), 100000000ull);
         }
         __syncwarp();
     }
@@ -339,7 +567,7 @@ SparseKernel sparse_instance()
 {
     struct Tag {};
     return {&sparse_kernel<D, NT, KIND, PSPLIT>,
-            configured<Tag>(reinterpret_cast<const void *>(&sparse_kernel<D, NT, KIND, PSPLIT>), sparse_smem_bytes<D, NT, KIND>(),
+            configured<Tag>(reinterpret_cast<const void *>(&sparse_kernel<D, NT, KIND, PSPLIT>), SparseCfg<D, NT, KIND>::SMEM,
                             kThreads, false)};
 }
 
