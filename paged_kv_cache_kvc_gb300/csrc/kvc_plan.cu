@@ -20,8 +20,6 @@
 
 namespace kvc {
 
-constexpr int kPlanThreads = 512;
-constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kPlanCluster = 8;
 constexpr int kPlanMost = 32768;      // sequences: a CTA keeps five words for each of its own, and all row offsets
 
@@ -63,15 +61,26 @@ __device__ __forceinline__ int find_run(const uint32_t *off, int n, uint32_t x)
     return lo;
 }
 
+// One CTA of 256 threads for a decoding batch (CLUSTER false), else a cluster of CTAs of 1024.
+template <int kPlanThreads, bool CLUSTER>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
 {
+    constexpr int kPlanWarps = kPlanThreads / 32;
+    auto sync_all = [] {
+        if constexpr (CLUSTER) cluster_sync();
+        else __syncthreads();
+    };
+    auto peek = [](const uint32_t &x, int c) {   // CTA c's copy of a shared variable
+        if constexpr (CLUSTER) return cluster_ld(cluster_addr(static_cast<uint32_t>(__cvta_generic_to_shared(&x)), c));
+        else return x;
+    };
     // this CTA's sequences: lengths, and exclusive sums of what they return and take (one more: the total);
     // afterwards the row offsets of all sequences
     extern __shared__ uint32_t plan_smem[];
     __shared__ PlanSum warp_sum[kPlanWarps], total;   // total: this CTA's
     __shared__ uint2 granted;                         // the largest sums (blocks, rows) of this CTA that are not over
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int C = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
+    const int C = CLUSTER ? static_cast<int>(cluster_size()) : 1, rank = CLUSTER ? static_cast<int>(cluster_rank()) : 0;
     const int per = (p.B + C - 1) / C;
     const int b0 = min(p.B, rank * per), nb = min(p.B, b0 + per) - b0;
     uint32_t *s_len = plan_smem, *s_new = s_len + per, *s_rel = s_new + per, *s_grow = s_rel + per + 1,
@@ -136,13 +145,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
         total = carry;
         granted = make_uint2(0u, 0u);
     }
-    cluster_sync();
+    sync_all();
 
     // ---- sums of the CTAs before this one, and in all
     PlanSum first{0u, 0u, 0u}, whole{0u, 0u, 0u};
     for (int c = 0; c < C; ++c) {
-        const uint32_t a = cluster_addr(static_cast<uint32_t>(__cvta_generic_to_shared(&total)), c);
-        const PlanSum x{cluster_ld(a), cluster_ld(a + 4), cluster_ld(a + 8)};
+        const PlanSum x{peek(total.rel, c), peek(total.grow, c), peek(total.tok, c)};
         if (c < rank) first = first + x;
         whole = whole + x;
     }
@@ -159,23 +167,31 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
             granted = make_uint2(add_sat(first.grow, s_grow[i]), add_sat(first.tok, s_tok[i]));
 
     // ---- push what sequences return
-    for (uint32_t x = tid; x < s_rel[nb]; x += kPlanThreads) {
-        const int i = find_run(s_rel, nb, x);
-        const int b = b0 + i;
-        const int64_t j = static_cast<int64_t>(blocks_of(s_new[i])) + (x - s_rel[i]);
-        const int32_t blk = p.bt[static_cast<int64_t>(b) * p.max_blocks + j];
-        if (blk < 0 || blk >= p.N) atomicOr(p.err, KVC_EBIT_BAD_BLOCK);
-        const uint32_t at = add_sat(add_sat(count, first.rel), x);
-        if (at < static_cast<uint32_t>(p.capacity)) p.stack[at] = blk;
+    for (uint32_t x0 = 4u * tid; x0 < s_rel[nb]; x0 += 4u * kPlanThreads) {   // four neighbours a thread, one search
+        const uint32_t n = min(4u, s_rel[nb] - x0);
+        int i = find_run(s_rel, nb, x0);
+        int32_t blk[4];
+#pragma unroll
+        for (uint32_t u = 0; u < 4u; ++u) {
+            while (u < n && x0 + u >= s_rel[i + 1]) ++i;
+            blk[u] = 0;
+            if (u < n) blk[u] = p.bt[static_cast<int64_t>(b0 + i) * p.max_blocks + blocks_of(s_new[i]) + (x0 + u - s_rel[i])];
+        }
+#pragma unroll
+        for (uint32_t u = 0; u < 4u; ++u) {
+            if (u >= n) break;
+            if (blk[u] < 0 || blk[u] >= p.N) atomicOr(p.err, KVC_EBIT_BAD_BLOCK);
+            const uint32_t at = add_sat(add_sat(count, first.rel), x0 + u);
+            if (at < static_cast<uint32_t>(p.capacity)) p.stack[at] = blk[u];
+        }
     }
-    cluster_sync();
+    sync_all();
 
     // ---- lengths, row offsets, and blocks for those that grow
     uint32_t blocks_in_all = 0u, rows_in_all = 0u;
     for (int c = 0; c < C; ++c) {
-        const uint32_t a = cluster_addr(static_cast<uint32_t>(__cvta_generic_to_shared(&granted)), c);
-        blocks_in_all = max(blocks_in_all, cluster_ld(a));
-        rows_in_all = max(rows_in_all, cluster_ld(a + 4));
+        blocks_in_all = max(blocks_in_all, peek(granted.x, c));
+        rows_in_all = max(rows_in_all, peek(granted.y, c));
     }
     for (int i = tid; i < nb; i += kPlanThreads) {
         const bool refused = over(i + 1);
@@ -188,12 +204,20 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
         *p.count_out = static_cast<int32_t>(avail - blocks_in_all);   // every CTA has read the count by now
     }
     const uint32_t mine = blocks_in_all > first.grow ? min(s_grow[nb], blocks_in_all - first.grow) : 0u;
-    for (uint32_t x = tid; x < mine; x += kPlanThreads) {
-        const int i = find_run(s_grow, nb, x);
-        const int64_t j = static_cast<int64_t>(blocks_of(s_len[i])) + (x - s_grow[i]);
-        p.bt[static_cast<int64_t>(b0 + i) * p.max_blocks + j] = __ldcg(p.stack + (avail - 1u - first.grow - x));
+    for (uint32_t x0 = 4u * tid; x0 < mine; x0 += 4u * kPlanThreads) {
+        const uint32_t n = min(4u, mine - x0);
+        int32_t blk[4];
+#pragma unroll
+        for (uint32_t u = 0; u < 4u; ++u) blk[u] = u < n ? __ldcg(p.stack + (avail - 1u - first.grow - x0 - u)) : 0;
+        int i = find_run(s_grow, nb, x0);
+#pragma unroll
+        for (uint32_t u = 0; u < 4u; ++u) {
+            if (u >= n) break;
+            while (x0 + u >= s_grow[i + 1]) ++i;
+            p.bt[static_cast<int64_t>(b0 + i) * p.max_blocks + blocks_of(s_len[i]) + (x0 + u - s_grow[i])] = blk[u];
+        }
     }
-    cluster_sync();
+    sync_all();
 
     // ---- rows, four at a time
     uint32_t *cu = plan_smem;
@@ -202,32 +226,38 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
     const bool wide = ((reinterpret_cast<uintptr_t>(p.slots) | reinterpret_cast<uintptr_t>(p.positions) |
                         reinterpret_cast<uintptr_t>(p.seqs)) & 15) == 0;   // null pointers count as aligned
     for (int64_t r0 = 4ll * (rank * kPlanThreads + tid); r0 < p.n_rows; r0 += 4ll * C * kPlanThreads) {
+        // the four rows' sequences first, then what each has to look up: two loads after one another, not eight
         int s[4], pos[4], seq[4];
         int b = -1;
-        int32_t start = 0, blk = -1;
-        int64_t j_at = -1;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const uint32_t r = static_cast<uint32_t>(r0) + u;
-            s[u] = pos[u] = seq[u] = -1;
-            if (r >= rows_in_all) continue;
-            if (b < 0 || r >= cu[b + 1]) {
-                b = find_run(cu, p.B, r);
-                start = __ldcg(p.lens_out + b) - static_cast<int32_t>(cu[b + 1] - cu[b]);
-                j_at = -1;
+            seq[u] = -1;
+            if (r < rows_in_all) {
+                if (b < 0) b = find_run(cu, p.B, r);
+                while (r >= cu[b + 1]) ++b;
+                seq[u] = b;
             }
-            pos[u] = start + static_cast<int32_t>(r - cu[b]);
-            seq[u] = b;
-            const int32_t j = pos[u] / p.bs;
-            if (j != j_at) {
-                blk = __ldcg(p.bt + static_cast<int64_t>(b) * p.max_blocks + j);
-                j_at = j;
-                if (blk < 0 || blk >= p.N) {
-                    atomicOr(p.err, KVC_EBIT_BAD_BLOCK);
-                    blk = -1;
-                }
+        }
+        int32_t has[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) has[u] = seq[u] >= 0 ? __ldcg(p.lens_out + seq[u]) : 0;
+        int32_t blk[4], place[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            pos[u] = place[u] = blk[u] = -1;
+            if (seq[u] >= 0) {   // the last of the sequence's new tokens is at has - 1
+                pos[u] = has[u] - static_cast<int32_t>(cu[seq[u] + 1] - (static_cast<uint32_t>(r0) + u));
+                const int32_t j = pos[u] / p.bs;
+                place[u] = pos[u] - j * p.bs;
+                blk[u] = __ldcg(p.bt + static_cast<int64_t>(seq[u]) * p.max_blocks + j);
             }
-            s[u] = blk < 0 ? -1 : blk * p.bs + (pos[u] - j * p.bs);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const bool bad = seq[u] >= 0 && (blk[u] < 0 || blk[u] >= p.N);
+            if (bad) atomicOr(p.err, KVC_EBIT_BAD_BLOCK);
+            s[u] = seq[u] < 0 || bad ? -1 : blk[u] * p.bs + place[u];
         }
         if (wide && r0 + 4 <= p.n_rows) {
             *reinterpret_cast<int4 *>(p.slots + r0) = make_int4(s[0], s[1], s[2], s[3]);
@@ -244,6 +274,35 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
         }
     }
     // no CTA reads another's shared memory after the barrier above
+}
+
+template <int THREADS, bool CLUSTER>
+static kvc_status launch_plan(const PlanParams &p, cudaStream_t stream)
+{
+    constexpr int C = CLUSTER ? kPlanCluster : 1;
+    constexpr int kPer = CLUSTER ? kPlanMost / C : 512;   // sequences of a CTA at most
+    constexpr int kSmem = 4 * (5 * kPer + 3 > kPer * C + 1 ? 5 * kPer + 3 : kPer * C + 1);
+    struct Tag {};
+    const DecodeKernel k = configured<Tag>(reinterpret_cast<const void *>(&plan_kernel<THREADS, CLUSTER>), kSmem, THREADS, false);
+    if (k.ctas_per_sm <= 0) return KVC_ERR_CUDA;
+    const int per = (p.B + C - 1) / C;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = C;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(C);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = static_cast<size_t>(4) * std::max(5 * per + 3, p.B + 1);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = CLUSTER ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, plan_kernel<THREADS, CLUSTER>, p);
+    if (e != cudaSuccess) return cuda_status(e);
+    g_launches.fetch_add(1, std::memory_order_relaxed);
+    return KVC_OK;
 }
 
 static bool aligned4(const void *ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 3) == 0; }
@@ -287,28 +346,6 @@ extern "C" kvc_status kvc_plan_step(kvc_pool *pool, int32_t *block_tables, int32
     p.seqs = seq_ids;
     p.n_rows = static_cast<int32_t>(n_rows);
     p.err = pool->err;
-    const int C = B <= kPlanThreads && n_rows <= 4 * kPlanThreads ? 1 : kPlanCluster;
-    const int per = (B + C - 1) / C;
-    const int smem = 4 * std::max(5 * per + 3, B + 1);
-    constexpr int kMost = 4 * (5 * (kPlanMost / kPlanCluster) + 3 > kPlanMost + 1 ? 5 * (kPlanMost / kPlanCluster) + 3 : kPlanMost + 1);
-    struct Tag {};
-    const DecodeKernel k = configured<Tag>(reinterpret_cast<const void *>(&plan_kernel), kMost, kPlanThreads, false);
-    if (k.ctas_per_sm <= 0) return KVC_ERR_CUDA;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = C;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(C);
-    cfg.blockDim = dim3(kPlanThreads);
-    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-    cfg.stream = static_cast<cudaStream_t>(stream);
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, plan_kernel, p);
-    if (e != cudaSuccess) return cuda_status(e);
-    g_launches.fetch_add(1, std::memory_order_relaxed);
-    return KVC_OK;
+    const bool one = B <= 512 && n_rows <= 1024;   // 1024 rows are one pass of 256 threads
+    return one ? launch_plan<256, false>(p, static_cast<cudaStream_t>(stream)) : launch_plan<1024, true>(p, static_cast<cudaStream_t>(stream));
 }
