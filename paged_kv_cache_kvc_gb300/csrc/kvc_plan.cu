@@ -34,6 +34,7 @@ struct PlanParams {
     const int32_t *count;
     int32_t *lens_out, *count_out, *cu, *slots, *positions, *seqs;
     int32_t n_rows;
+    bool rows_here;   // the cluster writes the maps too
     uint32_t *err;
 };
 
@@ -61,7 +62,64 @@ __device__ __forceinline__ int find_run(const uint32_t *off, int n, uint32_t x)
     return lo;
 }
 
-// One CTA of 256 threads for a decoding batch (CLUSTER false), else a cluster of CTAs of 1024.
+__device__ __forceinline__ bool maps_aligned(const PlanParams &p)   // to 16 bytes; null pointers are
+{
+    return ((reinterpret_cast<uintptr_t>(p.slots) | reinterpret_cast<uintptr_t>(p.positions) | reinterpret_cast<uintptr_t>(p.seqs)) & 15) == 0;
+}
+
+// Rows r0 .. r0 + 3 of the maps.  cu: row offsets of n sequences from `first` on (and one more), which hold the rows below
+// `total`; rows from there on are padding.  wide: the maps are 16-byte aligned.
+__device__ __forceinline__ void write_rows(const PlanParams &p, int64_t r0, uint32_t total, const uint32_t *cu, int first, int n, bool wide)
+{
+    // the four rows' sequences first, then what each has to look up: two loads after one another, not eight
+    int s[4], pos[4], seq[4];
+    int b = -1;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const uint32_t r = static_cast<uint32_t>(r0) + u;
+        seq[u] = -1;
+        if (r < total) {
+            if (b < 0) b = find_run(cu, n, r);
+            while (r >= cu[b + 1]) ++b;
+            seq[u] = first + b;
+        }
+    }
+    int32_t has[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) has[u] = seq[u] >= 0 ? __ldcg(p.lens_out + seq[u]) : 0;
+    int32_t blk[4], place[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        pos[u] = place[u] = blk[u] = -1;
+        if (seq[u] >= 0) {   // the last of the sequence's new tokens is at has - 1
+            pos[u] = has[u] - static_cast<int32_t>(cu[seq[u] - first + 1] - (static_cast<uint32_t>(r0) + u));
+            const int32_t j = pos[u] / p.bs;
+            place[u] = pos[u] - j * p.bs;
+            blk[u] = __ldcg(p.bt + static_cast<int64_t>(seq[u]) * p.max_blocks + j);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const bool bad = seq[u] >= 0 && (blk[u] < 0 || blk[u] >= p.N);
+        if (bad) atomicOr(p.err, KVC_EBIT_BAD_BLOCK);
+        s[u] = seq[u] < 0 || bad ? -1 : blk[u] * p.bs + place[u];
+    }
+    if (wide && r0 + 4 <= p.n_rows) {
+        *reinterpret_cast<int4 *>(p.slots + r0) = make_int4(s[0], s[1], s[2], s[3]);
+        if (p.positions) *reinterpret_cast<int4 *>(p.positions + r0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+        if (p.seqs) *reinterpret_cast<int4 *>(p.seqs + r0) = make_int4(seq[0], seq[1], seq[2], seq[3]);
+    } else {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (r0 + u < p.n_rows) {
+                p.slots[r0 + u] = s[u];
+                if (p.positions) p.positions[r0 + u] = pos[u];
+                if (p.seqs) p.seqs[r0 + u] = seq[u];
+            }
+    }
+}
+
+// One CTA of 256 threads for a decoding batch (CLUSTER false), else a cluster of larger ones.
 template <int kPlanThreads, bool CLUSTER>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
 {
@@ -80,7 +138,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
     __shared__ PlanSum warp_sum[kPlanWarps], total;   // total: this CTA's
     __shared__ uint2 granted;                         // the largest sums (blocks, rows) of this CTA that are not over
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int C = CLUSTER ? static_cast<int>(cluster_size()) : 1, rank = CLUSTER ? static_cast<int>(cluster_rank()) : 0;
+    constexpr int C = CLUSTER ? kPlanCluster : 1;
+    const int rank = CLUSTER ? static_cast<int>(cluster_rank()) : 0;
     const int per = (p.B + C - 1) / C;
     const int b0 = min(p.B, rank * per), nb = min(p.B, b0 + per) - b0;
     uint32_t *s_len = plan_smem, *s_new = s_len + per, *s_rel = s_new + per, *s_grow = s_rel + per + 1,
@@ -122,7 +181,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
         if (lane == 31) warp_sum[warp] = inc;
         __syncthreads();
         PlanSum before = carry, all = carry;
-        for (int w = 0; w < kPlanWarps; ++w) {
+        const int used = min(kPlanWarps, (nb - base + 31) / 32);
+        for (int w = 0; w < used; ++w) {
             if (w < warp) before = before + warp_sum[w];
             all = all + warp_sum[w];
         }
@@ -148,11 +208,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
     sync_all();
 
     // ---- sums of the CTAs before this one, and in all
-    PlanSum first{0u, 0u, 0u}, whole{0u, 0u, 0u};
+    PlanSum first{0u, 0u, 0u}, whole{0u, 0u, 0u}, of[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) of[c] = PlanSum{peek(total.rel, c), peek(total.grow, c), peek(total.tok, c)};
+#pragma unroll
     for (int c = 0; c < C; ++c) {
-        const PlanSum x{peek(total.rel, c), peek(total.grow, c), peek(total.tok, c)};
-        if (c < rank) first = first + x;
-        whole = whole + x;
+        if (c < rank) first = first + of[c];
+        whole = whole + of[c];
     }
     const uint32_t count = static_cast<uint32_t>(min(max(raw_count, 0), p.capacity));
     if (rank == 0 && tid == 0 && (raw_count != static_cast<int>(count) || add_sat(count, whole.rel) > static_cast<uint32_t>(p.capacity)))
@@ -189,9 +251,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
 
     // ---- lengths, row offsets, and blocks for those that grow
     uint32_t blocks_in_all = 0u, rows_in_all = 0u;
+    uint2 got[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) got[c] = make_uint2(peek(granted.x, c), peek(granted.y, c));
+#pragma unroll
     for (int c = 0; c < C; ++c) {
-        blocks_in_all = max(blocks_in_all, peek(granted.x, c));
-        rows_in_all = max(rows_in_all, peek(granted.y, c));
+        blocks_in_all = max(blocks_in_all, got[c].x);
+        rows_in_all = max(rows_in_all, got[c].y);
     }
     for (int i = tid; i < nb; i += kPlanThreads) {
         const bool refused = over(i + 1);
@@ -219,61 +285,56 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
     }
     sync_all();
 
+    if (!p.rows_here) return;   // no CTA reads another's shared memory after the barrier above
+
     // ---- rows, four at a time
     uint32_t *cu = plan_smem;
     for (int i = tid; i <= p.B; i += kPlanThreads) cu[i] = static_cast<uint32_t>(__ldcg(p.cu + i));
     __syncthreads();
-    const bool wide = ((reinterpret_cast<uintptr_t>(p.slots) | reinterpret_cast<uintptr_t>(p.positions) |
-                        reinterpret_cast<uintptr_t>(p.seqs)) & 15) == 0;   // null pointers count as aligned
+    const bool wide = maps_aligned(p);
     for (int64_t r0 = 4ll * (rank * kPlanThreads + tid); r0 < p.n_rows; r0 += 4ll * C * kPlanThreads) {
-        // the four rows' sequences first, then what each has to look up: two loads after one another, not eight
-        int s[4], pos[4], seq[4];
-        int b = -1;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const uint32_t r = static_cast<uint32_t>(r0) + u;
-            seq[u] = -1;
-            if (r < rows_in_all) {
-                if (b < 0) b = find_run(cu, p.B, r);
-                while (r >= cu[b + 1]) ++b;
-                seq[u] = b;
+        write_rows(p, r0, rows_in_all, cu, 0, p.B, wide);
+    }
+}
+
+constexpr int kRowsThreads = 256;
+constexpr int kRowsCta = 4 * kRowsThreads;
+
+// The maps of many rows, over the whole GPU after the cluster's kernel: a CTA finds the sequences of its 1024 rows, a
+// warp narrowing the offsets by 32 at a time, and keeps their offsets in shared memory.
+__global__ void __launch_bounds__(kRowsThreads) plan_rows_kernel(const PlanParams p)
+{
+    __shared__ uint32_t cu[kRowsCta + 1];
+    __shared__ int ends[2];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t r0 = static_cast<int64_t>(blockIdx.x) * kRowsCta;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const uint32_t total = static_cast<uint32_t>(__ldcg(p.cu + p.B));
+    int b0 = 0, n = 0;
+    const uint32_t *offsets = cu;
+    if (r0 < total) {   // the same for the whole CTA
+        if (warp < 2) {
+            const uint32_t r = warp == 0 ? static_cast<uint32_t>(r0) : min(static_cast<uint32_t>(r0) + kRowsCta - 1u, total - 1u);
+            int lo = 0, hi = p.B;   // cu[lo] <= r < cu[hi]
+            while (hi - lo > 1) {
+                const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+                const uint32_t m = __ballot_sync(kFull, at < hi && static_cast<uint32_t>(__ldcg(p.cu + min(at, hi))) <= r);
+                lo += (31 - __clz(m)) * step;   // lane 0's offset is not above r
+                hi = min(hi, lo + step);
             }
+            if (lane == 0) ends[warp] = lo;
         }
-        int32_t has[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) has[u] = seq[u] >= 0 ? __ldcg(p.lens_out + seq[u]) : 0;
-        int32_t blk[4], place[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            pos[u] = place[u] = blk[u] = -1;
-            if (seq[u] >= 0) {   // the last of the sequence's new tokens is at has - 1
-                pos[u] = has[u] - static_cast<int32_t>(cu[seq[u] + 1] - (static_cast<uint32_t>(r0) + u));
-                const int32_t j = pos[u] / p.bs;
-                place[u] = pos[u] - j * p.bs;
-                blk[u] = __ldcg(p.bt + static_cast<int64_t>(seq[u]) * p.max_blocks + j);
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const bool bad = seq[u] >= 0 && (blk[u] < 0 || blk[u] >= p.N);
-            if (bad) atomicOr(p.err, KVC_EBIT_BAD_BLOCK);
-            s[u] = seq[u] < 0 || bad ? -1 : blk[u] * p.bs + place[u];
-        }
-        if (wide && r0 + 4 <= p.n_rows) {
-            *reinterpret_cast<int4 *>(p.slots + r0) = make_int4(s[0], s[1], s[2], s[3]);
-            if (p.positions) *reinterpret_cast<int4 *>(p.positions + r0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
-            if (p.seqs) *reinterpret_cast<int4 *>(p.seqs + r0) = make_int4(seq[0], seq[1], seq[2], seq[3]);
-        } else {
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-                if (r0 + u < p.n_rows) {
-                    p.slots[r0 + u] = s[u];
-                    if (p.positions) p.positions[r0 + u] = pos[u];
-                    if (p.seqs) p.seqs[r0 + u] = seq[u];
-                }
+        __syncthreads();
+        b0 = ends[0];
+        n = ends[1] - b0 + 1;
+        if (n <= kRowsCta) {
+            for (int i = tid; i <= n; i += kRowsThreads) cu[i] = static_cast<uint32_t>(__ldcg(p.cu + b0 + i));
+            __syncthreads();
+        } else {   // many sequences without rows among them
+            offsets = reinterpret_cast<const uint32_t *>(p.cu) + b0;
         }
     }
-    // no CTA reads another's shared memory after the barrier above
+    if (r0 + 4 * tid < p.n_rows) write_rows(p, r0 + 4 * tid, total, offsets, b0, n, maps_aligned(p));
 }
 
 template <int THREADS, bool CLUSTER>
@@ -300,6 +361,26 @@ static kvc_status launch_plan(const PlanParams &p, cudaStream_t stream)
     cfg.attrs = attr;
     cfg.numAttrs = CLUSTER ? 2 : 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, plan_kernel<THREADS, CLUSTER>, p);
+    if (e != cudaSuccess) return cuda_status(e);
+    g_launches.fetch_add(1, std::memory_order_relaxed);
+    return KVC_OK;
+}
+
+// Rows that the cluster's eight SMs write themselves; more go to a kernel of their own.
+constexpr int kRowsHere = 8192;
+
+static kvc_status launch_rows(const PlanParams &p, cudaStream_t stream)
+{
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((p.n_rows + kRowsCta - 1) / kRowsCta));
+    cfg.blockDim = dim3(kRowsThreads);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, plan_rows_kernel, p);
     if (e != cudaSuccess) return cuda_status(e);
     g_launches.fetch_add(1, std::memory_order_relaxed);
     return KVC_OK;
@@ -346,6 +427,9 @@ extern "C" kvc_status kvc_plan_step(kvc_pool *pool, int32_t *block_tables, int32
     p.seqs = seq_ids;
     p.n_rows = static_cast<int32_t>(n_rows);
     p.err = pool->err;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool one = B <= 512 && n_rows <= 1024;   // 1024 rows are one pass of 256 threads
-    return one ? launch_plan<256, false>(p, static_cast<cudaStream_t>(stream)) : launch_plan<1024, true>(p, static_cast<cudaStream_t>(stream));
+    p.rows_here = n_rows <= kRowsHere;
+    const kvc_status planned = one ? launch_plan<256, false>(p, s) : launch_plan<512, true>(p, s);
+    return planned != KVC_OK || p.rows_here ? planned : launch_rows(p, s);
 }
