@@ -227,27 +227,24 @@ __global__ void __launch_bounds__(kBoundsThreads, KIND == KV_BF16 && D == 128 ? 
 }
 
 // ------------------------------------------------------------------ selection
-// grid (C x rows, KV head), clusters of C CTAs along x.  CTA c of a cluster scores the c-th part of the row's blocks
-// into keys in shared memory; the k-th largest key is found digit by digit over the cluster's histograms, and each
-// CTA writes its part of the list in order.
+// One row and KV head, by a cluster of cs CTAs (a power of two up to 8).  CTA `rank` scores its part of the row's blocks
+// into `keys` in shared memory.  Lists of up to 128 blocks are ranked from a few candidates; for longer ones, and for
+// many equal keys, the k-th largest key is found digit by digit over the cluster's histograms, and each CTA writes its
+// part of the list in order.
 template <int D>
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams p)
+__device__ __forceinline__ void select_row(const SelectParams &p, const int64_t row, const int h, const int cs, const int rank, uint32_t *keys)
 {
     constexpr int LPR = D / 16;          // lanes per record: 16 channels each
     constexpr int RPS = 32 / LPR;        // records per step
     constexpr int U = 4;                 // steps at a time
-    extern __shared__ uint32_t keys[];
     __shared__ __align__(16) uint32_t qw[32][2][D / 4];   // the group's queries: positive parts, negative parts, int8
     __shared__ __align__(16) uint32_t hist[2][256], sum[256];
-    __shared__ Candidates cand;
+    __shared__ __align__(16) uint32_t cand_key[kCandRow + 4];
+    __shared__ int32_t cand_block[kCandRow];
     __shared__ uint32_t n_cand, limit;
     __shared__ uint32_t top_bits, pick_bin, pick_above, n_valid, n_gt, n_eq;
     __shared__ uint32_t warp_gt[kSelWarps], warp_eq[kSelWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int cs = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
-    const int64_t row = blockIdx.x / static_cast<unsigned>(cs);
-    const int h = blockIdx.y;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int seq = p.seqs ? __ldg(p.seqs + row) : static_cast<int>(row);
     const int pos = __ldg(p.positions + row);
     uint4 x[2];   // the group's queries: 16 bytes of each thread, twice
@@ -381,7 +378,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
 
     // ---- short lists: the largest keys of 256 groups over the cluster; at least top_k keys reach what top_k of those
     // reach, and not many more.  The first CTA ranks those few by counting.
-    if (p.top_k <= 128 && nb <= kPickMost) {
+    if (p.top_k <= kShortList) {
         uint32_t m = 0u;
         for (int i = tid; i < n; i += kSelThreads) m = max(m, keys[i]);
         for (int o = 1; o < cs; o <<= 1) m = max(m, __shfl_xor_sync(kFull, m, o));   // cs a power of two: 256 / cs groups
@@ -416,23 +413,24 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
             for (int i = tid; i < n; i += kSelThreads) {
                 const uint32_t k = keys[i];
                 if (k >= lim) {
-                    if (at < kCand) {
-                        cluster_st(cluster_addr(smem_u32(&cand.key[at]), 0), k);
-                        cluster_st(cluster_addr(smem_u32(&cand.block[at]), 0), static_cast<uint32_t>(j0 + i));
+                    if (at < kCandRow) {
+                        cluster_st(cluster_addr(smem_u32(&cand_key[at]), 0), k);
+                        cluster_st(cluster_addr(smem_u32(&cand_block[at]), 0), static_cast<uint32_t>(j0 + i));
                     }
                     ++at;
                 }
             }
         if (cs > 1) cluster_sync();
         else __syncthreads();
-        if (n_cand <= kSelThreads) {
+        static_assert(kCandRow == kSelThreads, "a thread ranks a candidate");
+        if (n_cand <= kCandRow) {
             if (rank == 0) {
                 const int c = static_cast<int>(n_cand);
-                if (tid < 4) cand.key[c + tid] = 0u;   // whole fours (kCand is more than kSelThreads + 4)
+                if (tid < 4) cand_key[c + tid] = 0u;   // whole fours
                 __syncthreads();
-                const uint32_t k = tid < c ? cand.key[tid] : 0xFFFFFFFFu;
-                const int blk = tid < c ? cand.block[tid] : -1;
-                const uint4 *k4 = reinterpret_cast<const uint4 *>(cand.key);
+                const uint32_t k = tid < c ? cand_key[tid] : 0xFFFFFFFFu;
+                const int blk = tid < c ? cand_block[tid] : -1;
+                const uint4 *k4 = reinterpret_cast<const uint4 *>(cand_key);
                 int larger = 0;
 #pragma unroll 8
                 for (int i = 0; i < (c + 3) / 4; ++i) {
@@ -442,7 +440,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
                 bool pick = tid < c && larger < p.top_k;
                 if (__syncthreads_count(pick) > p.top_k) {   // equal keys at the border: the lower blocks
                     if (pick)
-                        for (int i = 0; i < c; ++i) larger += cand.key[i] == k && cand.block[i] < blk;
+                        for (int i = 0; i < c; ++i) larger += cand_key[i] == k && cand_block[i] < blk;
                     pick = pick && larger < p.top_k;
                 }
                 sum[tid] = pick ? static_cast<uint32_t>(blk) : 0x7FFFFFFFu;
@@ -580,10 +578,49 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
     if (cs > 1) cluster_sync();   // a CTA's shared memory stays until the others have read it
 }
 
+// grid (C x rows, KV head), clusters of C CTAs along x
+template <int D>
+__global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams p)
+{
+    extern __shared__ uint32_t keys[];
+    const unsigned cs = cluster_size();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    select_row<D>(p, blockIdx.x / cs, blockIdx.y, static_cast<int>(cs), static_cast<int>(cluster_rank()), keys);
+}
+
+// The rows that select_tiles left unlisted.  grid (8 rows, KV head)
+constexpr int kRestRows = 8;
+template <int D>
+__global__ void __launch_bounds__(kSelThreads) select_rest_kernel(const SelectParams p, const int64_t rows)
+{
+    extern __shared__ uint32_t keys[];
+    const int64_t r0 = static_cast<int64_t>(blockIdx.x) * kRestRows;
+    const int lane = threadIdx.x & 31;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int64_t r = r0 + lane;
+    const bool mine = lane < kRestRows && r < rows && p.lists[(r * p.H_KV + blockIdx.y) * p.top_k] == kUnlisted;
+    uint32_t todo = __ballot_sync(kFull, mine);
+    __syncthreads();   // no row is written before every warp has looked
+    for (; todo; todo &= todo - 1u) {
+        select_row<D>(p, r0 + __ffs(todo) - 1, blockIdx.y, 1, 0, keys);
+        __syncthreads();
+    }
+}
+
 static bool aligned(const void *ptr, size_t a) { return (reinterpret_cast<uintptr_t>(ptr) & (a - 1)) == 0; }
 
 // Rows per sequence, on average, from which on rows are scored together.
 constexpr int kTileRuns = 8;
+
+template <int D>
+static kvc_status launch_rest(const SelectParams &p, int64_t rows, cudaStream_t stream)
+{
+    struct Tag {};
+    const DecodeKernel k = configured<Tag>(reinterpret_cast<const void *>(&select_rest_kernel<D>), 4 * kSelKeys, kSelThreads, false);
+    if (k.ctas_per_sm <= 0) return KVC_ERR_CUDA;
+    return launch(&select_rest_kernel<D>, dim3(static_cast<unsigned>((rows + kRestRows - 1) / kRestRows), p.H_KV), kSelThreads,
+                  4 * static_cast<size_t>(p.max_blocks), 1, stream, p, rows);
+}
 
 template <int D>
 static kvc_status launch_select(const SelectParams &p, int64_t rows, int sms, cudaStream_t stream)
@@ -687,9 +724,10 @@ extern "C" kvc_status kvc_select_blocks(kvc_pool *pool, int32_t layer, const voi
     p.lists = selected;
     p.err = pool->err;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (seq_ids && n_rows >= kTileRuns * static_cast<int64_t>(B)) {
-        const kvc_status tiled = select_tiles(p, pool->D, n_rows, pool->num_sms, s);
-        if (tiled != KVC_ERR_UNSUPPORTED) return tiled;
+    if (seq_ids && n_rows >= kTileRuns * static_cast<int64_t>(B) && top_k <= kShortList && max_blocks <= kSelKeys) {
+        const kvc_status tiled = select_tiles(p, pool->D, n_rows, s);
+        if (tiled != KVC_OK) return tiled;
+        return pool->D == 64 ? launch_rest<64>(p, n_rows, s) : launch_rest<128>(p, n_rows, s);
     }
     return pool->D == 64 ? launch_select<64>(p, n_rows, pool->num_sms, s) : launch_select<128>(p, n_rows, pool->num_sms, s);
 }

@@ -33,6 +33,7 @@ struct SelectParams {
 constexpr int kSelThreads = 256;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelMostBlocks = 262144;
+constexpr int kShortList = 128;     // blocks of a list that is ranked from a few candidates
 constexpr int kSelKeys = 32768;     // keys that a CTA holds
 
 // Scores as unsigned numbers of the same order; 0 and ~0 are no finite score's.
@@ -65,26 +66,36 @@ struct Cut {
     uint32_t above, equal;
 };
 
-// One warp: the cut that lists `want` of more than `want` keys that are not 0.  count(m, c): this lane's keys >= m[i];
-// lo, hi: the least and the largest key below ~0; forced: the number of keys ~0.  SMALL: fewer than 1024 keys.
-template <bool SMALL, typename Count>
-__device__ __forceinline__ Cut find_cut(uint32_t want, uint32_t forced, uint32_t lo, uint32_t hi, Count count)
+// One warp: the cut that lists `want` of more than `want` keys that are not 0, S < 32 of them per lane in k (unused: 0).
+template <int S>
+__device__ __forceinline__ Cut find_cut(const uint32_t (&k)[S], uint32_t want)
 {
+    uint32_t lo = 0xFFFFFFFFu, hi = 0u, forced = 0u;
+#pragma unroll
+    for (int u = 0; u < S; ++u) {
+        const bool top = k[u] == 0xFFFFFFFFu;
+        forced += top;
+        lo = min(lo, k[u] == 0u ? 0xFFFFFFFFu : k[u]);
+        hi = max(hi, top ? 0u : k[u]);
+    }
+    forced = __reduce_add_sync(kFull, forced);
+    lo = __reduce_min_sync(kFull, lo);
+    hi = __reduce_max_sync(kFull, hi);
     if (forced >= want) return {0xFFFFFFFEu, 0u};   // the forced ones fill the list
     uint32_t n_hi = forced;   // keys > hi: fewer than wanted; keys >= lo: more
     for (int it = 0; lo < hi; ++it) {
         uint32_t m[3], c[3];
         quarter(lo, hi, it < 12, m);
-        count(m, c);
-        if constexpr (SMALL) {
-            const uint32_t all = __reduce_add_sync(kFull, c[0] | (c[1] << 10) | (c[2] << 20));
-            c[0] = all & 1023u;
-            c[1] = (all >> 10) & 1023u;
-            c[2] = all >> 20;
-        } else {
 #pragma unroll
-            for (int i = 0; i < 3; ++i) c[i] = __reduce_add_sync(kFull, c[i]);
+        for (int i = 0; i < 3; ++i) {
+            c[i] = 0u;
+#pragma unroll
+            for (int u = 0; u < S; ++u) c[i] += k[u] >= m[i];
         }
+        const uint32_t all = __reduce_add_sync(kFull, c[0] | (c[1] << 10) | (c[2] << 20));   // 32 S < 1024
+        c[0] = all & 1023u;
+        c[1] = (all >> 10) & 1023u;
+        c[2] = all >> 20;
 #pragma unroll
         for (int i = 0; i < 3; ++i)
             if (c[i] == want) return {m[i] - 1u, 0u};
@@ -107,40 +118,24 @@ __device__ __forceinline__ Cut find_cut(uint32_t want, uint32_t forced, uint32_t
 }
 
 // Keys that a row's list is chosen from, in any order: those at or above a limit that at least top_k keys reach.
-constexpr int kCand = 384;
-struct alignas(16) Candidates {
-    uint32_t key[kCand];
-    int32_t block[kCand];
-};
-constexpr int kPickMost = 2 * kCand * 32;   // blocks of a row that pick_row serves: a bit each in the candidates' place
+constexpr int kCandRow = 256;
+constexpr int kCandWords = 2 * kCandRow;   // of a row: keys, then blocks
 
-// One warp: the list of a row from n candidates, n <= 32 S, of `blocks` blocks, in order of the blocks.
+// One warp: the list of a row from n <= 32 S candidates of `blocks` blocks, the whole of them when n <= top_k.
 template <int S>
-__device__ __forceinline__ void list_candidates(Candidates &s, int n, int blocks, int32_t *list, int top_k, int lane)
+__device__ __forceinline__ void list_candidates(uint32_t *key, int n, int blocks, int32_t *list, int top_k, int lane)
 {
-    uint32_t k[S], forced = 0u, lo = 0xFFFFFFFFu, hi = 0u;
+    const int32_t *block = reinterpret_cast<const int32_t *>(key) + kCandRow;
+    uint32_t k[S];
     int32_t blk[S];
 #pragma unroll
     for (int u = 0; u < S; ++u) {
         const bool in = 32 * u + lane < n;
-        k[u] = in ? s.key[32 * u + lane] : 0u;
-        blk[u] = in ? s.block[32 * u + lane] : 0;
-        const bool top = k[u] == 0xFFFFFFFFu;
-        forced += top;
-        lo = min(lo, in ? k[u] : 0xFFFFFFFFu);
-        hi = max(hi, top ? 0u : k[u]);
+        k[u] = in ? key[32 * u + lane] : 0u;
+        blk[u] = in ? block[32 * u + lane] : 0;
     }
     Cut cut{0u, 0u};
-    if (n > top_k)
-        cut = find_cut<true>(static_cast<uint32_t>(top_k), __reduce_add_sync(kFull, forced), __reduce_min_sync(kFull, lo),
-                             __reduce_max_sync(kFull, hi), [&](const uint32_t (&m)[3], uint32_t (&c)[3]) {
-#pragma unroll
-                                 for (int i = 0; i < 3; ++i) {
-                                     c[i] = 0u;
-#pragma unroll
-                                     for (int u = 0; u < S; ++u) c[i] += k[u] >= m[i];
-                                 }
-                             });
+    if (n > top_k) cut = find_cut(k, static_cast<uint32_t>(top_k));
     uint32_t same = 0u;
 #pragma unroll
     for (int u = 0; u < S; ++u) same += k[u] != 0u && k[u] == cut.above;
@@ -152,94 +147,48 @@ __device__ __forceinline__ void list_candidates(Candidates &s, int n, int blocks
         if (cut.equal != 0u && k[u] != 0u && k[u] == cut.above) {
             uint32_t before = 0u;   // equal ones in lower blocks
             if (!all_same)
-                for (int i = 0; i < n; ++i) before += s.key[i] == cut.above && s.block[i] < blk[u];
+                for (int i = 0; i < n; ++i) before += key[i] == cut.above && block[i] < blk[u];
             pick[u] = before < cut.equal;
         }
     }
-    // a bit for each block, then the blocks in order of the bits
     __syncwarp();
-    uint32_t *bits = s.key;
-    const int words = blocks / 32, per = (words + 31) / 32;
-    for (int i = lane; i < words; i += 32) bits[i] = 0u;
-    __syncwarp();
-#pragma unroll
-    for (int u = 0; u < S; ++u)
-        if (pick[u]) atomicOr(&bits[blk[u] >> 5], 1u << (blk[u] & 31));
-    __syncwarp();
-    int mine = 0;
-    for (int i = 0; i < per; ++i) mine += lane * per + i < words ? __popc(bits[lane * per + i]) : 0;
-    int at = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(kFull, at, o);
-        if (lane >= o) at += y;
-    }
-    const int total = __shfl_sync(kFull, at, 31);
-    at -= mine;
-    for (int i = 0; i < per && lane * per + i < words; ++i)
-        for (uint32_t w = bits[lane * per + i]; w; w &= w - 1u) list[at++] = (lane * per + i) * 32 + __ffs(w) - 1;
-    for (int i = total + lane; i < top_k; i += 32) list[i] = -1;
-}
-
-// One warp: the same for n <= 128 candidates by counting, for each, the larger ones and then the listed ones in lower
-// blocks: more additions than a search, but no chain of them.
-__device__ __forceinline__ void list_few(Candidates &s, int n, int blocks, int32_t *list, int top_k, int lane)
-{
-    constexpr int S = 4;
-    uint32_t k[S];
-    int32_t blk[S], larger[S] = {0, 0, 0, 0};
-    const int n4 = (n + 3) / 4;
-    if (lane < 4 * n4 - n) {   // whole fours: keys of 0, blocks past all
-        s.key[n + lane] = 0u;
-        s.block[n + lane] = 0x7FFFFFFF;
-    }
-    __syncwarp();
-#pragma unroll
-    for (int u = 0; u < S; ++u) {
-        const bool in = 32 * u + lane < n;
-        k[u] = in ? s.key[32 * u + lane] : 0xFFFFFFFFu;
-        blk[u] = in ? s.block[32 * u + lane] : -1;
-    }
-    const uint4 *k4 = reinterpret_cast<const uint4 *>(s.key);
-#pragma unroll 4
-    for (int j = 0; j < n4; ++j) {
-        const uint4 v = k4[j];
-#pragma unroll
-        for (int u = 0; u < S; ++u) larger[u] += (v.x > k[u]) + (v.y > k[u]) + (v.z > k[u]) + (v.w > k[u]);
-    }
-    bool pick[S];
-    int picks = 0;
-#pragma unroll
-    for (int u = 0; u < S; ++u) {
-        pick[u] = blk[u] >= 0 && larger[u] < top_k;
-        picks += pick[u];
-    }
-    if (__reduce_add_sync(kFull, picks) > top_k) {   // equal keys at the border: the lower blocks
-        list_candidates<S>(s, n, blocks, list, top_k, lane);
-        return;
-    }
-    __syncwarp();
-    int total = 0;
-#pragma unroll
-    for (int u = 0; u < S; ++u) {   // the listed blocks, in the keys' place
-        const uint32_t m = __ballot_sync(kFull, pick[u]);
-        if (pick[u]) s.key[total + __popc(m & ((1u << lane) - 1u))] = static_cast<uint32_t>(blk[u]);
-        total += __popc(m);
-    }
-    const int t4 = (total + 3) / 4;
-    if (lane < 4 * t4 - total) s.key[total + lane] = 0x7FFFFFFFu;
-    __syncwarp();
-    int at[S] = {0, 0, 0, 0};
-#pragma unroll 4
-    for (int j = 0; j < t4; ++j) {
-        const uint4 v = k4[j];
+    const int words = (blocks + 31) / 32, per = (words + 31) / 32;
+    int total;
+    if (words <= kCandWords) {   // a bit for each block in the candidates' place, then the blocks in order of the bits
+        for (int i = lane; i < words; i += 32) key[i] = 0u;
+        __syncwarp();
 #pragma unroll
         for (int u = 0; u < S; ++u)
-            at[u] += (static_cast<int>(v.x) < blk[u]) + (static_cast<int>(v.y) < blk[u]) + (static_cast<int>(v.z) < blk[u]) + (static_cast<int>(v.w) < blk[u]);
-    }
+            if (pick[u]) atomicOr(&key[blk[u] >> 5], 1u << (blk[u] & 31));
+        __syncwarp();
+        int mine = 0;
+        for (int i = 0; i < per; ++i) mine += lane * per + i < words ? __popc(key[lane * per + i]) : 0;
+        int at = mine;
 #pragma unroll
-    for (int u = 0; u < S; ++u)
-        if (pick[u]) list[at[u]] = blk[u];
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(kFull, at, o);
+            if (lane >= o) at += y;
+        }
+        total = __shfl_sync(kFull, at, 31);
+        at -= mine;
+        for (int i = 0; i < per && lane * per + i < words; ++i)
+            for (uint32_t w = key[lane * per + i]; w; w &= w - 1u) list[at++] = (lane * per + i) * 32 + __ffs(w) - 1;
+    } else {   // too many blocks for that: each listed one counts those before it
+        total = 0;
+#pragma unroll
+        for (int u = 0; u < S; ++u) {
+            const uint32_t m = __ballot_sync(kFull, pick[u]);
+            if (pick[u]) key[total + __popc(m & ((1u << lane) - 1u))] = static_cast<uint32_t>(blk[u]);
+            total += __popc(m);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int u = 0; u < S; ++u) {
+            int at = 0;
+            for (int i = 0; i < total; ++i) at += static_cast<int>(key[i]) < blk[u];
+            if (pick[u]) list[at] = blk[u];
+        }
+    }
     for (int i = total + lane; i < top_k; i += 32) list[i] = -1;
 }
 
@@ -284,91 +233,9 @@ __device__ __forceinline__ uint32_t reach_limit(const uint32_t (&v)[S], uint32_t
     return lo;
 }
 
-// One warp: writes the list of a row from its keys k[0 .. n) in shared memory (n a multiple of 128, unused ones 0).
-__device__ __forceinline__ void pick_row(const uint32_t *k, int n, Candidates &s, int32_t *list, int top_k, int lane)
-{
-    const uint4 *k4 = reinterpret_cast<const uint4 *>(k);
-    // the largest keys of 256 groups: at least top_k keys reach what top_k of those reach, and not many more
-    if (top_k <= 128) {
-        uint32_t m[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-#pragma unroll 4
-        for (int i = lane; i < n / 4; i += 64) {
-            const uint4 v = k4[i], w = i + 32 < n / 4 ? k4[i + 32] : make_uint4(0u, 0u, 0u, 0u);
-            m[0] = max(m[0], v.x), m[1] = max(m[1], v.y), m[2] = max(m[2], v.z), m[3] = max(m[3], v.w);
-            m[4] = max(m[4], w.x), m[5] = max(m[5], w.y), m[6] = max(m[6], w.z), m[7] = max(m[7], w.w);
-        }
-        const uint32_t limit = max(reach_limit(m, static_cast<uint32_t>(top_k)), 1u);
-        int mine = 0;
-#pragma unroll 4
-        for (int i = lane; i < n / 4; i += 32) {
-            const uint4 v = k4[i];
-            mine += (v.x >= limit) + (v.y >= limit) + (v.z >= limit) + (v.w >= limit);
-        }
-        int at = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(kFull, at, o);
-            if (lane >= o) at += y;
-        }
-        const int c = __shfl_sync(kFull, at, 31);
-        if (c <= kCand) {
-            at -= mine;
-#pragma unroll 4
-            for (int i = lane; i < n / 4; i += 32) {
-                const uint4 v = k4[i];
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    if (w[u] >= limit) {
-                        s.key[at] = w[u];
-                        s.block[at++] = 4 * i + u;
-                    }
-            }
-            __syncwarp();
-            if (c <= 128) list_few(s, c, n, list, top_k, lane);
-            else list_candidates<kCand / 32>(s, c, n, list, top_k, lane);
-            return;
-        }
-    }
-    // long lists, and runs of equal keys: the cut by counting all keys
-    uint32_t valid = 0u, forced = 0u, lo = 0xFFFFFFFFu, hi = 0u;
-    for (int i = lane; i < n; i += 32) {
-        const uint32_t w = k[i];
-        const bool top = w == 0xFFFFFFFFu;
-        valid += w != 0u;
-        forced += top;
-        lo = min(lo, w == 0u ? 0xFFFFFFFFu : w);
-        hi = max(hi, top ? 0u : w);
-    }
-    Cut cut{0u, 0u};
-    if (__reduce_add_sync(kFull, valid) > static_cast<uint32_t>(top_k))
-        cut = find_cut<false>(static_cast<uint32_t>(top_k), __reduce_add_sync(kFull, forced), __reduce_min_sync(kFull, lo),
-                              __reduce_max_sync(kFull, hi), [&](const uint32_t (&m)[3], uint32_t (&c)[3]) {
-                                  c[0] = c[1] = c[2] = 0u;
-                                  for (int i = lane; i < n / 4; i += 32) {
-                                      const uint4 v = k4[i];
-#pragma unroll
-                                      for (int x = 0; x < 3; ++x) c[x] += (v.x >= m[x]) + (v.y >= m[x]) + (v.z >= m[x]) + (v.w >= m[x]);
-                                  }
-                              });
-    const uint32_t below = (1u << lane) - 1u;
-    uint32_t g0 = 0u, e0 = 0u;
-    for (int i = 0; i < n; i += 32) {
-        const uint32_t w = k[i + lane];
-        const bool gt = w > cut.above, eq = w != 0u && w == cut.above;
-        const uint32_t mg = __ballot_sync(kFull, gt), me = __ballot_sync(kFull, eq);
-        if ((mg | me) == 0u) continue;
-        const uint32_t ge = g0 + __popc(mg & below), ee = e0 + __popc(me & below);
-        if (gt || (eq && ee < cut.equal)) list[ge + min(ee, cut.equal)] = i + lane;
-        g0 += __popc(mg);
-        e0 += __popc(me);
-    }
-    for (int i = static_cast<int>(g0 + min(e0, cut.equal)) + lane; i < top_k; i += 32) list[i] = -1;
-}
-
 // A launch that may start while the kernel before it drains, in clusters of `cluster` CTAs along x.
-template <typename P>
-kvc_status launch(void (*fn)(P), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t stream, const P &p)
+template <typename... P, typename... A>
+kvc_status launch(void (*fn)(P...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t stream, const A &...args)
 {
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -383,15 +250,18 @@ kvc_status launch(void (*fn)(P), dim3 grid, int threads, size_t smem, int cluste
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = cluster > 1 ? 2 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, args...);
     if (e != cudaSuccess) return cuda_status(e);
     g_launches.fetch_add(1, std::memory_order_relaxed);
     return KVC_OK;
 }
 
 
-// Scores on the tensor cores for runs of rows of one sequence (kvc_select_tc.cu); KVC_ERR_UNSUPPORTED, with nothing
-// launched, for tables that it has no room for.
-kvc_status select_tiles(const SelectParams &p, int D, int64_t rows, int sms, cudaStream_t stream);
+// What a list starts with while it waits for select_rest.
+constexpr int32_t kUnlisted = -2;
+
+// Scores on the tensor cores for runs of rows of one sequence (kvc_select_tc.cu), lists of up to 128 blocks.  Rows whose
+// candidates are too many (equal scores) are left unlisted.
+kvc_status select_tiles(const SelectParams &p, int D, int64_t rows, cudaStream_t stream);
 
 }  // namespace kvc

@@ -5,12 +5,15 @@
 // product of length 2 d:  sum_i Q_i (Q_i > 0 ? hi_i : lo_i) = <(Q+, Q-), (hi, lo)>.  Codes and queries are integers
 // up to 127, exact in f16; products are below 2^14 and sums below 2^21, exact in the fp32 accumulator in any order.
 //
-// A cluster of C CTAs takes RT rows of one KV head; the CTAs share the blocks in tiles of 128 (tile t to CTA t mod C).
-// Per tile: D[128 blocks x RT g query columns] = A[128 x 2d] B[2d x RT g].  The blocks are the M rows, so that a
-// thread of the epilogue holds one block's products with every query head and takes their maximum without a shuffle.
+// A CTA takes RT rows of one KV head and walks all blocks in tiles of 128, twice:
+//   D[128 blocks x RT g query columns] = A[128 x 2d] B[2d x RT g].
+// The blocks are the M rows, so that a thread of the epilogue holds one block's products with every query head and
+// takes their maximum without a shuffle.  Keeping a score for every row and block would fill shared memory and keep
+// the rest of the SM idle while rows are finished; multiplying again costs little.  So the first walk only keeps the
+// largest score of 256 groups of blocks per row: the top_k-th of those is a limit that at least top_k blocks reach.
+// The second walk collects the few blocks that reach it, and a warp per row ranks them by counting.
 // B (the queries) stays in shared memory; A is read as int8 into registers while the tile before is multiplied,
-// widened to f16 and stored in the 128-byte swizzle.  The keys stay in shared memory, and each row is finished by one
-// warp: it gathers the row's keys from the cluster, narrows the k-th largest by counting, and writes the list.
+// widened to f16 and stored in the 128-byte swizzle.
 //
 // A tile of rows may hold several sequences (runs): they are done one after the other.
 #include <algorithm>
@@ -20,12 +23,14 @@
 
 namespace kvc {
 
-constexpr int kStThreads = 512;
+constexpr int kStThreads = 512;   // the threads that widen and read; one warp more issues the products
 constexpr int kStWarps = kStThreads / 32;
+constexpr int kStCta = kStThreads + 32;
 constexpr int kStTile = 128;       // blocks per MMA
 constexpr int kStCols = 128;       // query columns at most
 constexpr int kStRows = 32;        // rows at most
-constexpr int kStPick = 8;         // warps that finish rows
+constexpr int kStChunk = 16;       // tiles whose table entries and units are looked up at a time
+constexpr int kStGroups = 256;     // per row: a lane's place in its tile, even and odd tiles apart
 
 template <int D>
 struct StCfg {
@@ -33,7 +38,12 @@ struct StCfg {
     static constexpr int BANDS = K / 64;            // 128-byte bands of f16
     static constexpr int BAND = 128 * 128;          // bytes of a band of 128 rows
     static constexpr int A = BANDS * BAND;          // bytes
-    static constexpr int KEYS = 2 * A;              // offset of the keys: after A and B
+    static constexpr int CAND = 2 * A;              // after A and B: groups' maxima, then candidates
+    static constexpr int ROW_CAND = kCandWords * 4;
+    static constexpr int PHYS = CAND + kStRows * ROW_CAND;   // blocks of a chunk's tiles
+    static constexpr int UNIT = PHYS + kStChunk * kStTile * 4;
+    static constexpr int SMEM = 1024 /* alignment */ + UNIT + kStChunk * kStTile * 4;
+    static_assert(ROW_CAND >= kStGroups * 4, "the groups' maxima lie in the candidates' place");
     static constexpr int CPR = K / 16;              // 16-byte chunks per record
     static constexpr int STEP = kStThreads / CPR;   // records per pass of the CTA's threads
     static constexpr int U = kStTile / STEP;        // passes per tile
@@ -43,7 +53,6 @@ struct SelectTileParams {
     SelectParams s;
     int64_t rows;
     int32_t RT;            // rows per tile
-    int32_t tiles;         // tiles of blocks per CTA that the keys have room for
 };
 
 // Two pairs of f16 from four int8 codes, exact.
@@ -56,33 +65,34 @@ __device__ __forceinline__ uint2 s8x4_to_f16(uint32_t x)
     return r;
 }
 
-// grid (C x row tiles, KV head), clusters of C CTAs along x; one CTA per SM.
+// grid (row tiles, KV head); one CTA per SM.
 // G: query heads per KV head where that divides 32 and is at most 8, else 0 (any).
 template <int D, int G>
-__global__ void __launch_bounds__(kStThreads, 1) select_tile_kernel(const SelectTileParams tp)
+__global__ void __launch_bounds__(kStCta, 1) select_tile_kernel(const SelectTileParams tp)
 {
     using C = StCfg<D>;
     const SelectParams &p = tp.s;
     extern __shared__ uint8_t st_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(st_raw) + 1023) & ~uintptr_t(1023));
-    Candidates *cand = reinterpret_cast<Candidates *>(smem + C::KEYS);                     // [kStPick]
-    int32_t *phys_s = reinterpret_cast<int32_t *>(smem + C::KEYS + kStPick * sizeof(Candidates));   // [tile of this CTA][128]
-    float *unit_s = reinterpret_cast<float *>(phys_s + tp.tiles * kStTile);                // [tile of this CTA][128]
-    uint32_t *keys = reinterpret_cast<uint32_t *>(unit_s + tp.tiles * kStTile);            // [row][tile of this CTA][128]
-    __shared__ int32_t row_seq[kStRows], row_nb[kStRows];            // sequence (-1: no work), blocks of the row
-    __shared__ uint64_t bar;
+    uint32_t *groups = reinterpret_cast<uint32_t *>(smem + C::CAND);     // [row][kStGroups]
+    int32_t *phys_s = reinterpret_cast<int32_t *>(smem + C::PHYS);       // [tile of the chunk][128]
+    float *unit_s = reinterpret_cast<float *>(smem + C::UNIT);
+    auto cand = [&](int r) { return reinterpret_cast<uint32_t *>(smem + C::CAND + r * C::ROW_CAND); };   // keys, blocks
+    __shared__ int32_t row_seq[kStRows], row_nb[kStRows];                // sequence (< 0: no work), blocks of the row
+    __shared__ float row_limit[kStRows];
+    __shared__ int32_t row_count[kStRows];                               // candidates
+    __shared__ uint64_t full_bar, done_bar;   // A is written; the product is there (and A free)
     __shared__ uint32_t tmem_base;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, h = blockIdx.y;
-    const int cs = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
-    const int64_t r0 = static_cast<int64_t>(blockIdx.x / static_cast<unsigned>(cs)) * tp.RT;
+    const int64_t r0 = static_cast<int64_t>(blockIdx.x) * tp.RT;
     const int cols = (tp.RT * p.g + 15) & ~15;
-    const int stride = tp.tiles * kStTile;   // keys of a row
     if (warp == 0) {
         tmem_alloc(smem_u32(&tmem_base), 2 * kStCols);
         tmem_relinquish();
     }
     if (tid == 0) {
-        mbar_init(smem_u32(&bar), 1);
+        mbar_init(smem_u32(&full_bar), kStWarps);
+        mbar_init(smem_u32(&done_bar), 1);
         fence_barrier_init();
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -95,7 +105,7 @@ __global__ void __launch_bounds__(kStThreads, 1) select_tile_kernel(const Select
             if (seq == -1 || pos == -1) {
                 seq = -1;
             } else if (seq < 0 || seq >= p.B || pos < 0 || pos / p.bs >= p.max_blocks) {
-                if (rank == 0 && h == 0) atomicOr(p.err, KVC_EBIT_RANGE);
+                if (h == 0) atomicOr(p.err, KVC_EBIT_RANGE);
                 seq = -2;   // lists nothing
             } else {
                 nb = pos / p.bs + 1;
@@ -109,18 +119,6 @@ __global__ void __launch_bounds__(kStThreads, 1) select_tile_kernel(const Select
     tc_fence_after();
     const uint32_t tmem = tmem_base;
     const uint32_t a_base = smem_u32(smem), b_base = a_base + C::A;
-
-    // the first run's table entries, ahead of their use
-    int early = -1;
-    {
-        const int s = lane < tp.RT ? row_seq[lane] : -1;
-        const uint32_t live = __ballot_sync(kFull, s >= 0);
-        const int j = (rank + (tid / kStTile) * cs) * kStTile + tid % kStTile;
-        if (live) {
-            const int64_t at = static_cast<int64_t>(__shfl_sync(kFull, s, __ffs(live) - 1)) * p.max_blocks;
-            if (j < p.max_blocks) early = __ldg(p.bt + at + j);
-        }
-    }
 
     // ---- the rows' queries as whole numbers, positive parts then negative ones: a warp per row
     constexpr int KEEP = 2;   // chunks of a lane that stay in registers between the two passes
@@ -136,15 +134,15 @@ __global__ void __launch_bounds__(kStThreads, 1) select_tile_kernel(const Select
         }
     };
     uint4 next[KEEP];
-    fetch(warp, next);
-    for (int r = warp; r < tp.RT; r += kStWarps) {
+    if (warp < kStWarps) fetch(warp, next);
+    for (int r = warp; r < tp.RT && warp < kStWarps; r += kStWarps) {
         uint4 kept[KEEP];
 #pragma unroll
         for (int u = 0; u < KEEP; ++u) kept[u] = next[u];
         fetch(r + kStWarps, next);
         if (row_seq[r] == -2) {
             int32_t *list = p.lists + ((r0 + r) * p.H_KV + h) * p.top_k;
-            for (int i = rank * 32 + lane; i < p.top_k; i += 32 * cs) list[i] = -1;
+            for (int i = lane; i < p.top_k; i += 32) list[i] = -1;
         }
         if (row_seq[r] < 0) continue;
         float m = 0.f;
@@ -183,8 +181,7 @@ __global__ void __launch_bounds__(kStThreads, 1) select_tile_kernel(const Select
     const uint32_t idesc = tc_idesc_f16(128, cols, false, false, false);
     const uint64_t desc_a = tc_smem_desc(a_base, 16, 1024, kSwizzle128B), desc_b = tc_smem_desc(b_base, 16, 1024, kSwizzle128B);
     const int chunk = tid % C::CPR, rec0 = tid / C::CPR;
-    uint32_t phase = 0u;
-    bool begun = false;
+    uint32_t phase = 0u;   // of both barriers: a tile each
 
     const int lane_seq = lane < tp.RT ? row_seq[lane] : -3, lane_nb = lane < tp.RT ? row_nb[lane] : 0;   // RT <= 32
     for (int first = 0; first < tp.RT;) {   // runs of rows of one sequence
@@ -199,21 +196,7 @@ __global__ void __launch_bounds__(kStThreads, 1) select_tile_kernel(const Select
         const int most = __reduce_max_sync(kFull, mine_row ? lane_nb : 0), least = __reduce_min_sync(kFull, mine_row ? lane_nb : 0x7FFFFFFF);
         const int32_t *bt = p.bt + static_cast<int64_t>(seq) * p.max_blocks;
         const int n_tiles = (most + kStTile - 1) / kStTile;
-        const int mine = n_tiles > rank ? (n_tiles - rank + cs - 1) / cs : 0;
-
-        // the blocks and units of this CTA's tiles
-        for (int i = tid; i < mine * kStTile; i += kStThreads) {
-            const int j = (rank + (i / kStTile) * cs) * kStTile + i % kStTile;
-            int phys = j >= most ? -1 : (begun || i != tid ? __ldg(bt + j) : early);
-            if (j < most && (phys < 0 || static_cast<int64_t>(phys) >= p.N)) {
-                if (h == 0) atomicOr(p.err, KVC_EBIT_BAD_BLOCK);
-                phys = -1;
-            }
-            phys_s[i] = phys;
-            unit_s[i] = phys < 0 ? 0.f : __ldg(p.units + static_cast<int64_t>(phys) * p.H_KV + h);
-        }
-        begun = true;
-        __syncthreads();
+        int t0 = 0;   // the chunk's first tile
 
         // this thread's 16 bytes of U records of a tile
         uint4 raw[C::U];
@@ -238,65 +221,88 @@ __global__ void __launch_bounds__(kStThreads, 1) select_tile_kernel(const Select
                 sts128(base + sw128(row, c0 + 1 - flip), flip ? v0 : v1);
             }
         };
-        auto multiply = [&](int t) {
+        auto written = [&] {   // this warp's part of A is there, and it has read what it wanted of the tile before last
             fence_proxy_async_smem();
             tc_fence_before();
-            __syncthreads();
-            if (warp == 0) {
-                tc_fence_after();
-                const uint32_t d = tmem + (t & 1) * kStCols;
-#pragma unroll
-                for (int kk = 0; kk < C::K / 16; ++kk)
-                    tc_mma_f16_warp(d, tc_desc_advance(desc_a, (kk >> 2) * C::BAND + (kk & 3) * 32),
-                                    tc_desc_advance(desc_b, (kk >> 2) * C::BAND + (kk & 3) * 32), idesc, kk > 0 ? 1u : 0u);
-                tc_commit_warp(smem_u32(&bar));
-            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&full_bar));
         };
-        if (mine > 0) {
-            load(0);
-            widen();
-            multiply(0);
-        }
-        for (int t = 0; t < mine; ++t) {
-            if (t + 1 < mine) load(t + 1);
-            if (!mbar_wait_bounded(smem_u32(&bar), phase) && lane == 0) atomicOr(p.err, KVC_EBIT_TIMEOUT);
-            phase ^= 1u;
-            tc_fence_after();
-            if (t + 1 < mine) {
-                widen();
-                multiply(t + 1);
-            }
-            // a lane holds a block; warps w, w + 4, ... of its quarter take a part of the run's rows each
-            const int place = t * kStTile + 32 * (warp & 3) + lane, j = (rank + t * cs) * kStTile + 32 * (warp & 3) + lane;
-            const int phys = phys_s[place];
-            const float unit = unit_s[place];
-            // tiles between the forced blocks of every row look at no row's length
-            const bool plain = (rank + t * cs) * kStTile >= p.sink && (rank + t * cs + 1) * kStTile <= least - p.recent;
-            auto keep = [&](int r, float best) {
-                uint32_t key = score_key(best * unit);
-                if (!plain) {
-                    const int nb = row_nb[r];
-                    if (j < p.sink || j >= nb - p.recent) key = 0xFFFFFFFFu;
-                    if (j >= nb) key = 0u;
-                }
-                keys[r * stride + place] = phys < 0 ? 0u : key;
-            };
-            const uint32_t d = tmem + (t & 1) * kStCols + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
-            if constexpr (G > 0) {   // 32 columns are whole rows
-                constexpr int RPC = 32 / G;
-                for (int r = (first / RPC + (warp >> 2)) * RPC; r < end; r += (kStWarps / 4) * RPC) {
-                    uint32_t v[32];
-                    tmem_ld32(d + r * G, v);
-                    tmem_ld_wait(v);
-#pragma unroll
-                    for (int x = 0; x < RPC; ++x) {
-                        float best = __uint_as_float(v[x * G]);
-#pragma unroll
-                        for (int y = 1; y < G; ++y) best = fmaxf(best, __uint_as_float(v[x * G + y]));
-                        if (r + x >= first && r + x < end) keep(r + x, best);
+        // One walk over the blocks.  read(t, d): the epilogue of tile t, whose products stand at d in tensor memory.
+        auto walk = [&](bool report, auto read) {
+            for (t0 = 0; t0 < n_tiles; t0 += kStChunk) {
+                const int nt = min(kStChunk, n_tiles - t0);
+                __syncthreads();   // the chunk before is done with its table entries
+                for (int i = tid; i < nt * kStTile; i += kStCta) {
+                    const int j = t0 * kStTile + i;
+                    int phys = j < most ? __ldg(bt + j) : -1;
+                    if (j < most && (phys < 0 || static_cast<int64_t>(phys) >= p.N)) {
+                        if (report && h == 0) atomicOr(p.err, KVC_EBIT_BAD_BLOCK);
+                        phys = -1;
                     }
+                    phys_s[i] = phys;
+                    unit_s[i] = phys < 0 ? 0.f : __ldg(p.units + static_cast<int64_t>(phys) * p.H_KV + h);
                 }
-            } else {
+                __syncthreads();
+                if (warp == kStWarps) {
+                    for (int t = 0; t < nt; ++t, phase ^= 1u) {
+                        if (!mbar_wait_bounded(smem_u32(&full_bar), phase) && lane == 0) atomicOr(p.err, KVC_EBIT_TIMEOUT);
+                        tc_fence_after();
+                        const uint32_t d = tmem + (t & 1) * kStCols;
+#pragma unroll
+                        for (int kk = 0; kk < C::K / 16; ++kk)
+                            tc_mma_f16_warp(d, tc_desc_advance(desc_a, (kk >> 2) * C::BAND + (kk & 3) * 32),
+                                            tc_desc_advance(desc_b, (kk >> 2) * C::BAND + (kk & 3) * 32), idesc, kk > 0 ? 1u : 0u);
+                        tc_commit_warp(smem_u32(&done_bar));
+                    }
+                    continue;
+                }
+                load(0);
+                widen();
+                written();
+                for (int t = 0; t < nt; ++t) {
+                    if (t + 1 < nt) load(t + 1);
+                    if (!mbar_wait_bounded(smem_u32(&done_bar), phase) && lane == 0) atomicOr(p.err, KVC_EBIT_TIMEOUT);
+                    phase ^= 1u;
+                    tc_fence_after();
+                    if (t + 1 < nt) {
+                        widen();
+                        written();
+                    }
+                    read(t, tmem + (t & 1) * kStCols + (static_cast<uint32_t>(32 * (warp & 3)) << 16));
+                }
+            }
+            tc_fence_before();
+            __syncthreads();
+        };
+
+        // A lane holds a block of the tile; warps w, w + 4, ... of its quarter take a part of the rows each.  score(x, s):
+        // the score of row (warp / 4) RPC + x, -inf where the block is none of the row's, +inf where it is always listed.
+        constexpr int RPC = G > 1 ? 32 / G : 1;   // rows of 32 columns
+        const int in_tile = 32 * (warp & 3) + lane, row0 = (warp >> 2) * RPC;
+        auto scores = [&](int t, uint32_t d, auto score) {
+            const int j = (t0 + t) * kStTile + in_tile;
+            const float unit = unit_s[t * kStTile + in_tile], none = phys_s[t * kStTile + in_tile] < 0 ? -INFINITY : 0.f;
+            // tiles between the forced blocks of every row look at no row's length
+            const bool plain = (t0 + t) * kStTile >= p.sink && (t0 + t + 1) * kStTile <= least - p.recent;
+            auto edge = [&](int r, float s) {
+                const int nb = row_nb[r];
+                return j >= nb ? -INFINITY : (none == 0.f && (j < p.sink || j >= nb - p.recent) ? INFINITY : s);
+            };
+            if constexpr (G > 1) {
+                if (row0 >= tp.RT) return;
+                uint32_t v[32];
+                tmem_ld32(d + row0 * G, v);
+                tmem_ld_wait(v);
+#pragma unroll
+                for (int x = 0; x < RPC; ++x) {
+                    float best = __uint_as_float(v[x * G]);
+#pragma unroll
+                    for (int y = 1; y < G; ++y) best = fmaxf(best, __uint_as_float(v[x * G + y]));
+                    float s = fmaf(best, unit, none);   // 0, never -0
+                    if (!plain) s = edge(min(row0 + x, kStRows - 1), s);
+                    score(x, s);
+                }
+            } else {   // any group: x is the row itself
                 const int part = (end - first + kStWarps / 4 - 1) / (kStWarps / 4);
                 const int ra = min(end, first + (warp >> 2) * part), rb = min(end, ra + part);
                 float best = -INFINITY;
@@ -310,7 +316,9 @@ __global__ void __launch_bounds__(kStThreads, 1) select_tile_kernel(const Select
                         if (c0 + x < ra * p.g || r >= rb) continue;   // warp-uniform
                         best = fmaxf(best, __uint_as_float(v[x]));
                         if (--left == 0) {
-                            keep(r, best);
+                            float s = fmaf(best, unit, none);
+                            if (!plain) s = edge(r, s);
+                            score(r, s);
                             best = -INFINITY;
                             left = p.g;
                             ++r;
@@ -318,37 +326,97 @@ __global__ void __launch_bounds__(kStThreads, 1) select_tile_kernel(const Select
                     }
                 }
             }
-            tc_fence_before();
-        }
-        if (cs > 1) cluster_sync();
-        else __syncthreads();
+        };
+        auto to_key = [](float s) { return s == -INFINITY ? 0u : (s == INFINITY ? 0xFFFFFFFFu : score_key(s)); };
 
-        // ---- a warp per row: gather its keys into A's place, choose, write
-        const int n4 = n_tiles * kStTile;
-        const int lanes_of = min(kStPick, C::A / 4 / n4);   // rows at a time
-        if (warp < lanes_of) {
-            uint32_t *mine_k = reinterpret_cast<uint32_t *>(smem) + warp * n4;
-            for (int r = first + rank + cs * warp; r < end; r += cs * lanes_of) {
-                constexpr int UG = 8;
-                for (int i0 = lane; i0 < n4 / 4; i0 += 32 * UG) {
-                    float4 v[UG];
+        // ---- the largest key of every group, and of those the limit that top_k blocks reach
+        if constexpr (G > 1) {
+            float most_of[2][RPC];   // even and odd tiles
 #pragma unroll
-                    for (int u = 0; u < UG; ++u) {
-                        const int i = min(i0 + 32 * u, n4 / 4 - 1), t = i / (kStTile / 4);
-                        const uint32_t a = smem_u32(keys + r * stride + (t / cs) * kStTile + 4 * (i % (kStTile / 4)));
-                        v[u] = cluster_ld4(cluster_addr(a, t % cs));
-                    }
+            for (int x = 0; x < RPC; ++x) most_of[0][x] = most_of[1][x] = -INFINITY;
+            walk(true, [&](int t, uint32_t d) {
+                const bool odd = (t & 1) != 0;
+                scores(t, d, [&](int x, float s) {
+                    most_of[0][x] = fmaxf(most_of[0][x], odd ? -INFINITY : s);
+                    most_of[1][x] = fmaxf(most_of[1][x], odd ? s : -INFINITY);
+                });
+            });
 #pragma unroll
-                    for (int u = 0; u < UG; ++u)
-                        if (i0 + 32 * u < n4 / 4) reinterpret_cast<float4 *>(mine_k)[i0 + 32 * u] = v[u];
+            for (int x = 0; x < RPC; ++x)
+                if (warp < kStWarps && row0 + x >= first && row0 + x < end) {
+                    groups[(row0 + x) * kStGroups + in_tile] = to_key(most_of[0][x]);
+                    groups[(row0 + x) * kStGroups + kStTile + in_tile] = to_key(most_of[1][x]);
                 }
-                __syncwarp();
-                pick_row(mine_k, n4, cand[warp], p.lists + ((r0 + r) * p.H_KV + h) * p.top_k, p.top_k, lane);
-                __syncwarp();
+        } else {
+            for (int i = first * kStGroups + tid; i < end * kStGroups; i += kStCta) groups[i] = 0u;
+            walk(true, [&](int t, uint32_t d) {   // begins with a barrier; each place is this lane's own
+                scores(t, d, [&](int r, float s) {
+                    uint32_t *g = groups + r * kStGroups + (t & 1) * kStTile + in_tile;
+                    *g = max(*g, to_key(s));
+                });
+            });
+        }
+        __syncthreads();
+        for (int r = first + warp; r < end && warp < kStWarps; r += kStWarps) {
+            uint32_t v[kStGroups / 32];
+#pragma unroll
+            for (int u = 0; u < kStGroups / 32; ++u) v[u] = groups[r * kStGroups + 32 * u + lane];
+            const uint32_t limit = reach_limit(v, static_cast<uint32_t>(p.top_k));
+            if (lane == 0) {
+                row_limit[r] = limit == 0u ? -FLT_MAX : (limit == 0xFFFFFFFFu ? INFINITY : key_score(limit));
+                row_count[r] = 0;
             }
         }
-        if (cs > 1) cluster_sync();   // the others have read this CTA's keys
-        else __syncthreads();
+        __syncthreads();
+
+        // ---- the blocks that reach it
+        if constexpr (G > 1) {
+            float limit[RPC];
+#pragma unroll
+            for (int x = 0; x < RPC; ++x)   // nothing reaches a NaN: the rows of other runs
+                limit[x] = row0 + x >= first && row0 + x < end ? row_limit[row0 + x] : __uint_as_float(0x7FFFFFFFu);
+            const uint32_t counts = smem_u32(&row_count[row0 < kStRows ? row0 : 0]);
+            walk(false, [&](int t, uint32_t d) {
+                float hit[RPC];
+                uint32_t at[RPC];
+                scores(t, d, [&](int x, float s) { hit[x] = s; });
+                if (row0 >= tp.RT) return;
+#pragma unroll
+                for (int x = 0; x < RPC; ++x)   // all of the additions are on their way before the first is used
+                    asm volatile(
+                        "{\n\t.reg .pred p;\n\tsetp.ge.f32 p, %2, %3;\n\tmov.u32 %0, 0xffffffff;\n\t"
+                        "@p atom.shared.add.u32 %0, [%1], 1;\n\t}"
+                        : "=r"(at[x])
+                        : "r"(counts + 4 * x), "f"(hit[x]), "f"(limit[x])
+                        : "memory");
+#pragma unroll
+                for (int x = 0; x < RPC; ++x)
+                    if (at[x] < kCandRow) {
+                        cand(row0 + x)[at[x]] = to_key(hit[x]);
+                        cand(row0 + x)[kCandRow + at[x]] = static_cast<uint32_t>((t0 + t) * kStTile + in_tile);
+                    }
+            });
+        } else {
+            walk(false, [&](int t, uint32_t d) {
+                scores(t, d, [&](int r, float s) {
+                    if (s >= row_limit[r]) {
+                        const int at = atomicAdd(&row_count[r], 1);
+                        if (at < kCandRow) {
+                            cand(r)[at] = to_key(s);
+                            cand(r)[kCandRow + at] = static_cast<uint32_t>((t0 + t) * kStTile + in_tile);
+                        }
+                    }
+                });
+            });
+        }
+        for (int r = first + warp; r < end && warp < kStWarps; r += kStWarps) {
+            int32_t *list = p.lists + ((r0 + r) * p.H_KV + h) * p.top_k;
+            const int n = row_count[r];
+            if (n <= 128) list_candidates<4>(cand(r), n, most, list, p.top_k, lane);
+            else if (n <= kCandRow) list_candidates<kCandRow / 32>(cand(r), n, most, list, p.top_k, lane);
+            else if (lane == 0) list[0] = kUnlisted;   // many equal keys
+        }
+        __syncthreads();
         first = end;
     }
     tc_fence_before();
@@ -359,55 +427,37 @@ __global__ void __launch_bounds__(kStThreads, 1) select_tile_kernel(const Select
     }
 }
 
-// Largest shared memory that the kernel is launched with, beside its static variables.
-constexpr int kStRoom = 226 * 1024;
-
 template <int D, int G>
-static kvc_status launch_tile_kernel(const SelectTileParams &tp, dim3 grid, size_t smem, int c, cudaStream_t stream)
+static kvc_status launch_tile_kernel(const SelectTileParams &tp, cudaStream_t stream)
 {
+    // At least 80 KB: no more than two CTAs to an SM, whose tensor memory holds two allocations.
+    constexpr int kSmem = StCfg<D>::SMEM > 80 * 1024 ? StCfg<D>::SMEM : 80 * 1024;
     struct Tag {};
-    const DecodeKernel k = configured<Tag>(reinterpret_cast<const void *>(&select_tile_kernel<D, G>), kStRoom, kStThreads, false);
+    const DecodeKernel k = configured<Tag>(reinterpret_cast<const void *>(&select_tile_kernel<D, G>), kSmem, kStCta, false);
     if (k.ctas_per_sm <= 0) return KVC_ERR_CUDA;
-    return launch(&select_tile_kernel<D, G>, grid, kStThreads, smem, c, stream, tp);
+    const dim3 grid(static_cast<unsigned>((tp.rows + tp.RT - 1) / tp.RT), tp.s.H_KV);
+    return launch(&select_tile_kernel<D, G>, grid, kStCta, kSmem, 1, stream, tp);
 }
 
 template <int D>
-static kvc_status launch_tiles(SelectTileParams &tp, int sms, cudaStream_t stream)
+static kvc_status launch_tiles(const SelectTileParams &tp, cudaStream_t stream)
 {
-    using C = StCfg<D>;
-    const SelectParams &p = tp.s;
-    constexpr int kFixed = 1024 + C::KEYS + kStPick * static_cast<int>(sizeof(Candidates));
-    constexpr int kTiles = (kStRoom - kFixed) / (4 * kStTile);      // runs of 128 words that there is room for
-    const int blocks = (p.max_blocks + kStTile - 1) / kStTile;      // tiles of the widest row
-    tp.RT = std::min(kStRows, kStCols / p.g);
-    int c = 1;
-    auto room = [&] { return (blocks + c - 1) / c * (tp.RT + 2) <= kTiles; };   // keys, blocks and units
-    while (c < 8 && !room()) c *= 2;
-    while (tp.RT > 4 && !room()) tp.RT /= 2;
-    if (!room() || blocks * kStTile > C::A / 4 || blocks * kStTile > kPickMost) return KVC_ERR_UNSUPPORTED;
-    const int64_t row_tiles = (tp.rows + tp.RT - 1) / tp.RT;
-    while (c < 8 && c < blocks && row_tiles * p.H_KV * c < sms) c *= 2;
-    tp.tiles = (blocks + c - 1) / c;
-    if (row_tiles * c > 0x7FFFFFFF) return KVC_ERR_UNSUPPORTED;
-    // At least 80 KB: no more than two CTAs to an SM, whose tensor memory holds two allocations.  (A CTA that waited for
-    // tensor memory while its cluster waits for it could wait for a CTA of another cluster that does the same.)
-    const size_t smem = std::max<size_t>(80 * 1024, kFixed + static_cast<size_t>(4) * kStTile * tp.tiles * (tp.RT + 2));
-    const dim3 grid(static_cast<unsigned>(row_tiles * c), p.H_KV);
-    switch (p.g) {
-    case 1: return launch_tile_kernel<D, 1>(tp, grid, smem, c, stream);
-    case 2: return launch_tile_kernel<D, 2>(tp, grid, smem, c, stream);
-    case 4: return launch_tile_kernel<D, 4>(tp, grid, smem, c, stream);
-    case 8: return launch_tile_kernel<D, 8>(tp, grid, smem, c, stream);
+    switch (tp.s.g) {
+    case 1: return launch_tile_kernel<D, 1>(tp, stream);
+    case 2: return launch_tile_kernel<D, 2>(tp, stream);
+    case 4: return launch_tile_kernel<D, 4>(tp, stream);
+    case 8: return launch_tile_kernel<D, 8>(tp, stream);
     }
-    return launch_tile_kernel<D, 0>(tp, grid, smem, c, stream);
+    return launch_tile_kernel<D, 0>(tp, stream);
 }
 
-kvc_status select_tiles(const SelectParams &p, int D, int64_t rows, int sms, cudaStream_t stream)
+kvc_status select_tiles(const SelectParams &p, int D, int64_t rows, cudaStream_t stream)
 {
     SelectTileParams tp{};
     tp.s = p;
     tp.rows = rows;
-    return D == 64 ? launch_tiles<64>(tp, sms, stream) : launch_tiles<128>(tp, sms, stream);
+    tp.RT = std::min(kStRows, kStCols / p.g);
+    return D == 64 ? launch_tiles<64>(tp, stream) : launch_tiles<128>(tp, stream);
 }
 
 }  // namespace kvc
