@@ -46,6 +46,7 @@ struct StCfg {
     static_assert(ROW_CAND >= kStGroups * 4, "the groups' maxima lie in the candidates' place");
     static constexpr int CPR = K / 16;              // 16-byte chunks per record
     static constexpr int STEP = kStThreads / CPR;   // records per pass of the CTA's threads
+    static_assert(STEP % 8 == 0, "a thread's records keep their place in the swizzle");
     static constexpr int U = kStTile / STEP;        // passes per tile
 };
 
@@ -180,7 +181,14 @@ __global__ void __launch_bounds__(kStCta, 1) select_tile_kernel(const SelectTile
 
     const uint32_t idesc = tc_idesc_f16(128, cols, false, false, false);
     const uint64_t desc_a = tc_smem_desc(a_base, 16, 1024, kSwizzle128B), desc_b = tc_smem_desc(b_base, 16, 1024, kSwizzle128B);
-    const int chunk = tid % C::CPR, rec0 = tid / C::CPR;
+    // This thread's 16-byte chunk and first record.  Eight neighbours hold four chunks of one 128-byte band in two
+    // records, whose swizzles differ: both of a thread's stores are free of conflicts.
+    constexpr int BAND_BITS = C::BANDS == 4 ? 2 : 1;
+    const int band = (lane >> 3) & (C::BANDS - 1), chunk = 4 * band + (lane & 3);
+    const int rec0 = (((tid >> 3) >> BAND_BITS) << 1) | ((lane >> 2) & 1);
+    const uint32_t a_dst[2] = {a_base + band * C::BAND + sw128(rec0, 2 * (chunk & 3)), a_base + band * C::BAND + sw128(rec0, 2 * (chunk & 3) + 1)};
+    const int8_t *codes = p.codes + h * (2 * D) + 16 * chunk;
+    const uint32_t record_stride = static_cast<uint32_t>(p.H_KV) * (2 * D);   // H_KV is at most 256
     uint32_t phase = 0u;   // of both barriers: a tile each
 
     const int lane_seq = lane < tp.RT ? row_seq[lane] : -3, lane_nb = lane < tp.RT ? row_nb[lane] : 0;   // RT <= 32
@@ -198,27 +206,23 @@ __global__ void __launch_bounds__(kStCta, 1) select_tile_kernel(const SelectTile
         const int n_tiles = (most + kStTile - 1) / kStTile;
         int t0 = 0;   // the chunk's first tile
 
-        // this thread's 16 bytes of U records of a tile
+        // this thread's 16 bytes of U records of a tile, on their way while the tile before is read
         uint4 raw[C::U];
         auto load = [&](int t) {
 #pragma unroll
             for (int u = 0; u < C::U; ++u) {
-                const int phys = phys_s[t * kStTile + u * C::STEP + rec0];
-                raw[u] = make_uint4(0u, 0u, 0u, 0u);
-                if (phys >= 0)
-                    raw[u] = __ldg(reinterpret_cast<const uint4 *>(p.codes + (static_cast<int64_t>(phys) * p.H_KV + h) * (2 * D)) + chunk);
+                // no block: block 0's, whose scores are not used
+                const uint32_t phys = static_cast<uint32_t>(max(phys_s[t * kStTile + u * C::STEP + rec0], 0));
+                raw[u] = __ldg(reinterpret_cast<const uint4 *>(codes + static_cast<uint64_t>(phys) * record_stride));
             }
         };
-        auto widen = [&] {   // to A; the upper half of a 128-byte band's writers store their second chunk first: no conflicts
+        auto widen = [&] {   // to A
 #pragma unroll
             for (int u = 0; u < C::U; ++u) {
                 const uint2 x0 = s8x4_to_f16(raw[u].x), x1 = s8x4_to_f16(raw[u].y), x2 = s8x4_to_f16(raw[u].z),
                             x3 = s8x4_to_f16(raw[u].w);
-                const uint4 v0 = make_uint4(x0.x, x0.y, x1.x, x1.y), v1 = make_uint4(x2.x, x2.y, x3.x, x3.y);
-                const int row = u * C::STEP + rec0, band = chunk >> 2, c0 = 2 * (chunk & 3), flip = band & 1;
-                const uint32_t base = a_base + band * C::BAND;
-                sts128(base + sw128(row, c0 + flip), flip ? v1 : v0);
-                sts128(base + sw128(row, c0 + 1 - flip), flip ? v0 : v1);
+                sts128(a_dst[0] + u * C::STEP * 128, make_uint4(x0.x, x0.y, x1.x, x1.y));
+                sts128(a_dst[1] + u * C::STEP * 128, make_uint4(x2.x, x2.y, x3.x, x3.y));
             }
         };
         auto written = [&] {   // this warp's part of A is there, and it has read what it wanted of the tile before last
@@ -259,8 +263,8 @@ __global__ void __launch_bounds__(kStCta, 1) select_tile_kernel(const SelectTile
                 load(0);
                 widen();
                 written();
+                if (nt > 1) load(1);
                 for (int t = 0; t < nt; ++t) {
-                    if (t + 1 < nt) load(t + 1);
                     if (!mbar_wait_bounded(smem_u32(&done_bar), phase) && lane == 0) atomicOr(p.err, KVC_EBIT_TIMEOUT);
                     phase ^= 1u;
                     tc_fence_after();
@@ -268,6 +272,7 @@ __global__ void __launch_bounds__(kStCta, 1) select_tile_kernel(const SelectTile
                         widen();
                         written();
                     }
+                    if (t + 2 < nt) load(t + 2);
                     read(t, tmem + (t & 1) * kStCols + (static_cast<uint32_t>(32 * (warp & 3)) << 16));
                 }
             }
@@ -335,11 +340,8 @@ __global__ void __launch_bounds__(kStCta, 1) select_tile_kernel(const SelectTile
 #pragma unroll
             for (int x = 0; x < RPC; ++x) most_of[0][x] = most_of[1][x] = -INFINITY;
             walk(true, [&](int t, uint32_t d) {
-                const bool odd = (t & 1) != 0;
-                scores(t, d, [&](int x, float s) {
-                    most_of[0][x] = fmaxf(most_of[0][x], odd ? -INFINITY : s);
-                    most_of[1][x] = fmaxf(most_of[1][x], odd ? s : -INFINITY);
-                });
+                if (t & 1) scores(t, d, [&](int x, float s) { most_of[1][x] = fmaxf(most_of[1][x], s); });
+                else scores(t, d, [&](int x, float s) { most_of[0][x] = fmaxf(most_of[0][x], s); });
             });
 #pragma unroll
             for (int x = 0; x < RPC; ++x)
@@ -392,7 +394,7 @@ __global__ void __launch_bounds__(kStCta, 1) select_tile_kernel(const SelectTile
 #pragma unroll
                 for (int x = 0; x < RPC; ++x)
                     if (at[x] < kCandRow) {
-                        cand(row0 + x)[at[x]] = to_key(hit[x]);
+                        cand(row0 + x)[at[x]] = __float_as_uint(hit[x]);
                         cand(row0 + x)[kCandRow + at[x]] = static_cast<uint32_t>((t0 + t) * kStTile + in_tile);
                     }
             });
@@ -402,16 +404,18 @@ __global__ void __launch_bounds__(kStCta, 1) select_tile_kernel(const SelectTile
                     if (s >= row_limit[r]) {
                         const int at = atomicAdd(&row_count[r], 1);
                         if (at < kCandRow) {
-                            cand(r)[at] = to_key(s);
+                            cand(r)[at] = __float_as_uint(s);
                             cand(r)[kCandRow + at] = static_cast<uint32_t>((t0 + t) * kStTile + in_tile);
                         }
                     }
                 });
             });
         }
-        for (int r = first + warp; r < end && warp < kStWarps; r += kStWarps) {
+        for (int r = first + warp; r < end && warp < kStWarps; r += kStWarps) {   // a warp per row
             int32_t *list = p.lists + ((r0 + r) * p.H_KV + h) * p.top_k;
             const int n = row_count[r];
+            for (int i = lane; i < min(n, kCandRow); i += 32) cand(r)[i] = to_key(__uint_as_float(cand(r)[i]));   // keys from here on
+            __syncwarp();
             if (n <= 128) list_candidates<4>(cand(r), n, most, list, p.top_k, lane);
             else if (n <= kCandRow) list_candidates<kCandRow / 32>(cand(r), n, most, list, p.top_k, lane);
             else if (lane == 0) list[0] = kUnlisted;   // many equal keys
