@@ -12,8 +12,9 @@
 // the rest of the SM idle while rows are finished; multiplying again costs little.  So the first walk only keeps the
 // largest score of 256 groups of blocks per row: the top_k-th of those is a limit that at least top_k blocks reach.
 // The second walk collects the few blocks that reach it, and a warp per row ranks them by counting.
-// B (the queries) stays in shared memory; A is read as int8 into registers while the tile before is multiplied,
-// widened to f16 and stored in the 128-byte swizzle.
+// B (the queries) stays in shared memory.  A goes through tensor memory: with both operands in shared memory the
+// products alone would take all of its bandwidth (8 KB in 68 cycles), and every warp can stage, widen and store its own
+// part without a barrier: 32 blocks and a quarter of the 2 d channels, by copies two tiles ahead.
 //
 // A tile of rows may hold several sequences (runs): they are done one after the other.
 #include <algorithm>
@@ -37,18 +38,22 @@ struct StCfg {
     static constexpr int K = 2 * D;
     static constexpr int BANDS = K / 64;            // 128-byte bands of f16
     static constexpr int BAND = 128 * 128;          // bytes of a band of 128 rows
-    static constexpr int A = BANDS * BAND;          // bytes
-    static constexpr int CAND = 2 * A;              // after A and B: groups' maxima, then candidates
+    static constexpr int B = BANDS * BAND;          // bytes of the queries
+    static constexpr int SEG = K / 4;               // bytes of a record that a warp widens
+    static constexpr int CH = SEG / 16;             // in 16-byte chunks: 4 or 2
+    static constexpr int STAGE = 32 * SEG;          // bytes of a warp's stage
+    static constexpr int STAGES = 2;
+    static constexpr int STAGED = B;                // offset of the stages
+    static constexpr int CAND = STAGED + kStWarps * STAGES * STAGE;   // groups' maxima, then candidates
     static constexpr int ROW_CAND = kCandWords * 4;
     static constexpr int PHYS = CAND + kStRows * ROW_CAND;   // blocks of a chunk's tiles
     static constexpr int UNIT = PHYS + kStChunk * kStTile * 4;
     static constexpr int SMEM = 1024 /* alignment */ + UNIT + kStChunk * kStTile * 4;
+    static constexpr int A_COLS = K / 2;            // columns of A in tensor memory
+    static constexpr int A_TMEM = 2 * kStCols;      // A's two buffers, after the products' two
     static_assert(ROW_CAND >= kStGroups * 4, "the groups' maxima lie in the candidates' place");
-    static constexpr int CPR = K / 16;              // 16-byte chunks per record
-    static constexpr int STEP = kStThreads / CPR;   // records per pass of the CTA's threads
-    static_assert(STEP % 8 == 0, "a thread's records keep their place in the swizzle");
-    static constexpr int U = kStTile / STEP;        // passes per tile
 };
+constexpr int kStTmem = 512;   // columns: all of them
 
 struct SelectTileParams {
     SelectParams s;
@@ -82,18 +87,20 @@ __global__ void __launch_bounds__(kStCta, 1) select_tile_kernel(const SelectTile
     __shared__ int32_t row_seq[kStRows], row_nb[kStRows];                // sequence (< 0: no work), blocks of the row
     __shared__ float row_limit[kStRows];
     __shared__ int32_t row_count[kStRows];                               // candidates
-    __shared__ uint64_t full_bar, done_bar;   // A is written; the product is there (and A free)
+    __shared__ uint64_t full_bar[2], done_bar[2];   // a buffer of A is written; its products are there (and it is free)
     __shared__ uint32_t tmem_base;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, h = blockIdx.y;
     const int64_t r0 = static_cast<int64_t>(blockIdx.x) * tp.RT;
     const int cols = (tp.RT * p.g + 15) & ~15;
     if (warp == 0) {
-        tmem_alloc(smem_u32(&tmem_base), 2 * kStCols);
+        tmem_alloc(smem_u32(&tmem_base), kStTmem);
         tmem_relinquish();
     }
     if (tid == 0) {
-        mbar_init(smem_u32(&full_bar), kStWarps);
-        mbar_init(smem_u32(&done_bar), 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&full_bar[i]), kStWarps);
+            mbar_init(smem_u32(&done_bar[i]), 1);
+        }
         fence_barrier_init();
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -119,7 +126,7 @@ __global__ void __launch_bounds__(kStCta, 1) select_tile_kernel(const SelectTile
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_base;
-    const uint32_t a_base = smem_u32(smem), b_base = a_base + C::A;
+    const uint32_t b_base = smem_u32(smem);
 
     // ---- the rows' queries as whole numbers, positive parts then negative ones: a warp per row
     constexpr int KEEP = 2;   // chunks of a lane that stay in registers between the two passes
@@ -180,16 +187,17 @@ __global__ void __launch_bounds__(kStCta, 1) select_tile_kernel(const SelectTile
     __syncthreads();
 
     const uint32_t idesc = tc_idesc_f16(128, cols, false, false, false);
-    const uint64_t desc_a = tc_smem_desc(a_base, 16, 1024, kSwizzle128B), desc_b = tc_smem_desc(b_base, 16, 1024, kSwizzle128B);
-    // This thread's 16-byte chunk and first record.  Eight neighbours hold four chunks of one 128-byte band in two
-    // records, whose swizzles differ: both of a thread's stores are free of conflicts.
-    constexpr int BAND_BITS = C::BANDS == 4 ? 2 : 1;
-    const int band = (lane >> 3) & (C::BANDS - 1), chunk = 4 * band + (lane & 3);
-    const int rec0 = (((tid >> 3) >> BAND_BITS) << 1) | ((lane >> 2) & 1);
-    const uint32_t a_dst[2] = {a_base + band * C::BAND + sw128(rec0, 2 * (chunk & 3)), a_base + band * C::BAND + sw128(rec0, 2 * (chunk & 3) + 1)};
-    const int8_t *codes = p.codes + h * (2 * D) + 16 * chunk;
+    const uint64_t desc_b = tc_smem_desc(b_base, 16, 1024, kSwizzle128B);
+    const int quarter = warp & 3, part = (warp >> 2) & 3;   // this warp's 32 blocks of a tile, and its part of the channels
+    const uint32_t stage = b_base + C::STAGED + (warp & (kStWarps - 1)) * (C::STAGES * C::STAGE);
+    // where chunk c of row r stands in a stage, so that eight rows' chunks c are free of conflicts
+    auto staged = [](int r, int c) { return static_cast<uint32_t>(r * C::SEG + ((c ^ ((C::CH == 4 ? r >> 1 : r >> 2) & (C::CH - 1))) << 4)); };
+    const int8_t *codes = p.codes + h * (2 * D) + part * C::SEG;
     const uint32_t record_stride = static_cast<uint32_t>(p.H_KV) * (2 * D);   // H_KV is at most 256
-    uint32_t phase = 0u;   // of both barriers: a tile each
+    uint32_t tile_no = 0u;   // tiles of this CTA so far: the barriers' phases
+    auto wait = [&](uint64_t &b, uint32_t parity) {
+        if (!mbar_wait_bounded(smem_u32(&b), parity & 1u) && lane == 0) atomicOr(p.err, KVC_EBIT_TIMEOUT);
+    };
 
     const int lane_seq = lane < tp.RT ? row_seq[lane] : -3, lane_nb = lane < tp.RT ? row_nb[lane] : 0;   // RT <= 32
     for (int first = 0; first < tp.RT;) {   // runs of rows of one sequence
@@ -206,31 +214,44 @@ __global__ void __launch_bounds__(kStCta, 1) select_tile_kernel(const SelectTile
         const int n_tiles = (most + kStTile - 1) / kStTile;
         int t0 = 0;   // the chunk's first tile
 
-        // this thread's 16 bytes of U records of a tile, on their way while the tile before is read
-        uint4 raw[C::U];
-        auto load = [&](int t) {
+        // this warp's part of tile t to its stage: CH lanes a record
+        auto copy = [&](int t) {
+            const uint32_t to = stage + (t & 1) * C::STAGE;
+            const int c = lane % C::CH;
 #pragma unroll
-            for (int u = 0; u < C::U; ++u) {
+            for (int i = 0; i < C::CH; ++i) {
+                const int r = i * (32 / C::CH) + lane / C::CH;
                 // no block: block 0's, whose scores are not used
-                const uint32_t phys = static_cast<uint32_t>(max(phys_s[t * kStTile + u * C::STEP + rec0], 0));
-                raw[u] = __ldg(reinterpret_cast<const uint4 *>(codes + static_cast<uint64_t>(phys) * record_stride));
+                const uint32_t phys = static_cast<uint32_t>(max(phys_s[t * kStTile + 32 * quarter + r], 0));
+                cp_async16(to + staged(r, c), codes + static_cast<uint64_t>(phys) * record_stride + 16 * c);
             }
+            cp_async_commit();
         };
-        auto widen = [&] {   // to A
+        // from there to A's buffer in tensor memory, widened: lane = block
+        auto widen = [&](int t, uint32_t buf) {
+            uint32_t w[32];
 #pragma unroll
-            for (int u = 0; u < C::U; ++u) {
-                const uint2 x0 = s8x4_to_f16(raw[u].x), x1 = s8x4_to_f16(raw[u].y), x2 = s8x4_to_f16(raw[u].z),
-                            x3 = s8x4_to_f16(raw[u].w);
-                sts128(a_dst[0] + u * C::STEP * 128, make_uint4(x0.x, x0.y, x1.x, x1.y));
-                sts128(a_dst[1] + u * C::STEP * 128, make_uint4(x2.x, x2.y, x3.x, x3.y));
+            for (int c = 0; c < C::CH; ++c) {
+                const uint4 x = lds128(stage + (t & 1) * C::STAGE + staged(lane, c));
+                const uint2 x0 = s8x4_to_f16(x.x), x1 = s8x4_to_f16(x.y), x2 = s8x4_to_f16(x.z), x3 = s8x4_to_f16(x.w);
+                w[8 * c + 0] = x0.x, w[8 * c + 1] = x0.y, w[8 * c + 2] = x1.x, w[8 * c + 3] = x1.y;
+                w[8 * c + 4] = x2.x, w[8 * c + 5] = x2.y, w[8 * c + 6] = x3.x, w[8 * c + 7] = x3.y;
             }
-        };
-        auto written = [&] {   // this warp's part of A is there, and it has read what it wanted of the tile before last
-            fence_proxy_async_smem();
-            tc_fence_before();
+            const uint32_t to = tmem + C::A_TMEM + buf * C::A_COLS + part * (C::A_COLS / 4) + (static_cast<uint32_t>(32 * quarter) << 16);
+            if constexpr (C::CH == 4) {
+                tmem_st32(to, w);
+            } else {
+                uint32_t w16[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) w16[i] = w[i];
+                tmem_st16(to, w16);
+            }
+            tmem_st_wait();
+            tc_fence_before();   // and what this warp read of tensor memory it has read
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&full_bar));
+            if (lane == 0) mbar_arrive(smem_u32(&full_bar[buf]));
         };
+
         // One walk over the blocks.  read(t, d): the epilogue of tile t, whose products stand at d in tensor memory.
         auto walk = [&](bool report, auto read) {
             for (t0 = 0; t0 < n_tiles; t0 += kStChunk) {
@@ -247,34 +268,41 @@ __global__ void __launch_bounds__(kStCta, 1) select_tile_kernel(const SelectTile
                     unit_s[i] = phys < 0 ? 0.f : __ldg(p.units + static_cast<int64_t>(phys) * p.H_KV + h);
                 }
                 __syncthreads();
+                // Barrier phases: tile i of the CTA is use i / 2 of buffer i mod 2.
                 if (warp == kStWarps) {
-                    for (int t = 0; t < nt; ++t, phase ^= 1u) {
-                        if (!mbar_wait_bounded(smem_u32(&full_bar), phase) && lane == 0) atomicOr(p.err, KVC_EBIT_TIMEOUT);
+                    for (int t = 0; t < nt; ++t) {
+                        const uint32_t i = tile_no + t, buf = i & 1u;
+                        wait(full_bar[buf], i >> 1);
                         tc_fence_after();
-                        const uint32_t d = tmem + (t & 1) * kStCols;
 #pragma unroll
                         for (int kk = 0; kk < C::K / 16; ++kk)
-                            tc_mma_f16_warp(d, tc_desc_advance(desc_a, (kk >> 2) * C::BAND + (kk & 3) * 32),
-                                            tc_desc_advance(desc_b, (kk >> 2) * C::BAND + (kk & 3) * 32), idesc, kk > 0 ? 1u : 0u);
-                        tc_commit_warp(smem_u32(&done_bar));
+                            tc_mma_f16_tmem_a_warp(tmem + buf * kStCols, tmem + C::A_TMEM + buf * C::A_COLS + kk * 8,
+                                                   tc_desc_advance(desc_b, (kk >> 2) * C::BAND + (kk & 3) * 32), idesc, kk > 0 ? 1u : 0u);
+                        tc_commit_warp(smem_u32(&done_bar[buf]));
                     }
-                    continue;
-                }
-                load(0);
-                widen();
-                written();
-                if (nt > 1) load(1);
-                for (int t = 0; t < nt; ++t) {
-                    if (!mbar_wait_bounded(smem_u32(&done_bar), phase) && lane == 0) atomicOr(p.err, KVC_EBIT_TIMEOUT);
-                    phase ^= 1u;
-                    tc_fence_after();
-                    if (t + 1 < nt) {
-                        widen();
-                        written();
+                } else {
+                    copy(0);
+                    if (nt > 1) copy(1);
+                    else cp_async_commit();
+                    cp_async_wait<1>();
+                    __syncwarp();
+                    widen(0, tile_no & 1u);
+                    for (int t = 0; t < nt; ++t) {
+                        const uint32_t i = tile_no + t, buf = i & 1u;
+                        __syncwarp();   // stage t mod 2 has been read
+                        if (t + 2 < nt) copy(t + 2);
+                        else cp_async_commit();   // a group each time, so that the wait below counts
+                        if (t + 1 < nt) {   // A's other buffer is free: tile t - 1's products were waited for
+                            cp_async_wait<1>();
+                            __syncwarp();
+                            widen(t + 1, buf ^ 1u);
+                        }
+                        wait(done_bar[buf], i >> 1);
+                        tc_fence_after();
+                        read(t, tmem + buf * kStCols + (static_cast<uint32_t>(32 * quarter) << 16));
                     }
-                    if (t + 2 < nt) load(t + 2);
-                    read(t, tmem + (t & 1) * kStCols + (static_cast<uint32_t>(32 * (warp & 3)) << 16));
                 }
+                tile_no += nt;
             }
             tc_fence_before();
             __syncthreads();
@@ -294,7 +322,7 @@ __global__ void __launch_bounds__(kStCta, 1) select_tile_kernel(const SelectTile
                 return j >= nb ? -INFINITY : (none == 0.f && (j < p.sink || j >= nb - p.recent) ? INFINITY : s);
             };
             if constexpr (G > 1) {
-                if (row0 >= tp.RT) return;
+                if (row0 >= tp.RT) return;   // warp-uniform
                 uint32_t v[32];
                 tmem_ld32(d + row0 * G, v);
                 tmem_ld_wait(v);
@@ -340,8 +368,11 @@ __global__ void __launch_bounds__(kStCta, 1) select_tile_kernel(const SelectTile
 #pragma unroll
             for (int x = 0; x < RPC; ++x) most_of[0][x] = most_of[1][x] = -INFINITY;
             walk(true, [&](int t, uint32_t d) {
-                if (t & 1) scores(t, d, [&](int x, float s) { most_of[1][x] = fmaxf(most_of[1][x], s); });
-                else scores(t, d, [&](int x, float s) { most_of[0][x] = fmaxf(most_of[0][x], s); });
+                const bool odd = (t & 1) != 0;
+                scores(t, d, [&](int x, float s) {
+                    if (odd) most_of[1][x] = fmaxf(most_of[1][x], s);
+                    else most_of[0][x] = fmaxf(most_of[0][x], s);
+                });
             });
 #pragma unroll
             for (int x = 0; x < RPC; ++x)
@@ -372,6 +403,16 @@ __global__ void __launch_bounds__(kStCta, 1) select_tile_kernel(const SelectTile
         __syncthreads();
 
         // ---- the blocks that reach it
+        auto append = [&](int r, uint32_t count, float s, float limit, int j) {   // if s reaches the limit; no branch
+            asm volatile(
+                "{\n\t.reg .pred p, q;\n\t.reg .u32 at, a;\n\t"
+                "setp.ge.f32 p, %0, %1;\n\tmov.u32 at, 0xffffffff;\n\t"
+                "@p atom.shared.add.u32 at, [%2], 1;\n\t"
+                "setp.lt.u32 q, at, %5;\n\tshl.b32 a, at, 2;\n\tadd.u32 a, a, %3;\n\t"
+                "@q st.shared.f32 [a], %0;\n\t@q st.shared.u32 [a + %6], %4;\n\t}"
+                ::"f"(s), "f"(limit), "r"(count), "r"(smem_u32(cand(r))), "r"(j), "n"(kCandRow), "n"(4 * kCandRow)
+                : "memory");
+        };
         if constexpr (G > 1) {
             float limit[RPC];
 #pragma unroll
@@ -379,36 +420,11 @@ __global__ void __launch_bounds__(kStCta, 1) select_tile_kernel(const SelectTile
                 limit[x] = row0 + x >= first && row0 + x < end ? row_limit[row0 + x] : __uint_as_float(0x7FFFFFFFu);
             const uint32_t counts = smem_u32(&row_count[row0 < kStRows ? row0 : 0]);
             walk(false, [&](int t, uint32_t d) {
-                float hit[RPC];
-                uint32_t at[RPC];
-                scores(t, d, [&](int x, float s) { hit[x] = s; });
-                if (row0 >= tp.RT) return;
-#pragma unroll
-                for (int x = 0; x < RPC; ++x)   // all of the additions are on their way before the first is used
-                    asm volatile(
-                        "{\n\t.reg .pred p;\n\tsetp.ge.f32 p, %2, %3;\n\tmov.u32 %0, 0xffffffff;\n\t"
-                        "@p atom.shared.add.u32 %0, [%1], 1;\n\t}"
-                        : "=r"(at[x])
-                        : "r"(counts + 4 * x), "f"(hit[x]), "f"(limit[x])
-                        : "memory");
-#pragma unroll
-                for (int x = 0; x < RPC; ++x)
-                    if (at[x] < kCandRow) {
-                        cand(row0 + x)[at[x]] = __float_as_uint(hit[x]);
-                        cand(row0 + x)[kCandRow + at[x]] = static_cast<uint32_t>((t0 + t) * kStTile + in_tile);
-                    }
+                scores(t, d, [&](int x, float s) { append(row0 + x, counts + 4 * x, s, limit[x], (t0 + t) * kStTile + in_tile); });
             });
         } else {
             walk(false, [&](int t, uint32_t d) {
-                scores(t, d, [&](int r, float s) {
-                    if (s >= row_limit[r]) {
-                        const int at = atomicAdd(&row_count[r], 1);
-                        if (at < kCandRow) {
-                            cand(r)[at] = __float_as_uint(s);
-                            cand(r)[kCandRow + at] = static_cast<uint32_t>((t0 + t) * kStTile + in_tile);
-                        }
-                    }
-                });
+                scores(t, d, [&](int r, float s) { append(r, smem_u32(&row_count[r]), s, row_limit[r], (t0 + t) * kStTile + in_tile); });
             });
         }
         for (int r = first + warp; r < end && warp < kStWarps; r += kStWarps) {   // a warp per row
@@ -427,15 +443,15 @@ __global__ void __launch_bounds__(kStCta, 1) select_tile_kernel(const SelectTile
     __syncthreads();
     if (warp == 0) {
         tc_fence_after();
-        tmem_dealloc(tmem, 2 * kStCols);
+        tmem_dealloc(tmem, kStTmem);
     }
 }
 
 template <int D, int G>
 static kvc_status launch_tile_kernel(const SelectTileParams &tp, cudaStream_t stream)
 {
-    // At least 80 KB: no more than two CTAs to an SM, whose tensor memory holds two allocations.
-    constexpr int kSmem = StCfg<D>::SMEM > 80 * 1024 ? StCfg<D>::SMEM : 80 * 1024;
+    // At least 116 KB: one CTA to an SM, whose tensor memory it takes whole.
+    constexpr int kSmem = StCfg<D>::SMEM > 116 * 1024 ? StCfg<D>::SMEM : 116 * 1024;
     struct Tag {};
     const DecodeKernel k = configured<Tag>(reinterpret_cast<const void *>(&select_tile_kernel<D, G>), kSmem, kStCta, false);
     if (k.ctas_per_sm <= 0) return KVC_ERR_CUDA;
