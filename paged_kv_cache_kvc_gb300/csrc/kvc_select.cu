@@ -609,8 +609,19 @@ __global__ void __launch_bounds__(kSelThreads) select_rest_kernel(const SelectPa
 
 static bool aligned(const void *ptr, size_t a) { return (reinterpret_cast<uintptr_t>(ptr) & (a - 1)) == 0; }
 
-// Rows per sequence, on average, from which on rows are scored together.
-constexpr int kTileRuns = 8;
+// Whether rows are scored together.  Alone, a row's cost per block is its group's int8 products, and at least the
+// bounds' way out of L2 (that of four heads); together, a tile of rows walks all blocks once per sequence it holds, one
+// tile to an SM at a time, whatever it holds.  Measured at 2048 blocks, 8 KV heads of 4 query heads: 64 rows 41 us
+// alone, 62 together; 128 rows 69 and 63; 512 rows 244 and 64.  One query head per KV head, 32 of them, 128 rows: 168
+// and 110; groups that do not divide 32 columns (3, 5), 128 rows: 62 and 79 alone, 147 and 152 together.
+static bool rows_together(const SelectParams &p, int64_t rows, int sms)
+{
+    const int64_t RT = std::min(32, 128 / p.g);
+    const int64_t walks = std::min(rows, (rows + RT - 1) / RT + p.B - 1) * p.H_KV;
+    const int64_t waves = (walks + sms - 1) / sms;
+    const bool whole = p.g == 2 || p.g == 4 || p.g == 8;
+    return rows * p.H_KV * std::max(p.g, 4) >= waves * (whole ? 4000 : (p.g == 1 ? 6500 : 10000));
+}
 
 template <int D>
 static kvc_status launch_rest(const SelectParams &p, int64_t rows, cudaStream_t stream)
@@ -724,7 +735,7 @@ extern "C" kvc_status kvc_select_blocks(kvc_pool *pool, int32_t layer, const voi
     p.lists = selected;
     p.err = pool->err;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (seq_ids && n_rows >= kTileRuns * static_cast<int64_t>(B) && top_k <= kShortList && max_blocks <= kSelKeys) {
+    if (seq_ids && top_k <= kShortList && max_blocks <= kSelKeys && rows_together(p, n_rows, pool->num_sms)) {
         const kvc_status tiled = select_tiles(p, pool->D, n_rows, s);
         if (tiled != KVC_OK) return tiled;
         return pool->D == 64 ? launch_rest<64>(p, n_rows, s) : launch_rest<128>(p, n_rows, s);

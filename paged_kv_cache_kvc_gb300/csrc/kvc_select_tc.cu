@@ -257,7 +257,8 @@ __global__ void __launch_bounds__(kStCta, 1) select_tile_kernel(const SelectTile
             for (t0 = 0; t0 < n_tiles; t0 += kStChunk) {
                 const int nt = min(kStChunk, n_tiles - t0);
                 __syncthreads();   // the chunk before is done with its table entries
-                for (int i = tid; i < nt * kStTile; i += kStCta) {
+                // a single chunk's are still there in the second walk
+                for (int i = tid; i < nt * kStTile && (report || n_tiles > kStChunk); i += kStCta) {
                     const int j = t0 * kStTile + i;
                     int phys = j < most ? __ldg(bt + j) : -1;
                     if (j < most && (phys < 0 || static_cast<int64_t>(phys) >= p.N)) {
