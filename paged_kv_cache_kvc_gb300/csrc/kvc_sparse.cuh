@@ -356,9 +356,12 @@ __global__ void __launch_bounds__(kThreads) sparse_kernel(const __grid_constant_
         return make_int2(tok0, phys);
     };
     int2 t_cur = load_tile(lane, e_cur), t_next = load_tile(32 + lane, e_next);
-    auto entry = [&](int jj, int jbase) -> int2 {   // tile jj, which may differ from lane to lane
-        const int2 v = (jj - jbase < 32) ? t_cur : t_next;
-        return make_int2(__shfl_sync(kFull, v.x, (jj - jbase) & 31), __shfl_sync(kFull, v.y, (jj - jbase) & 31));
+    // Tile jj, which may differ from lane to lane: the lane asked cannot know which of its two the asker wants.
+    auto entry = [&](int jj, int jbase) -> int2 {
+        const int from = (jj - jbase) & 31;
+        const int2 a = make_int2(__shfl_sync(kFull, t_cur.x, from), __shfl_sync(kFull, t_cur.y, from));
+        const int2 b = make_int2(__shfl_sync(kFull, t_next.x, from), __shfl_sync(kFull, t_next.y, from));
+        return jj - jbase < 32 ? a : b;
     };
     const int64_t layer_row = static_cast<int64_t>(p.layer) * p.N;
     // Tile j is stage j % R of the ring.  Lane t issues tile from + t, t < n.
@@ -420,7 +423,7 @@ __global__ void __launch_bounds__(kThreads) sparse_kernel(const __grid_constant_
         bool full = true, some = false;
 #pragma unroll
         for (int t = 0; t < T; ++t) {
-            const int2 e = entry(j + t, jbase);
+            const int2 e = make_int2(__shfl_sync(kFull, t_cur.x, (j + t) & 31), __shfl_sync(kFull, t_cur.y, (j + t) & 31));
             valid[t] = e.y < 0 ? 0 : min(kBS, len - e.x);
             full &= valid[t] == kBS;
             some |= valid[t] > 0;

@@ -381,7 +381,7 @@ def check_attend(c, q, rows, lists, out, lse, scale=None, untouched=7.0):
                 gl = lse[i, h * g:(h + 1) * g]
                 assert np.array_equal(np.isinf(gl), np.isinf(rl))
                 fin = np.isfinite(rl)
-                assert np.all(np.abs(gl - rl)[fin] <= tl[fin])
+                assert np.all(np.abs(gl[fin] - rl[fin]) <= tl[fin])
 
 
 def random_lists(c, rows, top_k, seed, shuffle=False):
@@ -446,6 +446,25 @@ def test_wide_blocks(kvc, dtype, bs):
             out, lse = attend_rows(c, q, rows, lists)
             check_attend(c, q, rows, dev(lists), out, lse)
         assert kvc.kvc_pool_sync_status(c.pool) == kvc.KVC_OK
+    finally:
+        c.close()
+
+
+@pytest.mark.parametrize("dtype,g", [("bf16", 4), ("bf16", 16), ("bf16", 32), ("fp8", 4), ("fp8", 32), ("int4", 8), ("int4", 32)])
+@pytest.mark.parametrize("top_k", [70, 129, 300])
+def test_long_lists_of_many_rows(kvc, dtype, g, top_k):
+    """So many rows that one CTA walks a row's whole list: tens of tiles for every warp, more than it looks up at once."""
+    c = Cache(kvc, [16 * 320 + 5, 16 * 200], H_KV=1, dtype=dtype)
+    try:
+        rows = [(0, p) for p in range(16 * 320 + 5 - 600, 16 * 320 + 5)] + [(1, 3199)] * 100
+        q = bf16(np.random.default_rng(top_k).standard_normal((len(rows), g, 128)) * 2).cuda()
+        lists = random_lists(c, rows, top_k, top_k, shuffle=top_k == 129)
+        out, lse = attend_rows(c, q, rows, lists)
+        assert kvc.kvc_pool_sync_status(c.pool) == kvc.KVC_OK
+        keep = [0, 1, 317, 599, 600, 699]
+        check_attend(c, q[keep], [rows[i] for i in keep], dev(lists[keep]), out[keep], lse[keep])
+        few, few_l = attend_rows(c, q[keep].contiguous(), [rows[i] for i in keep], lists[keep])   # clusters of CTAs
+        check_attend(c, q[keep], [rows[i] for i in keep], dev(lists[keep]), few, few_l)
     finally:
         c.close()
 
