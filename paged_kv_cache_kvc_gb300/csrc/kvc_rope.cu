@@ -222,7 +222,8 @@ __device__ __forceinline__ void build_factors(const RopeParams &p, RopeBatch<D, 
 // 74 us, 5.4 TB/s, 80 % of the copy rate; e4m3 pools 95 us and int4 98 (the exact divisions by the scales).  A CTA
 // per four tokens without the ninth warp took 97 us (each CTA began with the chain of loads), the same with one row
 // in flight 111 us; per-row address arithmetic and one loop over all kinds of head 95 us.
-// SLOTS: rows whose places and positions are given; else sequences' runs of tokens.
+// SLOTS: rows whose places and positions are given (16 384 tokens with three axes: 74 us too, the axes' positions
+// come out of L1); else sequences' runs of tokens.
 template <int D, int GPT, int U, bool SLOTS>
 __global__ void __launch_bounds__(kRopeCta, 3) rope_kernel(const RopeParams p)
 {
