@@ -544,6 +544,8 @@ KVC_API kvc_status kvc_bounds_bytes(const kvc_pool *pool, uint64_t *bytes);
  *       adjacent and in ascending order, as kvc_plan_step gives them; -1 rows
  *       are skipped, another slot outside the pool is recorded
  *       (KVC_ERR_BAD_BLOCK)
+ * Blocks that kvc_copy_blocks made keep their old bounds until a row of theirs
+ * is given here (the slot of its last filled place).
  * Pools of any block size.  Errors (synchronous): KVC_ERR_ARG (also a buffer
  * smaller than kvc_bounds_bytes), KVC_ERR_CUDA. */
 KVC_API kvc_status kvc_update_bounds(kvc_pool *pool, int32_t layer, const int32_t *slots, int64_t n_rows, void *bounds,

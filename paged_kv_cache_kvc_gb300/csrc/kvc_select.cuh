@@ -81,7 +81,7 @@ __device__ __forceinline__ Cut find_cut(const uint32_t (&k)[S], uint32_t want)
     forced = __reduce_add_sync(kFull, forced);
     lo = __reduce_min_sync(kFull, lo);
     hi = __reduce_max_sync(kFull, hi);
-    if (forced >= want) return {0xFFFFFFFEu, 0u};   // the forced ones fill the list
+    if (forced >= want) return {0xFFFFFFFFu, want};   // the forced ones fill the list
     uint32_t n_hi = forced;   // keys > hi: fewer than wanted; keys >= lo: more
     for (int it = 0; lo < hi; ++it) {
         uint32_t m[3], c[3];

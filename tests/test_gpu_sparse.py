@@ -343,6 +343,32 @@ def test_selection_in_error(kvc):
         c.close()
 
 
+@pytest.mark.parametrize("n_rows", [1, 1100])
+@pytest.mark.parametrize("unit", [float("inf"), float("nan"), 3e38, -1.0])
+def test_bounds_that_are_none_stay_inside_the_lists(kvc, n_rows, unit):
+    """A buffer that was never filled may hold any units: the lists are then of any blocks, but still lists."""
+    c = Cache(kvc, [16 * 700], H_KV=2, D=64)
+    try:
+        codes, units = random_bounds(c, 3)
+        kvc.kvc_block_bounds_views(c.pool, 0, c.bounds)[1][:] = unit
+        q = bf16(np.random.default_rng(2).standard_normal((n_rows, 8, 64))).cuda()
+        rows = [(0, 16 * 700 - 1 - i) for i in range(n_rows)]
+        seqs, pos = c.rows(rows)
+        for top_k in (5, 60, 128, 400):
+            room = torch.full((n_rows + 4, 2, top_k), -77, dtype=torch.int32, device="cuda")
+            kvc.kvc_select_blocks(c.pool, 0, c.bounds, q, dev(c.table), pos, room[:n_rows], seq_ids=seqs, sink=1, recent=1)
+            torch.cuda.synchronize()
+            assert torch.all(room[n_rows:] == -77)
+            got = room[:n_rows].cpu().numpy()
+            for i in (0, n_rows // 2, n_rows - 1):
+                for h in range(2):
+                    used = got[i, h][got[i, h] >= 0]
+                    assert np.all(np.diff(used) > 0) and np.all(got[i, h][len(used):] == -1)
+                    assert used.max() == rows[i][1] // 16 and (unit != unit or used.min() == 0)
+    finally:
+        c.close()
+
+
 def test_long_selection(kvc):
     """Hundreds of thousands of blocks in one row, lists of tens of thousands."""
     c = Cache(kvc, [1, 200000 * 1], H_KV=1, D=64, bs=1)
