@@ -8,13 +8,20 @@ namespace kvc {
 
 // Weights enter the value product as a bf16 high / low pair for up to 16 query heads per KV head, as one bf16 with more
 // (as in kvc_decode_attn_mod).
-SparseKernel select_sparse_bf16(int D, int g)
+template <int D, int W>
+static SparseKernel pick(int g)
 {
-    if (D == 64)
-        return n_tiles(g) == 1 ? sparse_instance<64, 1, KV_BF16, true>()
-                               : (n_tiles(g) == 2 ? sparse_instance<64, 2, KV_BF16, true>() : sparse_instance<64, 4, KV_BF16, false>());
-    return n_tiles(g) == 1 ? sparse_instance<128, 1, KV_BF16, true>()
-                           : (n_tiles(g) == 2 ? sparse_instance<128, 2, KV_BF16, true>() : sparse_instance<128, 4, KV_BF16, false>());
+    switch (n_tiles(g)) {
+    case 1: return sparse_instance<D, 1, KV_BF16, true, W>();
+    case 2: return sparse_instance<D, 2, KV_BF16, true, W>();
+    }
+    return sparse_instance<D, 4, KV_BF16, false, W>();
+}
+
+SparseKernel select_sparse_bf16(int D, int g, int warps)
+{
+    if (D == 64) return warps == 2 ? pick<64, 2>(g) : pick<64, 4>(g);
+    return warps == 2 ? pick<128, 2>(g) : pick<128, 4>(g);
 }
 
 static bool aligned(const void *ptr, size_t a) { return (reinterpret_cast<uintptr_t>(ptr) & (a - 1)) == 0; }
@@ -48,8 +55,15 @@ extern "C" kvc_status kvc_sparse_attn(kvc_pool *pool, int32_t layer, const void 
     const kvc_status st = check_device(pool);
     if (st != KVC_OK) return st;
     if (!pool->tmap_sub_ok) return KVC_ERR_CUDA;
-    const SparseKernel k = pool->dtype == KVC_BF16 ? select_sparse_bf16(D, g)
-                                                   : (pool->dtype == KVC_INT4 ? select_sparse_int4(g) : select_sparse_fp8(g));
+    const int64_t units = n_rows * pool->H_KV;
+    // Warps of a CTA: four, and two where there are more CTAs than a GPU takes in several turns, as in a chunk's rows: their
+    // starts and ends then overlap better and fewer warps' partials are joined.  Measured with four and with two, lists of
+    // 64 blocks, 8 KV heads: 512 rows of one sequence 149 and 140 us (bf16), 120 and 115 (e4m3), 156 and 154 (int4), with 16
+    // query heads per KV head 211 and 200, 191 and 178, 241 and 217; 256 rows of one sequence 82 and 83 (bf16); 64
+    // sequences of different lengths 48 and 60, 256 of them 150 and 164: a long row beside short ones wants more warps.
+    const int warps = units >= 16ll * pool->num_sms ? 2 : 4;
+    const SparseKernel k = pool->dtype == KVC_BF16 ? select_sparse_bf16(D, g, warps)
+                                                   : (pool->dtype == KVC_INT4 ? select_sparse_int4(g, warps) : select_sparse_fp8(g, warps));
     if (k.k.ctas_per_sm <= 0) return KVC_ERR_CUDA;
     SparseParams sp{};
     DecodeParams &p = sp.m.d;
@@ -78,9 +92,9 @@ extern "C" kvc_status kvc_sparse_attn(kvc_pool *pool, int32_t layer, const void 
     sp.top_k = top_k;
     sp.sub = pool->bs / kBS;
     // CTAs per (row, KV head): as many as the grid has room for, each with a few tiles for every warp
-    const int64_t units = n_rows * pool->H_KV, tiles = static_cast<int64_t>(top_k) * sp.sub;
+    const int64_t tiles = static_cast<int64_t>(top_k) * sp.sub;
     int c = 1;
-    while (c < kSparseMost && units * c * 2 <= static_cast<int64_t>(pool->num_sms) * k.k.ctas_per_sm && tiles >= 2 * kWarps * c) c *= 2;
+    while (c < kSparseMost && units * c * 2 <= static_cast<int64_t>(pool->num_sms) * k.k.ctas_per_sm && tiles >= 2 * warps * c) c *= 2;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -89,7 +103,7 @@ extern "C" kvc_status kvc_sparse_attn(kvc_pool *pool, int32_t layer, const void 
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(n_rows * c), pool->H_KV);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(32 * warps);
     cfg.dynamicSmemBytes = static_cast<size_t>(k.k.smem);
     cfg.stream = static_cast<cudaStream_t>(stream);
     cfg.attrs = attr;

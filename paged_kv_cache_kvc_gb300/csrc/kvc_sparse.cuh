@@ -6,16 +6,16 @@
 // (scores of the tile on tensor cores with the positions as rows, running maximum and sum in registers, weights
 // into the value product).
 //
-// Decomposition: a cluster of C CTAs (1, 2, 4 or 8) per (row, KV head), 4 warps each; warp w of CTA c takes tiles
-// c + C (w + 4 i), T of them at a time (32 positions, for up to 16 query heads), through a ring of TMA stages of its
+// Decomposition: a cluster of C CTAs (1, 2, 4 or 8) per (row, KV head), W = 4 or 2 warps each; warp w of CTA c takes
+// tiles c + C (w + W i), T of them at a time (32 positions, for up to 16 query heads), through a ring of TMA stages of its
 // own.  A step's instructions wait on one another (products, maximum, exponentials, products), so what counts is how
 // much a step does: two tiles to a step share the maximum over lanes, the rescaling and the loop.  The warps of a CTA
 // merge in shared memory and the CTAs through distributed shared memory: no partial goes to global memory, so a call
 // needs no workspace and one launch, and two calls share nothing.
 //
 // Measured, 8 KV heads of 4 query heads of 128: one row of 64 blocks (bf16) 5.4 us back to back, a chain of list, table,
-// tile and merge; 64 ragged rows of up to 128 e4m3 blocks (160 MB) 41 us, 3.9 TB/s: the longest rows, 32 tiles a warp,
-// end it; 512 rows of 64 blocks (2.15 GB out of L2) 151 us, 14 TB/s, 39 % of the issue slots with 12 warps an SM.  One
+// tile and merge; 64 ragged rows of up to 128 e4m3 blocks (160 MB) 40 us, 3.9 TB/s: the longest rows, 32 tiles a warp,
+// end it; 512 rows of 64 blocks (2.15 GB out of L2) 140 us, 15 TB/s, with 12 warps an SM.  One
 // tile to a step took 46 and 186 us; the CTAs' sums read one by one 8.2 us for the single row.
 #pragma once
 #include "kvc_cluster.cuh"
@@ -34,18 +34,26 @@ struct SparseParams {
 
 constexpr int kSparseMost = 8;   // CTAs of a cluster
 
-template <int D, int NT, int KIND>
+// W: warps of a CTA
+template <int D, int NT, int KIND, int W>
 struct SparseCfg {
     using C = DecodeCfg<D, KIND>;
     static constexpr int T = NT == 4 ? 1 : 2;          // tiles per step (more columns leave no registers for two)
-    // tiles in flight per warp, so that shared memory holds what registers hold: bf16 two (64 KB a CTA, three CTAs or 12
-    // warps to an SM), e4m3 three (48 KB, four CTAs), int4 six
+    // tiles in flight per warp, so that shared memory holds what registers hold: bf16 two (64 KB for four warps, 12 warps
+    // to an SM), e4m3 three (48 KB, 16 warps), int4 six
     static constexpr int R = KIND == KV_BF16 ? (D == 64 ? 3 : 2) : (KIND == KV_E4M3 ? 3 : 6);
-    static constexpr int RING = kWarps * R * C::STAGE;
+    static constexpr int RING = W * R * C::STAGE;
     static constexpr int QW = NT * 8;
-    static constexpr int MERGE = (kWarps * QW * 2 + kWarps * QW * D) * 4;   // the warps' partials, in the ring's place
+    // The warps' partials, in the ring's place.  A column has a row of COL floats, so long that the lanes of one store
+    // spread over all banks: four lanes hold columns of neighbouring places and eight hold channels, one each in a row of
+    // eight (bf16) or four each at 16 apart (the others).
+    static constexpr int COL = D + (KIND == KV_BF16 ? 8 : 4);
+    static constexpr int MERGE = (W * QW * 2 + W * QW * COL) * 4;
     static constexpr int BARS = RING > MERGE ? RING : MERGE;                // offset of the barriers
-    static constexpr int SMEM = 1024 /* alignment */ + BARS + kWarps * R * 8;
+// Warps that an SM keeps, for the compiler: one CTA's registers above a third of 64 K, say, would leave room for two
+    // only (e4m3 with 16 heads per KV head at 177 registers instead of 168: 63 us instead of 54, 64 sequences).
+    static constexpr int CTAS = (NT == 1 ? 16 : (NT == 2 ? 12 : 8)) / W;
+    static constexpr int SMEM = 1024 /* alignment */ + BARS + W * R * 8;
 };
 
 // One step of a warp's running softmax: T tiles of 16 positions at st[t], of which the first valid[t] are read (all of
@@ -258,10 +266,10 @@ __device__ __forceinline__ void tiles_update(float scale_log2, const uint32_t (&
 }
 
 // grid (C x rows, KV head), clusters of C CTAs along x
-template <int D, int NT, int KIND, bool PSPLIT>
-__global__ void __launch_bounds__(kThreads) sparse_kernel(const __grid_constant__ CUtensorMap tmap, const SparseParams sp)
+template <int D, int NT, int KIND, bool PSPLIT, int W>
+__global__ void __launch_bounds__(32 * W, SparseCfg<D, NT, KIND, W>::CTAS) sparse_kernel(const __grid_constant__ CUtensorMap tmap, const SparseParams sp)
 {
-    using S = SparseCfg<D, NT, KIND>;
+    using S = SparseCfg<D, NT, KIND, W>;
     using C = DecodeCfg<D, KIND>;
     constexpr bool INT4 = KIND == KV_INT4, QUANT = KIND != KV_BF16;
     constexpr int QW = S::QW, T = S::T, R = S::R;
@@ -289,7 +297,7 @@ __global__ void __launch_bounds__(kThreads) sparse_kernel(const __grid_constant_
     const int seq = sp.seqs ? __ldg(sp.seqs + row) : row;
     const int pos = __ldg(sp.positions + row);
     const int32_t *list = sp.lists + (static_cast<size_t>(row) * p.H_KV + h) * sp.top_k;
-    const int first = rank + cs * warp, step = cs * kWarps, listed = sp.top_k * sp.sub;   // this warp's tiles
+    const int first = rank + cs * warp, step = cs * W, listed = sp.top_k * sp.sub;   // this warp's tiles
     auto load_entry = [&](int jj) {
         const int t = first + step * jj;
         return t < listed ? __ldg(list + t / sp.sub) : -1;
@@ -476,37 +484,46 @@ __global__ void __launch_bounds__(kThreads) sparse_kernel(const __grid_constant_
     // ---- the warps' partials to shared memory (the ring is free), then one sum per CTA, then one per cluster
     __syncthreads();
     float *cm = reinterpret_cast<float *>(smem);
-    float *cl = cm + kWarps * QW;
-    float *co = cl + kWarps * QW;   // [warp][column][D]
+    float *cl = cm + W * QW;
+    float *co = cl + W * QW;   // [warp][place of column][COL]
+    constexpr int COL = S::COL;
+    auto place = [](int qi) { return (qi & ~7) + 4 * (qi & 1) + ((qi & 7) >> 1); };   // even columns first: a lane has two
 #pragma unroll
-    for (int jn = 0; jn < NT; ++jn) {
+    for (int jn = 0; jn < NT; ++jn)
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+        for (int c = 0; c < 2; ++c) {
+            const int qi = 8 * jn + 2 * tg + c;
+            if (qi >= p.g) continue;
             if (gq == 0) {
-                cm[warp * QW + 8 * jn + 2 * tg + c] = m_run[jn][c];
-                cl[warp * QW + 8 * jn + 2 * tg + c] = l_run[jn][c];
+                cm[warp * QW + qi] = m_run[jn][c];
+                cl[warp * QW + qi] = l_run[jn][c];
             }
+            float *col = co + (warp * QW + place(qi)) * COL;
+            if constexpr (QUANT) {   // channels gq D/8 + 2 mt and the one behind it
 #pragma unroll
-        for (int mt = 0; mt < C::MT; ++mt)
+                for (int mt = 0; mt < C::MT; mt += 2)
+                    *reinterpret_cast<float4 *>(col + gq * (D / 8) + 2 * mt) =
+                        make_float4(oacc[mt][jn][c], oacc[mt][jn][c + 2], oacc[mt + 1][jn][c], oacc[mt + 1][jn][c + 2]);
+            } else {   // 16 mt + gq and the one 8 behind it
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const int qi = 8 * jn + 2 * tg + (c & 1);
-                const int dim = QUANT ? gq * (D / 8) + 2 * mt + (c >> 1) : 16 * mt + gq + 8 * (c >> 1);
-                co[(warp * QW + qi) * D + dim] = oacc[mt][jn][c];
+                for (int mt = 0; mt < C::MT; ++mt) {
+                    col[16 * mt + gq] = oacc[mt][jn][c];
+                    col[16 * mt + gq + 8] = oacc[mt][jn][c + 2];
+                }
             }
-    }
+        }
     __syncthreads();
-    for (int i = threadIdx.x; i < p.g * (D / 2); i += kThreads) {
+    for (int i = threadIdx.x; i < p.g * (D / 2); i += 32 * W) {
         const int qi = i / (D / 2), d = 2 * (i - qi * (D / 2));
         float M = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, cm[w * QW + qi]);
+        for (int w = 0; w < W; ++w) M = fmaxf(M, cm[w * QW + qi]);
         const float Mref = M == -INFINITY ? 0.f : M;
         float L = 0.f, O0 = 0.f, O1 = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
+        for (int w = 0; w < W; ++w) {
             const float e = fast_exp2(cm[w * QW + qi] - Mref);   // warps that read nothing: exp2(-inf) = 0
-            const float2 o = *reinterpret_cast<const float2 *>(co + (w * QW + qi) * D + d);
+            const float2 o = *reinterpret_cast<const float2 *>(co + (w * QW + place(qi)) * COL + d);
             L += e * cl[w * QW + qi];
             O0 += e * o.x;
             O1 += e * o.y;
@@ -521,7 +538,7 @@ __global__ void __launch_bounds__(kThreads) sparse_kernel(const __grid_constant_
             *reinterpret_cast<uint32_t *>(mp.out + (orow + qi) * D + d) = pack_bf16(O0 * inv, O1 * inv);
             if (d == 0 && p.lse) p.lse[orow + qi] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
         } else {   // in the first warp's place, which no other thread reads
-            *reinterpret_cast<float2 *>(co + qi * D + d) = make_float2(O0, O1);
+            *reinterpret_cast<float2 *>(co + place(qi) * COL + d) = make_float2(O0, O1);
             if (d == 0) part[qi] = make_float2(M, L);
         }
     }
@@ -529,7 +546,7 @@ __global__ void __launch_bounds__(kThreads) sparse_kernel(const __grid_constant_
 
     // CTA `rank` finishes its part of the group's channels from all CTAs' sums
     cluster_sync();
-    for (int i = rank * kThreads + threadIdx.x; i < p.g * (D / 4); i += cs * kThreads) {
+    for (int i = rank * 32 * W + threadIdx.x; i < p.g * (D / 4); i += cs * 32 * W) {
         const int qi = i / (D / 4), d = 4 * (i - qi * (D / 4));
         float2 ml[kSparseMost];
         float4 o[kSparseMost];
@@ -539,7 +556,7 @@ __global__ void __launch_bounds__(kThreads) sparse_kernel(const __grid_constant_
             o[r] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (r < cs) {
                 ml[r] = cluster_ld2(cluster_addr(smem_u32(part + qi), r));
-                o[r] = cluster_ld4(cluster_addr(smem_u32(co + qi * D + d), r));
+                o[r] = cluster_ld4(cluster_addr(smem_u32(co + place(qi) * COL + d), r));
             }
         }
         float M = -INFINITY;
@@ -570,17 +587,17 @@ struct SparseKernel {
     DecodeKernel k;
 };
 
-template <int D, int NT, int KIND, bool PSPLIT>
+template <int D, int NT, int KIND, bool PSPLIT, int W>
 SparseKernel sparse_instance()
 {
     struct Tag {};
-    return {&sparse_kernel<D, NT, KIND, PSPLIT>,
-            configured<Tag>(reinterpret_cast<const void *>(&sparse_kernel<D, NT, KIND, PSPLIT>), SparseCfg<D, NT, KIND>::SMEM,
-                            kThreads, false)};
+    return {&sparse_kernel<D, NT, KIND, PSPLIT, W>,
+            configured<Tag>(reinterpret_cast<const void *>(&sparse_kernel<D, NT, KIND, PSPLIT, W>), SparseCfg<D, NT, KIND, W>::SMEM,
+                            32 * W, false)};
 }
 
-SparseKernel select_sparse_bf16(int D, int g);
-SparseKernel select_sparse_fp8(int g);
-SparseKernel select_sparse_int4(int g);
+SparseKernel select_sparse_bf16(int D, int g, int warps);
+SparseKernel select_sparse_fp8(int g, int warps);
+SparseKernel select_sparse_int4(int g, int warps);
 
 }  // namespace kvc

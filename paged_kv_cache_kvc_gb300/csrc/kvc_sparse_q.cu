@@ -3,17 +3,17 @@
 
 namespace kvc {
 
-template <int KIND>
+template <int KIND, int W>
 static SparseKernel pick(int g)
 {
     switch (n_tiles(g)) {
-    case 1: return sparse_instance<128, 1, KIND, false>();
-    case 2: return sparse_instance<128, 2, KIND, false>();
+    case 1: return sparse_instance<128, 1, KIND, false, W>();
+    case 2: return sparse_instance<128, 2, KIND, false, W>();
     }
-    return sparse_instance<128, 4, KIND, false>();
+    return sparse_instance<128, 4, KIND, false, W>();
 }
 
-SparseKernel select_sparse_fp8(int g) { return pick<KV_E4M3>(g); }
-SparseKernel select_sparse_int4(int g) { return pick<KV_INT4>(g); }
+SparseKernel select_sparse_fp8(int g, int warps) { return warps == 2 ? pick<KV_E4M3, 2>(g) : pick<KV_E4M3, 4>(g); }
+SparseKernel select_sparse_int4(int g, int warps) { return warps == 2 ? pick<KV_INT4, 2>(g) : pick<KV_INT4, 4>(g); }
 
 }  // namespace kvc

@@ -495,6 +495,27 @@ def test_long_lists_of_many_rows(kvc, dtype, g, top_k):
         c.close()
 
 
+@pytest.mark.parametrize("dtype,D,g", [("bf16", 64, 5), ("bf16", 128, 4), ("bf16", 128, 13), ("bf16", 128, 32), ("fp8", 128, 1),
+                                       ("fp8", 128, 16), ("int4", 128, 8), ("int4", 128, 27)])
+@pytest.mark.parametrize("top_k", [1, 13, 100])
+def test_thousands_of_rows(kvc, dtype, D, g, top_k):
+    """Rows for several turns of the whole GPU, whose CTAs have fewer warps; short ones, empty ones and padding among them."""
+    c = Cache(kvc, [2600, 33], H_KV=2, D=D, dtype=dtype)
+    try:
+        rows = [(0, p) for p in range(2600)] + [(1, p) for p in range(33)] + [(-1, 5), (1, -1)]
+        q = bf16(np.random.default_rng(top_k).standard_normal((len(rows), 2 * g, D)) * 2).cuda()
+        lists = random_lists(c, rows, top_k, 1, shuffle=top_k == 13)
+        lists[2000] = -1
+        out, lse = attend_rows(c, q, rows, lists)
+        assert kvc.kvc_pool_sync_status(c.pool) == kvc.KVC_OK
+        keep = [0, 1, 15, 16, 17, 511, 1999, 2000, 2001, 2598, 2599, 2600, 2616, 2632, 2633, 2634]
+        check_attend(c, q[keep], [rows[i] for i in keep], dev(lists[keep]), out[keep], lse[keep])
+        few, few_l = attend_rows(c, q[keep].contiguous(), [rows[i] for i in keep], lists[keep])   # more warps, clusters
+        check_attend(c, q[keep], [rows[i] for i in keep], dev(lists[keep]), few, few_l)
+    finally:
+        c.close()
+
+
 @pytest.mark.parametrize("n_q", [2, 45, 700])
 def test_chunks_and_padding(kvc, n_q):
     c = Cache(kvc, [1500, 90], H_KV=2, D=64)
