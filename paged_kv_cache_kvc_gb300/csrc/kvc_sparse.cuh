@@ -14,8 +14,8 @@
 // needs no workspace and one launch, and two calls share nothing.
 //
 // Measured, 8 KV heads of 4 query heads of 128: one row of 64 blocks (bf16) 5.4 us back to back, a chain of list, table,
-// tile and merge; 64 ragged rows of up to 128 e4m3 blocks (160 MB) 40 us, 3.9 TB/s: the longest rows, 32 tiles a warp,
-// end it; 512 rows of 64 blocks (2.15 GB out of L2) 140 us, 15 TB/s, with 12 warps an SM.  One
+// tile and merge; 64 ragged rows of up to 128 e4m3 blocks (160 MB) 36 us, 4.4 TB/s, with the longest first (40 in their own
+// order); 512 rows of 64 blocks (2.15 GB out of L2) 140 us, 15 TB/s, with 12 warps an SM.  One
 // tile to a step took 46 and 186 us; the CTAs' sums read one by one 8.2 us for the single row.
 #pragma once
 #include "kvc_cluster.cuh"
@@ -30,9 +30,11 @@ struct SparseParams {
     const int32_t *lists;      // [rows][H_KV][top_k]
     int32_t top_k;
     int32_t sub;               // tiles per block: bs / 16
+    bool longest_first;        // rows are taken in the order of what they read
 };
 
 constexpr int kSparseMost = 8;   // CTAs of a cluster
+constexpr int kOrderMost = 512;  // rows that are ordered
 
 // W: warps of a CTA
 template <int D, int NT, int KIND, int W>
@@ -265,6 +267,63 @@ __device__ __forceinline__ void tiles_update(float scale_log2, const uint32_t (&
     }
 }
 
+// The row of rank r when at most kOrderMost rows are ordered by what they read, most first: 32 classes, in a class by
+// number.  Every CTA finds its own row so, from the positions alone (about 1 us before the first tile).
+template <int W>
+__device__ __forceinline__ int row_of_rank(const SparseParams &sp, int rows, int r)
+{
+    __shared__ int in_class[32];
+    __shared__ __align__(16) uint32_t cls[kOrderMost / 4];   // of every row, in bytes
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int bs = sp.sub * kBS;
+    int pos[kOrderMost / (32 * W)];
+#pragma unroll
+    for (int u = 0; u < kOrderMost / (32 * W); ++u) pos[u] = tid + 32 * W * u < rows ? __ldg(sp.positions + tid + 32 * W * u) : -1;
+    if (tid < 32) in_class[tid] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kOrderMost / (32 * W); ++u) {
+        const int i = tid + 32 * W * u;
+        const int n = pos[u] < 0 ? 0 : min(pos[u] / bs + 1, sp.top_k);
+        const int c = i < rows ? 31 - static_cast<int>(31.f * static_cast<float>(n) / static_cast<float>(sp.top_k)) : 32;
+        reinterpret_cast<uint8_t *>(cls)[i] = static_cast<uint8_t>(c);
+        if (c < 32) atomicAdd(&in_class[c], 1);
+    }
+    __syncthreads();
+    auto before = [&](int n) {   // sum of the lanes before this one
+        int sum = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(kFull, sum, o);
+            if (lane >= o) sum += y;
+        }
+        return sum - n;
+    };
+    // the class that holds rank r, and how many rows of it come before
+    const int n = in_class[lane], ahead = before(n);
+    const int c = __popc(__ballot_sync(kFull, ahead + n <= r));
+    const int left = r - __shfl_sync(kFull, ahead, c);
+    // a lane's rows are kOrderMost / 32 neighbours
+    constexpr int kWords = kOrderMost / 128;
+    uint32_t is[kWords];
+    int mine = 0;
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) {
+        is[w] = __vcmpeq4(cls[lane * kWords + w], 0x01010101u * static_cast<uint32_t>(c));
+        mine += __popc(is[w]) >> 3;
+    }
+    int row = 0, k = left - before(mine);   // the k-th of this lane's
+    if (k >= 0 && k < mine) {
+#pragma unroll
+        for (int x = 0; x < kOrderMost / 32; ++x)
+            if ((is[x / 4] >> (8 * (x % 4))) & 1u) {
+                if (k == 0) row = lane * (kOrderMost / 32) + x;
+                --k;
+            }
+    }
+    return __reduce_max_sync(kFull, row);
+}
+
 // grid (C x rows, KV head), clusters of C CTAs along x
 template <int D, int NT, int KIND, bool PSPLIT, int W>
 __global__ void __launch_bounds__(32 * W, SparseCfg<D, NT, KIND, W>::CTAS) sparse_kernel(const __grid_constant__ CUtensorMap tmap, const SparseParams sp)
@@ -279,11 +338,9 @@ __global__ void __launch_bounds__(32 * W, SparseCfg<D, NT, KIND, W>::CTAS) spars
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ float2 part[QW];   // this CTA's (maximum, sum) of every column
     const int cs = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
-    const int row = static_cast<int>(blockIdx.x / static_cast<unsigned>(cs)), h = blockIdx.y;
+    int row = static_cast<int>(blockIdx.x / static_cast<unsigned>(cs)), h = blockIdx.y;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int gq = lane >> 2, tg = lane & 3;
-    const size_t orow = static_cast<size_t>(row) * p.H_Q + static_cast<size_t>(h) * p.g;   // of the group's first head
-
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::BARS) + warp * R;   // this warp's
     if (lane == 0) {
         for (int i = 0; i < R; ++i) mbar_init(smem_u32(&bars[i]), 1);
@@ -291,6 +348,12 @@ __global__ void __launch_bounds__(32 * W, SparseCfg<D, NT, KIND, W>::CTAS) spars
     }
     if (threadIdx.x == 0) prefetch_tensormap(&tmap);
     grid_dependency_wait();
+    if (sp.longest_first) {
+        const int unit = (blockIdx.y * gridDim.x + blockIdx.x) / cs;
+        h = unit % gridDim.y;
+        row = row_of_rank<W>(sp, gridDim.x / cs, unit / gridDim.y);
+    }
+    const size_t orow = static_cast<size_t>(row) * p.H_Q + static_cast<size_t>(h) * p.g;   // of the group's first head
 
     // What is known from the row alone is on its way before the first answer: sequence, position, this lane's list
     // entries and the queries.

@@ -516,6 +516,37 @@ def test_thousands_of_rows(kvc, dtype, D, g, top_k):
         c.close()
 
 
+@pytest.mark.parametrize("dtype,H_KV,B,n_rows,top_k", [("bf16", 8, 64, 64, 40), ("bf16", 4, 97, 90, 7), ("fp8", 2, 512, 512, 9),
+                                                       ("int4", 8, 33, 33, 64), ("fp8", 8, 130, 130, 3), ("bf16", 1, 512, 400, 1)])
+def test_batches_of_different_lengths(kvc, dtype, H_KV, B, n_rows, top_k):
+    """Decoding batches that fill the GPU once or a few times, whose rows are taken in an order of their own: lengths that
+    are equal, rising, zero (padding) and wrong, rows that are not the sequences in order, and unused sequences."""
+    r = np.random.default_rng(n_rows + top_k)
+    lens = [int(n) for n in r.integers(1, 900, B)]
+    lens[:6] = [1, 16, 17, 900, 900, 900]
+    c = Cache(kvc, lens, H_KV=H_KV, dtype=dtype)
+    try:
+        order = [int(b) for b in r.permutation(B)[:n_rows]]
+        rows = [(b, lens[b] - 1) for b in order]
+        rows[3] = rows[n_rows - 1] = (-1, -1)
+        q = bf16(r.standard_normal((n_rows, 2 * H_KV, 128)) * 2).cuda()
+        lists = random_lists(c, rows, top_k, 2, shuffle=n_rows == 90)
+        out, lse = attend_rows(c, q, rows, lists)
+        assert kvc.kvc_pool_sync_status(c.pool) == kvc.KVC_OK
+        check_attend(c, q, rows, dev(lists), out, lse)
+        # a row out of range is recorded and sums nothing; the others keep their bits
+        seqs, pos = c.rows(rows)
+        pos[5], pos[6] = 2 ** 31 - 1, -7
+        bad, bad_l = torch.full_like(out, 7.0), torch.full_like(lse, 7.0)
+        kvc.kvc_sparse_attn(c.pool, 0, q, dev(c.table), pos, dev(lists), bad, bad_l, seq_ids=seqs)
+        assert kvc.kvc_pool_sync_status(c.pool) == kvc.KVC_ERR_RANGE
+        same = [i for i in range(n_rows) if i not in (5, 6)]
+        assert torch.equal(bad[same], out[same]) and torch.equal(bad_l[same], lse[same])
+        assert torch.all(bad[5:7] == 0) and torch.all(bad_l[5:7] == -float("inf"))
+    finally:
+        c.close()
+
+
 @pytest.mark.parametrize("n_q", [2, 45, 700])
 def test_chunks_and_padding(kvc, n_q):
     c = Cache(kvc, [1500, 90], H_KV=2, D=64)
