@@ -87,8 +87,9 @@ __global__ void __launch_bounds__(kBoundsThreads, KIND == KV_BF16 && D == 128 ? 
         const int32_t slot = __ldg(p.slots + r);
         if (slot < -1 || (slot >= 0 && slot / p.bs >= p.N)) {
             atomicOr(p.err, KVC_EBIT_BAD_BLOCK);
-        } else if (slot >= 0 && ((slot + 1) % p.bs == 0 || r + 1 == p.rows || __ldg(p.slots + r + 1) != slot + 1)) {
-            ends[atomicAdd(&n_ends, 1)] = make_int2(slot / p.bs, slot % p.bs);
+        } else if (slot >= 0) {   // rows of a block ascend, not always by one
+            const int32_t blk = slot / p.bs, behind = r + 1 < p.rows ? __ldg(p.slots + r + 1) : -1;
+            if (behind < 0 || behind / p.bs != blk) ends[atomicAdd(&n_ends, 1)] = make_int2(blk, slot - blk * p.bs);
         }
     }
     __syncthreads();

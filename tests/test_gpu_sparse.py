@@ -118,6 +118,21 @@ def test_bounds_of_many_rows(kvc, rows):
             c.close()
 
 
+@pytest.mark.parametrize("H_KV", [1, 2, 3])
+def test_bounds_of_rows_that_skip_places(kvc, H_KV):
+    """The rows of a block ascend but need not follow one another, and one may come twice: the last counts."""
+    c = Cache(kvc, [16 * 3000], H_KV=H_KV, D=64)
+    try:
+        slots = np.concatenate([b * 16 + np.array([0, 3, 9, 9, 14]) for b in c.table[0]]).astype(np.int32)
+        for _ in range(5):
+            c.bounds.zero_()
+            c.kvc.kvc_update_bounds(c.pool, 0, c.bounds, dev(slots))
+            check_bounds(c, slots)
+        assert kvc.kvc_pool_sync_status(c.pool) == kvc.KVC_OK
+    finally:
+        c.close()
+
+
 def test_bounds_of_unusual_keys(kvc):
     """Zeros, subnormals, the largest values, infinities, NaN; what stands behind the last token is not read."""
     big = torch.finfo(torch.bfloat16).max
