@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kBoundsThreads, KIND == KV_BF16 && D == 128 ? 
 // into `keys` in shared memory.  Lists of up to 128 blocks are ranked from a few candidates; for longer ones, and for
 // many equal keys, the k-th largest key is found digit by digit over the cluster's histograms, and each CTA writes its
 // part of the list in order.
-// One row of 512 blocks and 8 KV heads takes 7.4 us back to back: launch, table and codes 4, the groups' maxima, the
+// One row of 512 blocks and 8 KV heads takes 7.1 us back to back: launch, table and codes 4, the groups' maxima, the
 // limit, the candidates and their ranks a barrier each (10.2 with the digits alone).  16 rows of 8192 blocks (273 MB) 57
 // us: the scores stream at 7 TB/s, then every CTA of the one wave ranks at once.
 template <int D>
