@@ -8,6 +8,7 @@
 // the blocks chosen depend on the inputs alone, not on the grid, and equal scores go to the lower block.
 #include <algorithm>
 
+#include "kvc_order.cuh"
 #include "kvc_select.cuh"
 
 namespace kvc {
@@ -317,10 +318,12 @@ __device__ __forceinline__ void select_row(const SelectParams &p, const int64_t 
 
     // ---- scores of this CTA's blocks, 32 blocks a warp at a time
     const int c = lane % LPR, sub = lane / LPR;
+    int next_phys = warp * 32 + lane < n ? __ldg(bt + j0 + warp * 32 + lane) : -1;
     for (int t0 = warp * 32; t0 < n; t0 += kSelThreads) {
         const int j = j0 + t0 + lane;
         const bool in = t0 + lane < n;
-        int phys = in ? __ldg(bt + j) : -1;
+        int phys = next_phys;
+        next_phys = t0 + kSelThreads + lane < n ? __ldg(bt + j + kSelThreads) : -1;
         if (in && (phys < 0 || static_cast<int64_t>(phys) >= p.N)) {
             if (h == 0) atomicOr(p.err, KVC_EBIT_BAD_BLOCK);
             phys = -1;
@@ -591,7 +594,13 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
     extern __shared__ uint32_t keys[];
     const unsigned cs = cluster_size();
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    select_row<D>(p, blockIdx.x / cs, blockIdx.y, static_cast<int>(cs), static_cast<int>(cluster_rank()), keys);
+    int row = static_cast<int>(blockIdx.x / cs), h = blockIdx.y;
+    if (p.longest_first) {
+        const int unit = static_cast<int>((blockIdx.y * gridDim.x + blockIdx.x) / cs);
+        h = unit % gridDim.y;
+        row = row_of_rank<kSelThreads>(p.positions, gridDim.x / cs, p.bs, p.max_blocks, unit / gridDim.y);
+    }
+    select_row<D>(p, row, h, static_cast<int>(cs), static_cast<int>(cluster_rank()), keys);
 }
 
 // The rows that select_tiles left unlisted.  grid (8 rows, KV head)
@@ -650,16 +659,25 @@ static kvc_status launch_select(const SelectParams &p, int64_t rows, int sms, cu
     // blocks while they fill the GPU twice over, or 128 while they leave half of it free.  Measured, 8 KV heads: one row
     // of 256 blocks 6.1 us with one CTA, 6.6 with two; 512 blocks 8.2, 7.1 and 6.7 with one, two and four; 8 rows of 512
     // blocks 8.0 with two, 8.5 with four; 16 rows of 8192 blocks 57.5 with four, 61.4 with eight.
+    // A CTA has 4096 blocks at most, or 2048 while they fill the GPU four times over: it takes 13 us for 1024 blocks, so one
+    // long row would outlast the others.  64 rows of up to 8192 blocks, with one, two and four: 100, 59 and 61 us (all of
+    // them long: 212, 192 and 201); 32 rows, with two and four: 54 and 35 (100 and 105).
     int c = 1;
     auto more = [&] {
         return (units * c < 2ll * sms && p.max_blocks > 256 * c) ||
-               (units * c * 2 <= sms && p.max_blocks > 256 && p.max_blocks > 128 * c) || p.max_blocks > kSelKeys / 2 * c;
+               (units * c * 2 <= sms && p.max_blocks > 256 && p.max_blocks > 128 * c) ||
+               (units * c < 4ll * sms && p.max_blocks > 2048 * c) || p.max_blocks > 4096 * c;
     };
     while (c < 8 && more()) c *= 2;
+    // Measured by number and longest first: 64 rows of up to 8192 blocks 72 and 59 us, 32 rows 44 and 35; 128 rows of up to
+    // 2048 blocks 42 and 34; 64 rows of up to 512 blocks 12.2 and 10.9 (all long: 20.3 and 21.8); 16 rows of 8192 blocks
+    // 59.5 and 60.6.
+    SelectParams sp = p;
+    sp.longest_first = longest_first(rows, p.B, units, c, sms);
     if (rows * c > 0x7FFFFFFF) return KVC_ERR_UNSUPPORTED;
     const int per = (p.max_blocks + c - 1) / c;
     return launch(&select_kernel<D>, dim3(static_cast<unsigned>(rows * c), p.H_KV), kSelThreads, 4 * static_cast<size_t>(per), c,
-                  stream, p);
+                  stream, sp);
 }
 
 template <int D, int KIND>

@@ -27,6 +27,7 @@ struct SelectParams {
     const int32_t *seqs, *positions;
     int32_t top_k, sink, recent;
     int32_t *lists;            // [rows][H_KV][top_k]
+    bool longest_first;        // rows are taken in the order of what they read
     uint32_t *err;
 };
 

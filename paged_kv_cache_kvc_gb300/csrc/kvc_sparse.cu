@@ -95,13 +95,11 @@ extern "C" kvc_status kvc_sparse_attn(kvc_pool *pool, int32_t layer, const void 
     const int64_t tiles = static_cast<int64_t>(top_k) * sp.sub;
     int c = 1;
     while (c < kSparseMost && units * c * 2 <= static_cast<int64_t>(pool->num_sms) * k.k.ctas_per_sm && tiles >= 2 * warps * c) c *= 2;
-    // A decoding batch (no more rows than sequences) whose CTAs fill the GPU once or a few times: long rows first, so that no
-    // SM is left with several long ones and none begins late.  Measured by number and longest first, rows of 1 to 128 blocks,
-    // 8 KV heads: 64 rows 40.4 and 36.6 us (e4m3), 48.0 and 43.9 (bf16), 47 and 35 (int4), with 16 query heads per KV head
-    // 54 and 43 (e4m3); 128 rows 69 and 62 (e4m3), 79 and 79 (bf16); 32 rows 22.9 and 21.8.  64 rows of one length 97.7 and
-    // 99.2; finding the row costs more than it gives with clusters of 4 (16 rows 21.3 and 21.7) and when CTAs come by the
-    // thousand (256 rows 92 and 99).
-    sp.longest_first = n_rows <= std::min(B, kOrderMost) && c <= 2 && units * c > pool->num_sms && units <= 8ll * pool->num_sms;
+    // Measured by number and longest first, 64 rows of 1 to 128 blocks, 8 KV heads: 40.4 and 36.6 us (e4m3), 48.0 and 43.9
+    // (bf16), 47 and 35 (int4), with 16 query heads per KV head 54 and 43 (e4m3); 128 rows 69 and 62 (e4m3), 79 and 79
+    // (bf16); 32 rows 22.9 and 21.8.  64 rows of one length 97.7 and 99.2; finding the row costs more than it gives with
+    // clusters of 4 (16 rows 21.3 and 21.7) and when CTAs come by the thousand (256 rows 92 and 99).
+    sp.longest_first = c <= 2 && longest_first(n_rows, B, units, c, pool->num_sms);
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;

@@ -20,6 +20,7 @@
 #pragma once
 #include "kvc_cluster.cuh"
 #include "kvc_mod.cuh"
+#include "kvc_order.cuh"
 
 namespace kvc {
 
@@ -34,7 +35,6 @@ struct SparseParams {
 };
 
 constexpr int kSparseMost = 8;   // CTAs of a cluster
-constexpr int kOrderMost = 512;  // rows that are ordered
 
 // W: warps of a CTA
 template <int D, int NT, int KIND, int W>
@@ -267,63 +267,6 @@ __device__ __forceinline__ void tiles_update(float scale_log2, const uint32_t (&
     }
 }
 
-// The row of rank r when at most kOrderMost rows are ordered by what they read, most first: 32 classes, in a class by
-// number.  Every CTA finds its own row so, from the positions alone (about 1 us before the first tile).
-template <int W>
-__device__ __forceinline__ int row_of_rank(const SparseParams &sp, int rows, int r)
-{
-    __shared__ int in_class[32];
-    __shared__ __align__(16) uint32_t cls[kOrderMost / 4];   // of every row, in bytes
-    const int tid = threadIdx.x, lane = tid & 31;
-    const int bs = sp.sub * kBS;
-    int pos[kOrderMost / (32 * W)];
-#pragma unroll
-    for (int u = 0; u < kOrderMost / (32 * W); ++u) pos[u] = tid + 32 * W * u < rows ? __ldg(sp.positions + tid + 32 * W * u) : -1;
-    if (tid < 32) in_class[tid] = 0;
-    __syncthreads();
-#pragma unroll
-    for (int u = 0; u < kOrderMost / (32 * W); ++u) {
-        const int i = tid + 32 * W * u;
-        const int n = pos[u] < 0 ? 0 : min(pos[u] / bs + 1, sp.top_k);
-        const int c = i < rows ? 31 - static_cast<int>(31.f * static_cast<float>(n) / static_cast<float>(sp.top_k)) : 32;
-        reinterpret_cast<uint8_t *>(cls)[i] = static_cast<uint8_t>(c);
-        if (c < 32) atomicAdd(&in_class[c], 1);
-    }
-    __syncthreads();
-    auto before = [&](int n) {   // sum of the lanes before this one
-        int sum = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(kFull, sum, o);
-            if (lane >= o) sum += y;
-        }
-        return sum - n;
-    };
-    // the class that holds rank r, and how many rows of it come before
-    const int n = in_class[lane], ahead = before(n);
-    const int c = __popc(__ballot_sync(kFull, ahead + n <= r));
-    const int left = r - __shfl_sync(kFull, ahead, c);
-    // a lane's rows are kOrderMost / 32 neighbours
-    constexpr int kWords = kOrderMost / 128;
-    uint32_t is[kWords];
-    int mine = 0;
-#pragma unroll
-    for (int w = 0; w < kWords; ++w) {
-        is[w] = __vcmpeq4(cls[lane * kWords + w], 0x01010101u * static_cast<uint32_t>(c));
-        mine += __popc(is[w]) >> 3;
-    }
-    int row = 0, k = left - before(mine);   // the k-th of this lane's
-    if (k >= 0 && k < mine) {
-#pragma unroll
-        for (int x = 0; x < kOrderMost / 32; ++x)
-            if ((is[x / 4] >> (8 * (x % 4))) & 1u) {
-                if (k == 0) row = lane * (kOrderMost / 32) + x;
-                --k;
-            }
-    }
-    return __reduce_max_sync(kFull, row);
-}
-
 // grid (C x rows, KV head), clusters of C CTAs along x
 template <int D, int NT, int KIND, bool PSPLIT, int W>
 __global__ void __launch_bounds__(32 * W, SparseCfg<D, NT, KIND, W>::CTAS) sparse_kernel(const __grid_constant__ CUtensorMap tmap, const SparseParams sp)
@@ -351,7 +294,7 @@ __global__ void __launch_bounds__(32 * W, SparseCfg<D, NT, KIND, W>::CTAS) spars
     if (sp.longest_first) {
         const int unit = (blockIdx.y * gridDim.x + blockIdx.x) / cs;
         h = unit % gridDim.y;
-        row = row_of_rank<W>(sp, gridDim.x / cs, unit / gridDim.y);
+        row = row_of_rank<32 * W>(sp.positions, gridDim.x / cs, sp.sub * kBS, sp.top_k, unit / gridDim.y);
     }
     const size_t orow = static_cast<size_t>(row) * p.H_Q + static_cast<size_t>(h) * p.g;   // of the group's first head
 

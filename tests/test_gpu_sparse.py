@@ -237,6 +237,31 @@ def test_selection(kvc, D, g, H_KV, bs):
         c.close()
 
 
+@pytest.mark.parametrize("bs,H_KV,B,n_rows,long", [(16, 8, 64, 64, 300), (4, 4, 97, 90, 1100), (1, 2, 512, 512, 400),
+                                                   (4, 8, 33, 33, 2500), (1, 8, 20, 20, 4500)])
+def test_selection_of_batches_of_different_lengths(kvc, bs, H_KV, B, n_rows, long):
+    """Decoding batches that fill the GPU once or a few times, whose rows are taken in an order of their own: up to `long`
+    blocks, equal lengths, one token, padding, positions out of range, rows that are not the sequences in order."""
+    r = np.random.default_rng(n_rows + bs)
+    lens = [int(n) for n in bs * long * r.random(B) ** 4 + 1]
+    lens[:6] = [1, bs, bs + 1, bs * long, bs * long, bs * long - 1]
+    c = Cache(kvc, lens, H_KV=H_KV, D=64, bs=bs)
+    try:
+        codes, units = random_bounds(c, 3)
+        order = [int(b) for b in r.permutation(B)[:n_rows]]
+        rows = [(b, lens[b] - 1) for b in order]
+        rows[3] = rows[n_rows - 1] = (-1, -1)
+        rows[5], rows[6] = (order[5], 2 ** 31 - 1), (order[6], -7)
+        q = bf16(r.standard_normal((n_rows, 2 * H_KV, 64))).cuda()
+        got = select(c, q, rows, 24, 1, 2)
+        assert kvc.kvc_pool_sync_status(c.pool) == kvc.KVC_ERR_RANGE
+        assert torch.all(got[5:7] == -1)
+        fine = [i for i in range(n_rows) if i not in (5, 6)]
+        check_select(c, q[fine], [rows[i] for i in fine], codes, units, got[fine], 24, 1, 2)
+    finally:
+        c.close()
+
+
 @pytest.mark.parametrize("n_q", [3, 40, 333])
 def test_selection_of_chunks_and_padding(kvc, n_q):
     c = Cache(kvc, [2000, 3100, 60], H_KV=2, D=64)
