@@ -236,8 +236,9 @@ __global__ void __launch_bounds__(kBoundsThreads, KIND == KV_BF16 && D == 128 ? 
 // many equal keys, the k-th largest key is found digit by digit over the cluster's histograms, and each CTA writes its
 // part of the list in order.
 // One row of 512 blocks and 8 KV heads takes 7.1 us back to back: launch, table and codes 4, the groups' maxima, the
-// limit, the candidates and their ranks a barrier each (10.2 with the digits alone).  16 rows of 8192 blocks (273 MB) 57
-// us: the scores stream at 7 TB/s, then every CTA of the one wave ranks at once.
+// limit, the candidates and their ranks a barrier each (10.2 with the digits alone).  16 rows of 8192 blocks (273 MB) 59
+// us: the scores stream at 7 TB/s, then every CTA of the one wave ranks at once.  The next records copied to shared memory
+// during the products left room for fewer CTAs (73 us).
 template <int D>
 __device__ __forceinline__ void select_row(const SelectParams &p, const int64_t row, const int h, const int cs, const int rank, uint32_t *keys)
 {
