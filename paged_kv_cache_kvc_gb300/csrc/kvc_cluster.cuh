@@ -44,8 +44,6 @@ __device__ __forceinline__ uint32_t cluster_ld(uint32_t addr)
     return v;
 }
 
-__device__ __forceinline__ float cluster_ldf(uint32_t addr) { return __uint_as_float(cluster_ld(addr)); }
-
 __device__ __forceinline__ float4 cluster_ld4(uint32_t addr)
 {
     float4 v;

@@ -13,9 +13,9 @@
 // merge in shared memory and the CTAs through distributed shared memory: no partial goes to global memory, so a call
 // needs no workspace and one launch, and two calls share nothing.
 //
-// Measured, 8 KV heads of 4 query heads of 128: one row of 64 blocks (bf16) 5.4 us back to back, a chain of list, table,
+// Measured, 8 KV heads of 4 query heads of 128: one row of 64 blocks (bf16) 5.2 us back to back, a chain of list, table,
 // tile and merge; 64 ragged rows of up to 128 e4m3 blocks (160 MB) 36 us, 4.4 TB/s, with the longest first (40 in their own
-// order); 512 rows of 64 blocks (2.15 GB out of L2) 140 us, 15 TB/s, with 12 warps an SM.  One
+// order); 512 rows of 64 blocks (2.15 GB out of L2) 132 us, 16 TB/s, with 12 warps an SM.  One
 // tile to a step took 46 and 186 us; the CTAs' sums read one by one 8.2 us for the single row.
 #pragma once
 #include "kvc_cluster.cuh"
@@ -52,7 +52,7 @@ struct SparseCfg {
     static constexpr int COL = D + (KIND == KV_BF16 ? 8 : 4);
     static constexpr int MERGE = (W * QW * 2 + W * QW * COL) * 4;
     static constexpr int BARS = RING > MERGE ? RING : MERGE;                // offset of the barriers
-// Warps that an SM keeps, for the compiler: one CTA's registers above a third of 64 K, say, would leave room for two
+    // Warps that an SM keeps, for the compiler: one CTA's registers above a third of 64 K, say, would leave room for two
     // only (e4m3 with 16 heads per KV head at 177 registers instead of 168: 63 us instead of 54, 64 sequences).
     static constexpr int CTAS = (NT == 1 ? 16 : (NT == 2 ? 12 : 8)) / W;
     static constexpr int SMEM = 1024 /* alignment */ + BARS + W * R * 8;
@@ -357,7 +357,9 @@ __global__ void __launch_bounds__(32 * W, SparseCfg<D, NT, KIND, W>::CTAS) spars
     const uint32_t bar_base = smem_u32(bars);
     const int own = pos / (sp.sub * kBS);
 
-    // This warp's tiles, 32 at a time in registers: (first position, block), block -1: nothing to read.
+    // This warp's tiles, 32 at a time in registers: (positions to read, the keys' row of the map), 0 and -1: nothing to read.
+    constexpr int rows_per_tile = C::BOX_ROWS / 2;   // map rows (int4: 128-byte lines) of 16 positions
+    const int64_t first_head = static_cast<int64_t>(p.layer) * p.N * p.H_KV + h;
     auto load_tile = [&](int jj, int j) -> int2 {
         if (jj >= nmine || j == -1) return make_int2(0, -1);
         const int t = first + step * jj, part = t - t / sp.sub * sp.sub;
@@ -367,47 +369,42 @@ __global__ void __launch_bounds__(32 * W, SparseCfg<D, NT, KIND, W>::CTAS) spars
         }
         const int tok0 = (j * sp.sub + part) * kBS;
         if (tok0 >= len) return make_int2(0, -1);   // past the query in its own block
-        int phys = __ldg(bt_row + j);
+        const int phys = __ldg(bt_row + j);
         if (phys < 0 || static_cast<int64_t>(phys) >= p.N) {
             atomicOr(p.err, KVC_EBIT_BAD_BLOCK);
-            phys = -1;
+            return make_int2(0, -1);
         }
-        return make_int2(tok0, phys);
+        const int64_t y = (first_head + static_cast<int64_t>(phys) * p.H_KV) * (2 * rows_per_tile * sp.sub) + part * rows_per_tile;
+        return make_int2(min(kBS, len - tok0), static_cast<int>(y));
     };
     int2 t_cur = load_tile(lane, e_cur), t_next = load_tile(32 + lane, e_next);
-    // Tile jj, which may differ from lane to lane: the lane asked cannot know which of its two the asker wants.
-    auto entry = [&](int jj, int jbase) -> int2 {
+    // The map's row of tile jj, which may differ from lane to lane: the lane asked cannot know which of its two the asker wants.
+    auto row_of = [&](int jj, int jbase) {
         const int from = (jj - jbase) & 31;
-        const int2 a = make_int2(__shfl_sync(kFull, t_cur.x, from), __shfl_sync(kFull, t_cur.y, from));
-        const int2 b = make_int2(__shfl_sync(kFull, t_next.x, from), __shfl_sync(kFull, t_next.y, from));
+        const int a = __shfl_sync(kFull, t_cur.y, from), b = __shfl_sync(kFull, t_next.y, from);
         return jj - jbase < 32 ? a : b;
     };
-    const int64_t layer_row = static_cast<int64_t>(p.layer) * p.N;
-    // Tile j is stage j % R of the ring.  Lane t issues tile from + t, t < n.
-    auto issue = [&](int from, int n, int jbase) {   // warp-collective
-        const int j = from + lane;
-        const int2 e = entry(j, jbase);
-        if (lane < n && j < nmine && !p.stall_loads) {
-            const uint32_t bar = bar_base + 8u * static_cast<uint32_t>(j % R);
-            if (e.y < 0) {
-                mbar_arrive(bar);   // complete the phase without data; the consumer skips it
-            } else {
-                const uint32_t dst = st_base + static_cast<uint32_t>((j % R) * C::STAGE);
-                // keys, then the values behind them in the same stage, one box per 128-byte band each
-                constexpr int rows_per_tile = C::BOX_ROWS / 2;   // map rows (int4: 128-byte lines) of 16 positions
-                const int part_i = (e.x / kBS) % sp.sub;
-                const int32_t y = static_cast<int32_t>(((layer_row + e.y) * p.H_KV + h) * (2 * rows_per_tile) * sp.sub) + part_i * rows_per_tile;
-                mbar_arrive_expect_tx(bar, C::STAGE);
+    // A lane copies tile j, whose keys stand at y, to a stage of the ring: keys, then the values behind them, one box per
+    // 128-byte band each.
+    auto issue = [&](int j, int y, int stage) {
+        if (j >= nmine || p.stall_loads) return;
+        const uint32_t bar = bar_base + 8u * static_cast<uint32_t>(stage);
+        if (y < 0) {
+            mbar_arrive(bar);   // complete the phase without data; the consumer skips it
+            return;
+        }
+        const uint32_t dst = st_base + static_cast<uint32_t>(stage * C::STAGE);
+        mbar_arrive_expect_tx(bar, C::STAGE);
 #pragma unroll
-                for (int band = 0; band < C::BANDS; ++band) {
-                    tma_load_2d(dst + band * C::BOX_BYTES, &tmap, bar, band * C::BOX_X, y);
-                    tma_load_2d(dst + band * C::BOX_BYTES + C::BOX_BYTES / 2, &tmap, bar, band * C::BOX_X,
-                                y + rows_per_tile * sp.sub);
-                }
-            }
+        for (int band = 0; band < C::BANDS; ++band) {
+            tma_load_2d(dst + band * C::BOX_BYTES, &tmap, bar, band * C::BOX_X, y);
+            tma_load_2d(dst + band * C::BOX_BYTES + C::BOX_BYTES / 2, &tmap, bar, band * C::BOX_X, y + rows_per_tile * sp.sub);
         }
     };
-    issue(0, R, 0);
+    {
+        const int y = row_of(lane, 0);
+        if (lane < R) issue(lane, y, lane);
+    }
 
     float m_run[NT][2], l_run[NT][2];
     float oacc[C::MT][NT][4];
@@ -419,7 +416,9 @@ __global__ void __launch_bounds__(32 * W, SparseCfg<D, NT, KIND, W>::CTAS) spars
         for (int mt = 0; mt < C::MT; ++mt) oacc[mt][j][0] = oacc[mt][j][1] = oacc[mt][j][2] = oacc[mt][j][3] = 0.f;
     }
 
-    int i = 0;
+    // Tile j is stage j % R of the ring, and its use j / R.
+    int i = 0, stage = 0;
+    uint32_t use = 0u;
     bool timed_out = false;
     for (; i < nsteps; ++i) {
         const int j = i * T, jbase = j & ~31;
@@ -431,8 +430,10 @@ __global__ void __launch_bounds__(32 * W, SparseCfg<D, NT, KIND, W>::CTAS) spars
         bool ok = true;
 #pragma unroll
         for (int t = 0; t < T; ++t) {
-            st[t] = st_base + static_cast<uint32_t>(((j + t) % R) * C::STAGE);
-            if (j + t < nmine) ok &= mbar_wait_bounded(bar_base + 8u * ((j + t) % R), static_cast<uint32_t>(((j + t) / R) & 1));
+            const bool wrap = stage + t >= R;   // T <= R
+            const int at = wrap ? stage + t - R : stage + t;
+            st[t] = st_base + static_cast<uint32_t>(at * C::STAGE);
+            if (j + t < nmine) ok &= mbar_wait_bounded(bar_base + 8u * static_cast<uint32_t>(at), (use + (wrap ? 1u : 0u)) & 1u);
         }
         if (!__all_sync(kFull, ok)) {
             timed_out = true;
@@ -442,8 +443,7 @@ __global__ void __launch_bounds__(32 * W, SparseCfg<D, NT, KIND, W>::CTAS) spars
         bool full = true, some = false;
 #pragma unroll
         for (int t = 0; t < T; ++t) {
-            const int2 e = make_int2(__shfl_sync(kFull, t_cur.x, (j + t) & 31), __shfl_sync(kFull, t_cur.y, (j + t) & 31));
-            valid[t] = e.y < 0 ? 0 : min(kBS, len - e.x);
+            valid[t] = __shfl_sync(kFull, t_cur.x, (j + t) & 31);
             full &= valid[t] == kBS;
             some |= valid[t] > 0;
         }
@@ -462,9 +462,17 @@ __global__ void __launch_bounds__(32 * W, SparseCfg<D, NT, KIND, W>::CTAS) spars
             tiles_update<D, NT, KIND, PSPLIT, T>(p.scale_log2, st, qf, m_run, l_run, oacc, full, valid, lane);
         }
         __syncwarp();
-        if (j + R < nmine) {
-            if (lane < T) fence_proxy_async_smem();   // the lanes that issue
-            issue(j + R, T, jbase);
+        if (j + R < nmine) {   // the next ones into the places of these
+            const int y = row_of(j + R + lane, jbase);
+            if (lane < T) {
+                fence_proxy_async_smem();
+                issue(j + R + lane, y, stage + lane >= R ? stage + lane - R : stage + lane);
+            }
+        }
+        stage += T;
+        if (stage >= R) {
+            stage -= R;
+            ++use;
         }
     }
     if (timed_out) {   // record, then let copies already in flight land before the CTA exits
