@@ -54,7 +54,7 @@ extern "C" kvc_status kvc_sparse_attn(kvc_pool *pool, int32_t layer, const void 
     }
     const kvc_status st = check_device(pool);
     if (st != KVC_OK) return st;
-    if (!pool->tmap_sub_ok) return KVC_ERR_CUDA;
+    if (!pool->tmap_ok || !pool->tmap_sub_ok) return KVC_ERR_CUDA;
     const int64_t units = n_rows * pool->H_KV;
     // Warps of a CTA: four, and two where there are more CTAs than a GPU takes in several turns, as in a chunk's rows: their
     // starts and ends then overlap better and fewer warps' partials are joined.  Measured with four and with two, lists of
@@ -113,7 +113,7 @@ extern "C" kvc_status kvc_sparse_attn(kvc_pool *pool, int32_t layer, const void 
     cfg.stream = static_cast<cudaStream_t>(stream);
     cfg.attrs = attr;
     cfg.numAttrs = c > 1 ? 2 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, k.fn, pool->tmap_sub, sp);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, k.fn, sp.sub == 1 ? pool->tmap : pool->tmap_sub, sp);
     if (e != cudaSuccess) return cuda_status(e);
     g_launches.fetch_add(1, std::memory_order_relaxed);
     return KVC_OK;

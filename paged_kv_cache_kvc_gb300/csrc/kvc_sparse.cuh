@@ -384,8 +384,8 @@ __global__ void __launch_bounds__(32 * W, SparseCfg<D, NT, KIND, W>::CTAS) spars
         const int a = __shfl_sync(kFull, t_cur.y, from), b = __shfl_sync(kFull, t_next.y, from);
         return jj - jbase < 32 ? a : b;
     };
-    // A lane copies tile j, whose keys stand at y, to a stage of the ring: keys, then the values behind them, one box per
-    // 128-byte band each.
+    // A lane copies tile j, whose keys stand at y, to a stage of the ring: keys, then the values behind them, a box each per
+    // 128-byte band, or one for both where they are a whole block.
     auto issue = [&](int j, int y, int stage) {
         if (j >= nmine || p.stall_loads) return;
         const uint32_t bar = bar_base + 8u * static_cast<uint32_t>(stage);
@@ -398,7 +398,8 @@ __global__ void __launch_bounds__(32 * W, SparseCfg<D, NT, KIND, W>::CTAS) spars
 #pragma unroll
         for (int band = 0; band < C::BANDS; ++band) {
             tma_load_2d(dst + band * C::BOX_BYTES, &tmap, bar, band * C::BOX_X, y);
-            tma_load_2d(dst + band * C::BOX_BYTES + C::BOX_BYTES / 2, &tmap, bar, band * C::BOX_X, y + rows_per_tile * sp.sub);
+            if (sp.sub > 1)
+                tma_load_2d(dst + band * C::BOX_BYTES + C::BOX_BYTES / 2, &tmap, bar, band * C::BOX_X, y + rows_per_tile * sp.sub);
         }
     };
     {
