@@ -14,8 +14,8 @@
 // needs no workspace and one launch, and two calls share nothing.
 //
 // Measured, 8 KV heads of 4 query heads of 128: one row of 64 blocks (bf16) 5.2 us back to back, a chain of list, table,
-// tile and merge; 64 ragged rows of up to 128 e4m3 blocks (160 MB) 36 us, 4.4 TB/s, with the longest first (40 in their own
-// order); 512 rows of 64 blocks (2.15 GB out of L2) 132 us, 16 TB/s, with 12 warps an SM.  One
+// tile and merge; 64 ragged rows of up to 128 e4m3 blocks (160 MB) 35 us, 4.6 TB/s, with the longest first (40 in their own
+// order); 512 rows of 64 blocks (2.15 GB out of L2) 128 us, 17 TB/s, with 12 warps an SM.  One
 // tile to a step took 46 and 186 us; the CTAs' sums read one by one 8.2 us for the single row.
 #pragma once
 #include "kvc_cluster.cuh"
@@ -41,9 +41,11 @@ template <int D, int NT, int KIND, int W>
 struct SparseCfg {
     using C = DecodeCfg<D, KIND>;
     static constexpr int T = NT == 4 ? 1 : 2;          // tiles per step (more columns leave no registers for two)
-    // tiles in flight per warp, so that shared memory holds what registers hold: bf16 two (64 KB for four warps, 12 warps
-    // to an SM), e4m3 three (48 KB, 16 warps), int4 six
-    static constexpr int R = KIND == KV_BF16 ? (D == 64 ? 3 : 2) : (KIND == KV_E4M3 ? 3 : 6);
+    // tiles in flight per warp: the next step's, on their way while other warps compute.  More cost shared memory, and with
+    // it warps or cache, or places that change from step to step: 64 e4m3 rows of 128 blocks 48.0 us with two, 49.4 with
+    // three, 61.6 with four; int4 50.3 with two, 52.2 with six.  With 9 to 16 heads per KV head registers leave room for
+    // four (64 ragged e4m3 rows 41.2 us with three, 39.4).
+    static constexpr int R = KIND == KV_E4M3 && NT > 1 ? 4 : 2;
     static constexpr int RING = W * R * C::STAGE;
     static constexpr int QW = NT * 8;
     // The warps' partials, in the ring's place.  A column has a row of COL floats, so long that the lanes of one store
