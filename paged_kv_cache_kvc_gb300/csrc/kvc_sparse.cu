@@ -58,9 +58,9 @@ extern "C" kvc_status kvc_sparse_attn(kvc_pool *pool, int32_t layer, const void 
     const int64_t units = n_rows * pool->H_KV;
     // Warps of a CTA: four, and two where there are more CTAs than a GPU takes in several turns, as in a chunk's rows: their
     // starts and ends then overlap better and fewer warps' partials are joined.  Measured with four and with two, lists of
-    // 64 blocks, 8 KV heads: 512 rows of one sequence 149 and 140 us (bf16), 120 and 115 (e4m3), 156 and 154 (int4), with 16
-    // query heads per KV head 211 and 200, 191 and 178, 241 and 217; 256 rows of one sequence 82 and 83 (bf16); 64
-    // sequences of different lengths 48 and 60, 256 of them 150 and 164: a long row beside short ones wants more warps.
+    // 64 blocks, 8 KV heads: 512 rows of one sequence 137 and 128 us (bf16), 110 and 105 (e4m3), 146 and 141 (int4), with 16
+    // query heads per KV head 199 and 184, 182 and 169, 239 and 211; 256 rows of one sequence 75.7 and 76.5 (bf16); 64
+    // sequences of different lengths 43 and 56, 256 of them 149 and 160: a long row beside short ones wants more warps.
     const int warps = units >= 16ll * pool->num_sms ? 2 : 4;
     const SparseKernel k = pool->dtype == KVC_BF16 ? select_sparse_bf16(D, g, warps)
                                                    : (pool->dtype == KVC_INT4 ? select_sparse_int4(g, warps) : select_sparse_fp8(g, warps));
@@ -95,10 +95,10 @@ extern "C" kvc_status kvc_sparse_attn(kvc_pool *pool, int32_t layer, const void 
     const int64_t tiles = static_cast<int64_t>(top_k) * sp.sub;
     int c = 1;
     while (c < kSparseMost && units * c * 2 <= static_cast<int64_t>(pool->num_sms) * k.k.ctas_per_sm && tiles >= 2 * warps * c) c *= 2;
-    // Measured by number and longest first, 64 rows of 1 to 128 blocks, 8 KV heads: 40.4 and 36.6 us (e4m3), 48.0 and 43.9
-    // (bf16), 47 and 35 (int4), with 16 query heads per KV head 54 and 43 (e4m3); 128 rows 69 and 62 (e4m3), 79 and 79
-    // (bf16); 32 rows 22.9 and 21.8.  64 rows of one length 97.7 and 99.2; finding the row costs more than it gives with
-    // clusters of 4 (16 rows 21.3 and 21.7) and when CTAs come by the thousand (256 rows 92 and 99).
+    // Measured by number and longest first, rows of 1 to 128 blocks, 8 KV heads: 64 rows 38.2 and 35.5 us (e4m3), 45.8 and
+    // 42.8 (bf16), 48.7 and 39.6 (int4), with 16 query heads per KV head 50 and 40 (e4m3); 128 rows 67 and 61 (e4m3), 70 and
+    // 56 (int4), 76.8 and 77.7 (bf16); 32 rows 22.3 and 22.0.  64 rows of one length 94.1 and 95.3; finding the row costs more
+    // than it gives with clusters of 4 (16 rows 19.8 and 20.1) and when CTAs come by the thousand (256 rows 106 and 112).
     sp.longest_first = c <= 2 && longest_first(n_rows, B, units, c, pool->num_sms);
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

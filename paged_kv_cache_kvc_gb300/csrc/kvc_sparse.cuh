@@ -13,10 +13,11 @@
 // merge in shared memory and the CTAs through distributed shared memory: no partial goes to global memory, so a call
 // needs no workspace and one launch, and two calls share nothing.
 //
-// Measured, 8 KV heads of 4 query heads of 128: one row of 64 blocks (bf16) 5.2 us back to back, a chain of list, table,
-// tile and merge; 64 ragged rows of up to 128 e4m3 blocks (160 MB) 35 us, 4.6 TB/s, with the longest first (40 in their own
-// order); 512 rows of 64 blocks (2.15 GB out of L2) 128 us, 17 TB/s, with 12 warps an SM.  One
-// tile to a step took 46 and 186 us; the CTAs' sums read one by one 8.2 us for the single row.
+// Measured, 8 KV heads of 4 query heads of 128: one row of 64 blocks (bf16) 5.3 us back to back, a chain of list, table,
+// tile and merge; 64 ragged rows of up to 128 e4m3 blocks (160 MB) 35 us, 4.6 TB/s, with the longest first (38 in their own
+// order); 512 rows of 64 blocks (2.15 GB out of L2) 128 us, 17 TB/s, with 12 warps an SM.  One tile to a step takes 33 and
+// 143 us: a chunk gains more by two than the decoding batch loses.  The CTAs' sums read one by one took 3 us more for the
+// single row.
 #pragma once
 #include "kvc_cluster.cuh"
 #include "kvc_mod.cuh"
@@ -54,9 +55,10 @@ struct SparseCfg {
     static constexpr int COL = D + (KIND == KV_BF16 ? 8 : 4);
     static constexpr int MERGE = (W * QW * 2 + W * QW * COL) * 4;
     static constexpr int BARS = RING > MERGE ? RING : MERGE;                // offset of the barriers
-    // Warps that an SM keeps, for the compiler: one CTA's registers above a third of 64 K, say, would leave room for two
-    // only (e4m3 with 16 heads per KV head at 177 registers instead of 168: 63 us instead of 54, 64 sequences).
-    static constexpr int CTAS = (NT == 1 ? 16 : (NT == 2 ? 12 : 8)) / W;
+    // Warps that an SM keeps, for the compiler: a register more may cost a whole CTA.  With bounds and without, 512 rows of
+    // one sequence: bf16 128 us and 131, with 16 heads per KV head 185 and 221, e4m3 105 and 116; with 64 channels, as many
+    // warps as for 128 would do (16 and not 24), 79 us instead of 72.
+    static constexpr int CTAS = (D == 64 ? (NT == 1 ? 24 : (NT == 2 ? 16 : 12)) : (NT == 1 ? 16 : (NT == 2 ? 12 : 8))) / W;
     static constexpr int SMEM = 1024 /* alignment */ + BARS + W * R * 8;
 };
 
