@@ -354,9 +354,8 @@ __global__ void __launch_bounds__(32 * W, SparseCfg<D, NT, KIND, W>::CTAS) spars
     __syncwarp();   // the barriers are this warp's own
 
     const int tiles = len > 0 ? listed : 0;
-    const int nmine = tiles > first ? (tiles - first + step - 1) / step : 0;
+    int nmine = tiles > first ? (tiles - first + step - 1) / step : 0;
     const int32_t *bt_row = p.bt + static_cast<int64_t>(seq) * p.bt_stride;
-    const int nsteps = (nmine + T - 1) / T;
     const uint32_t st_base = smem_u32(smem + warp * R * C::STAGE);
     const uint32_t bar_base = smem_u32(bars);
     const int own = pos / (sp.sub * kBS);
@@ -410,6 +409,19 @@ __global__ void __launch_bounds__(32 * W, SparseCfg<D, NT, KIND, W>::CTAS) spars
         const int y = row_of(lane, 0);
         if (lane < R) issue(lane, y, lane);
     }
+
+    // The tiles end with the last that reads anything: lists of rows shorter than top_k end with empty entries.
+    uint32_t last = 0u;
+    int tail = (nmine - 1) & ~31;
+    for (; tail >= 64; tail -= 32)
+        if ((last = __ballot_sync(kFull, tail + lane < nmine && load_entry(tail + lane) != -1)) != 0u) break;
+    if (tail == 32) {
+        last = __ballot_sync(kFull, t_next.y >= 0);
+        if (last == 0u) tail = 0;
+    }
+    if (tail == 0) last = __ballot_sync(kFull, t_cur.y >= 0);
+    nmine = last ? tail + 32 - __clz(last) : 0;
+    const int nsteps = (nmine + T - 1) / T;
 
     float m_run[NT][2], l_run[NT][2];
     float oacc[C::MT][NT][4];
