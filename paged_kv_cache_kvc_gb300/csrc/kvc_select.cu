@@ -59,13 +59,15 @@ struct BoundsParams {
 };
 
 constexpr int kBoundsThreads = 256;
+constexpr int kBoundsWarps = kBoundsThreads / 32;
 
-// grid (row chunk).  A CTA finds the chunk's last rows of blocks, then its warps take a (block, head) each, the next
+// grid (row chunk, heads of a CTA: one for each warp).  A CTA finds the chunk's last rows of blocks, then its warps take a (block, head) each, the next
 // one's keys on their way meanwhile: LPR lanes per key row, 16 bytes a lane, 32 / LPR rows at a time; the channels'
 // extremes in packed halves.  Across the row's lanes each halving step passes on half the channels, so that every lane
 // ends with 2 or 4 channels of its own to round and store.  Bound by instruction issue beside HBM: 65 500 tokens of 8
-// heads take 18 us on an e4m3 pool (76 MB, 4.2 TB/s, issue slots 62 % busy), 29 on a bf16 one (4.9 TB/s); with every
-// lane finishing all of its row's channels and each block's address divided out, 31 and more.  64 single tokens 2.3 us.
+// heads take 18 us on an e4m3 pool (76 MB, 4.2 TB/s, issue slots 61 % busy), 28 on a bf16 one (5.1 TB/s); with every
+// lane finishing all of its row's channels and each block's address divided out, 31 and more.  64 single tokens 2.2 us.
+// With 32 heads a CTA for all of them took 10.1 us for 83 runs of 972 tokens in all (bf16), one for eight 5.5.
 template <int D, int KIND>
 __global__ void __launch_bounds__(kBoundsThreads, KIND == KV_BF16 && D == 128 ? 3 : 4) bounds_kernel(const BoundsParams p)
 {
@@ -95,9 +97,9 @@ __global__ void __launch_bounds__(kBoundsThreads, KIND == KV_BF16 && D == 128 ? 
     }
     __syncthreads();
     const int c = lane % LPR, sub = lane / LPR;
-    constexpr int kBoundsWarps = kBoundsThreads / 32;
+    const int h0 = blockIdx.y * kBoundsWarps, heads = min(p.H_KV - h0, kBoundsWarps);   // this CTA's; h counts from h0
     const int count = n_ends;
-    const uint8_t *layer = p.base + static_cast<int64_t>(p.layer) * p.N * p.H_KV * (2ll * p.bs * ROW) + 16 * c;
+    const uint8_t *layer = p.base + static_cast<int64_t>(p.layer) * p.N * p.H_KV * (2ll * p.bs * ROW) + h0 * (2 * p.bs * ROW) + 16 * c;
 
     // rows t0 + sub, t0 + sub + RPS, ... of the keys of (end, head); past the last row: the last one again
     auto fetch = [&](int i, int h, int t0, uint4 (&v)[U]) {
@@ -108,8 +110,8 @@ __global__ void __launch_bounds__(kBoundsThreads, KIND == KV_BF16 && D == 128 ? 
     };
     auto advance = [&](int &i, int &h) {
         h += kBoundsWarps;
-        while (h >= p.H_KV) {
-            h -= p.H_KV;
+        while (h >= heads) {
+            h -= heads;
             ++i;
         }
     };
@@ -190,7 +192,7 @@ __global__ void __launch_bounds__(kBoundsThreads, KIND == KV_BF16 && D == 128 ? 
                 if constexpr (KIND == KV_BF16) f = make_float2(bf16_lo(w), bf16_hi(w));
                 else f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
                 if constexpr (KIND != KV_BF16) {
-                    const float *sc = p.s_k + static_cast<int64_t>(h) * D + first + (KIND == KV_INT4 ? x : 2 * x);
+                    const float *sc = p.s_k + static_cast<int64_t>(h0 + h) * D + first + (KIND == KV_INT4 ? x : 2 * x);
                     f.x *= __ldg(sc);
                     f.y *= __ldg(sc + (KIND == KV_INT4 ? 4 : 1));
                 }
@@ -200,7 +202,7 @@ __global__ void __launch_bounds__(kBoundsThreads, KIND == KV_BF16 && D == 128 ? 
             }
         const int e = unit_exponent(__uint_as_float(__reduce_max_sync(kFull, top)));
         const float inv = exp2_int(-e);
-        const int64_t rec = static_cast<int64_t>(blk) * p.H_KV + h;
+        const int64_t rec = static_cast<int64_t>(blk) * p.H_KV + h0 + h;
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
             uint32_t code[KEEP][2];
@@ -686,9 +688,11 @@ static kvc_status launch_bounds(const kvc_pool *pool, BoundsParams &p, cudaStrea
 {
     // Few rows are a decoding batch's, nearly each the last one of its block: as many CTAs as rows, until there are four
     // for every SM.
-    p.rows_per_cta = static_cast<int32_t>(std::min<int64_t>(std::max<int64_t>((p.rows + 4 * pool->num_sms - 1) / (4 * pool->num_sms), 1), kBoundsThreads));
+    const int64_t per_chunk = (p.H_KV + kBoundsWarps - 1) / kBoundsWarps, most = std::max<int64_t>(4 * pool->num_sms / per_chunk, 1);
+    p.rows_per_cta = static_cast<int32_t>(std::min<int64_t>((p.rows + most - 1) / most, kBoundsThreads));
     const int64_t chunks = (p.rows + p.rows_per_cta - 1) / p.rows_per_cta;
-    return launch(&bounds_kernel<D, KIND>, dim3(static_cast<unsigned>(chunks)), kBoundsThreads, 0, 1, stream, p);
+    return launch(&bounds_kernel<D, KIND>, dim3(static_cast<unsigned>(chunks), static_cast<unsigned>(per_chunk)), kBoundsThreads, 0, 1,
+                  stream, p);
 }
 
 }  // namespace kvc

@@ -118,6 +118,20 @@ def test_bounds_of_many_rows(kvc, rows):
             c.close()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp8", "int4"])
+@pytest.mark.parametrize("H_KV", [7, 9, 20, 33])
+def test_bounds_of_many_heads(kvc, dtype, H_KV):
+    """A CTA takes eight heads, the last one of a row of CTAs what is left; decoding rows and a prompt over many blocks."""
+    c = Cache(kvc, [700, 33, 1], H_KV=H_KV, dtype=dtype)
+    try:
+        slots = np.concatenate([c.slots([(0, 0, 700), (1, 32, 33), (2, 0, 1)]), [-1]]).astype(np.int32)
+        c.kvc.kvc_update_bounds(c.pool, 0, c.bounds, dev(slots))
+        assert kvc.kvc_pool_sync_status(c.pool) == kvc.KVC_OK
+        check_bounds(c, slots)
+    finally:
+        c.close()
+
+
 @pytest.mark.parametrize("H_KV", [1, 2, 3])
 def test_bounds_of_rows_that_skip_places(kvc, H_KV):
     """The rows of a block ascend but need not follow one another, and one may come twice: the last counts."""
