@@ -14,7 +14,7 @@
 //
 // Latency bounds it: a decoding batch reads and writes a few kilobytes.  8 sequences, one more token each, take 3.8 us
 // back to back (one CTA; 6.7 with the cluster's barriers and a thread's four rows looked up one after another).  512
-// sequences with 65 536 new rows take 12.7: 8 in the cluster (three barriers, two passes over the tables), then the
+// sequences with 65 536 new rows take 13: 8 in the cluster (three barriers, two passes over the tables), then the
 // maps in a kernel over the whole GPU (written by the cluster's eight SMs they took 12 alone: 60 instructions a row).
 #include <algorithm>
 
