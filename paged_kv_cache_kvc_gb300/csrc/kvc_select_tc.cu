@@ -191,6 +191,7 @@ __global__ void __launch_bounds__(kStCta, 1) select_tile_kernel(const SelectTile
             if (lane + 32 * u < chunks) place(lane + 32 * u, kept[u]);
         for (int i = lane + 32 * KEEP; i < chunks; i += 32) place(i, __ldg(source(r) + i));
     }
+    fence_proxy_async_smem();   // the tensor cores read the queries through the async proxy, which the barrier alone does not order
     __syncthreads();
 
     const uint32_t idesc = tc_idesc_f16(128, cols, false, false, false);

@@ -1,0 +1,29 @@
+"""Rows scored together on the tensor cores: what the first products, every group size and long tables depend on."""
+import numpy as np
+import pytest
+import torch
+
+from mod_reference import bf16
+from test_gpu_sparse import Cache, check_select, random_bounds, select
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("D,g,H_KV", [(64, 1, 2), (64, 4, 2), (128, 4, 1), (128, 5, 1), (128, 8, 2), (128, 2, 2)])
+def test_the_first_products_take_the_queries_of_the_call(kvc, D, g, H_KV):
+    """A sequence of one tile: its product follows the queries' stores at once.  Every row is checked, and calls after
+    one another have other queries, so that what an earlier one left is no answer."""
+    c = Cache(kvc, [16 * 100], H_KV=H_KV, D=D)
+    try:
+        codes, units = random_bounds(c, D + g)
+        n = -(-10500 // (H_KV * max(g, 4)))   # enough rows for any group size, see rows_together
+        rows = [(0, 16 * 100 - 1 - i % 400) for i in range(n)]
+        r = np.random.default_rng(g)
+        for call in range(6):
+            q = bf16(r.standard_normal((n, g * H_KV, D)) * 2).cuda()
+            got = select(c, q, rows, 9, 1, 1)
+            keep = list(range(call, n, 6))
+            check_select(c, q[keep], [rows[i] for i in keep], codes, units, got[keep], 9, 1, 1)
+        assert kvc.kvc_pool_sync_status(c.pool) == kvc.KVC_OK
+    finally:
+        c.close()
