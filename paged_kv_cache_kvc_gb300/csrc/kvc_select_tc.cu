@@ -25,6 +25,7 @@
 //
 // A tile of rows may hold several sequences (runs): they are done one after the other.
 #include <algorithm>
+#include <cstdlib>
 
 #include "kvc_select.cuh"
 #include "kvc_tc.cuh"
@@ -66,6 +67,7 @@ struct SelectTileParams {
     SelectParams s;
     int64_t rows;
     int32_t RT;            // rows per tile
+    uint32_t stall_from;   // test hook: tiles of a CTA from this one on are never announced, so that the waits run out
 };
 
 // Two pairs of f16 from four int8 codes, exact.
@@ -96,6 +98,7 @@ __global__ void __launch_bounds__(kStCta, 1) select_tile_kernel(const SelectTile
     __shared__ int32_t row_count[kStRows];                               // candidates
     __shared__ uint64_t full_bar[2], done_bar[2];   // a buffer of A is written; its products are there (and it is free)
     __shared__ uint32_t tmem_base;
+    __shared__ int32_t expired;   // a wait ran out: written between a walk's barriers only, so all threads read the same
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, h = blockIdx.y;
     const int64_t r0 = static_cast<int64_t>(blockIdx.x) * tp.RT;
     const int cols = (tp.RT * p.g + 15) & ~15;
@@ -108,6 +111,7 @@ __global__ void __launch_bounds__(kStCta, 1) select_tile_kernel(const SelectTile
             mbar_init(smem_u32(&full_bar[i]), kStWarps);
             mbar_init(smem_u32(&done_bar[i]), 1);
         }
+        expired = 0;
         fence_barrier_init();
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -203,12 +207,21 @@ __global__ void __launch_bounds__(kStCta, 1) select_tile_kernel(const SelectTile
     const int8_t *codes = p.codes + h * (2 * D) + part * C::SEG;
     const uint32_t record_stride = static_cast<uint32_t>(p.H_KV) * (2 * D);   // H_KV is at most 256
     uint32_t tile_no = 0u;   // tiles of this CTA so far: the barriers' phases
+    uint32_t issued = 0u;    // tiles whose products have begun (the last warp's)
+    // A wait that runs out ends the walk for its warp, and the kernel after the next barrier: the other warps' waits run out
+    // with it or one tile later.
     auto wait = [&](uint64_t &b, uint32_t parity) {
-        if (!mbar_wait_bounded(smem_u32(&b), parity & 1u) && lane == 0) atomicOr(p.err, KVC_EBIT_TIMEOUT);
+        const bool ok = __all_sync(kFull, mbar_wait_bounded(smem_u32(&b), parity & 1u));
+        if (!ok && lane == 0) {
+            atomicOr(p.err, KVC_EBIT_TIMEOUT);
+            expired = 1;
+        }
+        return ok;
     };
 
     const int lane_seq = lane < tp.RT ? row_seq[lane] : -3, lane_nb = lane < tp.RT ? row_nb[lane] : 0;   // RT <= 32
-    for (int first = 0; first < tp.RT;) {   // runs of rows of one sequence
+    int first = 0;
+    while (first < tp.RT) {   // runs of rows of one sequence
         const int seq = __shfl_sync(kFull, lane_seq, first);
         const uint32_t others = __ballot_sync(kFull, lane_seq != seq) & (0xFFFFFFFFu << first);
         const int end = others ? __ffs(others) - 1 : 32;
@@ -257,7 +270,7 @@ __global__ void __launch_bounds__(kStCta, 1) select_tile_kernel(const SelectTile
             tmem_st_wait();
             tc_fence_before();   // and what this warp read of tensor memory it has read
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&full_bar[buf]));
+            if (lane == 0 && tile_no + t < tp.stall_from) mbar_arrive(smem_u32(&full_bar[buf]));
         };
 
         // One walk over the blocks.  read(t, d): the epilogue of tile t, whose products stand at d in tensor memory.
@@ -265,6 +278,7 @@ __global__ void __launch_bounds__(kStCta, 1) select_tile_kernel(const SelectTile
             for (t0 = 0; t0 < n_tiles; t0 += kStChunk) {
                 const int nt = min(kStChunk, n_tiles - t0);
                 __syncthreads();   // the chunk before is done with its table entries
+                if (expired) break;
                 // a single chunk's are still there in the second walk
                 for (int i = tid; i < nt * kStTile && (report || n_tiles > kStChunk); i += kStCta) {
                     const int j = t0 * kStTile + i;
@@ -281,13 +295,14 @@ __global__ void __launch_bounds__(kStCta, 1) select_tile_kernel(const SelectTile
                 if (warp == kStWarps) {
                     for (int t = 0; t < nt; ++t) {
                         const uint32_t i = tile_no + t, buf = i & 1u;
-                        wait(full_bar[buf], i >> 1);
+                        if (!wait(full_bar[buf], i >> 1)) break;
                         tc_fence_after();
 #pragma unroll
                         for (int kk = 0; kk < C::K / 16; ++kk)
                             tc_mma_f16_tmem_a_warp(tmem + buf * kStCols, tmem + C::A_TMEM + buf * C::A_COLS + kk * 8,
                                                    tc_desc_advance(desc_b, (kk >> 2) * C::BAND + (kk & 3) * 32), idesc, kk > 0 ? 1u : 0u);
                         tc_commit_warp(smem_u32(&done_bar[buf]));
+                        issued = i + 1u;
                     }
                 } else {
                     copy(0);
@@ -306,7 +321,7 @@ __global__ void __launch_bounds__(kStCta, 1) select_tile_kernel(const SelectTile
                             __syncwarp();
                             widen(t + 1, buf ^ 1u);
                         }
-                        wait(done_bar[buf], i >> 1);
+                        if (!wait(done_bar[buf], i >> 1)) break;
                         tc_fence_after();
                         read(t, tmem + buf * kStCols + (static_cast<uint32_t>(32 * quarter) << 16));
                     }
@@ -398,6 +413,7 @@ __global__ void __launch_bounds__(kStCta, 1) select_tile_kernel(const SelectTile
                 });
             });
         }
+        if (expired) break;
         __syncthreads();
         for (int r = first + warp; r < end && warp < kStWarps; r += kStWarps) {
             uint32_t v[kStGroups / 32];
@@ -436,6 +452,7 @@ __global__ void __launch_bounds__(kStCta, 1) select_tile_kernel(const SelectTile
                 scores(t, d, [&](int r, float s) { append(r, smem_u32(&row_count[r]), s, row_limit[r], (t0 + t) * kStTile + in_tile); });
             });
         }
+        if (expired) break;
         for (int r = first + warp; r < end && warp < kStWarps; r += kStWarps) {   // a warp per row
             int32_t *list = p.lists + ((r0 + r) * p.H_KV + h) * p.top_k;
             const int n = row_count[r];
@@ -447,6 +464,15 @@ __global__ void __launch_bounds__(kStCta, 1) select_tile_kernel(const SelectTile
         }
         __syncthreads();
         first = end;
+    }
+    if (expired) {   // what is on its way lands; this run's rows and those behind it list nothing
+        cp_async_wait<0>();
+        if (issued > 0u) (void)mbar_wait_bounded(smem_u32(&done_bar[(issued - 1u) & 1u]), ((issued - 1u) >> 1) & 1u);
+        for (int r = first + warp; r < tp.RT; r += kStCta / 32) {
+            if (row_seq[r] < 0) continue;
+            int32_t *list = p.lists + ((r0 + r) * p.H_KV + h) * p.top_k;
+            for (int i = lane; i < p.top_k; i += 32) list[i] = -1;
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -486,6 +512,8 @@ kvc_status select_tiles(const SelectParams &p, int D, int64_t rows, cudaStream_t
     tp.s = p;
     tp.rows = rows;
     tp.RT = std::min(kStRows, kStCols / p.g);
+    const char *stall = std::getenv("KVC_TEST_STALL");   // "n": from the n-th tile of every CTA on
+    tp.stall_from = stall ? static_cast<uint32_t>(std::max(std::atoi(stall), 1) - 1) : 0xFFFFFFFFu;
     return D == 64 ? launch_tiles<64>(tp, stream) : launch_tiles<128>(tp, stream);
 }
 
