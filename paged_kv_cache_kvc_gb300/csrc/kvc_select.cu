@@ -210,7 +210,9 @@ __global__ void __launch_bounds__(kBoundsThreads, KIND == KV_BF16 && D == 128 ? 
             for (int x = 0; x < KEEP; ++x)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const float z = y[which][x][k] * inv;   // a NaN becomes the first bound that it is compared with
+                    // rounded outward, so that a product that is too small for fp32 still counts as one (inv is a power of two:
+                    // all others are exact); a NaN becomes the first bound that it is compared with
+                    const float z = which ? __fmul_rd(y[which][x][k], inv) : __fmul_ru(y[which][x][k], inv);
                     code[x][k] = static_cast<uint32_t>(which ? __float2int_rd(fminf(fmaxf(z, -127.f), 127.f))
                                                              : __float2int_ru(fmaxf(fminf(z, 127.f), -127.f))) & 255u;
                 }
