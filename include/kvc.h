@@ -489,7 +489,10 @@ KVC_API kvc_status kvc_prefill_attn_mod(kvc_pool *pool, int32_t layer, const voi
  * kvc_pool_sync_status); so are a count outside [0, free_capacity] (taken as
  * the nearest bound) and more returned blocks than the list holds (dropped).
  * A token whose table entry is outside the pool gets slot -1 and is recorded
- * (KVC_ERR_BAD_BLOCK).  B = 0 fills the rows with -1.  The pool gives block
+ * (KVC_ERR_BAD_BLOCK).  A returned entry outside the pool is recorded too, and
+ * pushed as it stands: a later step grants it like any other block, and the
+ * tokens that fall into it get slot -1, so after KVC_ERR_BAD_BLOCK the free list
+ * has to be built again.  B = 0 fills the rows with -1.  The pool gives block
  * size, block count, device and error word; its keys and values are not
  * touched.  Errors (synchronous): KVC_ERR_ARG, KVC_ERR_UNSUPPORTED, KVC_ERR_CUDA. */
 KVC_API kvc_status kvc_plan_step(kvc_pool *pool, int32_t *block_tables, int32_t max_blocks, const int32_t *seq_lens,
@@ -542,11 +545,16 @@ KVC_API kvc_status kvc_bounds_bytes(const kvc_pool *pool, uint64_t *bytes);
  * the pool (after the write, on the same stream): places 0 .. slot mod bs of the
  * last row in each block.
  *   slots: device int32 [n_rows], the write's slot map: the rows of one block
- *       adjacent and in ascending order, as kvc_plan_step gives them; -1 rows
- *       are skipped, another slot outside the pool is recorded
- *       (KVC_ERR_BAD_BLOCK)
- * Blocks that kvc_copy_blocks made keep their old bounds until a row of theirs
- * is given here (the slot of its last filled place).
+ *       adjacent (no other row between them, -1 rows included) and in ascending
+ *       order, as kvc_plan_step gives them; -1 rows are skipped, another slot
+ *       outside the pool is recorded (KVC_ERR_BAD_BLOCK)
+ * Nothing else changes bounds.  The calls that write keys (kvc_append,
+ * kvc_write_tokens, kvc_decode_step, kvc_mixed_step, kvc_rope_append,
+ * kvc_rope_write_tokens, kvc_rope_write_slots) and kvc_copy_blocks leave them as
+ * they were, and no error tells a selection that the bounds it reads are of
+ * older keys.  So after any of them, and before the next selection, the blocks
+ * that were written or copied to are given here: through the write's slot map,
+ * or one row for each block, block * bs + its last filled place.
  * Pools of any block size.  Errors (synchronous): KVC_ERR_ARG (also a buffer
  * smaller than kvc_bounds_bytes), KVC_ERR_CUDA. */
 KVC_API kvc_status kvc_update_bounds(kvc_pool *pool, int32_t layer, const int32_t *slots, int64_t n_rows, void *bounds,
@@ -573,7 +581,9 @@ KVC_API kvc_status kvc_update_bounds(kvc_pool *pool, int32_t layer, const int32_
  * KVC_ERR_BAD_BLOCK); a row whose sequence is not below B, whose position is past the table, or
  * where either is below -1, lists nothing (KVC_ERR_RANGE).  H_Q / H_KV as
  * kvc_decode_attn; pools of any block size; max_blocks up to 262144 (else
- * KVC_ERR_UNSUPPORTED).  Nothing is allocated.  Errors (synchronous):
+ * KVC_ERR_UNSUPPORTED).  A step's long chunks and its decoding rows are faster in
+ * a call each than in one (the lists are the same): rows are scored together, or
+ * each alone, for the call as a whole.  Nothing is allocated.  Errors (synchronous):
  * KVC_ERR_ARG, KVC_ERR_UNSUPPORTED, KVC_ERR_CUDA. */
 KVC_API kvc_status kvc_select_blocks(kvc_pool *pool, int32_t layer, const void *bounds, uint64_t bounds_bytes,
                                      const void *q, int32_t num_q_heads, const int32_t *block_tables,
@@ -593,8 +603,12 @@ KVC_API kvc_status kvc_select_blocks(kvc_pool *pool, int32_t layer, const void *
  *   Rows, sequences and positions as kvc_select_blocks: rows of padding leave
  *   out and lse as they are, rows in error read nothing.
  *   scale: finite and > 0
- * block_size 16, 32, 48 .. 128 (a multiple of 16, else KVC_ERR_UNSUPPORTED);
- * weights and precision as kvc_decode_attn_mod.  Nothing is allocated and no
+ * block_size 16, 32, 48 .. 128 (a multiple of 16, else KVC_ERR_UNSUPPORTED).
+ * Weights as kvc_decode_attn_mod: a bf16 high / low pair on bf16 pools with up
+ * to 16 query heads per KV head, one bf16 with more, f16 on e4m3 and int4 pools.
+ * On those two a query enters its products as f16, times the channel's key
+ * scale: that product is below 65504 in magnitude (else infinite).  Sums,
+ * maxima and outputs are fp32 until the outputs' one rounding.  Nothing is allocated and no
  * workspace is needed: the CTAs of a row merge in shared memory.  Other
  * requirements and errors as kvc_decode_attn. */
 KVC_API kvc_status kvc_sparse_attn(kvc_pool *pool, int32_t layer, const void *q, int32_t num_q_heads,

@@ -520,7 +520,10 @@ def kvc_block_bounds_views(pool, layer, bounds):
 
 
 def kvc_update_bounds(pool, layer, bounds, slots, stream=None):
-    """Recompute the bounds of every block that the rows of a slot map were written to (after the write)."""
+    """Recompute the bounds of every block that the rows of a slot map were written to (after the write).
+
+    The rows of a block stand next to one another, ascending.  No other call changes bounds: after kvc_append,
+    kvc_decode_step, kvc_copy_blocks and the like, give the slots that they wrote (the last one of each block will do)."""
     s = (_call or _native()).update_bounds(pool.args, layer, bounds, slots, None if stream is None else _stream(stream))
     if s:
         raise KvcError(s, "kvc_update_bounds")

@@ -45,3 +45,28 @@ def test_tiny_scales_beside_large_ones(kvc, dtype):
         assert kvc.kvc_pool_sync_status(c.pool) == kvc.KVC_OK
     finally:
         c.close()
+
+
+def test_blocks_that_other_calls_wrote(kvc):
+    """Writes by table and copies leave bounds as they were; one row for each block, its last filled place, renews them."""
+    c = Cache(kvc, [100, 30], H_KV=2, D=64)
+    try:
+        slots = c.slots([(0, 0, 100), (1, 0, 30)])
+        c.kvc.kvc_update_bounds(c.pool, 0, c.bounds, dev(slots))
+        check_bounds(c, slots)
+        old = c.bounds.clone()
+        r = np.random.default_rng(0)
+        new = lambda n: torch.from_numpy(r.standard_normal((n, 2, 64)).astype(np.float32) * 30).bfloat16().cuda()
+        # sequence 0: five tokens from position 95 on, which end in a block of their own; sequence 1: one at position 30
+        c.kvc.kvc_write_tokens(c.pool, 0, dev(c.table), dev([95, 30]), dev([0, 5, 5]), new(5), new(5))
+        c.kvc.kvc_append(c.pool, 0, dev(c.table[1:]), dev([30]), new(1), new(1))
+        free = [b for b in range(c.N) if b not in c.table][0]
+        c.kvc.kvc_copy_blocks(c.pool, dev([[int(c.table[0, 2]), free]]))
+        assert torch.equal(c.bounds, old)
+        last = [c.table[0, 5] * 16 + 15, c.table[0, 6] * 16 + 3, c.table[1, 1] * 16 + 14, free * 16 + 15]
+        c.kvc.kvc_update_bounds(c.pool, 0, c.bounds, dev(last))
+        check_bounds(c, list(slots) + last)
+        assert not torch.equal(c.bounds, old)
+        assert kvc.kvc_pool_sync_status(c.pool) == kvc.KVC_OK
+    finally:
+        c.close()
