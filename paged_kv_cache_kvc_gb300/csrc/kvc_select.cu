@@ -64,9 +64,9 @@ constexpr int kBoundsWarps = kBoundsThreads / 32;
 // grid (row chunk, heads of a CTA: one for each warp).  A CTA finds the chunk's last rows of blocks, then its warps take a (block, head) each, the next
 // one's keys on their way meanwhile: LPR lanes per key row, 16 bytes a lane, 32 / LPR rows at a time; the channels'
 // extremes in packed halves.  Across the row's lanes each halving step passes on half the channels, so that every lane
-// ends with 2 or 4 channels of its own to round and store.  Bound by instruction issue beside HBM: 65 500 tokens of 8
-// heads take 18 us on an e4m3 pool (76 MB, 4.2 TB/s, issue slots 61 % busy), 28 on a bf16 one (5.1 TB/s); with every
-// lane finishing all of its row's channels and each block's address divided out, 31 and more.  64 single tokens 2.2 us.
+// ends with 2 or 4 channels of its own to round and store.  65 500 tokens of 8 heads take 18 us on an e4m3 pool (76 MB, 4.2
+// TB/s: 400 instructions a block and head, warps waiting for the pipe of the conversions and extremes, issue slots 64 % and
+// HBM 40 % busy), 27.5 on a bf16 one (143 MB, 5.2 TB/s), 23.6 on an int4 one (42 MB; 565 instructions); with every lane finishing all of its row's channels and each block's address divided out, 31 and more.  64 single tokens 2.2 us.
 // With 32 heads a CTA for all of them took 10.1 us for 83 runs of 972 tokens in all (bf16), one for eight 5.5.
 template <int D, int KIND>
 __global__ void __launch_bounds__(kBoundsThreads, KIND == KV_BF16 && D == 128 ? 3 : 4) bounds_kernel(const BoundsParams p)
@@ -634,6 +634,10 @@ static bool aligned(const void *ptr, size_t a) { return (reinterpret_cast<uintpt
 // tile to an SM at a time, whatever it holds.  Measured at 2048 blocks, 8 KV heads of 4 query heads: 64 rows 41 us
 // alone, 62 together; 128 rows 69 and 63; 512 rows 244 and 64.  One query head per KV head, 32 of them, 128 rows: 168
 // and 110; groups that do not divide 32 columns (3, 5), 128 rows: 62 and 79 alone, 147 and 152 together.
+// The host does not know which sequence has how many rows, and B counts the table's.  So a chunk and decoding rows in one
+// call are planned for the worse of both: a 512-row chunk (65 us alone) takes 334 us with 7 single rows of other sequences
+// and 710 with 15 (a tile's sequences are walked one after another), 303 with 63 (every row goes alone).  Two calls take 81,
+// 86 and 120.
 static bool rows_together(const SelectParams &p, int64_t rows, int sms)
 {
     const int64_t RT = std::min(32, 128 / p.g);

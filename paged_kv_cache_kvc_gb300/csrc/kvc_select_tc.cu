@@ -18,12 +18,12 @@
 //
 // 512 rows of 2048 blocks, 8 KV heads of 4 query heads: 64 us (273 scored row by row; 181 and then 92 with the scores
 // of all blocks kept in shared memory of a cluster, 76 with A in shared memory).  A tile costs 1.1 us in the first walk
-// and 1.35 in the second, instruction issue of 16 warps (widening 110 instructions, maxima 70); the products themselves
-// are 0.56 (tensor pipe 19 %).  15 us are code that runs once: queries, limits, ranks.
+// and 1.35 in the second: each warp's chain of copies, widening (110 instructions), barrier, products and maxima (70), with
+// 16 warps to hide it in (issue slots 54 % busy); the products themselves are 0.56 (tensor pipe 20 %).  15 us are code that runs once: queries, limits, ranks.
 // Reading and widening by warps of their own was slower (126 us: half the warps for each, loads of TMEM one after
 // another).
 //
-// A tile of rows may hold several sequences (runs): they are done one after the other.
+// A tile of rows may hold several sequences (runs): they are done one after the other, each with two walks of its own.
 #include <algorithm>
 #include <cstdlib>
 
@@ -485,8 +485,8 @@ __global__ void __launch_bounds__(kStCta, 1) select_tile_kernel(const SelectTile
 template <int D, int G>
 static kvc_status launch_tile_kernel(const SelectTileParams &tp, cudaStream_t stream)
 {
-    // At least 116 KB: one CTA to an SM, whose tensor memory it takes whole.
-    constexpr int kSmem = StCfg<D>::SMEM > 116 * 1024 ? StCfg<D>::SMEM : 116 * 1024;
+    constexpr int kSmem = StCfg<D>::SMEM;
+    static_assert(2 * kSmem > 228 * 1024, "one CTA to an SM, whose tensor memory it takes whole");
     struct Tag {};
     const DecodeKernel k = configured<Tag>(reinterpret_cast<const void *>(&select_tile_kernel<D, G>), kSmem, kStCta, false);
     if (k.ctas_per_sm <= 0) return KVC_ERR_CUDA;

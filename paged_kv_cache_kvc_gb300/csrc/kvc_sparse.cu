@@ -6,8 +6,9 @@
 
 namespace kvc {
 
-// Weights enter the value product as a bf16 high / low pair for up to 16 query heads per KV head, as one bf16 with more
-// (as in kvc_decode_attn_mod).
+// Weights enter the value product as a bf16 high / low pair for up to 16 query heads per KV head (1.5e-6 of the output's norm),
+// as one bf16 with more (1.0e-3, below the output's own rounding: the second part would double four column tiles' products),
+// as in kvc_decode_attn_mod.
 template <int D, int W>
 static SparseKernel pick(int g)
 {

@@ -44,8 +44,9 @@ struct SparseCfg {
     static constexpr int T = NT == 4 ? 1 : 2;          // tiles per step (more columns leave no registers for two)
     // tiles in flight per warp: the next step's, on their way while other warps compute.  More cost shared memory, and with
     // it warps or cache, or places that change from step to step: 64 e4m3 rows of 128 blocks 48.0 us with two, 49.4 with
-    // three, 61.6 with four; int4 50.3 with two, 52.2 with six.  With 9 to 16 heads per KV head registers leave room for
-    // four (64 ragged e4m3 rows 41.2 us with three, 39.4).
+    // three, 61.6 with four; int4 50.3 with two, 49.1 with four, 51.9 with six, ragged 38.6, 37.9 and 39.1.  With 9 to 16
+    // heads per KV head registers leave room for four (64 ragged e4m3 rows 41.2 us with three, 39.4; int4 would gain too:
+    // even rows 80.9 with two, 73.9 with four, ragged 48.2 and 46.0).
     static constexpr int R = KIND == KV_E4M3 && NT > 1 ? 4 : 2;
     static constexpr int RING = W * R * C::STAGE;
     static constexpr int QW = NT * 8;
@@ -175,7 +176,7 @@ __device__ __forceinline__ void tiles_update(float scale_log2, const uint32_t (&
             l_run[jn][c] = fmaf(l_run[jn][c], alpha[jn][c], sum);
         }
 #pragma unroll
-        for (int t = 0; t < T; ++t) {
+        for (int t = 0; t < T; ++t) {   // weights as operands: bf16 (as a pair: 16 bits), or f16 beside widened codes
             if constexpr (!QUANT) {
                 const uint32_t h0 = pack_bf16(sc[t][jn][0], sc[t][jn][1]), h1 = pack_bf16(sc[t][jn][2], sc[t][jn][3]);
                 pb[t][jn][0] = movmatrix_trans(h0);
@@ -314,7 +315,9 @@ __global__ void __launch_bounds__(32 * W, SparseCfg<D, NT, KIND, W>::CTAS) spars
     };
     const int e_cur = load_entry(lane), e_next = load_entry(32 + lane);
 
-    // ---- query fragments, see kvc_decode.cuh
+    // ---- query fragments, see kvc_decode.cuh.  Quantised pools: codes are exact in f16, so the queries are f16 too, with the
+    // key scales in them: of the output's norm that rounding is 3.4e-4 (e4m3) and 3.8e-4 (int4), the f16 weights' 1.2e-4, the
+    // output's own to bf16 1.7e-3 (2048 positions).
     uint32_t qf[NT][C::KSTEPS][2];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
